@@ -27,7 +27,10 @@ EXPORTS = ("kda_fwd_workspace_size", "kda_bwd_workspace_size", "kda_fwd", "kda_f
            "kda_short_conv_fwd", "kda_short_conv_bwd_workspace_size", "kda_short_conv_bwd",
            "kda_fwd_segmented_workspace_size", "kda_fwd_segmented", "kda_bwd_segmented_workspace_size",
            "kda_bwd_segmented", "kda_selftest_wait_timeout",
-           "kda_gated_norm_fwd", "kda_gated_norm_bwd_workspace_size", "kda_gated_norm_bwd")
+           "kda_gated_norm_fwd", "kda_gated_norm_bwd_workspace_size", "kda_gated_norm_bwd",
+           "kda_decode_step", "kda_ssm_fwd_workspace_size", "kda_ssm_fwd", "kda_ssm_step",
+           "kda_short_conv_prompt", "kda_short_conv_step", "kda_pages_workspace_size", "kda_pages_copy",
+           "kda_pages_fork", "kda_pages_extend", "kda_pages_free", "kda_pages_compact")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 GATES = {"lower_bounded": 0, "softplus": 1}   # kda_gate
 
@@ -36,6 +39,19 @@ class KdaDims(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int), ("K", ctypes.c_int),
                 ("V", ctypes.c_int), ("dtype", ctypes.c_int), ("num_seqs", ctypes.c_int), ("Hk", ctypes.c_int),
                 ("gate", ctypes.c_int)]
+
+
+class SsmDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int), ("G", ctypes.c_int),
+                ("N", ctypes.c_int), ("P", ctypes.c_int), ("dtype", ctypes.c_int), ("num_seqs", ctypes.c_int),
+                ("x_stride", ctypes.c_int64), ("b_stride", ctypes.c_int64), ("c_stride", ctypes.c_int64),
+                ("dt_stride", ctypes.c_int64)]
+
+
+class PagesDims(ctypes.Structure):
+    _fields_ = [("layers", ctypes.c_int), ("num_pages", ctypes.c_int), ("num_seqs", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("page_tokens", ctypes.c_int), ("page_bytes", ctypes.c_int64),
+                ("layer_stride", ctypes.c_int64)]
 
 
 class KdaError(RuntimeError):
@@ -123,6 +139,26 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.kda_short_conv_bwd_workspace_size.argtypes = [ctypes.c_int] * 4
         lib.kda_short_conv_bwd.restype = ctypes.c_int
         lib.kda_short_conv_bwd.argtypes = conv + [_vp] * 5 + [ctypes.c_size_t, _vp]
+        i, i64, sz, f = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+        ssm_p, pages_p = ctypes.POINTER(SsmDims), ctypes.POINTER(PagesDims)
+        serving = {   # argument types; the two sizes return size_t, the others a status
+            "kda_decode_step": [dims_p] + [_vp] * 7 + [f, f, _vp, i] + [_vp] * 4,
+            "kda_ssm_fwd_workspace_size": [ssm_p],
+            "kda_ssm_fwd": [ssm_p] + [_vp] * 12 + [_vp, sz, _vp],
+            "kda_ssm_step": [ssm_p] + [_vp] * 8 + [i] + [_vp] * 4,
+            "kda_short_conv_prompt": [i] * 5 + [_vp, i64] + [_vp] * 4 + [i] + [_vp] * 4,
+            "kda_short_conv_step": [i] * 4 + [_vp, i64] + [_vp] * 3 + [i] + [_vp] * 4,
+            "kda_pages_workspace_size": [pages_p, i],
+            "kda_pages_copy": [i, i64, _vp, i64, i, _vp, i64, i, _vp, _vp, i, _vp],
+            "kda_pages_fork": [pages_p] + [_vp] * 6 + [i] + [_vp] * 4 + [_vp, sz, _vp],
+            "kda_pages_extend": [pages_p] + [_vp] * 5 + [i] + [_vp] * 4 + [_vp, sz, _vp],
+            "kda_pages_free": [pages_p] + [_vp] * 4 + [i] + [_vp] * 4,
+            "kda_pages_compact": [pages_p] + [_vp] * 6 + [_vp, sz, _vp],
+        }
+        for name, types in serving.items():
+            fn = getattr(lib, name)
+            fn.restype = sz if name.endswith("_workspace_size") else i
+            fn.argtypes = types
         _lib = lib
         return lib
 
@@ -455,3 +491,375 @@ def gated_norm_backward(o, gate, weight, dy, *, eps: float = 1e-6, stream: Optio
                                   _ptr(g["do"]), _ptr(g["dgate"]), _ptr(g["dweight"]), _ptr(ws),
                                   ctypes.c_size_t(ws.numel()), ctypes.c_void_p(st.cuda_stream)), "kda_gated_norm_bwd")
     return g
+
+
+# ---- serving: states carried from prompts to single tokens ----
+
+
+def _cuda(*ts):
+    """Every tensor given is on one CUDA device; returns it."""
+    dev = ts[0].device
+    if dev.type != "cuda":
+        raise ValueError("KDA inputs must be CUDA tensors")
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError("all tensors of a call must be on one CUDA device")
+    return dev
+
+
+def _typed(name: str, t, dtype, shape=None):
+    """A contiguous tensor of the given dtype and shape (None passes)."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _token_stride(name: str, t, lead: int) -> int:
+    """Elements between neighbouring tokens of t, whose first ``lead`` axes are tokens ([B, T] or [B]) and
+    whose other axes are one token's contiguous values: t may be a slice of a wider projection."""
+    want = 1
+    for size, stride in zip(reversed(t.shape[lead:]), reversed(t.stride()[lead:])):
+        if size > 1 and stride != want:
+            raise ValueError(f"{name}: the values of one token must be contiguous")
+        want *= size
+    shape, strides = t.shape[:lead], t.stride()[:lead]
+    step = None
+    for size, stride in zip(reversed(shape), reversed(strides)):
+        if size > 1:
+            if step is None:
+                step, span = stride, stride * size
+            elif stride != span:
+                raise ValueError(f"{name}: tokens must be evenly spaced over the leading axes")
+            else:
+                span = stride * size
+    return want if step is None else step
+
+
+class _OnStream:
+    """The stream a call runs on: the given one or the current one.  Inside, torch allocates for that
+    stream, so buffers made there are safe to use and to drop there."""
+
+    def __init__(self, device, stream):
+        self.given = stream
+        self.ptr = (stream or torch.cuda.current_stream(device)).cuda_stream
+        self.ctx = None
+
+    def __enter__(self):
+        if self.given is not None:
+            self.ctx = torch.cuda.stream(self.given)
+            self.ctx.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+    def workspace(self, device, kind: str, nbytes: int) -> torch.Tensor:
+        """One buffer per device, kind and stream: calls on different streams may overlap."""
+        return workspace_cache.get(device, f"{kind}@{self.ptr}", nbytes)
+
+
+def _out(name: str, t, like_shape, dtype, device):
+    if t is None:
+        return torch.empty(like_shape, dtype=dtype, device=device)
+    _typed(name, t, dtype, like_shape)
+    return t
+
+
+def _ssm_dims(x, dt_raw, b, c, a_log, dt_bias, d_skip, lead: int, num_seqs: int) -> SsmDims:
+    H, P = x.shape[lead:]
+    G, N = b.shape[lead:]
+    tokens = tuple(x.shape[:lead])
+    if tuple(b.shape[:lead]) != tokens or c.shape != b.shape or tuple(dt_raw.shape) != (*tokens, H):
+        raise ValueError("x must be [..., H, P], b and c [..., G, N] and dt_raw [..., H] over the same tokens")
+    if G < 1 or H % G:
+        raise ValueError(f"heads ({H}) must be a multiple of the groups of b and c ({G})")
+    if not x.dtype == b.dtype == c.dtype == dt_raw.dtype:
+        raise ValueError("x, b, c and dt_raw must have one dtype")
+    for name, t in (("a_log", a_log), ("dt_bias", dt_bias), ("d_skip", d_skip)):
+        _typed(name, t, torch.float32, (H,))
+    B, T = (tokens if lead == 2 else (tokens[0], 1))
+    return SsmDims(B, T, H, G, N, P, _dtype_code(x), num_seqs, _token_stride("x", x, lead), _token_stride("b", b, lead),
+                   _token_stride("c", c, lead), _token_stride("dt_raw", dt_raw, lead))
+
+
+def ssm_scan(x, dt_raw, b, c, a_log, dt_bias, d_skip=None, *, cu_seqlens=None, cu_seqlens_host=None,
+             initial_state=None, output_final_state: bool = False, out=None, final_state=None,
+             stream: Optional[torch.cuda.Stream] = None):
+    """Selective state space scan over prompts through ``kda_ssm_fwd``.  Returns (y, final_state or None).
+
+    x [B, T, H, P], b and c [B, T, G, N], dt_raw [B, T, H] (bf16 or fp32, one dtype; slices of a wider
+    projection are taken as they are); a_log, dt_bias, d_skip [H] fp32; states [rows, H, N, P] fp32 with
+    rows = B, or one per document of ``cu_seqlens`` (int32).
+        S_t = exp(D_t a) S_{t-1} + D_t b_t x_t^T,  y_t = S_t^T c_t + d_skip x_t,
+        D = softplus(dt_raw + dt_bias), a = -exp(a_log)."""
+    lib = load()
+    dev = _cuda(x, dt_raw, b, c, a_log, dt_bias, d_skip, cu_seqlens, initial_state)
+    if x.dim() != 4 or b.dim() != 4:
+        raise ValueError("x must be [B, T, H, P] and b [B, T, G, N]")
+    _typed("cu_seqlens", cu_seqlens, torch.int32)
+    n = int(cu_seqlens.numel() - 1) if cu_seqlens is not None else 0
+    dims = _ssm_dims(x, dt_raw, b, c, a_log, dt_bias, d_skip, 2, n)
+    rows = n if cu_seqlens is not None else dims.B
+    _typed("initial_state", initial_state, torch.float32, (rows, dims.H, dims.N, dims.P))
+    cu_h = host_offsets(cu_seqlens_host, rows + 1 if cu_seqlens is not None else None)
+    with _OnStream(dev, stream) as st:
+        out = _out("out", out, x.shape, x.dtype, dev)
+        if output_final_state:
+            final_state = _out("final_state", final_state, (rows, dims.H, dims.N, dims.P), torch.float32, dev)
+        else:
+            final_state = None
+        ws = st.workspace(dev, "ssm", int(lib.kda_ssm_fwd_workspace_size(ctypes.byref(dims))))
+        _check(lib.kda_ssm_fwd(ctypes.byref(dims), _ptr(x), _ptr(dt_raw), _ptr(b), _ptr(c), _ptr(a_log), _ptr(dt_bias),
+                               _ptr(d_skip), _ptr(cu_seqlens), cu_h, _ptr(initial_state), _ptr(out), _ptr(final_state),
+                               _ptr(ws), ws.numel(), st.ptr), "kda_ssm_fwd")
+    return out, final_state
+
+
+def _pool(name, pool, slots, B: int, cell, dtype, pool_out):
+    """Checks of a slot pool [num_slots, *cell]; returns (num_slots, the pool written)."""
+    if pool.dim() != 1 + len(cell) or tuple(pool.shape[1:]) != tuple(cell):
+        raise ValueError(f"{name} must be [slots, {', '.join(map(str, cell))}], got {list(pool.shape)}")
+    _typed(name, pool, dtype)
+    _typed("slots", slots, torch.int32, (B,))
+    if pool_out is None:
+        pool_out = pool
+    _typed(f"{name}_out", pool_out, dtype, pool.shape)
+    return int(pool.shape[0]), pool_out
+
+
+def ssm_step(x, dt_raw, b, c, a_log, dt_bias, d_skip=None, *, state, slots=None, state_out=None, out=None,
+             stream: Optional[torch.cuda.Stream] = None):
+    """One token per row through ``kda_ssm_step``: x [B, H, P], b, c [B, G, N], dt_raw [B, H].
+
+    ``state`` [slots, H, N, P] fp32 is the pool, row r works on slot ``slots[r]`` (int32; None: slot r; negative:
+    the row is idle and gets zeros).  The pool is updated in place, or into ``state_out`` (only the named slots
+    are written).  Returns (y, the pool written)."""
+    lib = load()
+    dev = _cuda(x, dt_raw, b, c, a_log, dt_bias, d_skip, state, slots, state_out)
+    if x.dim() != 3 or b.dim() != 3:
+        raise ValueError("x must be [B, H, P] and b [B, G, N]")
+    dims = _ssm_dims(x, dt_raw, b, c, a_log, dt_bias, d_skip, 1, 0)
+    n, state_out = _pool("state", state, slots, dims.B, (dims.H, dims.N, dims.P), torch.float32, state_out)
+    with _OnStream(dev, stream) as st:
+        out = _out("out", out, x.shape, x.dtype, dev)
+        _check(lib.kda_ssm_step(ctypes.byref(dims), _ptr(x), _ptr(dt_raw), _ptr(b), _ptr(c), _ptr(a_log), _ptr(dt_bias),
+                                _ptr(d_skip), _ptr(slots), n, _ptr(state), _ptr(state_out), _ptr(out), st.ptr),
+               "kda_ssm_step")
+    return out, state_out
+
+
+def decode_step(q, k, v, g_raw, beta_raw, a_log, dt_bias, *, scale: float, lower_bound: float = -5.0,
+                gate: str = "lower_bounded", state, slots=None, state_out=None, out=None,
+                stream: Optional[torch.cuda.Stream] = None):
+    """The delta rule for one token per row through ``kda_decode_step``: :func:`forward` at T = 1 on a pool.
+
+    q, k [B, Hk, K], v [B, H, V], g_raw [B, H, K], beta_raw [B, H]; ``state`` [slots, H, K, V] fp32, ``slots``,
+    ``state_out`` as for :func:`ssm_step`.  Returns (out, the pool written)."""
+    lib = load()
+    dev = _cuda(q, k, v, g_raw, beta_raw, a_log, dt_bias, state, slots, state_out)
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q must be [B, Hk, K] and v [B, H, V]")
+    B, Hk, K = q.shape
+    H, V = v.shape[1:]
+    for name, t, shape in (("q", q, (B, Hk, K)), ("k", k, (B, Hk, K)), ("v", v, (B, H, V)), ("g_raw", g_raw, (B, H, K)),
+                           ("beta_raw", beta_raw, (B, H))):
+        _typed(name, t, q.dtype, shape)
+    _typed("a_log", a_log, torch.float32, (H,))
+    _typed("dt_bias", dt_bias, torch.float32, (H * K,))
+    n, state_out = _pool("state", state, slots, B, (H, K, V), torch.float32, state_out)
+    dims = KdaDims(B, 1, H, K, V, _dtype_code(q), 0, Hk, _gate_code(gate))
+    with _OnStream(dev, stream) as st:
+        out = _out("out", out, v.shape, v.dtype, dev)
+        _check(lib.kda_decode_step(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(g_raw), _ptr(beta_raw), _ptr(a_log),
+                                   _ptr(dt_bias), float(scale), float(lower_bound), _ptr(slots), n, _ptr(state),
+                                   _ptr(state_out), _ptr(out), st.ptr), "kda_decode_step")
+    return out, state_out
+
+
+def short_conv_prompt(x, weight, bias=None, *, cu_seqlens=None, cu_seqlens_host=None, initial_history=None, out=None,
+                      final_history=None, stream: Optional[torch.cuda.Stream] = None):
+    """:func:`short_conv` with a carried history, through ``kda_short_conv_prompt``.  Returns (y, final_history).
+
+    x [B, T, C] (a slice of a wider projection is taken as it is); histories [rows, W - 1, C] like x, oldest input
+    first: the last W - 1 inputs before the row (None: zeros) and at its end."""
+    lib = load()
+    dev = _cuda(x, weight, bias, cu_seqlens, initial_history)
+    if x.dim() != 3:
+        raise ValueError("x must be [B, T, C]")
+    B, T, C = x.shape
+    W = weight.shape[-1]
+    _typed("weight", weight, torch.float32)
+    if weight.numel() != C * W:
+        raise ValueError("weight must be [C, W]")
+    _typed("bias", bias, torch.float32, (C,))
+    _typed("cu_seqlens", cu_seqlens, torch.int32)
+    n = int(cu_seqlens.numel() - 1) if cu_seqlens is not None else 0
+    rows = n if cu_seqlens is not None else B
+    _typed("initial_history", initial_history, x.dtype, (rows, W - 1, C))
+    xs = _token_stride("x", x, 2)
+    cu_h = host_offsets(cu_seqlens_host, rows + 1 if cu_seqlens is not None else None)
+    with _OnStream(dev, stream) as st:
+        out = _out("out", out, x.shape, x.dtype, dev)
+        final_history = _out("final_history", final_history, (rows, W - 1, C), x.dtype, dev)
+        _check(lib.kda_short_conv_prompt(B, T, C, W, _dtype_code(x), _ptr(x), xs, _ptr(weight), _ptr(bias),
+                                         _ptr(cu_seqlens), cu_h, n, _ptr(initial_history), _ptr(out),
+                                         _ptr(final_history), st.ptr), "kda_short_conv_prompt")
+    return out, final_history
+
+
+def short_conv_step(x, weight, bias=None, *, history, slots=None, history_out=None, out=None,
+                    stream: Optional[torch.cuda.Stream] = None):
+    """One token per row through ``kda_short_conv_step``: x [B, C], ``history`` [slots, W - 1, C] like x; ``slots``
+    and ``history_out`` as for :func:`ssm_step`.  Returns (y, the pool written)."""
+    lib = load()
+    dev = _cuda(x, weight, bias, history, slots, history_out)
+    if x.dim() != 2:
+        raise ValueError("x must be [B, C]")
+    B, C = x.shape
+    W = weight.shape[-1]
+    _typed("weight", weight, torch.float32)
+    if weight.numel() != C * W:
+        raise ValueError("weight must be [C, W]")
+    _typed("bias", bias, torch.float32, (C,))
+    n, history_out = _pool("history", history, slots, B, (W - 1, C), x.dtype, history_out)
+    xs = _token_stride("x", x, 1)
+    with _OnStream(dev, stream) as st:
+        out = _out("out", out, x.shape, x.dtype, dev)
+        _check(lib.kda_short_conv_step(B, C, W, _dtype_code(x), _ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(slots), n,
+                                       _ptr(history), _ptr(history_out), _ptr(out), st.ptr), "kda_short_conv_step")
+    return out, history_out
+
+
+def _pool_layers(name: str, pool):
+    """(layers, pages, bytes of a page, bytes between layers) of a pool [layers, pages, ...]."""
+    if pool.dim() < 2 or pool.numel() == 0:
+        raise ValueError(f"{name} must be [layers, pages, ...]")
+    if not pool[0].is_contiguous():
+        raise ValueError(f"{name}: the pages of a layer must be contiguous")
+    es = pool.element_size()
+    page = pool[0, 0].numel() * es
+    return int(pool.shape[0]), int(pool.shape[1]), page, int(pool.stride(0)) * es
+
+
+def _pages_dims(pool, table, lengths, refs, page_tokens: int) -> PagesDims:
+    if table.dim() != 2:
+        raise ValueError("table must be [sequences, pages of a row]")
+    _typed("table", table, torch.int32)
+    _typed("lengths", lengths, torch.int32, (table.shape[0],))
+    _typed("refs", refs, torch.int32)
+    d = PagesDims(1, refs.numel(), table.shape[0], table.shape[1], int(page_tokens), 1, 0)
+    if pool is not None:
+        layers, pages, page, stride = _pool_layers("pool", pool)
+        if pages != refs.numel():
+            raise ValueError(f"refs must hold one count per page ({pages}), got {refs.numel()}")
+        d.layers, d.page_bytes, d.layer_stride = layers, page, stride
+    return d
+
+
+def _pages_outs(table, lengths, refs, table_out, lengths_out, refs_out):
+    outs = []
+    for name, t, o in (("table", table, table_out), ("lengths", lengths, lengths_out), ("refs", refs, refs_out)):
+        o = t if o is None else o
+        _typed(f"{name}_out", o, torch.int32, t.shape if t is not None else None)
+        outs.append(o)
+    return outs
+
+
+def _requests(**named):
+    n = None
+    for name, t in named.items():
+        if t.dim() != 1:
+            raise ValueError(f"{name} must be one-dimensional")
+        _typed(name, t, torch.int32)
+        if n is not None and t.numel() != n:
+            raise ValueError(f"{' and '.join(named)} must have the same length")
+        n = t.numel()
+    return n
+
+
+def pages_copy(pool, src, dst, *, src_pool=None, stream: Optional[torch.cuda.Stream] = None):
+    """Page ``src[i]`` of ``src_pool`` (default: ``pool``) to page ``dst[i]`` of ``pool`` [layers, pages, ...], every
+    layer, through ``kda_pages_copy``.  Pairs out of range are skipped; dst must not repeat nor meet src in one pool."""
+    lib = load()
+    src_pool = pool if src_pool is None else src_pool
+    dev = _cuda(pool, src_pool, src, dst)
+    layers, pages, page, stride = _pool_layers("pool", pool)
+    s_layers, s_pages, s_page, s_stride = _pool_layers("src_pool", src_pool)
+    if layers != s_layers or page != s_page:
+        raise ValueError("both pools must have the same layers and page size")
+    n = _requests(src=src, dst=dst)
+    with _OnStream(dev, stream) as st:
+        _check(lib.kda_pages_copy(layers, page, _ptr(pool), stride, pages, _ptr(src_pool), s_stride, s_pages, _ptr(src),
+                                  _ptr(dst), n, st.ptr), "kda_pages_copy")
+    return pool
+
+
+def pages_fork(pool, table, lengths, refs, parents, children, *, page_tokens: int, table_out=None, lengths_out=None,
+               refs_out=None, ok=None, stream: Optional[torch.cuda.Stream] = None):
+    """Row ``children[i]`` becomes a copy of row ``parents[i]`` through ``kda_pages_fork``: full pages are shared, a
+    partly filled last page is copied into a free one.  pool [layers, pages, ...], table [sequences, M], lengths
+    [sequences], refs [pages] int32, updated in place or into the ``*_out`` arrays.  Returns ok [n] int32."""
+    lib = load()
+    dev = _cuda(pool, table, lengths, refs, parents, children, table_out, lengths_out, refs_out)
+    dims = _pages_dims(pool, table, lengths, refs, page_tokens)
+    to, lo, ro = _pages_outs(table, lengths, refs, table_out, lengths_out, refs_out)
+    n = _requests(parents=parents, children=children)
+    with _OnStream(dev, stream) as st:
+        ok = _out("ok", ok, (n,), torch.int32, dev)
+        ws = st.workspace(dev, "pages", int(lib.kda_pages_workspace_size(ctypes.byref(dims), n)))
+        _check(lib.kda_pages_fork(ctypes.byref(dims), _ptr(pool), _ptr(table), _ptr(lengths), _ptr(refs), _ptr(parents),
+                                  _ptr(children), n, _ptr(to), _ptr(lo), _ptr(ro), _ptr(ok), _ptr(ws), ws.numel(),
+                                  st.ptr), "kda_pages_fork")
+    return ok
+
+
+def pages_extend(table, lengths, refs, seqs, new_lengths, *, page_tokens: int, table_out=None, lengths_out=None,
+                 refs_out=None, ok=None, stream: Optional[torch.cuda.Stream] = None):
+    """Row ``seqs[i]`` grows to ``new_lengths[i]`` tokens through ``kda_pages_extend``.  Returns ok [n] int32."""
+    lib = load()
+    dev = _cuda(table, lengths, refs, seqs, new_lengths, table_out, lengths_out, refs_out)
+    dims = _pages_dims(None, table, lengths, refs, page_tokens)
+    to, lo, ro = _pages_outs(table, lengths, refs, table_out, lengths_out, refs_out)
+    n = _requests(seqs=seqs, new_lengths=new_lengths)
+    with _OnStream(dev, stream) as st:
+        ok = _out("ok", ok, (n,), torch.int32, dev)
+        ws = st.workspace(dev, "pages", int(lib.kda_pages_workspace_size(ctypes.byref(dims), n)))
+        _check(lib.kda_pages_extend(ctypes.byref(dims), _ptr(table), _ptr(lengths), _ptr(refs), _ptr(seqs),
+                                    _ptr(new_lengths), n, _ptr(to), _ptr(lo), _ptr(ro), _ptr(ok), _ptr(ws), ws.numel(),
+                                    st.ptr), "kda_pages_extend")
+    return ok
+
+
+def pages_free(table, lengths, refs, seqs, *, table_out=None, lengths_out=None, refs_out=None,
+               stream: Optional[torch.cuda.Stream] = None):
+    """Rows ``seqs`` give up their pages through ``kda_pages_free``."""
+    lib = load()
+    dev = _cuda(table, lengths, refs, seqs, table_out, lengths_out, refs_out)
+    dims = _pages_dims(None, table, lengths, refs, 1)
+    to, lo, ro = _pages_outs(table, lengths, refs, table_out, lengths_out, refs_out)
+    n = _requests(seqs=seqs)
+    with _OnStream(dev, stream) as st:
+        _check(lib.kda_pages_free(ctypes.byref(dims), _ptr(table), _ptr(lengths), _ptr(refs), _ptr(seqs), n, _ptr(to),
+                                  _ptr(lo), _ptr(ro), st.ptr), "kda_pages_free")
+
+
+def pages_compact(pool, table, refs, *, table_out=None, refs_out=None, page_map=None,
+                  stream: Optional[torch.cuda.Stream] = None):
+    """Moves the live pages of pool [layers, pages, ...] to the lowest indices through ``kda_pages_compact``; table
+    and refs follow.  Returns page_map [pages] int32: the new index of each page, -1 for a free one."""
+    lib = load()
+    dev = _cuda(pool, table, refs, table_out, refs_out, page_map)
+    dims = _pages_dims(pool, table, None, refs, 1)
+    to, _, ro = _pages_outs(table, None, refs, table_out, None, refs_out)
+    with _OnStream(dev, stream) as st:
+        page_map = _out("page_map", page_map, (dims.num_pages,), torch.int32, dev)
+        ws = st.workspace(dev, "pages", int(lib.kda_pages_workspace_size(ctypes.byref(dims), 0)))
+        _check(lib.kda_pages_compact(ctypes.byref(dims), _ptr(pool), _ptr(table), _ptr(refs), _ptr(to), _ptr(ro),
+                                     _ptr(page_map), _ptr(ws), ws.numel(), st.ptr), "kda_pages_compact")
+    return page_map

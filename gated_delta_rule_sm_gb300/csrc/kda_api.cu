@@ -147,7 +147,7 @@ static TcBwdPlan plan_tc_bwd(const Shape& s) {
     return w;
 }
 
-static kda_status status_ptr(int** out) {
+kda_status status_ptr(int** out) {
     void* p = nullptr;
     if (cudaGetSymbolAddress(&p, g_status_word) != cudaSuccess) return KDA_ERR_CUDA;
     *out = static_cast<int*>(p);
@@ -190,13 +190,17 @@ static void carve(Params& p, const WsPlan& w, void* ws) {
 // `doc_ids_from_cu_seqlens`): N + 1 entries, starting at 0, never decreasing, ending at the token
 // count.  Checked here when the caller hands over a host copy; plan_kernel checks the device array
 // otherwise.
-static kda_status check_cu_host(const Shape& s, const int32_t* cu, const int32_t* cu_host) {
+kda_status check_offsets_host(int rows, int TT, const int32_t* cu, const int32_t* cu_host) {
     if (!cu_host) return KDA_OK;
     if (!cu) return KDA_ERR_INVALID_ARG;   // a host copy of offsets the call does not use
-    if (cu_host[0] != 0 || cu_host[s.N] != s.TT) return KDA_ERR_INVALID_ARG;
-    for (int n = 0; n < s.N; ++n)
+    if (cu_host[0] != 0 || cu_host[rows] != TT) return KDA_ERR_INVALID_ARG;
+    for (int n = 0; n < rows; ++n)
         if (cu_host[n + 1] < cu_host[n]) return KDA_ERR_INVALID_ARG;
     return KDA_OK;
+}
+
+static kda_status check_cu_host(const Shape& s, const int32_t* cu, const int32_t* cu_host) {
+    return check_offsets_host(s.N, s.TT, cu, cu_host);
 }
 
 static kda_status common_checks(const kda_dims* dims, int chunk_size, const int32_t* cu, const int32_t* cu_host,
@@ -280,7 +284,11 @@ static const char* kKernelNames[] = {"kda_plan",          "kda_intra_simt",   "k
                                      "kda_chain_rec_tc",  "kda_group_sum",    "kda_short_conv_fwd",
                                      "kda_short_conv_bwd", "kda_short_conv_reduce", "kda_diag_tc",
                                      "kda_seg_combine",   "kda_gated_norm_fwd", "kda_gated_norm_bwd",
-                                     "kda_gated_norm_reduce"};
+                                     "kda_gated_norm_reduce", "kda_decode_step",  "kda_ssm_step",
+                                     "kda_short_conv_prompt", "kda_short_conv_step", "kda_ssm_plan",
+                                     "kda_ssm_state",     "kda_ssm_join",     "kda_ssm_out",
+                                     "kda_pages_count",   "kda_pages_assign", "kda_pages_apply",
+                                     "kda_pages_copy"};
 
 // saved != NULL: also keep the fp32 backward record there (kda_fwd_save)
 static kda_status fwd_tc(const Shape& s, Params p, void* ws, size_t ws_bytes, cudaStream_t stream,

@@ -1,0 +1,303 @@
+// kda_hist.cu -- the short convolution with a carried history: prompts that go on from the last W - 1
+// inputs of what came before, and single tokens on a pool of histories.
+//
+//     a[t, c] = bias[c] + sum_{i < W} weight[c, i] x[t - (W - 1) + i, c],    y = a * sigmoid(a)
+// with x at negative times taken from the history.  Bound by memory: x read once, y written once.  A
+// thread owns eight channels over a tile of tokens and keeps the last W - 1 inputs in registers.
+#include <math.h>
+#include <string.h>
+
+#include "kda.h"
+#include "kda_common.cuh"
+#include "kda_internal.h"
+#include "kda_sm100.cuh"
+
+namespace kda {
+
+using namespace sm100;
+
+namespace {
+
+constexpr int kHistMaxW = 8;
+constexpr int kHistTile = 64;       // tokens per CTA
+constexpr int kHistThreads = 128;   // x 8 channels
+
+struct HistArgs {
+    int TT, T, C, W, dtype, rows, tiles, num_slots;
+    int64_t xs;            // elements between tokens of x
+    const void* x;
+    const float* w;        // [C, W]
+    const float* b;        // [C] or nullptr
+    const int32_t* cu;     // [rows + 1] or nullptr
+    const int32_t* slots;
+    const void* h_in;      // [rows or num_slots, W - 1, C] or nullptr
+    void* h_out;           // likewise
+    void* y;               // [TT, C]
+    int* status;
+};
+
+template <typename T> struct Raw8;
+template <> struct Raw8<__nv_bfloat16> {
+    uint4 u;
+    __device__ __forceinline__ void load(const void* p, size_t i) {
+        u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
+    }
+    __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void store(void* p, size_t i) const {
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + i) = u;
+    }
+    __device__ __forceinline__ void get(float* v) const {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[2 * k] = __uint_as_float(w[k] << 16);
+            v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+        }
+    }
+    __device__ __forceinline__ void put(const float* v) { u = pack8_bf16(v); }
+};
+template <> struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const void* p, size_t i) {
+        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+        a = f[0];
+        b = f[1];
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void store(void* p, size_t i) const {
+        float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+        f[0] = a;
+        f[1] = b;
+    }
+    __device__ __forceinline__ void get(float* v) const {
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+    __device__ __forceinline__ void put(const float* v) {
+        a = make_float4(v[0], v[1], v[2], v[3]);
+        b = make_float4(v[4], v[5], v[6], v[7]);
+    }
+};
+
+template <int W>
+__device__ __forceinline__ void load_weights(const HistArgs& a, int c0, float (*w)[W], float* bias) {
+    const float* src = a.w + (size_t)c0 * W;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        bias[e] = a.b ? a.b[c0 + e] : 0.f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[e][i] = src[e * W + i];
+    }
+}
+
+// silu(bias + w . window), the newest input last
+template <int W, typename R>
+__device__ __forceinline__ void conv_out(const float (*w)[W], const float* bias, const float (*win)[8], R& out) {
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        float acc = bias[e];
+#pragma unroll
+        for (int i = 0; i < W; ++i) acc = fmaf(w[e][i], win[i][e], acc);
+        y[e] = acc * __fdividef(1.f, 1.f + __expf(-acc));
+    }
+    out.put(y);
+}
+
+// Whether the offsets keep the contract; the same answer in every thread.  A CTA reads them all: they are
+// few next to its tokens, and no separate pass has to run first.
+__device__ __forceinline__ bool offsets_ok(const HistArgs& a) {
+    bool bad = false;
+    for (int n = threadIdx.x; n < a.rows; n += kHistThreads) bad |= a.cu[n + 1] < a.cu[n];
+    if (threadIdx.x == 0) bad |= a.cu[0] != 0 || a.cu[a.rows] != a.TT;
+    return !__syncthreads_or(bad);
+}
+
+__device__ __forceinline__ int row_begin(const HistArgs& a, int n) { return a.cu ? a.cu[n] : n * a.T; }
+
+// CTAs below `tiles` take 64 tokens each; the others write the final history of one row each.
+template <int W, typename E>
+__global__ void __launch_bounds__(kHistThreads) conv_prompt_kernel(HistArgs a) {
+    if (a.cu && !offsets_ok(a)) {
+        if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) record_error(a.status, KDA_ERR_INVALID_ARG);
+        return;
+    }
+    const int c0 = (blockIdx.y * kHistThreads + threadIdx.x) * 8;
+    if (c0 >= a.C) return;
+    Raw8<E> raw;
+    if ((int)blockIdx.x >= a.tiles) {
+        const int n = blockIdx.x - a.tiles;
+        const int s0 = row_begin(a, n), s1 = row_begin(a, n + 1);
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) {
+            const int t = s1 - (W - 1) + i;       // before s0: row i + (s1 - s0) of the old history
+            if (t >= s0) raw.load(a.x, (size_t)t * a.xs + c0);
+            else if (a.h_in) raw.load(a.h_in, ((size_t)n * (W - 1) + i + (s1 - s0)) * a.C + c0);
+            else raw.zero();
+            raw.store(a.h_out, ((size_t)n * (W - 1) + i) * a.C + c0);
+        }
+        return;
+    }
+    float w[8][W], bias[8], win[W][8];
+    load_weights<W>(a, c0, w, bias);
+    const int t0 = blockIdx.x * kHistTile, t1 = min(t0 + kHistTile, a.TT);
+    int n, s0, s1;
+    if (a.cu) {
+        int lo = 0, hi = a.rows - 1;   // last n with cu[n] <= t0
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (a.cu[mid] <= t0) lo = mid; else hi = mid - 1;
+        }
+        n = lo;
+    } else {
+        n = t0 / a.T;
+    }
+    s0 = row_begin(a, n);
+    s1 = row_begin(a, n + 1);
+    auto fill = [&](int t) {   // the W - 1 inputs before token t of row n
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) {
+            const int tau = t - (W - 1) + i;
+            if (tau >= s0) raw.load(a.x, (size_t)tau * a.xs + c0);
+            else if (a.h_in) raw.load(a.h_in, ((size_t)n * (W - 1) + (tau - s0 + W - 1)) * a.C + c0);
+            else raw.zero();
+            raw.get(win[i]);
+        }
+    };
+    fill(t0);
+    for (int t = t0; t < t1; ++t) {
+        if (t == s1) {
+            while (t >= s1) {   // empty rows in between
+                ++n;
+                s0 = s1;
+                s1 = row_begin(a, n + 1);
+            }
+            fill(t);
+        }
+        raw.load(a.x, (size_t)t * a.xs + c0);
+        raw.get(win[W - 1]);
+        Raw8<E> out;
+        conv_out<W>(w, bias, win, out);
+        out.store(a.y, (size_t)t * a.C + c0);
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) win[i][e] = win[i + 1][e];
+    }
+}
+
+// Rows blockIdx.x, blockIdx.x + gridDim.x, ... of the batch with one set of weights.
+template <int W, typename E>
+__global__ void __launch_bounds__(kHistThreads) conv_step_kernel(HistArgs a) {
+    const int c0 = (blockIdx.y * kHistThreads + threadIdx.x) * 8;
+    if (c0 >= a.C) return;
+    float w[8][W], bias[8], win[W][8];
+    load_weights<W>(a, c0, w, bias);
+    for (int r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        int slot = a.slots ? a.slots[r] : r;
+        if (slot >= a.num_slots) {
+            if (c0 == 0) record_error(a.status, KDA_ERR_INVALID_ARG);
+            slot = -1;
+        }
+        Raw8<E> raw[W], out;
+        if (slot < 0) {
+            out.zero();
+            out.store(a.y, (size_t)r * a.C + c0);
+            continue;
+        }
+        const size_t hb = (size_t)slot * (W - 1) * a.C + c0;
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) raw[i].load(a.h_in, hb + (size_t)i * a.C);
+        raw[W - 1].load(a.x, (size_t)r * a.xs + c0);
+#pragma unroll
+        for (int i = 0; i < W; ++i) raw[i].get(win[i]);
+        conv_out<W>(w, bias, win, out);
+        out.store(a.y, (size_t)r * a.C + c0);
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) raw[i + 1].store(a.h_out, hb + (size_t)i * a.C);
+    }
+}
+
+kda_status hist_check(int B, int T, int C, int W, int dtype, const void* x, int64_t xs, const float* weight,
+                      const void* h_in, const void* h_out, const void* y) {
+    if (B < 1 || T < 1 || C < 1 || W < 1) return KDA_ERR_INVALID_ARG;
+    if (dtype != KDA_BF16 && dtype != KDA_FP32) return KDA_ERR_INVALID_ARG;
+    if (!x || !weight || !y || (xs != 0 && xs < C)) return KDA_ERR_INVALID_ARG;
+    if (W > kHistMaxW || C % 8 || xs % 8) return KDA_ERR_UNSUPPORTED;
+    if ((long long)B * T > (1LL << 30) || (long long)B * T * (xs ? xs : C) > (1LL << 40)) return KDA_ERR_UNSUPPORTED;
+    for (const void* p : {x, h_in, h_out, y})
+        if (reinterpret_cast<uintptr_t>(p) % 16) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+}  // namespace
+
+#define KDA_HIST_CASE(KERNEL, w, a, grid, st)                                                      \
+    case w:                                                                                        \
+        if ((a).dtype == KDA_BF16) KERNEL<w, __nv_bfloat16><<<grid, kHistThreads, 0, st>>>(a);     \
+        else KERNEL<w, float><<<grid, kHistThreads, 0, st>>>(a);                                   \
+        break;
+#define KDA_HIST_DISPATCH(KERNEL, a, grid, st)                                                     \
+    switch ((a).W) {                                                                               \
+        KDA_HIST_CASE(KERNEL, 1, a, grid, st)                                                      \
+        KDA_HIST_CASE(KERNEL, 2, a, grid, st)                                                      \
+        KDA_HIST_CASE(KERNEL, 3, a, grid, st)                                                      \
+        KDA_HIST_CASE(KERNEL, 4, a, grid, st)                                                      \
+        KDA_HIST_CASE(KERNEL, 5, a, grid, st)                                                      \
+        KDA_HIST_CASE(KERNEL, 6, a, grid, st)                                                      \
+        KDA_HIST_CASE(KERNEL, 7, a, grid, st)                                                      \
+        KDA_HIST_CASE(KERNEL, 8, a, grid, st)                                                      \
+    }
+
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" {
+
+kda_status kda_short_conv_prompt(int B, int T, int C, int W, kda_dtype dtype, const void* x, int64_t x_stride,
+                                 const float* weight, const float* bias, const int32_t* cu_seqlens,
+                                 const int32_t* cu_seqlens_host, int num_seqs, const void* initial_history, void* y,
+                                 void* final_history, cudaStream_t stream) {
+    kda_status st = hist_check(B, T, C, W, dtype, x, x_stride, weight, initial_history, final_history, y);
+    if (st != KDA_OK) return st;
+    if (cu_seqlens && (B != 1 || num_seqs < 1)) return KDA_ERR_INVALID_ARG;
+    if (cu_seqlens && num_seqs > (1 << 24)) return KDA_ERR_UNSUPPORTED;
+    HistArgs a;
+    memset(&a, 0, sizeof(a));
+    a.TT = B * T; a.T = T; a.C = C; a.W = W; a.dtype = dtype; a.rows = cu_seqlens ? num_seqs : B;
+    st = check_offsets_host(a.rows, a.TT, cu_seqlens, cu_seqlens_host);
+    if (st != KDA_OK) return st;
+    a.xs = x_stride ? x_stride : C;
+    a.x = x; a.w = weight; a.b = bias; a.cu = cu_seqlens; a.h_in = initial_history; a.h_out = final_history; a.y = y;
+    st = status_ptr(&a.status);
+    if (st != KDA_OK) return st;
+    a.tiles = (a.TT + kHistTile - 1) / kHistTile;
+    const dim3 grid(a.tiles + (final_history && W > 1 ? a.rows : 0), (C / 8 + kHistThreads - 1) / kHistThreads);
+    timing_pre(stream, K_CONV_PROMPT);
+    KDA_HIST_DISPATCH(conv_prompt_kernel, a, grid, stream);
+    timing_post(stream);
+    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status kda_short_conv_step(int B, int C, int W, kda_dtype dtype, const void* x, int64_t x_stride,
+                               const float* weight, const float* bias, const int32_t* slots, int num_slots,
+                               const void* history_in, void* history_out, void* y, cudaStream_t stream) {
+    kda_status st = hist_check(B, 1, C, W, dtype, x, x_stride, weight, history_in, history_out, y);
+    if (st != KDA_OK) return st;
+    if (num_slots < 1 || (!slots && num_slots < B)) return KDA_ERR_INVALID_ARG;
+    if (W > 1 && (!history_in || !history_out)) return KDA_ERR_INVALID_ARG;
+    HistArgs a;
+    memset(&a, 0, sizeof(a));
+    a.C = C; a.W = W; a.dtype = dtype; a.rows = B; a.num_slots = num_slots; a.xs = x_stride ? x_stride : C;
+    a.x = x; a.w = weight; a.b = bias; a.slots = slots; a.h_in = history_in; a.h_out = history_out; a.y = y;
+    st = status_ptr(&a.status);
+    if (st != KDA_OK) return st;
+    const int gy = (C / 8 + kHistThreads - 1) / kHistThreads;
+    const int gx = (8 * 152 + gy - 1) / gy;
+    timing_pre(stream, K_CONV_STEP);
+    KDA_HIST_DISPATCH(conv_step_kernel, a, dim3(B < gx ? B : gx, gy), stream);
+    timing_post(stream);
+    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -68,6 +68,8 @@ enum KernelId {
     K_PLAN = 0, K_INTRA_SIMT, K_CHAIN_FWD_SIMT, K_CHAIN_BWD_SIMT, K_GRAD_SIMT, K_PARAM_REDUCE, K_EMPTY_SEG,
     K_INTRA_TC, K_CHAIN_FWD_TC, K_GRAD_TC, K_BWD_PRE, K_CHAIN_BWD_TC, K_CHAIN_REC_TC, K_GROUP_SUM,
     K_CONV_FWD, K_CONV_BWD, K_CONV_REDUCE, K_DIAG_TC, K_SEG_COMBINE, K_NORM_FWD, K_NORM_BWD, K_NORM_REDUCE,
+    K_DECODE_STEP, K_SSM_STEP, K_CONV_PROMPT, K_CONV_STEP, K_SSM_PLAN, K_SSM_STATE, K_SSM_JOIN, K_SSM_OUT,
+    K_PAGES_COUNT, K_PAGES_ASSIGN, K_PAGES_APPLY, K_PAGES_COPY,
     K_NUM_KERNELS
 };
 
@@ -134,6 +136,19 @@ __host__ __device__ constexpr size_t x4_off(int row, int j, int rows) {
 // Launch bracketing for kda_timing_*: no-ops unless timing is active.
 void timing_pre(cudaStream_t st, int kernel_id);
 void timing_post(cudaStream_t st);
+
+// Device address of the status word on the current device.
+kda_status status_ptr(int** out);
+// The packed-document contract on a host copy of the offsets (KDA_OK without one).
+kda_status check_offsets_host(int rows, int TT, const int32_t* cu, const int32_t* cu_host);
+
+// A checked kda_ssm_dims, strides resolved.
+struct SsmShape {
+    int B, T, TT, H, G, N, P, dtype, rows;
+    int64_t xs, bs, cs, ds;
+};
+kda_status ssm_check(const kda_ssm_dims* d, bool varlen, const void* x, const void* dt_raw, const void* b,
+                     const void* c, const float* a_log, const float* dt_bias, SsmShape* s);
 
 cudaError_t launch_plan(const Params& p, cudaStream_t st);
 cudaError_t launch_intra_simt(const Params& p, bool bwd, cudaStream_t st);

@@ -1,0 +1,382 @@
+// kda_ssm.cu -- selective state space scan: arguments, schedule and the fp32 token-by-token kernel.
+//
+//     S_t = exp(D_t a) S_{t-1} + D_t B_t x_t^T,   y_t = S_t^T C_t + d x_t,   D_t = softplus(dt_raw_t + dt_bias)
+// The end state of a span of tokens is affine in its entering state with the scalar factor exp(sum D a),
+// so rows are cut into segments: one pass forms each segment's end state from zero (all segments at
+// once), a join walks each row's segments (fp32, elementwise), and a second pass forms the outputs from
+// the entering states.  Rows of one segment, and calls with enough rows x heads to fill the GPU, take the
+// output pass alone.
+#include <math.h>
+#include <string.h>
+
+#include "kda.h"
+#include "kda_ssm.h"
+
+namespace kda {
+
+kda_status ssm_check(const kda_ssm_dims* d, bool varlen, const void* x, const void* dt_raw, const void* b,
+                     const void* c, const float* a_log, const float* dt_bias, SsmShape* s) {
+    if (!d) return KDA_ERR_INVALID_ARG;
+    if (d->B < 1 || d->T < 1 || d->H < 1 || d->G < 1 || d->H % d->G || d->N < 1 || d->P < 1) return KDA_ERR_INVALID_ARG;
+    if (d->dtype != KDA_BF16 && d->dtype != KDA_FP32) return KDA_ERR_INVALID_ARG;
+    if (!x || !dt_raw || !b || !c || !a_log || !dt_bias) return KDA_ERR_INVALID_ARG;
+    const int64_t xw = (int64_t)d->H * d->P, bw = (int64_t)d->G * d->N;
+    if ((d->x_stride && d->x_stride < xw) || (d->b_stride && d->b_stride < bw) || (d->c_stride && d->c_stride < bw) ||
+        (d->dt_stride && d->dt_stride < d->H))
+        return KDA_ERR_INVALID_ARG;
+    if (varlen && (d->B != 1 || d->num_seqs < 1)) return KDA_ERR_INVALID_ARG;
+    if (d->N > 256 || d->P > 256) return KDA_ERR_UNSUPPORTED;
+    if (varlen && d->num_seqs > (1 << 24)) return KDA_ERR_UNSUPPORTED;
+    const long long TT = (long long)d->B * d->T;
+    if (TT > (1LL << 30) || xw > (1 << 30) || bw > (1 << 30)) return KDA_ERR_UNSUPPORTED;
+    s->B = d->B; s->T = d->T; s->TT = (int)TT; s->H = d->H; s->G = d->G; s->N = d->N; s->P = d->P;
+    s->dtype = d->dtype; s->rows = varlen ? d->num_seqs : d->B;
+    s->xs = d->x_stride ? d->x_stride : xw;
+    s->bs = d->b_stride ? d->b_stride : bw;
+    s->cs = d->c_stride ? d->c_stride : bw;
+    s->ds = d->dt_stride ? d->dt_stride : d->H;
+    int64_t most = s->xs > s->bs ? s->xs : s->bs;
+    if (s->cs > most) most = s->cs;
+    if (s->ds > most) most = s->ds;
+    if (most > (1LL << 40) / TT) return KDA_ERR_UNSUPPORTED;
+    if ((long long)s->rows * d->H > (1LL << 30)) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+namespace {
+
+// ------------------------------------------------------------------ schedule
+
+constexpr int kSsmMinSeg = 512;    // tokens: a shorter segment spends more on its state than on its tokens
+
+struct Schedule {
+    int L, per_row, nseg;
+    bool single;
+    size_t off_seg, off_row, off_decay, off_states, total;
+};
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Segments of L tokens such that rows x segments x heads x `ctas` CTAs per (segment, head) fill the GPU
+// about twice; single where the rows alone do.
+Schedule make_schedule(const SsmShape& s, bool varlen, int ctas_per_head) {
+    Schedule w;
+    memset(&w, 0, sizeof(w));
+    const int64_t span = varlen ? (s.TT + s.rows - 1) / s.rows : s.T;
+    const int64_t units = (int64_t)s.rows * s.H * ctas_per_head;
+    int64_t want = units >= 304 ? 1 : (304 + units - 1) / units;   // segments per row
+    const int64_t most = (span + kSsmMinSeg - 1) / kSsmMinSeg;
+    if (want > most) want = most;
+    if (want < 1) want = 1;
+    w.single = want == 1;
+    const int64_t longest = varlen ? s.TT : s.T;
+    w.L = w.single ? (int)((longest + 127) / 128 * 128) : (int)((span + want - 1) / want + 127) / 128 * 128;
+    w.per_row = varlen ? 0 : (s.T + w.L - 1) / w.L;
+    w.nseg = varlen ? (w.single ? s.rows : s.rows + s.TT / w.L) : s.rows * w.per_row;
+    if (!varlen && w.per_row == 1) w.single = true;
+    size_t o = 0;
+    if (varlen) {
+        w.off_seg = o; o = up256(o + sizeof(SsmSeg) * (size_t)w.nseg);
+        w.off_row = o; o = up256(o + sizeof(int32_t) * ((size_t)s.rows + 1));
+    }
+    if (!w.single) {
+        w.off_decay = o; o = up256(o + sizeof(float) * (size_t)w.nseg * s.H);
+        w.off_states = o; o = up256(o + sizeof(float) * (size_t)w.nseg * s.H * s.N * s.P);
+    }
+    w.total = o;
+    return w;
+}
+
+int ctas_per_head(const SsmShape& s) { return (s.P + 31) / 32; }
+
+// Segments of every row in order: ceil(len / L) of them, one empty segment for an empty row (its state
+// passes through).  Offsets that break the contract are recorded and give every row one empty segment.
+__global__ void __launch_bounds__(1024) ssm_plan_kernel(SsmArgs a, SsmSeg* seg, int32_t* row_seg) {
+    __shared__ int part[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    bool bad = tid == 0 && (a.cu[0] != 0 || a.cu[a.rows] != a.TT);
+    for (int n = tid; n < a.rows; n += 1024) bad |= a.cu[n + 1] < a.cu[n];
+    bad = __syncthreads_or(bad);
+    if (bad && tid == 0) record_error(a.status, KDA_ERR_INVALID_ARG);
+    int carry = 0;
+    for (int n0 = 0; n0 < a.rows; n0 += 1024) {
+        const int n = n0 + tid;
+        int b0 = 0, len = 0, cnt = 0;
+        if (n < a.rows) {
+            if (!bad) {
+                b0 = a.cu[n];
+                len = a.cu[n + 1] - b0;
+            }
+            cnt = len > 0 ? (len - 1) / a.L + 1 : 1;
+        }
+        int inc = cnt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        __syncthreads();
+        if (lane == 31) part[warp] = inc;
+        __syncthreads();
+        if (warp == 0) {
+            int v = part[lane];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += u;
+            }
+            part[lane] = v;
+        }
+        __syncthreads();
+        const int first = carry + inc - cnt + (warp ? part[warp - 1] : 0);
+        carry += part[31];
+        if (n < a.rows) {
+            row_seg[n] = first;
+            for (int k = 0; k < cnt; ++k) {
+                SsmSeg s;
+                s.n = n;
+                s.k = k;
+                s.t0 = b0 + k * a.L;
+                s.t1 = (int)min((long long)b0 + len, (long long)s.t0 + a.L);
+                if (first + k < a.nseg) seg[first + k] = s;
+            }
+        }
+    }
+    if (tid == 0) row_seg[a.rows] = carry;
+    for (int i = carry + tid; i < a.nseg; i += 1024) {
+        SsmSeg s;
+        s.n = -1;
+        s.t0 = s.t1 = s.k = 0;
+        seg[i] = s;
+    }
+}
+
+// Entering states of a row's segments: S <- decay_k S + loc_k, in place of loc_k.  Elementwise over the
+// state: one thread per element, the next segment's value in flight while this one is used.
+__global__ void __launch_bounds__(256) ssm_join_kernel(SsmArgs a) {
+    const int np = a.N * a.P;
+    const int e = blockIdx.y * 256 + threadIdx.x;
+    const int n = blockIdx.x / a.H, h = blockIdx.x - n * a.H;
+    if (e >= np) return;
+    int first;
+    const int segs = ssm_row_segments(a, n, &first);
+    float S = a.S0 ? a.S0[((size_t)n * a.H + h) * np + e] : 0.f;
+    for (int k = 0; k < segs; ++k) {
+        float* p = a.states + ((size_t)(first + k) * a.H + h) * np + e;
+        // the last segment's end state comes from the output pass
+        const float loc = k + 1 < segs ? *p : 0.f;
+        const float d = k + 1 < segs ? a.decay[(size_t)(first + k) * a.H + h] : 0.f;
+        *p = S;
+        S = fmaf(d, S, loc);
+    }
+}
+
+// ------------------------------------------------------------------ fp32 kernel
+//
+// A CTA takes one (segment, head, 32 columns of P); a warp four columns, eight lanes each, a lane
+// N / 8 state values of its column in registers (groups of four n, eight lanes apart, so that the
+// 16-byte reads of B and C from shared memory are free of conflicts).  Per token and state value: one
+// multiply and two fused multiply-adds; the eight lanes' partial outputs of eight tokens are summed
+// together (seven shuffles for eight tokens).  Bound by issue: about 2.5 instructions per state value.
+constexpr int kSimtTok = 16, kSimtCols = 32;
+
+template <int NJ, bool OUT>
+__global__ void __launch_bounds__(256) ssm_simt_kernel(SsmArgs a) {
+    constexpr int NP = 32 * NJ;
+    __shared__ __align__(16) float sb[kSimtTok][NP], sc[OUT ? kSimtTok : 1][NP];
+    __shared__ float sx[kSimtTok][kSimtCols], sy[kSimtTok][kSimtCols], sal[kSimtTok], sdt[kSimtTok];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int slice = lane & 7, pc = warp * 4 + (lane >> 3);
+    const int h = blockIdx.y, p0 = blockIdx.z * kSimtCols, p = p0 + pc;
+    const SsmSeg sg = ssm_segment(a, blockIdx.x);
+    if (sg.n < 0) return;
+    if (!OUT) {   // the last segment's end state comes from the output pass
+        int first;
+        const int segs = ssm_row_segments(a, sg.n, &first);
+        if ((int)blockIdx.x == first + segs - 1) return;
+    }
+    const bool pin = p < a.P;
+    const int g = h / (a.H / a.G);
+    const float ea = expf(a.a_log[h]), bias = a.dt_bias[h];
+    const float dsk = OUT && a.d_skip ? a.d_skip[h] : 0.f;
+    float S[NJ][4];
+    const float* from = OUT ? ssm_entering(a, sg, blockIdx.x, h) : nullptr;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int n = (j * 8 + slice) * 4 + e;
+            S[j][e] = from && pin && n < a.N ? from[(size_t)n * a.P + p] : 0.f;
+        }
+    float lsum = 0.f;
+    for (int t0 = sg.t0; t0 < sg.t1; t0 += kSimtTok) {
+        const int nt = min(kSimtTok, sg.t1 - t0);
+        __syncthreads();
+        for (int i = tid; i < kSimtTok * NP; i += 256) {
+            const int t = i / NP, n = i - t * NP;
+            const bool in = t < nt && n < a.N;
+            sb[t][n] = in ? load_act(a.b, (size_t)(t0 + t) * a.bs + (size_t)g * a.N + n, a.dtype) : 0.f;
+            if (OUT) sc[t][n] = in ? load_act(a.c, (size_t)(t0 + t) * a.cs + (size_t)g * a.N + n, a.dtype) : 0.f;
+        }
+        for (int i = tid; i < kSimtTok * kSimtCols; i += 256) {
+            const int t = i / kSimtCols, c = i - t * kSimtCols;
+            sx[t][c] = t < nt && p0 + c < a.P
+                           ? load_act(a.x, (size_t)(t0 + t) * a.xs + (size_t)h * a.P + p0 + c, a.dtype) : 0.f;
+        }
+        if (tid < kSimtTok) {
+            const float dt = tid < nt ? softplusf(load_act(a.dt, (size_t)(t0 + tid) * a.ds + h, a.dtype) + bias) : 0.f;
+            sdt[tid] = dt;
+            sal[tid] = expf(-ea * dt);   // a token past the end keeps the state
+            if (!OUT) lsum += dt;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int t8 = 0; t8 < kSimtTok; t8 += 8) {
+            float y[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int t = t8 + u;
+                const float al = sal[t], ux = sdt[t] * sx[t][pc];
+                float acc = 0.f;
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    const float4 b4 = *reinterpret_cast<const float4*>(&sb[t][(j * 8 + slice) * 4]);
+                    S[j][0] = fmaf(al, S[j][0], ux * b4.x);
+                    S[j][1] = fmaf(al, S[j][1], ux * b4.y);
+                    S[j][2] = fmaf(al, S[j][2], ux * b4.z);
+                    S[j][3] = fmaf(al, S[j][3], ux * b4.w);
+                    if (OUT) {
+                        const float4 c4 = *reinterpret_cast<const float4*>(&sc[t][(j * 8 + slice) * 4]);
+                        acc = fmaf(S[j][0], c4.x, acc);
+                        acc = fmaf(S[j][1], c4.y, acc);
+                        acc = fmaf(S[j][2], c4.z, acc);
+                        acc = fmaf(S[j][3], c4.w, acc);
+                    }
+                }
+                y[u] = acc;
+            }
+            if (OUT) {   // lane `slice` ends with the sum of token t8 + slice
+#pragma unroll
+                for (int w = 4; w >= 1; w >>= 1) {
+                    const bool up = slice & w;
+#pragma unroll
+                    for (int i = 0; i < w; ++i) {
+                        const float send = up ? y[i] : y[i + w], keep = up ? y[i + w] : y[i];
+                        y[i] = keep + __shfl_xor_sync(0xffffffffu, send, w);
+                    }
+                }
+                sy[t8 + slice][pc] = fmaf(dsk, sx[t8 + slice][pc], y[0]);
+            }
+        }
+        if (OUT) {
+            __syncthreads();
+            for (int i = tid; i < nt * kSimtCols; i += 256) {
+                const int t = i / kSimtCols, c = i - t * kSimtCols;
+                if (p0 + c < a.P) store_act(a.y, ((size_t)(t0 + t) * a.H + h) * a.P + p0 + c, sy[t][c], a.dtype);
+            }
+        }
+    }
+    float* to = OUT ? ssm_leaving(a, sg, blockIdx.x, h) : a.states + ((size_t)blockIdx.x * a.H + h) * a.N * a.P;
+    if (to && pin)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int n = (j * 8 + slice) * 4 + e;
+                if (n < a.N) to[(size_t)n * a.P + p] = S[j][e];
+            }
+    if (!OUT && blockIdx.z == 0 && warp == 0) {
+        lsum = warp_sum(lsum);
+        if (lane == 0) a.decay[(size_t)blockIdx.x * a.H + h] = expf(-ea * lsum);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_ssm_simt(const SsmArgs& a, bool out, cudaStream_t st) {
+    const dim3 grid(a.nseg, a.H, (a.P + kSimtCols - 1) / kSimtCols);
+    timing_pre(st, out ? K_SSM_OUT : K_SSM_STATE);
+#define KDA_SSM_SIMT(NJ)                                             \
+    do {                                                             \
+        if (out) ssm_simt_kernel<NJ, true><<<grid, 256, 0, st>>>(a); \
+        else ssm_simt_kernel<NJ, false><<<grid, 256, 0, st>>>(a);    \
+    } while (0)
+    if (a.N <= 32) KDA_SSM_SIMT(1);
+    else if (a.N <= 64) KDA_SSM_SIMT(2);
+    else if (a.N <= 128) KDA_SSM_SIMT(4);
+    else KDA_SSM_SIMT(8);
+    timing_post(st);
+    return cudaGetLastError();
+}
+
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" {
+
+size_t kda_ssm_fwd_workspace_size(const kda_ssm_dims* dims) {
+    SsmShape s;
+    const int some = 0;   // the checks want pointers
+    const float* f = reinterpret_cast<const float*>(&some);
+    if (!dims) return 0;
+    // with num_seqs the larger of the packed and the row layout
+    size_t most = 0;
+    bool valid = false;
+    for (int varlen = 0; varlen < 2; ++varlen) {
+        if (varlen && !(dims->num_seqs > 0 && dims->B == 1)) continue;
+        if (ssm_check(dims, varlen != 0, f, f, f, f, f, f, &s) != KDA_OK) continue;
+        valid = true;
+        const size_t t = make_schedule(s, varlen != 0, ctas_per_head(s)).total;
+        if (t > most) most = t;
+    }
+    return valid ? (most ? most : 256) : 0;
+}
+
+kda_status kda_ssm_fwd(const kda_ssm_dims* dims, const void* x, const void* dt_raw, const void* b, const void* c,
+                       const float* a_log, const float* dt_bias, const float* d_skip, const int32_t* cu_seqlens,
+                       const int32_t* cu_seqlens_host, const float* initial_state, void* y, float* final_state,
+                       void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    SsmShape s;
+    kda_status st = ssm_check(dims, cu_seqlens != nullptr, x, dt_raw, b, c, a_log, dt_bias, &s);
+    if (st != KDA_OK) return st;
+    if (!y) return KDA_ERR_INVALID_ARG;
+    st = check_offsets_host(s.rows, s.TT, cu_seqlens, cu_seqlens_host);
+    if (st != KDA_OK) return st;
+    const Schedule w = make_schedule(s, cu_seqlens != nullptr, ctas_per_head(s));
+    if (workspace_bytes < w.total || (w.total && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256)))
+        return KDA_ERR_WORKSPACE;
+    if (w.nseg > (1 << 30) / s.H || s.H > 65535) return KDA_ERR_UNSUPPORTED;
+    char* ws = static_cast<char*>(workspace);
+    SsmArgs a;
+    memset(&a, 0, sizeof(a));
+    a.T = s.T; a.TT = s.TT; a.H = s.H; a.G = s.G; a.N = s.N; a.P = s.P; a.dtype = s.dtype; a.rows = s.rows;
+    a.xs = s.xs; a.bs = s.bs; a.cs = s.cs; a.ds = s.ds;
+    a.x = x; a.dt = dt_raw; a.b = b; a.c = c; a.a_log = a_log; a.dt_bias = dt_bias; a.d_skip = d_skip;
+    a.S0 = initial_state; a.cu = cu_seqlens; a.y = y; a.ST = final_state;
+    a.L = w.L; a.per_row = w.per_row; a.nseg = w.nseg; a.single = w.single;
+    st = status_ptr(&a.status);
+    if (st != KDA_OK) return st;
+    if (cu_seqlens) {
+        SsmSeg* seg = reinterpret_cast<SsmSeg*>(ws + w.off_seg);
+        int32_t* row = reinterpret_cast<int32_t*>(ws + w.off_row);
+        a.seg = seg;
+        a.row_seg = row;
+        timing_pre(stream, K_SSM_PLAN);
+        ssm_plan_kernel<<<1, 1024, 0, stream>>>(a, seg, row);
+        timing_post(stream);
+        if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+    }
+    if (!w.single) {
+        a.decay = reinterpret_cast<float*>(ws + w.off_decay);
+        a.states = reinterpret_cast<float*>(ws + w.off_states);
+        if (launch_ssm_simt(a, false, stream) != cudaSuccess) return KDA_ERR_CUDA;
+        timing_pre(stream, K_SSM_JOIN);
+        ssm_join_kernel<<<dim3(s.rows * s.H, (s.N * s.P + 255) / 256), 256, 0, stream>>>(a);
+        timing_post(stream);
+        if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+    }
+    return launch_ssm_simt(a, true, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // extern "C"

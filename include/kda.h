@@ -425,6 +425,146 @@ kda_status kda_short_conv_bwd(int B, int T, int C, int W, kda_dtype dtype, const
                               float* dx, float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
                               cudaStream_t stream);
 
+/*
+ * ---- Serving: states carried from prompts to single tokens ----
+ *
+ * Slot pools.  The single-token entries keep the states of many sequences in one pool, [num_slots, ...]
+ * fp32 (or the activations' dtype for convolution histories), and row r of a batch works on slot
+ * slots[r] (DEVICE, int32).  slots == NULL: row r works on slot r.  A negative slot marks an idle row:
+ * its output row is written as zeros and no state is touched.  A slot >= num_slots records
+ * KDA_ERR_INVALID_ARG in the device status word and the row is treated as idle.  The rows of one call
+ * must name distinct slots.  state_out may be the same pointer as state_in (in place) or another pool
+ * of the same shape (only the named slots are written); partly overlapping pools are not allowed.
+ *
+ * One KDA token per row: the recurrence at the top of this file for T = 1, with dims->T == 1, B rows
+ * and num_seqs unused; q, k [B, Hk, K], g_raw [B, H, K], v, out [B, H, V], beta_raw [B, H] in dtype,
+ * state_in / state_out [num_slots, H, K, V] fp32.  Any K, V, Hk, gate and dtype that kda_fwd takes;
+ * arithmetic in fp32.  Errors as for kda_fwd; num_slots < 1, or slots == NULL with num_slots < B, is
+ * KDA_ERR_INVALID_ARG.
+ */
+kda_status kda_decode_step(const kda_dims* dims, const void* q, const void* k, const void* v, const void* g_raw,
+                           const void* beta_raw, const float* a_log, const float* dt_bias, float scale,
+                           float lower_bound, const int32_t* slots, int num_slots, const float* state_in,
+                           float* state_out, void* out, cudaStream_t stream);
+
+/*
+ * Selective state space scan, the recurrent mixer with one scalar decay per head and token:
+ *     D_t = softplus(dt_raw_t + dt_bias_h),   a_h = -exp(a_log_h)
+ *     S_t = exp(D_t a_h) S_{t-1} + D_t B_t x_t^T,     y_t = S_t^T C_t + d_skip_h x_t
+ * Head h reads group h / (H / G) of B and C (H a multiple of G).  Layouts, activations in dtype:
+ *     x, y      [B, T, H, P]          b, c   [B, T, G, N]          dt_raw [B, T, H]
+ *     a_log, dt_bias, d_skip [H] fp32 (d_skip may be NULL: no skip term)
+ *     states    [rows, H, N, P] fp32  (rows = B, or num_seqs with cu_seqlens)
+ * x, b, c and dt_raw may be slices of one projection's output: *_stride is the distance in elements
+ * between the rows of neighbouring tokens (also from the last token of a row of B to the first of the
+ * next), 0 meaning contiguous; the values of one token are contiguous.  y is contiguous.
+ * Requirements: 1 <= N, P <= 256, strides no shorter than a token's values.
+ * cu_seqlens and cu_seqlens_host: as for kda_fwd (B == 1).  An empty document passes its state through.
+ * A device-only cu_seqlens that breaks the contract records KDA_ERR_INVALID_ARG in the device status
+ * word; y is then not written and final_state gets the entering state (zero without one).
+ * All sums and states are fp32.  bf16 inputs with N, P <= 128, N, P and the strides multiples of 8 and
+ * 16-byte aligned x, b, c and y run on the tensor cores in chunks of 128 tokens: the products inside a
+ * chunk and the read of the entering state round one operand to bf16 (y is bf16), the state update
+ * keeps its operand as a sum of two bf16 values (relative error ~1e-6 of the state).  There a
+ * non-finite x, B or C spreads over its whole chunk instead of only the later tokens.  Every other
+ * shape runs an fp32 token-by-token kernel.
+ * Long rows with few rows x heads are cut into segments whose end states are computed in parallel and
+ * joined before the outputs; the library chooses the cut.  Results do not depend on timing.
+ * The workspace is kda_ssm_fwd_workspace_size() bytes (0 on invalid input).
+ */
+typedef struct {
+    int B, T, H, G, N, P;
+    kda_dtype dtype;
+    int num_seqs;
+    int64_t x_stride, b_stride, c_stride, dt_stride;
+} kda_ssm_dims;
+size_t kda_ssm_fwd_workspace_size(const kda_ssm_dims* dims);
+kda_status kda_ssm_fwd(const kda_ssm_dims* dims, const void* x, const void* dt_raw, const void* b, const void* c,
+                       const float* a_log, const float* dt_bias, const float* d_skip, const int32_t* cu_seqlens,
+                       const int32_t* cu_seqlens_host, const float* initial_state, void* y, float* final_state,
+                       void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* One token per row (dims->T == 1) on a slot pool [num_slots, H, N, P] fp32; strides are row strides. */
+kda_status kda_ssm_step(const kda_ssm_dims* dims, const void* x, const void* dt_raw, const void* b, const void* c,
+                        const float* a_log, const float* dt_bias, const float* d_skip, const int32_t* slots,
+                        int num_slots, const float* state_in, float* state_out, void* y, cudaStream_t stream);
+
+/*
+ * The short convolution of kda_short_conv_fwd with a carried history: the W - 1 inputs before a
+ * segment's first token are initial_history [rows, W - 1, C] in dtype (oldest first; NULL: zeros), and
+ * final_history (same layout, may be NULL) gets the last W - 1 inputs of each segment, its own history
+ * included where the segment is shorter.  rows = B, or num_seqs with cu_seqlens (contract as for
+ * kda_ssm_fwd: a device-only violation is recorded in the status word and nothing is written).
+ * x_stride: elements between neighbouring tokens of x (0: C).  y is contiguous.
+ * Errors as for kda_short_conv_fwd; x_stride not a multiple of 8, or a history pointer that is not
+ * 16-byte aligned, is KDA_ERR_UNSUPPORTED.
+ */
+kda_status kda_short_conv_prompt(int B, int T, int C, int W, kda_dtype dtype, const void* x, int64_t x_stride,
+                                 const float* weight, const float* bias, const int32_t* cu_seqlens,
+                                 const int32_t* cu_seqlens_host, int num_seqs, const void* initial_history, void* y,
+                                 void* final_history, cudaStream_t stream);
+
+/* One token per row: x, y [B, C] (x_stride between rows), histories in a slot pool
+ * [num_slots, W - 1, C] in dtype; the step shifts the history by one and appends x. */
+kda_status kda_short_conv_step(int B, int C, int W, kda_dtype dtype, const void* x, int64_t x_stride,
+                               const float* weight, const float* bias, const int32_t* slots, int num_slots,
+                               const void* history_in, void* history_out, void* y, cudaStream_t stream);
+
+/*
+ * Pages of a cache.  A pool holds `layers` arrays of `num_pages` pages of page_bytes bytes, layer l at
+ * pool + l * layer_stride (bytes; >= num_pages * page_bytes).  Every sequence has a row of
+ * table [num_seqs, max_pages] (int32 page ids, -1 past its end) and a length in tokens; it holds
+ * ceil(length / page_tokens) pages.  refs [num_pages] counts the rows that hold a page; a page with no
+ * references is free, and the i-th page a call allocates is the i-th free page by index.  A recurrent
+ * state is a page that never fills: one page per sequence and page_tokens above any length.
+ * All arrays are DEVICE memory.  Each *_out may be its input (in place) or a separate array of the same
+ * size, which is then written in full.  A page id outside [0, num_pages) in a table is kept and
+ * otherwise ignored.  Results do not depend on the order in which the GPU runs the requests.
+ *
+ * kda_pages_copy: page src[i] of src_pool to page dst[i] of dst_pool, every layer; pairs with a page
+ *   out of range are skipped.  dst must not repeat, and no dst may also be a src where the pools are one.
+ * kda_pages_fork: row children[i] becomes a copy of row parents[i]: the full pages are shared (their
+ *   references grow by one), a last page that is partly filled is copied into a free page.  ok[i] is 1, or
+ *   0 and nothing is done where a row is out of range, the child still has a length above 0, parent and
+ *   child are one row, the last page is not one of the pool, or no free page was left.  children must not repeat, nor be parents of this call.
+ * kda_pages_extend: row seqs[i] grows to new_lengths[i] tokens and gets the pages that needs.  ok[i] is 0
+ *   and nothing is done for a row out of range, a length below the present one or above
+ *   max_pages * page_tokens, or too few free pages left (requests are served in order; one that finds
+ *   too few is refused and its pages are not given to later ones).  seqs must not repeat.
+ * kda_pages_free: drops the references of rows seqs[i], clears the rows and their lengths.  Rows out of
+ *   range are skipped; seqs must not repeat.
+ * kda_pages_compact: moves the live pages to the lowest indices.  With L live pages, the k-th highest live
+ *   page at or above L moves into the k-th lowest free page below L; table and refs follow, and
+ *   page_map[p] (may be NULL) is the new index of page p, -1 for a free one.
+ *
+ * The workspace of fork, extend and compact is kda_pages_workspace_size() bytes (0 on invalid input),
+ * n = the number of requests (0 for compact).  Errors: sizes < 1 (n < 0), a NULL pointer or a layer
+ * stride that is too short give KDA_ERR_INVALID_ARG; num_pages, num_seqs * max_pages or n above 2^30
+ * give KDA_ERR_UNSUPPORTED.  n == 0 does nothing but fill separate *_out arrays.
+ */
+typedef struct {
+    int layers, num_pages, num_seqs, max_pages, page_tokens;
+    int64_t page_bytes, layer_stride;
+} kda_pages_dims;
+size_t kda_pages_workspace_size(const kda_pages_dims* dims, int n);
+kda_status kda_pages_copy(int layers, int64_t page_bytes, void* dst_pool, int64_t dst_layer_stride, int dst_pages,
+                          const void* src_pool, int64_t src_layer_stride, int src_pages, const int32_t* src,
+                          const int32_t* dst, int n, cudaStream_t stream);
+kda_status kda_pages_fork(const kda_pages_dims* dims, void* pool, const int32_t* table, const int32_t* lengths,
+                          const int32_t* refs, const int32_t* parents, const int32_t* children, int n,
+                          int32_t* table_out, int32_t* lengths_out, int32_t* refs_out, int32_t* ok, void* workspace,
+                          size_t workspace_bytes, cudaStream_t stream);
+kda_status kda_pages_extend(const kda_pages_dims* dims, const int32_t* table, const int32_t* lengths,
+                            const int32_t* refs, const int32_t* seqs, const int32_t* new_lengths, int n,
+                            int32_t* table_out, int32_t* lengths_out, int32_t* refs_out, int32_t* ok, void* workspace,
+                            size_t workspace_bytes, cudaStream_t stream);
+kda_status kda_pages_free(const kda_pages_dims* dims, const int32_t* table, const int32_t* lengths,
+                          const int32_t* refs, const int32_t* seqs, int n, int32_t* table_out, int32_t* lengths_out,
+                          int32_t* refs_out, cudaStream_t stream);
+kda_status kda_pages_compact(const kda_pages_dims* dims, void* pool, const int32_t* table, const int32_t* refs,
+                             int32_t* table_out, int32_t* refs_out, int32_t* page_map, void* workspace,
+                             size_t workspace_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
