@@ -47,7 +47,15 @@ namespace {
 
 // ------------------------------------------------------------------ schedule
 
-constexpr int kSsmMinSeg = 512;    // tokens: a shorter segment spends more on its state than on its tokens
+// A schedule's cost in chunk times of the output pass: a segment costs its chunks and about two more to
+// start; the state pass about half of that again, the join and the two launches about four.
+constexpr int kSsmSms = 152;
+double schedule_cost(int64_t chunks, int64_t segs, int64_t rows, int64_t units, int64_t* len) {
+    const int64_t L = (chunks + segs - 1) / segs, n = (chunks + L - 1) / L;
+    *len = L;
+    const int64_t waves = (rows * n * units + kSsmSms - 1) / kSsmSms;
+    return n == 1 ? waves * (L + 2.0) : 1.5 * waves * (L + 2.0) + 4.0;
+}
 
 struct Schedule {
     int L, per_row, nseg;
@@ -57,23 +65,26 @@ struct Schedule {
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Segments of L tokens such that rows x segments x heads x `ctas` CTAs per (segment, head) fill the GPU
-// about twice; single where the rows alone do.
-Schedule make_schedule(const SsmShape& s, bool varlen, int ctas_per_head) {
+// units: CTAs per segment over all heads, counted in CTAs that have an SM to themselves.
+Schedule make_schedule(const SsmShape& s, bool varlen, int64_t units) {
     Schedule w;
     memset(&w, 0, sizeof(w));
-    const int64_t span = varlen ? (s.TT + s.rows - 1) / s.rows : s.T;
-    const int64_t units = (int64_t)s.rows * s.H * ctas_per_head;
-    int64_t want = units >= 304 ? 1 : (304 + units - 1) / units;   // segments per row
-    const int64_t most = (span + kSsmMinSeg - 1) / kSsmMinSeg;
-    if (want > most) want = most;
-    if (want < 1) want = 1;
-    w.single = want == 1;
+    const int64_t span = varlen ? (s.TT + s.rows - 1) / s.rows : s.T;   // of documents: their mean
+    const int64_t chunks = (span + 127) / 128;
+    int64_t best = chunks, len;
+    double least = schedule_cost(chunks, 1, s.rows, units, &len);
+    for (int64_t segs = 2; segs <= chunks && s.rows * (segs - 1) * units < 4 * kSsmSms; ++segs) {
+        const double c = schedule_cost(chunks, segs, s.rows, units, &len);
+        if (c < least) {
+            least = c;
+            best = len;
+        }
+    }
+    w.single = best == chunks;
     const int64_t longest = varlen ? s.TT : s.T;
-    w.L = w.single ? (int)((longest + 127) / 128 * 128) : (int)((span + want - 1) / want + 127) / 128 * 128;
+    w.L = (int)((w.single ? (longest + 127) / 128 : best) * 128);
     w.per_row = varlen ? 0 : (s.T + w.L - 1) / w.L;
     w.nseg = varlen ? (w.single ? s.rows : s.rows + s.TT / w.L) : s.rows * w.per_row;
-    if (!varlen && w.per_row == 1) w.single = true;
     size_t o = 0;
     if (varlen) {
         w.off_seg = o; o = up256(o + sizeof(SsmSeg) * (size_t)w.nseg);
@@ -87,7 +98,9 @@ Schedule make_schedule(const SsmShape& s, bool varlen, int ctas_per_head) {
     return w;
 }
 
-int ctas_per_head(const SsmShape& s) { return (s.P + 31) / 32; }
+// Four CTAs of the fp32 kernel share an SM.
+int64_t simt_units(const SsmShape& s) { return ((int64_t)s.H * ((s.P + 31) / 32) + 3) / 4; }
+int64_t tc_units(const SsmShape& s) { return ssm_tc_units(s.H, s.G, s.P); }
 
 // Segments of every row in order: ceil(len / L) of them, one empty segment for an empty row (its state
 // passes through).  Offsets that break the contract are recorded and give every row one empty segment.
@@ -327,8 +340,11 @@ size_t kda_ssm_fwd_workspace_size(const kda_ssm_dims* dims) {
         if (varlen && !(dims->num_seqs > 0 && dims->B == 1)) continue;
         if (ssm_check(dims, varlen != 0, f, f, f, f, f, f, &s) != KDA_OK) continue;
         valid = true;
-        const size_t t = make_schedule(s, varlen != 0, ctas_per_head(s)).total;
-        if (t > most) most = t;
+        // which kernels run also depends on the pointers' alignment
+        for (const int64_t units : {simt_units(s), tc_units(s)}) {
+            const size_t t = make_schedule(s, varlen != 0, units).total;
+            if (t > most) most = t;
+        }
     }
     return valid ? (most ? most : 256) : 0;
 }
@@ -343,7 +359,8 @@ kda_status kda_ssm_fwd(const kda_ssm_dims* dims, const void* x, const void* dt_r
     if (!y) return KDA_ERR_INVALID_ARG;
     st = check_offsets_host(s.rows, s.TT, cu_seqlens, cu_seqlens_host);
     if (st != KDA_OK) return st;
-    const Schedule w = make_schedule(s, cu_seqlens != nullptr, ctas_per_head(s));
+    const bool tc = ssm_tc_ok(s, x, b, c, y);
+    const Schedule w = make_schedule(s, cu_seqlens != nullptr, tc ? tc_units(s) : simt_units(s));
     if (workspace_bytes < w.total || (w.total && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256)))
         return KDA_ERR_WORKSPACE;
     if (w.nseg > (1 << 30) / s.H || s.H > 65535) return KDA_ERR_UNSUPPORTED;
@@ -370,13 +387,13 @@ kda_status kda_ssm_fwd(const kda_ssm_dims* dims, const void* x, const void* dt_r
     if (!w.single) {
         a.decay = reinterpret_cast<float*>(ws + w.off_decay);
         a.states = reinterpret_cast<float*>(ws + w.off_states);
-        if (launch_ssm_simt(a, false, stream) != cudaSuccess) return KDA_ERR_CUDA;
+        if ((tc ? launch_ssm_tc(a, false, stream) : launch_ssm_simt(a, false, stream)) != cudaSuccess) return KDA_ERR_CUDA;
         timing_pre(stream, K_SSM_JOIN);
         ssm_join_kernel<<<dim3(s.rows * s.H, (s.N * s.P + 255) / 256), 256, 0, stream>>>(a);
         timing_post(stream);
         if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
     }
-    return launch_ssm_simt(a, true, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return (tc ? launch_ssm_tc(a, true, stream) : launch_ssm_simt(a, true, stream)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -62,4 +62,9 @@ __device__ __forceinline__ float* ssm_leaving(const SsmArgs& a, const SsmSeg& s,
 
 cudaError_t launch_ssm_simt(const SsmArgs& a, bool out, cudaStream_t st);
 
+// The tensor-core kernels: whether they take these arguments, CTAs per segment, launch.
+bool ssm_tc_ok(const SsmShape& s, const void* x, const void* b, const void* c, const void* y);
+int ssm_tc_units(int H, int G, int P);
+cudaError_t launch_ssm_tc(const SsmArgs& a, bool out, cudaStream_t st);
+
 }  // namespace kda
