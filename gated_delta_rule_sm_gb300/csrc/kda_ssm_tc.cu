@@ -11,7 +11,7 @@
 //
 // Operands: B, C and X tiles arrive by TMA with the 128-byte swizzle and are read by the products as they
 // are, K-major for G and C S, MN-major (tokens as K) for M X and U^T B.  M and U are A operands in TMEM:
-// M is written over G, 32 fp32 columns of G giving 16 + 16 packed columns for the two heads.  The state
+// M is written over G, 16 fp32 columns of G giving 8 + 8 packed columns for the two heads.  The state
 // stays in fp32 registers; its bf16 copy in shared memory is the B operand of C S.
 // Precision: M is rounded to bf16 (relative 2^-9 of each term of y, which is bf16 itself); C S takes S as
 // two bf16 values, one after the other in one buffer: with one, a large entering state alone cost y up to
@@ -30,6 +30,8 @@
 // 1.95 us and 1.49 us of an SM's share at the measured rates.
 #include <cudaTypedefs.h>
 #include <string.h>
+
+#include <type_traits>
 
 #include "kda.h"
 #include "kda_sm100.cuh"
@@ -52,12 +54,12 @@ template <int NB> struct Lay {
     static constexpr uint32_t C = B + 2 * NB * HALF;       // NB halves
     static constexpr uint32_t SB = C + NB * HALF;          // NB halves: S^T rounded to bf16
     static constexpr uint32_t PREP = SB + NB * HALF;       // 2 buffers x 2 slots x kPrepFloats
-    static constexpr uint32_t BAR = PREP + 2 * 2 * 4 * 400;
+    static constexpr uint32_t BAR = PREP + 2 * 2 * 4 * 528;
     static constexpr uint32_t TOTAL = BAR + 256;
 };
 // A slot's decays: [0] lb - log2 D, [128] D 2^(sum to the chunk's end), [256] lb = running sum inside the
-// block of 32 tokens, [384..387] the blocks' sums, [388] 2^(chunk's sum)
-constexpr int kPrepFloats = 400;
+// block of 32 tokens, [384] D 2^(sum to the block's end), [512..515] the blocks' sums, [516] 2^(chunk's sum)
+constexpr int kPrepFloats = 528;
 
 enum Bars {
     kFull = 0,        // [2] X and B of a stage landed
@@ -85,18 +87,37 @@ enum Bars {
 // TMEM columns
 constexpr uint32_t TG = 0, TY = 128, TD = 256, TU = 384, TCOLS = 512;
 
-// Shared-memory operand descriptor, 128-byte swizzle (tiles are 1 KB aligned).
-__device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t lbo) {
-    return smem_desc(addr, lbo, 1024) | (2ull << 61);
+// Low word of a shared-memory operand descriptor, 128-byte swizzle (tiles are 1 KB aligned), and the high
+// word, which is one for all.  A step inside a tile adds to the low word; the sum is formed beside its one
+// use so that a loop's steps do not occupy registers.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | (lbo >> 4 << 16); }
+constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
+
+// D[tmem] (+)= A[smem] * B[smem]^T, issued by one thread; a, b: low descriptor words, oa, ob: bytes from them.
+template <int OA, int OB>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 da, db;\n\tadd.u32 x, %1, %5;\n\tadd.u32 y, %2, %6;\n\t"
+        "mov.b64 da, {x, %7};\n\tmov.b64 db, {y, %7};\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(OA >> 4), "n"(OB >> 4), "r"(kDescHi));
+}
+// D[tmem] (+)= A[tmem] * B[smem]^T
+template <int OB>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b32 y;\n\t.reg .b64 db;\n\tadd.u32 y, %2, %5;\n\tmov.b64 db, {y, %6};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(OB >> 4), "r"(kDescHi));
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]^T, issued by one thread.
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate));
+// Calls f with 0 .. N - 1 as constants.
+template <int N, typename F, int I = 0>
+__device__ __forceinline__ void steps(F&& f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>());
+        steps<N, F, I + 1>(static_cast<F&&>(f));
+    }
 }
 
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0, int c1, int c2) {
@@ -108,14 +129,88 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
-    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
-// softplus, one copy of the code for its four uses
-__device__ __noinline__ float step_of(float x) { return softplusf(x); }
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\t"
+        "mov.b64 {%0, %1}, d;\n\t}" : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 dup(float x) { return make_float2(x, x); }
+// The two values of a packed bf16 pair; what is left of a pair of fp32 values beside it.
+__device__ __forceinline__ float2 bf2(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+__device__ __forceinline__ float2 rest2(float2 u, uint32_t w) { return fma2(bf2(w), dup(-1.f), u); }
 
-// Byte of 16-byte chunk j of row r in a HALF tile.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// Four 8 x 8 blocks of 16-bit values, transposed; lane i gives the address of row i % 8 of block i / 8.
+__device__ __forceinline__ void ldmatrix4t(uint32_t addr, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// 16 lanes x 16 columns: word w of lane l from thread 4 (l % 8) + w % 4, register 2 (w / 4) + l / 8.
+__device__ __forceinline__ void tmem_st_16x16(uint32_t taddr, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// softplus(x) = max(x, 0) + log1p(e^-|x|) to about 2 ulp: e^-|x| from a product split in two, log1p(e) from
+// the series of 2 artanh(e / (2 + e)), whose argument is at most 1/3.
+__device__ __forceinline__ float step_of(float x) {
+    const float y = fmaxf(-fabsf(x), -200.f), t = y * kLog2e;
+    const float r = fmaf(y, kLog2e, -t) + y * 1.925963033500e-8f;
+    float e = ex2(t);
+    e = fmaf(e * 0.6931471806f, r, e);
+    const float z = __fdividef(e, 2.f + e), q = z * z;
+    float s = 1.f / 15.f;
+    s = fmaf(s, q, 1.f / 13.f);
+    s = fmaf(s, q, 1.f / 11.f);
+    s = fmaf(s, q, 1.f / 9.f);
+    s = fmaf(s, q, 1.f / 7.f);
+    s = fmaf(s, q, 1.f / 5.f);
+    s = fmaf(s, q, 1.f / 3.f);
+    s = fmaf(s, q, 1.f);
+    const float l = fmaf(2.f * z, s, fmaxf(x, 0.f));
+    return x != x ? x : l;
+}
+
+// Shared memory by 32-bit address: fewer registers than a pointer, and nothing to keep across a loop.
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 lds4f(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float lds1f(uint32_t a) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, const uint32_t* v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+
+// Byte of 16-byte chunk j of row r in a HALF tile; from the address of chunk 0, chunk j is that XOR 16 j.
 __device__ __forceinline__ uint32_t sw(int r, int j) { return (uint32_t)(r * 128 + ((j ^ (r & 7)) << 4)); }
 
 struct Unit {
@@ -164,6 +259,7 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
     float* prep = reinterpret_cast<float*>(smem + L::PREP);
 
     if (tid == 0) {
+#pragma unroll 1
         for (int i = 0; i < kBars; ++i) {
             const int cnt = i == kM || i == kD3Free || i == kSB || i == kYOut || i == kYOut + 1 ||
                             i == kSBLo || i == kTail ? 8
@@ -180,19 +276,26 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
     tc_fence_after();
     const uint32_t tmem = *tslot;
 
-    // Bounded wait of one thread; false once any wait of the CTA has given up.  (Kept short: it is inlined
-    // some thirty times, and the loop's code has to stay in the instruction cache.)
+    // Bounded waits; false, and the CTA marked as failed, where one gives up: its role then leaves its loop, and
+    // the roles that wait for it give up in turn.  Kept short: they are inlined some thirty times, and the
+    // code of all roles' loops has to stay in the instruction cache.
+    constexpr uint32_t kTries = 1u << 22;
     auto wait1 = [&](int b, uint32_t parity) {
         if (mbar_test_wait(&bar[b], parity)) return true;
-        for (uint32_t i = 0; i < (1u << 22); ++i) {
+#pragma unroll 1
+        for (uint32_t i = 0; i < kTries; ++i)
             if (mbar_try_wait(&bar[b], parity)) return true;
-            if ((i & 255) == 255 && *fail) return false;
-        }
         *fail = 1;
         return false;
     };
-    // The same with one answer for the whole warp.
-    auto wait = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, wait1(b, parity)) != 0; };
+    auto wait = [&](int b, uint32_t parity) {      // one answer for the whole warp
+        if (__all_sync(0xffffffffu, mbar_test_wait(&bar[b], parity))) return true;
+#pragma unroll 1
+        for (uint32_t i = 0; i < kTries; ++i)
+            if (__all_sync(0xffffffffu, mbar_try_wait(&bar[b], parity))) return true;
+        *fail = 1;
+        return false;
+    };
     auto arrive_warp = [&](int b) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar[b]);
@@ -200,6 +303,47 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
     auto chunk_len = [&](int c) { return min(Q, sg.t1 - (sg.t0 + c * Q)); };
     auto slot_prep = [&](int c, int s) { return prep + ((c & 1) * 2 + (SAME ? 0 : s)) * kPrepFloats; };
 
+    // A quarter of U, transposed: rows (slot, p) 32 (warp % 4) .., 32 tokens, as three bf16 terms in TMEM.  The
+    // tile is read through transposing 8 x 8 loads, so that a thread's word holds two tokens of one row.
+    auto u_quarter = [&](int c, int q) {
+        const int st = c & 1, b = q & 1, k = 2 * c + (q >> 1), lq = warp & 3;
+        if (k > 0 && !wait(kUEmpty + b, (k - 1) & 1)) return false;
+        tc_fence_after();
+        const float* w = slot_prep(c, lq >> 1) + 128 + 32 * q + 2 * (lane & 3);
+        float2 wk[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) wk[i] = *reinterpret_cast<const float2*>(w + 8 * i);
+        const uint32_t x0 = smem_u32(smem + L::X + (2 * st + (lq >> 1)) * HALF) + q * 4096 + (lane >> 4) * 1024 + (lane & 7) * 128;
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {      // 16 rows
+            uint32_t x[8], hi[8], mid[8], lo[8];
+            const uint32_t at = x0 + ((((lq & 1) * 4 + 2 * hh + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
+            ldmatrix4t(at, x);
+            ldmatrix4t(at + 2048, x + 4);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float2 u = mul2(bf2(x[i]), wk[i >> 1]);
+                hi[i] = pack_bf16(u.x, u.y);
+                u = rest2(u, hi[i]);
+                mid[i] = pack_bf16(u.x, u.y);
+                u = rest2(u, mid[i]);
+                lo[i] = pack_bf16(u.x, u.y);
+            }
+            const uint32_t tu = tmem + TU + 48 * b + ((uint32_t)(lq * 32 + 16 * hh) << 16);
+            tmem_st_16x16(tu, hi);
+            tmem_st_16x16(tu + 16, mid);
+            tmem_st_16x16(tu + 32, lo);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        arrive_warp(kUFull + b);
+        return true;
+    };
+
+    // registers by role: 256 x 160 + 128 x 96 + 128 x 72 of the launch's 512 x 128
+    if (warp >= 12) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    else if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
     if (warp < 8) {
         // ---------------------------------------------------------------- M, C S, state, Y
         const int wg = warp >> 2, lq = warp & 3;
@@ -211,29 +355,30 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
         {
             const int h = un.h[srow];
             const float* from = OUT && h >= 0 && p < a.P ? ssm_entering(a, sg, seg, h) : nullptr;
+            const int rows = from ? a.N - SN * wg : 0;
+            from += (size_t)(SN * wg) * a.P + p;
 #pragma unroll
-            for (int j = 0; j < SN; ++j) {
-                const int n = SN * wg + j;
-                S[j] = from && n < a.N ? from[(size_t)n * a.P + p] : 0.f;
-            }
+            for (int j = 0; j < SN; ++j, from += a.P) S[j] = j < rows ? *from : 0.f;
         }
-        // S rounded to bf16, or what that rounding left, as C S's operand
+        const uint32_t sbrow = smem_u32(smem + L::SB + (SN == 64 ? wg * HALF : 0)) + sw(row, SN == 64 ? 0 : 4 * wg);
+        // S cut to bf16, or what the cut left rounded to it, as C S's operand
         auto copy_state = [&](bool rest) {
 #pragma unroll
             for (int j = 0; j < SN; j += 8) {
-                const int n = SN * wg + j;
-                uint4 o = pack8_bf16(S + j);
-                if (rest) {
-                    const uint32_t w[4] = {o.x, o.y, o.z, o.w};
-                    float r[8];
+                uint32_t o[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        r[2 * e] = S[j + 2 * e] - __uint_as_float(w[e] << 16);
-                        r[2 * e + 1] = S[j + 2 * e + 1] - __uint_as_float(w[e] & 0xffff0000u);
+                for (int e = 0; e < 4; ++e) {
+                    if (rest)   // not before its place: the results of all of S at once would not fit the registers
+                        asm volatile("" : "+f"(S[j + 2 * e]), "+f"(S[j + 2 * e + 1]));
+                    const float2 v = make_float2(S[j + 2 * e], S[j + 2 * e + 1]);
+                    o[e] = __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632);
+                    if (rest) {
+                        const float2 r = rest2(v, o[e]);
+                        o[e] = pack_bf16(r.x, r.y);
                     }
-                    o = pack8_bf16(r);
                 }
-                *reinterpret_cast<uint4*>(smem + L::SB + (n >> 6) * HALF + sw(row, (n & 63) >> 3)) = o;
+                // the thread's columns are one half tile (SN 64) or half the chunks of one (SN 32)
+                sts128(sbrow ^ (j << 1), o);
             }
             fence_async_smem();
         };
@@ -256,8 +401,8 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                 arrive_warp(kTail);
             }
             if (OUT) {
-                const float* pr = slot_prep(c, 0);
-                constexpr int PS = SAME ? 0 : kPrepFloats;
+                const uint32_t pr = smem_u32(slot_prep(c, 0));
+                constexpr uint32_t PS = SAME ? 0 : 4 * kPrepFloats;
                 if (!wait(kG, par)) break;
                 tc_fence_after();
                 // (not unrolled: fetching code that all roles' loops cannot keep in the instruction cache
@@ -266,41 +411,71 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
 #pragma unroll 1
                 for (int b = 0; b < 2; ++b) {
                     const int J = wg == 0 ? 3 * b : 1 + b;
-                    const uint32_t tg = tmem + TG + lanes + 32 * J;
-                    uint32_t m[16];
-                    if (b == 1) {     // C S of the rounded state is complete: its remainder takes the same place
+                    if (b == 1) {     // C S of the cut state is complete: its remainder takes the same place
                         ok = wait(kY2, par);
                         if (!ok) break;
                         copy_state(true);
                         arrive_warp(kSBLo);
                     }
+                    const uint32_t tg = tmem + TG + lanes + 32 * J;
                     if (J > lq) {
+                        uint32_t m[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) m[i] = 0;
                         tmem_st16(tg, m);
-                        if (!SAME) tmem_st16(tg + 16, m);
+                        tmem_st16(tg + 16, m);
                         continue;
                     }
                     float v[32];
                     tmem_ld16(tg, v);
                     tmem_ld16(tg + 16, v + 16);
                     tmem_ld_wait();
-                    const int last = J == lq ? lane : 31;    // the diagonal block's columns end at the row
 #pragma unroll 1
                     for (int s = 0; s < (SAME ? 1 : 2); ++s) {
-                        const float* ps = pr + s * PS;
-                        float l = ps[256 + row];             // from the column block's start to the row
-                        for (int k = J; k < lq; ++k) l += ps[384 + k];
-                        const float4* ld = reinterpret_cast<const float4*>(ps + 32 * J);
+                        const uint32_t ps = pr + s * PS;
+                        float l = lds1f(ps + 4 * (256 + row));
+                        if (J == lq) {           // the diagonal block: an exponential each, columns up to the row
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            const float4 l4 = ld[i >> 2];
-                            const float e0 = v[i] * ex2(l - l4.x), e1 = v[i + 1] * ex2(l - l4.y);
-                            const float e2 = v[i + 2] * ex2(l - l4.z), e3 = v[i + 3] * ex2(l - l4.w);
-                            m[i >> 1] = pack_bf16(i <= last ? e0 : 0.f, i + 1 <= last ? e1 : 0.f);
-                            m[(i >> 1) + 1] = pack_bf16(i + 2 <= last ? e2 : 0.f, i + 3 <= last ? e3 : 0.f);
+                            for (int c0 = 0; c0 < 32; c0 += 16) {
+                                float4 l4[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) l4[i] = lds4f(ps + 4 * (32 * J + c0 + 4 * i));
+                                uint32_t m[8];
+#pragma unroll
+                                for (int i = 0; i < 16; i += 4) {
+                                    const float4 k = l4[i >> 2];
+                                    const float2 x0 = fma2(make_float2(k.x, k.y), dup(-1.f), dup(l));
+                                    const float2 x1 = fma2(make_float2(k.z, k.w), dup(-1.f), dup(l));
+                                    const int j = c0 + i;
+                                    const float2 e0 = mul2(make_float2(v[j], v[j + 1]), make_float2(ex2(x0.x), ex2(x0.y)));
+                                    const float2 e1 = mul2(make_float2(v[j + 2], v[j + 3]), make_float2(ex2(x1.x), ex2(x1.y)));
+                                    m[i >> 1] = pack_bf16(j <= lane ? e0.x : 0.f, j + 1 <= lane ? e0.y : 0.f);
+                                    m[(i >> 1) + 1] = pack_bf16(j + 2 <= lane ? e1.x : 0.f, j + 3 <= lane ? e1.y : 0.f);
+                                }
+                                tmem_st8(tg + c0 + 8 * s, m);
+                            }
+                        } else {                 // a factor of the column to the block's end, one of the row from there
+#pragma unroll 1
+                            for (int k = J + 1; k < lq; ++k) l += lds1f(ps + 4 * (512 + k));
+                            const float2 rf = dup(ex2(l));
+#pragma unroll
+                            for (int c0 = 0; c0 < 32; c0 += 16) {
+                                float4 f4[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) f4[i] = lds4f(ps + 4 * (384 + 32 * J + c0 + 4 * i));
+                                uint32_t m[8];
+#pragma unroll
+                                for (int i = 0; i < 16; i += 4) {
+                                    const float4 k = f4[i >> 2];
+                                    const int j = c0 + i;
+                                    const float2 e0 = mul2(make_float2(v[j], v[j + 1]), mul2(make_float2(k.x, k.y), rf));
+                                    const float2 e1 = mul2(make_float2(v[j + 2], v[j + 3]), mul2(make_float2(k.z, k.w), rf));
+                                    m[i >> 1] = pack_bf16(e0.x, e0.y);
+                                    m[(i >> 1) + 1] = pack_bf16(e1.x, e1.y);
+                                }
+                                tmem_st8(tg + c0 + 8 * s, m);
+                            }
                         }
-                        tmem_st16(tg + 16 * s, m);
                     }
                 }
                 if (!ok) break;
@@ -308,19 +483,24 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                 if (!wait(kY2Lo, par)) break;
                 tc_fence_after();
                 {
-                    float l = pr[wg * PS + 256 + row];
-                    for (int k = 0; k < lq; ++k) l += pr[wg * PS + 384 + k];
-                    const float el = ex2(l);
+                    float l = lds1f(pr + wg * PS + 4 * (256 + row));
+#pragma unroll 1
+                    for (int k = 0; k < lq; ++k) l += lds1f(pr + wg * PS + 4 * (512 + k));
+                    const float2 el = dup(ex2(l));
                     const uint32_t ty = tmem + TY + lanes + 64 * wg;
 #pragma unroll 1
                     for (int j = 0; j < 64; j += 32) {
                         float v[32];
+                        uint32_t r[32];
                         tmem_ld16(ty + j, v);
                         tmem_ld16(ty + j + 16, v + 16);
                         tmem_ld_wait();
-                        uint32_t r[32];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i] * el);
+                        for (int i = 0; i < 32; i += 2) {
+                            const float2 y = mul2(make_float2(v[i], v[i + 1]), el);
+                            r[i] = __float_as_uint(y.x);
+                            r[i + 1] = __float_as_uint(y.y);
+                        }
                         tmem_st16(ty + j, r);
                         tmem_st16(ty + j + 16, r + 16);
                     }
@@ -329,18 +509,28 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                 tc_fence_before();
                 arrive_warp(kM);
             }
+            if (!OUT && wg == 1) {
+                if (len == Q && !wait(kFull + st, (c >> 1) & 1)) break;
+                if (len < Q && !wait(kTail, 0)) break;
+                if (!u_quarter(c, 1) || !u_quarter(c, 3)) break;
+            }
             if (!wait(kD3, par)) break;
             tc_fence_after();
             {
-                const float eq = slot_prep(c, srow)[388];
+                const float eq = lds1f(smem_u32(slot_prep(c, srow)) + 4 * 516);
                 const uint32_t td = tmem + TD + lanes + SN * wg;
 #pragma unroll
-                for (int j = 0; j < SN; j += 16) {
-                    float v[16];
+                for (int j = 0; j < SN; j += 32) {
+                    float v[32];
                     tmem_ld16(td + j, v);
+                    tmem_ld16(td + j + 16, v + 16);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) S[j + i] = fmaf(eq, S[j + i], v[i]);
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 n = fma2(dup(eq), make_float2(S[j + i], S[j + i + 1]), make_float2(v[i], v[i + 1]));
+                        S[j + i] = n.x;
+                        S[j + i + 1] = n.y;
+                    }
                 }
             }
             tc_fence_before();
@@ -351,12 +541,15 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                 tc_fence_after();
                 const int h = un.h[wg];
                 const float dsk = a.d_skip && h >= 0 ? a.d_skip[h] : 0.f;
-                const uint32_t ty = tmem + TY + lanes + 64 * wg;
+                const uint32_t ty = tmem + TY + lanes + 64 * wg, xrow = smem_u32(xh) + sw(row, 0);
 #pragma unroll 1
                 for (int j = 0; j < 8; j += 4) {
                     float v[32];
+                    uint4 u[4];
                     tmem_ld16(ty + 8 * j, v);
                     tmem_ld16(ty + 8 * j + 16, v + 16);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) u[k] = lds128(xrow ^ ((j + k) << 4));
                     tmem_ld_wait();
                     if (j) {
                         tc_fence_before();
@@ -365,16 +558,14 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                     // y over x, which nothing else reads any more
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        uint4* at = reinterpret_cast<uint4*>(xh + sw(row, j + k));
-                        const uint4 u = *at;
-                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-                        float y[8];
+                        const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+                        uint32_t o[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            y[2 * e] = fmaf(dsk, __uint_as_float(w[e] << 16), v[8 * k + 2 * e]);
-                            y[2 * e + 1] = fmaf(dsk, __uint_as_float(w[e] & 0xffff0000u), v[8 * k + 2 * e + 1]);
+                            const float2 y = fma2(dup(dsk), bf2(w[e]), make_float2(v[8 * k + 2 * e], v[8 * k + 2 * e + 1]));
+                            o[e] = pack_bf16(y.x, y.y);
                         }
-                        *at = pack8_bf16(y);
+                        sts128(xrow ^ ((j + k) << 4), o);
                     }
                 }
                 if (len == Q) {
@@ -395,22 +586,18 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
             const int h = un.h[srow];
             float* to = h < 0 || p >= a.P ? nullptr
                       : OUT ? ssm_leaving(a, sg, seg, h) : a.states + ((size_t)seg * a.H + h) * a.N * a.P;
-            if (to)
+            const int rows = to ? a.N - SN * wg : 0;
+            to += (size_t)(SN * wg) * a.P + p;
 #pragma unroll
-                for (int j = 0; j < SN; ++j) {
-                    const int n = SN * wg + j;
-                    if (n < a.N) to[(size_t)n * a.P + p] = S[j];
-                }
+            for (int j = 0; j < SN; ++j, to += a.P)
+                if (j < rows) *to = S[j];
         }
     } else if (warp < 12) {
         // ---------------------------------------------------------------- U, transposed: row (slot, p), 32 tokens a quarter
-        const int lq = warp & 3, row = 32 * lq + lane;
-        const uint32_t lanes = (uint32_t)(lq * 32) << 16;
+        const int row = 32 * (warp & 3) + lane;
         for (int c = 0; c < nch; ++c) {
             const int st = c & 1, len = chunk_len(c);
             if (!wait(kFull + st, (c >> 1) & 1) || !wait(kPrepFull + st, (c >> 1) & 1)) break;
-            const float* w = slot_prep(c, row >> 6) + 128;
-            const uint8_t* xh = smem + L::X + (2 * st + (row >> 6)) * HALF;
             if (len < Q) {
                 // B past the end: zeros for the same reason as X there
                 if (row >= len)
@@ -421,41 +608,9 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                 fence_async_smem();
             }
             bool ok = len == Q || wait(kTail, 0);
+            // (with the state alone to form, the second warpgroup takes every other quarter)
 #pragma unroll 1
-            for (int q = 0; q < 4 && ok; ++q) {
-                const int b = q & 1, k = 2 * c + (q >> 1);
-                if (k > 0 && !wait(kUEmpty + b, (k - 1) & 1)) { ok = false; break; }
-                tc_fence_after();
-                uint32_t hi[16], mid[16], lo[16];
-                const uint32_t pb = 2 * (row & 63);
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    const float4 w4 = *reinterpret_cast<const float4*>(w + 32 * q + i);
-                    const float wv[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-                    for (int e = 0; e < 4; e += 2) {
-                        const int t = i + e;      // (32 q is a multiple of 8: the swizzle is the same)
-                        const uint32_t x0 = *reinterpret_cast<const uint16_t*>(xh + q * 4096 + t * 128 + (pb ^ ((t & 7) << 4)));
-                        const uint32_t x1 = *reinterpret_cast<const uint16_t*>(xh + q * 4096 + (t + 1) * 128 + (pb ^ (((t + 1) & 7) << 4)));
-                        float u0 = __uint_as_float(x0 << 16) * wv[e], u1 = __uint_as_float(x1 << 16) * wv[e + 1];
-                        const int o = (i + e) >> 1;
-                        hi[o] = pack_bf16(u0, u1);
-                        u0 -= __uint_as_float(hi[o] << 16);
-                        u1 -= __uint_as_float(hi[o] & 0xffff0000u);
-                        mid[o] = pack_bf16(u0, u1);
-                        u0 -= __uint_as_float(mid[o] << 16);
-                        u1 -= __uint_as_float(mid[o] & 0xffff0000u);
-                        lo[o] = pack_bf16(u0, u1);
-                    }
-                }
-                const uint32_t tu = tmem + TU + 48 * b + lanes;
-                tmem_st16(tu, hi);
-                tmem_st16(tu + 16, mid);
-                tmem_st16(tu + 32, lo);
-                tmem_st_wait();
-                tc_fence_before();
-                arrive_warp(kUFull + b);
-            }
+            for (int q = 0; q < 4 && ok; q += OUT ? 1 : 2) ok = u_quarter(c, q);
             if (!ok) break;
             arrive_warp(kPrepEmpty + st);
         }
@@ -470,11 +625,12 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                 if (!wait1(kCFull, c & 1) || !wait1(kFull + st, (c >> 1) & 1)) break;
                 if (c > 0 && !wait1(kMX, (c - 1) & 1)) break;    // M, over which G goes, has been read
                 tc_fence_after();
+                const uint32_t dc = desc_lo(sc, 16), db = desc_lo(sbt, 16), ds = desc_lo(ss, 16), dx = desc_lo(sx, HALF);
 #pragma unroll 1
-                for (int kk = 0; kk < 4 * NB; ++kk) {
-                    const uint32_t o = (kk >> 2) * HALF + (kk & 3) * 32;
-                    mma_bf16(tmem + TG, desc128(sc + o, 16), desc128(sbt + o, 16), idG, kk > 0);
-                }
+                for (uint32_t h = 0; h < NB; ++h)
+                    steps<4>([&](auto kk) {
+                        mma_ss<kk * 32, kk * 32>(tmem + TG, dc + h * (HALF >> 4), db + h * (HALF >> 4), idG, h + kk > 0);
+                    });
                 mma_commit(&bar[kG]);
                 bool ok = true;
 #pragma unroll 1
@@ -483,10 +639,10 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int kk = 0; kk < 4 * NB; ++kk) {
-                        const uint32_t o = (kk >> 2) * HALF + (kk & 3) * 32;
-                        mma_bf16(tmem + TY, desc128(sc + o, 16), desc128(ss + o, 16), idG, part + kk > 0);
-                    }
+                    for (uint32_t h = 0; h < NB; ++h)
+                        steps<4>([&](auto kk) {
+                            mma_ss<kk * 32, kk * 32>(tmem + TY, dc + h * (HALF >> 4), ds + h * (HALF >> 4), idG, part + h + kk > 0);
+                        });
                     mma_commit(&bar[part ? kY2Lo : kY2]);
                 }
                 if (!ok) break;
@@ -494,10 +650,12 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                 if (!wait1(kM, c & 1)) break;
                 tc_fence_after();
 #pragma unroll 1
-                for (int i = 0; i < (SAME ? 8 : 16); ++i) {
-                    const int s = i >> 3, kk = i & 7;
-                    mma_bf16_ts(tmem + TY + 64 * s, tmem + TG + 32 * (kk >> 1) + 16 * s + 8 * (kk & 1),
-                                desc128(sx + s * HALF + kk * 2048, HALF), idX, 1);
+                for (uint32_t i = 0; i < (SAME ? 2 : 4); ++i) {      // four of a slot's eight steps
+                    const uint32_t sl = i >> 1, k0 = 4 * (i & 1);
+                    steps<4>([&](auto kk) {
+                        mma_ts<kk * 2048>(tmem + TY + 64 * sl, tmem + TG + 16 * (k0 + kk) + 8 * sl,
+                                          dx + ((sl * HALF + k0 * 2048) >> 4), idX, 1);
+                    });
                 }
                 mma_commit(&bar[kMX]);
             }
@@ -553,31 +711,25 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
         // ---------------------------------------------------------------- decays: lane = 4 tokens
         float total[2] = {0.f, 0.f};
         float ea[2], bias[2];
-        uint16_t raw[2][4];       // dt_raw of the chunk to come: requested a chunk ahead
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             ea[s] = un.h[s] >= 0 ? expf(a.a_log[un.h[s]]) * kLog2e : 0.f;
             bias[s] = un.h[s] >= 0 ? a.dt_bias[un.h[s]] : 0.f;
         }
-        auto fetch = [&](int c) {
-            const int t0 = sg.t0 + c * Q + 4 * lane;
-#pragma unroll
-            for (int s = 0; s < (SAME ? 1 : 2); ++s)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    raw[s][e] = un.h[s] >= 0 && t0 + e < sg.t1
-                                    ? static_cast<const uint16_t*>(a.dt)[(size_t)(t0 + e) * a.ds + un.h[s]] : 0;
-        };
-        if (nch > 0) fetch(0);
-        for (int c = 0; c < nch; ++c) {
+        const bool two = !SAME && un.h[1] >= 0;
+        const uint16_t* dt = static_cast<const uint16_t*>(a.dt) + (size_t)(sg.t0 + 4 * lane) * a.ds + un.h[0];
+        for (int c = 0; c < nch; ++c, dt += Q * a.ds) {
             const int st = c & 1, len = chunk_len(c);
+            uint32_t x[4];         // both heads' dt_raw, requested before the wait (heads of a unit are neighbours)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[e] = 0;
+                if (4 * lane + e < len) {
+                    x[e] = dt[e * a.ds];
+                    if (two) x[e] |= (uint32_t)dt[e * a.ds + 1] << 16;
+                }
+            }
             if (c >= 2 && !wait(kPrepEmpty + st, ((c >> 1) - 1) & 1)) break;
-            float x[2][4];
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[s][e] = __uint_as_float((uint32_t)raw[s][e] << 16) + bias[s];
-            if (c + 1 < nch) fetch(c + 1);
 #pragma unroll 1
             for (int s = 0; s < (SAME ? 1 : 2); ++s) {
                 const int h = s ? un.h[1] : un.h[0];
@@ -586,7 +738,9 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                 float D[4], la[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    D[e] = h >= 0 && 4 * lane + e < len ? step_of(s ? x[1][e] : x[0][e]) : 0.f;
+                    const float d = __uint_as_float(s ? x[e] & 0xffff0000u : x[e] << 16);
+                    D[e] = step_of(d + (s ? bias[1] : bias[0]));
+                    if (h < 0 || 4 * lane + e >= len) D[e] = 0.f;
                     la[e] = -es * D[e];
                     if (la[e] < -150.f) la[e] = -150.f;      // (a NaN stays one)
                 }
@@ -607,6 +761,7 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                 const float b0 = __shfl_sync(0xffffffffu, block, 0), b1 = __shfl_sync(0xffffffffu, block, 8);
                 const float b2 = __shfl_sync(0xffffffffu, block, 16), b3 = __shfl_sync(0xffffffffu, block, 24);
                 const int blk = lane >> 3;
+                const float suf = after;
                 after += blk == 0 ? (b1 + b2) + b3 : blk == 1 ? b2 + b3 : blk == 2 ? b3 : 0.f;
                 const float pre[4] = {before + p1, before + p2, before + p3, before + p4};
                 float4* o = reinterpret_cast<float4*>(pr + 4 * lane);
@@ -614,10 +769,11 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                                    pre[3] - __log2f(D[3]));
                 o[32] = make_float4(D[0] * ex2(after + s1), D[1] * ex2(after + s2), D[2] * ex2(after + s3), D[3] * ex2(after));
                 o[64] = make_float4(pre[0], pre[1], pre[2], pre[3]);
+                o[96] = make_float4(D[0] * ex2(suf + s1), D[1] * ex2(suf + s2), D[2] * ex2(suf + s3), D[3] * ex2(suf));
                 const float sum = (b0 + b1) + (b2 + b3);
                 if (lane == 0) {
-                    *reinterpret_cast<float4*>(pr + 384) = make_float4(b0, b1, b2, b3);
-                    pr[388] = exp2f(sum);
+                    *reinterpret_cast<float4*>(pr + 512) = make_float4(b0, b1, b2, b3);
+                    pr[516] = exp2f(sum);
                 }
                 if (s) total[1] += sum; else total[0] += sum;
             }
@@ -641,12 +797,11 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                     if (!wait1(kUFull + b, k & 1)) { ok = false; break; }
                     if (q == 0 && c > 0 && !wait1(kD3Free, (c - 1) & 1)) { ok = false; break; }
                     tc_fence_after();
-#pragma unroll 1
-                    for (int i = 0; i < 6; ++i) {
-                        const int j = i >= 3, term = i - 3 * j;
-                        mma_bf16_ts(tmem + TD, tmem + TU + 48 * b + 16 * term + 8 * j,
-                                    desc128(sbt + (2 * q + j) * 2048, HALF), idU, q + i > 0);
-                    }
+                    const uint32_t db = desc_lo(sbt + q * 4096, HALF);
+                    steps<6>([&](auto i) {
+                        constexpr int j = i >= 3, term = i - 3 * j;
+                        mma_ts<j * 2048>(tmem + TD, tmem + TU + 48 * b + 16 * term + 8 * j, db, idU, q + i > 0);
+                    });
                     mma_commit(&bar[kUEmpty + b]);
                 }
                 if (!ok) break;
@@ -660,6 +815,7 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
     if (*fail && tid == 0) {
         // give copies and products in flight a bounded chance to land before the memory is released
         record_error(a.status, KDA_ERR_TIMEOUT);
+#pragma unroll 1
         for (int b = 0; b < kBars; ++b)
             if (b <= kCFull || (b >= kG && b <= kD3)) {
                 mbar_wait(&bar[b], 0, 1u << 12);
