@@ -21,13 +21,15 @@
 // exponent is the difference of two large numbers; a token's exponent is cut at -150 (2^-150 is 0 in
 // fp32).
 //
-// Roles (512 threads): warps 0-7 form M, scale C S, update S and finish Y (two warpgroups: columns of G
-// and of the state are split between them, Y by head); warps 8-11 form U, a row of the unit per thread,
-// 32 tokens at a time into one of two TMEM buffers; warp 12 issues G, C S and M X, warp 13 the copies,
-// warp 14 prepares the decays of the next chunk, warp 15 issues U^T B.
+// Roles (20 warps): 0-7 form M, scale C S and finish Y (two warpgroups: columns of G are split between
+// them, Y by head); 8-11 form U, a quarter of a chunk at a time; 12-15 keep the state, a row each; 16
+// issues G, C S and M X, 17 the copies, 18 prepares the decays, 19 issues U^T B.  Roles meet at mbarriers
+// only, so the state's chain (U^T B, S, C S) runs beside the output's (G, M, M X, Y).
+// The pass that only forms states has no G, M, C S or Y: its first three warpgroups all form U, in four
+// TMEM buffers, with three stages of X and B.
 // TMEM columns: G / M 128, Y 128, U^T B 128, U 2 x 48.
-// Bound: per chunk and unit 25 MFLOP (half of them the state's three-term product) against 64 KB of x and y,
-// 1.95 us and 1.49 us of an SM's share at the measured rates.
+// Bound: per chunk and unit 29 MFLOP (the state's three terms 12.6, C S 8.4) against 64 KB of x and y: 2.3 us and
+// 1.5 us of an SM's share at the measured rates.
 #include <cudaTypedefs.h>
 #include <string.h>
 
@@ -45,43 +47,50 @@ namespace {
 
 constexpr int Q = 128;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kThreads = 640;
 
-// Shared memory (bytes).  HALF: a tile of 128 rows of 128 bytes (64 bf16 columns).
-constexpr uint32_t HALF = 16384;
-template <int NB> struct Lay {
-    static constexpr uint32_t X = 0;                       // 2 stages x 2 halves
-    static constexpr uint32_t B = X + 4 * HALF;            // 2 stages x NB halves
-    static constexpr uint32_t C = B + 2 * NB * HALF;       // NB halves
-    static constexpr uint32_t SB = C + NB * HALF;          // NB halves: S^T rounded to bf16
-    static constexpr uint32_t PREP = SB + NB * HALF;       // 2 buffers x 2 slots x kPrepFloats
-    static constexpr uint32_t BAR = PREP + 2 * 2 * 4 * 528;
-    static constexpr uint32_t TOTAL = BAR + 256;
-};
 // A slot's decays: [0] lb - log2 D, [128] D 2^(sum to the chunk's end), [256] lb = running sum inside the
 // block of 32 tokens, [384] D 2^(sum to the block's end), [512..515] the blocks' sums, [516] 2^(chunk's sum)
 constexpr int kPrepFloats = 528;
+constexpr int kPrepBufs = 4;
+
+// Shared memory (bytes).  HALF: a tile of 128 rows of 128 bytes (64 bf16 columns).
+constexpr uint32_t HALF = 16384;
+template <int NB, bool OUT> struct Lay {
+    static constexpr int STAGES = OUT ? 2 : 3;
+    static constexpr int BSTAGES = OUT ? 1 : 3;
+    static constexpr uint32_t X = 0;                               // STAGES x 2 halves
+    static constexpr uint32_t B = X + STAGES * 2 * HALF;           // BSTAGES x NB halves
+    static constexpr uint32_t C = B + BSTAGES * NB * HALF;         // NB halves
+    static constexpr uint32_t SB = C + (OUT ? NB * HALF : 0);      // 2 x NB halves: S^T cut to bf16, and the rest
+    static constexpr uint32_t PREP = SB + (OUT ? 2 * NB * HALF : 0);   // kPrepBufs x 2 slots
+    static constexpr uint32_t BAR = PREP + kPrepBufs * 2 * 4 * kPrepFloats;
+    static constexpr uint32_t TOTAL = BAR + 512;
+};
 
 enum Bars {
-    kFull = 0,        // [2] X and B of a stage landed
-    kCFull = 2,       // C landed
-    kCEmpty = 3,      // C read (G and both C S complete)
-    kPrepFull = 4,    // [2]
-    kPrepEmpty = 6,   // [2] 12 warps
-    kG = 8,           // G complete
-    kY2 = 9,          // C S complete
-    kM = 10,          // M written and C S scaled (8 warps)
-    kMX = 11,         // M X complete
-    kUFull = 12,      // [2] a quarter of U written (4 warps)
-    kUEmpty = 14,     // [2] its product complete
-    kD3 = 16,         // U^T B complete
-    kD3Free = 17,     // read (8 warps)
-    kSB = 18,         // S copied and Y read (8 warps)
-    kYOut = 19,       // [2] y over the stage's X (8 warps)
-    kStage = 21,      // [2] states only: the stage's last product complete
-    kSBLo = 23,       // the remainder of S copied (8 warps)
-    kY2Lo = 24,       // its product complete
-    kTail = 25,       // X past the end cleared (8 warps)
-    kBars = 26
+    kFull = 0,        // [3] X of a stage landed (states only: and B)
+    kStage = 3,       // [3] states only: the stage's last product complete
+    kYOut = 6,        // [2] y over the stage's X (8 warps)
+    kXRead = 8,       // [2] U has read the stage's X (4 warps)
+    kPrepFull = 10,   // [4]
+    kPrepEmpty = 14,  // [4] 16 warps
+    kUFull = 18,      // [4] a quarter of U written (4 warps)
+    kUEmpty = 22,     // [4] its product complete
+    kBFull = 26,      // B landed
+    kBEmpty = 27,     // B read (G and U^T B complete)
+    kCFull = 28,      // C landed
+    kCEmpty = 29,     // C read (G and C S complete)
+    kG = 30,          // G complete
+    kSB = 31,         // S copied (4 warps)
+    kY2 = 32,         // C S complete
+    kM = 33,          // [2] half the columns of M written, and C S scaled (8 warps)
+    kMX = 35,         // M X complete
+    kYRead = 36,      // Y read (8 warps)
+    kD3 = 37,         // U^T B complete
+    kD3Free = 38,     // read (4 warps)
+    kTail = 39,       // X and B past the end cleared (8 warps)
+    kBars = 40
 };
 
 // TMEM columns
@@ -235,12 +244,21 @@ __device__ __forceinline__ Unit unit_of(const SsmArgs& a, int u) {
     return r;
 }
 
+// The decays of a chunk's slot.
 template <int NB, bool SAME, bool OUT>
-__global__ void __launch_bounds__(512, 1)
+__device__ __forceinline__ float* prep_slot(uint8_t* smem, int c, int s) {
+    return reinterpret_cast<float*>(smem + Lay<NB, OUT>::PREP) + ((c & (kPrepBufs - 1)) * 2 + (SAME ? 0 : s)) * kPrepFloats;
+}
+
+template <int NB, bool SAME, bool OUT>
+__global__ void __launch_bounds__(kThreads, 1)
 ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mb,
               const __grid_constant__ CUtensorMap mc, const __grid_constant__ CUtensorMap my) {
-    using L = Lay<NB>;
+    using L = Lay<NB, OUT>;
     constexpr int NC = 64 * NB;                      // padded state columns
+    constexpr int NST = L::STAGES;
+    constexpr int NU = OUT ? 2 : 4;                  // U buffers (without G, M and Y their columns are free)
+    constexpr uint32_t U0 = OUT ? TU : 0;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int seg = blockIdx.x;
     const SsmSeg sg = ssm_segment(a, seg);
@@ -256,20 +274,22 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::BAR);
     volatile int* fail = reinterpret_cast<volatile int*>(smem + L::BAR + 8 * kBars);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::BAR + 8 * kBars + 4);
-    float* prep = reinterpret_cast<float*>(smem + L::PREP);
+    float* ptot = reinterpret_cast<float*>(smem + L::BAR + 8 * kBars + 8);    // [2 warps][2 slots]
 
     if (tid == 0) {
 #pragma unroll 1
         for (int i = 0; i < kBars; ++i) {
-            const int cnt = i == kM || i == kD3Free || i == kSB || i == kYOut || i == kYOut + 1 ||
-                            i == kSBLo || i == kTail ? 8
-                          : i == kUFull || i == kUFull + 1 ? 4
-                          : i == kPrepEmpty || i == kPrepEmpty + 1 ? 12 : 1;
+            int cnt = 1;
+            if (i == kYOut || i == kYOut + 1 || i == kM || i == kM + 1 || i == kYRead || i == kTail) cnt = 8;
+            if (i == kXRead || i == kXRead + 1 || (i >= kUFull && i < kUFull + 4) || i == kSB || i == kD3Free) cnt = 4;
+            if (i == kBEmpty) cnt = 2;
+            if (i >= kPrepEmpty && i < kPrepEmpty + 4) cnt = 16;
             mbar_init(&bar[i], cnt);
         }
         *fail = 0;
         mbar_fence_init();
     }
+    if (tid < 4) ptot[tid] = 0.f;
     if (warp == 0) tmem_alloc(tslot, TCOLS);
     tc_fence_before();
     __syncthreads();
@@ -301,13 +321,14 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
         if (lane == 0) mbar_arrive(&bar[b]);
     };
     auto chunk_len = [&](int c) { return min(Q, sg.t1 - (sg.t0 + c * Q)); };
-    auto slot_prep = [&](int c, int s) { return prep + ((c & 1) * 2 + (SAME ? 0 : s)) * kPrepFloats; };
+    auto slot_prep = [&](int c, int s) { return prep_slot<NB, SAME, OUT>(smem, c, s); };
+    auto wait_prep = [&](int c) { return wait(kPrepFull + (c & 3), (c >> 2) & 1); };
 
     // A quarter of U, transposed: rows (slot, p) 32 (warp % 4) .., 32 tokens, as three bf16 terms in TMEM.  The
     // tile is read through transposing 8 x 8 loads, so that a thread's word holds two tokens of one row.
-    auto u_quarter = [&](int c, int q) {
-        const int st = c & 1, b = q & 1, k = 2 * c + (q >> 1), lq = warp & 3;
-        if (k > 0 && !wait(kUEmpty + b, (k - 1) & 1)) return false;
+    auto u_quarter = [&](int c, int st, int q) {
+        const int k = 4 * c + q, b = k % NU, lq = warp & 3;
+        if (k >= NU && !wait(kUEmpty + b, (k / NU - 1) & 1)) return false;
         tc_fence_after();
         const float* w = slot_prep(c, lq >> 1) + 128 + 32 * q + 2 * (lane & 3);
         float2 wk[4];
@@ -329,7 +350,7 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                 u = rest2(u, mid[i]);
                 lo[i] = pack_bf16(u.x, u.y);
             }
-            const uint32_t tu = tmem + TU + 48 * b + ((uint32_t)(lq * 32 + 16 * hh) << 16);
+            const uint32_t tu = tmem + U0 + 48 * b + ((uint32_t)(lq * 32 + 16 * hh) << 16);
             tmem_st_16x16(tu, hi);
             tmem_st_16x16(tu + 16, mid);
             tmem_st_16x16(tu + 32, lo);
@@ -339,195 +360,259 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
         arrive_warp(kUFull + b);
         return true;
     };
-
-    // registers by role: 256 x 160 + 128 x 96 + 128 x 72 of the launch's 512 x 128
-    if (warp >= 12) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    else if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
-    if (warp < 8) {
-        // ---------------------------------------------------------------- M, C S, state, Y
-        const int wg = warp >> 2, lq = warp & 3;
-        const int row = 32 * lq + lane;              // token of the chunk; row (slot, p) of the state
-        const uint32_t lanes = (uint32_t)(lq * 32) << 16;
-        const int srow = row >> 6, p = SAME ? row : row & 63;
-        constexpr int SN = NC / 2;                   // state columns of this thread: SN wg ..
-        float S[SN];
-        {
-            const int h = un.h[srow];
-            const float* from = OUT && h >= 0 && p < a.P ? ssm_entering(a, sg, seg, h) : nullptr;
-            const int rows = from ? a.N - SN * wg : 0;
-            from += (size_t)(SN * wg) * a.P + p;
-#pragma unroll
-            for (int j = 0; j < SN; ++j, from += a.P) S[j] = j < rows ? *from : 0.f;
-        }
-        const uint32_t sbrow = smem_u32(smem + L::SB + (SN == 64 ? wg * HALF : 0)) + sw(row, SN == 64 ? 0 : 4 * wg);
-        // S cut to bf16, or what the cut left rounded to it, as C S's operand
-        auto copy_state = [&](bool rest) {
-#pragma unroll
-            for (int j = 0; j < SN; j += 8) {
-                uint32_t o[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (rest)   // not before its place: the results of all of S at once would not fit the registers
-                        asm volatile("" : "+f"(S[j + 2 * e]), "+f"(S[j + 2 * e + 1]));
-                    const float2 v = make_float2(S[j + 2 * e], S[j + 2 * e + 1]);
-                    o[e] = __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632);
-                    if (rest) {
-                        const float2 r = rest2(v, o[e]);
-                        o[e] = pack_bf16(r.x, r.y);
-                    }
-                }
-                // the thread's columns are one half tile (SN 64) or half the chunks of one (SN 32)
-                sts128(sbrow ^ (j << 1), o);
+    // What lies past the end of the row may be another document's and no number: X and B there become zeros,
+    // which cannot spoil a sum by meeting M's or U's zeros.  Eight warps, one row and one half tile each thread.
+    auto clear_tail = [&](int c, int st) {
+        const int len = chunk_len(c), row = tid & 127, half = tid >> 7;
+        if (len == Q) return true;
+        if (!wait(kFull + st, (c / NST) & 1) || (OUT && !wait(kBFull, c & 1))) return false;
+        if (row >= len)
+#pragma unroll 1
+            for (int j = 0; j < 128; j += 16) {
+                const uint32_t zero[4] = {0, 0, 0, 0};
+                sts128(smem_u32(smem + L::X + (2 * st + half) * HALF) + row * 128 + j, zero);
+                if (half < NB) sts128(smem_u32(smem + L::B + ((OUT ? 0 : NB * st) + half) * HALF) + row * 128 + j, zero);
             }
-            fence_async_smem();
-        };
-        if (OUT && nch > 0) {
-            copy_state(false);
-            arrive_warp(kSB);
+        fence_async_smem();
+        arrive_warp(kTail);
+        return true;
+    };
+
+    // registers by role (the launch has 640 x 96): 256 x 88 + 128 x 160 + 256 x 72
+    if (NB == 2) {
+        if (warp >= 16) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        else if (warp >= 12) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+        else if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    }
+
+    if (!OUT && warp < 12) {
+        // ---------------------------------------------------------------- states only: quarter k by warpgroup k % 3
+        const int wg = warp >> 2;
+        for (int c = 0, st = 0; c < nch; ++c, st = st + 1 == NST ? 0 : st + 1) {
+            if (!wait_prep(c) || !wait(kFull + st, (c / NST) & 1)) break;
+            if (wg < 2 && !clear_tail(c, st)) break;
+            if (chunk_len(c) < Q && !wait(kTail, 0)) break;
+            bool ok = true;
+#pragma unroll 1
+            for (int q = 0; q < 4 && ok; ++q)
+                if ((4 * c + q) % 3 == wg) ok = u_quarter(c, st, q);
+            if (!ok) break;
+            arrive_warp(kPrepEmpty + (c & 3));
         }
+    } else if (warp < 8) {
+        // ---------------------------------------------------------------- M, C S, Y
+        const int wg = warp >> 2, lq = warp & 3;
+        const int row = 32 * lq + lane;              // token of the chunk
+        const uint32_t lanes = (uint32_t)(lq * 32) << 16;
+        constexpr uint32_t PS = SAME ? 0 : 4 * kPrepFloats;
+        const int h = wg ? un.h[1] : un.h[0];
+        const float dsk = a.d_skip && h >= 0 ? a.d_skip[h] : 0.f;
+        const uint32_t ty = tmem + TY + lanes + 64 * wg;
         for (int c = 0; c < nch; ++c) {
             const uint32_t par = c & 1;
             const int st = c & 1, len = chunk_len(c);
-            uint8_t* xh = smem + L::X + (2 * st + wg) * HALF;
-            if (!wait(kPrepFull + st, (c >> 1) & 1)) break;
-            if (len < Q) {
-                // rows past the end may hold another document's values: as zeros they cannot meet M's zeros
-                if (!wait(kFull + st, (c >> 1) & 1)) break;
-                if (row >= len)
+            const uint32_t pr = smem_u32(slot_prep(c, 0));
+            const uint32_t xrow = smem_u32(smem + L::X + (2 * st + wg) * HALF) + sw(row, 0);
+            if (!wait_prep(c) || !clear_tail(c, st)) break;
+            // C S of this warpgroup's columns, scaled by exp(l_t)
+            float ls = lds1f(pr + wg * PS + 4 * (256 + row));
+#pragma unroll 1
+            for (int k = 0; k < lq; ++k) ls += lds1f(pr + wg * PS + 4 * (512 + k));
+            const float2 el = dup(ex2(ls));
+            if (!wait(kY2, par)) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int j = 0; j < 64; j += 32) {
+                float v[32];
+                uint32_t r[32];
+                tmem_ld16(ty + j, v);
+                tmem_ld16(ty + j + 16, v + 16);
+                tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(xh + row * 128 + 16 * j) = make_uint4(0, 0, 0, 0);
-                fence_async_smem();
-                arrive_warp(kTail);
+                for (int i = 0; i < 32; i += 2) {
+                    const float2 y = mul2(make_float2(v[i], v[i + 1]), el);
+                    r[i] = __float_as_uint(y.x);
+                    r[i + 1] = __float_as_uint(y.y);
+                }
+                tmem_st16(ty + j, r);
+                tmem_st16(ty + j + 16, r + 16);
             }
-            if (OUT) {
-                const uint32_t pr = smem_u32(slot_prep(c, 0));
-                constexpr uint32_t PS = SAME ? 0 : 4 * kPrepFloats;
-                if (!wait(kG, par)) break;
-                tc_fence_after();
-                // (not unrolled: fetching code that all roles' loops cannot keep in the instruction cache
-                // costs more than the loop)
-                bool ok = true;
+            if (!wait(kG, par)) break;
+            tc_fence_after();
+            // (not unrolled: fetching code that all roles' loops cannot keep in the instruction cache
+            // costs more than the loop)
 #pragma unroll 1
-                for (int b = 0; b < 2; ++b) {
-                    const int J = wg == 0 ? 3 * b : 1 + b;
-                    if (b == 1) {     // C S of the cut state is complete: its remainder takes the same place
-                        ok = wait(kY2, par);
-                        if (!ok) break;
-                        copy_state(true);
-                        arrive_warp(kSBLo);
-                    }
-                    const uint32_t tg = tmem + TG + lanes + 32 * J;
-                    if (J > lq) {
-                        uint32_t m[16];
+            for (int b = 0; b < 2; ++b) {
+                const int J = 2 * b + (wg ^ b);
+                const uint32_t tg = tmem + TG + lanes + 32 * J;
+                if (J > lq) {
+                    uint32_t m[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) m[i] = 0;
-                        tmem_st16(tg, m);
-                        tmem_st16(tg + 16, m);
-                        continue;
-                    }
-                    float v[32];
-                    tmem_ld16(tg, v);
-                    tmem_ld16(tg + 16, v + 16);
-                    tmem_ld_wait();
+                    for (int i = 0; i < 16; ++i) m[i] = 0;
+                    tmem_st16(tg, m);
+                    tmem_st16(tg + 16, m);
+                } else {
+                float v[32];
+                tmem_ld16(tg, v);
+                tmem_ld16(tg + 16, v + 16);
+                tmem_ld_wait();
 #pragma unroll 1
-                    for (int s = 0; s < (SAME ? 1 : 2); ++s) {
-                        const uint32_t ps = pr + s * PS;
-                        float l = lds1f(ps + 4 * (256 + row));
-                        if (J == lq) {           // the diagonal block: an exponential each, columns up to the row
+                for (int s = 0; s < (SAME ? 1 : 2); ++s) {
+                    const uint32_t ps = pr + s * PS;
+                    float l = lds1f(ps + 4 * (256 + row));
+                    if (J == lq) {           // the diagonal block: an exponential each, columns up to the row
 #pragma unroll
-                            for (int c0 = 0; c0 < 32; c0 += 16) {
-                                float4 l4[4];
+                        for (int c0 = 0; c0 < 32; c0 += 16) {
+                            float4 l4[4];
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) l4[i] = lds4f(ps + 4 * (32 * J + c0 + 4 * i));
-                                uint32_t m[8];
+                            for (int i = 0; i < 4; ++i) l4[i] = lds4f(ps + 4 * (32 * J + c0 + 4 * i));
+                            uint32_t m[8];
 #pragma unroll
-                                for (int i = 0; i < 16; i += 4) {
-                                    const float4 k = l4[i >> 2];
-                                    const float2 x0 = fma2(make_float2(k.x, k.y), dup(-1.f), dup(l));
-                                    const float2 x1 = fma2(make_float2(k.z, k.w), dup(-1.f), dup(l));
-                                    const int j = c0 + i;
-                                    const float2 e0 = mul2(make_float2(v[j], v[j + 1]), make_float2(ex2(x0.x), ex2(x0.y)));
-                                    const float2 e1 = mul2(make_float2(v[j + 2], v[j + 3]), make_float2(ex2(x1.x), ex2(x1.y)));
-                                    m[i >> 1] = pack_bf16(j <= lane ? e0.x : 0.f, j + 1 <= lane ? e0.y : 0.f);
-                                    m[(i >> 1) + 1] = pack_bf16(j + 2 <= lane ? e1.x : 0.f, j + 3 <= lane ? e1.y : 0.f);
-                                }
-                                tmem_st8(tg + c0 + 8 * s, m);
+                            for (int i = 0; i < 16; i += 4) {
+                                const float4 k = l4[i >> 2];
+                                const float2 x0 = fma2(make_float2(k.x, k.y), dup(-1.f), dup(l));
+                                const float2 x1 = fma2(make_float2(k.z, k.w), dup(-1.f), dup(l));
+                                const int j = c0 + i;
+                                const float2 e0 = mul2(make_float2(v[j], v[j + 1]), make_float2(ex2(x0.x), ex2(x0.y)));
+                                const float2 e1 = mul2(make_float2(v[j + 2], v[j + 3]), make_float2(ex2(x1.x), ex2(x1.y)));
+                                m[i >> 1] = pack_bf16(j <= lane ? e0.x : 0.f, j + 1 <= lane ? e0.y : 0.f);
+                                m[(i >> 1) + 1] = pack_bf16(j + 2 <= lane ? e1.x : 0.f, j + 3 <= lane ? e1.y : 0.f);
                             }
-                        } else {                 // a factor of the column to the block's end, one of the row from there
+                            tmem_st8(tg + c0 + 8 * s, m);
+                        }
+                    } else {                 // a factor of the column to the block's end, one of the row from there
 #pragma unroll 1
-                            for (int k = J + 1; k < lq; ++k) l += lds1f(ps + 4 * (512 + k));
-                            const float2 rf = dup(ex2(l));
+                        for (int k = J + 1; k < lq; ++k) l += lds1f(ps + 4 * (512 + k));
+                        const float2 rf = dup(ex2(l));
 #pragma unroll
-                            for (int c0 = 0; c0 < 32; c0 += 16) {
-                                float4 f4[4];
+                        for (int c0 = 0; c0 < 32; c0 += 16) {
+                            float4 f4[4];
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) f4[i] = lds4f(ps + 4 * (384 + 32 * J + c0 + 4 * i));
-                                uint32_t m[8];
+                            for (int i = 0; i < 4; ++i) f4[i] = lds4f(ps + 4 * (384 + 32 * J + c0 + 4 * i));
+                            uint32_t m[8];
 #pragma unroll
-                                for (int i = 0; i < 16; i += 4) {
-                                    const float4 k = f4[i >> 2];
-                                    const int j = c0 + i;
-                                    const float2 e0 = mul2(make_float2(v[j], v[j + 1]), mul2(make_float2(k.x, k.y), rf));
-                                    const float2 e1 = mul2(make_float2(v[j + 2], v[j + 3]), mul2(make_float2(k.z, k.w), rf));
-                                    m[i >> 1] = pack_bf16(e0.x, e0.y);
-                                    m[(i >> 1) + 1] = pack_bf16(e1.x, e1.y);
-                                }
-                                tmem_st8(tg + c0 + 8 * s, m);
+                            for (int i = 0; i < 16; i += 4) {
+                                const float4 k = f4[i >> 2];
+                                const int j = c0 + i;
+                                const float2 e0 = mul2(make_float2(v[j], v[j + 1]), mul2(make_float2(k.x, k.y), rf));
+                                const float2 e1 = mul2(make_float2(v[j + 2], v[j + 3]), mul2(make_float2(k.z, k.w), rf));
+                                m[i >> 1] = pack_bf16(e0.x, e0.y);
+                                m[(i >> 1) + 1] = pack_bf16(e1.x, e1.y);
                             }
+                            tmem_st8(tg + c0 + 8 * s, m);
                         }
                     }
                 }
-                if (!ok) break;
-                // C S of this warpgroup's columns, scaled by exp(l_t)
-                if (!wait(kY2Lo, par)) break;
-                tc_fence_after();
-                {
-                    float l = lds1f(pr + wg * PS + 4 * (256 + row));
-#pragma unroll 1
-                    for (int k = 0; k < lq; ++k) l += lds1f(pr + wg * PS + 4 * (512 + k));
-                    const float2 el = dup(ex2(l));
-                    const uint32_t ty = tmem + TY + lanes + 64 * wg;
-#pragma unroll 1
-                    for (int j = 0; j < 64; j += 32) {
-                        float v[32];
-                        uint32_t r[32];
-                        tmem_ld16(ty + j, v);
-                        tmem_ld16(ty + j + 16, v + 16);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            const float2 y = mul2(make_float2(v[i], v[i + 1]), el);
-                            r[i] = __float_as_uint(y.x);
-                            r[i + 1] = __float_as_uint(y.y);
-                        }
-                        tmem_st16(ty + j, r);
-                        tmem_st16(ty + j + 16, r + 16);
-                    }
                 }
                 tmem_st_wait();
                 tc_fence_before();
-                arrive_warp(kM);
+                arrive_warp(kM + b);
             }
-            if (!OUT && wg == 1) {
-                if (len == Q && !wait(kFull + st, (c >> 1) & 1)) break;
-                if (len < Q && !wait(kTail, 0)) break;
-                if (!u_quarter(c, 1) || !u_quarter(c, 3)) break;
+            arrive_warp(kPrepEmpty + (c & 3));
+            if (!wait(kXRead + st, (c >> 1) & 1) || !wait(kMX, par)) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int j = 0; j < 8; j += 4) {
+                float v[32];
+                uint4 u[4];
+                tmem_ld16(ty + 8 * j, v);
+                tmem_ld16(ty + 8 * j + 16, v + 16);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) u[k] = lds128(xrow ^ ((j + k) << 4));
+                tmem_ld_wait();
+                if (j) {
+                    tc_fence_before();
+                    arrive_warp(kYRead);      // C S of the next chunk may start
+                }
+                // y over x, which nothing else reads any more
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+                    uint32_t o[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 y = fma2(dup(dsk), bf2(w[e]), make_float2(v[8 * k + 2 * e], v[8 * k + 2 * e + 1]));
+                        o[e] = pack_bf16(y.x, y.y);
+                    }
+                    sts128(xrow ^ ((j + k) << 4), o);
+                }
             }
-            if (!wait(kD3, par)) break;
+            if (len == Q) {
+                fence_async_smem();       // the copy warp stores the tile
+            } else if (row < len && h >= 0) {
+                const int p0 = SAME ? 64 * wg : 0;
+                __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + ((size_t)(sg.t0 + c * Q + row) * a.H + h) * a.P + p0;
+#pragma unroll 1
+                for (int k = 0; k < 8 && p0 + 8 * k < a.P; ++k) *reinterpret_cast<uint4*>(y + 8 * k) = lds128(xrow ^ (k << 4));
+            }
+            arrive_warp(kYOut + st);
+        }
+    } else if (warp < 12) {
+        // ---------------------------------------------------------------- U
+        for (int c = 0; c < nch; ++c) {
+            const int st = c & 1;
+            if (!wait_prep(c) || !wait(kFull + st, (c / NST) & 1)) break;
+            if (chunk_len(c) < Q && !wait(kTail, 0)) break;
+            bool ok = true;
+#pragma unroll 1
+            for (int q = 0; q < 4 && ok; ++q) ok = u_quarter(c, st, q);
+            if (!ok) break;
+            arrive_warp(kXRead + st);
+            arrive_warp(kPrepEmpty + (c & 3));
+        }
+    } else if (warp < 16) {
+        // ---------------------------------------------------------------- the state: row (slot, p), NC columns
+        const int lq = warp & 3, row = 32 * lq + lane, srow = row >> 6, p = SAME ? row : row & 63;
+        const int h = srow ? un.h[1] : un.h[0];
+        float S[NC];
+        {
+            const float* from = OUT && h >= 0 && p < a.P ? ssm_entering(a, sg, seg, h) : nullptr;
+            const int rows = from ? a.N : 0;
+            from += p;
+#pragma unroll
+            for (int j = 0; j < NC; ++j, from += a.P) S[j] = j < rows ? *from : 0.f;
+        }
+        const uint32_t sbrow = smem_u32(smem + L::SB) + sw(row, 0);
+        // S cut to bf16, and what the cut left rounded to it, as C S's operands
+        auto copy_state = [&]() {
+#pragma unroll
+            for (int j = 0; j < NC; j += 8) {
+                uint32_t o[4], r[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    // not before its place: the results of all of S at once would not fit the registers
+                    asm volatile("" : "+f"(S[j + 2 * e]), "+f"(S[j + 2 * e + 1]));
+                    const float2 v = make_float2(S[j + 2 * e], S[j + 2 * e + 1]);
+                    o[e] = __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632);
+                    const float2 d = rest2(v, o[e]);
+                    r[e] = pack_bf16(d.x, d.y);
+                }
+                const uint32_t at = (sbrow + (j >> 6) * HALF) ^ ((j & 63) << 1);
+                sts128(at, o);
+                sts128(at + NB * HALF, r);
+            }
+            fence_async_smem();
+            arrive_warp(kSB);
+        };
+        if (OUT && nch > 0) {
+            copy_state();
+        }
+        for (int c = 0; c < nch; ++c) {
+            const uint32_t par = c & 1;
+            if (!wait_prep(c) || !wait(kD3, par)) break;
             tc_fence_after();
             {
-                const float eq = lds1f(smem_u32(slot_prep(c, srow)) + 4 * 516);
-                const uint32_t td = tmem + TD + lanes + SN * wg;
+                const float2 eq = dup(lds1f(smem_u32(slot_prep(c, srow)) + 4 * 516));
+                const uint32_t td = tmem + TD + ((uint32_t)(lq * 32) << 16);
 #pragma unroll
-                for (int j = 0; j < SN; j += 32) {
-                    float v[32];
+                for (int j = 0; j < NC; j += 16) {
+                    float v[16];
                     tmem_ld16(td + j, v);
-                    tmem_ld16(td + j + 16, v + 16);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const float2 n = fma2(dup(eq), make_float2(S[j + i], S[j + i + 1]), make_float2(v[i], v[i + 1]));
+                    for (int i = 0; i < 16; i += 2) {
+                        const float2 n = fma2(eq, make_float2(S[j + i], S[j + i + 1]), make_float2(v[i], v[i + 1]));
                         S[j + i] = n.x;
                         S[j + i + 1] = n.y;
                     }
@@ -535,191 +620,133 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
             }
             tc_fence_before();
             arrive_warp(kD3Free);
-            if (OUT) {
-                copy_state(false);
-                if (!wait(kMX, par)) break;
-                tc_fence_after();
-                const int h = un.h[wg];
-                const float dsk = a.d_skip && h >= 0 ? a.d_skip[h] : 0.f;
-                const uint32_t ty = tmem + TY + lanes + 64 * wg, xrow = smem_u32(xh) + sw(row, 0);
-#pragma unroll 1
-                for (int j = 0; j < 8; j += 4) {
-                    float v[32];
-                    uint4 u[4];
-                    tmem_ld16(ty + 8 * j, v);
-                    tmem_ld16(ty + 8 * j + 16, v + 16);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) u[k] = lds128(xrow ^ ((j + k) << 4));
-                    tmem_ld_wait();
-                    if (j) {
-                        tc_fence_before();
-                        arrive_warp(kSB);     // S is copied and Y read: C S of the next chunk may start
-                    }
-                    // y over x, which nothing else reads any more
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
-                        uint32_t o[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 y = fma2(dup(dsk), bf2(w[e]), make_float2(v[8 * k + 2 * e], v[8 * k + 2 * e + 1]));
-                            o[e] = pack_bf16(y.x, y.y);
-                        }
-                        sts128(xrow ^ ((j + k) << 4), o);
-                    }
-                }
-                if (len == Q) {
-                    fence_async_smem();       // the copy warp stores the tile
-                } else if (row < len && h >= 0) {
-                    const int p0 = SAME ? 64 * wg : 0;
-                    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) +
-                                       ((size_t)(sg.t0 + c * Q + row) * a.H + h) * a.P + p0;
-#pragma unroll 1
-                    for (int k = 0; k < 8 && p0 + 8 * k < a.P; ++k)
-                        *reinterpret_cast<uint4*>(y + 8 * k) = *reinterpret_cast<const uint4*>(xh + sw(row, k));
-                }
-                arrive_warp(kYOut + st);
+            arrive_warp(kPrepEmpty + (c & 3));
+            if (OUT && c + 1 < nch) {
+                if (!wait(kY2, par)) break;      // C S has read the copies
+                copy_state();
             }
-            arrive_warp(kPrepEmpty + st);
         }
         if (*fail == 0) {
-            const int h = un.h[srow];
             float* to = h < 0 || p >= a.P ? nullptr
                       : OUT ? ssm_leaving(a, sg, seg, h) : a.states + ((size_t)seg * a.H + h) * a.N * a.P;
-            const int rows = to ? a.N - SN * wg : 0;
-            to += (size_t)(SN * wg) * a.P + p;
+            const int rows = to ? a.N : 0;
+            to += p;
 #pragma unroll
-            for (int j = 0; j < SN; ++j, to += a.P)
+            for (int j = 0; j < NC; ++j, to += a.P)
                 if (j < rows) *to = S[j];
         }
-    } else if (warp < 12) {
-        // ---------------------------------------------------------------- U, transposed: row (slot, p), 32 tokens a quarter
-        const int row = 32 * (warp & 3) + lane;
-        for (int c = 0; c < nch; ++c) {
-            const int st = c & 1, len = chunk_len(c);
-            if (!wait(kFull + st, (c >> 1) & 1) || !wait(kPrepFull + st, (c >> 1) & 1)) break;
-            if (len < Q) {
-                // B past the end: zeros for the same reason as X there
-                if (row >= len)
-#pragma unroll
-                    for (int j = 0; j < 8 * NB; ++j)
-                        *reinterpret_cast<uint4*>(smem + L::B + (NB * st + (j >> 3)) * HALF + row * 128 + 16 * (j & 7)) =
-                            make_uint4(0, 0, 0, 0);
-                fence_async_smem();
-            }
-            bool ok = len == Q || wait(kTail, 0);
-            // (with the state alone to form, the second warpgroup takes every other quarter)
-#pragma unroll 1
-            for (int q = 0; q < 4 && ok; q += OUT ? 1 : 2) ok = u_quarter(c, q);
-            if (!ok) break;
-            arrive_warp(kPrepEmpty + st);
-        }
-    } else if (warp == 12) {
+    } else if (OUT && warp == 16) {
         // ---------------------------------------------------------------- G, C S, M X
-        if (OUT && lane == 0) {
+        if (lane == 0) {
             constexpr uint32_t idG = idesc_bf16(128, 128, 0, 0), idX = idesc_bf16(128, SAME ? 128 : 64, 0, 1);
-            const uint32_t sc = smem_u32(smem + L::C), ss = smem_u32(smem + L::SB);
+            const uint32_t dc = desc_lo(smem_u32(smem + L::C), 16), ds = desc_lo(smem_u32(smem + L::SB), 16);
+            const uint32_t db = desc_lo(smem_u32(smem + L::B), 16);
             for (int c = 0; c < nch; ++c) {
                 const int st = c & 1;
-                const uint32_t sbt = smem_u32(smem + L::B + NB * st * HALF), sx = smem_u32(smem + L::X + 2 * st * HALF);
-                if (!wait1(kCFull, c & 1) || !wait1(kFull + st, (c >> 1) & 1)) break;
+                const uint32_t dx = desc_lo(smem_u32(smem + L::X + 2 * st * HALF), HALF);
+                if (!wait1(kCFull, c & 1) || !wait1(kBFull, c & 1)) break;
                 if (c > 0 && !wait1(kMX, (c - 1) & 1)) break;    // M, over which G goes, has been read
                 tc_fence_after();
-                const uint32_t dc = desc_lo(sc, 16), db = desc_lo(sbt, 16), ds = desc_lo(ss, 16), dx = desc_lo(sx, HALF);
 #pragma unroll 1
-                for (uint32_t h = 0; h < NB; ++h)
+                for (uint32_t i = 0; i < NB; ++i)
                     steps<4>([&](auto kk) {
-                        mma_ss<kk * 32, kk * 32>(tmem + TG, dc + h * (HALF >> 4), db + h * (HALF >> 4), idG, h + kk > 0);
+                        mma_ss<kk * 32, kk * 32>(tmem + TG, dc + i * (HALF >> 4), db + i * (HALF >> 4), idG, i + kk > 0);
                     });
                 mma_commit(&bar[kG]);
-                bool ok = true;
-#pragma unroll 1
-                for (int part = 0; part < 2 && ok; ++part) {     // S rounded, then the remainder
-                    ok = wait1(part ? kSBLo : kSB, c & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-#pragma unroll 1
-                    for (uint32_t h = 0; h < NB; ++h)
-                        steps<4>([&](auto kk) {
-                            mma_ss<kk * 32, kk * 32>(tmem + TY, dc + h * (HALF >> 4), ds + h * (HALF >> 4), idG, part + h + kk > 0);
-                        });
-                    mma_commit(&bar[part ? kY2Lo : kY2]);
-                }
-                if (!ok) break;
-                mma_commit(&bar[kCEmpty]);
-                if (!wait1(kM, c & 1)) break;
+                mma_commit(&bar[kBEmpty]);
+                if (!wait1(kSB, c & 1) || (c > 0 && !wait1(kYRead, (c - 1) & 1))) break;
                 tc_fence_after();
 #pragma unroll 1
-                for (uint32_t i = 0; i < (SAME ? 2 : 4); ++i) {      // four of a slot's eight steps
-                    const uint32_t sl = i >> 1, k0 = 4 * (i & 1);
+                for (uint32_t i = 0; i < 2 * NB; ++i)            // S cut to bf16, then the rest
                     steps<4>([&](auto kk) {
-                        mma_ts<kk * 2048>(tmem + TY + 64 * sl, tmem + TG + 16 * (k0 + kk) + 8 * sl,
-                                          dx + ((sl * HALF + k0 * 2048) >> 4), idX, 1);
+                        mma_ss<kk * 32, kk * 32>(tmem + TY, dc + (i % NB) * (HALF >> 4), ds + i * (HALF >> 4), idG, i + kk > 0);
+                    });
+                mma_commit(&bar[kY2]);
+                mma_commit(&bar[kCEmpty]);
+                if (!wait1(kFull + st, (c / NST) & 1)) break;
+                bool ok = true;
+#pragma unroll 1
+                for (uint32_t b = 0; b < 2 && ok; ++b) {         // tokens 64 b .. of the sum, as M's halves come
+                    ok = wait1(kM + b, c & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    steps<SAME ? 4 : 8>([&](auto i) {
+                        constexpr int sl = i >> 2, kk = i & 3;
+                        mma_ts<sl * HALF + kk * 2048>(tmem + TY + 64 * sl, tmem + TG + 64 * b + 16 * kk + 8 * sl,
+                                                      dx + b * (8192 >> 4), idX, 1);
                     });
                 }
+                if (!ok) break;
                 mma_commit(&bar[kMX]);
             }
         }
         __syncwarp();
-    } else if (warp == 13) {
+    } else if (warp == 17) {
         // ---------------------------------------------------------------- copies
         if (lane == 0) {
+            auto load_b = [&](int c, int st, uint64_t* full) {
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+                    tma_load_3d(smem + L::B + (NB * st + i) * HALF, &mb, 64 * i, un.g, sg.t0 + c * Q, full);
+            };
             auto load = [&](int c) {
-                const int st = c & 1, t = sg.t0 + c * Q;
-                mbar_expect_tx(&bar[kFull + st], (2 + NB) * HALF);
+                const int st = c % NST, t = sg.t0 + c * Q;
+                mbar_expect_tx(&bar[kFull + st], (2 + (OUT ? 0 : NB)) * HALF);
                 uint8_t* xs = smem + L::X + 2 * st * HALF;
                 tma_load_3d(xs, &mx, 0, un.h[0], t, &bar[kFull + st]);
                 // no second head: head index H is out of range, the tile is filled with zeros
                 tma_load_3d(xs + HALF, &mx, SAME ? 64 : 0, un.h[1] < 0 ? a.H : un.h[1], t, &bar[kFull + st]);
-                for (int i = 0; i < NB; ++i)
-                    tma_load_3d(smem + L::B + (NB * st + i) * HALF, &mb, 64 * i, un.g, t, &bar[kFull + st]);
+                if (!OUT) load_b(c, st, &bar[kFull + st]);
             };
-            auto load_c = [&](int c) {
-                mbar_expect_tx(&bar[kCFull], NB * HALF);
-                for (int i = 0; i < NB; ++i)
-                    tma_load_3d(smem + L::C + i * HALF, &mc, 64 * i, un.g, sg.t0 + c * Q, &bar[kCFull]);
-            };
-            if (nch > 0) {
-                load(0);
-                if (OUT) load_c(0);
-                if (nch > 1) load(1);
-            }
-            for (int c = 0; c < nch; ++c) {
-                const int st = c & 1;
-                if (OUT) {
-                    if (c + 1 < nch) {
-                        if (!wait1(kCEmpty, c & 1)) break;
-                        load_c(c + 1);
-                    }
-                    if (!wait1(kYOut + st, (c >> 1) & 1)) break;
-                    if (chunk_len(c) == Q) {
-                        const uint8_t* xs = smem + L::X + 2 * st * HALF;
-                        const int t = sg.t0 + c * Q;
-                        tma_store_3d(&my, xs, 0, un.h[0], t);
-                        if (un.h[1] >= 0) tma_store_3d(&my, xs + HALF, SAME ? 64 : 0, un.h[1], t);
-                        bulk_commit();
-                        bulk_wait_read0();
-                    }
-                } else {
-                    if (!wait1(kStage + st, (c >> 1) & 1)) break;
+            // chunk c's iteration brings what its buffers' last users leave free, in the order they do
+#pragma unroll 1
+            for (int c = -NST; c < nch; ++c) {
+                const bool next = c >= -1 && c + 1 < nch;
+                if (OUT && next) {
+                    if (c >= 0 && !wait1(kBEmpty, c & 1)) break;
+                    mbar_expect_tx(&bar[kBFull], NB * HALF);
+                    load_b(c + 1, 0, &bar[kBFull]);
+                    if (c >= 0 && !wait1(kCEmpty, c & 1)) break;
+                    mbar_expect_tx(&bar[kCFull], NB * HALF);
+#pragma unroll
+                    for (int i = 0; i < NB; ++i)
+                        tma_load_3d(smem + L::C + i * HALF, &mc, 64 * i, un.g, sg.t0 + (c + 1) * Q, &bar[kCFull]);
                 }
-                if (c + 2 < nch) load(c + 2);
+                if (c >= 0) {
+                    const int st = c % NST;
+                    if (OUT) {
+                        if (!wait1(kYOut + st, (c / NST) & 1)) break;
+                        if (chunk_len(c) == Q) {
+                            const uint8_t* xs = smem + L::X + 2 * st * HALF;
+                            const int t = sg.t0 + c * Q;
+                            tma_store_3d(&my, xs, 0, un.h[0], t);
+                            if (un.h[1] >= 0) tma_store_3d(&my, xs + HALF, SAME ? 64 : 0, un.h[1], t);
+                            bulk_commit();
+                            bulk_wait_read0();
+                        }
+                    } else if (!wait1(kStage + st, (c / NST) & 1)) {
+                        break;
+                    }
+                }
+                if (c + NST < nch) load(c + NST);
             }
         }
         __syncwarp();
-    } else if (warp == 14) {
+    } else if (warp == 18 || (!OUT && warp == 16)) {
         // ---------------------------------------------------------------- decays: lane = 4 tokens
-        float total[2] = {0.f, 0.f};
-        float ea[2], bias[2];
+        // (states only: the two warps take every other chunk)
+        constexpr int STEP = OUT ? 1 : 2;
+        float total[2] = {0.f, 0.f}, ea[2], bias[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             ea[s] = un.h[s] >= 0 ? expf(a.a_log[un.h[s]]) * kLog2e : 0.f;
             bias[s] = un.h[s] >= 0 ? a.dt_bias[un.h[s]] : 0.f;
         }
         const bool two = !SAME && un.h[1] >= 0;
-        const uint16_t* dt = static_cast<const uint16_t*>(a.dt) + (size_t)(sg.t0 + 4 * lane) * a.ds + un.h[0];
-        for (int c = 0; c < nch; ++c, dt += Q * a.ds) {
-            const int st = c & 1, len = chunk_len(c);
+        const int c0 = !OUT && warp == 16;
+        const uint16_t* dt = static_cast<const uint16_t*>(a.dt) + (size_t)(sg.t0 + c0 * Q + 4 * lane) * a.ds + un.h[0];
+        for (int c = c0; c < nch; c += STEP, dt += STEP * Q * a.ds) {
+            const int len = chunk_len(c);
             uint32_t x[4];         // both heads' dt_raw, requested before the wait (heads of a unit are neighbours)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -729,7 +756,7 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                     if (two) x[e] |= (uint32_t)dt[e * a.ds + 1] << 16;
                 }
             }
-            if (c >= 2 && !wait(kPrepEmpty + st, ((c >> 1) - 1) & 1)) break;
+            if (c >= kPrepBufs && !wait(kPrepEmpty + (c & 3), ((c >> 2) - 1) & 1)) break;
 #pragma unroll 1
             for (int s = 0; s < (SAME ? 1 : 2); ++s) {
                 const int h = s ? un.h[1] : un.h[0];
@@ -765,11 +792,13 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                 after += blk == 0 ? (b1 + b2) + b3 : blk == 1 ? b2 + b3 : blk == 2 ? b3 : 0.f;
                 const float pre[4] = {before + p1, before + p2, before + p3, before + p4};
                 float4* o = reinterpret_cast<float4*>(pr + 4 * lane);
-                o[0] = make_float4(pre[0] - __log2f(D[0]), pre[1] - __log2f(D[1]), pre[2] - __log2f(D[2]),
-                                   pre[3] - __log2f(D[3]));
                 o[32] = make_float4(D[0] * ex2(after + s1), D[1] * ex2(after + s2), D[2] * ex2(after + s3), D[3] * ex2(after));
-                o[64] = make_float4(pre[0], pre[1], pre[2], pre[3]);
-                o[96] = make_float4(D[0] * ex2(suf + s1), D[1] * ex2(suf + s2), D[2] * ex2(suf + s3), D[3] * ex2(suf));
+                if (OUT) {
+                    o[0] = make_float4(pre[0] - __log2f(D[0]), pre[1] - __log2f(D[1]), pre[2] - __log2f(D[2]),
+                                       pre[3] - __log2f(D[3]));
+                    o[64] = make_float4(pre[0], pre[1], pre[2], pre[3]);
+                    o[96] = make_float4(D[0] * ex2(suf + s1), D[1] * ex2(suf + s2), D[2] * ex2(suf + s3), D[3] * ex2(suf));
+                }
                 const float sum = (b0 + b1) + (b2 + b3);
                 if (lane == 0) {
                     *reinterpret_cast<float4*>(pr + 512) = make_float4(b0, b1, b2, b3);
@@ -777,50 +806,49 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                 }
                 if (s) total[1] += sum; else total[0] += sum;
             }
-            arrive_warp(kPrepFull + st);
+            arrive_warp(kPrepFull + (c & 3));
         }
-        if (!OUT && lane == 0)
-#pragma unroll
-            for (int s = 0; s < (SAME ? 1 : 2); ++s)
-                if (un.h[s] >= 0) a.decay[(size_t)seg * a.H + un.h[s]] = exp2f(total[s]);
-    } else {
+        if (!OUT && lane < 2) ptot[2 * c0 + lane] = lane ? total[1] : total[0];
+    } else if (warp == 19) {
         // ---------------------------------------------------------------- U^T B
         if (lane == 0) {
             constexpr uint32_t idU = idesc_bf16(128, NC, 0, 1);
-            for (int c = 0; c < nch; ++c) {
-                const int st = c & 1;
-                const uint32_t sbt = smem_u32(smem + L::B + NB * st * HALF);
-                bool ok = wait1(kFull + st, (c >> 1) & 1);
+            for (int c = 0, st = 0; c < nch; ++c, st = st + 1 == NST ? 0 : st + 1) {
+                const uint32_t sbt = smem_u32(smem + L::B + (OUT ? 0 : NB * st) * HALF);
+                bool ok = OUT ? wait1(kBFull, c & 1) : wait1(kFull + st, (c / NST) & 1);
 #pragma unroll 1
                 for (int q = 0; q < 4 && ok; ++q) {
-                    const int b = q & 1, k = 2 * c + (q >> 1);
-                    if (!wait1(kUFull + b, k & 1)) { ok = false; break; }
+                    const int k = 4 * c + q, b = k % NU;
+                    if (!wait1(kUFull + b, (k / NU) & 1)) { ok = false; break; }
                     if (q == 0 && c > 0 && !wait1(kD3Free, (c - 1) & 1)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t db = desc_lo(sbt + q * 4096, HALF);
                     steps<6>([&](auto i) {
                         constexpr int j = i >= 3, term = i - 3 * j;
-                        mma_ts<j * 2048>(tmem + TD, tmem + TU + 48 * b + 16 * term + 8 * j, db, idU, q + i > 0);
+                        mma_ts<j * 2048>(tmem + TD, tmem + U0 + 48 * b + 16 * term + 8 * j, db, idU, q + i > 0);
                     });
                     mma_commit(&bar[kUEmpty + b]);
                 }
                 if (!ok) break;
                 mma_commit(&bar[kD3]);
-                if (!OUT) mma_commit(&bar[kStage + st]);
+                mma_commit(&bar[OUT ? kBEmpty : kStage + st]);
             }
         }
         __syncwarp();
     }
     __syncthreads();
+    if (!OUT && tid < (SAME ? 1 : 2)) {
+        const int h = tid ? un.h[1] : un.h[0];
+        if (h >= 0) a.decay[(size_t)seg * a.H + h] = exp2f(ptot[tid] + ptot[2 + tid]);
+    }
     if (*fail && tid == 0) {
         // give copies and products in flight a bounded chance to land before the memory is released
         record_error(a.status, KDA_ERR_TIMEOUT);
 #pragma unroll 1
-        for (int b = 0; b < kBars; ++b)
-            if (b <= kCFull || (b >= kG && b <= kD3)) {
-                mbar_wait(&bar[b], 0, 1u << 12);
-                mbar_wait(&bar[b], 1, 1u << 12);
-            }
+        for (int b = 0; b < kBars; ++b) {
+            mbar_wait(&bar[b], 0, 1u << 12);
+            mbar_wait(&bar[b], 1, 1u << 12);
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -857,9 +885,9 @@ bool tile_map(CUtensorMap* m, const void* base, int cols, int heads, int TT, int
 template <int NB, bool SAME, bool OUT>
 cudaError_t launch_one(const SsmArgs& a, const CUtensorMap* m, cudaStream_t st) {
     auto kern = ssm_tc_kernel<NB, SAME, OUT>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<NB>::TOTAL);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<NB, OUT>::TOTAL);
     if (e != cudaSuccess) return e;
-    kern<<<dim3(a.nseg, ssm_tc_units(a.H, a.G, a.P)), 512, Lay<NB>::TOTAL, st>>>(a, m[0], m[1], m[2], m[3]);
+    kern<<<dim3(a.nseg, ssm_tc_units(a.H, a.G, a.P)), kThreads, Lay<NB, OUT>::TOTAL, st>>>(a, m[0], m[1], m[2], m[3]);
     return cudaGetLastError();
 }
 
