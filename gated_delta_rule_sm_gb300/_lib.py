@@ -8,6 +8,7 @@ available the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional
@@ -494,98 +495,122 @@ def gated_norm_backward(o, gate, weight, dy, *, eps: float = 1e-6, stream: Optio
 
 
 # ---- serving: states carried from prompts to single tokens ----
+#
+# A step's kernel takes a few microseconds, so these calls keep their own time short: one test per tensor, plain
+# integers for pointers, dimension structures kept by their values.
+
+_F32, _I32 = torch.float32, torch.int32
+_DTYPE_CODES = {torch.bfloat16: KDA_BF16, torch.float32: KDA_FP32}
 
 
-def _cuda(*ts):
-    """Every tensor given is on one CUDA device; returns it."""
-    dev = ts[0].device
-    if dev.type != "cuda":
-        raise ValueError("KDA inputs must be CUDA tensors")
-    for t in ts:
-        if t is not None and t.device != dev:
-            raise ValueError("all tensors of a call must be on one CUDA device")
-    return dev
-
-
-def _typed(name: str, t, dtype, shape=None):
-    """A contiguous tensor of the given dtype and shape (None passes)."""
-    if t is None:
-        return
-    if t.dtype != dtype:
+def _refuse(name: str, t, dtype, shape, dev):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: all tensors of a call must be on one CUDA device")
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _token_stride(name: str, t, lead: int) -> int:
-    """Elements between neighbouring tokens of t, whose first ``lead`` axes are tokens ([B, T] or [B]) and
-    whose other axes are one token's contiguous values: t may be a slice of a wider projection."""
+def _need(name: str, t, dtype, shape, dev):
+    """t's address, once it is a contiguous tensor of the dtype and shape on the device (None: no tensor)."""
+    if t is None:
+        return None
+    if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev):
+        _refuse(name, t, dtype, shape, dev)
+    return t.data_ptr()
+
+
+def _first(name: str, t, dims: int):
+    """The device index and dtype code of a call's leading tensor."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} axes, got {list(t.shape)}")
+    code = _DTYPE_CODES.get(t.dtype)
+    return t.get_device(), _dtype_code(t) if code is None else code
+
+
+@functools.lru_cache(maxsize=4096)
+def _token_stride(name: str, shape, strides, lead: int) -> int:
+    """Elements between neighbouring tokens of a tensor whose first ``lead`` axes are tokens ([B, T] or [B]) and
+    whose other axes are one token's contiguous values: it may be a slice of a wider projection."""
     want = 1
-    for size, stride in zip(reversed(t.shape[lead:]), reversed(t.stride()[lead:])):
-        if size > 1 and stride != want:
+    for k in range(len(shape) - 1, lead - 1, -1):
+        if strides[k] != want and shape[k] > 1:
             raise ValueError(f"{name}: the values of one token must be contiguous")
-        want *= size
-    shape, strides = t.shape[:lead], t.stride()[:lead]
-    step = None
-    for size, stride in zip(reversed(shape), reversed(strides)):
-        if size > 1:
+        want *= shape[k]
+    step = span = None
+    for k in range(lead - 1, -1, -1):
+        if shape[k] > 1:
             if step is None:
-                step, span = stride, stride * size
-            elif stride != span:
+                step = strides[k]
+            elif strides[k] != span:
                 raise ValueError(f"{name}: tokens must be evenly spaced over the leading axes")
-            else:
-                span = stride * size
+            span = strides[k] * shape[k]
     return want if step is None else step
 
 
-class _OnStream:
-    """The stream a call runs on: the given one or the current one.  Inside, torch allocates for that
-    stream, so buffers made there are safe to use and to drop there."""
-
-    def __init__(self, device, stream):
-        self.given = stream
-        self.ptr = (stream or torch.cuda.current_stream(device)).cuda_stream
-        self.ctx = None
-
-    def __enter__(self):
-        if self.given is not None:
-            self.ctx = torch.cuda.stream(self.given)
-            self.ctx.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
-
-    def workspace(self, device, kind: str, nbytes: int) -> torch.Tensor:
-        """One buffer per device, kind and stream: calls on different streams may overlap."""
-        return workspace_cache.get(device, f"{kind}@{self.ptr}", nbytes)
+def _raw_stream(dev: int, stream) -> int:
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _out(name: str, t, like_shape, dtype, device):
-    if t is None:
-        return torch.empty(like_shape, dtype=dtype, device=device)
-    _typed(name, t, dtype, like_shape)
-    return t
+def _empty(like, shape, dtype, stream):
+    """A new tensor, allocated for the stream the call runs on."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _ssm_dims(x, dt_raw, b, c, a_log, dt_bias, d_skip, lead: int, num_seqs: int) -> SsmDims:
-    H, P = x.shape[lead:]
-    G, N = b.shape[lead:]
-    tokens = tuple(x.shape[:lead])
-    if tuple(b.shape[:lead]) != tokens or c.shape != b.shape or tuple(dt_raw.shape) != (*tokens, H):
+def _scratch(like, dev: int, kind: str, ptr: int, nbytes: int, stream):
+    """One workspace per device, kind and stream: calls on different streams may overlap."""
+    buf = workspace_cache.buf.get((dev, kind, ptr))
+    if buf is None or buf.numel() < nbytes:
+        buf = _empty(like, (max(nbytes, 256),), torch.uint8, stream)
+        workspace_cache.buf[(dev, kind, ptr)] = buf
+    return buf
+
+
+@functools.lru_cache(maxsize=4096)
+def _ssm_layout(lead: int, code: int, n: int, x, xs, b, bs, c, cs, dt, ds):
+    """Checks of the shapes and strides of x, b, c and dt_raw: (dims reference, bytes of workspace of the scan, H)."""
+    tokens, H = x[:lead], x[lead]
+    if len(b) != lead + 2 or b[:lead] != tokens or c != b or dt != x[:lead + 1]:
         raise ValueError("x must be [..., H, P], b and c [..., G, N] and dt_raw [..., H] over the same tokens")
+    G = b[lead]
     if G < 1 or H % G:
         raise ValueError(f"heads ({H}) must be a multiple of the groups of b and c ({G})")
-    if not x.dtype == b.dtype == c.dtype == dt_raw.dtype:
+    dims = SsmDims(tokens[0], tokens[1] if lead == 2 else 1, H, G, b[-1], x[-1], code, n, _token_stride("x", x, xs, lead),
+                   _token_stride("b", b, bs, lead), _token_stride("c", c, cs, lead), _token_stride("dt_raw", dt, ds, lead))
+    ref = ctypes.byref(dims)
+    return ref, int(load().kda_ssm_fwd_workspace_size(ref)), H
+
+
+def _ssm_args(x, dt_raw, b, c, a_log, dt_bias, d_skip, lead: int, n: int, dev: int, code: int):
+    """Checks of the arguments that the scan and the step share: (dims reference, workspace bytes, addresses)."""
+    ref, nbytes, H = _ssm_layout(lead, code, n, x.shape, x.stride(), b.shape, b.stride(), c.shape, c.stride(), dt_raw.shape,
+                                 dt_raw.stride())
+    dtype = x.dtype
+    if b.dtype is not dtype or c.dtype is not dtype or dt_raw.dtype is not dtype:
         raise ValueError("x, b, c and dt_raw must have one dtype")
-    for name, t in (("a_log", a_log), ("dt_bias", dt_bias), ("d_skip", d_skip)):
-        _typed(name, t, torch.float32, (H,))
-    B, T = (tokens if lead == 2 else (tokens[0], 1))
-    return SsmDims(B, T, H, G, N, P, _dtype_code(x), num_seqs, _token_stride("x", x, lead), _token_stride("b", b, lead),
-                   _token_stride("c", c, lead), _token_stride("dt_raw", dt_raw, lead))
+    if b.get_device() != dev or c.get_device() != dev or dt_raw.get_device() != dev:
+        raise ValueError("all tensors of a call must be on one CUDA device")
+    per_head = (H,)
+    return ref, nbytes, (x.data_ptr(), dt_raw.data_ptr(), b.data_ptr(), c.data_ptr(),
+                         _need("a_log", a_log, _F32, per_head, dev), _need("dt_bias", dt_bias, _F32, per_head, dev),
+                         _need("d_skip", d_skip, _F32, per_head, dev))
+
+
+def _offsets(cu_seqlens, cu_seqlens_host, B: int, dev: int):
+    """(documents, rows, device address, host copy) of a call's packed-document offsets."""
+    if cu_seqlens is None:
+        return 0, B, None, host_offsets(cu_seqlens_host)
+    n = cu_seqlens.numel() - 1
+    return n, n, _need("cu_seqlens", cu_seqlens, _I32, (n + 1,), dev), host_offsets(cu_seqlens_host, n + 1)
 
 
 def ssm_scan(x, dt_raw, b, c, a_log, dt_bias, d_skip=None, *, cu_seqlens=None, cu_seqlens_host=None,
@@ -598,39 +623,34 @@ def ssm_scan(x, dt_raw, b, c, a_log, dt_bias, d_skip=None, *, cu_seqlens=None, c
     rows = B, or one per document of ``cu_seqlens`` (int32).
         S_t = exp(D_t a) S_{t-1} + D_t b_t x_t^T,  y_t = S_t^T c_t + d_skip x_t,
         D = softplus(dt_raw + dt_bias), a = -exp(a_log)."""
-    lib = load()
-    dev = _cuda(x, dt_raw, b, c, a_log, dt_bias, d_skip, cu_seqlens, initial_state)
-    if x.dim() != 4 or b.dim() != 4:
-        raise ValueError("x must be [B, T, H, P] and b [B, T, G, N]")
-    _typed("cu_seqlens", cu_seqlens, torch.int32)
-    n = int(cu_seqlens.numel() - 1) if cu_seqlens is not None else 0
-    dims = _ssm_dims(x, dt_raw, b, c, a_log, dt_bias, d_skip, 2, n)
-    rows = n if cu_seqlens is not None else dims.B
-    _typed("initial_state", initial_state, torch.float32, (rows, dims.H, dims.N, dims.P))
-    cu_h = host_offsets(cu_seqlens_host, rows + 1 if cu_seqlens is not None else None)
-    with _OnStream(dev, stream) as st:
-        out = _out("out", out, x.shape, x.dtype, dev)
-        if output_final_state:
-            final_state = _out("final_state", final_state, (rows, dims.H, dims.N, dims.P), torch.float32, dev)
-        else:
-            final_state = None
-        ws = st.workspace(dev, "ssm", int(lib.kda_ssm_fwd_workspace_size(ctypes.byref(dims))))
-        _check(lib.kda_ssm_fwd(ctypes.byref(dims), _ptr(x), _ptr(dt_raw), _ptr(b), _ptr(c), _ptr(a_log), _ptr(dt_bias),
-                               _ptr(d_skip), _ptr(cu_seqlens), cu_h, _ptr(initial_state), _ptr(out), _ptr(final_state),
-                               _ptr(ws), ws.numel(), st.ptr), "kda_ssm_fwd")
+    lib = _lib or load()
+    dev, code = _first("x", x, 4)
+    n, rows, cu, cu_h = _offsets(cu_seqlens, cu_seqlens_host, x.shape[0], dev)
+    ref, nbytes, args = _ssm_args(x, dt_raw, b, c, a_log, dt_bias, d_skip, 2, n, dev, code)
+    state_shape = (rows, x.shape[2], b.shape[3], x.shape[3])
+    s0 = _need("initial_state", initial_state, _F32, state_shape, dev)
+    st = _raw_stream(dev, stream)
+    if out is None:
+        out = _empty(x, x.shape, x.dtype, stream)
+    if not output_final_state:
+        final_state = None
+    elif final_state is None:
+        final_state = _empty(x, state_shape, _F32, stream)
+    ws = _scratch(x, dev, "ssm", st, nbytes, stream)
+    _check(lib.kda_ssm_fwd(ref, *args, cu, cu_h, s0, _need("out", out, x.dtype, x.shape, dev),
+                           _need("final_state", final_state, _F32, state_shape, dev), ws.data_ptr(), ws.numel(), st),
+           "kda_ssm_fwd")
     return out, final_state
 
 
-def _pool(name, pool, slots, B: int, cell, dtype, pool_out):
-    """Checks of a slot pool [num_slots, *cell]; returns (num_slots, the pool written)."""
-    if pool.dim() != 1 + len(cell) or tuple(pool.shape[1:]) != tuple(cell):
-        raise ValueError(f"{name} must be [slots, {', '.join(map(str, cell))}], got {list(pool.shape)}")
-    _typed(name, pool, dtype)
-    _typed("slots", slots, torch.int32, (B,))
+def _pool_args(name: str, pool, slots, B: int, cell, dtype, pool_out, dev: int):
+    """Checks of a slot pool [slots, *cell]: (slots address, number of slots, pool address, address written, pool written)."""
+    n = pool.shape[0] if pool.dim() else 0
+    shape = (n, *cell)
     if pool_out is None:
         pool_out = pool
-    _typed(f"{name}_out", pool_out, dtype, pool.shape)
-    return int(pool.shape[0]), pool_out
+    return (_need("slots", slots, _I32, (B,), dev), n, _need(name, pool, dtype, shape, dev),
+            _need(f"{name}_out", pool_out, dtype, shape, dev)), pool_out
 
 
 def ssm_step(x, dt_raw, b, c, a_log, dt_bias, d_skip=None, *, state, slots=None, state_out=None, out=None,
@@ -640,18 +660,22 @@ def ssm_step(x, dt_raw, b, c, a_log, dt_bias, d_skip=None, *, state, slots=None,
     ``state`` [slots, H, N, P] fp32 is the pool, row r works on slot ``slots[r]`` (int32; None: slot r; negative:
     the row is idle and gets zeros).  The pool is updated in place, or into ``state_out`` (only the named slots
     are written).  Returns (y, the pool written)."""
-    lib = load()
-    dev = _cuda(x, dt_raw, b, c, a_log, dt_bias, d_skip, state, slots, state_out)
-    if x.dim() != 3 or b.dim() != 3:
-        raise ValueError("x must be [B, H, P] and b [B, G, N]")
-    dims = _ssm_dims(x, dt_raw, b, c, a_log, dt_bias, d_skip, 1, 0)
-    n, state_out = _pool("state", state, slots, dims.B, (dims.H, dims.N, dims.P), torch.float32, state_out)
-    with _OnStream(dev, stream) as st:
-        out = _out("out", out, x.shape, x.dtype, dev)
-        _check(lib.kda_ssm_step(ctypes.byref(dims), _ptr(x), _ptr(dt_raw), _ptr(b), _ptr(c), _ptr(a_log), _ptr(dt_bias),
-                                _ptr(d_skip), _ptr(slots), n, _ptr(state), _ptr(state_out), _ptr(out), st.ptr),
-               "kda_ssm_step")
+    lib = _lib or load()
+    dev, code = _first("x", x, 3)
+    ref, _, args = _ssm_args(x, dt_raw, b, c, a_log, dt_bias, d_skip, 1, 0, dev, code)
+    B, H, P = x.shape
+    pool, state_out = _pool_args("state", state, slots, B, (H, b.shape[2], P), _F32, state_out, dev)
+    if out is None:
+        out = _empty(x, x.shape, x.dtype, stream)
+    _check(lib.kda_ssm_step(ref, *args, *pool, _need("out", out, x.dtype, x.shape, dev), _raw_stream(dev, stream)),
+           "kda_ssm_step")
     return out, state_out
+
+
+@functools.lru_cache(maxsize=4096)
+def _step_dims(*fields):
+    dims = KdaDims(*fields)
+    return dims, ctypes.byref(dims)
 
 
 def decode_step(q, k, v, g_raw, beta_raw, a_log, dt_bias, *, scale: float, lower_bound: float = -5.0,
@@ -661,25 +685,29 @@ def decode_step(q, k, v, g_raw, beta_raw, a_log, dt_bias, *, scale: float, lower
 
     q, k [B, Hk, K], v [B, H, V], g_raw [B, H, K], beta_raw [B, H]; ``state`` [slots, H, K, V] fp32, ``slots``,
     ``state_out`` as for :func:`ssm_step`.  Returns (out, the pool written)."""
-    lib = load()
-    dev = _cuda(q, k, v, g_raw, beta_raw, a_log, dt_bias, state, slots, state_out)
-    if q.dim() != 3 or v.dim() != 3:
-        raise ValueError("q must be [B, Hk, K] and v [B, H, V]")
+    lib = _lib or load()
+    dev, code = _first("q", q, 3)
+    if v.dim() != 3:
+        raise ValueError("v must be [B, H, V]")
     B, Hk, K = q.shape
     H, V = v.shape[1:]
-    for name, t, shape in (("q", q, (B, Hk, K)), ("k", k, (B, Hk, K)), ("v", v, (B, H, V)), ("g_raw", g_raw, (B, H, K)),
-                           ("beta_raw", beta_raw, (B, H))):
-        _typed(name, t, q.dtype, shape)
-    _typed("a_log", a_log, torch.float32, (H,))
-    _typed("dt_bias", dt_bias, torch.float32, (H * K,))
-    n, state_out = _pool("state", state, slots, B, (H, K, V), torch.float32, state_out)
-    dims = KdaDims(B, 1, H, K, V, _dtype_code(q), 0, Hk, _gate_code(gate))
-    with _OnStream(dev, stream) as st:
-        out = _out("out", out, v.shape, v.dtype, dev)
-        _check(lib.kda_decode_step(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(g_raw), _ptr(beta_raw), _ptr(a_log),
-                                   _ptr(dt_bias), float(scale), float(lower_bound), _ptr(slots), n, _ptr(state),
-                                   _ptr(state_out), _ptr(out), st.ptr), "kda_decode_step")
+    dtype, key, gates = q.dtype, (B, Hk, K), (B, H, K)
+    args = (_need("q", q, dtype, key, dev), _need("k", k, dtype, key, dev), _need("v", v, dtype, (B, H, V), dev),
+            _need("g_raw", g_raw, dtype, gates, dev), _need("beta_raw", beta_raw, dtype, (B, H), dev),
+            _need("a_log", a_log, _F32, (H,), dev), _need("dt_bias", dt_bias, _F32, (H * K,), dev))
+    pool, state_out = _pool_args("state", state, slots, B, (H, K, V), _F32, state_out, dev)
+    if out is None:
+        out = _empty(v, v.shape, dtype, stream)
+    _, ref = _step_dims(B, 1, H, K, V, code, 0, Hk, _gate_code(gate))
+    _check(lib.kda_decode_step(ref, *args, scale, lower_bound, *pool, _need("out", out, dtype, (B, H, V), dev),
+                               _raw_stream(dev, stream)), "kda_decode_step")
     return out, state_out
+
+
+def _conv_args(x, weight, bias, dev: int, C: int):
+    W = weight.shape[-1]
+    return W, (_need("weight", weight, _F32, (C, 1, W) if weight.dim() == 3 else (C, W), dev),
+               _need("bias", bias, _F32, (C,), dev))
 
 
 def short_conv_prompt(x, weight, bias=None, *, cu_seqlens=None, cu_seqlens_host=None, initial_history=None, out=None,
@@ -688,28 +716,21 @@ def short_conv_prompt(x, weight, bias=None, *, cu_seqlens=None, cu_seqlens_host=
 
     x [B, T, C] (a slice of a wider projection is taken as it is); histories [rows, W - 1, C] like x, oldest input
     first: the last W - 1 inputs before the row (None: zeros) and at its end."""
-    lib = load()
-    dev = _cuda(x, weight, bias, cu_seqlens, initial_history)
-    if x.dim() != 3:
-        raise ValueError("x must be [B, T, C]")
+    lib = _lib or load()
+    dev, code = _first("x", x, 3)
     B, T, C = x.shape
-    W = weight.shape[-1]
-    _typed("weight", weight, torch.float32)
-    if weight.numel() != C * W:
-        raise ValueError("weight must be [C, W]")
-    _typed("bias", bias, torch.float32, (C,))
-    _typed("cu_seqlens", cu_seqlens, torch.int32)
-    n = int(cu_seqlens.numel() - 1) if cu_seqlens is not None else 0
-    rows = n if cu_seqlens is not None else B
-    _typed("initial_history", initial_history, x.dtype, (rows, W - 1, C))
-    xs = _token_stride("x", x, 2)
-    cu_h = host_offsets(cu_seqlens_host, rows + 1 if cu_seqlens is not None else None)
-    with _OnStream(dev, stream) as st:
-        out = _out("out", out, x.shape, x.dtype, dev)
-        final_history = _out("final_history", final_history, (rows, W - 1, C), x.dtype, dev)
-        _check(lib.kda_short_conv_prompt(B, T, C, W, _dtype_code(x), _ptr(x), xs, _ptr(weight), _ptr(bias),
-                                         _ptr(cu_seqlens), cu_h, n, _ptr(initial_history), _ptr(out),
-                                         _ptr(final_history), st.ptr), "kda_short_conv_prompt")
+    W, params = _conv_args(x, weight, bias, dev, C)
+    n, rows, cu, cu_h = _offsets(cu_seqlens, cu_seqlens_host, B, dev)
+    hist = (rows, W - 1, C)
+    h0 = _need("initial_history", initial_history, x.dtype, hist, dev)
+    if out is None:
+        out = _empty(x, x.shape, x.dtype, stream)
+    if final_history is None:
+        final_history = _empty(x, hist, x.dtype, stream)
+    _check(lib.kda_short_conv_prompt(B, T, C, W, code, x.data_ptr(), _token_stride("x", x.shape, x.stride(), 2), *params, cu, cu_h, n, h0,
+                                     _need("out", out, x.dtype, x.shape, dev),
+                                     _need("final_history", final_history, x.dtype, hist, dev), _raw_stream(dev, stream)),
+           "kda_short_conv_prompt")
     return out, final_history
 
 
@@ -717,86 +738,85 @@ def short_conv_step(x, weight, bias=None, *, history, slots=None, history_out=No
                     stream: Optional[torch.cuda.Stream] = None):
     """One token per row through ``kda_short_conv_step``: x [B, C], ``history`` [slots, W - 1, C] like x; ``slots``
     and ``history_out`` as for :func:`ssm_step`.  Returns (y, the pool written)."""
-    lib = load()
-    dev = _cuda(x, weight, bias, history, slots, history_out)
-    if x.dim() != 2:
-        raise ValueError("x must be [B, C]")
+    lib = _lib or load()
+    dev, code = _first("x", x, 2)
     B, C = x.shape
-    W = weight.shape[-1]
-    _typed("weight", weight, torch.float32)
-    if weight.numel() != C * W:
-        raise ValueError("weight must be [C, W]")
-    _typed("bias", bias, torch.float32, (C,))
-    n, history_out = _pool("history", history, slots, B, (W - 1, C), x.dtype, history_out)
-    xs = _token_stride("x", x, 1)
-    with _OnStream(dev, stream) as st:
-        out = _out("out", out, x.shape, x.dtype, dev)
-        _check(lib.kda_short_conv_step(B, C, W, _dtype_code(x), _ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(slots), n,
-                                       _ptr(history), _ptr(history_out), _ptr(out), st.ptr), "kda_short_conv_step")
+    W, params = _conv_args(x, weight, bias, dev, C)
+    pool, history_out = _pool_args("history", history, slots, B, (W - 1, C), x.dtype, history_out, dev)
+    if out is None:
+        out = _empty(x, x.shape, x.dtype, stream)
+    _check(lib.kda_short_conv_step(B, C, W, code, x.data_ptr(), _token_stride("x", x.shape, x.stride(), 1), *params, *pool,
+                                   _need("out", out, x.dtype, x.shape, dev), _raw_stream(dev, stream)),
+           "kda_short_conv_step")
     return out, history_out
 
 
-def _pool_layers(name: str, pool):
+@functools.lru_cache(maxsize=4096)
+def _pool_layers(name: str, shape, strides, es: int):
     """(layers, pages, bytes of a page, bytes between layers) of a pool [layers, pages, ...]."""
-    if pool.dim() < 2 or pool.numel() == 0:
+    if len(shape) < 2 or 0 in shape:
         raise ValueError(f"{name} must be [layers, pages, ...]")
-    if not pool[0].is_contiguous():
-        raise ValueError(f"{name}: the pages of a layer must be contiguous")
-    es = pool.element_size()
-    page = pool[0, 0].numel() * es
-    return int(pool.shape[0]), int(pool.shape[1]), page, int(pool.stride(0)) * es
+    want = 1
+    for k in range(len(shape) - 1, 0, -1):
+        if strides[k] != want and shape[k] > 1:
+            raise ValueError(f"{name}: the pages of a layer must be contiguous")
+        want *= shape[k]
+    return shape[0], shape[1], want // shape[1] * es, strides[0] * es
 
 
-def _pages_dims(pool, table, lengths, refs, page_tokens: int) -> PagesDims:
-    if table.dim() != 2:
-        raise ValueError("table must be [sequences, pages of a row]")
-    _typed("table", table, torch.int32)
-    _typed("lengths", lengths, torch.int32, (table.shape[0],))
-    _typed("refs", refs, torch.int32)
-    d = PagesDims(1, refs.numel(), table.shape[0], table.shape[1], int(page_tokens), 1, 0)
-    if pool is not None:
-        layers, pages, page, stride = _pool_layers("pool", pool)
-        if pages != refs.numel():
-            raise ValueError(f"refs must hold one count per page ({pages}), got {refs.numel()}")
-        d.layers, d.page_bytes, d.layer_stride = layers, page, stride
-    return d
+@functools.lru_cache(maxsize=4096)
+def _pages_dims(n: int, *fields):
+    """(the structure, its reference, bytes of workspace for n requests)."""
+    dims = PagesDims(*fields)
+    ref = ctypes.byref(dims)
+    return dims, ref, int(load().kda_pages_workspace_size(ref, n))
 
 
-def _pages_outs(table, lengths, refs, table_out, lengths_out, refs_out):
-    outs = []
-    for name, t, o in (("table", table, table_out), ("lengths", lengths, lengths_out), ("refs", refs, refs_out)):
-        o = t if o is None else o
-        _typed(f"{name}_out", o, torch.int32, t.shape if t is not None else None)
-        outs.append(o)
-    return outs
+def _pages_args(pool, table, lengths, refs, table_out, lengths_out, refs_out, page_tokens: int, n: int):
+    """Checks of a cache's arrays: (device, dims reference, workspace bytes, inputs, outputs); lengths may be None."""
+    dev = table.get_device()
+    if (not table.is_cuda) or table.dim() != 2:
+        raise ValueError("table must be a CUDA tensor [sequences, pages of a row]")
+    shape = table.shape
+    rows, pages = (shape[0],), (refs.numel(),)
+    ins = (_need("table", table, _I32, shape, dev), _need("lengths", lengths, _I32, rows, dev),
+           _need("refs", refs, _I32, pages, dev))
+    outs = (ins[0] if table_out is None else _need("table_out", table_out, _I32, shape, dev),
+            ins[1] if lengths_out is None else _need("lengths_out", lengths_out, _I32, rows, dev),
+            ins[2] if refs_out is None else _need("refs_out", refs_out, _I32, pages, dev))
+    if pool is None:
+        layers, page, stride = 1, 1, 0
+    else:
+        layers, held, page, stride = _pool_layers("pool", pool.shape, pool.stride(), pool.element_size())
+        if pool.get_device() != dev:
+            raise ValueError("all tensors of a call must be on one CUDA device")
+        if held != pages[0]:
+            raise ValueError(f"refs must hold one count per page ({held}), got {pages[0]}")
+    _, ref, nbytes = _pages_dims(n, layers, pages[0], shape[0], shape[1], int(page_tokens), page, stride)
+    return dev, ref, nbytes, ins, outs
 
 
-def _requests(**named):
-    n = None
-    for name, t in named.items():
-        if t.dim() != 1:
-            raise ValueError(f"{name} must be one-dimensional")
-        _typed(name, t, torch.int32)
-        if n is not None and t.numel() != n:
-            raise ValueError(f"{' and '.join(named)} must have the same length")
-        n = t.numel()
-    return n
+def _requests(dev: int, n: int, **named):
+    return tuple(_need(name, t, _I32, (n,), dev) for name, t in named.items())
 
 
 def pages_copy(pool, src, dst, *, src_pool=None, stream: Optional[torch.cuda.Stream] = None):
     """Page ``src[i]`` of ``src_pool`` (default: ``pool``) to page ``dst[i]`` of ``pool`` [layers, pages, ...], every
     layer, through ``kda_pages_copy``.  Pairs out of range are skipped; dst must not repeat nor meet src in one pool."""
-    lib = load()
+    lib = _lib or load()
     src_pool = pool if src_pool is None else src_pool
-    dev = _cuda(pool, src_pool, src, dst)
-    layers, pages, page, stride = _pool_layers("pool", pool)
-    s_layers, s_pages, s_page, s_stride = _pool_layers("src_pool", src_pool)
+    dev = pool.get_device()
+    if not pool.is_cuda or src_pool.get_device() != dev:
+        raise ValueError("both pools must be on one CUDA device")
+    layers, pages, page, stride = _pool_layers("pool", pool.shape, pool.stride(), pool.element_size())
+    s_layers, s_pages, s_page, s_stride = _pool_layers("src_pool", src_pool.shape, src_pool.stride(),
+                                                       src_pool.element_size())
     if layers != s_layers or page != s_page:
         raise ValueError("both pools must have the same layers and page size")
-    n = _requests(src=src, dst=dst)
-    with _OnStream(dev, stream) as st:
-        _check(lib.kda_pages_copy(layers, page, _ptr(pool), stride, pages, _ptr(src_pool), s_stride, s_pages, _ptr(src),
-                                  _ptr(dst), n, st.ptr), "kda_pages_copy")
+    n = src.numel()
+    ps, pd = _requests(dev, n, src=src, dst=dst)
+    _check(lib.kda_pages_copy(layers, page, pool.data_ptr(), stride, pages, src_pool.data_ptr(), s_stride, s_pages, ps, pd,
+                              n, _raw_stream(dev, stream)), "kda_pages_copy")
     return pool
 
 
@@ -805,61 +825,56 @@ def pages_fork(pool, table, lengths, refs, parents, children, *, page_tokens: in
     """Row ``children[i]`` becomes a copy of row ``parents[i]`` through ``kda_pages_fork``: full pages are shared, a
     partly filled last page is copied into a free one.  pool [layers, pages, ...], table [sequences, M], lengths
     [sequences], refs [pages] int32, updated in place or into the ``*_out`` arrays.  Returns ok [n] int32."""
-    lib = load()
-    dev = _cuda(pool, table, lengths, refs, parents, children, table_out, lengths_out, refs_out)
-    dims = _pages_dims(pool, table, lengths, refs, page_tokens)
-    to, lo, ro = _pages_outs(table, lengths, refs, table_out, lengths_out, refs_out)
-    n = _requests(parents=parents, children=children)
-    with _OnStream(dev, stream) as st:
-        ok = _out("ok", ok, (n,), torch.int32, dev)
-        ws = st.workspace(dev, "pages", int(lib.kda_pages_workspace_size(ctypes.byref(dims), n)))
-        _check(lib.kda_pages_fork(ctypes.byref(dims), _ptr(pool), _ptr(table), _ptr(lengths), _ptr(refs), _ptr(parents),
-                                  _ptr(children), n, _ptr(to), _ptr(lo), _ptr(ro), _ptr(ok), _ptr(ws), ws.numel(),
-                                  st.ptr), "kda_pages_fork")
+    lib = _lib or load()
+    n = parents.numel()
+    dev, ref, nbytes, ins, outs = _pages_args(pool, table, lengths, refs, table_out, lengths_out, refs_out, page_tokens, n)
+    req = _requests(dev, n, parents=parents, children=children)
+    st = _raw_stream(dev, stream)
+    if ok is None:
+        ok = _empty(table, (n,), _I32, stream)
+    ws = _scratch(table, dev, "pages", st, nbytes, stream)
+    _check(lib.kda_pages_fork(ref, pool.data_ptr(), *ins, *req, n, *outs, _need("ok", ok, _I32, (n,), dev), ws.data_ptr(),
+                              ws.numel(), st), "kda_pages_fork")
     return ok
 
 
 def pages_extend(table, lengths, refs, seqs, new_lengths, *, page_tokens: int, table_out=None, lengths_out=None,
                  refs_out=None, ok=None, stream: Optional[torch.cuda.Stream] = None):
     """Row ``seqs[i]`` grows to ``new_lengths[i]`` tokens through ``kda_pages_extend``.  Returns ok [n] int32."""
-    lib = load()
-    dev = _cuda(table, lengths, refs, seqs, new_lengths, table_out, lengths_out, refs_out)
-    dims = _pages_dims(None, table, lengths, refs, page_tokens)
-    to, lo, ro = _pages_outs(table, lengths, refs, table_out, lengths_out, refs_out)
-    n = _requests(seqs=seqs, new_lengths=new_lengths)
-    with _OnStream(dev, stream) as st:
-        ok = _out("ok", ok, (n,), torch.int32, dev)
-        ws = st.workspace(dev, "pages", int(lib.kda_pages_workspace_size(ctypes.byref(dims), n)))
-        _check(lib.kda_pages_extend(ctypes.byref(dims), _ptr(table), _ptr(lengths), _ptr(refs), _ptr(seqs),
-                                    _ptr(new_lengths), n, _ptr(to), _ptr(lo), _ptr(ro), _ptr(ok), _ptr(ws), ws.numel(),
-                                    st.ptr), "kda_pages_extend")
+    lib = _lib or load()
+    n = seqs.numel()
+    dev, ref, nbytes, ins, outs = _pages_args(None, table, lengths, refs, table_out, lengths_out, refs_out, page_tokens, n)
+    req = _requests(dev, n, seqs=seqs, new_lengths=new_lengths)
+    st = _raw_stream(dev, stream)
+    if ok is None:
+        ok = _empty(table, (n,), _I32, stream)
+    ws = _scratch(table, dev, "pages", st, nbytes, stream)
+    _check(lib.kda_pages_extend(ref, *ins, *req, n, *outs, _need("ok", ok, _I32, (n,), dev), ws.data_ptr(), ws.numel(), st),
+           "kda_pages_extend")
     return ok
 
 
 def pages_free(table, lengths, refs, seqs, *, table_out=None, lengths_out=None, refs_out=None,
                stream: Optional[torch.cuda.Stream] = None):
     """Rows ``seqs`` give up their pages through ``kda_pages_free``."""
-    lib = load()
-    dev = _cuda(table, lengths, refs, seqs, table_out, lengths_out, refs_out)
-    dims = _pages_dims(None, table, lengths, refs, 1)
-    to, lo, ro = _pages_outs(table, lengths, refs, table_out, lengths_out, refs_out)
-    n = _requests(seqs=seqs)
-    with _OnStream(dev, stream) as st:
-        _check(lib.kda_pages_free(ctypes.byref(dims), _ptr(table), _ptr(lengths), _ptr(refs), _ptr(seqs), n, _ptr(to),
-                                  _ptr(lo), _ptr(ro), st.ptr), "kda_pages_free")
+    lib = _lib or load()
+    n = seqs.numel()
+    dev, ref, _, ins, outs = _pages_args(None, table, lengths, refs, table_out, lengths_out, refs_out, 1, n)
+    _check(lib.kda_pages_free(ref, *ins, *_requests(dev, n, seqs=seqs), n, *outs, _raw_stream(dev, stream)),
+           "kda_pages_free")
 
 
 def pages_compact(pool, table, refs, *, table_out=None, refs_out=None, page_map=None,
                   stream: Optional[torch.cuda.Stream] = None):
     """Moves the live pages of pool [layers, pages, ...] to the lowest indices through ``kda_pages_compact``; table
     and refs follow.  Returns page_map [pages] int32: the new index of each page, -1 for a free one."""
-    lib = load()
-    dev = _cuda(pool, table, refs, table_out, refs_out, page_map)
-    dims = _pages_dims(pool, table, None, refs, 1)
-    to, _, ro = _pages_outs(table, None, refs, table_out, None, refs_out)
-    with _OnStream(dev, stream) as st:
-        page_map = _out("page_map", page_map, (dims.num_pages,), torch.int32, dev)
-        ws = st.workspace(dev, "pages", int(lib.kda_pages_workspace_size(ctypes.byref(dims), 0)))
-        _check(lib.kda_pages_compact(ctypes.byref(dims), _ptr(pool), _ptr(table), _ptr(refs), _ptr(to), _ptr(ro),
-                                     _ptr(page_map), _ptr(ws), ws.numel(), st.ptr), "kda_pages_compact")
+    lib = _lib or load()
+    dev, ref, nbytes, ins, outs = _pages_args(pool, table, None, refs, table_out, None, refs_out, 1, 0)
+    st = _raw_stream(dev, stream)
+    if page_map is None:
+        page_map = _empty(refs, refs.shape, _I32, stream)
+    ws = _scratch(table, dev, "pages", st, nbytes, stream)
+    _check(lib.kda_pages_compact(ref, pool.data_ptr(), ins[0], ins[2], outs[0], outs[2],
+                                 _need("page_map", page_map, _I32, refs.shape, dev), ws.data_ptr(), ws.numel(), st),
+           "kda_pages_compact")
     return page_map

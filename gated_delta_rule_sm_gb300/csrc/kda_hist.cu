@@ -19,11 +19,12 @@ using namespace sm100;
 namespace {
 
 constexpr int kHistMaxW = 8;
-constexpr int kHistTile = 64;       // tokens per CTA
+constexpr int kHistTile = 32;       // tokens per CTA
+constexpr int kHistAhead = 8;       // tokens whose loads a thread has in flight
 constexpr int kHistThreads = 128;   // x 8 channels
 
 struct HistArgs {
-    int TT, T, C, W, dtype, rows, tiles, num_slots;
+    int TT, T, C, W, dtype, rows, tiles, num_slots, wide;   // wide: the weights allow 16-byte loads
     int64_t xs;            // elements between tokens of x
     const void* x;
     const float* w;        // [C, W]
@@ -36,6 +37,12 @@ struct HistArgs {
     int* status;
 };
 
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 template <typename T> struct Raw8;
 template <> struct Raw8<__nv_bfloat16> {
     uint4 u;
@@ -46,15 +53,14 @@ template <> struct Raw8<__nv_bfloat16> {
     __device__ __forceinline__ void store(void* p, size_t i) const {
         *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + i) = u;
     }
-    __device__ __forceinline__ void get(float* v) const {
+    __device__ __forceinline__ void get(float2* v) const {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            v[2 * k] = __uint_as_float(w[k] << 16);
-            v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-        }
+        for (int k = 0; k < 4; ++k) v[k] = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
     }
-    __device__ __forceinline__ void put(const float* v) { u = pack8_bf16(v); }
+    __device__ __forceinline__ void put(const float2* v) {
+        u = make_uint4(pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y), pack_bf16(v[2].x, v[2].y), pack_bf16(v[3].x, v[3].y));
+    }
 };
 template <> struct Raw8<float> {
     float4 a, b;
@@ -69,36 +75,53 @@ template <> struct Raw8<float> {
         f[0] = a;
         f[1] = b;
     }
-    __device__ __forceinline__ void get(float* v) const {
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    __device__ __forceinline__ void get(float2* v) const {
+        v[0] = make_float2(a.x, a.y);
+        v[1] = make_float2(a.z, a.w);
+        v[2] = make_float2(b.x, b.y);
+        v[3] = make_float2(b.z, b.w);
     }
-    __device__ __forceinline__ void put(const float* v) {
-        a = make_float4(v[0], v[1], v[2], v[3]);
-        b = make_float4(v[4], v[5], v[6], v[7]);
+    __device__ __forceinline__ void put(const float2* v) {
+        a = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+        b = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
     }
 };
 
+// A thread's eight channels' taps are 8 W consecutive floats; kept as pairs of channels.
 template <int W>
-__device__ __forceinline__ void load_weights(const HistArgs& a, int c0, float (*w)[W], float* bias) {
+__device__ __forceinline__ void load_weights(const HistArgs& a, int c0, float2 (*w)[W], float2* bias) {
     const float* src = a.w + (size_t)c0 * W;
+    float f[8 * W];
+    if (a.wide) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        bias[e] = a.b ? a.b[c0 + e] : 0.f;
+        for (int i = 0; i < 8 * W; i += 4) *reinterpret_cast<float4*>(f + i) = __ldg(reinterpret_cast<const float4*>(src + i));
+    } else {
 #pragma unroll
-        for (int i = 0; i < W; ++i) w[e][i] = src[e * W + i];
+        for (int i = 0; i < 8 * W; ++i) f[i] = src[i];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        bias[k] = a.b ? make_float2(a.b[c0 + 2 * k], a.b[c0 + 2 * k + 1]) : make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[k][i] = make_float2(f[2 * k * W + i], f[(2 * k + 1) * W + i]);
     }
 }
 
-// silu(bias + w . window), the newest input last
+// silu(bias + w . window), win[0] .. win[W - 1] the inputs, the newest last.
+// a / (1 + e^-a) takes one reciprocal for two values (the special function unit is half as busy); the
+// exponential stops at 2^60, where a times the sigmoid is below 1e-16.
 template <int W, typename R>
-__device__ __forceinline__ void conv_out(const float (*w)[W], const float* bias, const float (*win)[8], R& out) {
-    float y[8];
+__device__ __forceinline__ void conv_out(const float2 (*w)[W], const float2* bias, const float2 (*win)[4], R& out) {
+    float2 y[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        float acc = bias[e];
+    for (int k = 0; k < 4; ++k) {
+        y[k] = bias[k];
 #pragma unroll
-        for (int i = 0; i < W; ++i) acc = fmaf(w[e][i], win[i][e], acc);
-        y[e] = acc * __fdividef(1.f, 1.f + __expf(-acc));
+        for (int i = 0; i < W; ++i) y[k] = fma2(w[k][i], win[i][k], y[k]);
+        const float2 x = mul2(y[k], dup(-1.4426950408889634f));
+        const float2 d = fma2(make_float2(fminf(exp2_fast(x.x), 0x1p60f), fminf(exp2_fast(x.y), 0x1p60f)), dup(1.f), dup(1.f));
+        const float r = __fdividef(1.f, d.x * d.y);
+        y[k] = mul2(y[k], mul2(dup(r), make_float2(d.y, d.x)));
     }
     out.put(y);
 }
@@ -137,7 +160,8 @@ __global__ void __launch_bounds__(kHistThreads) conv_prompt_kernel(HistArgs a) {
         }
         return;
     }
-    float w[8][W], bias[8], win[W][8];
+    // win: the W - 1 inputs before a token, then a batch of tokens
+    float2 w[4][W], bias[4], win[W - 1 + kHistAhead][4];
     load_weights<W>(a, c0, w, bias);
     const int t0 = blockIdx.x * kHistTile, t1 = min(t0 + kHistTile, a.TT);
     int n, s0, s1;
@@ -164,7 +188,7 @@ __global__ void __launch_bounds__(kHistThreads) conv_prompt_kernel(HistArgs a) {
         }
     };
     fill(t0);
-    for (int t = t0; t < t1; ++t) {
+    for (int t = t0; t < t1;) {
         if (t == s1) {
             while (t >= s1) {   // empty rows in between
                 ++n;
@@ -173,47 +197,85 @@ __global__ void __launch_bounds__(kHistThreads) conv_prompt_kernel(HistArgs a) {
             }
             fill(t);
         }
-        raw.load(a.x, (size_t)t * a.xs + c0);
-        raw.get(win[W - 1]);
-        Raw8<E> out;
-        conv_out<W>(w, bias, win, out);
-        out.store(a.y, (size_t)t * a.C + c0);
+        // tokens up to the row's or the tile's end, each one's load kHistAhead tokens before its use
+        const int end = min(t1, s1);
+        Raw8<E> in[kHistAhead];
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i)
+        for (int i = 0; i < kHistAhead; ++i)
+            if (t + i < end) in[i].load(a.x, (size_t)(t + i) * a.xs + c0);
+        auto put = [&](int i) {
+            Raw8<E> out;
+            conv_out<W>(w, bias, win + i, out);
+            out.store(a.y, (size_t)(t + i) * a.C + c0);
+        };
+        for (; t + kHistAhead <= end; t += kHistAhead) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) win[i][e] = win[i + 1][e];
+            for (int i = 0; i < kHistAhead; ++i) {
+                in[i].get(win[W - 1 + i]);
+                if (t + i + kHistAhead < end) in[i].load(a.x, (size_t)(t + i + kHistAhead) * a.xs + c0);
+                put(i);
+            }
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) win[i][k] = win[kHistAhead + i][k];
+        }
+#pragma unroll
+        for (int i = 0; i < kHistAhead; ++i) {
+            if (t + i >= end) break;
+            in[i].get(win[W - 1 + i]);
+            put(i);
+        }
+        t = end;
     }
 }
 
-// Rows blockIdx.x, blockIdx.x + gridDim.x, ... of the batch with one set of weights.
+// kHistRows rows of the batch with one set of weights (16 bytes of weights per channel beside 16 bytes of
+// inputs, outputs and histories per channel and row), all rows' loads in flight at once.
+constexpr int kHistRows = 2;
 template <int W, typename E>
 __global__ void __launch_bounds__(kHistThreads) conv_step_kernel(HistArgs a) {
     const int c0 = (blockIdx.y * kHistThreads + threadIdx.x) * 8;
     if (c0 >= a.C) return;
-    float w[8][W], bias[8], win[W][8];
-    load_weights<W>(a, c0, w, bias);
-    for (int r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        int slot = a.slots ? a.slots[r] : r;
-        if (slot >= a.num_slots) {
+    Raw8<E> raw[kHistRows][W];
+    int slot[kHistRows];
+#pragma unroll
+    for (int k = 0; k < kHistRows; ++k) {
+        const int r = blockIdx.x * kHistRows + k;
+        slot[k] = r >= a.rows ? -1 : a.slots ? a.slots[r] : r;
+        if (slot[k] >= a.num_slots) {
             if (c0 == 0) record_error(a.status, KDA_ERR_INVALID_ARG);
-            slot = -1;
+            slot[k] = -1;
         }
-        Raw8<E> raw[W], out;
-        if (slot < 0) {
+    }
+#pragma unroll
+    for (int k = 0; k < kHistRows; ++k) {
+        const int r = blockIdx.x * kHistRows + k;
+        if (slot[k] < 0) continue;
+        const size_t hb = (size_t)slot[k] * (W - 1) * a.C + c0;
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) raw[k][i].load(a.h_in, hb + (size_t)i * a.C);
+        raw[k][W - 1].load(a.x, (size_t)r * a.xs + c0);
+    }
+    float2 w[4][W], bias[4], win[W][4];
+    load_weights<W>(a, c0, w, bias);
+#pragma unroll
+    for (int k = 0; k < kHistRows; ++k) {
+        const int r = blockIdx.x * kHistRows + k;
+        if (r >= a.rows) break;
+        Raw8<E> out;
+        if (slot[k] < 0) {
             out.zero();
             out.store(a.y, (size_t)r * a.C + c0);
             continue;
         }
-        const size_t hb = (size_t)slot * (W - 1) * a.C + c0;
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i) raw[i].load(a.h_in, hb + (size_t)i * a.C);
-        raw[W - 1].load(a.x, (size_t)r * a.xs + c0);
-#pragma unroll
-        for (int i = 0; i < W; ++i) raw[i].get(win[i]);
+        for (int i = 0; i < W; ++i) raw[k][i].get(win[i]);
         conv_out<W>(w, bias, win, out);
         out.store(a.y, (size_t)r * a.C + c0);
+        const size_t hb = (size_t)slot[k] * (W - 1) * a.C + c0;
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i) raw[i + 1].store(a.h_out, hb + (size_t)i * a.C);
+        for (int i = 0; i < W - 1; ++i) raw[k][i + 1].store(a.h_out, hb + (size_t)i * a.C);
     }
 }
 
@@ -268,6 +330,7 @@ kda_status kda_short_conv_prompt(int B, int T, int C, int W, kda_dtype dtype, co
     st = check_offsets_host(a.rows, a.TT, cu_seqlens, cu_seqlens_host);
     if (st != KDA_OK) return st;
     a.xs = x_stride ? x_stride : C;
+    a.wide = reinterpret_cast<uintptr_t>(weight) % 16 == 0;
     a.x = x; a.w = weight; a.b = bias; a.cu = cu_seqlens; a.h_in = initial_history; a.h_out = final_history; a.y = y;
     st = status_ptr(&a.status);
     if (st != KDA_OK) return st;
@@ -289,13 +352,13 @@ kda_status kda_short_conv_step(int B, int C, int W, kda_dtype dtype, const void*
     HistArgs a;
     memset(&a, 0, sizeof(a));
     a.C = C; a.W = W; a.dtype = dtype; a.rows = B; a.num_slots = num_slots; a.xs = x_stride ? x_stride : C;
+    a.wide = reinterpret_cast<uintptr_t>(weight) % 16 == 0;
     a.x = x; a.w = weight; a.b = bias; a.slots = slots; a.h_in = history_in; a.h_out = history_out; a.y = y;
     st = status_ptr(&a.status);
     if (st != KDA_OK) return st;
-    const int gy = (C / 8 + kHistThreads - 1) / kHistThreads;
-    const int gx = (8 * 152 + gy - 1) / gy;
+    const dim3 grid((B + kHistRows - 1) / kHistRows, (C / 8 + kHistThreads - 1) / kHistThreads);
     timing_pre(stream, K_CONV_STEP);
-    KDA_HIST_DISPATCH(conv_step_kernel, a, dim3(B < gx ? B : gx, gy), stream);
+    KDA_HIST_DISPATCH(conv_step_kernel, a, grid, stream);
     timing_post(stream);
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -165,22 +165,43 @@ __global__ void __launch_bounds__(1024) ssm_plan_kernel(SsmArgs a, SsmSeg* seg, 
 }
 
 // Entering states of a row's segments: S <- decay_k S + loc_k, in place of loc_k.  Elementwise over the
-// state: one thread per element, the next segment's value in flight while this one is used.
-__global__ void __launch_bounds__(256) ssm_join_kernel(SsmArgs a) {
+// state, bound by memory: a thread walks VEC elements along the row's segments, kJoinAhead of them in flight.
+constexpr int kJoinAhead = 8;
+template <int VEC>
+__global__ void __launch_bounds__(128) ssm_join_kernel(SsmArgs a) {
     const int np = a.N * a.P;
-    const int e = blockIdx.y * 256 + threadIdx.x;
+    const int e = (blockIdx.y * 128 + threadIdx.x) * VEC;
     const int n = blockIdx.x / a.H, h = blockIdx.x - n * a.H;
     if (e >= np) return;
     int first;
     const int segs = ssm_row_segments(a, n, &first);
-    float S = a.S0 ? a.S0[((size_t)n * a.H + h) * np + e] : 0.f;
-    for (int k = 0; k < segs; ++k) {
-        float* p = a.states + ((size_t)(first + k) * a.H + h) * np + e;
-        // the last segment's end state comes from the output pass
-        const float loc = k + 1 < segs ? *p : 0.f;
-        const float d = k + 1 < segs ? a.decay[(size_t)(first + k) * a.H + h] : 0.f;
-        *p = S;
-        S = fmaf(d, S, loc);
+    float S[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) S[v] = a.S0 ? a.S0[((size_t)n * a.H + h) * np + e + v] : 0.f;
+    const size_t step = (size_t)a.H * np;
+    float* p = a.states + ((size_t)first * a.H + h) * np + e;
+    // the last segment's end state comes from the output pass
+    for (int k0 = 0; k0 < segs; k0 += kJoinAhead, p += kJoinAhead * step) {
+        float loc[kJoinAhead][VEC], d[kJoinAhead];
+#pragma unroll
+        for (int k = 0; k < kJoinAhead; ++k) {
+            const bool in = k0 + k + 1 < segs;
+            d[k] = in ? a.decay[(size_t)(first + k0 + k) * a.H + h] : 0.f;
+            if constexpr (VEC == 4) {
+                const float4 f = in ? *reinterpret_cast<const float4*>(p + k * step) : make_float4(0.f, 0.f, 0.f, 0.f);
+                loc[k][0] = f.x; loc[k][1] = f.y; loc[k][2] = f.z; loc[k][3] = f.w;
+            } else {
+                loc[k][0] = in ? p[k * step] : 0.f;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kJoinAhead; ++k) {
+            if (k0 + k >= segs) break;
+            if constexpr (VEC == 4) *reinterpret_cast<float4*>(p + k * step) = make_float4(S[0], S[1], S[2], S[3]);
+            else p[k * step] = S[0];
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) S[v] = fmaf(d[k], S[v], loc[k][v]);
+        }
     }
 }
 
@@ -389,7 +410,9 @@ kda_status kda_ssm_fwd(const kda_ssm_dims* dims, const void* x, const void* dt_r
         a.states = reinterpret_cast<float*>(ws + w.off_states);
         if ((tc ? launch_ssm_tc(a, false, stream) : launch_ssm_simt(a, false, stream)) != cudaSuccess) return KDA_ERR_CUDA;
         timing_pre(stream, K_SSM_JOIN);
-        ssm_join_kernel<<<dim3(s.rows * s.H, (s.N * s.P + 255) / 256), 256, 0, stream>>>(a);
+        const int np = s.N * s.P;
+        if (np % 4 == 0) ssm_join_kernel<4><<<dim3(s.rows * s.H, (np + 511) / 512), 128, 0, stream>>>(a);
+        else ssm_join_kernel<1><<<dim3(s.rows * s.H, (np + 127) / 128), 128, 0, stream>>>(a);
         timing_post(stream);
         if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
     }

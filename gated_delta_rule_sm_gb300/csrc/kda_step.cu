@@ -67,24 +67,15 @@ __device__ __forceinline__ void store_cols(float* p, const Cols<VEC>& r) {
     else *p = r.v[0];
 }
 
-// Sum of one value per thread over the CTA; every thread gets it.  red: 8 floats.
-__device__ __forceinline__ float block_sum(float x, float* red) {
-    x = warp_sum(x);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-    __syncthreads();
-    float t = 0.f;
-#pragma unroll
-    for (int w = 0; w < kStepThreads / 32; ++w) t += red[w];
-    return t;
-}
-
 // K <= 128: a thread holds rows ty, ty + RY, ... of its VEC columns, 32 floats.
 template <int VEC>
 __global__ void __launch_bounds__(kStepThreads) decode_step_kernel(StepArgs a) {
     constexpr int CX = kStepTile / VEC, RY = kStepThreads / CX, PER = 128 / RY;
+    constexpr int WROWS = kStepThreads / 32;          // partial sums left per column after a warp's own
     __shared__ float sk[128], sq[128], sal[128];
-    __shared__ float sr[RY][kStepTile + 4], sw[RY][kStepTile + 4];
-    __shared__ float red[3][8];
+    __shared__ float sr[WROWS][kStepTile], sw[WROWS][kStepTile];
+    __shared__ __align__(16) float su[kStepTile];
+    __shared__ float red[3][4];
     const int tid = threadIdx.x, cx = tid % CX, ry = tid / CX;
     const int bh = blockIdx.x, b = bh / a.H, h = bh - b * a.H;
     const int col = blockIdx.y * kStepTile + cx * VEC;
@@ -117,13 +108,21 @@ __global__ void __launch_bounds__(kStepThreads) decode_step_kernel(StepArgs a) {
         const float g = a.gate == KDA_GATE_SOFTPLUS ? -ea * softplusf(z) : a.lb * sigmoidf_acc(ea * z);
         sal[tid] = expf(g);
     }
-    const float qq = block_sum(qv * qv, red[0]), kk = block_sum(kv * kv, red[1]), qk = block_sum(qv * kv, red[2]);
-    const float rq = 1.0f / sqrtf(qq + kNormEps), rk = 1.0f / sqrtf(kk + kNormEps);
-    if (tid < a.K) {
-        sq[tid] = qv * rq;
-        sk[tid] = kv * rk;
+    if (tid < 128) {
+        sq[tid] = qv;
+        sk[tid] = kv;
+        const float qq = warp_sum(qv * qv), kk = warp_sum(kv * kv), qk = warp_sum(qv * kv);
+        if ((tid & 31) == 0) {
+            red[0][tid >> 5] = qq;
+            red[1][tid >> 5] = kk;
+            red[2][tid >> 5] = qk;
+        }
     }
     __syncthreads();
+    float sum[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) sum[i] = (red[i][0] + red[i][1]) + (red[i][2] + red[i][3]);
+    const float rq = 1.0f / sqrtf(sum[0] + kNormEps), rk = 1.0f / sqrtf(sum[1] + kNormEps);
     float r_[VEC], w_[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) r_[e] = w_[e] = 0.f;
@@ -139,26 +138,41 @@ __global__ void __launch_bounds__(kStepThreads) decode_step_kernel(StepArgs a) {
             w_[e] = fmaf(S[i].v[e], qr, w_[e]);
         }
     }
+    // S'^T k and S'^T q (k, q not yet divided by their norms): first the warp's rows, then the warps
+    if (CX == 16) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        sr[ry][cx * VEC + e] = r_[e];
-        sw[ry][cx * VEC + e] = w_[e];
+        for (int e = 0; e < VEC; ++e) {
+            r_[e] += __shfl_xor_sync(0xffffffffu, r_[e], 16);
+            w_[e] += __shfl_xor_sync(0xffffffffu, w_[e], 16);
+        }
+    }
+    constexpr int PARTS = CX == 16 ? WROWS : RY;
+    const int part = CX == 16 ? tid >> 5 : ry;
+    if (CX != 16 || (tid & 16) == 0)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            sr[part][cx * VEC + e] = r_[e];
+            sw[part][cx * VEC + e] = w_[e];
+        }
+    __syncthreads();
+    const int c = blockIdx.y * kStepTile + tid;
+    if (tid < kStepTile && c < a.V) {
+        float r = 0.f, w = 0.f;
+#pragma unroll
+        for (int j = 0; j < PARTS; ++j) {
+            r += sr[j][tid];
+            w += sw[j][tid];
+        }
+        const float beta = sigmoidf_acc(load_act(a.beta_raw, bh, a.dtype));
+        const float u = beta * (load_act(a.v, (size_t)bh * a.V + c, a.dtype) - r * rk);
+        su[tid] = u * rk;
+        store_act(a.out, (size_t)bh * a.V + c, a.scale * rq * fmaf(sum[2] * rk, u, w), a.dtype);
     }
     __syncthreads();
     if (!in) return;
-    const float beta = sigmoidf_acc(load_act(a.beta_raw, bh, a.dtype));
     float u[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        float r = 0.f, w = 0.f;
-#pragma unroll
-        for (int j = 0; j < RY; ++j) {
-            r += sr[j][cx * VEC + e];
-            w += sw[j][cx * VEC + e];
-        }
-        u[e] = beta * (load_act(a.v, (size_t)bh * a.V + col + e, a.dtype) - r);
-        if (ry == 0) store_act(a.out, (size_t)bh * a.V + col + e, a.scale * fmaf(qk * rq * rk, u[e], w), a.dtype);
-    }
+    for (int e = 0; e < VEC; ++e) u[e] = su[cx * VEC + e];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int r = ry + i * RY;
@@ -187,27 +201,34 @@ __global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(StepArgs a) {
     }
     const size_t base = ((size_t)slot * a.H + h) * a.K * a.V + col;
     const size_t gb = (size_t)(h / (a.H / a.G)) * a.K;
-    const float dt = softplusf(load_act(a.beta_raw, (size_t)b * a.ds + h, a.dtype) + a.dt_bias[h]);
-    const float al = expf(-expf(a.a_log[h]) * dt);
-    float x[VEC], u[VEC], y[VEC];
+    Cols<VEC> S[BATCH];
+    float bv[BATCH], cv[BATCH];
+    auto load = [&](int r0) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        x[e] = in ? load_act(a.v, (size_t)b * a.xs + (size_t)h * a.V + col + e, a.dtype) : 0.f;
-        u[e] = dt * x[e];
-        y[e] = 0.f;
-    }
-    for (int r0 = ry; r0 < a.K; r0 += BATCH * RY) {
-        Cols<VEC> S[BATCH];
-        float bv[BATCH], cv[BATCH];
+        for (int i = 0; i < BATCH; ++i) {
+            const int r = r0 + i * RY;
+            if (r < a.K && in) S[i] = load_cols<VEC>(a.s_in + base + (size_t)r * a.V);
+        }
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
             const int r = r0 + i * RY;
             if (r < a.K) {
-                if (in) S[i] = load_cols<VEC>(a.s_in + base + (size_t)r * a.V);
                 bv[i] = load_act(a.k, (size_t)b * a.bs + gb + r, a.dtype);
                 cv[i] = load_act(a.q, (size_t)b * a.cs + gb + r, a.dtype);
             }
         }
+    };
+    load(ry);     // on its way while the row's scalars are formed
+    const float dt = softplusf(load_act(a.beta_raw, (size_t)b * a.ds + h, a.dtype) + a.dt_bias[h]);
+    const float al = expf(-expf(a.a_log[h]) * dt);
+    float u[VEC], y[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        u[e] = in ? dt * load_act(a.v, (size_t)b * a.xs + (size_t)h * a.V + col + e, a.dtype) : 0.f;
+        y[e] = 0.f;
+    }
+    for (int r0 = ry; r0 < a.K; r0 += BATCH * RY) {
+        if (r0 != ry) load(r0);
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
             const int r = r0 + i * RY;

@@ -179,11 +179,12 @@ def test_binding_refuses_host_tensors():
 
 
 def test_token_strides():
+    stride = lambda t, lead: _lib._token_stride("x", t.shape, t.stride(), lead)  # noqa: E731
     wide = torch.zeros(3, 5, 40)
-    assert _lib._token_stride("x", wide[..., 8:32].unflatten(-1, (3, 8)), 2) == 40
-    assert _lib._token_stride("x", wide[:, 0, :16], 1) == 200
-    assert _lib._token_stride("x", torch.zeros(1, 1, 4, 8)[:, :, :, ::1], 2) == 32
+    assert stride(wide[..., 8:32].unflatten(-1, (3, 8)), 2) == 40
+    assert stride(wide[:, 0, :16], 1) == 200
+    assert stride(torch.zeros(1, 1, 4, 8), 2) == 32
     with pytest.raises(ValueError):
-        _lib._token_stride("x", wide[..., ::2], 2)                       # values not contiguous
+        stride(wide[..., ::2], 2)                       # values not contiguous
     with pytest.raises(ValueError):
-        _lib._token_stride("x", wide[:, :4], 2)                          # rows not evenly spaced
+        stride(wide[:, :4], 2)                          # rows not evenly spaced
