@@ -20,7 +20,9 @@ namespace {
 
 constexpr int kHistMaxW = 8;
 constexpr int kHistTile = 32;       // tokens per CTA
-constexpr int kHistAhead = 8;       // tokens whose loads a thread has in flight
+// tokens whose loads a thread has in flight: a multiple of W, so that the window's place in its registers is
+// the same in every batch
+constexpr int hist_ahead(int W) { return 8 / W * W; }
 constexpr int kHistThreads = 128;   // x 8 channels
 
 struct HistArgs {
@@ -107,17 +109,17 @@ __device__ __forceinline__ void load_weights(const HistArgs& a, int c0, float2 (
     }
 }
 
-// silu(bias + w . window), win[0] .. win[W - 1] the inputs, the newest last.
+// silu(bias + w . window); the window is a ring of W inputs, the oldest at place `first`.
 // a / (1 + e^-a) takes one reciprocal for two values (the special function unit is half as busy); the
 // exponential stops at 2^60, where a times the sigmoid is below 1e-16.
 template <int W, typename R>
-__device__ __forceinline__ void conv_out(const float2 (*w)[W], const float2* bias, const float2 (*win)[4], R& out) {
+__device__ __forceinline__ void conv_out(const float2 (*w)[W], const float2* bias, const float2 (*win)[4], int first, R& out) {
     float2 y[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         y[k] = bias[k];
 #pragma unroll
-        for (int i = 0; i < W; ++i) y[k] = fma2(w[k][i], win[i][k], y[k]);
+        for (int i = 0; i < W; ++i) y[k] = fma2(w[k][i], win[(first + i) % W][k], y[k]);
         const float2 x = mul2(y[k], dup(-1.4426950408889634f));
         const float2 d = fma2(make_float2(fminf(exp2_fast(x.x), 0x1p60f), fminf(exp2_fast(x.y), 0x1p60f)), dup(1.f), dup(1.f));
         const float r = __fdividef(1.f, d.x * d.y);
@@ -139,7 +141,7 @@ __device__ __forceinline__ int row_begin(const HistArgs& a, int n) { return a.cu
 
 // CTAs below `tiles` take 64 tokens each; the others write the final history of one row each.
 template <int W, typename E>
-__global__ void __launch_bounds__(kHistThreads) conv_prompt_kernel(HistArgs a) {
+__global__ void __launch_bounds__(kHistThreads, sizeof(E) == 2 && W <= 4 ? 4 : 2) conv_prompt_kernel(HistArgs a) {
     if (a.cu && !offsets_ok(a)) {
         if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) record_error(a.status, KDA_ERR_INVALID_ARG);
         return;
@@ -160,8 +162,8 @@ __global__ void __launch_bounds__(kHistThreads) conv_prompt_kernel(HistArgs a) {
         }
         return;
     }
-    // win: the W - 1 inputs before a token, then a batch of tokens
-    float2 w[4][W], bias[4], win[W - 1 + kHistAhead][4];
+    constexpr int AHEAD = hist_ahead(W);
+    float2 w[4][W], bias[4], win[W][4];
     load_weights<W>(a, c0, w, bias);
     const int t0 = blockIdx.x * kHistTile, t1 = min(t0 + kHistTile, a.TT);
     int n, s0, s1;
@@ -197,33 +199,26 @@ __global__ void __launch_bounds__(kHistThreads) conv_prompt_kernel(HistArgs a) {
             }
             fill(t);
         }
-        // tokens up to the row's or the tile's end, each one's load kHistAhead tokens before its use
+        // tokens up to the row's or the tile's end, each one's load AHEAD tokens before its use
         const int end = min(t1, s1);
-        Raw8<E> in[kHistAhead];
+        Raw8<E> in[AHEAD];
 #pragma unroll
-        for (int i = 0; i < kHistAhead; ++i)
+        for (int i = 0; i < AHEAD; ++i)
             if (t + i < end) in[i].load(a.x, (size_t)(t + i) * a.xs + c0);
+        // fill() leaves the inputs before t at places 0 .. W - 2: token t + i goes to place (W - 1 + i) % W
         auto put = [&](int i) {
+            in[i].get(win[(W - 1 + i) % W]);
+            if (t + i + AHEAD < end) in[i].load(a.x, (size_t)(t + i + AHEAD) * a.xs + c0);
             Raw8<E> out;
-            conv_out<W>(w, bias, win + i, out);
+            conv_out<W>(w, bias, win, i % W, out);
             out.store(a.y, (size_t)(t + i) * a.C + c0);
         };
-        for (; t + kHistAhead <= end; t += kHistAhead) {
+        for (; t + AHEAD <= end; t += AHEAD)
 #pragma unroll
-            for (int i = 0; i < kHistAhead; ++i) {
-                in[i].get(win[W - 1 + i]);
-                if (t + i + kHistAhead < end) in[i].load(a.x, (size_t)(t + i + kHistAhead) * a.xs + c0);
-                put(i);
-            }
+            for (int i = 0; i < AHEAD; ++i) put(i);
 #pragma unroll
-            for (int i = 0; i < W - 1; ++i)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) win[i][k] = win[kHistAhead + i][k];
-        }
-#pragma unroll
-        for (int i = 0; i < kHistAhead; ++i) {
+        for (int i = 0; i < AHEAD; ++i) {
             if (t + i >= end) break;
-            in[i].get(win[W - 1 + i]);
             put(i);
         }
         t = end;
@@ -271,7 +266,7 @@ __global__ void __launch_bounds__(kHistThreads) conv_step_kernel(HistArgs a) {
         }
 #pragma unroll
         for (int i = 0; i < W; ++i) raw[k][i].get(win[i]);
-        conv_out<W>(w, bias, win, out);
+        conv_out<W>(w, bias, win, 0, out);
         out.store(a.y, (size_t)r * a.C + c0);
         const size_t hb = (size_t)slot[k] * (W - 1) * a.C + c0;
 #pragma unroll

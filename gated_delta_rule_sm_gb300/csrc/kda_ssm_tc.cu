@@ -87,10 +87,10 @@ enum Bars {
     kM = 33,          // [2] half the columns of M written, and C S scaled (8 warps)
     kMX = 35,         // M X complete
     kYRead = 36,      // Y read (8 warps)
-    kD3 = 37,         // U^T B complete
-    kD3Free = 38,     // read (4 warps)
-    kTail = 39,       // X and B past the end cleared (8 warps)
-    kBars = 40
+    kD3 = 37,         // [2] U^T B complete
+    kD3Free = 39,     // [2] read (4 warps)
+    kTail = 41,       // X and B past the end cleared (8 warps)
+    kBars = 42
 };
 
 // TMEM columns
@@ -244,6 +244,8 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
     constexpr int NST = L::STAGES;
     constexpr int NU = OUT ? 2 : 4;                  // U buffers (without G, M and Y their columns are free)
     constexpr uint32_t U0 = OUT ? TU : 0;
+    constexpr int ND = OUT ? 1 : 2;                  // accumulators of U^T B
+    constexpr uint32_t D0 = OUT ? TD : 192;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int seg = blockIdx.x;
     const SsmSeg sg = ssm_segment(a, seg);
@@ -266,7 +268,7 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
         for (int i = 0; i < kBars; ++i) {
             int cnt = 1;
             if (i == kYOut || i == kYOut + 1 || i == kM || i == kM + 1 || i == kYRead || i == kTail) cnt = 8;
-            if (i == kXRead || i == kXRead + 1 || (i >= kUFull && i < kUFull + 4) || i == kSB || i == kD3Free) cnt = 4;
+            if (i == kXRead || i == kXRead + 1 || (i >= kUFull && i < kUFull + 4) || i == kSB || i == kD3Free || i == kD3Free + 1) cnt = 4;
             if (i == kBEmpty) cnt = 2;
             if (i >= kPrepEmpty && i < kPrepEmpty + 4) cnt = 16;
             mbar_init(&bar[i], cnt);
@@ -400,33 +402,24 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
             const uint32_t pr = smem_u32(slot_prep(c, 0));
             const uint32_t xrow = smem_u32(smem + L::X + (2 * st + wg) * HALF) + sw(row, 0);
             if (!wait_prep(c) || !clear_tail(c, st)) break;
-            // C S of this warpgroup's columns, scaled by exp(l_t)
-            float ls = lds1f(pr + wg * PS + 4 * (256 + row));
-#pragma unroll 1
-            for (int k = 0; k < lq; ++k) ls += lds1f(pr + wg * PS + 4 * (512 + k));
-            const float2 el = dup(ex2(ls));
-            if (!wait(kY2, par)) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int j = 0; j < 64; j += 32) {
-                float v[32];
-                uint32_t r[32];
-                tmem_ld16(ty + j, v);
-                tmem_ld16(ty + j + 16, v + 16);
-                tmem_ld_wait();
+            // the row's exponents while G is formed: from its block's start (lt), for C S's scale (ly), and from the
+            // end of each column block of this warpgroup that lies before the diagonal (lj)
+            float lt[2], lj[2][2], ly;
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    const float2 y = mul2(make_float2(v[i], v[i + 1]), el);
-                    r[i] = __float_as_uint(y.x);
-                    r[i + 1] = __float_as_uint(y.y);
-                }
-                tmem_st16(ty + j, r);
-                tmem_st16(ty + j + 16, r + 16);
+            for (int s = 0; s < 2; ++s) {
+                const float4 sum = lds4f(pr + s * PS + 4 * 512);
+                lt[s] = lds1f(pr + s * PS + 4 * (256 + row));
+                // blocks 0 and 3 (wg 0) or 1 and 2: what lies between the block's end and the row's block
+                const float s1 = lq > 1 ? sum.y : 0.f, s2 = lq > 2 ? sum.z : 0.f;
+                lj[0][s] = lt[s] + (wg ? s2 : s1 + s2);
+                lj[1][s] = lt[s];
+                if (s == wg) ly = lt[s] + ((lq > 0 ? sum.x : 0.f) + s1) + s2;
             }
             if (!wait(kG, par)) break;
             tc_fence_after();
             // (not unrolled: fetching code that all roles' loops cannot keep in the instruction cache
             // costs more than the loop)
+            bool ok = true;
 #pragma unroll 1
             for (int b = 0; b < 2; ++b) {
                 const int J = 2 * b + (wg ^ b);
@@ -445,7 +438,6 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
 #pragma unroll 1
                 for (int s = 0; s < (SAME ? 1 : 2); ++s) {
                     const uint32_t ps = pr + s * PS;
-                    float l = lds1f(ps + 4 * (256 + row));
                     if (J == lq) {           // the diagonal block: an exponential each, columns up to the row
 #pragma unroll
                         for (int c0 = 0; c0 < 32; c0 += 16) {
@@ -456,8 +448,8 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
 #pragma unroll
                             for (int i = 0; i < 16; i += 4) {
                                 const float4 k = l4[i >> 2];
-                                const float2 x0 = fma2(make_float2(k.x, k.y), dup(-1.f), dup(l));
-                                const float2 x1 = fma2(make_float2(k.z, k.w), dup(-1.f), dup(l));
+                                const float2 x0 = fma2(make_float2(k.x, k.y), dup(-1.f), dup(s ? lt[1] : lt[0]));
+                                const float2 x1 = fma2(make_float2(k.z, k.w), dup(-1.f), dup(s ? lt[1] : lt[0]));
                                 const int j = c0 + i;
                                 const float2 e0 = mul2(make_float2(v[j], v[j + 1]), make_float2(ex2(x0.x), ex2(x0.y)));
                                 const float2 e1 = mul2(make_float2(v[j + 2], v[j + 3]), make_float2(ex2(x1.x), ex2(x1.y)));
@@ -467,9 +459,7 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                             tmem_st8(tg + c0 + 8 * s, m);
                         }
                     } else {                 // a factor of the column to the block's end, one of the row from there
-#pragma unroll 1
-                        for (int k = J + 1; k < lq; ++k) l += lds1f(ps + 4 * (512 + k));
-                        const float2 rf = dup(ex2(l));
+                        const float2 rf = dup(ex2(b ? (s ? lj[1][1] : lj[1][0]) : (s ? lj[0][1] : lj[0][0])));
 #pragma unroll
                         for (int c0 = 0; c0 < 32; c0 += 16) {
                             float4 f4[4];
@@ -490,10 +480,33 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                     }
                 }
                 }
+                if (b == 0) {     // C S of this warpgroup's columns, scaled by exp(l_t)
+                    const float2 el = dup(ex2(ly));
+                    ok = wait(kY2, par);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int j = 0; j < 64; j += 32) {
+                        float v[32];
+                        uint32_t r[32];
+                        tmem_ld16(ty + j, v);
+                        tmem_ld16(ty + j + 16, v + 16);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const float2 y = mul2(make_float2(v[i], v[i + 1]), el);
+                            r[i] = __float_as_uint(y.x);
+                            r[i + 1] = __float_as_uint(y.y);
+                        }
+                        tmem_st16(ty + j, r);
+                        tmem_st16(ty + j + 16, r + 16);
+                    }
+                }
                 tmem_st_wait();
                 tc_fence_before();
                 arrive_warp(kM + b);
             }
+            if (!ok) break;
             arrive_warp(kPrepEmpty + (c & 3));
             if (!wait(kXRead + st, (c >> 1) & 1) || !wait(kMX, par)) break;
             tc_fence_after();
@@ -585,11 +598,11 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
         }
         for (int c = 0; c < nch; ++c) {
             const uint32_t par = c & 1;
-            if (!wait_prep(c) || !wait(kD3, par)) break;
+            if (!wait_prep(c) || !wait(kD3 + c % ND, (c / ND) & 1)) break;
             tc_fence_after();
             {
                 const float2 eq = dup(lds1f(smem_u32(slot_prep(c, srow)) + 4 * 516));
-                const uint32_t td = tmem + TD + ((uint32_t)(lq * 32) << 16);
+                const uint32_t td = tmem + D0 + 128 * (c % ND) + ((uint32_t)(lq * 32) << 16);
 #pragma unroll
                 for (int j = 0; j < NC; j += 16) {
                     float v[16];
@@ -604,7 +617,7 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                 }
             }
             tc_fence_before();
-            arrive_warp(kD3Free);
+            arrive_warp(kD3Free + c % ND);
             arrive_warp(kPrepEmpty + (c & 3));
             if (OUT && c + 1 < nch) {
                 if (!wait(kY2, par)) break;      // C S has read the copies
@@ -805,17 +818,17 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                 for (int q = 0; q < 4 && ok; ++q) {
                     const int k = 4 * c + q, b = k % NU;
                     if (!wait1(kUFull + b, (k / NU) & 1)) { ok = false; break; }
-                    if (q == 0 && c > 0 && !wait1(kD3Free, (c - 1) & 1)) { ok = false; break; }
+                    if (q == 0 && c >= ND && !wait1(kD3Free + c % ND, (c / ND - 1) & 1)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t db = desc_lo(sbt + q * 4096, HALF);
                     steps<6>([&](auto i) {
                         constexpr int j = i >= 3, term = i - 3 * j;
-                        mma_ts<j * 2048>(tmem + TD, tmem + U0 + 48 * b + 16 * term + 8 * j, db, idU, q + i > 0);
+                        mma_ts<j * 2048>(tmem + D0 + 128 * (c % ND), tmem + U0 + 48 * b + 16 * term + 8 * j, db, idU, q + i > 0);
                     });
                     mma_commit(&bar[kUEmpty + b]);
                 }
                 if (!ok) break;
-                mma_commit(&bar[kD3]);
+                mma_commit(&bar[kD3 + c % ND]);
                 mma_commit(&bar[OUT ? kBEmpty : kStage + st]);
             }
         }

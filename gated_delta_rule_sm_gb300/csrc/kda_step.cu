@@ -69,7 +69,7 @@ __device__ __forceinline__ void store_cols(float* p, const Cols<VEC>& r) {
 
 // K <= 128: a thread holds rows ty, ty + RY, ... of its VEC columns, 32 floats.
 template <int VEC>
-__global__ void __launch_bounds__(kStepThreads) decode_step_kernel(StepArgs a) {
+__global__ void __launch_bounds__(kStepThreads, VEC == 4 ? 4 : 3) decode_step_kernel(StepArgs a) {
     constexpr int CX = kStepTile / VEC, RY = kStepThreads / CX, PER = 128 / RY;
     constexpr int WROWS = kStepThreads / 32;          // partial sums left per column after a warp's own
     __shared__ float sk[128], sq[128], sal[128];
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kStepThreads) decode_step_kernel(StepArgs a) {
 }
 
 template <int VEC>
-__global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(StepArgs a) {
+__global__ void __launch_bounds__(kStepThreads, 3) ssm_step_kernel(StepArgs a) {
     constexpr int CX = kStepTile / VEC, RY = kStepThreads / CX, BATCH = VEC == 4 ? 8 : 16;
     __shared__ float sy[RY][kStepTile + 4];
     const int tid = threadIdx.x, cx = tid % CX, ry = tid / CX;
