@@ -21,9 +21,9 @@
 // exponent is the difference of two large numbers; a token's exponent is cut at -150 (2^-150 is 0 in
 // fp32).
 //
-// Roles (20 warps): 0-7 form M, scale C S and finish Y (two warpgroups: columns of G are split between
-// them, Y by head); 8-11 form U, a quarter of a chunk at a time; 12-15 keep the state, a row each; 16
-// issues G, C S and M X, 17 the copies, 18 prepares the decays, 19 issues U^T B.  Roles meet at mbarriers
+// Roles (24 warps): 0-7 form M, scale C S and finish Y (two warpgroups: columns of G are split between
+// them, Y by head); 8-11 form U, a quarter of a chunk at a time; 12-19 keep the state, half a row a thread;
+// 20 issues G, C S and M X, 21 the copies, 22 prepares the decays, 23 issues U^T B.  Roles meet at mbarriers
 // only, so the state's chain (U^T B, S, C S) runs beside the output's (G, M, M X, Y).
 // The pass that only forms states has no G, M, C S or Y: its first three warpgroups all form U, in four
 // TMEM buffers, with three stages of X and B.
@@ -47,7 +47,7 @@ namespace {
 
 constexpr int Q = 128;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kThreads = 640;
+constexpr int kThreads = 768;
 
 // A slot's decays: [0] lb - log2 D, [128] D 2^(sum to the chunk's end), [256] lb = running sum inside the
 // block of 32 tokens, [384] D 2^(sum to the block's end), [512..515] the blocks' sums, [516] 2^(chunk's sum)
@@ -74,7 +74,7 @@ enum Bars {
     kYOut = 6,        // [2] y over the stage's X (8 warps)
     kXRead = 8,       // [2] U has read the stage's X (4 warps)
     kPrepFull = 10,   // [4]
-    kPrepEmpty = 14,  // [4] 16 warps
+    kPrepEmpty = 14,  // [4] 20 warps
     kUFull = 18,      // [4] a quarter of U written (4 warps)
     kUEmpty = 22,     // [4] its product complete
     kBFull = 26,      // B landed
@@ -82,13 +82,13 @@ enum Bars {
     kCFull = 28,      // C landed
     kCEmpty = 29,     // C read (G and C S complete)
     kG = 30,          // G complete
-    kSB = 31,         // S copied (4 warps)
+    kSB = 31,         // S copied (8 warps)
     kY2 = 32,         // C S complete
     kM = 33,          // [2] half the columns of M written, and C S scaled (8 warps)
     kMX = 35,         // M X complete
     kYRead = 36,      // Y read (8 warps)
     kD3 = 37,         // [2] U^T B complete
-    kD3Free = 39,     // [2] read (4 warps)
+    kD3Free = 39,     // [2] read (8 warps)
     kTail = 41,       // X and B past the end cleared (8 warps)
     kBars = 42
 };
@@ -267,10 +267,12 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
 #pragma unroll 1
         for (int i = 0; i < kBars; ++i) {
             int cnt = 1;
-            if (i == kYOut || i == kYOut + 1 || i == kM || i == kM + 1 || i == kYRead || i == kTail) cnt = 8;
-            if (i == kXRead || i == kXRead + 1 || (i >= kUFull && i < kUFull + 4) || i == kSB || i == kD3Free || i == kD3Free + 1) cnt = 4;
+            if (i == kYOut || i == kYOut + 1 || i == kM || i == kM + 1 || i == kYRead || i == kTail || i == kSB || i == kD3Free ||
+                i == kD3Free + 1)
+                cnt = 8;
+            if (i == kXRead || i == kXRead + 1 || (i >= kUFull && i < kUFull + 4)) cnt = 4;
             if (i == kBEmpty) cnt = 2;
-            if (i >= kPrepEmpty && i < kPrepEmpty + 4) cnt = 16;
+            if (i >= kPrepEmpty && i < kPrepEmpty + 4) cnt = 20;
             mbar_init(&bar[i], cnt);
         }
         *fail = 0;
@@ -365,12 +367,11 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
         return true;
     };
 
-    // registers by role (the launch has 640 x 96): 256 x 88 + 128 x 160 + 256 x 72
+    // registers by role (the launch has 768 x 80): 256 x 80 + 128 x 64 + 256 x 96 + 128 x 64
     if (NB == 2) {
-        if (warp >= 16) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        else if (warp >= 12) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
-        else if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp >= 20) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        else if (warp >= 12) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+        else if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     }
 
     if (!OUT && warp < 12) {
@@ -559,23 +560,25 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
             arrive_warp(kXRead + st);
             arrive_warp(kPrepEmpty + (c & 3));
         }
-    } else if (warp < 16) {
-        // ---------------------------------------------------------------- the state: row (slot, p), NC columns
-        const int lq = warp & 3, row = 32 * lq + lane, srow = row >> 6, p = SAME ? row : row & 63;
+    } else if (warp < 20) {
+        // ---------------------------------------------------------------- the state: row (slot, p), NC / 2 columns
+        constexpr int SN = NC / 2;
+        const int half = (warp - 12) >> 2, lq = warp & 3, row = 32 * lq + lane, srow = row >> 6, p = SAME ? row : row & 63;
         const int h = srow ? un.h[1] : un.h[0];
-        float S[NC];
+        float S[SN];
         {
             const float* from = OUT && h >= 0 && p < a.P ? ssm_entering(a, sg, seg, h) : nullptr;
-            const int rows = from ? a.N : 0;
-            from += p;
+            const int rows = from ? a.N - SN * half : 0;
+            from += (size_t)(SN * half) * a.P + p;
 #pragma unroll
-            for (int j = 0; j < NC; ++j, from += a.P) S[j] = j < rows ? *from : 0.f;
+            for (int j = 0; j < SN; ++j, from += a.P) S[j] = j < rows ? *from : 0.f;
         }
-        const uint32_t sbrow = smem_u32(smem + L::SB) + sw(row, 0);
+        // the thread's columns are one half tile (SN 64) or half the chunks of one (SN 32)
+        const uint32_t sbrow = smem_u32(smem + L::SB + (SN == 64 ? half * HALF : 0)) + sw(row, SN == 64 ? 0 : 4 * half);
         // S cut to bf16, and what the cut left rounded to it, as C S's operands
         auto copy_state = [&]() {
 #pragma unroll
-            for (int j = 0; j < NC; j += 8) {
+            for (int j = 0; j < SN; j += 8) {
                 uint32_t o[4], r[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -586,7 +589,7 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                     const float2 d = rest2(v, o[e]);
                     r[e] = pack_bf16(d.x, d.y);
                 }
-                const uint32_t at = (sbrow + (j >> 6) * HALF) ^ ((j & 63) << 1);
+                const uint32_t at = sbrow ^ (j << 1);
                 sts128(at, o);
                 sts128(at + NB * HALF, r);
             }
@@ -602,9 +605,9 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
             tc_fence_after();
             {
                 const float2 eq = dup(lds1f(smem_u32(slot_prep(c, srow)) + 4 * 516));
-                const uint32_t td = tmem + D0 + 128 * (c % ND) + ((uint32_t)(lq * 32) << 16);
+                const uint32_t td = tmem + D0 + 128 * (c % ND) + SN * half + ((uint32_t)(lq * 32) << 16);
 #pragma unroll
-                for (int j = 0; j < NC; j += 16) {
+                for (int j = 0; j < SN; j += 16) {
                     float v[16];
                     tmem_ld16(td + j, v);
                     tmem_ld_wait();
@@ -627,13 +630,13 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
         if (*fail == 0) {
             float* to = h < 0 || p >= a.P ? nullptr
                       : OUT ? ssm_leaving(a, sg, seg, h) : a.states + ((size_t)seg * a.H + h) * a.N * a.P;
-            const int rows = to ? a.N : 0;
-            to += p;
+            const int rows = to ? a.N - SN * half : 0;
+            to += (size_t)(SN * half) * a.P + p;
 #pragma unroll
-            for (int j = 0; j < NC; ++j, to += a.P)
+            for (int j = 0; j < SN; ++j, to += a.P)
                 if (j < rows) *to = S[j];
         }
-    } else if (OUT && warp == 16) {
+    } else if (OUT && warp == 20) {
         // ---------------------------------------------------------------- G, C S, M X
         if (lane == 0) {
             constexpr uint32_t idG = idesc_bf16(128, 128, 0, 0), idX = idesc_bf16(128, SAME ? 128 : 64, 0, 1);
@@ -679,7 +682,7 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
             }
         }
         __syncwarp();
-    } else if (warp == 17) {
+    } else if (warp == 21) {
         // ---------------------------------------------------------------- copies
         if (lane == 0) {
             auto load_b = [&](int c, int st, uint64_t* full) {
@@ -730,7 +733,7 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
             }
         }
         __syncwarp();
-    } else if (warp == 18 || (!OUT && warp == 16)) {
+    } else if (warp == 22 || (!OUT && warp == 20)) {
         // ---------------------------------------------------------------- decays: lane = 4 tokens
         // (states only: the two warps take every other chunk)
         constexpr int STEP = OUT ? 1 : 2;
@@ -741,7 +744,7 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
             bias[s] = un.h[s] >= 0 ? a.dt_bias[un.h[s]] : 0.f;
         }
         const bool two = !SAME && un.h[1] >= 0;
-        const int c0 = !OUT && warp == 16;
+        const int c0 = !OUT && warp == 20;
         const uint16_t* dt = static_cast<const uint16_t*>(a.dt) + (size_t)(sg.t0 + c0 * Q + 4 * lane) * a.ds + un.h[0];
         for (int c = c0; c < nch; c += STEP, dt += STEP * Q * a.ds) {
             const int len = chunk_len(c);
@@ -807,7 +810,7 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
             arrive_warp(kPrepFull + (c & 3));
         }
         if (!OUT && lane < 2) ptot[2 * c0 + lane] = lane ? total[1] : total[0];
-    } else if (warp == 19) {
+    } else if (warp == 23) {
         // ---------------------------------------------------------------- U^T B
         if (lane == 0) {
             constexpr uint32_t idU = idesc_bf16(128, NC, 0, 1);
