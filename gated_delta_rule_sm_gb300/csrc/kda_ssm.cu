@@ -47,14 +47,22 @@ namespace {
 
 // ------------------------------------------------------------------ schedule
 
-// A schedule's cost in chunk times of the output pass: a segment costs its chunks and about two more to
-// start; the state pass about half of that again, the join and the two launches about four.
+// A schedule's cost, in times that the output pass takes for q tokens of a segment.  A segment costs its tokens
+// and `start`; the states-only pass `state` of the output pass again; the join and the launches `join`.  CTAs
+// run in waves of equal segments, or (documents, of any lengths) as SMs fall free: then the last one may start
+// when the others are done.
+//   tensor cores: 4.1 us for 128 tokens; start two chunks, states 0.55 (134 and 237 us on a row of 65536
+//   tokens, 32 heads), join and launches 16 us;
+//   fp32: 2 us for 32 tokens; start 0.5, states 0.6, join and launches 7 us.
 constexpr int kSsmSms = 152;
-double schedule_cost(int64_t chunks, int64_t segs, int64_t rows, int64_t units, int64_t* len) {
-    const int64_t L = (chunks + segs - 1) / segs, n = (chunks + L - 1) / L;
-    *len = L;
-    const int64_t waves = (rows * n * units + kSsmSms - 1) / kSsmSms;
-    return n == 1 ? waves * (L + 2.0) : 1.5 * waves * (L + 2.0) + 4.0;
+struct Costs {
+    int64_t units;       // CTAs per segment over all heads, counted in CTAs that have an SM to themselves
+    int q;               // tokens of a unit of time, and what a segment's length is a multiple of
+    double start, state, join;
+};
+double segment_cost(const Costs& k, double work, double longest, bool even, bool one_pass) {
+    const double out = even ? work : work / kSsmSms + longest / 2 > longest ? work / kSsmSms + longest / 2 : longest;
+    return one_pass ? out : (1 + k.state) * out + k.join;
 }
 
 struct Schedule {
@@ -65,24 +73,39 @@ struct Schedule {
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// units: CTAs per segment over all heads, counted in CTAs that have an SM to themselves.
-Schedule make_schedule(const SsmShape& s, bool varlen, int64_t units) {
+Schedule make_schedule(const SsmShape& s, bool varlen, const Costs& k) {
+    const int64_t units = k.units, q = k.q;
     Schedule w;
     memset(&w, 0, sizeof(w));
-    const int64_t span = varlen ? (s.TT + s.rows - 1) / s.rows : s.T;   // of documents: their mean
-    const int64_t chunks = (span + 127) / 128;
-    int64_t best = chunks, len;
-    double least = schedule_cost(chunks, 1, s.rows, units, &len);
-    for (int64_t segs = 2; segs <= chunks && s.rows * (segs - 1) * units < 4 * kSsmSms; ++segs) {
-        const double c = schedule_cost(chunks, segs, s.rows, units, &len);
-        if (c < least) {
-            least = c;
-            best = len;
+    int64_t best = 0;                       // length of a segment in q; 0: rows are not cut
+    if (!varlen) {
+        const int64_t chunks = (s.T + q - 1) / q, ctas = s.rows * units;
+        double least = segment_cost(k, (ctas + kSsmSms - 1) / kSsmSms * (chunks + k.start), 0, true, true);
+        for (int64_t segs = 2; segs <= chunks && (segs - 1) * ctas < 4 * kSsmSms; ++segs) {
+            const int64_t len = (chunks + segs - 1) / segs, n = (chunks + len - 1) / len;
+            const double c = segment_cost(k, (n * ctas + kSsmSms - 1) / kSsmSms * (len + k.start), 0, true, false);
+            if (n > 1 && c < least) {
+                least = c;
+                best = len;
+            }
+        }
+    } else {
+        // The lengths are on the device: take the longest of a random cut of the tokens, (1 + ln rows) / rows
+        const double chunks = (double)s.TT / q, share = (1.0 + log((double)s.rows)) / s.rows;
+        const double longest = chunks * (share < 1 ? share : 1) + k.start;
+        double least = segment_cost(k, (chunks + (k.start + 0.5) * s.rows) * units, longest, false, true);
+        for (int64_t len = 4; len < longest; len += len < 16 ? 4 : len / 4) {
+            const double ctas = s.rows + chunks / len;
+            const double c = segment_cost(k, (chunks + (k.start + 0.5) * ctas) * units, len + k.start, false, false);
+            if (c < least) {
+                least = c;
+                best = len;
+            }
         }
     }
-    w.single = best == chunks;
+    w.single = best == 0;
     const int64_t longest = varlen ? s.TT : s.T;
-    w.L = (int)((w.single ? (longest + 127) / 128 : best) * 128);
+    w.L = (int)((w.single ? (longest + q - 1) / q : best) * q);
     w.per_row = varlen ? 0 : (s.T + w.L - 1) / w.L;
     w.nseg = varlen ? (w.single ? s.rows : s.rows + s.TT / w.L) : s.rows * w.per_row;
     size_t o = 0;
@@ -99,8 +122,8 @@ Schedule make_schedule(const SsmShape& s, bool varlen, int64_t units) {
 }
 
 // Four CTAs of the fp32 kernel share an SM.
-int64_t simt_units(const SsmShape& s) { return ((int64_t)s.H * ((s.P + 31) / 32) + 3) / 4; }
-int64_t tc_units(const SsmShape& s) { return ssm_tc_units(s.H, s.G, s.P); }
+Costs simt_costs(const SsmShape& s) { return {((int64_t)s.H * ((s.P + 31) / 32) + 3) / 4, 32, 0.5, 0.6, 3.5}; }
+Costs tc_costs(const SsmShape& s) { return {ssm_tc_units(s.H, s.G, s.P), 128, 2.0, 0.55, 4.0}; }
 
 // Segments of every row in order: ceil(len / L) of them, one empty segment for an empty row (its state
 // passes through).  Offsets that break the contract are recorded and give every row one empty segment.
@@ -215,7 +238,7 @@ __global__ void __launch_bounds__(128) ssm_join_kernel(SsmArgs a) {
 constexpr int kSimtTok = 16, kSimtCols = 32;
 
 template <int NJ, bool OUT>
-__global__ void __launch_bounds__(256) ssm_simt_kernel(SsmArgs a) {
+__global__ void __launch_bounds__(256, NJ <= 2 ? 3 : NJ == 4 ? 2 : 1) ssm_simt_kernel(SsmArgs a) {
     constexpr int NP = 32 * NJ;
     __shared__ __align__(16) float sb[kSimtTok][NP], sc[OUT ? kSimtTok : 1][NP];
     __shared__ float sx[kSimtTok][kSimtCols], sy[kSimtTok][kSimtCols], sal[kSimtTok], sdt[kSimtTok];
@@ -243,27 +266,44 @@ __global__ void __launch_bounds__(256) ssm_simt_kernel(SsmArgs a) {
             S[j][e] = from && pin && n < a.N ? from[(size_t)n * a.P + p] : 0.f;
         }
     float lsum = 0.f;
+    // a block of tokens is loaded into registers while the one before it is worked on
+    constexpr int PB = kSimtTok * NP / 256, PX = kSimtTok * kSimtCols / 256;
+    float rb[PB], rc[OUT ? PB : 1], rx[PX], rdt = 0.f;
+    auto fetch = [&](int t0) {
+        const int nt = min(kSimtTok, sg.t1 - t0);
+#pragma unroll
+        for (int i = 0; i < PB; ++i) {
+            const int t = (tid + 256 * i) / NP, n = (tid + 256 * i) % NP;
+            const bool in = t < nt && n < a.N;
+            rb[i] = in ? load_act(a.b, (size_t)(t0 + t) * a.bs + (size_t)g * a.N + n, a.dtype) : 0.f;
+            if (OUT) rc[i] = in ? load_act(a.c, (size_t)(t0 + t) * a.cs + (size_t)g * a.N + n, a.dtype) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < PX; ++i) {
+            const int t = (tid + 256 * i) / kSimtCols, c = (tid + 256 * i) % kSimtCols;
+            rx[i] = t < nt && p0 + c < a.P ? load_act(a.x, (size_t)(t0 + t) * a.xs + (size_t)h * a.P + p0 + c, a.dtype) : 0.f;
+        }
+        if (tid < nt) rdt = load_act(a.dt, (size_t)(t0 + tid) * a.ds + h, a.dtype);
+    };
+    if (sg.t0 < sg.t1) fetch(sg.t0);
     for (int t0 = sg.t0; t0 < sg.t1; t0 += kSimtTok) {
         const int nt = min(kSimtTok, sg.t1 - t0);
-        __syncthreads();
-        for (int i = tid; i < kSimtTok * NP; i += 256) {
-            const int t = i / NP, n = i - t * NP;
-            const bool in = t < nt && n < a.N;
-            sb[t][n] = in ? load_act(a.b, (size_t)(t0 + t) * a.bs + (size_t)g * a.N + n, a.dtype) : 0.f;
-            if (OUT) sc[t][n] = in ? load_act(a.c, (size_t)(t0 + t) * a.cs + (size_t)g * a.N + n, a.dtype) : 0.f;
+#pragma unroll
+        for (int i = 0; i < PB; ++i) {
+            const int t = (tid + 256 * i) / NP, n = (tid + 256 * i) % NP;
+            sb[t][n] = rb[i];
+            if (OUT) sc[t][n] = rc[i];
         }
-        for (int i = tid; i < kSimtTok * kSimtCols; i += 256) {
-            const int t = i / kSimtCols, c = i - t * kSimtCols;
-            sx[t][c] = t < nt && p0 + c < a.P
-                           ? load_act(a.x, (size_t)(t0 + t) * a.xs + (size_t)h * a.P + p0 + c, a.dtype) : 0.f;
-        }
+#pragma unroll
+        for (int i = 0; i < PX; ++i) sx[(tid + 256 * i) / kSimtCols][(tid + 256 * i) % kSimtCols] = rx[i];
         if (tid < kSimtTok) {
-            const float dt = tid < nt ? softplusf(load_act(a.dt, (size_t)(t0 + tid) * a.ds + h, a.dtype) + bias) : 0.f;
+            const float dt = tid < nt ? softplusf(rdt + bias) : 0.f;
             sdt[tid] = dt;
             sal[tid] = expf(-ea * dt);   // a token past the end keeps the state
             if (!OUT) lsum += dt;
         }
         __syncthreads();
+        if (t0 + kSimtTok < sg.t1) fetch(t0 + kSimtTok);
 #pragma unroll
         for (int t8 = 0; t8 < kSimtTok; t8 += 8) {
             float y[8];
@@ -302,13 +342,12 @@ __global__ void __launch_bounds__(256) ssm_simt_kernel(SsmArgs a) {
                 sy[t8 + slice][pc] = fmaf(dsk, sx[t8 + slice][pc], y[0]);
             }
         }
-        if (OUT) {
-            __syncthreads();
+        __syncthreads();
+        if (OUT)
             for (int i = tid; i < nt * kSimtCols; i += 256) {
                 const int t = i / kSimtCols, c = i - t * kSimtCols;
                 if (p0 + c < a.P) store_act(a.y, ((size_t)(t0 + t) * a.H + h) * a.P + p0 + c, sy[t][c], a.dtype);
             }
-        }
     }
     float* to = OUT ? ssm_leaving(a, sg, blockIdx.x, h) : a.states + ((size_t)blockIdx.x * a.H + h) * a.N * a.P;
     if (to && pin)
@@ -362,8 +401,8 @@ size_t kda_ssm_fwd_workspace_size(const kda_ssm_dims* dims) {
         if (ssm_check(dims, varlen != 0, f, f, f, f, f, f, &s) != KDA_OK) continue;
         valid = true;
         // which kernels run also depends on the pointers' alignment
-        for (const int64_t units : {simt_units(s), tc_units(s)}) {
-            const size_t t = make_schedule(s, varlen != 0, units).total;
+        for (const Costs& k : {simt_costs(s), tc_costs(s)}) {
+            const size_t t = make_schedule(s, varlen != 0, k).total;
             if (t > most) most = t;
         }
     }
@@ -381,7 +420,7 @@ kda_status kda_ssm_fwd(const kda_ssm_dims* dims, const void* x, const void* dt_r
     st = check_offsets_host(s.rows, s.TT, cu_seqlens, cu_seqlens_host);
     if (st != KDA_OK) return st;
     const bool tc = ssm_tc_ok(s, x, b, c, y);
-    const Schedule w = make_schedule(s, cu_seqlens != nullptr, tc ? tc_units(s) : simt_units(s));
+    const Schedule w = make_schedule(s, cu_seqlens != nullptr, tc ? tc_costs(s) : simt_costs(s));
     if (workspace_bytes < w.total || (w.total && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256)))
         return KDA_ERR_WORKSPACE;
     if (w.nseg > (1 << 30) / s.H || s.H > 65535) return KDA_ERR_UNSUPPORTED;
