@@ -566,6 +566,17 @@ def _empty(like, shape, dtype, stream):
         return like.new_empty(shape, dtype=dtype)
 
 
+def _result(name: str, out, like, dev: int, stream):
+    """The output tensor of like's shape and dtype, given or new, and its address."""
+    if out is not None:
+        return out, _need(name, out, like.dtype, like.shape, dev)
+    if stream is None and like.is_contiguous():
+        out = torch.empty_like(like)
+    else:
+        out = _empty(like, like.shape, like.dtype, stream)
+    return out, out.data_ptr()
+
+
 def _scratch(like, dev: int, kind: str, ptr: int, nbytes: int, stream):
     """One workspace per device, kind and stream: calls on different streams may overlap."""
     buf = workspace_cache.buf.get((dev, kind, ptr))
@@ -630,16 +641,16 @@ def ssm_scan(x, dt_raw, b, c, a_log, dt_bias, d_skip=None, *, cu_seqlens=None, c
     state_shape = (rows, x.shape[2], b.shape[3], x.shape[3])
     s0 = _need("initial_state", initial_state, _F32, state_shape, dev)
     st = _raw_stream(dev, stream)
-    if out is None:
-        out = _empty(x, x.shape, x.dtype, stream)
+    out, po = _result("out", out, x, dev, stream)
     if not output_final_state:
-        final_state = None
+        final_state = pf = None
     elif final_state is None:
-        final_state = _empty(x, state_shape, _F32, stream)
+        final_state = _empty(a_log, state_shape, _F32, stream)
+        pf = final_state.data_ptr()
+    else:
+        pf = _need("final_state", final_state, _F32, state_shape, dev)
     ws = _scratch(x, dev, "ssm", st, nbytes, stream)
-    _check(lib.kda_ssm_fwd(ref, *args, cu, cu_h, s0, _need("out", out, x.dtype, x.shape, dev),
-                           _need("final_state", final_state, _F32, state_shape, dev), ws.data_ptr(), ws.numel(), st),
-           "kda_ssm_fwd")
+    _check(lib.kda_ssm_fwd(ref, *args, cu, cu_h, s0, po, pf, ws.data_ptr(), ws.numel(), st), "kda_ssm_fwd")
     return out, final_state
 
 
@@ -665,10 +676,8 @@ def ssm_step(x, dt_raw, b, c, a_log, dt_bias, d_skip=None, *, state, slots=None,
     ref, _, args = _ssm_args(x, dt_raw, b, c, a_log, dt_bias, d_skip, 1, 0, dev, code)
     B, H, P = x.shape
     pool, state_out = _pool_args("state", state, slots, B, (H, b.shape[2], P), _F32, state_out, dev)
-    if out is None:
-        out = _empty(x, x.shape, x.dtype, stream)
-    _check(lib.kda_ssm_step(ref, *args, *pool, _need("out", out, x.dtype, x.shape, dev), _raw_stream(dev, stream)),
-           "kda_ssm_step")
+    out, po = _result("out", out, x, dev, stream)
+    _check(lib.kda_ssm_step(ref, *args, *pool, po, _raw_stream(dev, stream)), "kda_ssm_step")
     return out, state_out
 
 
@@ -696,11 +705,9 @@ def decode_step(q, k, v, g_raw, beta_raw, a_log, dt_bias, *, scale: float, lower
             _need("g_raw", g_raw, dtype, gates, dev), _need("beta_raw", beta_raw, dtype, (B, H), dev),
             _need("a_log", a_log, _F32, (H,), dev), _need("dt_bias", dt_bias, _F32, (H * K,), dev))
     pool, state_out = _pool_args("state", state, slots, B, (H, K, V), _F32, state_out, dev)
-    if out is None:
-        out = _empty(v, v.shape, dtype, stream)
+    out, po = _result("out", out, v, dev, stream)
     _, ref = _step_dims(B, 1, H, K, V, code, 0, Hk, _gate_code(gate))
-    _check(lib.kda_decode_step(ref, *args, scale, lower_bound, *pool, _need("out", out, dtype, (B, H, V), dev),
-                               _raw_stream(dev, stream)), "kda_decode_step")
+    _check(lib.kda_decode_step(ref, *args, scale, lower_bound, *pool, po, _raw_stream(dev, stream)), "kda_decode_step")
     return out, state_out
 
 
@@ -723,12 +730,11 @@ def short_conv_prompt(x, weight, bias=None, *, cu_seqlens=None, cu_seqlens_host=
     n, rows, cu, cu_h = _offsets(cu_seqlens, cu_seqlens_host, B, dev)
     hist = (rows, W - 1, C)
     h0 = _need("initial_history", initial_history, x.dtype, hist, dev)
-    if out is None:
-        out = _empty(x, x.shape, x.dtype, stream)
+    out, po = _result("out", out, x, dev, stream)
     if final_history is None:
         final_history = _empty(x, hist, x.dtype, stream)
-    _check(lib.kda_short_conv_prompt(B, T, C, W, code, x.data_ptr(), _token_stride("x", x.shape, x.stride(), 2), *params, cu, cu_h, n, h0,
-                                     _need("out", out, x.dtype, x.shape, dev),
+    _check(lib.kda_short_conv_prompt(B, T, C, W, code, x.data_ptr(), _token_stride("x", x.shape, x.stride(), 2), *params,
+                                     cu, cu_h, n, h0, po,
                                      _need("final_history", final_history, x.dtype, hist, dev), _raw_stream(dev, stream)),
            "kda_short_conv_prompt")
     return out, final_history
@@ -743,11 +749,9 @@ def short_conv_step(x, weight, bias=None, *, history, slots=None, history_out=No
     B, C = x.shape
     W, params = _conv_args(x, weight, bias, dev, C)
     pool, history_out = _pool_args("history", history, slots, B, (W - 1, C), x.dtype, history_out, dev)
-    if out is None:
-        out = _empty(x, x.shape, x.dtype, stream)
+    out, po = _result("out", out, x, dev, stream)
     _check(lib.kda_short_conv_step(B, C, W, code, x.data_ptr(), _token_stride("x", x.shape, x.stride(), 1), *params, *pool,
-                                   _need("out", out, x.dtype, x.shape, dev), _raw_stream(dev, stream)),
-           "kda_short_conv_step")
+                                   po, _raw_stream(dev, stream)), "kda_short_conv_step")
     return out, history_out
 
 
