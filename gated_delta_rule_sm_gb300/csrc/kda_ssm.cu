@@ -419,7 +419,10 @@ kda_status kda_ssm_fwd(const kda_ssm_dims* dims, const void* x, const void* dt_r
     if (!y) return KDA_ERR_INVALID_ARG;
     st = check_offsets_host(s.rows, s.TT, cu_seqlens, cu_seqlens_host);
     if (st != KDA_OK) return st;
-    const bool tc = ssm_tc_ok(s, x, b, c, y);
+    // A few tokens to a row: one wave of the fp32 kernel's CTAs takes 4.6 to 7.4 us up to 16 tokens, the
+    // tensor-core kernel 11.6 to 14.2 us however few they are (at 37 tokens both take as long)
+    const bool few = s.TT <= 16 * s.rows && (long long)s.rows * s.H * ((s.P + 31) / 32) <= 2 * kSsmSms;
+    const bool tc = !few && ssm_tc_ok(s, x, b, c, y);
     const Schedule w = make_schedule(s, cu_seqlens != nullptr, tc ? tc_costs(s) : simt_costs(s));
     if (workspace_bytes < w.total || (w.total && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256)))
         return KDA_ERR_WORKSPACE;
