@@ -21,10 +21,10 @@
 // exponent is the difference of two large numbers; a token's exponent is cut at -150 (2^-150 is 0 in
 // fp32).
 //
-// Roles (24 warps): 0-7 form M, scale C S and finish Y (two warpgroups: columns of G are split between
-// them, Y by head); 8-11 form U, a quarter of a chunk at a time; 12-19 keep the state, half a row a thread;
-// 20 issues G, C S and M X, 21 the copies, 22 prepares the decays, 23 issues U^T B.  Roles meet at mbarriers
-// only, so the state's chain (U^T B, S, C S) runs beside the output's (G, M, M X, Y).
+// Roles (24 warps): 0-7 form M (two warpgroups, which split the columns); 8-11 form U, a quarter of a chunk at
+// a time; 12-19 scale C S, keep the state (half a row a thread) and finish Y (a head each warpgroup); 20
+// issues G, C S and M X, 21 the copies, 22 prepares the decays, 23 issues U^T B.  Roles meet at mbarriers
+// only: M of a chunk is formed while Y of the one before it is finished.
 // The pass that only forms states has no G, M, C S or Y: its first three warpgroups all form U, in four
 // TMEM buffers, with three stages of X and B.
 // TMEM columns: G / M 128, Y 128, U^T B 128, U 2 x 48.
@@ -84,13 +84,14 @@ enum Bars {
     kG = 30,          // G complete
     kSB = 31,         // S copied (8 warps)
     kY2 = 32,         // C S complete
-    kM = 33,          // [2] half the columns of M written, and C S scaled (8 warps)
+    kM = 33,          // [2] half the columns of M written (8 warps)
     kMX = 35,         // M X complete
     kYRead = 36,      // Y read (8 warps)
     kD3 = 37,         // [2] U^T B complete
     kD3Free = 39,     // [2] read (8 warps)
     kTail = 41,       // X and B past the end cleared (8 warps)
-    kBars = 42
+    kYS = 42,         // C S scaled (8 warps)
+    kBars = 43
 };
 
 // TMEM columns
@@ -267,7 +268,7 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
 #pragma unroll 1
         for (int i = 0; i < kBars; ++i) {
             int cnt = 1;
-            if (i == kYOut || i == kYOut + 1 || i == kM || i == kM + 1 || i == kYRead || i == kTail || i == kSB || i == kD3Free ||
+            if (i == kYOut || i == kYOut + 1 || i == kM || i == kM + 1 || i == kYRead || i == kTail || i == kSB || i == kYS || i == kD3Free ||
                 i == kD3Free + 1)
                 cnt = 8;
             if (i == kXRead || i == kXRead + 1 || (i >= kUFull && i < kUFull + 4)) cnt = 4;
@@ -367,11 +368,12 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
         return true;
     };
 
-    // registers by role (the launch has 768 x 80): 256 x 80 + 128 x 64 + 256 x 96 + 128 x 64
+    // registers by role (the launch has 768 x 80): 256 x 72 + 128 x 64 + 256 x 104 + 128 x 64
     if (NB == 2) {
         if (warp >= 20) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        else if (warp >= 12) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+        else if (warp >= 12) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
         else if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     }
 
     if (!OUT && warp < 12) {
@@ -389,38 +391,28 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
             arrive_warp(kPrepEmpty + (c & 3));
         }
     } else if (warp < 8) {
-        // ---------------------------------------------------------------- M, C S, Y
+        // ---------------------------------------------------------------- M
         const int wg = warp >> 2, lq = warp & 3;
         const int row = 32 * lq + lane;              // token of the chunk
         const uint32_t lanes = (uint32_t)(lq * 32) << 16;
         constexpr uint32_t PS = SAME ? 0 : 4 * kPrepFloats;
-        const int h = wg ? un.h[1] : un.h[0];
-        const float dsk = a.d_skip && h >= 0 ? a.d_skip[h] : 0.f;
-        const uint32_t ty = tmem + TY + lanes + 64 * wg;
         for (int c = 0; c < nch; ++c) {
-            const uint32_t par = c & 1;
-            const int st = c & 1, len = chunk_len(c);
             const uint32_t pr = smem_u32(slot_prep(c, 0));
-            const uint32_t xrow = smem_u32(smem + L::X + (2 * st + wg) * HALF) + sw(row, 0);
-            if (!wait_prep(c) || !clear_tail(c, st)) break;
-            // the row's exponents while G is formed: from its block's start (lt), for C S's scale (ly), and from the
-            // end of each column block of this warpgroup that lies before the diagonal (lj)
-            float lt[2], lj[2][2], ly;
+            if (!wait_prep(c) || !clear_tail(c, c & 1)) break;
+            // the row's exponents while G is formed: from its block's start (lt), and from the end of each column
+            // block of this warpgroup that lies before the diagonal (lj)
+            float lt[2], lj[2];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const float4 sum = lds4f(pr + s * PS + 4 * 512);
                 lt[s] = lds1f(pr + s * PS + 4 * (256 + row));
                 // blocks 0 and 3 (wg 0) or 1 and 2: what lies between the block's end and the row's block
-                const float s1 = lq > 1 ? sum.y : 0.f, s2 = lq > 2 ? sum.z : 0.f;
-                lj[0][s] = lt[s] + (wg ? s2 : s1 + s2);
-                lj[1][s] = lt[s];
-                if (s == wg) ly = lt[s] + ((lq > 0 ? sum.x : 0.f) + s1) + s2;
+                lj[s] = lt[s] + ((lq > 1 && !wg ? sum.y : 0.f) + (lq > 2 ? sum.z : 0.f));
             }
-            if (!wait(kG, par)) break;
+            if (!wait(kG, c & 1)) break;
             tc_fence_after();
             // (not unrolled: fetching code that all roles' loops cannot keep in the instruction cache
             // costs more than the loop)
-            bool ok = true;
 #pragma unroll 1
             for (int b = 0; b < 2; ++b) {
                 const int J = 2 * b + (wg ^ b);
@@ -460,7 +452,7 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                             tmem_st8(tg + c0 + 8 * s, m);
                         }
                     } else {                 // a factor of the column to the block's end, one of the row from there
-                        const float2 rf = dup(ex2(b ? (s ? lj[1][1] : lj[1][0]) : (s ? lj[0][1] : lj[0][0])));
+                        const float2 rf = dup(ex2(b ? (s ? lt[1] : lt[0]) : (s ? lj[1] : lj[0])));
 #pragma unroll
                         for (int c0 = 0; c0 < 32; c0 += 16) {
                             float4 f4[4];
@@ -481,71 +473,11 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                     }
                 }
                 }
-                if (b == 0) {     // C S of this warpgroup's columns, scaled by exp(l_t)
-                    const float2 el = dup(ex2(ly));
-                    ok = wait(kY2, par);
-                    if (!ok) break;
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int j = 0; j < 64; j += 32) {
-                        float v[32];
-                        uint32_t r[32];
-                        tmem_ld16(ty + j, v);
-                        tmem_ld16(ty + j + 16, v + 16);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            const float2 y = mul2(make_float2(v[i], v[i + 1]), el);
-                            r[i] = __float_as_uint(y.x);
-                            r[i + 1] = __float_as_uint(y.y);
-                        }
-                        tmem_st16(ty + j, r);
-                        tmem_st16(ty + j + 16, r + 16);
-                    }
-                }
                 tmem_st_wait();
                 tc_fence_before();
                 arrive_warp(kM + b);
             }
-            if (!ok) break;
             arrive_warp(kPrepEmpty + (c & 3));
-            if (!wait(kXRead + st, (c >> 1) & 1) || !wait(kMX, par)) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int j = 0; j < 8; j += 4) {
-                float v[32];
-                uint4 u[4];
-                tmem_ld16(ty + 8 * j, v);
-                tmem_ld16(ty + 8 * j + 16, v + 16);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) u[k] = lds128(xrow ^ ((j + k) << 4));
-                tmem_ld_wait();
-                if (j) {
-                    tc_fence_before();
-                    arrive_warp(kYRead);      // C S of the next chunk may start
-                }
-                // y over x, which nothing else reads any more
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
-                    uint32_t o[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 y = fma2(dup(dsk), bf2(w[e]), make_float2(v[8 * k + 2 * e], v[8 * k + 2 * e + 1]));
-                        o[e] = pack_bf16(y.x, y.y);
-                    }
-                    sts128(xrow ^ ((j + k) << 4), o);
-                }
-            }
-            if (len == Q) {
-                fence_async_smem();       // the copy warp stores the tile
-            } else if (row < len && h >= 0) {
-                const int p0 = SAME ? 64 * wg : 0;
-                __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + ((size_t)(sg.t0 + c * Q + row) * a.H + h) * a.P + p0;
-#pragma unroll 1
-                for (int k = 0; k < 8 && p0 + 8 * k < a.P; ++k) *reinterpret_cast<uint4*>(y + 8 * k) = lds128(xrow ^ (k << 4));
-            }
-            arrive_warp(kYOut + st);
         }
     } else if (warp < 12) {
         // ---------------------------------------------------------------- U
@@ -561,7 +493,8 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
             arrive_warp(kPrepEmpty + (c & 3));
         }
     } else if (warp < 20) {
-        // ---------------------------------------------------------------- the state: row (slot, p), NC / 2 columns
+        // ---------------------------------------------------------------- the state (row (slot, p), NC / 2 columns), C S and Y
+        // (row: token, 64 columns)
         constexpr int SN = NC / 2;
         const int half = (warp - 12) >> 2, lq = warp & 3, row = 32 * lq + lane, srow = row >> 6, p = SAME ? row : row & 63;
         const int h = srow ? un.h[1] : un.h[0];
@@ -599,9 +532,38 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
         if (OUT && nch > 0) {
             copy_state();
         }
+        const uint32_t ty = tmem + TY + ((uint32_t)(lq * 32) << 16) + 64 * half;
+        const int hy = half ? un.h[1] : un.h[0];
+        const float dsk = OUT && a.d_skip && hy >= 0 ? a.d_skip[hy] : 0.f;
         for (int c = 0; c < nch; ++c) {
             const uint32_t par = c & 1;
-            if (!wait_prep(c) || !wait(kD3 + c % ND, (c / ND) & 1)) break;
+            if (!wait_prep(c)) break;
+            if (OUT) {     // C S scaled by exp(l_t)
+                const uint32_t pr = smem_u32(slot_prep(c, half));
+                const float4 sum = lds4f(pr + 4 * 512);
+                const float l = lds1f(pr + 4 * (256 + row)) + (((lq > 0 ? sum.x : 0.f) + (lq > 1 ? sum.y : 0.f)) + (lq > 2 ? sum.z : 0.f));
+                const float2 el = dup(ex2(l));
+                if (!wait(kY2, par)) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int j = 0; j < 64; j += 16) {
+                    float v[16];
+                    uint32_t r[16];
+                    tmem_ld16(ty + j, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        const float2 y = mul2(make_float2(v[i], v[i + 1]), el);
+                        r[i] = __float_as_uint(y.x);
+                        r[i + 1] = __float_as_uint(y.y);
+                    }
+                    tmem_st16(ty + j, r);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                arrive_warp(kYS);
+            }
+            if (!wait(kD3 + c % ND, (c / ND) & 1)) break;
             tc_fence_after();
             {
                 const float2 eq = dup(lds1f(smem_u32(slot_prep(c, srow)) + 4 * 516));
@@ -622,9 +584,46 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
             tc_fence_before();
             arrive_warp(kD3Free + c % ND);
             arrive_warp(kPrepEmpty + (c & 3));
-            if (OUT && c + 1 < nch) {
-                if (!wait(kY2, par)) break;      // C S has read the copies
-                copy_state();
+            if (OUT) {
+                if (c + 1 < nch) copy_state();      // (C S has read the last copies)
+                const int st = c & 1, len = chunk_len(c);
+                const uint32_t xrow = smem_u32(smem + L::X + (2 * st + half) * HALF) + sw(row, 0);
+                if (!wait(kXRead + st, (c >> 1) & 1) || !wait(kMX, par)) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int j = 0; j < 8; j += 2) {
+                    float v[16];
+                    uint4 u[2];
+                    tmem_ld16(ty + 8 * j, v);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) u[k] = lds128(xrow ^ ((j + k) << 4));
+                    tmem_ld_wait();
+                    if (j == 6) {
+                        tc_fence_before();
+                        arrive_warp(kYRead);      // C S of the next chunk may start
+                    }
+                    // y over x, which nothing else reads any more
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+                        uint32_t o[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 y = fma2(dup(dsk), bf2(w[e]), make_float2(v[8 * k + 2 * e], v[8 * k + 2 * e + 1]));
+                            o[e] = pack_bf16(y.x, y.y);
+                        }
+                        sts128(xrow ^ ((j + k) << 4), o);
+                    }
+                }
+                if (len == Q) {
+                    fence_async_smem();       // the copy warp stores the tile
+                } else if (row < len && hy >= 0) {
+                    const int p0 = SAME ? 64 * half : 0;
+                    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + ((size_t)(sg.t0 + c * Q + row) * a.H + hy) * a.P + p0;
+#pragma unroll 1
+                    for (int k = 0; k < 8 && p0 + 8 * k < a.P; ++k) *reinterpret_cast<uint4*>(y + 8 * k) = lds128(xrow ^ (k << 4));
+                }
+                arrive_warp(kYOut + st);
             }
         }
         if (*fail == 0) {
@@ -668,7 +667,7 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                 bool ok = true;
 #pragma unroll 1
                 for (uint32_t b = 0; b < 2 && ok; ++b) {         // tokens 64 b .. of the sum, as M's halves come
-                    ok = wait1(kM + b, c & 1);
+                    ok = wait1(kM + b, c & 1) && (b || wait1(kYS, c & 1));
                     if (!ok) break;
                     tc_fence_after();
                     steps<SAME ? 4 : 8>([&](auto i) {
