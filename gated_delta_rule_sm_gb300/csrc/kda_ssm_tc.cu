@@ -286,10 +286,11 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
     tc_fence_after();
     const uint32_t tmem = *tslot;
 
-    // Bounded waits; false, and the CTA marked as failed, where one gives up: its role then leaves its loop, and
+    // Bounded waits (one in good order takes microseconds, and a try suspends the thread for some at most);
+    // false, and the CTA marked as failed, where one gives up: its role then leaves its loop, and
     // the roles that wait for it give up in turn.  Kept short: they are inlined some thirty times, and the
     // code of all roles' loops has to stay in the instruction cache.
-    constexpr uint32_t kTries = 1u << 22;
+    constexpr uint32_t kTries = 1u << 17;
     auto wait1 = [&](int b, uint32_t parity) {
         if (mbar_test_wait(&bar[b], parity)) return true;
 #pragma unroll 1
@@ -314,6 +315,10 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
     auto slot_prep = [&](int c, int s) { return prep_slot<NB, SAME, OUT>(smem, c, s); };
     auto wait_prep = [&](int c) { return wait(kPrepFull + (c & 3), (c >> 2) & 1); };
 
+    // The barriers' parities tell a phase from its neighbours only, so nobody may be two phases ahead of or
+    // behind one it waits for.  U's producers: whoever forms quarter k has formed quarter k - NU or a later one
+    // before (three warpgroups, four buffers), so the product of k - 2 NU is complete; and every waiter of a
+    // stage has a part in the work that its next load waits for.
     // A quarter of U, transposed: rows (slot, p) 32 (warp % 4) .., 32 tokens, as three bf16 terms in TMEM.  The
     // tile is read through transposing 8 x 8 loads, so that a thread's word holds two tokens of one row.
     auto u_quarter = [&](int c, int st, int q) {
