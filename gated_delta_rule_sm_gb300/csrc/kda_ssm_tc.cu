@@ -26,7 +26,8 @@
 // issues G, C S and M X, 21 the copies, 22 prepares the decays, 23 issues U^T B.  Roles meet at mbarriers
 // only: M of a chunk is formed while Y of the one before it is finished.
 // The pass that only forms states has no G, M, C S or Y: its first three warpgroups all form U, in four
-// TMEM buffers, with three stages of X and B.
+// TMEM buffers, with three stages of X and B.  Its U^T B is issued by warps 20 and 23, a chunk each in turn:
+// one thread takes some 1000 cycles for the six products of a quarter, tensor time 400.
 // TMEM columns: G / M 128, Y 128, U^T B 128, U 2 x 48.
 // Bound: per chunk and unit 29 MFLOP (the state's three terms 12.6, C S 8.4) against 64 KB of x and y: 2.3 us and
 // 1.5 us of an SM's share at the measured rates.
@@ -243,8 +244,7 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
     using L = Lay<NB, OUT>;
     constexpr int NC = 64 * NB;                      // padded state columns
     constexpr int NST = L::STAGES;
-    constexpr int NU = OUT ? 2 : 4;                  // U buffers (without G, M and Y their columns are free)
-    constexpr uint32_t U0 = OUT ? TU : 0;
+    constexpr uint32_t U0 = OUT ? TU : 0;            // two U buffers, or four where G, M and Y leave their columns
     constexpr int ND = OUT ? 1 : 2;                  // accumulators of U^T B
     constexpr uint32_t D0 = OUT ? TD : 192;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -262,7 +262,7 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::BAR);
     volatile int* fail = reinterpret_cast<volatile int*>(smem + L::BAR + 8 * kBars);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::BAR + 8 * kBars + 4);
-    float* ptot = reinterpret_cast<float*>(smem + L::BAR + 8 * kBars + 8);    // [2 warps][2 slots]
+    float* ptot = reinterpret_cast<float*>(smem + L::BAR + 8 * kBars + 8);    // [2 slots]
 
     if (tid == 0) {
 #pragma unroll 1
@@ -279,7 +279,6 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
         *fail = 0;
         mbar_fence_init();
     }
-    if (tid < 4) ptot[tid] = 0.f;
     if (warp == 0) tmem_alloc(tslot, TCOLS);
     tc_fence_before();
     __syncthreads();
@@ -316,14 +315,14 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
     auto wait_prep = [&](int c) { return wait(kPrepFull + (c & 3), (c >> 2) & 1); };
 
     // The barriers' parities tell a phase from its neighbours only, so nobody may be two phases ahead of or
-    // behind one it waits for.  U's producers: whoever forms quarter k has formed quarter k - NU or a later one
-    // before (three warpgroups, four buffers), so the product of k - 2 NU is complete; and every waiter of a
-    // stage has a part in the work that its next load waits for.
+    // behind one it waits for: every waiter of a stage has a part in the work that its next load waits for, and a
+    // U buffer's former use but one is complete by the order of the products (outputs) or by the wait for the
+    // last chunk but one (states only).
     // A quarter of U, transposed: rows (slot, p) 32 (warp % 4) .., 32 tokens, as three bf16 terms in TMEM.  The
     // tile is read through transposing 8 x 8 loads, so that a thread's word holds two tokens of one row.
     auto u_quarter = [&](int c, int st, int q) {
-        const int k = 4 * c + q, b = k % NU, lq = warp & 3;
-        if (k >= NU && !wait(kUEmpty + b, (k / NU - 1) & 1)) return false;
+        const int k = 4 * c + q, b = OUT ? k & 1 : 2 * (c & 1) + (q & 1), lq = warp & 3;
+        if (OUT ? k >= 2 && !wait(kUEmpty + b, ((k >> 1) - 1) & 1) : q >= 2 && !wait(kUEmpty + b, 0)) return false;
         tc_fence_after();
         const float* w = slot_prep(c, lq >> 1) + 128 + 32 * q + 2 * (lane & 3);
         float2 wk[4];
@@ -386,6 +385,7 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
         const int wg = warp >> 2;
         for (int c = 0, st = 0; c < nch; ++c, st = st + 1 == NST ? 0 : st + 1) {
             if (!wait_prep(c) || !wait(kFull + st, (c / NST) & 1)) break;
+            if (c > 1 && !wait(kD3 + (c & 1), ((c >> 1) - 1) & 1)) break;    // chunk c - 2 has left the U buffers
             if (wg < 2 && !clear_tail(c, st)) break;
             if (chunk_len(c) < Q && !wait(kTail, 0)) break;
             bool ok = true;
@@ -737,94 +737,106 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
             }
         }
         __syncwarp();
-    } else if (warp == 22 || (!OUT && warp == 20)) {
-        // ---------------------------------------------------------------- decays: lane = 4 tokens
-        // (states only: the two warps take every other chunk)
-        constexpr int STEP = OUT ? 1 : 2;
-        float total[2] = {0.f, 0.f}, ea[2], bias[2];
+    } else if (warp == 22) {
+        // ---------------------------------------------------------------- decays: half a warp a head, a lane 8 tokens
+        const int sl = SAME ? 0 : lane >> 4, l = lane & 15, blk = l >> 2;
+        const int h = un.h[sl];
+        const bool writes = !SAME || lane < 16;
+        const float es = h >= 0 ? expf(a.a_log[h]) * kLog2e : 0.f, bias = h >= 0 ? a.dt_bias[h] : 0.f;
+        float total = 0.f;
+        const uint16_t* dt = static_cast<const uint16_t*>(a.dt) + (size_t)(sg.t0 + 8 * l) * a.ds + (h >= 0 ? h : 0);
+        uint32_t next[8];      // dt_raw, requested a chunk ahead: under load it takes longer than a chunk's decays
+        auto fetch = [&](int len) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            ea[s] = un.h[s] >= 0 ? expf(a.a_log[un.h[s]]) * kLog2e : 0.f;
-            bias[s] = un.h[s] >= 0 ? a.dt_bias[un.h[s]] : 0.f;
-        }
-        const bool two = !SAME && un.h[1] >= 0;
-        const int c0 = !OUT && warp == 20;
-        const uint16_t* dt = static_cast<const uint16_t*>(a.dt) + (size_t)(sg.t0 + c0 * Q + 4 * lane) * a.ds + un.h[0];
-        for (int c = c0; c < nch; c += STEP, dt += STEP * Q * a.ds) {
+            for (int e = 0; e < 8; ++e) next[e] = 8 * l + e < len ? dt[e * a.ds] : 0;
+        };
+        if (nch > 0) fetch(chunk_len(0));
+        for (int c = 0; c < nch; ++c) {
             const int len = chunk_len(c);
-            uint32_t x[4];         // both heads' dt_raw, requested before the wait (heads of a unit are neighbours)
+            float D[8], up[8], dn[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x[e] = 0;
-                if (4 * lane + e < len) {
-                    x[e] = dt[e * a.ds];
-                    if (two) x[e] |= (uint32_t)dt[e * a.ds + 1] << 16;
-                }
-            }
+            for (int e = 0; e < 8; ++e) D[e] = __uint_as_float(next[e] << 16);
+            dt += Q * a.ds;
+            if (c + 1 < nch) fetch(chunk_len(c + 1));
             if (c >= kPrepBufs && !wait(kPrepEmpty + (c & 3), ((c >> 2) - 1) & 1)) break;
-#pragma unroll 1
-            for (int s = 0; s < (SAME ? 1 : 2); ++s) {
-                const int h = s ? un.h[1] : un.h[0];
-                float* pr = slot_prep(c, s);
-                const float es = s ? ea[1] : ea[0];
-                float D[4], la[4];
+            // running sums from the lane's start (its own token with it) and to its end (without)
+            float run = 0.f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float d = __uint_as_float(s ? x[e] & 0xffff0000u : x[e] << 16);
-                    D[e] = step_of(d + (s ? bias[1] : bias[0]));
-                    if (h < 0 || 4 * lane + e >= len) D[e] = 0.f;
-                    la[e] = -es * D[e];
-                    if (la[e] < -150.f) la[e] = -150.f;      // (a NaN stays one)
-                }
-                // a block of 32 tokens is eight lanes: running sums from its start and to its end
-                const float p1 = la[0], p2 = p1 + la[1], p3 = p2 + la[2], p4 = p3 + la[3];
-                const float s3 = la[3], s2 = s3 + la[2], s1 = s2 + la[1];
-                float up = p4, dn = p4;
+            for (int e = 0; e < 8; ++e) {
+                D[e] = step_of(D[e] + bias);
+                if (h < 0 || 8 * l + e >= len) D[e] = 0.f;
+                float la = -es * D[e];
+                if (la < -150.f) la = -150.f;      // (a NaN stays one)
+                dn[e] = la;
+                run += la;
+                up[e] = run;
+            }
+            float back = 0.f;
 #pragma unroll
-                for (int o = 1; o < 8; o <<= 1) {
-                    const float u = __shfl_up_sync(0xffffffffu, up, o, 8), d = __shfl_down_sync(0xffffffffu, dn, o, 8);
-                    if ((lane & 7) >= o) up += u;
-                    if ((lane & 7) + o < 8) dn += d;
+            for (int e = 7; e >= 0; --e) {
+                const float la = dn[e];
+                dn[e] = back;
+                back += la;
+            }
+            // a block of 32 tokens is four lanes
+            float u = run, d = back;
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+                const float x = __shfl_up_sync(0xffffffffu, u, o, 4), y = __shfl_down_sync(0xffffffffu, d, o, 4);
+                if ((lane & 3) >= o) u += x;
+                if ((lane & 3) + o < 4) d += y;
+            }
+            const float block = __shfl_sync(0xffffffffu, u, 3, 4);
+            float before = __shfl_up_sync(0xffffffffu, u, 1, 4), after = __shfl_down_sync(0xffffffffu, d, 1, 4);
+            if ((lane & 3) == 0) before = 0.f;
+            if ((lane & 3) == 3) after = 0.f;
+            const float b0 = __shfl_sync(0xffffffffu, block, 0, 16), b1 = __shfl_sync(0xffffffffu, block, 4, 16);
+            const float b2 = __shfl_sync(0xffffffffu, block, 8, 16), b3 = __shfl_sync(0xffffffffu, block, 12, 16);
+            const float rest = blk == 0 ? (b1 + b2) + b3 : blk == 1 ? b2 + b3 : blk == 2 ? b3 : 0.f;
+            const float sum = (b0 + b1) + (b2 + b3);
+            float* pr = slot_prep(c, sl);
+            if (writes) {
+#pragma unroll
+                for (int e = 0; e < 8; e += 4) {
+                    float4* o = reinterpret_cast<float4*>(pr + 8 * l + e);
+                    float s[4], p[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        s[i] = after + dn[e + i];
+                        p[i] = before + up[e + i];
+                    }
+                    const float* De = D + e;
+                    o[32] = make_float4(De[0] * ex2(rest + s[0]), De[1] * ex2(rest + s[1]), De[2] * ex2(rest + s[2]),
+                                        De[3] * ex2(rest + s[3]));
+                    if (OUT) {
+                        o[0] = make_float4(p[0] - __log2f(De[0]), p[1] - __log2f(De[1]), p[2] - __log2f(De[2]),
+                                           p[3] - __log2f(De[3]));
+                        o[64] = make_float4(p[0], p[1], p[2], p[3]);
+                        o[96] = make_float4(De[0] * ex2(s[0]), De[1] * ex2(s[1]), De[2] * ex2(s[2]), De[3] * ex2(s[3]));
+                    }
                 }
-                const float block = __shfl_sync(0xffffffffu, up, 7, 8);
-                float before = __shfl_up_sync(0xffffffffu, up, 1, 8), after = __shfl_down_sync(0xffffffffu, dn, 1, 8);
-                if ((lane & 7) == 0) before = 0.f;
-                if ((lane & 7) == 7) after = 0.f;
-                const float b0 = __shfl_sync(0xffffffffu, block, 0), b1 = __shfl_sync(0xffffffffu, block, 8);
-                const float b2 = __shfl_sync(0xffffffffu, block, 16), b3 = __shfl_sync(0xffffffffu, block, 24);
-                const int blk = lane >> 3;
-                const float suf = after;
-                after += blk == 0 ? (b1 + b2) + b3 : blk == 1 ? b2 + b3 : blk == 2 ? b3 : 0.f;
-                const float pre[4] = {before + p1, before + p2, before + p3, before + p4};
-                float4* o = reinterpret_cast<float4*>(pr + 4 * lane);
-                o[32] = make_float4(D[0] * ex2(after + s1), D[1] * ex2(after + s2), D[2] * ex2(after + s3), D[3] * ex2(after));
-                if (OUT) {
-                    o[0] = make_float4(pre[0] - __log2f(D[0]), pre[1] - __log2f(D[1]), pre[2] - __log2f(D[2]),
-                                       pre[3] - __log2f(D[3]));
-                    o[64] = make_float4(pre[0], pre[1], pre[2], pre[3]);
-                    o[96] = make_float4(D[0] * ex2(suf + s1), D[1] * ex2(suf + s2), D[2] * ex2(suf + s3), D[3] * ex2(suf));
-                }
-                const float sum = (b0 + b1) + (b2 + b3);
-                if (lane == 0) {
+                if (l == 0) {
                     *reinterpret_cast<float4*>(pr + 512) = make_float4(b0, b1, b2, b3);
                     pr[516] = exp2f(sum);
                 }
-                if (s) total[1] += sum; else total[0] += sum;
             }
+            total += sum;
             arrive_warp(kPrepFull + (c & 3));
         }
-        if (!OUT && lane < 2) ptot[2 * c0 + lane] = lane ? total[1] : total[0];
-    } else if (warp == 23) {
+        if (!OUT && l == 0 && writes) ptot[sl] = total;
+    } else if (warp == 23 || (!OUT && warp == 20)) {
         // ---------------------------------------------------------------- U^T B
+        // (states only: the two warps take every other chunk, each with its accumulator and U buffers)
         if (lane == 0) {
             constexpr uint32_t idU = idesc_bf16(128, NC, 0, 1);
-            for (int c = 0, st = 0; c < nch; ++c, st = st + 1 == NST ? 0 : st + 1) {
+            for (int c = !OUT && warp == 20; c < nch; c += OUT ? 1 : 2) {
+                const int st = c % NST;
                 const uint32_t sbt = smem_u32(smem + L::B + (OUT ? 0 : NB * st) * HALF);
                 bool ok = OUT ? wait1(kBFull, c & 1) : wait1(kFull + st, (c / NST) & 1);
 #pragma unroll 1
                 for (int q = 0; q < 4 && ok; ++q) {
-                    const int k = 4 * c + q, b = k % NU;
-                    if (!wait1(kUFull + b, (k / NU) & 1)) { ok = false; break; }
+                    const int b = OUT ? q & 1 : 2 * (c & 1) + (q & 1);
+                    if (!wait1(kUFull + b, q >> 1)) { ok = false; break; }
                     if (q == 0 && c >= ND && !wait1(kD3Free + c % ND, (c / ND - 1) & 1)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t db = desc_lo(sbt + q * 4096, HALF);
@@ -844,7 +856,7 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
     __syncthreads();
     if (!OUT && tid < (SAME ? 1 : 2)) {
         const int h = tid ? un.h[1] : un.h[0];
-        if (h >= 0) a.decay[(size_t)seg * a.H + h] = exp2f(ptot[tid] + ptot[2 + tid]);
+        if (h >= 0) a.decay[(size_t)seg * a.H + h] = exp2f(ptot[tid]);
     }
     if (*fail && tid == 0) {
         // give copies and products in flight a bounded chance to land before the memory is released
