@@ -401,6 +401,9 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
         const int row = 32 * lq + lane;              // token of the chunk
         const uint32_t lanes = (uint32_t)(lq * 32) << 16;
         constexpr uint32_t PS = SAME ? 0 : 4 * kPrepFloats;
+        const uint32_t ty = tmem + TY + lanes + 64 * wg;
+        const int hy = wg ? un.h[1] : un.h[0];
+        const float dsk = a.d_skip && hy >= 0 ? a.d_skip[hy] : 0.f;
         for (int c = 0; c < nch; ++c) {
             const uint32_t pr = smem_u32(slot_prep(c, 0));
             if (!wait_prep(c) || !clear_tail(c, c & 1)) break;
@@ -483,6 +486,45 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                 arrive_warp(kM + b);
             }
             arrive_warp(kPrepEmpty + (c & 3));
+            // Y
+            const int st = c & 1, len = chunk_len(c);
+            const uint32_t xrow = smem_u32(smem + L::X + (2 * st + wg) * HALF) + sw(row, 0);
+            if (!wait(kXRead + st, (c >> 1) & 1) || !wait(kMX, c & 1)) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int j = 0; j < 8; j += 2) {
+                float v[16];
+                uint4 u[2];
+                tmem_ld16(ty + 8 * j, v);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) u[k] = lds128(xrow ^ ((j + k) << 4));
+                tmem_ld_wait();
+                if (j == 6) {
+                    tc_fence_before();
+                    arrive_warp(kYRead);      // C S of the next chunk may start
+                }
+                // y over x, which nothing else reads any more
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+                    uint32_t o[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 y = fma2(dup(dsk), bf2(w[e]), make_float2(v[8 * k + 2 * e], v[8 * k + 2 * e + 1]));
+                        o[e] = pack_bf16(y.x, y.y);
+                    }
+                    sts128(xrow ^ ((j + k) << 4), o);
+                }
+            }
+            if (len == Q) {
+                fence_async_smem();       // the copy warp stores the tile
+            } else if (row < len && hy >= 0) {
+                const int p0 = SAME ? 64 * wg : 0;
+                __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + ((size_t)(sg.t0 + c * Q + row) * a.H + hy) * a.P + p0;
+#pragma unroll 1
+                for (int k = 0; k < 8 && p0 + 8 * k < a.P; ++k) *reinterpret_cast<uint4*>(y + 8 * k) = lds128(xrow ^ (k << 4));
+            }
+            arrive_warp(kYOut + st);
         }
     } else if (warp < 12) {
         // ---------------------------------------------------------------- U
@@ -538,8 +580,6 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
             copy_state();
         }
         const uint32_t ty = tmem + TY + ((uint32_t)(lq * 32) << 16) + 64 * half;
-        const int hy = half ? un.h[1] : un.h[0];
-        const float dsk = OUT && a.d_skip && hy >= 0 ? a.d_skip[hy] : 0.f;
         for (int c = 0; c < nch; ++c) {
             const uint32_t par = c & 1;
             if (!wait_prep(c)) break;
@@ -589,47 +629,7 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
             tc_fence_before();
             arrive_warp(kD3Free + c % ND);
             arrive_warp(kPrepEmpty + (c & 3));
-            if (OUT) {
-                if (c + 1 < nch) copy_state();      // (C S has read the last copies)
-                const int st = c & 1, len = chunk_len(c);
-                const uint32_t xrow = smem_u32(smem + L::X + (2 * st + half) * HALF) + sw(row, 0);
-                if (!wait(kXRead + st, (c >> 1) & 1) || !wait(kMX, par)) break;
-                tc_fence_after();
-#pragma unroll 1
-                for (int j = 0; j < 8; j += 2) {
-                    float v[16];
-                    uint4 u[2];
-                    tmem_ld16(ty + 8 * j, v);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) u[k] = lds128(xrow ^ ((j + k) << 4));
-                    tmem_ld_wait();
-                    if (j == 6) {
-                        tc_fence_before();
-                        arrive_warp(kYRead);      // C S of the next chunk may start
-                    }
-                    // y over x, which nothing else reads any more
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
-                        uint32_t o[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 y = fma2(dup(dsk), bf2(w[e]), make_float2(v[8 * k + 2 * e], v[8 * k + 2 * e + 1]));
-                            o[e] = pack_bf16(y.x, y.y);
-                        }
-                        sts128(xrow ^ ((j + k) << 4), o);
-                    }
-                }
-                if (len == Q) {
-                    fence_async_smem();       // the copy warp stores the tile
-                } else if (row < len && hy >= 0) {
-                    const int p0 = SAME ? 64 * half : 0;
-                    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + ((size_t)(sg.t0 + c * Q + row) * a.H + hy) * a.P + p0;
-#pragma unroll 1
-                    for (int k = 0; k < 8 && p0 + 8 * k < a.P; ++k) *reinterpret_cast<uint4*>(y + 8 * k) = lds128(xrow ^ (k << 4));
-                }
-                arrive_warp(kYOut + st);
-            }
+            if (OUT && c + 1 < nch) copy_state();      // (C S has read the last copies)
         }
         if (*fail == 0) {
             float* to = h < 0 || p >= a.P ? nullptr
