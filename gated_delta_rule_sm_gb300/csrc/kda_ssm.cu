@@ -67,7 +67,7 @@ double segment_cost(const Costs& k, double work, double longest, bool even, bool
 
 struct Schedule {
     int L, per_row, nseg;
-    bool single;
+    bool single, plan;
     size_t off_seg, off_row, off_decay, off_states, total;
 };
 
@@ -109,7 +109,8 @@ Schedule make_schedule(const SsmShape& s, bool varlen, const Costs& k) {
     w.per_row = varlen ? 0 : (s.T + w.L - 1) / w.L;
     w.nseg = varlen ? (w.single ? s.rows : s.rows + s.TT / w.L) : s.rows * w.per_row;
     size_t o = 0;
-    if (varlen) {
+    w.plan = varlen && (!w.single || s.rows > kSsmOwnRows);
+    if (w.plan) {
         w.off_seg = o; o = up256(o + sizeof(SsmSeg) * (size_t)w.nseg);
         w.off_row = o; o = up256(o + sizeof(int32_t) * ((size_t)s.rows + 1));
     }
@@ -245,7 +246,8 @@ __global__ void __launch_bounds__(256, NJ <= 2 ? 3 : NJ == 4 ? 2 : 1) ssm_simt_k
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int slice = lane & 7, pc = warp * 4 + (lane >> 3);
     const int h = blockIdx.y, p0 = blockIdx.z * kSimtCols, p = p0 + pc;
-    const SsmSeg sg = ssm_segment(a, blockIdx.x);
+    __shared__ SsmSeg found;
+    const SsmSeg sg = ssm_segment(a, blockIdx.x, &found);
     if (sg.n < 0) return;
     if (!OUT) {   // the last segment's end state comes from the output pass
         int first;
@@ -437,7 +439,7 @@ kda_status kda_ssm_fwd(const kda_ssm_dims* dims, const void* x, const void* dt_r
     a.L = w.L; a.per_row = w.per_row; a.nseg = w.nseg; a.single = w.single;
     st = status_ptr(&a.status);
     if (st != KDA_OK) return st;
-    if (cu_seqlens) {
+    if (w.plan) {
         SsmSeg* seg = reinterpret_cast<SsmSeg*>(ws + w.off_seg);
         int32_t* row = reinterpret_cast<int32_t*>(ws + w.off_row);
         a.seg = seg;

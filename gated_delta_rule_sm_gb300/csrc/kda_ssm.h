@@ -20,15 +20,38 @@ struct SsmArgs {
     float* ST;
     // schedule: rows cut into segments of L tokens; nseg entries at most
     int L, per_row, nseg, single;
-    const SsmSeg* seg;       // packed documents: the planner's table; nullptr: segment i is i % per_row of row i / per_row
+    const SsmSeg* seg;       // packed documents: the planner's table; nullptr: document i, or the (i % per_row)-th of row i / per_row
     const int32_t* row_seg;  // [rows + 1] first segment of each row (with seg)
     float* states;           // [nseg, H, N, P] end states from zero, then the entering states (not single)
     float* decay;            // [nseg, H] product of the decays of a segment (not single)
     int* status;
 };
 
-__device__ __forceinline__ SsmSeg ssm_segment(const SsmArgs& a, int i) {
+// Documents that are not cut, and not more of them than this, need no planner: every CTA checks the offsets itself,
+// two loads a thread, which saves a launch (12 documents of 16384 tokens in all: 155 -> 150 us; above, each
+// CTA's reading costs more than the one planner's).  Offsets that break the contract are recorded and leave
+// every row empty, so that its state passes through.  Not inlined: there its registers cost the tensor-core
+// kernel's loops 7 %.
+constexpr int kSsmOwnRows = 1024;
+static __device__ __noinline__ void ssm_document(const SsmArgs& a, int i, SsmSeg* out) {
+    bool bad = threadIdx.x == 0 && (a.cu[0] != 0 || a.cu[a.rows] != a.TT);
+    for (int n = threadIdx.x; n < a.rows; n += blockDim.x) bad |= a.cu[n + 1] < a.cu[n];
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) {
+        if (bad) record_error(a.status, KDA_ERR_INVALID_ARG);
+        const SsmSeg s = {i, bad ? 0 : a.cu[i], bad ? 0 : a.cu[i + 1], 0};
+        *out = s;
+    }
+    __syncthreads();
+}
+
+// All threads of a CTA call it; tmp: in shared memory.
+__device__ __forceinline__ SsmSeg ssm_segment(const SsmArgs& a, int i, SsmSeg* tmp) {
     if (a.seg) return a.seg[i];
+    if (a.cu) {
+        ssm_document(a, i, tmp);
+        return *tmp;
+    }
     SsmSeg s;
     s.n = i / a.per_row;
     s.k = i - s.n * a.per_row;
@@ -39,6 +62,10 @@ __device__ __forceinline__ SsmSeg ssm_segment(const SsmArgs& a, int i) {
 }
 // Segments of row n, and the first of them.
 __device__ __forceinline__ int ssm_row_segments(const SsmArgs& a, int n, int* first) {
+    if (a.cu && !a.seg) {
+        *first = n;
+        return 1;
+    }
     if (a.seg) {
         *first = a.row_seg[n];
         return a.row_seg[n + 1] - *first;

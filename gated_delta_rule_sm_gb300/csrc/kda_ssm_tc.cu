@@ -239,7 +239,7 @@ __device__ __forceinline__ float* prep_slot(uint8_t* smem, int c, int s) {
 
 template <int NB, bool SAME, bool OUT>
 __global__ void __launch_bounds__(kThreads, 1)
-ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mb,
+ssm_tc_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mb,
               const __grid_constant__ CUtensorMap mc, const __grid_constant__ CUtensorMap my) {
     using L = Lay<NB, OUT>;
     constexpr int NC = 64 * NB;                      // padded state columns
@@ -249,7 +249,7 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
     constexpr uint32_t D0 = OUT ? TD : 192;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int seg = blockIdx.x;
-    const SsmSeg sg = ssm_segment(a, seg);
+    const SsmSeg sg = ssm_segment(a, seg, reinterpret_cast<SsmSeg*>(smem + L::BAR + 8 * kBars + 16));
     if (sg.n < 0) return;
     if (!OUT) {   // the last segment's end state comes from the output pass
         int first;
@@ -432,54 +432,44 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
                     tmem_st16(tg, m);
                     tmem_st16(tg + 16, m);
                 } else {
-                float v[32];
-                tmem_ld16(tg, v);
-                tmem_ld16(tg + 16, v + 16);
-                tmem_ld_wait();
+                    const bool diag = J == lq;
 #pragma unroll 1
-                for (int s = 0; s < (SAME ? 1 : 2); ++s) {
-                    const uint32_t ps = pr + s * PS;
-                    if (J == lq) {           // the diagonal block: an exponential each, columns up to the row
-#pragma unroll
-                        for (int c0 = 0; c0 < 32; c0 += 16) {
-                            float4 l4[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) l4[i] = lds4f(ps + 4 * (32 * J + c0 + 4 * i));
+                    for (int c0 = 0; c0 < 32; c0 += 16) {
+                        float v[16];
+                        tmem_ld16(tg + c0, v);
+                        uint32_t pc = pr + 4 * ((diag ? 0 : 384) + 32 * J + c0);
+                        tmem_ld_wait();
+#pragma unroll 1
+                        for (int s = 0; s < (SAME ? 1 : 2); ++s, pc += PS) {
                             uint32_t m[8];
+                            float4 k[4];
 #pragma unroll
-                            for (int i = 0; i < 16; i += 4) {
-                                const float4 k = l4[i >> 2];
-                                const float2 x0 = fma2(make_float2(k.x, k.y), dup(-1.f), dup(s ? lt[1] : lt[0]));
-                                const float2 x1 = fma2(make_float2(k.z, k.w), dup(-1.f), dup(s ? lt[1] : lt[0]));
-                                const int j = c0 + i;
-                                const float2 e0 = mul2(make_float2(v[j], v[j + 1]), make_float2(ex2(x0.x), ex2(x0.y)));
-                                const float2 e1 = mul2(make_float2(v[j + 2], v[j + 3]), make_float2(ex2(x1.x), ex2(x1.y)));
-                                m[i >> 1] = pack_bf16(j <= lane ? e0.x : 0.f, j + 1 <= lane ? e0.y : 0.f);
-                                m[(i >> 1) + 1] = pack_bf16(j + 2 <= lane ? e1.x : 0.f, j + 3 <= lane ? e1.y : 0.f);
-                            }
-                            tmem_st8(tg + c0 + 8 * s, m);
-                        }
-                    } else {                 // a factor of the column to the block's end, one of the row from there
-                        const float2 rf = dup(ex2(b ? (s ? lt[1] : lt[0]) : (s ? lj[1] : lj[0])));
+                            for (int i = 0; i < 4; ++i) k[i] = lds4f(pc + 16 * i);
+                            if (diag) {          // an exponential each, columns up to the row
+                                const float2 l = dup(s ? lt[1] : lt[0]);
 #pragma unroll
-                        for (int c0 = 0; c0 < 32; c0 += 16) {
-                            float4 f4[4];
+                                for (int i = 0; i < 4; ++i) {
+                                    const float2 x0 = fma2(make_float2(k[i].x, k[i].y), dup(-1.f), l);
+                                    const float2 x1 = fma2(make_float2(k[i].z, k[i].w), dup(-1.f), l);
+                                    const float2 e0 = mul2(make_float2(v[4 * i], v[4 * i + 1]), make_float2(ex2(x0.x), ex2(x0.y)));
+                                    const float2 e1 = mul2(make_float2(v[4 * i + 2], v[4 * i + 3]), make_float2(ex2(x1.x), ex2(x1.y)));
+                                    const int j = c0 + 4 * i;
+                                    m[2 * i] = pack_bf16(j <= lane ? e0.x : 0.f, j + 1 <= lane ? e0.y : 0.f);
+                                    m[2 * i + 1] = pack_bf16(j + 2 <= lane ? e1.x : 0.f, j + 3 <= lane ? e1.y : 0.f);
+                                }
+                            } else {             // a factor of the column to the block's end, one of the row from there
+                                const float2 rf = dup(ex2(b ? (s ? lt[1] : lt[0]) : (s ? lj[1] : lj[0])));
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) f4[i] = lds4f(ps + 4 * (384 + 32 * J + c0 + 4 * i));
-                            uint32_t m[8];
-#pragma unroll
-                            for (int i = 0; i < 16; i += 4) {
-                                const float4 k = f4[i >> 2];
-                                const int j = c0 + i;
-                                const float2 e0 = mul2(make_float2(v[j], v[j + 1]), mul2(make_float2(k.x, k.y), rf));
-                                const float2 e1 = mul2(make_float2(v[j + 2], v[j + 3]), mul2(make_float2(k.z, k.w), rf));
-                                m[i >> 1] = pack_bf16(e0.x, e0.y);
-                                m[(i >> 1) + 1] = pack_bf16(e1.x, e1.y);
+                                for (int i = 0; i < 4; ++i) {
+                                    const float2 e0 = mul2(make_float2(v[4 * i], v[4 * i + 1]), mul2(make_float2(k[i].x, k[i].y), rf));
+                                    const float2 e1 = mul2(make_float2(v[4 * i + 2], v[4 * i + 3]), mul2(make_float2(k[i].z, k[i].w), rf));
+                                    m[2 * i] = pack_bf16(e0.x, e0.y);
+                                    m[2 * i + 1] = pack_bf16(e1.x, e1.y);
+                                }
                             }
                             tmem_st8(tg + c0 + 8 * s, m);
                         }
                     }
-                }
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -576,12 +566,10 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
             fence_async_smem();
             arrive_warp(kSB);
         };
-        if (OUT && nch > 0) {
-            copy_state();
-        }
         const uint32_t ty = tmem + TY + ((uint32_t)(lq * 32) << 16) + 64 * half;
         for (int c = 0; c < nch; ++c) {
             const uint32_t par = c & 1;
+            if (OUT) copy_state();      // (C S has read the last copies)
             if (!wait_prep(c)) break;
             if (OUT) {     // C S scaled by exp(l_t)
                 const uint32_t pr = smem_u32(slot_prep(c, half));
@@ -629,7 +617,6 @@ ssm_tc_kernel(SsmArgs a, const __grid_constant__ CUtensorMap mx, const __grid_co
             tc_fence_before();
             arrive_warp(kD3Free + c % ND);
             arrive_warp(kPrepEmpty + (c & 3));
-            if (OUT && c + 1 < nch) copy_state();      // (C S has read the last copies)
         }
         if (*fail == 0) {
             float* to = h < 0 || p >= a.P ? nullptr

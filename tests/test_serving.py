@@ -197,6 +197,65 @@ def test_scan_bad_device_offsets_are_reported(offsets):
     assert bool(torch.isnan(co.float()).all()) and bool(torch.isnan(hist.float()).all())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("init", [True, False])
+def test_scan_of_long_documents_in_segments(dtype, init):
+    """Documents of many segments, of a segment and a token, and of none, side by side."""
+    lengths = [2600, 0, 5, 1024, 129, 2817, 1, 513]
+    off = [0, *np.cumsum(lengths).tolist()]
+    i, g = ssm_inputs(37, (1, off[-1]), 4, 2, 64, 16, dtype)
+    S0 = randn(g, len(lengths), 4, 64, 16).to(DEV) if init else None
+    y, S = run_scan(i, initial_state=S0, output_final_state=True, cu_seqlens=torch.tensor(off, dtype=torch.int32, device=DEV))
+    check_scan(i, off, S0, y, S, dtype, dtype == "bf16")
+
+
+def test_scan_of_many_chunks_to_a_segment():
+    """Enough heads and tokens that a segment is longer than any ring of buffers.  With so many values the bound of
+    y is taken for each: its storage rounding, and one rounding to bf16 (2^-9, doubled for the fp32 sums) of each
+    token's factor inside a chunk of 128."""
+    T, H, N, P, Q = 16300, 32, 128, 8, 128
+    i, g = ssm_inputs(41, (1, T), H, 1, N, P, "bf16")
+    S0 = randn(g, 1, H, N, P).to(DEV)
+    y, S = run_scan(i, initial_state=S0, output_final_state=True)
+    x, dt, b, c = (ref.d(i[n][0]) for n in ("x", "dt_raw", "b", "c"))
+    ry, rS = ref.ssm(x, dt, b, c, i["a_log"], i["dt_bias"], i["d_skip"], [0, T], S0)
+    delta = ref.softplus(dt + ref.d(i["dt_bias"]))
+    la = -torch.exp(ref.d(i["a_log"])) * delta
+    terms = torch.zeros_like(ry)
+    for t in range(0, T, Q):
+        e = min(T, t + Q)
+        cum = la[t:e].cumsum(0).t()                                                # [H, q]
+        m = (c[t:e, 0] @ b[t:e, 0].t()).abs() * torch.exp(cum[:, :, None] - cum[:, None, :]).tril()
+        terms[t:e] = ((m * delta[t:e].t()[:, None, :]) @ x[t:e].abs().transpose(0, 1)).transpose(0, 1)
+    err = (ref.d(y[0]) - ry).abs()
+    assert bool((err <= 2.0 ** -8 * (ry.abs() + terms)).all()), float((err / (ry.abs() + terms)).max())
+    assert rel_err(S, rS.numpy(), "fp32") <= SCAN
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_scan_of_more_documents_than_a_block_has_threads(dtype):
+    lengths = [(0, 1, 3, 2, 17)[n % 5] for n in range(1100)]
+    off = [0, *np.cumsum(lengths).tolist()]
+    i, g = ssm_inputs(43, (1, off[-1]), 2, 1, 16, 8, dtype)
+    S0 = randn(g, 1100, 2, 16, 8).to(DEV)
+    y, S = run_scan(i, initial_state=S0, output_final_state=True, cu_seqlens=torch.tensor(off, dtype=torch.int32, device=DEV))
+    check_scan(i, off, S0, y, S, dtype, dtype == "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,T", [(3, 6000), (1100, 6000)])
+def test_scan_bad_device_offsets_of_long_and_many_documents(dtype, rows, T):
+    i, g = ssm_inputs(47, (1, T), 4, 2, 16, 8, dtype)
+    S0 = randn(g, rows, 4, 16, 8).to(DEV)
+    out = torch.full_like(i["x"], float("nan"))
+    cu = torch.linspace(0, T, rows + 1).to(torch.int32)
+    cu[1] = cu[2] + 1
+    _, S = kda.ssm_scan(*[i[n] for n in ARGS], cu_seqlens=cu.to(DEV), initial_state=S0, output_final_state=True, out=out)
+    torch.cuda.synchronize()
+    assert kda.device_status() == 1
+    assert bool(torch.isnan(out.float()).all()) and torch.equal(S, S0)
+
+
 def test_scan_is_repeatable_and_runs_on_another_stream():
     i, g = ssm_inputs(23, (1, 3000), 2, 1, 128, 64, "bf16")
     S0 = randn(g, 1, 2, 128, 64).to(DEV)
