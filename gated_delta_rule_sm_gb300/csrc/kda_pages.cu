@@ -8,8 +8,9 @@
 //            more CTA); separate output arrays filled from the inputs;
 //   assign   ranks of the pages, tile by tile, from the counts before it: the page of each rank;
 //   apply    rows, references and the pages' data.
-// Three short launches: a rank needs the counts of every tile before it, and a grid-wide wait inside one
-// kernel would cost about what a launch does.  Copies are bound by memory.
+// A rank needs the counts of every tile before it, and a grid-wide wait inside one kernel would cost about what
+// a launch does.  Up to kDirectTiles tiles the first two passes are one launch: each tile's CTA counts all
+// tiles before its own, which it reads from L2.  Copies are bound by memory.
 #include <limits.h>
 #include <string.h>
 
@@ -23,12 +24,14 @@ namespace {
 
 constexpr int kThreads = 1024, kPer = 4, kTile = kThreads * kPer;
 constexpr int kCopyThreads = 256, kCopyUnroll = 4;
-constexpr int64_t kCopyBytes = 16 * kCopyThreads * kCopyUnroll;   // of a page, per work item of a copying CTA
+// A page is copied in parts, each by a team of threads, 64 bytes a thread: a CTA, or a warp where that is the
+// whole page (SMALL_FIGURES).
+constexpr int64_t kPartBytes = 16 * kCopyUnroll;
 
 enum Mode { kFork, kExtend, kCompact };
 
 struct PageArgs {
-    int layers, P, S, M, pt, n, tiles, mode;
+    int layers, P, S, M, pt, n, tiles, mode, direct, team;
     int64_t page_bytes, layer_stride;
     uint8_t* pool;
     const int32_t *table, *lengths, *refs, *ra, *rb;   // ra, rb: the requests (parents, children | seqs, new lengths)
@@ -113,16 +116,19 @@ __device__ __forceinline__ void copy_ints(int32_t* dst, const int32_t* src, size
         dst[i] = src[i];
 }
 
+// Output arrays of their own filled from the inputs, and the requests' CTA (true there: nothing is left to do).
+__device__ __forceinline__ bool requests(const PageArgs& a) {
+    if (a.mode == kCompact) return false;      // it has no requests, and writes its outputs in full by itself
+    copy_ints(a.table_o, a.table, (size_t)a.S * a.M);
+    copy_ints(a.lengths_o, a.lengths, a.S);
+    copy_ints(a.refs_o, a.refs, a.P);
+    if ((int)blockIdx.x < a.tiles) return false;
+    request_needs(a);
+    return true;
+}
+
 __global__ void __launch_bounds__(kThreads) pages_count_kernel(PageArgs a) {
-    if (a.mode != kCompact) {   // compaction writes its outputs in full by itself
-        copy_ints(a.table_o, a.table, (size_t)a.S * a.M);
-        copy_ints(a.lengths_o, a.lengths, a.S);
-        copy_ints(a.refs_o, a.refs, a.P);
-    }
-    if ((int)blockIdx.x == a.tiles) {
-        if (a.mode != kCompact) request_needs(a);
-        return;
-    }
+    if (requests(a)) return;
     const bool live = a.mode == kCompact;
     int cnt = 0;
 #pragma unroll
@@ -135,19 +141,46 @@ __global__ void __launch_bounds__(kThreads) pages_count_kernel(PageArgs a) {
     if (threadIdx.x == 0) a.counts[blockIdx.x] = total;
 }
 
-// Sum of counts[from .. to) over the CTA.
-__device__ int count_sum(const PageArgs& a, int from, int to) {
-    int s = 0, total;
-    for (int i = from + threadIdx.x; i < to; i += kThreads) s += a.counts[i];
-    block_scan<int>(s, &total);
-    return total;
+// Free (live) pages of the tiles before the CTA's, and (all) of all tiles.
+__device__ int pages_before(const PageArgs& a, int tile, bool live, int* all) {
+    const int upto = all ? a.tiles : tile;
+    int before = 0, sum = 0;
+    if (a.direct) {
+        const int64_t own = (int64_t)tile * kTile, end = (int64_t)upto * kTile < a.P ? (int64_t)upto * kTile : a.P;
+        for (int64_t p0 = 0; p0 < end; p0 += kTile) {
+            int r[kPer];
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                const int64_t p = p0 + e * kThreads + threadIdx.x;
+                r[e] = p < end ? a.refs[p] : 0;
+            }
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                const int64_t p = p0 + e * kThreads + threadIdx.x;
+                const int hit = p < end && (r[e] > 0) == live;
+                sum += hit;
+                before += hit && p < own;
+            }
+        }
+    } else {
+        for (int i = threadIdx.x; i < upto; i += kThreads) {
+            const int c = a.counts[i];
+            sum += c;
+            before += i < tile ? c : 0;
+        }
+    }
+    long long total;
+    block_scan<long long>((long long)sum << 32 | before, &total);
+    if (all) *all = (int)(total >> 32);
+    return (int)total;
 }
 
 __global__ void __launch_bounds__(kThreads) pages_assign_kernel(PageArgs a) {
-    const int base = count_sum(a, 0, blockIdx.x);
+    if (a.direct && requests(a)) return;
     const bool live = a.mode == kCompact;
-    const int all = live ? base + count_sum(a, blockIdx.x, a.tiles) : 0;
-    const int want = live ? 0 : a.head[0];
+    int all = 0;
+    const int base = pages_before(a, blockIdx.x, live, live ? &all : nullptr);
+    const int want = live ? 0 : a.direct ? a.P : a.head[0];
     bool hit[kPer];
     int cnt = 0;
     const long long p0 = (long long)blockIdx.x * kTile + threadIdx.x * kPer;
@@ -194,49 +227,58 @@ __global__ void __launch_bounds__(kThreads) pages_assign_kernel(PageArgs a) {
     }
 }
 
-// One item of a page copy: kCopyBytes from byte `at` of the page.
+// A team's place in the grid.
+struct Team {
+    int size, rank;          // threads, this thread's number
+    int64_t first, step;     // the first work item, and from one to the next
+};
+__device__ __forceinline__ Team team_of(int size) {
+    const int per = kCopyThreads / size;
+    return {size, (int)threadIdx.x % size, (int64_t)blockIdx.x * per + threadIdx.x / size, (int64_t)gridDim.x * per};
+}
+__host__ __device__ __forceinline__ int64_t parts_of(int64_t page_bytes, int team) {
+    return (page_bytes + kPartBytes * team - 1) / (kPartBytes * team);
+}
+
+// Part k of a page.
 template <typename V>
-__device__ __forceinline__ void copy_part(uint8_t* dst, const uint8_t* src, int64_t at, int64_t end) {
+__device__ __forceinline__ void copy_part(const Team& t, uint8_t* dst, const uint8_t* src, int64_t k, int64_t page_bytes) {
     constexpr int U = kCopyUnroll * 16 / sizeof(V) > 16 ? 16 : kCopyUnroll * 16 / sizeof(V);
-    const int64_t stop = at + kCopyBytes < end ? at + kCopyBytes : end;
-    for (int64_t o = at + threadIdx.x * sizeof(V); o < stop; o += (int64_t)U * kCopyThreads * sizeof(V)) {
+    const int64_t at = k * kPartBytes * t.size, step = t.size * (int64_t)sizeof(V);
+    const int64_t stop = at + kPartBytes * t.size < page_bytes ? at + kPartBytes * t.size : page_bytes;
+    for (int64_t o = at + t.rank * sizeof(V); o < stop; o += U * step) {
         V v[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t i = o + (int64_t)u * kCopyThreads * sizeof(V);
-            if (i < stop) v[u] = __ldcs(reinterpret_cast<const V*>(src + i));
-        }
+        for (int u = 0; u < U; ++u)
+            if (o + u * step < stop) v[u] = __ldcs(reinterpret_cast<const V*>(src + o + u * step));
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t i = o + (int64_t)u * kCopyThreads * sizeof(V);
-            if (i < stop) __stcs(reinterpret_cast<V*>(dst + i), v[u]);
-        }
+        for (int u = 0; u < U; ++u)
+            if (o + u * step < stop) __stcs(reinterpret_cast<V*>(dst + o + u * step), v[u]);
     }
 }
 
-__device__ __forceinline__ int64_t parts_of(int64_t page_bytes) { return (page_bytes + kCopyBytes - 1) / kCopyBytes; }
-
 template <typename V>
 __global__ void __launch_bounds__(kCopyThreads) pages_fork_kernel(PageArgs a) {
-    const int64_t parts = parts_of(a.page_bytes), per = parts * a.layers, items = per * a.n;
-    for (int64_t w = blockIdx.x; w < items; w += gridDim.x) {
+    const Team t = team_of(a.team);
+    const int64_t parts = parts_of(a.page_bytes, t.size), per = parts * a.layers, items = per * a.n;
+    for (int64_t w = t.first; w < items; w += t.step) {
         const int i = (int)(w / per);
         const int64_t rest = w - i * per;
         const int need = a.need[i], rank = a.rank[i];
         const bool ok = need == 0 || (need > 0 && rank < a.head[1]);
-        if (rest == 0 && threadIdx.x == 0) a.ok[i] = ok;
+        if (rest == 0 && t.rank == 0) a.ok[i] = ok;
         if (!ok) continue;
         const int s = a.ra[i], ch = a.rb[i], len = a.lengths[s];
         const int full = len > 0 ? len / a.pt : 0;
         const int fresh = need > 0 ? a.list[rank] : -1;
         const int32_t* row = a.table + (size_t)s * a.M;
         if (rest == 0) {
-            for (int j = threadIdx.x; j < a.M; j += kCopyThreads) {
+            for (int j = t.rank; j < a.M; j += t.size) {
                 const int p = row[j];
                 a.table_o[(size_t)ch * a.M + j] = j < full ? p : (j == full && need > 0 ? fresh : -1);
                 if (j < full && page_ok(a, p)) atomicAdd(&a.refs_o[p], 1);
             }
-            if (threadIdx.x == 0) {
+            if (t.rank == 0) {
                 a.lengths_o[ch] = len;
                 if (need > 0) a.refs_o[fresh] = 1;
             }
@@ -244,8 +286,7 @@ __global__ void __launch_bounds__(kCopyThreads) pages_fork_kernel(PageArgs a) {
         if (need > 0) {
             const int l = (int)(rest / parts);
             uint8_t* base = a.pool + l * a.layer_stride;
-            copy_part<V>(base + fresh * a.page_bytes, base + row[full] * a.page_bytes, (rest - l * parts) * kCopyBytes,
-                         a.page_bytes);
+            copy_part<V>(t, base + fresh * a.page_bytes, base + row[full] * a.page_bytes, rest - l * parts, a.page_bytes);
         }
     }
 }
@@ -308,19 +349,19 @@ __global__ void __launch_bounds__(kCopyThreads) pages_compact_kernel(PageArgs a)
         }
         a.table_o[i] = p;
     }
-    const int64_t parts = parts_of(a.page_bytes), per = parts * a.layers, items = per * moves;
-    for (int64_t w = blockIdx.x; w < items; w += gridDim.x) {
+    const Team t = team_of(a.team);
+    const int64_t parts = parts_of(a.page_bytes, t.size), per = parts * a.layers, items = per * moves;
+    for (int64_t w = t.first; w < items; w += t.step) {
         const int k = (int)(w / per);
         const int64_t rest = w - k * per;
         const int l = (int)(rest / parts);
         uint8_t* base = a.pool + l * a.layer_stride;
-        copy_part<V>(base + a.list[k] * a.page_bytes, base + a.movers[k] * a.page_bytes, (rest - l * parts) * kCopyBytes,
-                     a.page_bytes);
+        copy_part<V>(t, base + a.list[k] * a.page_bytes, base + a.movers[k] * a.page_bytes, rest - l * parts, a.page_bytes);
     }
 }
 
 struct CopyArgs {
-    int layers, n, src_pages, dst_pages;
+    int layers, n, src_pages, dst_pages, team;
     int64_t page_bytes, src_stride, dst_stride;
     uint8_t* dst_pool;
     const uint8_t* src_pool;
@@ -329,15 +370,16 @@ struct CopyArgs {
 
 template <typename V>
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(CopyArgs a) {
-    const int64_t parts = parts_of(a.page_bytes), per = parts * a.layers, items = per * a.n;
-    for (int64_t w = blockIdx.x; w < items; w += gridDim.x) {
+    const Team t = team_of(a.team);
+    const int64_t parts = parts_of(a.page_bytes, t.size), per = parts * a.layers, items = per * a.n;
+    for (int64_t w = t.first; w < items; w += t.step) {
         const int i = (int)(w / per);
         const int64_t rest = w - i * per;
         const int s = a.src[i], d = a.dst[i];
         if ((unsigned)s >= (unsigned)a.src_pages || (unsigned)d >= (unsigned)a.dst_pages) continue;
         const int l = (int)(rest / parts);
-        copy_part<V>(a.dst_pool + l * a.dst_stride + d * a.page_bytes, a.src_pool + l * a.src_stride + s * a.page_bytes,
-                     (rest - l * parts) * kCopyBytes, a.page_bytes);
+        copy_part<V>(t, a.dst_pool + l * a.dst_stride + d * a.page_bytes, a.src_pool + l * a.src_stride + s * a.page_bytes,
+                     rest - l * parts, a.page_bytes);
     }
 }
 
@@ -350,6 +392,13 @@ int access_bytes(const void* base, int64_t page_bytes, int64_t stride) {
 int copy_grid(int64_t items) {
     const int64_t most = 8 * 152;   // eight CTAs of 256 threads fill an SM
     return (int)(items < 1 ? 1 : items < most ? items : most);
+}
+
+int team_size(int64_t page_bytes) { return page_bytes <= 32 * kPartBytes ? 32 : kCopyThreads; }
+// CTAs for the copies of n pages of every layer.
+int pages_grid(int64_t page_bytes, int team, int layers, int64_t n) {
+    const int per = kCopyThreads / team;
+    return copy_grid((parts_of(page_bytes, team) * layers * n + per - 1) / per);
 }
 
 int tiles_of(int pages) { return (int)(((int64_t)pages + kTile - 1) / kTile); }
@@ -376,6 +425,7 @@ PageArgs page_args(const kda_pages_dims* d, int n, void* ws, int mode) {
     a.layers = d->layers; a.P = d->num_pages; a.S = d->num_seqs; a.M = d->max_pages; a.pt = d->page_tokens;
     a.n = n; a.tiles = tiles_of(d->num_pages); a.mode = mode;
     a.page_bytes = d->page_bytes; a.layer_stride = d->layers > 1 ? d->layer_stride : 0;
+    a.team = team_size(d->page_bytes);
     if (ws) {
         int32_t* w = static_cast<int32_t*>(ws);
         a.head = w; w += 64;
@@ -393,13 +443,20 @@ bool ws_ok(const kda_pages_dims* d, int n, void* ws, size_t bytes) {
     return ws && bytes >= pages_ws(d, n) && reinterpret_cast<uintptr_t>(ws) % 256 == 0;
 }
 
-cudaError_t run_plan(const PageArgs& a, cudaStream_t stream) {
-    timing_pre(stream, K_PAGES_COUNT);
-    pages_count_kernel<<<a.tiles + 1, kThreads, 0, stream>>>(a);
-    timing_post(stream);
-    if (cudaError_t e = cudaGetLastError()) return e;
+// Tiles that the passes' one launch is quicker for (DIRECT_FIGURES).
+constexpr int kDirectTiles = 16;
+
+cudaError_t run_plan(PageArgs a, cudaStream_t stream) {
+    a.direct = a.tiles <= kDirectTiles;
+    const int requests = a.mode != kCompact;
+    if (!a.direct) {
+        timing_pre(stream, K_PAGES_COUNT);
+        pages_count_kernel<<<a.tiles + requests, kThreads, 0, stream>>>(a);
+        timing_post(stream);
+        if (cudaError_t e = cudaGetLastError()) return e;
+    }
     timing_pre(stream, K_PAGES_ASSIGN);
-    pages_assign_kernel<<<a.tiles, kThreads, 0, stream>>>(a);
+    pages_assign_kernel<<<a.tiles + (a.direct ? requests : 0), kThreads, 0, stream>>>(a);
     timing_post(stream);
     return cudaGetLastError();
 }
@@ -451,7 +508,8 @@ kda_status kda_pages_copy(int layers, int64_t page_bytes, void* dst_pool, int64_
     a.dst_pool = static_cast<uint8_t*>(dst_pool); a.src_pool = static_cast<const uint8_t*>(src_pool);
     a.src = src; a.dst = dst;
     const int w1 = access_bytes(dst_pool, page_bytes, a.dst_stride), w2 = access_bytes(src_pool, page_bytes, a.src_stride);
-    const int grid = copy_grid((page_bytes + kCopyBytes - 1) / kCopyBytes * layers * n);
+    a.team = team_size(page_bytes);
+    const int grid = pages_grid(page_bytes, a.team, layers, n);
     timing_pre(stream, K_PAGES_COPY);
     KDA_PAGES_LAUNCH(pages_copy_kernel, grid, a, (w1 < w2 ? w1 : w2), stream);
     timing_post(stream);
@@ -473,7 +531,7 @@ kda_status kda_pages_fork(const kda_pages_dims* dims, void* pool, const int32_t*
     a.table_o = table_out; a.lengths_o = lengths_out; a.refs_o = refs_out; a.ok = ok;
     if (n == 0) return run_fill(a, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
     if (run_plan(a, stream) != cudaSuccess) return KDA_ERR_CUDA;
-    const int grid = copy_grid((a.page_bytes + kCopyBytes - 1) / kCopyBytes * a.layers * n);
+    const int grid = pages_grid(a.page_bytes, a.team, a.layers, n);
     timing_pre(stream, K_PAGES_APPLY);
     KDA_PAGES_LAUNCH(pages_fork_kernel, grid, a, access_bytes(pool, a.page_bytes, a.layer_stride), stream);
     timing_post(stream);
@@ -529,7 +587,7 @@ kda_status kda_pages_compact(const kda_pages_dims* dims, void* pool, const int32
     a.table = table; a.refs = refs; a.table_o = table_out; a.refs_o = refs_out; a.map = page_map;
     if (run_plan(a, stream) != cudaSuccess) return KDA_ERR_CUDA;
     // the number of moves is known on the device only: at most half the pages
-    const int grid = copy_grid((a.page_bytes + kCopyBytes - 1) / kCopyBytes * a.layers * ((a.P + 1) / 2));
+    const int grid = pages_grid(a.page_bytes, a.team, a.layers, (a.P + 1) / 2);
     timing_pre(stream, K_PAGES_APPLY);
     KDA_PAGES_LAUNCH(pages_compact_kernel, grid, a, access_bytes(pool, a.page_bytes, a.layer_stride), stream);
     timing_post(stream);
