@@ -24,8 +24,9 @@ namespace {
 
 constexpr int kThreads = 1024, kPer = 4, kTile = kThreads * kPer;
 constexpr int kCopyThreads = 256, kCopyUnroll = 4;
-// A page is copied in parts, each by a team of threads, 64 bytes a thread: a CTA, or a warp where that is the
-// whole page (SMALL_FIGURES).
+// A page is copied in parts, each by a team of threads, 64 bytes a thread: a warp for pages up to 8 KB, so that
+// many small pages are in flight at once, else a CTA (16384 pages compacted: pages of 4 KB 12.1 us by warps,
+// 16.1 by CTAs, of 8 KB 17.0 and 19.6; four layers of 16 KB 88.2 and 87.5).
 constexpr int64_t kPartBytes = 16 * kCopyUnroll;
 
 enum Mode { kFork, kExtend, kCompact };
@@ -394,7 +395,7 @@ int copy_grid(int64_t items) {
     return (int)(items < 1 ? 1 : items < most ? items : most);
 }
 
-int team_size(int64_t page_bytes) { return page_bytes <= 32 * kPartBytes ? 32 : kCopyThreads; }
+int team_size(int64_t page_bytes) { return page_bytes <= 8192 ? 32 : kCopyThreads; }
 // CTAs for the copies of n pages of every layer.
 int pages_grid(int64_t page_bytes, int team, int layers, int64_t n) {
     const int per = kCopyThreads / team;
@@ -443,8 +444,9 @@ bool ws_ok(const kda_pages_dims* d, int n, void* ws, size_t bytes) {
     return ws && bytes >= pages_ws(d, n) && reinterpret_cast<uintptr_t>(ws) % 256 == 0;
 }
 
-// Tiles that the passes' one launch is quicker for (DIRECT_FIGURES).
-constexpr int kDirectTiles = 16;
+// Tiles up to which one launch is quicker: a fork in 4096, 16384 and 65536 pages takes 7.6, 8.7 and 13.8 us, in two
+// launches 9.8, 10.0 and 10.2; a compaction 8.3, 10.4 and 17.9, 10.0, 15.1 and 32.0 (the latter with CTAs for teams).
+constexpr int kDirectTiles = 4;
 
 cudaError_t run_plan(PageArgs a, cudaStream_t stream) {
     a.direct = a.tiles <= kDirectTiles;
