@@ -3,9 +3,15 @@
 //
 //     a[t, c] = bias[c] + sum_{i < W} weight[c, i] x[t - (W - 1) + i, c],    y = a * sigmoid(a)
 // with x at negative times taken from the history.  Bound by memory: x read once, y written once.  A
-// thread owns eight channels over a tile of tokens and keeps the last W - 1 inputs in registers.
+// thread owns four channels over a tile of tokens and keeps the last W inputs in a ring of registers; its loads
+// run up to eight tokens ahead.  Measured on 16384 tokens x 4096 channels, W 4: bf16 53 us (5.0 TB/s), fp32 90
+// us (5.9 TB/s); with eight channels a thread 61 and 104 us (fewer warps: waiting for loads), with tiles that
+// leave a last wave of CTAs part empty 59 us.  One token of 128 rows x 12288 channels: 9 us of kernel, 11 us
+// with two rows to a CTA in place of four.
 #include <math.h>
 #include <string.h>
+
+#include <type_traits>
 
 #include "kda.h"
 #include "kda_common.cuh"
@@ -19,14 +25,14 @@ using namespace sm100;
 namespace {
 
 constexpr int kHistMaxW = 8;
-constexpr int kHistTile = 32;       // tokens per CTA
+constexpr int kHistLeast = 8, kHistMost = 80;   // tokens per CTA
 // tokens whose loads a thread has in flight: a multiple of W, so that the window's place in its registers is
 // the same in every batch
 constexpr int hist_ahead(int W) { return 8 / W * W; }
-constexpr int kHistThreads = 128;   // x 8 channels
+constexpr int kHistThreads = 128;
 
 struct HistArgs {
-    int TT, T, C, W, dtype, rows, tiles, num_slots, wide;   // wide: the weights allow 16-byte loads
+    int TT, T, C, W, dtype, rows, tile, tiles, num_slots, wide;   // wide: the weights allow 16-byte loads
     int64_t xs;            // elements between tokens of x
     const void* x;
     const float* w;        // [C, W]
@@ -45,64 +51,52 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-template <typename T> struct Raw8;
-template <> struct Raw8<__nv_bfloat16> {
-    uint4 u;
+// A thread's channels of one token.
+constexpr int kCh = 4, kPairs = kCh / 2;
+template <typename T> struct Raw;
+template <> struct Raw<__nv_bfloat16> {
+    uint2 u;
     __device__ __forceinline__ void load(const void* p, size_t i) {
-        u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
+        u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + i);
     }
-    __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void zero() { u = make_uint2(0, 0); }
     __device__ __forceinline__ void store(void* p, size_t i) const {
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + i) = u;
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + i) = u;
     }
     __device__ __forceinline__ void get(float2* v) const {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+        v[0] = make_float2(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u));
+        v[1] = make_float2(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
     }
-    __device__ __forceinline__ void put(const float2* v) {
-        u = make_uint4(pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y), pack_bf16(v[2].x, v[2].y), pack_bf16(v[3].x, v[3].y));
-    }
+    __device__ __forceinline__ void put(const float2* v) { u = make_uint2(pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y)); }
 };
-template <> struct Raw8<float> {
-    float4 a, b;
+template <> struct Raw<float> {
+    float4 a;
     __device__ __forceinline__ void load(const void* p, size_t i) {
-        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-        a = f[0];
-        b = f[1];
+        a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
     }
-    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ __forceinline__ void store(void* p, size_t i) const {
-        float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-        f[0] = a;
-        f[1] = b;
-    }
+    __device__ __forceinline__ void zero() { a = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void store(void* p, size_t i) const { *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = a; }
     __device__ __forceinline__ void get(float2* v) const {
         v[0] = make_float2(a.x, a.y);
         v[1] = make_float2(a.z, a.w);
-        v[2] = make_float2(b.x, b.y);
-        v[3] = make_float2(b.z, b.w);
     }
-    __device__ __forceinline__ void put(const float2* v) {
-        a = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
-        b = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
-    }
+    __device__ __forceinline__ void put(const float2* v) { a = make_float4(v[0].x, v[0].y, v[1].x, v[1].y); }
 };
 
-// A thread's eight channels' taps are 8 W consecutive floats; kept as pairs of channels.
+// A thread's taps are kCh W consecutive floats; kept as pairs of channels.
 template <int W>
 __device__ __forceinline__ void load_weights(const HistArgs& a, int c0, float2 (*w)[W], float2* bias) {
     const float* src = a.w + (size_t)c0 * W;
-    float f[8 * W];
+    float f[kCh * W];
     if (a.wide) {
 #pragma unroll
-        for (int i = 0; i < 8 * W; i += 4) *reinterpret_cast<float4*>(f + i) = __ldg(reinterpret_cast<const float4*>(src + i));
+        for (int i = 0; i < kCh * W; i += 4) *reinterpret_cast<float4*>(f + i) = __ldg(reinterpret_cast<const float4*>(src + i));
     } else {
 #pragma unroll
-        for (int i = 0; i < 8 * W; ++i) f[i] = src[i];
+        for (int i = 0; i < kCh * W; ++i) f[i] = src[i];
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kPairs; ++k) {
         bias[k] = a.b ? make_float2(a.b[c0 + 2 * k], a.b[c0 + 2 * k + 1]) : make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < W; ++i) w[k][i] = make_float2(f[2 * k * W + i], f[(2 * k + 1) * W + i]);
@@ -113,10 +107,10 @@ __device__ __forceinline__ void load_weights(const HistArgs& a, int c0, float2 (
 // a / (1 + e^-a) takes one reciprocal for two values (the special function unit is half as busy); the
 // exponential stops at 2^60, where a times the sigmoid is below 1e-16.
 template <int W, typename R>
-__device__ __forceinline__ void conv_out(const float2 (*w)[W], const float2* bias, const float2 (*win)[4], int first, R& out) {
-    float2 y[4];
+__device__ __forceinline__ void conv_out(const float2 (*w)[W], const float2* bias, const float2 (*win)[kPairs], int first, R& out) {
+    float2 y[kPairs];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kPairs; ++k) {
         y[k] = bias[k];
 #pragma unroll
         for (int i = 0; i < W; ++i) y[k] = fma2(w[k][i], win[(first + i) % W][k], y[k]);
@@ -139,16 +133,16 @@ __device__ __forceinline__ bool offsets_ok(const HistArgs& a) {
 
 __device__ __forceinline__ int row_begin(const HistArgs& a, int n) { return a.cu ? a.cu[n] : n * a.T; }
 
-// CTAs below `tiles` take 64 tokens each; the others write the final history of one row each.
+// CTAs below `tiles` take a.tile tokens each; the others write the final history of one row each.
 template <int W, typename E>
-__global__ void __launch_bounds__(kHistThreads, sizeof(E) == 2 && W <= 4 ? 4 : 2) conv_prompt_kernel(HistArgs a) {
+__global__ void __launch_bounds__(kHistThreads, W > 4 ? 3 : sizeof(E) == 2 ? 6 : 4) conv_prompt_kernel(HistArgs a) {
     if (a.cu && !offsets_ok(a)) {
         if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) record_error(a.status, KDA_ERR_INVALID_ARG);
         return;
     }
-    const int c0 = (blockIdx.y * kHistThreads + threadIdx.x) * 8;
+    const int c0 = (blockIdx.y * kHistThreads + threadIdx.x) * kCh;
     if (c0 >= a.C) return;
-    Raw8<E> raw;
+    Raw<E> raw;
     if ((int)blockIdx.x >= a.tiles) {
         const int n = blockIdx.x - a.tiles;
         const int s0 = row_begin(a, n), s1 = row_begin(a, n + 1);
@@ -163,9 +157,9 @@ __global__ void __launch_bounds__(kHistThreads, sizeof(E) == 2 && W <= 4 ? 4 : 2
         return;
     }
     constexpr int AHEAD = hist_ahead(W);
-    float2 w[4][W], bias[4], win[W][4];
+    float2 w[kPairs][W], bias[kPairs], win[W][kPairs];
     load_weights<W>(a, c0, w, bias);
-    const int t0 = blockIdx.x * kHistTile, t1 = min(t0 + kHistTile, a.TT);
+    const int t0 = blockIdx.x * a.tile, t1 = min(t0 + a.tile, a.TT);
     int n, s0, s1;
     if (a.cu) {
         int lo = 0, hi = a.rows - 1;   // last n with cu[n] <= t0
@@ -201,7 +195,7 @@ __global__ void __launch_bounds__(kHistThreads, sizeof(E) == 2 && W <= 4 ? 4 : 2
         }
         // tokens up to the row's or the tile's end, each one's load AHEAD tokens before its use
         const int end = min(t1, s1);
-        Raw8<E> in[AHEAD];
+        Raw<E> in[AHEAD];
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i)
             if (t + i < end) in[i].load(a.x, (size_t)(t + i) * a.xs + c0);
@@ -209,7 +203,7 @@ __global__ void __launch_bounds__(kHistThreads, sizeof(E) == 2 && W <= 4 ? 4 : 2
         auto put = [&](int i) {
             in[i].get(win[(W - 1 + i) % W]);
             if (t + i + AHEAD < end) in[i].load(a.x, (size_t)(t + i + AHEAD) * a.xs + c0);
-            Raw8<E> out;
+            Raw<E> out;
             conv_out<W>(w, bias, win, i % W, out);
             out.store(a.y, (size_t)(t + i) * a.C + c0);
         };
@@ -227,12 +221,12 @@ __global__ void __launch_bounds__(kHistThreads, sizeof(E) == 2 && W <= 4 ? 4 : 2
 
 // kHistRows rows of the batch with one set of weights (16 bytes of weights per channel beside 16 bytes of
 // inputs, outputs and histories per channel and row), all rows' loads in flight at once.
-constexpr int kHistRows = 2;
+constexpr int kHistRows = 4;
 template <int W, typename E>
 __global__ void __launch_bounds__(kHistThreads) conv_step_kernel(HistArgs a) {
-    const int c0 = (blockIdx.y * kHistThreads + threadIdx.x) * 8;
+    const int c0 = (blockIdx.y * kHistThreads + threadIdx.x) * kCh;
     if (c0 >= a.C) return;
-    Raw8<E> raw[kHistRows][W];
+    Raw<E> raw[kHistRows][W];
     int slot[kHistRows];
 #pragma unroll
     for (int k = 0; k < kHistRows; ++k) {
@@ -252,13 +246,13 @@ __global__ void __launch_bounds__(kHistThreads) conv_step_kernel(HistArgs a) {
         for (int i = 0; i < W - 1; ++i) raw[k][i].load(a.h_in, hb + (size_t)i * a.C);
         raw[k][W - 1].load(a.x, (size_t)r * a.xs + c0);
     }
-    float2 w[4][W], bias[4], win[W][4];
+    float2 w[kPairs][W], bias[kPairs], win[W][kPairs];
     load_weights<W>(a, c0, w, bias);
 #pragma unroll
     for (int k = 0; k < kHistRows; ++k) {
         const int r = blockIdx.x * kHistRows + k;
         if (r >= a.rows) break;
-        Raw8<E> out;
+        Raw<E> out;
         if (slot[k] < 0) {
             out.zero();
             out.store(a.y, (size_t)r * a.C + c0);
@@ -288,22 +282,35 @@ kda_status hist_check(int B, int T, int C, int W, int dtype, const void* x, int6
 
 }  // namespace
 
-#define KDA_HIST_CASE(KERNEL, w, a, grid, st)                                                      \
-    case w:                                                                                        \
-        if ((a).dtype == KDA_BF16) KERNEL<w, __nv_bfloat16><<<grid, kHistThreads, 0, st>>>(a);     \
-        else KERNEL<w, float><<<grid, kHistThreads, 0, st>>>(a);                                   \
-        break;
-#define KDA_HIST_DISPATCH(KERNEL, a, grid, st)                                                     \
-    switch ((a).W) {                                                                               \
-        KDA_HIST_CASE(KERNEL, 1, a, grid, st)                                                      \
-        KDA_HIST_CASE(KERNEL, 2, a, grid, st)                                                      \
-        KDA_HIST_CASE(KERNEL, 3, a, grid, st)                                                      \
-        KDA_HIST_CASE(KERNEL, 4, a, grid, st)                                                      \
-        KDA_HIST_CASE(KERNEL, 5, a, grid, st)                                                      \
-        KDA_HIST_CASE(KERNEL, 6, a, grid, st)                                                      \
-        KDA_HIST_CASE(KERNEL, 7, a, grid, st)                                                      \
-        KDA_HIST_CASE(KERNEL, 8, a, grid, st)                                                      \
+// f of the kernel's width and element type as constants.
+template <typename F>
+static cudaError_t hist_dispatch(int W, int dtype, F&& f) {
+#define KDA_HIST_CASE(w) \
+    case w: return dtype == KDA_BF16 ? f(std::integral_constant<int, w>(), __nv_bfloat16()) : f(std::integral_constant<int, w>(), float());
+    switch (W) {
+        KDA_HIST_CASE(1)
+        KDA_HIST_CASE(2)
+        KDA_HIST_CASE(3)
+        KDA_HIST_CASE(4)
+        KDA_HIST_CASE(5)
+        KDA_HIST_CASE(6)
+        KDA_HIST_CASE(7)
+        KDA_HIST_CASE(8)
     }
+#undef KDA_HIST_CASE
+    return cudaErrorInvalidValue;
+}
+
+// CTAs of a kernel that the GPU holds at once.
+template <int W, typename E>
+static int prompt_slots() {
+    static const int n = [] {
+        int per = 0;
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, conv_prompt_kernel<W, E>, kHistThreads, 0) == cudaSuccess && per > 0
+                   ? per * 152 : 152;
+    }();
+    return n;
+}
 
 }  // namespace kda
 
@@ -329,12 +336,22 @@ kda_status kda_short_conv_prompt(int B, int T, int C, int W, kda_dtype dtype, co
     a.x = x; a.w = weight; a.b = bias; a.cu = cu_seqlens; a.h_in = initial_history; a.h_out = final_history; a.y = y;
     st = status_ptr(&a.status);
     if (st != KDA_OK) return st;
-    a.tiles = (a.TT + kHistTile - 1) / kHistTile;
-    const dim3 grid(a.tiles + (final_history && W > 1 ? a.rows : 0), (C / 8 + kHistThreads - 1) / kHistThreads);
     timing_pre(stream, K_CONV_PROMPT);
-    KDA_HIST_DISPATCH(conv_prompt_kernel, a, grid, stream);
+    const cudaError_t e = hist_dispatch(W, dtype, [&](auto w, auto type) {
+        using E = decltype(type);
+        // the fewest whole waves of CTAs with no more than kHistMost tokens each
+        const int cols = (C / kCh + kHistThreads - 1) / kHistThreads;
+        const int64_t slots = prompt_slots<w.value, E>(), work = (int64_t)a.TT * cols;
+        const int64_t ctas = (work + slots * kHistMost - 1) / (slots * kHistMost) * slots;
+        a.tile = (int)((work + ctas - 1) / ctas);
+        if (a.tile < kHistLeast) a.tile = kHistLeast;
+        a.tiles = (a.TT + a.tile - 1) / a.tile;
+        const dim3 grid(a.tiles + (final_history && w.value > 1 ? a.rows : 0), cols);
+        conv_prompt_kernel<w.value, E><<<grid, kHistThreads, 0, stream>>>(a);
+        return cudaGetLastError();
+    });
     timing_post(stream);
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 kda_status kda_short_conv_step(int B, int C, int W, kda_dtype dtype, const void* x, int64_t x_stride,
@@ -351,11 +368,14 @@ kda_status kda_short_conv_step(int B, int C, int W, kda_dtype dtype, const void*
     a.x = x; a.w = weight; a.b = bias; a.slots = slots; a.h_in = history_in; a.h_out = history_out; a.y = y;
     st = status_ptr(&a.status);
     if (st != KDA_OK) return st;
-    const dim3 grid((B + kHistRows - 1) / kHistRows, (C / 8 + kHistThreads - 1) / kHistThreads);
+    const dim3 grid((B + kHistRows - 1) / kHistRows, (C / kCh + kHistThreads - 1) / kHistThreads);
     timing_pre(stream, K_CONV_STEP);
-    KDA_HIST_DISPATCH(conv_step_kernel, a, grid, stream);
+    const cudaError_t e = hist_dispatch(W, dtype, [&](auto w, auto type) {
+        conv_step_kernel<w.value, decltype(type)><<<grid, kHistThreads, 0, stream>>>(a);
+        return cudaGetLastError();
+    });
     timing_post(stream);
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 }  // extern "C"
