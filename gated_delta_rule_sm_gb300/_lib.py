@@ -560,18 +560,19 @@ def _raw_stream(dev: int, stream) -> int:
 
 def _empty(like, shape, dtype, stream):
     """A new tensor, allocated for the stream the call runs on."""
+    # (half the time of new_empty)
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _result(name: str, out, like, dev: int, stream):
     """The output tensor of like's shape and dtype, given or new, and its address."""
     if out is not None:
         return out, _need(name, out, like.dtype, like.shape, dev)
-    if stream is None and like.is_contiguous():
-        out = torch.empty_like(like)
+    if stream is None:
+        out = torch.empty_like(like, memory_format=torch.contiguous_format)
     else:
         out = _empty(like, like.shape, like.dtype, stream)
     return out, out.data_ptr()

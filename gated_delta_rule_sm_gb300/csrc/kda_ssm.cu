@@ -110,7 +110,7 @@ Schedule make_schedule(const SsmShape& s, bool varlen, const Costs& k) {
     w.nseg = varlen ? (w.single ? s.rows : s.rows + s.TT / w.L) : s.rows * w.per_row;
     size_t o = 0;
     w.plan = varlen && (!w.single || s.rows > kSsmOwnRows);
-    if (w.plan) {
+    if (varlen) {      // (wanted of the caller whether or not this schedule has a planner)
         w.off_seg = o; o = up256(o + sizeof(SsmSeg) * (size_t)w.nseg);
         w.off_row = o; o = up256(o + sizeof(int32_t) * ((size_t)s.rows + 1));
     }
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(1024) ssm_plan_kernel(SsmArgs a, SsmSeg* seg, 
 
 // Entering states of a row's segments: S <- decay_k S + loc_k, in place of loc_k.  Elementwise over the
 // state, bound by memory: a thread walks VEC elements along the row's segments, kJoinAhead of them in flight.
-constexpr int kJoinAhead = 8;
+constexpr int kJoinAhead = 16;
 template <int VEC>
 __global__ void __launch_bounds__(128) ssm_join_kernel(SsmArgs a) {
     const int np = a.N * a.P;
