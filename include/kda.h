@@ -463,11 +463,11 @@ kda_status kda_decode_step(const kda_dims* dims, const void* q, const void* k, c
  * A device-only cu_seqlens that breaks the contract records KDA_ERR_INVALID_ARG in the device status
  * word; y is then not written and final_state gets the entering state (zero without one).
  * All sums and states are fp32.  bf16 inputs with N, P <= 128, N, P and the strides multiples of 8 and
- * 16-byte aligned x, b, c and y run on the tensor cores in chunks of 128 tokens: the products inside a
- * chunk and the read of the entering state round one operand to bf16 (y is bf16), the state update
- * keeps its operand as a sum of two bf16 values (relative error ~1e-6 of the state).  There a
- * non-finite x, B or C spreads over its whole chunk instead of only the later tokens.  Every other
- * shape runs an fp32 token-by-token kernel.
+ * 16-byte aligned x, b, c and y run on the tensor cores in chunks of 128 tokens: the factors inside a
+ * chunk are rounded to bf16 once (y is bf16), the entering state is read as the sum of two bf16 values,
+ * and the state update keeps its operand as the sum of three (fp32 rounding).  There a non-finite x, B
+ * or C spreads over its whole chunk instead of only the later tokens.  Every other shape, and calls of
+ * at most 16 tokens to a row that one wave of CTAs covers, run an fp32 token-by-token kernel.
  * Long rows with few rows x heads are cut into segments whose end states are computed in parallel and
  * joined before the outputs; the library chooses the cut.  Results do not depend on timing.
  * The workspace is kda_ssm_fwd_workspace_size() bytes (0 on invalid input).
