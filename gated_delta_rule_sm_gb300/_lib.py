@@ -2,13 +2,12 @@
 
 Argument marshalling only: torch provides device memory and the current CUDA
 stream, every step of the computation runs in the library's CUDA kernels.
-There is no fallback: if ``libkda_gb300.so`` is missing or CUDA is not
-available the calls raise.
+There is no fallback: if ``libkda_gb300.so`` (or ``_ops.so``, the native binding
+of the serving calls) is missing or CUDA is not available the calls raise.
 """
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import threading
 from typing import Optional
@@ -17,6 +16,7 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libkda_gb300.so")
+OPS_PATH = os.path.join(_PKG, "_ops.so")
 
 KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_CUDA, KDA_ERR_TIMEOUT, KDA_ERR_WORKSPACE = range(6)
 KDA_BF16, KDA_FP32 = 0, 1
@@ -496,133 +496,40 @@ def gated_norm_backward(o, gate, weight, dy, *, eps: float = 1e-6, stream: Optio
 
 # ---- serving: states carried from prompts to single tokens ----
 #
-# A step's kernel takes a few microseconds, so these calls keep their own time short: one test per tensor, plain
-# integers for pointers, dimension structures kept by their values.
+# A step's kernel takes a few microseconds, so what is around these calls is native too (csrc/torch_ops.cpp): checks,
+# outputs, workspaces and the C entry.  Here are their signatures.
 
-_F32, _I32 = torch.float32, torch.int32
-_DTYPE_CODES = {torch.bfloat16: KDA_BF16, torch.float32: KDA_FP32}
-
-
-def _refuse(name: str, t, dtype, shape, dev):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: all tensors of a call must be on one CUDA device")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    raise ValueError(f"{name} must be contiguous")
+_ops = None
 
 
-def _need(name: str, t, dtype, shape, dev):
-    """t's address, once it is a contiguous tensor of the dtype and shape on the device (None: no tensor)."""
-    if t is None:
-        return None
-    if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev):
-        _refuse(name, t, dtype, shape, dev)
-    return t.data_ptr()
+def _native():
+    """The native binding, loaded on first use."""
+    global _ops
+    load()
+    if not os.path.exists(OPS_PATH):
+        raise ImportError(f"KDA binding not built: {OPS_PATH} is missing "
+                          "(run `python -c 'import __graft_entry__ as g; g.build()'`)")
+    from . import _ops as ops
+    ops.setup(_check, workspace_cache.buf)
+    _ops = ops
+    return ops
 
 
-def _first(name: str, t, dims: int):
-    """The device index and dtype code of a call's leading tensor."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != dims:
-        raise ValueError(f"{name} must have {dims} axes, got {list(t.shape)}")
-    code = _DTYPE_CODES.get(t.dtype)
-    return t.get_device(), _dtype_code(t) if code is None else code
-
-
-@functools.lru_cache(maxsize=4096)
-def _token_stride(name: str, shape, strides, lead: int) -> int:
-    """Elements between neighbouring tokens of a tensor whose first ``lead`` axes are tokens ([B, T] or [B]) and
-    whose other axes are one token's contiguous values: it may be a slice of a wider projection."""
-    want = 1
-    for k in range(len(shape) - 1, lead - 1, -1):
-        if strides[k] != want and shape[k] > 1:
-            raise ValueError(f"{name}: the values of one token must be contiguous")
-        want *= shape[k]
-    step = span = None
-    for k in range(lead - 1, -1, -1):
-        if shape[k] > 1:
-            if step is None:
-                step = strides[k]
-            elif strides[k] != span:
-                raise ValueError(f"{name}: tokens must be evenly spaced over the leading axes")
-            span = strides[k] * shape[k]
-    return want if step is None else step
-
-
-def _raw_stream(dev: int, stream) -> int:
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
-
-
-def _empty(like, shape, dtype, stream):
-    """A new tensor, allocated for the stream the call runs on."""
-    # (half the time of new_empty)
+def _run(name: str, stream, *args):
+    """The native call, on the current stream or on the one given."""
+    call = getattr(_ops or _native(), name)
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return call(*args)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return call(*args)
 
 
-def _result(name: str, out, like, dev: int, stream):
-    """The output tensor of like's shape and dtype, given or new, and its address."""
-    if out is not None:
-        return out, _need(name, out, like.dtype, like.shape, dev)
-    if stream is None:
-        out = torch.empty_like(like, memory_format=torch.contiguous_format)
-    else:
-        out = _empty(like, like.shape, like.dtype, stream)
-    return out, out.data_ptr()
-
-
-def _scratch(like, dev: int, kind: str, ptr: int, nbytes: int, stream):
-    """One workspace per device, kind and stream: calls on different streams may overlap."""
-    buf = workspace_cache.buf.get((dev, kind, ptr))
-    if buf is None or buf.numel() < nbytes:
-        buf = _empty(like, (max(nbytes, 256),), torch.uint8, stream)
-        workspace_cache.buf[(dev, kind, ptr)] = buf
-    return buf
-
-
-@functools.lru_cache(maxsize=4096)
-def _ssm_layout(lead: int, code: int, n: int, x, xs, b, bs, c, cs, dt, ds):
-    """Checks of the shapes and strides of x, b, c and dt_raw: (dims reference, bytes of workspace of the scan, H)."""
-    tokens, H = x[:lead], x[lead]
-    if len(b) != lead + 2 or b[:lead] != tokens or c != b or dt != x[:lead + 1]:
-        raise ValueError("x must be [..., H, P], b and c [..., G, N] and dt_raw [..., H] over the same tokens")
-    G = b[lead]
-    if G < 1 or H % G:
-        raise ValueError(f"heads ({H}) must be a multiple of the groups of b and c ({G})")
-    dims = SsmDims(tokens[0], tokens[1] if lead == 2 else 1, H, G, b[-1], x[-1], code, n, _token_stride("x", x, xs, lead),
-                   _token_stride("b", b, bs, lead), _token_stride("c", c, cs, lead), _token_stride("dt_raw", dt, ds, lead))
-    ref = ctypes.byref(dims)
-    return ref, int(load().kda_ssm_fwd_workspace_size(ref)), H
-
-
-def _ssm_args(x, dt_raw, b, c, a_log, dt_bias, d_skip, lead: int, n: int, dev: int, code: int):
-    """Checks of the arguments that the scan and the step share: (dims reference, workspace bytes, addresses)."""
-    ref, nbytes, H = _ssm_layout(lead, code, n, x.shape, x.stride(), b.shape, b.stride(), c.shape, c.stride(), dt_raw.shape,
-                                 dt_raw.stride())
-    dtype = x.dtype
-    if b.dtype is not dtype or c.dtype is not dtype or dt_raw.dtype is not dtype:
-        raise ValueError("x, b, c and dt_raw must have one dtype")
-    if b.get_device() != dev or c.get_device() != dev or dt_raw.get_device() != dev:
-        raise ValueError("all tensors of a call must be on one CUDA device")
-    per_head = (H,)
-    return ref, nbytes, (x.data_ptr(), dt_raw.data_ptr(), b.data_ptr(), c.data_ptr(),
-                         _need("a_log", a_log, _F32, per_head, dev), _need("dt_bias", dt_bias, _F32, per_head, dev),
-                         _need("d_skip", d_skip, _F32, per_head, dev))
-
-
-def _offsets(cu_seqlens, cu_seqlens_host, B: int, dev: int):
-    """(documents, rows, device address, host copy) of a call's packed-document offsets."""
-    if cu_seqlens is None:
-        return 0, B, None, host_offsets(cu_seqlens_host)
-    n = cu_seqlens.numel() - 1
-    return n, n, _need("cu_seqlens", cu_seqlens, _I32, (n + 1,), dev), host_offsets(cu_seqlens_host, n + 1)
+def _host_address(cu_seqlens, cu_seqlens_host):
+    """(the address of a host copy of the offsets, what keeps it alive)."""
+    if cu_seqlens_host is None:
+        return None, None
+    held = host_offsets(cu_seqlens_host, None if cu_seqlens is None else cu_seqlens.numel())
+    return ctypes.addressof(held), held
 
 
 def ssm_scan(x, dt_raw, b, c, a_log, dt_bias, d_skip=None, *, cu_seqlens=None, cu_seqlens_host=None,
@@ -635,34 +542,9 @@ def ssm_scan(x, dt_raw, b, c, a_log, dt_bias, d_skip=None, *, cu_seqlens=None, c
     rows = B, or one per document of ``cu_seqlens`` (int32).
         S_t = exp(D_t a) S_{t-1} + D_t b_t x_t^T,  y_t = S_t^T c_t + d_skip x_t,
         D = softplus(dt_raw + dt_bias), a = -exp(a_log)."""
-    lib = _lib or load()
-    dev, code = _first("x", x, 4)
-    n, rows, cu, cu_h = _offsets(cu_seqlens, cu_seqlens_host, x.shape[0], dev)
-    ref, nbytes, args = _ssm_args(x, dt_raw, b, c, a_log, dt_bias, d_skip, 2, n, dev, code)
-    state_shape = (rows, x.shape[2], b.shape[3], x.shape[3])
-    s0 = _need("initial_state", initial_state, _F32, state_shape, dev)
-    st = _raw_stream(dev, stream)
-    out, po = _result("out", out, x, dev, stream)
-    if not output_final_state:
-        final_state = pf = None
-    elif final_state is None:
-        final_state = _empty(a_log, state_shape, _F32, stream)
-        pf = final_state.data_ptr()
-    else:
-        pf = _need("final_state", final_state, _F32, state_shape, dev)
-    ws = _scratch(x, dev, "ssm", st, nbytes, stream)
-    _check(lib.kda_ssm_fwd(ref, *args, cu, cu_h, s0, po, pf, ws.data_ptr(), ws.numel(), st), "kda_ssm_fwd")
-    return out, final_state
-
-
-def _pool_args(name: str, pool, slots, B: int, cell, dtype, pool_out, dev: int):
-    """Checks of a slot pool [slots, *cell]: (slots address, number of slots, pool address, address written, pool written)."""
-    n = pool.shape[0] if pool.dim() else 0
-    shape = (n, *cell)
-    if pool_out is None:
-        pool_out = pool
-    return (_need("slots", slots, _I32, (B,), dev), n, _need(name, pool, dtype, shape, dev),
-            _need(f"{name}_out", pool_out, dtype, shape, dev)), pool_out
+    address, held = _host_address(cu_seqlens, cu_seqlens_host)
+    return _run("ssm_scan", stream, x, dt_raw, b, c, a_log, dt_bias, d_skip, cu_seqlens, address, initial_state,
+                output_final_state, out, final_state)
 
 
 def ssm_step(x, dt_raw, b, c, a_log, dt_bias, d_skip=None, *, state, slots=None, state_out=None, out=None,
@@ -672,20 +554,7 @@ def ssm_step(x, dt_raw, b, c, a_log, dt_bias, d_skip=None, *, state, slots=None,
     ``state`` [slots, H, N, P] fp32 is the pool, row r works on slot ``slots[r]`` (int32; None: slot r; negative:
     the row is idle and gets zeros).  The pool is updated in place, or into ``state_out`` (only the named slots
     are written).  Returns (y, the pool written)."""
-    lib = _lib or load()
-    dev, code = _first("x", x, 3)
-    ref, _, args = _ssm_args(x, dt_raw, b, c, a_log, dt_bias, d_skip, 1, 0, dev, code)
-    B, H, P = x.shape
-    pool, state_out = _pool_args("state", state, slots, B, (H, b.shape[2], P), _F32, state_out, dev)
-    out, po = _result("out", out, x, dev, stream)
-    _check(lib.kda_ssm_step(ref, *args, *pool, po, _raw_stream(dev, stream)), "kda_ssm_step")
-    return out, state_out
-
-
-@functools.lru_cache(maxsize=4096)
-def _step_dims(*fields):
-    dims = KdaDims(*fields)
-    return dims, ctypes.byref(dims)
+    return _run("ssm_step", stream, x, dt_raw, b, c, a_log, dt_bias, d_skip, state, slots, state_out, out)
 
 
 def decode_step(q, k, v, g_raw, beta_raw, a_log, dt_bias, *, scale: float, lower_bound: float = -5.0,
@@ -695,27 +564,8 @@ def decode_step(q, k, v, g_raw, beta_raw, a_log, dt_bias, *, scale: float, lower
 
     q, k [B, Hk, K], v [B, H, V], g_raw [B, H, K], beta_raw [B, H]; ``state`` [slots, H, K, V] fp32, ``slots``,
     ``state_out`` as for :func:`ssm_step`.  Returns (out, the pool written)."""
-    lib = _lib or load()
-    dev, code = _first("q", q, 3)
-    if v.dim() != 3:
-        raise ValueError("v must be [B, H, V]")
-    B, Hk, K = q.shape
-    H, V = v.shape[1:]
-    dtype, key, gates = q.dtype, (B, Hk, K), (B, H, K)
-    args = (_need("q", q, dtype, key, dev), _need("k", k, dtype, key, dev), _need("v", v, dtype, (B, H, V), dev),
-            _need("g_raw", g_raw, dtype, gates, dev), _need("beta_raw", beta_raw, dtype, (B, H), dev),
-            _need("a_log", a_log, _F32, (H,), dev), _need("dt_bias", dt_bias, _F32, (H * K,), dev))
-    pool, state_out = _pool_args("state", state, slots, B, (H, K, V), _F32, state_out, dev)
-    out, po = _result("out", out, v, dev, stream)
-    _, ref = _step_dims(B, 1, H, K, V, code, 0, Hk, _gate_code(gate))
-    _check(lib.kda_decode_step(ref, *args, scale, lower_bound, *pool, po, _raw_stream(dev, stream)), "kda_decode_step")
-    return out, state_out
-
-
-def _conv_args(x, weight, bias, dev: int, C: int):
-    W = weight.shape[-1]
-    return W, (_need("weight", weight, _F32, (C, 1, W) if weight.dim() == 3 else (C, W), dev),
-               _need("bias", bias, _F32, (C,), dev))
+    return _run("decode_step", stream, q, k, v, g_raw, beta_raw, a_log, dt_bias, scale, lower_bound, _gate_code(gate), state,
+                slots, state_out, out)
 
 
 def short_conv_prompt(x, weight, bias=None, *, cu_seqlens=None, cu_seqlens_host=None, initial_history=None, out=None,
@@ -724,105 +574,21 @@ def short_conv_prompt(x, weight, bias=None, *, cu_seqlens=None, cu_seqlens_host=
 
     x [B, T, C] (a slice of a wider projection is taken as it is); histories [rows, W - 1, C] like x, oldest input
     first: the last W - 1 inputs before the row (None: zeros) and at its end."""
-    lib = _lib or load()
-    dev, code = _first("x", x, 3)
-    B, T, C = x.shape
-    W, params = _conv_args(x, weight, bias, dev, C)
-    n, rows, cu, cu_h = _offsets(cu_seqlens, cu_seqlens_host, B, dev)
-    hist = (rows, W - 1, C)
-    h0 = _need("initial_history", initial_history, x.dtype, hist, dev)
-    out, po = _result("out", out, x, dev, stream)
-    if final_history is None:
-        final_history = _empty(x, hist, x.dtype, stream)
-    _check(lib.kda_short_conv_prompt(B, T, C, W, code, x.data_ptr(), _token_stride("x", x.shape, x.stride(), 2), *params,
-                                     cu, cu_h, n, h0, po,
-                                     _need("final_history", final_history, x.dtype, hist, dev), _raw_stream(dev, stream)),
-           "kda_short_conv_prompt")
-    return out, final_history
+    address, held = _host_address(cu_seqlens, cu_seqlens_host)
+    return _run("short_conv_prompt", stream, x, weight, bias, cu_seqlens, address, initial_history, out, final_history)
 
 
 def short_conv_step(x, weight, bias=None, *, history, slots=None, history_out=None, out=None,
                     stream: Optional[torch.cuda.Stream] = None):
     """One token per row through ``kda_short_conv_step``: x [B, C], ``history`` [slots, W - 1, C] like x; ``slots``
     and ``history_out`` as for :func:`ssm_step`.  Returns (y, the pool written)."""
-    lib = _lib or load()
-    dev, code = _first("x", x, 2)
-    B, C = x.shape
-    W, params = _conv_args(x, weight, bias, dev, C)
-    pool, history_out = _pool_args("history", history, slots, B, (W - 1, C), x.dtype, history_out, dev)
-    out, po = _result("out", out, x, dev, stream)
-    _check(lib.kda_short_conv_step(B, C, W, code, x.data_ptr(), _token_stride("x", x.shape, x.stride(), 1), *params, *pool,
-                                   po, _raw_stream(dev, stream)), "kda_short_conv_step")
-    return out, history_out
-
-
-@functools.lru_cache(maxsize=4096)
-def _pool_layers(name: str, shape, strides, es: int):
-    """(layers, pages, bytes of a page, bytes between layers) of a pool [layers, pages, ...]."""
-    if len(shape) < 2 or 0 in shape:
-        raise ValueError(f"{name} must be [layers, pages, ...]")
-    want = 1
-    for k in range(len(shape) - 1, 0, -1):
-        if strides[k] != want and shape[k] > 1:
-            raise ValueError(f"{name}: the pages of a layer must be contiguous")
-        want *= shape[k]
-    return shape[0], shape[1], want // shape[1] * es, strides[0] * es
-
-
-@functools.lru_cache(maxsize=4096)
-def _pages_dims(n: int, *fields):
-    """(the structure, its reference, bytes of workspace for n requests)."""
-    dims = PagesDims(*fields)
-    ref = ctypes.byref(dims)
-    return dims, ref, int(load().kda_pages_workspace_size(ref, n))
-
-
-def _pages_args(pool, table, lengths, refs, table_out, lengths_out, refs_out, page_tokens: int, n: int):
-    """Checks of a cache's arrays: (device, dims reference, workspace bytes, inputs, outputs); lengths may be None."""
-    dev = table.get_device()
-    if (not table.is_cuda) or table.dim() != 2:
-        raise ValueError("table must be a CUDA tensor [sequences, pages of a row]")
-    shape = table.shape
-    rows, pages = (shape[0],), (refs.numel(),)
-    ins = (_need("table", table, _I32, shape, dev), _need("lengths", lengths, _I32, rows, dev),
-           _need("refs", refs, _I32, pages, dev))
-    outs = (ins[0] if table_out is None else _need("table_out", table_out, _I32, shape, dev),
-            ins[1] if lengths_out is None else _need("lengths_out", lengths_out, _I32, rows, dev),
-            ins[2] if refs_out is None else _need("refs_out", refs_out, _I32, pages, dev))
-    if pool is None:
-        layers, page, stride = 1, 1, 0
-    else:
-        layers, held, page, stride = _pool_layers("pool", pool.shape, pool.stride(), pool.element_size())
-        if pool.get_device() != dev:
-            raise ValueError("all tensors of a call must be on one CUDA device")
-        if held != pages[0]:
-            raise ValueError(f"refs must hold one count per page ({held}), got {pages[0]}")
-    _, ref, nbytes = _pages_dims(n, layers, pages[0], shape[0], shape[1], int(page_tokens), page, stride)
-    return dev, ref, nbytes, ins, outs
-
-
-def _requests(dev: int, n: int, **named):
-    return tuple(_need(name, t, _I32, (n,), dev) for name, t in named.items())
+    return _run("short_conv_step", stream, x, weight, bias, history, slots, history_out, out)
 
 
 def pages_copy(pool, src, dst, *, src_pool=None, stream: Optional[torch.cuda.Stream] = None):
     """Page ``src[i]`` of ``src_pool`` (default: ``pool``) to page ``dst[i]`` of ``pool`` [layers, pages, ...], every
     layer, through ``kda_pages_copy``.  Pairs out of range are skipped; dst must not repeat nor meet src in one pool."""
-    lib = _lib or load()
-    src_pool = pool if src_pool is None else src_pool
-    dev = pool.get_device()
-    if not pool.is_cuda or src_pool.get_device() != dev:
-        raise ValueError("both pools must be on one CUDA device")
-    layers, pages, page, stride = _pool_layers("pool", pool.shape, pool.stride(), pool.element_size())
-    s_layers, s_pages, s_page, s_stride = _pool_layers("src_pool", src_pool.shape, src_pool.stride(),
-                                                       src_pool.element_size())
-    if layers != s_layers or page != s_page:
-        raise ValueError("both pools must have the same layers and page size")
-    n = src.numel()
-    ps, pd = _requests(dev, n, src=src, dst=dst)
-    _check(lib.kda_pages_copy(layers, page, pool.data_ptr(), stride, pages, src_pool.data_ptr(), s_stride, s_pages, ps, pd,
-                              n, _raw_stream(dev, stream)), "kda_pages_copy")
-    return pool
+    return _run("pages_copy", stream, pool, src, dst, src_pool)
 
 
 def pages_fork(pool, table, lengths, refs, parents, children, *, page_tokens: int, table_out=None, lengths_out=None,
@@ -830,56 +596,25 @@ def pages_fork(pool, table, lengths, refs, parents, children, *, page_tokens: in
     """Row ``children[i]`` becomes a copy of row ``parents[i]`` through ``kda_pages_fork``: full pages are shared, a
     partly filled last page is copied into a free one.  pool [layers, pages, ...], table [sequences, M], lengths
     [sequences], refs [pages] int32, updated in place or into the ``*_out`` arrays.  Returns ok [n] int32."""
-    lib = _lib or load()
-    n = parents.numel()
-    dev, ref, nbytes, ins, outs = _pages_args(pool, table, lengths, refs, table_out, lengths_out, refs_out, page_tokens, n)
-    req = _requests(dev, n, parents=parents, children=children)
-    st = _raw_stream(dev, stream)
-    if ok is None:
-        ok = _empty(table, (n,), _I32, stream)
-    ws = _scratch(table, dev, "pages", st, nbytes, stream)
-    _check(lib.kda_pages_fork(ref, pool.data_ptr(), *ins, *req, n, *outs, _need("ok", ok, _I32, (n,), dev), ws.data_ptr(),
-                              ws.numel(), st), "kda_pages_fork")
-    return ok
+    return _run("pages_fork", stream, pool, table, lengths, refs, parents, children, page_tokens, table_out, lengths_out,
+                refs_out, ok)
 
 
 def pages_extend(table, lengths, refs, seqs, new_lengths, *, page_tokens: int, table_out=None, lengths_out=None,
                  refs_out=None, ok=None, stream: Optional[torch.cuda.Stream] = None):
     """Row ``seqs[i]`` grows to ``new_lengths[i]`` tokens through ``kda_pages_extend``.  Returns ok [n] int32."""
-    lib = _lib or load()
-    n = seqs.numel()
-    dev, ref, nbytes, ins, outs = _pages_args(None, table, lengths, refs, table_out, lengths_out, refs_out, page_tokens, n)
-    req = _requests(dev, n, seqs=seqs, new_lengths=new_lengths)
-    st = _raw_stream(dev, stream)
-    if ok is None:
-        ok = _empty(table, (n,), _I32, stream)
-    ws = _scratch(table, dev, "pages", st, nbytes, stream)
-    _check(lib.kda_pages_extend(ref, *ins, *req, n, *outs, _need("ok", ok, _I32, (n,), dev), ws.data_ptr(), ws.numel(), st),
-           "kda_pages_extend")
-    return ok
+    return _run("pages_extend", stream, table, lengths, refs, seqs, new_lengths, page_tokens, table_out, lengths_out,
+                refs_out, ok)
 
 
 def pages_free(table, lengths, refs, seqs, *, table_out=None, lengths_out=None, refs_out=None,
                stream: Optional[torch.cuda.Stream] = None):
     """Rows ``seqs`` give up their pages through ``kda_pages_free``."""
-    lib = _lib or load()
-    n = seqs.numel()
-    dev, ref, _, ins, outs = _pages_args(None, table, lengths, refs, table_out, lengths_out, refs_out, 1, n)
-    _check(lib.kda_pages_free(ref, *ins, *_requests(dev, n, seqs=seqs), n, *outs, _raw_stream(dev, stream)),
-           "kda_pages_free")
+    return _run("pages_free", stream, table, lengths, refs, seqs, table_out, lengths_out, refs_out)
 
 
 def pages_compact(pool, table, refs, *, table_out=None, refs_out=None, page_map=None,
                   stream: Optional[torch.cuda.Stream] = None):
     """Moves the live pages of pool [layers, pages, ...] to the lowest indices through ``kda_pages_compact``; table
     and refs follow.  Returns page_map [pages] int32: the new index of each page, -1 for a free one."""
-    lib = _lib or load()
-    dev, ref, nbytes, ins, outs = _pages_args(pool, table, None, refs, table_out, None, refs_out, 1, 0)
-    st = _raw_stream(dev, stream)
-    if page_map is None:
-        page_map = _empty(refs, refs.shape, _I32, stream)
-    ws = _scratch(table, dev, "pages", st, nbytes, stream)
-    _check(lib.kda_pages_compact(ref, pool.data_ptr(), ins[0], ins[2], outs[0], outs[2],
-                                 _need("page_map", page_map, _I32, refs.shape, dev), ws.data_ptr(), ws.numel(), st),
-           "kda_pages_compact")
-    return page_map
+    return _run("pages_compact", stream, pool, table, refs, table_out, refs_out, page_map)
