@@ -288,7 +288,8 @@ ssm_tc_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ CUtenso
     tc_fence_after();
     const uint32_t tmem = *tslot;
 
-    // Bounded waits (one in good order takes microseconds, and a try suspends the thread for some at most);
+    // Bounded waits (one in good order takes microseconds; a try suspends the thread for ten at most, so that a wait gives
+    // up after about a second);
     // false, and the CTA marked as failed, where one gives up: its role then leaves its loop, and
     // the roles that wait for it give up in turn.  Kept short: they are inlined some thirty times, and the
     // code of all roles' loops has to stay in the instruction cache.
@@ -297,7 +298,7 @@ ssm_tc_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ CUtenso
         if (mbar_test_wait(&bar[b], parity)) return true;
 #pragma unroll 1
         for (uint32_t i = 0; i < kTries; ++i)
-            if (mbar_try_wait(&bar[b], parity)) return true;
+            if (mbar_try_wait_ns(&bar[b], parity, 10000)) return true;
         *fail = 1;
         return false;
     };
@@ -305,7 +306,7 @@ ssm_tc_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ CUtenso
         if (__all_sync(0xffffffffu, mbar_test_wait(&bar[b], parity))) return true;
 #pragma unroll 1
         for (uint32_t i = 0; i < kTries; ++i)
-            if (__all_sync(0xffffffffu, mbar_try_wait(&bar[b], parity))) return true;
+            if (__all_sync(0xffffffffu, mbar_try_wait_ns(&bar[b], parity, 10000))) return true;
         *fail = 1;
         return false;
     };
