@@ -10,9 +10,12 @@
 #include <string.h>
 
 #include "kda.h"
+#include "kda_sm100.cuh"
 #include "kda_ssm.h"
 
 namespace kda {
+
+using namespace sm100;
 
 kda_status ssm_check(const kda_ssm_dims* d, bool varlen, const void* x, const void* dt_raw, const void* b,
                      const void* c, const float* a_log, const float* dt_bias, SsmShape* s) {
@@ -51,9 +54,10 @@ namespace {
 // and `start`; the states-only pass `state` of the output pass again; the join and the launches `join`.  CTAs
 // run in waves of equal segments, or (documents, of any lengths) as SMs fall free: then the last one may start
 // when the others are done.
-//   tensor cores: 4.1 us for 128 tokens; start two chunks, states 0.55 (134 and 237 us on a row of 65536
-//   tokens, 32 heads), join and launches 16 us;
-//   fp32: 2 us for 32 tokens; start 0.5, states 0.6, join and launches 7 us.
+//   tensor cores: 3.8 us for 128 tokens; start two chunks, states 0.5 (109 and 218 us on a row of 65536
+//   tokens, 32 heads), join and launches 15 us;
+//   fp32: 3.3 us for 32 tokens; start 0.5, states 0.6, join and launches 6.6 us (3.5 units in place of 2: 128 tokens
+//   uncut, 16.3 us and not 12.6).
 constexpr int kSsmSms = 152;
 struct Costs {
     int64_t units;       // CTAs per segment over all heads, counted in CTAs that have an SM to themselves
@@ -122,9 +126,10 @@ Schedule make_schedule(const SsmShape& s, bool varlen, const Costs& k) {
     return w;
 }
 
-// Four CTAs of the fp32 kernel share an SM.
-Costs simt_costs(const SsmShape& s) { return {((int64_t)s.H * ((s.P + 31) / 32) + 3) / 4, 32, 0.5, 0.6, 3.5}; }
-Costs tc_costs(const SsmShape& s) { return {ssm_tc_units(s.H, s.G, s.P), 128, 2.0, 0.55, 4.0}; }
+// Two CTAs of the fp32 kernel share an SM, each 64 columns of P.
+int simt_parts(int P) { return (P + 63) / 64; }
+Costs simt_costs(const SsmShape& s) { return {((int64_t)s.H * simt_parts(s.P) + 1) / 2, 32, 0.5, 0.6, 2.0}; }
+Costs tc_costs(const SsmShape& s) { return {ssm_tc_units(s.H, s.G, s.P), 128, 2.0, 0.5, 4.0}; }
 
 // Segments of every row in order: ceil(len / L) of them, one empty segment for an empty row (its state
 // passes through).  Offsets that break the contract are recorded and give every row one empty segment.
@@ -231,21 +236,31 @@ __global__ void __launch_bounds__(128) ssm_join_kernel(SsmArgs a) {
 
 // ------------------------------------------------------------------ fp32 kernel
 //
-// A CTA takes one (segment, head, 32 columns of P); a warp four columns, eight lanes each, a lane
-// N / 8 state values of its column in registers (groups of four n, eight lanes apart, so that the
-// 16-byte reads of B and C from shared memory are free of conflicts).  Per token and state value: one
-// multiply and two fused multiply-adds; the eight lanes' partial outputs of eight tokens are summed
-// together (seven shuffles for eight tokens).  Bound by issue: about 2.5 instructions per state value.
-constexpr int kSimtTok = 16, kSimtCols = 32;
+// A CTA takes one (segment, head, 64 columns of P); a warp eight columns, eight lanes for two of them, a lane
+// N / 8 state values of each in registers (groups of four n, eight lanes apart, so that the 16-byte reads of B and
+// C from shared memory are free of conflicts).  Per token and state value: one multiply and two fused
+// multiply-adds, two columns to an instruction; the eight lanes' partial outputs of eight tokens are summed
+// together (seven shuffles for eight tokens and a column).  Bound by the shared memory's reads of B and C: a warp's
+// 16-byte read takes four cycles although its lanes want 128 bytes in all.  So a lane has two columns, not one: 4096
+// tokens x 32 heads of 128 x 64 take 266 us, with one column 500 us.  Few CTAs are bound by latency, some 150
+// cycles a token: 2 x 1021 tokens x 6 heads of 48 x 40 take 25 us, 37 us with one column and the element type asked
+// at every load.
+constexpr int kSimtCols = 64;
+constexpr int simt_tokens(int NJ) { return NJ <= 4 ? 32 : 16; }      // staged in shared memory at once
 
-template <int NJ, bool OUT>
-__global__ void __launch_bounds__(256, NJ <= 2 ? 3 : NJ == 4 ? 2 : 1) ssm_simt_kernel(SsmArgs a) {
-    constexpr int NP = 32 * NJ;
-    __shared__ __align__(16) float sb[kSimtTok][NP], sc[OUT ? kSimtTok : 1][NP];
-    __shared__ float sx[kSimtTok][kSimtCols], sy[kSimtTok][kSimtCols], sal[kSimtTok], sdt[kSimtTok];
+template <typename E> __device__ __forceinline__ float as_f32(E v);
+template <> __device__ __forceinline__ float as_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ float as_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+template <int NJ, bool OUT, typename E>
+__global__ void __launch_bounds__(256, NJ <= 4 ? 2 : 1) ssm_simt_kernel(SsmArgs a) {
+    constexpr int NP = 32 * NJ, TOK = simt_tokens(NJ);
+    __shared__ __align__(16) float sb[TOK][NP], sc[OUT ? TOK : 1][NP];
+    __shared__ __align__(8) float2 sx[TOK][kSimtCols / 2];      // y takes x's place
+    __shared__ __align__(8) float2 sad[TOK];                    // a token's decay and step
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int slice = lane & 7, pc = warp * 4 + (lane >> 3);
-    const int h = blockIdx.y, p0 = blockIdx.z * kSimtCols, p = p0 + pc;
+    const int slice = lane & 7, pp = warp * 4 + (lane >> 3);     // pair of columns
+    const int h = blockIdx.y, p0 = blockIdx.z * kSimtCols, p = p0 + 2 * pp;
     __shared__ SsmSeg found;
     const SsmSeg sg = ssm_segment(a, blockIdx.x, &found);
     if (sg.n < 0) return;
@@ -254,111 +269,122 @@ __global__ void __launch_bounds__(256, NJ <= 2 ? 3 : NJ == 4 ? 2 : 1) ssm_simt_k
         const int segs = ssm_row_segments(a, sg.n, &first);
         if ((int)blockIdx.x == first + segs - 1) return;
     }
-    const bool pin = p < a.P;
+    const bool in0 = p < a.P, in1 = p + 1 < a.P, works = p0 + 8 * warp < a.P;      // (the warp has columns)
     const int g = h / (a.H / a.G);
     const float ea = expf(a.a_log[h]), bias = a.dt_bias[h];
     const float dsk = OUT && a.d_skip ? a.d_skip[h] : 0.f;
-    float S[NJ][4];
+    float2 S[NJ][4];
     const float* from = OUT ? ssm_entering(a, sg, blockIdx.x, h) : nullptr;
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int n = (j * 8 + slice) * 4 + e;
-            S[j][e] = from && pin && n < a.N ? from[(size_t)n * a.P + p] : 0.f;
+            const bool in = from && n < a.N;
+            S[j][e] = make_float2(in && in0 ? from[(size_t)n * a.P + p] : 0.f, in && in1 ? from[(size_t)n * a.P + p + 1] : 0.f);
         }
     float lsum = 0.f;
-    // a block of tokens is loaded into registers while the one before it is worked on
-    constexpr int PB = kSimtTok * NP / 256, PX = kSimtTok * kSimtCols / 256;
-    float rb[PB], rc[OUT ? PB : 1], rx[PX], rdt = 0.f;
-    auto fetch = [&](int t0) {
-        const int nt = min(kSimtTok, sg.t1 - t0);
+    // a block of tokens is loaded into registers while the one before it is worked on; a thread has one column of b
+    // and c (NP divides 256 or is it), and one of x
+    constexpr int TB = 256 / NP, PB = TOK / TB, TX = 256 / kSimtCols, PX = TOK / TX;
+    const int bn = tid % NP, bt = tid / NP, xc = tid % kSimtCols, xt = tid / kSimtCols;
+    const bool bin = bn < a.N, xin = p0 + xc < a.P;
+    const E* pb = static_cast<const E*>(a.b) + (size_t)(sg.t0 + bt) * a.bs + (size_t)g * a.N + bn;
+    const E* pcc = static_cast<const E*>(a.c) + (size_t)(sg.t0 + bt) * a.cs + (size_t)g * a.N + bn;
+    const E* px = static_cast<const E*>(a.x) + (size_t)(sg.t0 + xt) * a.xs + (size_t)h * a.P + p0 + xc;
+    const E* pd = static_cast<const E*>(a.dt) + (size_t)(sg.t0 + tid) * a.ds + h;
+    E* py = static_cast<E*>(a.y) + ((size_t)(sg.t0 + xt) * a.H + h) * a.P + p0 + xc;
+    E rb[PB], rc[OUT ? PB : 1], rx[PX], rdt = E(0.f);
+    auto fetch = [&](int nt) {
 #pragma unroll
         for (int i = 0; i < PB; ++i) {
-            const int t = (tid + 256 * i) / NP, n = (tid + 256 * i) % NP;
-            const bool in = t < nt && n < a.N;
-            rb[i] = in ? load_act(a.b, (size_t)(t0 + t) * a.bs + (size_t)g * a.N + n, a.dtype) : 0.f;
-            if (OUT) rc[i] = in ? load_act(a.c, (size_t)(t0 + t) * a.cs + (size_t)g * a.N + n, a.dtype) : 0.f;
+            const bool in = bin && bt + i * TB < nt;
+            rb[i] = in ? pb[i * TB * a.bs] : E(0.f);
+            if (OUT) rc[i] = in ? pcc[i * TB * a.cs] : E(0.f);
         }
 #pragma unroll
-        for (int i = 0; i < PX; ++i) {
-            const int t = (tid + 256 * i) / kSimtCols, c = (tid + 256 * i) % kSimtCols;
-            rx[i] = t < nt && p0 + c < a.P ? load_act(a.x, (size_t)(t0 + t) * a.xs + (size_t)h * a.P + p0 + c, a.dtype) : 0.f;
-        }
-        if (tid < nt) rdt = load_act(a.dt, (size_t)(t0 + tid) * a.ds + h, a.dtype);
+        for (int i = 0; i < PX; ++i) rx[i] = xin && xt + i * TX < nt ? px[i * TX * a.xs] : E(0.f);
+        if (tid < nt) rdt = *pd;
+        pb += TOK * a.bs;
+        pcc += TOK * a.cs;
+        px += TOK * a.xs;
+        pd += TOK * a.ds;
     };
-    if (sg.t0 < sg.t1) fetch(sg.t0);
-    for (int t0 = sg.t0; t0 < sg.t1; t0 += kSimtTok) {
-        const int nt = min(kSimtTok, sg.t1 - t0);
+    if (sg.t0 < sg.t1) fetch(min(TOK, sg.t1 - sg.t0));
+    for (int t0 = sg.t0; t0 < sg.t1; t0 += TOK) {
+        const int nt = min(TOK, sg.t1 - t0);
+        float* fx = reinterpret_cast<float*>(sx);
 #pragma unroll
         for (int i = 0; i < PB; ++i) {
-            const int t = (tid + 256 * i) / NP, n = (tid + 256 * i) % NP;
-            sb[t][n] = rb[i];
-            if (OUT) sc[t][n] = rc[i];
+            sb[bt + i * TB][bn] = as_f32<E>(rb[i]);
+            if (OUT) sc[bt + i * TB][bn] = as_f32<E>(rc[i]);
         }
 #pragma unroll
-        for (int i = 0; i < PX; ++i) sx[(tid + 256 * i) / kSimtCols][(tid + 256 * i) % kSimtCols] = rx[i];
-        if (tid < kSimtTok) {
-            const float dt = tid < nt ? softplusf(rdt + bias) : 0.f;
-            sdt[tid] = dt;
-            sal[tid] = expf(-ea * dt);   // a token past the end keeps the state
+        for (int i = 0; i < PX; ++i) fx[(xt + i * TX) * kSimtCols + xc] = as_f32<E>(rx[i]);
+        if (tid < TOK) {
+            const float dt = tid < nt ? softplusf(as_f32<E>(rdt) + bias) : 0.f;
+            sad[tid] = make_float2(expf(-ea * dt), dt);   // a token past the end keeps the state
             if (!OUT) lsum += dt;
         }
         __syncthreads();
-        if (t0 + kSimtTok < sg.t1) fetch(t0 + kSimtTok);
-#pragma unroll
-        for (int t8 = 0; t8 < kSimtTok; t8 += 8) {
-            float y[8];
+        if (t0 + TOK < sg.t1) fetch(min(TOK, sg.t1 - t0 - TOK));
+#pragma unroll 1
+        for (int t8 = 0; t8 < nt && works; t8 += 8) {
+            float2 y[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
                 const int t = t8 + u;
-                const float al = sal[t], ux = sdt[t] * sx[t][pc];
-                float acc = 0.f;
+                const float2 ad = sad[t], al = dup(ad.x), ux = mul2(dup(ad.y), sx[t][pp]);
+                float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) {
                     const float4 b4 = *reinterpret_cast<const float4*>(&sb[t][(j * 8 + slice) * 4]);
-                    S[j][0] = fmaf(al, S[j][0], ux * b4.x);
-                    S[j][1] = fmaf(al, S[j][1], ux * b4.y);
-                    S[j][2] = fmaf(al, S[j][2], ux * b4.z);
-                    S[j][3] = fmaf(al, S[j][3], ux * b4.w);
+                    S[j][0] = fma2(al, S[j][0], mul2(ux, dup(b4.x)));
+                    S[j][1] = fma2(al, S[j][1], mul2(ux, dup(b4.y)));
+                    S[j][2] = fma2(al, S[j][2], mul2(ux, dup(b4.z)));
+                    S[j][3] = fma2(al, S[j][3], mul2(ux, dup(b4.w)));
                     if (OUT) {
                         const float4 c4 = *reinterpret_cast<const float4*>(&sc[t][(j * 8 + slice) * 4]);
-                        acc = fmaf(S[j][0], c4.x, acc);
-                        acc = fmaf(S[j][1], c4.y, acc);
-                        acc = fmaf(S[j][2], c4.z, acc);
-                        acc = fmaf(S[j][3], c4.w, acc);
+                        acc = fma2(S[j][0], dup(c4.x), acc);
+                        acc = fma2(S[j][1], dup(c4.y), acc);
+                        acc = fma2(S[j][2], dup(c4.z), acc);
+                        acc = fma2(S[j][3], dup(c4.w), acc);
                     }
                 }
                 y[u] = acc;
             }
-            if (OUT) {   // lane `slice` ends with the sum of token t8 + slice
+            if (OUT) {   // lane `slice` ends with the sums of token t8 + slice
 #pragma unroll
                 for (int w = 4; w >= 1; w >>= 1) {
                     const bool up = slice & w;
 #pragma unroll
                     for (int i = 0; i < w; ++i) {
-                        const float send = up ? y[i] : y[i + w], keep = up ? y[i + w] : y[i];
-                        y[i] = keep + __shfl_xor_sync(0xffffffffu, send, w);
+                        const float2 send = up ? y[i] : y[i + w], keep = up ? y[i + w] : y[i];
+                        y[i] = make_float2(keep.x + __shfl_xor_sync(0xffffffffu, send.x, w), keep.y + __shfl_xor_sync(0xffffffffu, send.y, w));
                     }
                 }
-                sy[t8 + slice][pc] = fmaf(dsk, sx[t8 + slice][pc], y[0]);
+                __syncwarp();      // the warp has read its columns' x
+                sx[t8 + slice][pp] = fma2(dup(dsk), sx[t8 + slice][pp], y[0]);
             }
         }
         __syncthreads();
-        if (OUT)
-            for (int i = tid; i < nt * kSimtCols; i += 256) {
-                const int t = i / kSimtCols, c = i - t * kSimtCols;
-                if (p0 + c < a.P) store_act(a.y, ((size_t)(t0 + t) * a.H + h) * a.P + p0 + c, sy[t][c], a.dtype);
-            }
+        if (OUT) {
+#pragma unroll
+            for (int i = 0; i < PX; ++i)
+                if (xin && xt + i * TX < nt) py[(size_t)i * TX * a.H * a.P] = E(fx[(xt + i * TX) * kSimtCols + xc]);
+            py += (size_t)TOK * a.H * a.P;
+            __syncthreads();      // the next block's x goes there
+        }
     }
     float* to = OUT ? ssm_leaving(a, sg, blockIdx.x, h) : a.states + ((size_t)blockIdx.x * a.H + h) * a.N * a.P;
-    if (to && pin)
+    if (to)
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int n = (j * 8 + slice) * 4 + e;
-                if (n < a.N) to[(size_t)n * a.P + p] = S[j][e];
+                if (n < a.N && in0) to[(size_t)n * a.P + p] = S[j][e].x;
+                if (n < a.N && in1) to[(size_t)n * a.P + p + 1] = S[j][e].y;
             }
     if (!OUT && blockIdx.z == 0 && warp == 0) {
         lsum = warp_sum(lsum);
@@ -371,15 +397,21 @@ __global__ void __launch_bounds__(256, NJ <= 2 ? 3 : NJ == 4 ? 2 : 1) ssm_simt_k
 cudaError_t launch_ssm_simt(const SsmArgs& a, bool out, cudaStream_t st) {
     const dim3 grid(a.nseg, a.H, (a.P + kSimtCols - 1) / kSimtCols);
     timing_pre(st, out ? K_SSM_OUT : K_SSM_STATE);
-#define KDA_SSM_SIMT(NJ)                                             \
-    do {                                                             \
-        if (out) ssm_simt_kernel<NJ, true><<<grid, 256, 0, st>>>(a); \
-        else ssm_simt_kernel<NJ, false><<<grid, 256, 0, st>>>(a);    \
+#define KDA_SSM_SIMT(NJ)                                                                         \
+    do {                                                                                         \
+        if (a.dtype == KDA_BF16) {                                                               \
+            if (out) ssm_simt_kernel<NJ, true, __nv_bfloat16><<<grid, 256, 0, st>>>(a);          \
+            else ssm_simt_kernel<NJ, false, __nv_bfloat16><<<grid, 256, 0, st>>>(a);             \
+        } else {                                                                                 \
+            if (out) ssm_simt_kernel<NJ, true, float><<<grid, 256, 0, st>>>(a);                  \
+            else ssm_simt_kernel<NJ, false, float><<<grid, 256, 0, st>>>(a);                     \
+        }                                                                                        \
     } while (0)
     if (a.N <= 32) KDA_SSM_SIMT(1);
     else if (a.N <= 64) KDA_SSM_SIMT(2);
     else if (a.N <= 128) KDA_SSM_SIMT(4);
     else KDA_SSM_SIMT(8);
+#undef KDA_SSM_SIMT
     timing_post(st);
     return cudaGetLastError();
 }
@@ -423,7 +455,7 @@ kda_status kda_ssm_fwd(const kda_ssm_dims* dims, const void* x, const void* dt_r
     if (st != KDA_OK) return st;
     // A few tokens to a row: one wave of the fp32 kernel's CTAs takes 4.6 to 7.4 us up to 16 tokens, the
     // tensor-core kernel 11.6 to 14.2 us however few they are (at 37 tokens both take as long)
-    const bool few = s.TT <= 16 * s.rows && (long long)s.rows * s.H * ((s.P + 31) / 32) <= 2 * kSsmSms;
+    const bool few = s.TT <= 16 * s.rows && (long long)s.rows * s.H * simt_parts(s.P) <= 2 * kSsmSms;
     const bool tc = !few && ssm_tc_ok(s, x, b, c, y);
     const Schedule w = make_schedule(s, cu_seqlens != nullptr, tc ? tc_costs(s) : simt_costs(s));
     if (workspace_bytes < w.total || (w.total && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256)))
