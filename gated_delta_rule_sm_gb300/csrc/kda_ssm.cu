@@ -453,9 +453,12 @@ kda_status kda_ssm_fwd(const kda_ssm_dims* dims, const void* x, const void* dt_r
     if (!y) return KDA_ERR_INVALID_ARG;
     st = check_offsets_host(s.rows, s.TT, cu_seqlens, cu_seqlens_host);
     if (st != KDA_OK) return st;
-    // A few tokens to a row: one wave of the fp32 kernel's CTAs takes 4.6 to 7.4 us up to 16 tokens, the
-    // tensor-core kernel 11.6 to 14.2 us however few they are (at 37 tokens both take as long)
-    const bool few = s.TT <= 16 * s.rows && (long long)s.rows * s.H * simt_parts(s.P) <= 2 * kSsmSms;
+    // A few tokens to a row.  The tensor-core kernel takes 10.6 to 13 us for a chunk, however few its tokens are; one
+    // wave of the fp32 kernel's CTAs 4.5 to 12.8 us up to 16 tokens, and with N up to 64 and an SM to each CTA 8.7 us
+    // for 37 tokens, 11.2 us for 64 (N 128, 32 heads: 13.4 and 17.8 us)
+    const int64_t ctas = (int64_t)s.rows * s.H * simt_parts(s.P);
+    const bool few = (s.TT <= 16 * (int64_t)s.rows && ctas <= 2 * kSsmSms) ||
+                     (s.TT <= 48 * (int64_t)s.rows && ctas <= kSsmSms && s.N <= 64);
     const bool tc = !few && ssm_tc_ok(s, x, b, c, y);
     const Schedule w = make_schedule(s, cu_seqlens != nullptr, tc ? tc_costs(s) : simt_costs(s));
     if (workspace_bytes < w.total || (w.total && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256)))

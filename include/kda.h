@@ -467,7 +467,7 @@ kda_status kda_decode_step(const kda_dims* dims, const void* q, const void* k, c
  * chunk are rounded to bf16 once (y is bf16), the entering state is read as the sum of two bf16 values,
  * and the state update keeps its operand as the sum of three (fp32 rounding).  There a non-finite x, B
  * or C spreads over its whole chunk instead of only the later tokens.  Every other shape, and calls of
- * at most 16 tokens to a row that one wave of CTAs covers, run an fp32 token-by-token kernel.
+ * a few tokens to a row that one wave of CTAs covers, run an fp32 token-by-token kernel.
  * Long rows with few rows x heads are cut into segments whose end states are computed in parallel and
  * joined before the outputs; the library chooses the cut.  Results do not depend on timing.
  * The workspace is kda_ssm_fwd_workspace_size() bytes (0 on invalid input).
