@@ -31,8 +31,8 @@
 // Bound: per chunk and unit 29 MFLOP (the state's three terms 12.6, C S 8.4) against 64 KB of x and y: 2.3 us and
 // 1.5 us of an SM's share at the measured rates.  Measured on a row of 65536 tokens, 32 heads, N 128, P 64: 218
 // us for the outputs, 3.8 us a chunk, and 109 us for the states, 1.9 us a chunk.  What holds the output pass is
-// shared memory: 320 KB of operands, 200 KB of the warps' reads and writes and 128 KB of copies a chunk, 5000
-// of 7200 cycles at 128 bytes a cycle; and the roles' loops together fill the instruction cache, which is why
+// shared memory: 320 KB of operands and 128 KB of copies at 128 bytes a cycle and 3200 accesses of the warps, some 6600
+// of a chunk's 7300 cycles; and the roles' loops together fill the instruction cache, which is why
 // they are kept short (M unrolled over its 32 columns and two copies of copy_state: 222 us).
 #include <cudaTypedefs.h>
 #include <string.h>
