@@ -188,3 +188,17 @@ def test_token_strides():
         stride(wide[..., ::2], 2)                       # values not contiguous
     with pytest.raises(ValueError):
         stride(wide[:, :4], 2)                          # rows not evenly spaced
+
+
+def test_binding_refuses_what_is_no_tensor():
+    t, v = torch.zeros(2, 4, 8), torch.zeros(4)
+    with pytest.raises(TypeError):
+        kda.ssm_step([[0.0]], t[..., 0], t, t, v, v, state=torch.zeros(2, 4, 8, 8))
+    with pytest.raises(TypeError):
+        kda.pages_free(None, None, None, None)
+    with pytest.raises(ValueError):
+        kda.decode_step(t, t, t, t, t[..., 0], v, v, scale=1.0, gate="no such gate", state=torch.zeros(2, 4, 8, 8))
+    with pytest.raises(ValueError):
+        kda.short_conv_step(torch.zeros(2, 8), torch.zeros(8, 4), history=torch.zeros(2, 3, 8))
+    with pytest.raises(TypeError):
+        _lib._native().ssm_step(t)                      # too few arguments
