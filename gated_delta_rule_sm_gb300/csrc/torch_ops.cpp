@@ -115,7 +115,8 @@ const int32_t* host_copy(PyObject* o) {      // an address, None: none
 }
 
 // Elements between neighbouring tokens of a tensor whose first `lead` axes are tokens ([B, T] or [B]) and whose other
-// axes are one token's contiguous values: it may be a slice of a wider projection.
+// axes are one token's contiguous values: it may be a slice of a wider projection.  Tokens that share memory are
+// refused: an expanded axis has stride 0, which is "contiguous" to the C entries.
 int64_t token_stride(const char* name, const Tensor& t, int lead) {
     const IntArrayRef size = t.sizes(), stride = t.strides();
     int64_t want = 1, step = -1, span = -1;
@@ -129,6 +130,9 @@ int64_t token_stride(const char* name, const Tensor& t, int lead) {
             else if (stride[k] != span) refuse(std::string(name) + ": tokens must be evenly spaced over the leading axes");
             span = stride[k] * size[k];
         }
+    if (step >= 0 && step < want)
+        refuse(std::string(name) + ": tokens must not share memory, got a stride of " + std::to_string(step) + " for " +
+               std::to_string(want) + " values (expanded tensors: call contiguous())");
     return step < 0 ? want : step;
 }
 

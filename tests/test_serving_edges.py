@@ -1,0 +1,38 @@
+"""GPU tests of the serving operators where a value, an argument or a buffer is unusual.
+
+Tolerances are those of the operators' parity tests unless a test derives its own."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+import gated_delta_rule_sm_gb300 as kda  # noqa: E402
+from test_serving import ARGS, DEV, ssm_inputs  # noqa: E402
+
+
+# ------------------------------------------------------------------------------------------- arguments
+
+
+@pytest.mark.parametrize("name", ["x", "b", "c", "dt_raw"])
+def test_expanded_tokens_are_refused(name):
+    i, _ = ssm_inputs(1, (1, 8), 2, 1, 16, 16, "bf16")
+    i[name] = i[name][:, :1].expand(i[name].shape)
+    with pytest.raises(ValueError):
+        kda.ssm_scan(*[i[n] for n in ARGS])
+    j, _ = ssm_inputs(1, (8,), 2, 1, 16, 16, "bf16")
+    j[name] = j[name][:1].expand(j[name].shape)
+    with pytest.raises(ValueError):
+        kda.ssm_step(*[j[n] for n in ARGS], state=torch.zeros(8, 2, 16, 16, device=DEV))
+
+
+def test_expanded_tokens_are_refused_by_the_convolution():
+    x, w = torch.zeros(1, 1, 64, device=DEV), torch.zeros(64, 4, device=DEV)
+    with pytest.raises(ValueError):
+        kda.short_conv_prompt(x.expand(1, 9, 64), w)
+    with pytest.raises(ValueError):
+        kda.short_conv_step(x[0].expand(9, 64), w, history=torch.zeros(9, 3, 64, device=DEV))
