@@ -133,7 +133,10 @@ __device__ __forceinline__ bool offsets_ok(const HistArgs& a) {
 
 __device__ __forceinline__ int row_begin(const HistArgs& a, int n) { return a.cu ? a.cu[n] : n * a.T; }
 
-// CTAs below `tiles` take a.tile tokens each; the others write the final history of one row each.
+// CTAs below `tiles` take a.tile tokens each; the others write the final history of one row each.  Where that goes
+// over the initial history, which the first tokens' CTAs read, they are a launch of their own after the tokens'
+// (tiles 0): there a thread reads and writes only its own channels of one row, the oldest input first, and its
+// reads are never behind its writes.
 template <int W, typename E>
 __global__ void __launch_bounds__(kHistThreads, W > 4 ? 3 : sizeof(E) == 2 ? 6 : 4) conv_prompt_kernel(HistArgs a) {
     if (a.cu && !offsets_ok(a)) {
@@ -334,6 +337,13 @@ kda_status kda_short_conv_prompt(int B, int T, int C, int W, kda_dtype dtype, co
     a.xs = x_stride ? x_stride : C;
     a.wide = reinterpret_cast<uintptr_t>(weight) % 16 == 0;
     a.x = x; a.w = weight; a.b = bias; a.cu = cu_seqlens; a.h_in = initial_history; a.h_out = final_history; a.y = y;
+    // other CTAs read what one writes: the results get memory of their own, but for histories in place
+    const size_t es = dtype == KDA_BF16 ? 2 : 4, nx = ((size_t)(a.TT - 1) * a.xs + C) * es, ny = (size_t)a.TT * C * es;
+    const size_t nh = (size_t)a.rows * (W - 1) * C * es;
+    const bool in_place = nh && final_history == initial_history;
+    if (ranges_meet(y, ny, x, nx) || ranges_meet(y, ny, initial_history, nh) || ranges_meet(y, ny, final_history, nh) ||
+        ranges_meet(final_history, nh, x, nx) || (!in_place && ranges_meet(final_history, nh, initial_history, nh)))
+        return KDA_ERR_INVALID_ARG;
     st = status_ptr(&a.status);
     if (st != KDA_OK) return st;
     timing_pre(stream, K_CONV_PROMPT);
@@ -346,8 +356,12 @@ kda_status kda_short_conv_prompt(int B, int T, int C, int W, kda_dtype dtype, co
         a.tile = (int)((work + ctas - 1) / ctas);
         if (a.tile < kHistLeast) a.tile = kHistLeast;
         a.tiles = (a.TT + a.tile - 1) / a.tile;
-        const dim3 grid(a.tiles + (final_history && w.value > 1 ? a.rows : 0), cols);
-        conv_prompt_kernel<w.value, E><<<grid, kHistThreads, 0, stream>>>(a);
+        const int ends = final_history && w.value > 1 ? a.rows : 0;
+        conv_prompt_kernel<w.value, E><<<dim3(a.tiles + (in_place ? 0 : ends), cols), kHistThreads, 0, stream>>>(a);
+        if (in_place) {
+            a.tiles = 0;
+            conv_prompt_kernel<w.value, E><<<dim3(ends, cols), kHistThreads, 0, stream>>>(a);
+        }
         return cudaGetLastError();
     });
     timing_post(stream);

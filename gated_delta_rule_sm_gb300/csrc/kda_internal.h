@@ -142,6 +142,12 @@ kda_status status_ptr(int** out);
 // The packed-document contract on a host copy of the offsets (KDA_OK without one).
 kda_status check_offsets_host(int rows, int TT, const int32_t* cu, const int32_t* cu_host);
 
+// Whether two arrays share a byte (a NULL one shares none).
+inline bool ranges_meet(const void* p, size_t np, const void* q, size_t nq) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return p && q && np && nq && a < b + nq && b < a + np;
+}
+
 // A checked kda_ssm_dims, strides resolved.
 struct SsmShape {
     int B, T, TT, H, G, N, P, dtype, rows;

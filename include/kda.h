@@ -496,6 +496,8 @@ kda_status kda_ssm_step(const kda_ssm_dims* dims, const void* x, const void* dt_
  * included where the segment is shorter.  rows = B, or num_seqs with cu_seqlens (contract as for
  * kda_ssm_fwd: a device-only violation is recorded in the status word and nothing is written).
  * x_stride: elements between neighbouring tokens of x (0: C).  y is contiguous.
+ * final_history may be initial_history itself (in place: one launch more); any other overlap of y or
+ * final_history with each other, x or initial_history is KDA_ERR_INVALID_ARG.
  * Errors as for kda_short_conv_fwd; x_stride not a multiple of 8, or a history pointer that is not
  * 16-byte aligned, is KDA_ERR_UNSUPPORTED.
  */

@@ -3,6 +3,7 @@
 Tolerances are those of the operators' parity tests unless a test derives its own."""
 from __future__ import annotations
 
+import numpy as np
 import pytest
 import torch
 
@@ -12,7 +13,7 @@ if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
 import gated_delta_rule_sm_gb300 as kda  # noqa: E402
-from test_serving import ARGS, DEV, ssm_inputs  # noqa: E402
+from test_serving import ARGS, DEV, DT, randn, ssm_inputs  # noqa: E402
 
 
 # ------------------------------------------------------------------------------------------- arguments
@@ -36,3 +37,26 @@ def test_expanded_tokens_are_refused_by_the_convolution():
         kda.short_conv_prompt(x.expand(1, 9, 64), w)
     with pytest.raises(ValueError):
         kda.short_conv_step(x[0].expand(9, 64), w, history=torch.zeros(9, 3, 64, device=DEV))
+
+
+# ------------------------------------------------------------------------------------------- convolution
+
+
+@pytest.mark.parametrize("W", [1, 2, 4, 8])
+@pytest.mark.parametrize("dtype,C", [("bf16", 1032), ("fp32", 64)])
+@pytest.mark.parametrize("lengths", [[1] * 5, [0, 3, 2000, 1, 0, 0, 7, 2, 5, 600, 0], [1500] * 3])
+def test_conv_history_in_place(W, dtype, C, lengths):
+    """final_history over initial_history gives what separate buffers give: rows shorter than the window,
+    empty ones, and rows that many CTAs read."""
+    rows, T = len(lengths), sum(lengths)
+    g = torch.Generator().manual_seed(T + W)
+    x = randn(g, 1, T, C).to(DT[dtype]).to(DEV)
+    w, h = randn(g, C, W).to(DEV), randn(g, rows, W - 1, C).to(DT[dtype]).to(DEV)
+    cu = torch.tensor([0, *np.cumsum(lengths).tolist()], dtype=torch.int32, device=DEV)
+    y, last = kda.short_conv_prompt(x, w, cu_seqlens=cu, initial_history=h)
+    for _ in range(5):
+        k = h.clone()
+        y2, last2 = kda.short_conv_prompt(x, w, cu_seqlens=cu, initial_history=k, final_history=k)
+        assert last2 is k
+        assert torch.equal(y, y2) and torch.equal(last, k)
+    assert kda.device_status() == 0
