@@ -300,13 +300,14 @@ __global__ void __launch_bounds__(kCopyThreads) pages_extend_kernel(PageArgs a) 
         const bool done = ok || need == 0;
         if (threadIdx.x == 0) a.ok[i] = done;
         if (!done) continue;
-        const int s = a.ra[i], had = pages_of(a, a.lengths[s]);
+        // (the length may be another's already where a row is named twice: what the request was checked with stays
+        // inside the row)
+        const int s = a.ra[i], had = pages_of(a, a.rb[i]) - need;
         for (int j = threadIdx.x; j < need; j += kCopyThreads) {
             const int p = a.list[rank + j];
             a.table_o[(size_t)s * a.M + had + j] = p;
             a.refs_o[p] = 1;
         }
-        __syncthreads();   // every thread has read the old length
         if (threadIdx.x == 0) a.lengths_o[s] = a.rb[i];
     }
 }

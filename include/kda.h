@@ -532,7 +532,8 @@ kda_status kda_short_conv_step(int B, int C, int W, kda_dtype dtype, const void*
  * kda_pages_extend: row seqs[i] grows to new_lengths[i] tokens and gets the pages that needs.  ok[i] is 0
  *   and nothing is done for a row out of range, a length below the present one or above
  *   max_pages * page_tokens, or too few free pages left (requests are served in order; one that finds
- *   too few is refused and its pages are not given to later ones).  seqs must not repeat.
+ *   too few is refused and its pages are not given to later ones).  seqs must not repeat (a row named
+ *   twice stays inside its table row, but the pages of one of its requests are lost).
  * kda_pages_free: drops the references of rows seqs[i], clears the rows and their lengths.  Rows out of
  *   range are skipped; seqs must not repeat.
  * kda_pages_compact: moves the live pages to the lowest indices.  With L live pages, the k-th highest live

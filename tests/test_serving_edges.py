@@ -13,7 +13,7 @@ if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
 import gated_delta_rule_sm_gb300 as kda  # noqa: E402
-from test_serving import ARGS, DEV, DT, randn, ssm_inputs  # noqa: E402
+from test_serving import ARGS, DEV, DT, ints, randn, ssm_inputs  # noqa: E402
 
 
 # ------------------------------------------------------------------------------------------- arguments
@@ -60,3 +60,20 @@ def test_conv_history_in_place(W, dtype, C, lengths):
         assert last2 is k
         assert torch.equal(y, y2) and torch.equal(last, k)
     assert kda.device_status() == 0
+
+
+# ------------------------------------------------------------------------------------------- pages
+
+
+def test_extend_of_a_row_named_twice_stays_in_its_row():
+    """Against the contract, but known to the device only: nothing outside the row is written."""
+    S, M, pt = 4, 6, 4
+    for _ in range(20):
+        wide = torch.full((S + 2, M), -1, dtype=torch.int32, device=DEV)
+        lens = torch.zeros(S, dtype=torch.int32, device=DEV)
+        refs = torch.zeros(64, dtype=torch.int32, device=DEV)
+        kda.pages_extend(wide[:S], lens, refs, ints(*[S - 1] * 8, 0), ints(*[M * pt] * 8, 5), page_tokens=pt)
+        rows = wide.tolist()
+        assert rows[1:S - 1] == [[-1] * M] * (S - 2) and rows[S:] == [[-1] * M] * 2
+        assert all(0 <= p < 64 for p in rows[S - 1]) and lens.tolist() == [5, 0, 0, M * pt]
+        assert rows[0][2:] == [-1] * (M - 2)
