@@ -8,6 +8,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -164,25 +165,37 @@ PyObject* pair(PyObject* a, PyObject* b) {      // takes both references
     return r;
 }
 
-// One workspace per device, kind and stream: calls on different streams may overlap.
-void* scratch(const Tensor& like, const char* kind, cudaStream_t st, size_t bytes, size_t* size) {
-    PyObject* key = Py_BuildValue("(isK)", (int)like.get_device(), kind, (unsigned long long)reinterpret_cast<uintptr_t>(st));
-    if (!key) throw Raised();
-    PyObject* had = PyDict_GetItemWithError(g_scratch, key);
-    if (had && THPVariable_Check(had) && (size_t)THPVariable_Unpack(had).numel() >= bytes) {
-        Py_DECREF(key);
-        *size = (size_t)THPVariable_Unpack(had).numel();
-        return THPVariable_Unpack(had).data_ptr();
+// A call's workspace: one per device, kind and stream (calls on different streams may overlap), grown on demand.  While
+// the stream is captured the call gets a buffer of its own, which the graph keeps: a kept one may be given up for a
+// larger one later, and one made here would belong to the graph.
+struct Scratch {
+    Tensor own;
+    void* p;
+    size_t size;
+    Scratch(const Tensor& like, const char* kind, cudaStream_t st, size_t bytes) {
+        const int64_t want = (int64_t)(bytes > 256 ? bytes : 256);
+        if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) {
+            own = fresh(like, {want}, at::kByte);
+        } else {
+            PyObject* key = Py_BuildValue("(isK)", (int)like.get_device(), kind, (unsigned long long)reinterpret_cast<uintptr_t>(st));
+            if (!key) throw Raised();
+            PyObject* had = PyDict_GetItemWithError(g_scratch, key);
+            if (had && THPVariable_Check(had) && (size_t)THPVariable_Unpack(had).numel() >= bytes) {
+                Py_DECREF(key);
+                own = THPVariable_Unpack(had);
+            } else {
+                own = fresh(like, {want}, at::kByte);
+                PyObject* o = THPVariable_Wrap(own);
+                const bool kept = o && PyDict_SetItem(g_scratch, key, o) == 0;
+                Py_DECREF(key);
+                Py_XDECREF(o);
+                if (!kept) throw Raised();
+            }
+        }
+        p = own.data_ptr();
+        size = (size_t)own.numel();
     }
-    const Tensor t = fresh(like, {(int64_t)(bytes > 256 ? bytes : 256)}, at::kByte);
-    PyObject* o = THPVariable_Wrap(t);
-    const bool kept = o && PyDict_SetItem(g_scratch, key, o) == 0;
-    Py_DECREF(key);
-    Py_XDECREF(o);
-    if (!kept) throw Raised();
-    *size = (size_t)t.numel();
-    return t.data_ptr();
-}
+};
 
 // ------------------------------------------------------------------ state space scan and step
 
@@ -276,10 +289,9 @@ PyObject* ssm_scan(PyObject* const* o) {
         last = f.given;
         pf = f.p;
     }
-    size_t size;
-    void* ws = scratch(*s.x, "ssm", st, ssm_workspace(s.dims), &size);
+    const Scratch ws(*s.x, "ssm", st, ssm_workspace(s.dims));
     check(kda_ssm_fwd(&s.dims, s.x->data_ptr(), s.dt->data_ptr(), s.b->data_ptr(), s.c->data_ptr(), s.a_log, s.dt_bias,
-                      s.d_skip, cu, host_copy(o[8]), s0, out.p, static_cast<float*>(pf), ws, size, st), "kda_ssm_fwd");
+                      s.d_skip, cu, host_copy(o[8]), s0, out.p, static_cast<float*>(pf), ws.p, ws.size, st), "kda_ssm_fwd");
     return pair(out.object(), last ? Py_NewRef(last) : THPVariable_Wrap(own));
 }
 
@@ -477,9 +489,8 @@ PyObject* pages_fork(PyObject* const* o) {
     const int32_t *pa = need_i("parents", o[4], {n}, c.dev), *ch = need_i("children", o[5], {n}, c.dev);
     const cudaStream_t st = current_stream(c.dev);
     const Result ok("ok", o[10], *c.table, {n}, at::kInt);
-    size_t size;
-    void* ws = scratch(*c.table, "pages", st, kda_pages_workspace_size(&c.d, as_int("requests", n)), &size);
-    check(kda_pages_fork(&c.d, c.pool, c.t, c.l, c.r, pa, ch, (int)n, c.t_out, c.l_out, c.r_out, static_cast<int32_t*>(ok.p), ws, size,
+    const Scratch ws(*c.table, "pages", st, kda_pages_workspace_size(&c.d, as_int("requests", n)));
+    check(kda_pages_fork(&c.d, c.pool, c.t, c.l, c.r, pa, ch, (int)n, c.t_out, c.l_out, c.r_out, static_cast<int32_t*>(ok.p), ws.p, ws.size,
                          st), "kda_pages_fork");
     return ok.object();
 }
@@ -491,9 +502,8 @@ PyObject* pages_extend(PyObject* const* o) {
     const int32_t *seqs = need_i("seqs", o[3], {n}, c.dev), *lens = need_i("new_lengths", o[4], {n}, c.dev);
     const cudaStream_t st = current_stream(c.dev);
     const Result ok("ok", o[9], *c.table, {n}, at::kInt);
-    size_t size;
-    void* ws = scratch(*c.table, "pages", st, kda_pages_workspace_size(&c.d, as_int("requests", n)), &size);
-    check(kda_pages_extend(&c.d, c.t, c.l, c.r, seqs, lens, (int)n, c.t_out, c.l_out, c.r_out, static_cast<int32_t*>(ok.p), ws, size,
+    const Scratch ws(*c.table, "pages", st, kda_pages_workspace_size(&c.d, as_int("requests", n)));
+    check(kda_pages_extend(&c.d, c.t, c.l, c.r, seqs, lens, (int)n, c.t_out, c.l_out, c.r_out, static_cast<int32_t*>(ok.p), ws.p, ws.size,
                            st), "kda_pages_extend");
     return ok.object();
 }
@@ -514,9 +524,8 @@ PyObject* pages_compact(PyObject* const* o) {
     const Cache c = cache_in(o[0], o[1], Py_None, o[2], o[3], Py_None, o[4], 1);
     const cudaStream_t st = current_stream(c.dev);
     const Result map("page_map", o[5], *c.table, {(int64_t)c.d.num_pages}, at::kInt);
-    size_t size;
-    void* ws = scratch(*c.table, "pages", st, kda_pages_workspace_size(&c.d, 0), &size);
-    check(kda_pages_compact(&c.d, c.pool, c.t, c.r, c.t_out, c.r_out, static_cast<int32_t*>(map.p), ws, size, st),
+    const Scratch ws(*c.table, "pages", st, kda_pages_workspace_size(&c.d, 0));
+    check(kda_pages_compact(&c.d, c.pool, c.t, c.r, c.t_out, c.r_out, static_cast<int32_t*>(map.p), ws.p, ws.size, st),
           "kda_pages_compact");
     return map.object();
 }

@@ -13,7 +13,8 @@ if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
 import gated_delta_rule_sm_gb300 as kda  # noqa: E402
-from test_serving import ARGS, DEV, DT, ints, randn, ssm_inputs  # noqa: E402
+from gated_delta_rule_sm_gb300 import _lib  # noqa: E402
+from test_serving import ARGS, DEV, DT, cache, ints, randn, ssm_inputs  # noqa: E402
 
 
 # ------------------------------------------------------------------------------------------- arguments
@@ -77,3 +78,59 @@ def test_extend_of_a_row_named_twice_stays_in_its_row():
         assert rows[1:S - 1] == [[-1] * M] * (S - 2) and rows[S:] == [[-1] * M] * 2
         assert all(0 <= p < 64 for p in rows[S - 1]) and lens.tolist() == [5, 0, 0, M * pt]
         assert rows[0][2:] == [-1] * (M - 2)
+
+
+# ------------------------------------------------------------------------------------------- captured calls
+
+
+def test_captured_calls_keep_their_workspaces():
+    """A graph's workspaces are its own: later calls on its stream that want more do not take them away, and its
+    replays write nobody else's memory."""
+    small, _ = ssm_inputs(61, (1, 3000), 2, 1, 64, 64, "bf16")
+    large, _ = ssm_inputs(62, (1, 9000), 4, 1, 64, 64, "bf16")
+    pool, table, lens, refs = cache(3, 6, 4, 40, 4, 64, lengths=[9, 5, 1, 0, 0, 0])
+    outs = [torch.empty_like(t) for t in (table, lens, refs)]
+    kw = dict(page_tokens=4, table_out=outs[0], lengths_out=outs[1], refs_out=outs[2])
+    parents, children = ints(0, 1), ints(3, 4)
+    side = torch.cuda.Stream()
+
+    def calls():
+        y, S = kda.ssm_scan(*[small[n] for n in ARGS], output_final_state=True)
+        return y, S, kda.pages_fork(pool, table, lens, refs, parents, children, **kw), *outs
+
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        want = [t.clone() for t in calls()]
+    side.synchronize()
+    kept = {k: (t.data_ptr(), t.numel()) for k, t in _lib.workspace_cache.buf.items()}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = calls()
+    assert {k: (t.data_ptr(), t.numel()) for k, t in _lib.workspace_cache.buf.items()} == kept
+    with torch.cuda.stream(side):
+        kda.ssm_scan(*[large[n] for n in ARGS], output_final_state=True)       # wants more
+        sizes = [n for _, n in kept.values()]
+        others = [torch.full((n,), 7, dtype=torch.uint8, device=DEV) for n in sizes for _ in range(3)]
+        for t in outs:
+            t.fill_(99)
+        graph.replay()
+        graph.replay()
+    side.synchronize()
+    assert max(t.numel() for t in _lib.workspace_cache.buf.values()) > max(sizes)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all(bool((t == 7).all()) for t in others)
+    assert kda.device_status() == 0
+
+
+def test_first_call_on_a_stream_may_be_captured():
+    i, _ = ssm_inputs(63, (1, 3000), 2, 1, 64, 64, "bf16")
+    want, _ = kda.ssm_scan(*[i[n] for n in ARGS])
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    before = set(_lib.workspace_cache.buf)
+    with torch.cuda.graph(graph, stream=side):
+        got, _ = kda.ssm_scan(*[i[n] for n in ARGS])
+    assert set(_lib.workspace_cache.buf) == before
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and kda.device_status() == 0
