@@ -9,6 +9,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -535,6 +536,14 @@ PyObject* token_stride_of(PyObject* const* o) { return PyLong_FromLongLong(token
 
 // ------------------------------------------------------------------ module
 
+// The device of a call: its first CUDA tensor's (the checks hold the others to it); -1 without one.
+int device_of(PyObject* const* args, Py_ssize_t n) {
+    for (Py_ssize_t i = 0; i < n; ++i)
+        if (THPVariable_Check(args[i]) && THPVariable_Unpack(args[i]).is_cuda()) return (int)THPVariable_Unpack(args[i]).get_device();
+    return -1;
+}
+
+// Launches, function attributes and the status word's address are the current device's: it is the tensors' for the call.
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -542,7 +551,10 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
         PyErr_Format(PyExc_TypeError, "expected %d arguments, got %zd", N, n);
         return nullptr;
     }
+    c10::cuda::OptionalCUDAGuard guard;
     try {
+        const int dev = device_of(args, n);
+        if (dev >= 0) guard.set_index((c10::DeviceIndex)dev);
         return F(args);
     } catch (const Refused& e) {
         PyErr_SetString(e.type, e.what.c_str());
@@ -550,6 +562,13 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     } catch (const Raised&) {
         return nullptr;
     }
+    END_HANDLE_TH_ERRORS
+}
+
+// device_of(...): the device that a call with these arguments runs on, -1: none
+PyObject* device_of_args(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    return PyLong_FromLong(device_of(args, n));
     END_HANDLE_TH_ERRORS
 }
 
@@ -575,6 +594,7 @@ PyMethodDef methods[] = {
     method<pages_copy, 4>("pages_copy"), method<pages_fork, 11>("pages_fork"), method<pages_extend, 10>("pages_extend"),
     method<pages_free, 7>("pages_free"), method<pages_compact, 6>("pages_compact"),
     method<token_stride_of, 2>("token_stride"),
+    {"device_of", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&device_of_args)), METH_FASTCALL, nullptr},
     {"setup", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&setup)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -31,3 +31,14 @@ def test_overlapping_tokens_have_no_stride(ops):
     with pytest.raises(ValueError):
         ops.token_stride(torch.zeros(1, 5, 4).expand(3, 5, 4), 2)       # each row of tokens the same memory
     assert ops.token_stride(flat.as_strided((1, 6, 8), (0, 9, 1)), 2) == 9
+
+
+def test_a_call_runs_on_its_tensors_device(ops):
+    """Whatever device is current.  (Fake tensors: a device's number without the device.)"""
+    fake = pytest.importorskip("torch._subclasses.fake_tensor").FakeTensorMode
+    with fake():
+        here, there = torch.empty(2, 3, device="cuda:0"), torch.empty(2, 3, device="cuda:1")
+    host = torch.zeros(2)
+    assert ops.device_of(there) == 1 and ops.device_of(here) == 0
+    assert ops.device_of(None, 3, host, there) == 1          # the first CUDA tensor decides
+    assert ops.device_of() == ops.device_of(None, host, [1]) == -1
