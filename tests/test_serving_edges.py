@@ -7,6 +7,8 @@ import numpy as np
 import pytest
 import torch
 
+import serving_ref as ref
+
 pytestmark = pytest.mark.gpu
 
 if not torch.cuda.is_available():
@@ -41,6 +43,33 @@ def test_expanded_tokens_are_refused_by_the_convolution():
 
 
 # ------------------------------------------------------------------------------------------- convolution
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("step", [False, True])
+def test_conv_far_below_zero(dtype, step):
+    """y = a sigmoid(a) tends to zero as a falls, and is -inf * 0 at -inf; each value beside an ordinary one.
+
+    fp32: the exponent of 2 is up to 60 and rounded to 2^-24 of itself, which is 2.5e-6 of the exponential, and a
+    few roundings follow: 1e-5.  Below a = -60 ln 2 the result may be 0, which is 60 ln 2 / 2^60 = 4e-17 off."""
+    low = [-30.0, -40.0, -41.0, -42.0, -50.0, -64.0, -88.0, -1e3, -1e12, -1e20, -3e38, float("-inf")]
+    a = torch.tensor([v for i, x in enumerate(low) for v in ((x, 0.7 - i) if i % 2 else (i - 5.3, x))]).to(DT[dtype])
+    C = a.numel()
+    assert C % 8 == 0
+    w = torch.zeros(C, 4)
+    w[:, 3] = 1.0
+    if step:
+        h = torch.zeros(1, 3, C, dtype=DT[dtype], device=DEV)
+        y, _ = kda.short_conv_step(a[None].to(DEV), w.to(DEV), history=h)
+    else:
+        y, _ = kda.short_conv_prompt(a[None, None].to(DEV), w.to(DEV))
+    torch.cuda.synchronize()
+    y, want = ref.d(y).flatten(), ref.d(a) * torch.sigmoid(ref.d(a))
+    nan = torch.isnan(want)
+    assert int(nan.sum()) == 1 and torch.equal(torch.isnan(y), nan)
+    rel = 2.0 ** -8 if dtype == "bf16" else 1e-5
+    err = (y - want).abs()[~nan]
+    assert bool((err <= rel * want.abs()[~nan] + 1e-16).all()), (err - rel * want.abs()[~nan]).max()
 
 
 @pytest.mark.parametrize("W", [1, 2, 4, 8])
