@@ -84,10 +84,12 @@ class StateCache:
         return self.table[rows.long(), 0].contiguous()
 
     def fork(self, parents, children):
-        """children go on from copies of the parents' states."""
+        """children go on from copies of the parents' states.  Returns ok: 0 where nothing was done (no free page, or
+        the child holds one)."""
         first, *others = self.every_pool()
         ok = pages_fork(first, self.table, self.lengths, self.refs, parents, children, page_tokens=WHOLE)
         src, dst = self.slots(parents), self.slots(children)
+        dst = torch.where(ok > 0, dst, -1)       # pairs out of range are skipped
         for pool in others:
             pages_copy(pool, src, dst)
         return ok

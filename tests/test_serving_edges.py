@@ -15,7 +15,7 @@ if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
 import gated_delta_rule_sm_gb300 as kda  # noqa: E402
-from gated_delta_rule_sm_gb300 import _lib  # noqa: E402
+from gated_delta_rule_sm_gb300 import _lib, serve  # noqa: E402
 from test_serving import ARGS, DEV, DT, cache, ints, randn, ssm_inputs  # noqa: E402
 
 
@@ -163,3 +163,24 @@ def test_first_call_on_a_stream_may_be_captured():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(got, want) and kda.device_status() == 0
+
+
+# ------------------------------------------------------------------------------------------- the served decoder
+
+
+def test_refused_fork_leaves_every_pool():
+    """A child that still holds its page keeps it, in every layer's pools; the other request is served."""
+    model = serve.Decoder(layers=2, heads=2, groups=1, dim=32, head_dim=16, state_dim=16)
+    cch = serve.StateCache(model, slots=6, sequences=4)
+    assert cch.admit(ints(0, 1), ints(5, 9)).tolist() == [1, 1]
+    for k, pool in enumerate(cch.every_pool()):
+        pool.copy_(torch.randn(pool.shape, generator=torch.Generator().manual_seed(k)).to(pool.dtype))
+    before = [pool.clone() for pool in cch.every_pool()]
+    held, parent = cch.slots(ints(1)).item(), cch.slots(ints(0)).item()
+    assert cch.fork(ints(0, 0), ints(1, 2)).tolist() == [0, 1]
+    child = cch.slots(ints(2)).item()
+    assert cch.slots(ints(1)).item() == held and child not in (held, parent)
+    for pool, old in zip(cch.every_pool(), before):
+        old[:, child] = old[:, parent]
+        assert torch.equal(pool, old)
+    assert kda.device_status() == 0
