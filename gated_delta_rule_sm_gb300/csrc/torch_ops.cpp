@@ -280,7 +280,8 @@ PyObject* ssm_scan(PyObject* const* o) {
     const float* s0 = need_f("initial_state", o[9], state, s.dev);
     const cudaStream_t st = current_stream(s.dev);
     const Result out("out", o[11], *s.x, s.x->sizes(), s.x->scalar_type());
-    const bool wants = PyObject_IsTrue(o[10]) == 1;
+    const int wants = PyObject_IsTrue(o[10]);
+    if (wants < 0) throw Raised();
     PyObject* last = Py_None;
     void* pf = nullptr;
     Tensor own;

@@ -42,6 +42,17 @@ def test_expanded_tokens_are_refused_by_the_convolution():
         kda.short_conv_step(x[0].expand(9, 64), w, history=torch.zeros(9, 3, 64, device=DEV))
 
 
+def test_scan_flag_that_raises():
+    class Flag:
+        def __bool__(self):
+            raise ArithmeticError("no truth value")
+
+    i, _ = ssm_inputs(1, (1, 8), 2, 1, 16, 16, "bf16")
+    with pytest.raises(ArithmeticError):
+        kda.ssm_scan(*[i[n] for n in ARGS], output_final_state=Flag())
+
+
+
 # ------------------------------------------------------------------------------------------- convolution
 
 
