@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(256, NJ <= 4 ? 2 : 1) ssm_simt_kernel(SsmArgs 
     }
     const bool in0 = p < a.P, in1 = p + 1 < a.P, works = p0 + 8 * warp < a.P;      // (the warp has columns)
     const int g = h / (a.H / a.G);
-    const float ea = expf(a.a_log[h]), bias = a.dt_bias[h];
+    const float ea = ssm_rate(a.a_log[h]), bias = a.dt_bias[h];
     const float dsk = OUT && a.d_skip ? a.d_skip[h] : 0.f;
     float2 S[NJ][4];
     const float* from = OUT ? ssm_entering(a, sg, blockIdx.x, h) : nullptr;

@@ -74,6 +74,13 @@ __device__ __forceinline__ int ssm_row_segments(const SsmArgs& a, int n, int* fi
     return a.per_row;
 }
 
+// exp(a_log), kept finite: tokens past a row's end have the step 0, and infinity times that is no number.  Any step
+// above 1e-36 forgets everything at the limit as it would at infinity.
+__device__ __forceinline__ float ssm_rate(float a_log) {
+    const float e = expf(a_log);
+    return e > 1e38f ? 1e38f : e;      // (a NaN stays one)
+}
+
 // The state a segment starts from (nullptr: zero) and where its end state goes (nullptr: nowhere).
 __device__ __forceinline__ const float* ssm_entering(const SsmArgs& a, const SsmSeg& s, int seg, int h) {
     const size_t np = (size_t)a.N * a.P;

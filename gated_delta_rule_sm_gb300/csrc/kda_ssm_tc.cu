@@ -733,7 +733,7 @@ ssm_tc_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ CUtenso
         const int sl = SAME ? 0 : lane >> 4, l = lane & 15, blk = l >> 2;
         const int h = un.h[sl];
         const bool writes = !SAME || lane < 16;
-        const float es = h >= 0 ? expf(a.a_log[h]) * kLog2e : 0.f, bias = h >= 0 ? a.dt_bias[h] : 0.f;
+        const float es = h >= 0 ? ssm_rate(a.a_log[h]) * kLog2e : 0.f, bias = h >= 0 ? a.dt_bias[h] : 0.f;
         float total = 0.f;
         const uint16_t* dt = static_cast<const uint16_t*>(a.dt) + (size_t)(sg.t0 + 8 * l) * a.ds + (h >= 0 ? h : 0);
         uint32_t next[8];      // dt_raw, requested a chunk ahead: under load it takes longer than a chunk's decays

@@ -16,7 +16,7 @@ if not torch.cuda.is_available():
 
 import gated_delta_rule_sm_gb300 as kda  # noqa: E402
 from gated_delta_rule_sm_gb300 import _lib, serve  # noqa: E402
-from test_serving import ARGS, DEV, DT, cache, ints, randn, ssm_inputs  # noqa: E402
+from test_serving import ARGS, DEV, DT, cache, check_scan, ints, randn, run_scan, ssm_inputs  # noqa: E402
 
 
 # ------------------------------------------------------------------------------------------- arguments
@@ -51,6 +51,20 @@ def test_scan_flag_that_raises():
     with pytest.raises(ArithmeticError):
         kda.ssm_scan(*[i[n] for n in ARGS], output_final_state=Flag())
 
+
+# ------------------------------------------------------------------------------------------- scan
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T", [5, 200, 3001])
+def test_scan_with_a_decay_rate_past_fp32(dtype, T):
+    """exp(a_log) is infinite in fp32: every token forgets what was before it, also in a row that ends inside a
+    block of tokens."""
+    i, g = ssm_inputs(51, (1, T), 2, 1, 64, 64, dtype)
+    i["a_log"][0] = 100.0
+    S0 = randn(g, 1, 2, 64, 64).to(DEV)
+    y, S = run_scan(i, initial_state=S0, output_final_state=True)
+    check_scan(i, [0, T], S0, y, S, dtype, dtype == "bf16")
 
 
 # ------------------------------------------------------------------------------------------- convolution
