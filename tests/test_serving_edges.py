@@ -16,7 +16,7 @@ if not torch.cuda.is_available():
 
 import gated_delta_rule_sm_gb300 as kda  # noqa: E402
 from gated_delta_rule_sm_gb300 import _lib, serve  # noqa: E402
-from test_serving import ARGS, DEV, DT, cache, check_scan, ints, randn, run_scan, ssm_inputs  # noqa: E402
+from test_serving import ARGS, DEV, DT, cache, check_scan, ints, randn, run_scan, same, ssm_inputs  # noqa: E402
 
 
 # ------------------------------------------------------------------------------------------- arguments
@@ -118,6 +118,86 @@ def test_conv_history_in_place(W, dtype, C, lengths):
 
 
 # ------------------------------------------------------------------------------------------- pages
+
+
+def many(*v):
+    return torch.tensor(np.asarray(v).reshape(-1), dtype=torch.int32, device=DEV)
+
+
+def outputs(table, lens, refs, in_place):
+    if in_place:
+        return {}
+    return dict(table_out=torch.full_like(table, 7), lengths_out=torch.full_like(lens, 7), refs_out=torch.full_like(refs, 7))
+
+
+# one pass over the pages (up to 16384 of them) with several tiles, and two passes; the free pages lie in all tiles
+@pytest.mark.parametrize("pages", [5000, 9000, 16384, 16385, 40000])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_fork_and_extend_over_many_tiles(pages, in_place):
+    S, M, pt = pages // 4, 8, 4
+    rng = np.random.default_rng(pages)
+    lengths = rng.integers(1, M * pt + 1, S)
+    children = rng.permutation(S)[:S // 3]
+    lengths[children] = 0
+    pool, table, lens, refs = cache(pages, S, M, pages, pt, 8, layers=2, lengths=lengths)
+    r = ref.Cache(pool, table, lens, refs, pt)
+    others = np.append(np.setdiff1d(np.arange(S), children), [-1, S])
+    parents = rng.choice(others, len(children))
+    o = outputs(table, lens, refs, in_place)
+    ok = kda.pages_fork(pool, table, lens, refs, many(parents), many(children), page_tokens=pt, **o)
+    assert ok.cpu().tolist() == r.fork(parents.tolist(), children.tolist())
+    if o:
+        table, lens, refs = o["table_out"], o["lengths_out"], o["refs_out"]
+    same(r, pool, table, lens, refs)
+    # more than the pages that are left: the last requests are refused
+    seqs = rng.permutation(S)
+    new = np.minimum(r.lengths[seqs] + rng.integers(0, 2 * M * pt, S), M * pt + 1)
+    o = outputs(table, lens, refs, in_place)
+    ok = kda.pages_extend(table, lens, refs, many(seqs), many(new), page_tokens=pt, **o).cpu().tolist()
+    assert ok == r.extend(seqs.tolist(), new.tolist()) and 0 < sum(ok) < len(ok)
+    if o:
+        table, lens, refs = o["table_out"], o["lengths_out"], o["refs_out"]
+    same(r, None, table, lens, refs)
+
+
+@pytest.mark.parametrize("pages,page_bytes", [(16384, 16), (16385, 4), (40000, 16)])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_free_and_compact_over_many_tiles(pages, page_bytes, in_place):
+    S, M = pages // 10, 8
+    pool, table, lens, refs = cache(pages, S, M, pages, 4, page_bytes, layers=2)
+    r = ref.Cache(pool, table, lens, refs, 4)
+    gone = np.random.default_rng(1).permutation(S)[:S // 2]
+    o = outputs(table, lens, refs, in_place)
+    kda.pages_free(table, lens, refs, many(gone), **o)
+    r.free(gone.tolist())
+    if o:
+        table, lens, refs = o["table_out"], o["lengths_out"], o["refs_out"]
+    same(r, pool, table, lens, refs)
+    o = outputs(table, lens, refs, in_place)
+    o.pop("lengths_out", None)
+    m = kda.pages_compact(pool, table, refs, **o)
+    assert np.array_equal(m.cpu().numpy(), r.compact())
+    if o:
+        table, refs = o["table_out"], o["refs_out"]
+    same(r, pool, table, lens, refs)
+
+
+def test_more_requests_than_a_block_has_threads():
+    """Ranks carry on from one 1024 requests to the next; the pages run out in the third."""
+    S, M, pt = 3000, 2, 4
+    lengths = np.where(np.arange(S) < 400, 5, 0)
+    pool, table, lens, refs = cache(3, S, M, 3000, pt, 4, lengths=lengths)
+    r = ref.Cache(pool, table, lens, refs, pt)
+    parents, children = np.arange(2600) % 400, np.arange(400, 3000)
+    ok = kda.pages_fork(pool, table, lens, refs, many(parents), many(children), page_tokens=pt).cpu().tolist()
+    assert ok == r.fork(parents.tolist(), children.tolist()) and 2048 < sum(ok) < 2600
+    same(r, pool, table, lens, refs)
+    pool, table, lens, refs = cache(4, S, M, 2300, pt, 4, lengths=[0] * S)
+    r = ref.Cache(pool, table, lens, refs, pt)
+    new = [1 + (n % 7 == 0) * 4 for n in range(2600)]
+    ok = kda.pages_extend(table, lens, refs, many(np.arange(2600)), many(new), page_tokens=pt).cpu().tolist()
+    assert ok == r.extend(list(range(2600)), new) and 0 < sum(ok) < 2600
+    same(r, None, table, lens, refs)
 
 
 def test_extend_of_a_row_named_twice_stays_in_its_row():
