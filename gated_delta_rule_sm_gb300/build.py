@@ -4,7 +4,8 @@ Each translation unit compiles in parallel to an object file; one nvcc call
 links them into a shared library next to this file.  It exposes a plain C ABI
 (``include/kda.h``) and knows nothing of torch.  The serving calls' binding
 (``_ops.so``, from ``csrc/torch_ops.cpp``) is compiled beside it with the host
-compiler against the installed torch, and links to it.
+compiler against the installed torch, and links to it; with another torch it
+is built again, and where it does not compile the library is linked all the same.
 """
 from __future__ import annotations
 
@@ -23,6 +24,7 @@ LIB_NAME = "libkda_gb300.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 OPS_SRC = os.path.join(CSRC, "torch_ops.cpp")
 OPS_PATH = os.path.join(PKG, "_ops.so")
+OPS_TORCH = os.path.join(BUILD_DIR, "torch_ops.torch")     # the torch that _ops.so was compiled against
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -49,7 +51,20 @@ def up_to_date() -> bool:
     if not os.path.exists(LIB_PATH) or not os.path.exists(OPS_PATH):
         return False
     t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(OPS_PATH))
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    return all(os.path.getmtime(f) <= t for f in _deps()) and _bound_torch() == _this_torch()
+
+
+def _this_torch() -> str:
+    import torch
+    return f"{torch.__version__} {os.path.dirname(torch.__file__)}"
+
+
+def _bound_torch() -> str:
+    try:
+        with open(OPS_TORCH) as f:
+            return f.read()
+    except OSError:
+        return ""
 
 
 def _compile_ops() -> str:
@@ -78,6 +93,8 @@ def _link_ops(obj: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"linking {os.path.basename(OPS_PATH)} failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, OPS_PATH)
+    with open(OPS_TORCH, "w") as f:
+        f.write(_this_torch())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
@@ -101,14 +118,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
         ops = ex.submit(_compile_ops)
         objs = list(ex.map(compile_one, srcs))
-        ops_obj = ops.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *objs, "-lcuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
-    _link_ops(ops_obj)
+    _link_ops(ops.result())      # (the library is there whatever becomes of the binding)
     return LIB_PATH
 
 
