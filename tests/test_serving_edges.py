@@ -227,6 +227,7 @@ def test_captured_calls_keep_their_workspaces():
     kw = dict(page_tokens=4, table_out=outs[0], lengths_out=outs[1], refs_out=outs[2])
     parents, children = ints(0, 1), ints(3, 4)
     side = torch.cuda.Stream()
+    _lib.workspace_cache.clear()       # (earlier tests' calls on this stream may have wanted more)
 
     def calls():
         y, S = kda.ssm_scan(*[small[n] for n in ARGS], output_final_state=True)
