@@ -126,6 +126,23 @@ Schedule make_schedule(const SsmShape& s, bool varlen, const Costs& k) {
     return w;
 }
 
+// Whether the results lie apart from what other CTAs still read.  In place are right: y over x of the same layout (a
+// CTA reads a token's columns before it writes them, and no other CTA uses them but as zeros), the end states over
+// the entering ones (a thread writes the elements that it read, or the join has read them all before).
+bool results_apart(const SsmShape& s, const void* x, const void* dt, const void* b, const void* c, const void* S0,
+                   const void* y, const void* ST) {
+    const size_t es = s.dtype == KDA_BF16 ? 2 : 4, state = (size_t)s.rows * s.H * s.N * s.P * 4;
+    auto span = [&](int64_t stride, int64_t width) { return ((size_t)(s.TT - 1) * stride + width) * es; };
+    const int64_t xw = (int64_t)s.H * s.P, bw = (int64_t)s.G * s.N;
+    const size_t nx = span(s.xs, xw), nb = span(s.bs, bw), nc = span(s.cs, bw), nd = span(s.ds, s.H), ny = span(xw, xw);
+    const bool over_x = y == x && s.xs == xw, over_S0 = ST == S0;
+    if (ranges_meet(y, ny, b, nb) || ranges_meet(y, ny, c, nc) || ranges_meet(y, ny, dt, nd) || ranges_meet(y, ny, S0, state) ||
+        ranges_meet(y, ny, ST, state) || (!over_x && ranges_meet(y, ny, x, nx)))
+        return false;
+    return !ranges_meet(ST, state, x, nx) && !ranges_meet(ST, state, b, nb) && !ranges_meet(ST, state, c, nc) &&
+           !ranges_meet(ST, state, dt, nd) && (over_S0 || !ranges_meet(ST, state, S0, state));
+}
+
 // Two CTAs of the fp32 kernel share an SM, each 64 columns of P.
 int simt_parts(int P) { return (P + 63) / 64; }
 Costs simt_costs(const SsmShape& s) { return {((int64_t)s.H * simt_parts(s.P) + 1) / 2, 32, 0.5, 0.6, 2.0}; }
@@ -464,6 +481,7 @@ kda_status kda_ssm_fwd(const kda_ssm_dims* dims, const void* x, const void* dt_r
     if (workspace_bytes < w.total || (w.total && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256)))
         return KDA_ERR_WORKSPACE;
     if (w.nseg > (1 << 30) / s.H || s.H > 65535) return KDA_ERR_UNSUPPORTED;
+    if (!results_apart(s, x, dt_raw, b, c, initial_state, y, final_state)) return KDA_ERR_INVALID_ARG;
     char* ws = static_cast<char*>(workspace);
     SsmArgs a;
     memset(&a, 0, sizeof(a));

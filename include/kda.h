@@ -470,6 +470,8 @@ kda_status kda_decode_step(const kda_dims* dims, const void* q, const void* k, c
  * a few tokens to a row that one wave of CTAs covers, run an fp32 token-by-token kernel.
  * Long rows with few rows x heads are cut into segments whose end states are computed in parallel and
  * joined before the outputs; the library chooses the cut.  Results do not depend on timing.
+ * In place: y may be x where x is contiguous, final_state may be initial_state; any other overlap of the
+ * two results with each other or an input is KDA_ERR_INVALID_ARG.
  * The workspace is kda_ssm_fwd_workspace_size() bytes (0 on invalid input).
  */
 typedef struct {

@@ -67,6 +67,23 @@ def test_scan_with_a_decay_rate_past_fp32(dtype, T):
     check_scan(i, [0, T], S0, y, S, dtype, dtype == "bf16")
 
 
+@pytest.mark.parametrize("dtype,N,P,T,docs", [
+    ("bf16", 128, 64, 3000, None), ("bf16", 64, 128, 700, None), ("bf16", 64, 64, 420, [70, 0, 150, 200]), ("bf16", 64, 64, 6, None),
+    ("fp32", 48, 40, 2100, None), ("fp32", 64, 64, 420, [70, 0, 150, 200]), ("bf16", 256, 64, 300, None),
+])
+def test_scan_in_place(dtype, N, P, T, docs):
+    """y over x and the end states over the entering ones give what separate buffers give."""
+    i, g = ssm_inputs(53, (1, T), 4, 2, N, P, dtype)
+    cu = None if docs is None else torch.tensor([0, *np.cumsum(docs).tolist()], dtype=torch.int32, device=DEV)
+    S0 = randn(g, len(docs) if docs else 1, 4, N, P).to(DEV)
+    y, S = run_scan(i, initial_state=S0, output_final_state=True, cu_seqlens=cu)
+    for _ in range(3):
+        x, state = i["x"].clone(), S0.clone()
+        y2, S2 = run_scan(dict(i, x=x), initial_state=state, output_final_state=True, cu_seqlens=cu, out=x, final_state=state)
+        assert y2 is x and S2 is state
+        assert torch.equal(y, x) and torch.equal(S, state)
+
+
 # ------------------------------------------------------------------------------------------- convolution
 
 
