@@ -173,7 +173,8 @@ __device__ __forceinline__ void tmem_st_16x16(uint32_t taddr, const uint32_t* v)
 // the series of 2 artanh(e / (2 + e)), whose argument is at most 1/3.
 __device__ __forceinline__ float step_of(float x) {
     const float y = fmaxf(-fabsf(x), -200.f), t = y * kLog2e;
-    const float r = fmaf(y, kLog2e, -t) + y * 1.925963033500e-8f;
+    constexpr float low = (float)(1.4426950408889634074 - (double)kLog2e);      // log2(e) less its fp32 value
+    const float r = fmaf(y, kLog2e, -t) + y * low;
     float e = ex2(t);
     e = fmaf(e * 0.6931471806f, r, e);
     const float z = __fdividef(e, 2.f + e), q = z * z;
