@@ -541,7 +541,9 @@ def ssm_scan(x, dt_raw, b, c, a_log, dt_bias, d_skip=None, *, cu_seqlens=None, c
     projection are taken as they are); a_log, dt_bias, d_skip [H] fp32; states [rows, H, N, P] fp32 with
     rows = B, or one per document of ``cu_seqlens`` (int32).
         S_t = exp(D_t a) S_{t-1} + D_t b_t x_t^T,  y_t = S_t^T c_t + d_skip x_t,
-        D = softplus(dt_raw + dt_bias), a = -exp(a_log)."""
+        D = softplus(dt_raw + dt_bias), a = -exp(a_log).
+    Tokens must not share memory (an expanded tensor is refused).  ``final_state`` may be ``initial_state`` and ``out``
+    a contiguous x; results over any other input are refused."""
     address, held = _host_address(cu_seqlens, cu_seqlens_host)
     return _run("ssm_scan", stream, x, dt_raw, b, c, a_log, dt_bias, d_skip, cu_seqlens, address, initial_state,
                 output_final_state, out, final_state)
@@ -573,7 +575,8 @@ def short_conv_prompt(x, weight, bias=None, *, cu_seqlens=None, cu_seqlens_host=
     """:func:`short_conv` with a carried history, through ``kda_short_conv_prompt``.  Returns (y, final_history).
 
     x [B, T, C] (a slice of a wider projection is taken as it is); histories [rows, W - 1, C] like x, oldest input
-    first: the last W - 1 inputs before the row (None: zeros) and at its end."""
+    first: the last W - 1 inputs before the row (None: zeros) and at its end.  ``final_history`` may be
+    ``initial_history``; results over any other input are refused."""
     address, held = _host_address(cu_seqlens, cu_seqlens_host)
     return _run("short_conv_prompt", stream, x, weight, bias, cu_seqlens, address, initial_history, out, final_history)
 

@@ -6,7 +6,7 @@
 // thread owns four channels over a tile of tokens and keeps the last W inputs in a ring of registers; its loads
 // run up to eight tokens ahead.  Measured on 16384 tokens x 4096 channels, W 4: bf16 53 us (5.0 TB/s), fp32 90
 // us (5.9 TB/s); with eight channels a thread 61 and 104 us (fewer warps: waiting for loads), with tiles that
-// leave a last wave of CTAs part empty 59 us.  One token of 128 rows x 12288 channels: 9 us of kernel, 11 us
+// leave a last wave of CTAs part empty 59 us, with histories in place 59 us (a second launch).  One token of 128 rows x 12288 channels: 9 us of kernel, 11 us
 // with two rows to a CTA in place of four.
 #include <math.h>
 #include <string.h>

@@ -12,14 +12,15 @@
 // Operands: B, C and X tiles arrive by TMA with the 128-byte swizzle and are read by the products as they
 // are, K-major for G and C S, MN-major (tokens as K) for M X and U^T B.  M and U are A operands in TMEM:
 // M is written over G, 16 fp32 columns of G giving 8 + 8 packed columns for the two heads.  The state
-// stays in fp32 registers; its bf16 copy in shared memory is the B operand of C S.
-// Precision: M is rounded to bf16 (relative 2^-9 of each term of y, which is bf16 itself); C S takes S as
-// two bf16 values, one after the other in one buffer: with one, a large entering state alone cost y up to
+// stays in fp32 registers; its two bf16 copies in shared memory are the B operands of C S.
+// Precision: M is rounded to bf16 (relative 2^-9 of each term of y, which is bf16 itself: 12 documents of 16384 tokens
+// are 1.72e-3 of the norm from 64 bits, 1.66e-3 of which the storage alone takes); C S takes S as
+// two bf16 values, a buffer each: with one, a large entering state alone cost y up to
 // 0.04 of its rms.  The state is an fp32 result, so U is kept as the sum of three bf16 values (24 bits) and X and
 // B are exact: two values would leave 1.5e-6 of the state, three leave fp32 rounding.
-// Decays: log2 units, every sum taken inside blocks of 32 tokens and extended by whole blocks' sums, so no
-// exponent is the difference of two large numbers; a token's exponent is cut at -150 (2^-150 is 0 in
-// fp32).
+// Decays: log2 units, every sum taken inside blocks of 32 tokens and extended by whole blocks' sums; a token's
+// exponent is cut at -150 (2^-150 is 0 in fp32).  Only on M's diagonal blocks is an exponent the difference of two sums,
+// of at most 32 tokens: 4800 at the cut, where it is 2^-12 off, an eighth of M's rounding.
 //
 // Roles (24 warps): 0-7 form M (two warpgroups, which split the columns) and finish Y (a head each); 8-11 form
 // U, a quarter of a chunk at a time; 12-19 scale C S and keep the state (half a row a thread); 20 issues G,
@@ -32,7 +33,8 @@
 // 1.5 us of an SM's share at the measured rates.  Measured on a row of 65536 tokens, 32 heads, N 128, P 64: 218
 // us for the outputs, 3.8 us a chunk, and 109 us for the states, 1.9 us a chunk.  What holds the output pass is
 // shared memory: 320 KB of operands and 128 KB of copies at 128 bytes a cycle and 3200 accesses of the warps, some 6600
-// of a chunk's 7300 cycles; and the roles' loops together fill the instruction cache, which is why
+// of a chunk's 7300 cycles.  The source asks for about 1650 of those accesses (M's factors 160, Y 512, the copies of S
+// 512, U's loads 256); the other 1500 are conflicts or replays whose cause has not been found.  And the roles' loops together fill the instruction cache, which is why
 // they are kept short (M unrolled over its 32 columns and two copies of copy_state: 222 us).
 #include <cudaTypedefs.h>
 #include <string.h>
