@@ -31,7 +31,10 @@ EXPORTS = ("kda_fwd_workspace_size", "kda_bwd_workspace_size", "kda_fwd", "kda_f
            "kda_gated_norm_fwd", "kda_gated_norm_bwd_workspace_size", "kda_gated_norm_bwd",
            "kda_decode_step", "kda_ssm_fwd_workspace_size", "kda_ssm_fwd", "kda_ssm_step",
            "kda_short_conv_prompt", "kda_short_conv_step", "kda_pages_workspace_size", "kda_pages_copy",
-           "kda_pages_fork", "kda_pages_extend", "kda_pages_free", "kda_pages_compact")
+           "kda_pages_fork", "kda_pages_extend", "kda_pages_free", "kda_pages_compact",
+           "kda_gated_scan_fwd_workspace_size", "kda_gated_scan_bwd_workspace_size", "kda_gated_scan_saved_size",
+           "kda_gated_scan_fwd", "kda_gated_scan_bwd", "kda_gated_step", "kda_pages_append",
+           "kda_pages_attention_workspace_size", "kda_pages_attention")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 GATES = {"lower_bounded": 0, "softplus": 1}   # kda_gate
 
@@ -47,6 +50,20 @@ class SsmDims(ctypes.Structure):
                 ("N", ctypes.c_int), ("P", ctypes.c_int), ("dtype", ctypes.c_int), ("num_seqs", ctypes.c_int),
                 ("x_stride", ctypes.c_int64), ("b_stride", ctypes.c_int64), ("c_stride", ctypes.c_int64),
                 ("dt_stride", ctypes.c_int64)]
+
+
+class GatedDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("C", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("num_seqs", ctypes.c_int), ("x_stride", ctypes.c_int64), ("g_stride", ctypes.c_int64),
+                ("i_stride", ctypes.c_int64)]
+
+
+class AttentionDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int), ("tokens", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int),
+                ("D", ctypes.c_int), ("dtype", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("page_tokens", ctypes.c_int), ("table_rows", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("window", ctypes.c_int), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64)]
 
 
 class PagesDims(ctypes.Structure):
@@ -142,7 +159,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.kda_short_conv_bwd.argtypes = conv + [_vp] * 5 + [ctypes.c_size_t, _vp]
         i, i64, sz, f = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
         ssm_p, pages_p = ctypes.POINTER(SsmDims), ctypes.POINTER(PagesDims)
-        serving = {   # argument types; the two sizes return size_t, the others a status
+        gated_p, attn_p = ctypes.POINTER(GatedDims), ctypes.POINTER(AttentionDims)
+        serving = {   # argument types; the sizes return size_t, the others a status
             "kda_decode_step": [dims_p] + [_vp] * 7 + [f, f, _vp, i] + [_vp] * 4,
             "kda_ssm_fwd_workspace_size": [ssm_p],
             "kda_ssm_fwd": [ssm_p] + [_vp] * 12 + [_vp, sz, _vp],
@@ -155,10 +173,19 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             "kda_pages_extend": [pages_p] + [_vp] * 5 + [i] + [_vp] * 4 + [_vp, sz, _vp],
             "kda_pages_free": [pages_p] + [_vp] * 4 + [i] + [_vp] * 4,
             "kda_pages_compact": [pages_p] + [_vp] * 6 + [_vp, sz, _vp],
+            "kda_gated_scan_fwd_workspace_size": [gated_p],
+            "kda_gated_scan_bwd_workspace_size": [gated_p],
+            "kda_gated_scan_saved_size": [gated_p],
+            "kda_gated_scan_fwd": [gated_p] + [_vp] * 9 + [_vp, sz] + [_vp, sz, _vp],
+            "kda_gated_scan_bwd": [gated_p] + [_vp] * 14 + [_vp, sz] + [_vp, sz, _vp],
+            "kda_gated_step": [gated_p] + [_vp] * 5 + [i] + [_vp] * 4,
+            "kda_pages_append": [attn_p] + [_vp] * 9,
+            "kda_pages_attention_workspace_size": [attn_p],
+            "kda_pages_attention": [attn_p] + [_vp] * 7 + [f] + [_vp] * 2 + [_vp, sz, _vp],
         }
         for name, types in serving.items():
             fn = getattr(lib, name)
-            fn.restype = sz if name.endswith("_workspace_size") else i
+            fn.restype = sz if name.endswith("_size") else i
             fn.argtypes = types
         _lib = lib
         return lib
@@ -621,3 +648,66 @@ def pages_compact(pool, table, refs, *, table_out=None, refs_out=None, page_map=
     """Moves the live pages of pool [layers, pages, ...] to the lowest indices through ``kda_pages_compact``; table
     and refs follow.  Returns page_map [pages] int32: the new index of each page, -1 for a free one."""
     return _run("pages_compact", stream, pool, table, refs, table_out, refs_out, page_map)
+
+
+def gated_scan(x, g_raw, i_raw, a_log, *, cu_seqlens=None, cu_seqlens_host=None, initial_state=None,
+               output_final_state: bool = False, out=None, final_state=None, saved=None,
+               stream: Optional[torch.cuda.Stream] = None):
+    """Gated linear recurrence over sequences through ``kda_gated_scan_fwd``.  Returns (y, final_state or None).
+
+    x, g_raw, i_raw [B, T, C] (bf16 or fp32, one dtype; slices of a wider projection are taken as they are); a_log [C]
+    fp32; states [rows, C] fp32 with rows = B, or one per document of ``cu_seqlens`` (int32).
+        log a_t = -exp(a_log) sigmoid(g_t),  h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t,  y_t = h_t.
+    ``saved``: a device buffer of ``gated_scan_saved_size(x)`` bytes, filled for ``gated_scan_backward(..., saved=...)``.
+    ``final_state`` may be ``initial_state`` and ``out`` a contiguous x; results over any other input are refused."""
+    address, held = _host_address(cu_seqlens, cu_seqlens_host)
+    return _run("gated_scan", stream, x, g_raw, i_raw, a_log, cu_seqlens, address, initial_state, output_final_state, out,
+                final_state, saved)
+
+
+def gated_scan_saved_size(x) -> int:
+    """Bytes of the buffer ``gated_scan(..., saved=...)`` fills for x [B, T, C]."""
+    return _run("gated_scan_saved_size", None, x)
+
+
+def gated_scan_backward(x, g_raw, i_raw, a_log, dy, *, cu_seqlens=None, cu_seqlens_host=None, initial_state=None,
+                        dfinal_state=None, want_dinitial_state: bool = True, saved=None,
+                        stream: Optional[torch.cuda.Stream] = None) -> dict:
+    """Reverse mode of :func:`gated_scan` through ``kda_gated_scan_bwd``: dict(dx, dg_raw, di_raw [B, T, C], da_log [C],
+    dinitial_state [rows, C] or None), fp32.  dy like x, contiguous; ``saved``: the buffer that a ``gated_scan(...,
+    saved=...)`` on the same inputs filled (without it the states are computed again)."""
+    address, held = _host_address(cu_seqlens, cu_seqlens_host)
+    return dict(zip(("dx", "dg_raw", "di_raw", "da_log", "dinitial_state"),
+                    _run("gated_scan_backward", stream, x, g_raw, i_raw, a_log, dy, cu_seqlens, address, initial_state,
+                         dfinal_state, want_dinitial_state, saved)))
+
+
+def gated_step(x, g_raw, i_raw, a_log, *, state, slots=None, state_out=None, out=None,
+               stream: Optional[torch.cuda.Stream] = None):
+    """One token per row of :func:`gated_scan` through ``kda_gated_step``: x, g_raw, i_raw [B, C], ``state`` [slots, C]
+    fp32; ``slots`` and ``state_out`` as for :func:`ssm_step`.  Returns (y, the pool written)."""
+    return _run("gated_step", stream, x, g_raw, i_raw, a_log, state, slots, state_out, out)
+
+
+def pages_append(pool, table, lengths, k, v, *, seqs=None, cu_seqlens=None, cu_seqlens_host=None,
+                 stream: Optional[torch.cuda.Stream] = None):
+    """New tokens' keys and values into their pages through ``kda_pages_append``.  Returns ``pool``.
+
+    ``pool`` [pages, 2, Hkv, page_tokens, D]: one layer of a pool of pages, keys and then values; table [sequences, M],
+    lengths [sequences] int32 as :func:`pages_extend` leaves them, the new tokens counted.  k, v [B, n, Hkv, D], or
+    [1, T, Hkv, D] with ``cu_seqlens`` (int32), like pool (slices of a wider projection are taken as they are): row r's
+    are the last tokens of sequence ``seqs[r]`` (int32; None: sequence r; negative: the row is idle)."""
+    address, held = _host_address(cu_seqlens, cu_seqlens_host)
+    return _run("pages_append", stream, pool, table, lengths, k, v, seqs, cu_seqlens, address)
+
+
+def pages_attention(q, pool, table, lengths, *, scale: float, seqs=None, cu_seqlens=None, cu_seqlens_host=None,
+                    window: int = 0, out=None, lse=None, stream: Optional[torch.cuda.Stream] = None):
+    """Causal attention of new tokens over the pages of their sequences through ``kda_pages_attention``.
+
+    q [B, n, Hq, D] or [1, T, Hq, D] with ``cu_seqlens``, rows as for :func:`pages_append`, whose keys and values come
+    first; query head h reads key head h // (Hq // Hkv).  The token at position p attends to the positions 0 .. p, with
+    ``window`` > 0 to the last ``window`` of them.  Returns out like q, contiguous; rows without keys (idle, empty) get
+    zeros.  ``lse`` [.., Hq] fp32, if given, gets the logarithms of the sums of exponentials."""
+    address, held = _host_address(cu_seqlens, cu_seqlens_host)
+    return _run("pages_attention", stream, q, pool, table, lengths, scale, seqs, cu_seqlens, address, window, out, lse)

@@ -288,7 +288,10 @@ static const char* kKernelNames[] = {"kda_plan",          "kda_intra_simt",   "k
                                      "kda_short_conv_prompt", "kda_short_conv_step", "kda_ssm_plan",
                                      "kda_ssm_state",     "kda_ssm_join",     "kda_ssm_out",
                                      "kda_pages_count",   "kda_pages_assign", "kda_pages_apply",
-                                     "kda_pages_copy"};
+                                     "kda_pages_copy",    "kda_gated_plan",   "kda_gated_scan",
+                                     "kda_gated_bwd",     "kda_gated_reduce", "kda_gated_step",
+                                     "kda_pages_append",  "kda_attention_plan", "kda_attention",
+                                     "kda_attention_join"};
 
 // saved != NULL: also keep the fp32 backward record there (kda_fwd_save)
 static kda_status fwd_tc(const Shape& s, Params p, void* ws, size_t ws_bytes, cudaStream_t stream,

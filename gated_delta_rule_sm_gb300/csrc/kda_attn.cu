@@ -1,0 +1,580 @@
+// kda_attn.cu -- keys and values into the pages of a cache, and attention over them: the entries, the plan of the
+// work, the join of what several CTAs share, and the fp32 kernel.
+#include <math.h>
+#include <string.h>
+
+#include <type_traits>
+
+#include "kda.h"
+#include "kda_attn.h"
+#include "kda_common.cuh"
+#include "kda_internal.h"
+#include "kda_sm100.cuh"
+
+namespace kda {
+
+using namespace sm100;
+
+namespace {
+
+// ------------------------------------------------------------------ append
+
+// A warp takes a token, its lanes the 16-byte pieces (elements where those are not aligned) of its keys and values.  Bound by
+// memory; the tokens' addresses come from three small loads, which the loads of the data do not wait for.
+constexpr int kAppendWarps = 8;
+struct AppendArgs {
+    AttnArgs a;
+    const void *k, *v;
+    int64_t ks, vs;      // elements between tokens
+    void* pool;
+};
+
+// The row of packed token t: the last one that begins at or before it, by 32 offsets at a time.
+__device__ __forceinline__ int row_of_token(const int32_t* cu, int rows, int t) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = rows;                      // the answer is in [lo, lo + n)
+    while (n > 1) {
+        const int step = (n + 31) / 32, at = lo + lane * step;
+        const unsigned hit = __ballot_sync(0xffffffffu, lane * step < n && cu[at] <= t);
+        const int k = 31 - __clz(hit | 1u);
+        n = min(step, n - k * step);
+        lo += k * step;
+    }
+    return lo;
+}
+
+template <typename W>
+__global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_constant__ AppendArgs p) {
+    const AttnArgs& a = p.a;
+    const int lane = threadIdx.x & 31;
+    if (a.cu) {
+        bool bad = threadIdx.x == 0 && (a.cu[0] != 0 || a.cu[a.rows] != a.tokens);
+        for (int n = threadIdx.x; n < a.rows; n += kAppendWarps * 32) bad |= a.cu[n + 1] < a.cu[n];
+        if (__syncthreads_or(bad)) {
+            if (blockIdx.x == 0 && threadIdx.x == 0) record_error(a.status, KDA_ERR_INVALID_ARG);
+            return;
+        }
+    }
+    const int t = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+    if (t >= a.tokens) return;
+    const int es = a.dtype == KDA_BF16 ? 2 : 4, per = a.D * es / (int)sizeof(W), all = a.Hkv * per;      // pieces of a head, of a token
+    const W *k = reinterpret_cast<const W*>(static_cast<const char*>(p.k) + t * p.ks * es),
+            *v = reinterpret_cast<const W*>(static_cast<const char*>(p.v) + t * p.vs * es);
+    constexpr int AHEAD = 8;
+    W rk[AHEAD], rv[AHEAD];
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int at = i0 + i * 32 + lane;
+            if (at < all) {
+                rk[i] = k[at];
+                rv[i] = v[at];
+            }
+        }
+    };
+    load(0);
+    const int r = a.cu ? row_of_token(a.cu, a.rows, t) : t / a.per_row;
+    const AttnRow w = attn_row(a, r, lane == 0);
+    const int pos = w.len - w.n + (t - w.first);
+    if (w.seq < 0 || pos < 0) return;
+    const int page = a.table[(size_t)w.seq * a.max_pages + pos / a.pt];
+    if (page < 0 || page >= a.pages) {
+        if (lane == 0) record_error(a.status, KDA_ERR_INVALID_ARG);
+        return;
+    }
+    const size_t head = (size_t)a.pt * per;                        // pieces of a head's keys in a page
+    W* to = static_cast<W*>(p.pool) + (size_t)page * 2 * a.Hkv * head + (size_t)(pos % a.pt) * per;
+    for (int i0 = 0; i0 < all; i0 += AHEAD * 32) {
+        if (i0) load(i0);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int at = i0 + i * 32 + lane;
+            if (at < all) {
+                const int h = at / per;
+                W* q = to + h * head + (at - h * per);
+                q[0] = rk[i];
+                q[a.Hkv * head] = rv[i];
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ plan
+
+// Units of every row, then tiles of every unit, each as a running sum.
+constexpr int kPlanThreads = 1024;
+__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* tmp, int64_t* total) {     // what comes before this thread
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t s = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += up;
+    }
+    __syncthreads();
+    if (lane == 31) tmp[warp] = s;
+    __syncthreads();
+    if (warp == 0) {
+        int64_t w = tmp[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t up = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += up;
+        }
+        tmp[lane] = w;
+    }
+    __syncthreads();
+    *total = tmp[31];
+    return s - x + (warp ? tmp[warp - 1] : 0);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_constant__ AttnArgs a) {
+    __shared__ int64_t tmp[32];
+    const int tid = threadIdx.x;
+    bool bad = false;
+    if (a.cu) {
+        for (int n = tid; n < a.rows; n += kPlanThreads) bad |= a.cu[n + 1] < a.cu[n];
+        if (tid == 0) bad |= a.cu[0] != 0 || a.cu[a.rows] != a.tokens;
+    }
+    if (__syncthreads_or(bad)) {
+        if (tid == 0) {
+            record_error(a.status, KDA_ERR_INVALID_ARG);
+            *a.units = -1;
+        }
+        return;
+    }
+    int64_t units = 0, total;
+    for (int r0 = 0; r0 < a.rows; r0 += kPlanThreads) {
+        const int r = r0 + tid;
+        const int64_t blocks = r < a.rows ? attn_blocks(a, a.cu ? a.cu[r + 1] - a.cu[r] : a.per_row) : 0;
+        const int64_t at = units + block_scan(blocks, tmp, &total);
+        // (a row has few blocks next to the work that each is)
+        for (int b = 0; b < blocks; ++b) {
+            a.unit_row[at + b] = r;
+            a.unit_row[a.units_most + at + b] = b;
+        }
+        units += total;
+    }
+    __syncthreads();
+    int64_t tiles = 0;
+    for (int u0 = 0; u0 < units; u0 += kPlanThreads) {
+        const int u = u0 + tid;
+        int64_t n = 0;
+        if (u < units) {
+            const int b = a.unit_row[a.units_most + u];
+            n = attn_span(a, attn_row(a, a.unit_row[u], b == 0), b).tiles;
+        }
+        const int64_t at = tiles + block_scan(n, tmp, &total);
+        if (u < units) a.start[u] = at;
+        tiles += total;
+    }
+    if (tid == 0) {
+        a.start[units] = tiles;
+        *a.units = (int)units;
+    }
+}
+
+// ------------------------------------------------------------------ join
+
+// A CTA takes one item (a unit for one key head); most items have one part and are done already.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnArgs a) {
+    const int units = *a.units, u = blockIdx.x / a.Hkv, head = blockIdx.x - u * a.Hkv;
+    if (u >= units) return;
+    const int64_t first = a.start[u];
+    const int tiles = (int)(a.start[u + 1] - first);
+    const AttnCut cut(a, a.start[units] * a.Hkv);
+    const int64_t x = first * a.Hkv + (int64_t)head * tiles;
+    const int c0 = cut.owner(x), c1 = cut.owner(x + tiles - 1);
+    if (c0 == c1) return;
+    const AttnRow w = attn_row(a, a.unit_row[u], false);
+    const int64_t r0 = (int64_t)a.unit_row[a.units_most + u] * a.block, left = (int64_t)w.n * a.G - r0;
+    const int n = (int)(left < a.block ? left : a.block), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const size_t size = attn_part_floats(a);
+    auto part = [&](int c) { return a.part + (size_t)(2 * c + (c == c0)) * size; };
+    for (int i = warp; i < n; i += kJoinThreads / 32) {
+        float top = -INFINITY;
+        for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, part(c)[(size_t)a.block * a.D + i]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float base = top == -INFINITY ? 0.f : top;
+        float sum = 0.f, o[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = 0.f;
+        for (int c = c0; c <= c1; ++c) {
+            const float* p = part(c);
+            const float f = exp2f(p[(size_t)a.block * a.D + i] - base);
+            sum = fmaf(f, p[(size_t)a.block * (a.D + 1) + i], sum);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k * 32 + lane < a.D) o[k] = fmaf(f, p[(size_t)i * a.D + k * 32 + lane], o[k]);
+        }
+        const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;      // (NaN stays)
+        const int64_t row = r0 + i;
+        const size_t token = w.first + row / a.G, at = token * a.Hq + head * a.G + row % a.G;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k * 32 + lane < a.D) store_act(a.out, at * a.D + k * 32 + lane, o[k] * inv, a.dtype);
+        if (a.lse && lane == 0) a.lse[at] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * 0.6931471805599453f;
+    }
+}
+
+// ------------------------------------------------------------------ fp32
+
+// 64 packed rows against 64 keys at a time, 256 threads of 4 x 4 scores each; Q, K and the weights lie transposed in
+// shared memory, so that a step of a product is two 16-byte reads for 16 multiplications.  A thread keeps 4 rows of D / 16
+// columns of the output.  Bound by fp32 arithmetic with full blocks; a block of few rows leaves most warps idle.
+constexpr int kSimtRows = 64, kSimtKeys = 64, kSimtThreads = 256, kSimtPad = 68;
+
+template <typename E> __device__ __forceinline__ float4 load4(const char* p, int d, int D, bool vec) {
+    const E* e = reinterpret_cast<const E*>(p) + d;
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (vec) {
+        if constexpr (sizeof(E) == 4) f = *reinterpret_cast<const float4*>(e);
+        else {
+            const uint2 u = *reinterpret_cast<const uint2*>(e);
+            f = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                            __uint_as_float(u.y & 0xffff0000u));
+        }
+    } else {
+        if (d < D) f.x = (float)e[0];
+        if (d + 1 < D) f.y = (float)e[1];
+        if (d + 2 < D) f.z = (float)e[2];
+        if (d + 3 < D) f.w = (float)e[3];
+    }
+    return f;
+}
+
+// DC: columns of the output a thread keeps, in groups of four: D <= 64 DC.
+template <typename E, int DC>
+__global__ void __launch_bounds__(kSimtThreads, DC > 2 ? 1 : 2) attn_simt_kernel(const __grid_constant__ AttnArgs a) {
+    extern __shared__ __align__(16) float sh[];
+    const int D4 = (a.D + 3) / 4 * 4;
+    float* sq = sh;                                  // [D4][kSimtPad] q by channel
+    float* sk = sq + (size_t)D4 * kSimtPad;          // [D4][kSimtPad] keys by channel
+    float* sv = sk + (size_t)D4 * kSimtPad;          // [kSimtKeys][64 DC] values
+    float* sp = sv + kSimtKeys * 64 * DC;            // [kSimtKeys][kSimtPad] weights by key
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, warp = tid >> 5;
+    const int units = *a.units;
+    if (units <= 0) return;
+    const AttnCut cut(a, a.start[units] * a.Hkv);
+    const int cta = blockIdx.x;
+    if (cta >= cut.ctas) return;
+    const bool vq = a.D % 4 == 0 && a.qs % 4 == 0 && reinterpret_cast<uintptr_t>(a.q) % (4 * sizeof(E)) == 0;
+    const bool vk = a.D % 4 == 0 && reinterpret_cast<uintptr_t>(a.pool) % (4 * sizeof(E)) == 0;
+    const size_t values = (size_t)a.Hkv * a.pt * a.D * sizeof(E);      // from a page's keys to its values
+    const float c = a.scale * 1.4426950408889634f;
+    const int64_t end = cut.begin(cta + 1);
+    for (int64_t x = cut.begin(cta); x < end;) {
+        const AttnPiece p = attn_piece(a, units, x, end);
+        x += p.t1 - p.t0;
+        const AttnRow w = attn_row(a, p.row, false);
+        const AttnSpan s = attn_span(a, w, p.block);
+        const int64_t r0 = (int64_t)p.block * a.block, left = (int64_t)w.n * a.G - r0;
+        const int n = (int)(left < a.block ? left : a.block);
+        __syncthreads();
+        for (int i = tid; i < kSimtRows * (D4 / 4); i += kSimtThreads) {
+            const int r = i % kSimtRows, d = i / kSimtRows * 4;
+            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < n) {
+                const int64_t row = r0 + r, token = w.first + row / a.G;
+                const char* q = static_cast<const char*>(a.q) + (token * a.qs + (int64_t)(p.head * a.G + row % a.G) * a.D) * (int64_t)sizeof(E);
+                f = load4<E>(q, d, a.D, vq);
+            }
+            sq[d * kSimtPad + r] = f.x;
+            sq[(d + 1) * kSimtPad + r] = f.y;
+            sq[(d + 2) * kSimtPad + r] = f.z;
+            sq[(d + 3) * kSimtPad + r] = f.w;
+        }
+        float o[DC][4][4], top[4], sum[4];
+        int pos[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            top[i] = -INFINITY;
+            sum[i] = 0.f;
+            const int64_t row = r0 + 4 * ty + i;
+            pos[i] = 4 * ty + i < n ? w.len - w.n + (int)(row / a.G) : -1;
+#pragma unroll
+            for (int k = 0; k < DC; ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[k][i][j] = 0.f;
+        }
+        const bool busy = warp * 8 < n;          // the warp's rows: 8
+        for (int t = p.t0; t < p.t1; ++t) {
+            const int k0 = (s.tile0 + t) * kSimtKeys;
+            __syncthreads();
+            for (int i = tid; i < kSimtKeys * (D4 / 4); i += kSimtThreads) {
+                const int k = i % kSimtKeys, d = i / kSimtKeys * 4, key = k0 + k;
+                float4 f = make_float4(0.f, 0.f, 0.f, 0.f), g = f;
+                if (key >= s.begin && key < s.end) {
+                    const char* page = attn_page(a, w.seq, key, p.head, sizeof(E));
+                    if (page) {
+                        f = load4<E>(page, d, a.D, vk);
+                        g = load4<E>(page + values, d, a.D, vk);
+                    }
+                }
+                sk[d * kSimtPad + k] = f.x;
+                sk[(d + 1) * kSimtPad + k] = f.y;
+                sk[(d + 2) * kSimtPad + k] = f.z;
+                sk[(d + 3) * kSimtPad + k] = f.w;
+                *reinterpret_cast<float4*>(sv + k * 64 * DC + d) = g;
+            }
+            __syncthreads();
+            if (!busy) continue;
+            float z[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) z[i][j] = 0.f;
+            for (int d = 0; d < a.D; ++d) {
+                const float4 q = *reinterpret_cast<const float4*>(sq + d * kSimtPad + 4 * ty);
+                const float4 k = *reinterpret_cast<const float4*>(sk + d * kSimtPad + 4 * tx);
+                const float qv[4] = {q.x, q.y, q.z, q.w}, kv[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) z[i][j] = fmaf(qv[i], kv[j], z[i][j]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float m = top[i];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int key = k0 + 4 * tx + j;
+                    z[i][j] *= c;
+                    if (key > pos[i] || (a.window && key <= pos[i] - a.window)) z[i][j] = -INFINITY;
+                    m = fmaxf(m, z[i][j]);
+                }
+#pragma unroll
+                for (int b = 8; b > 0; b >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, b));
+                const float base = m == -INFINITY ? 0.f : m, f = exp2f(top[i] - base);
+                top[i] = m;
+                float add = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    z[i][j] = exp2f(z[i][j] - base);
+                    add += z[i][j];
+                }
+#pragma unroll
+                for (int b = 8; b > 0; b >>= 1) add += __shfl_xor_sync(0xffffffffu, add, b);
+                sum[i] = fmaf(sum[i], f, add);
+#pragma unroll
+                for (int k = 0; k < DC; ++k)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[k][i][j] *= f;
+            }
+            // the weights of a row are used by the warp that made them
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<float4*>(sp + (4 * tx + j) * kSimtPad + 4 * ty) = make_float4(z[0][j], z[1][j], z[2][j], z[3][j]);
+            __syncwarp();
+            const int live = min(kSimtKeys, s.end - k0);
+            for (int k = 0; k < live; ++k) {
+                const float4 q = *reinterpret_cast<const float4*>(sp + k * kSimtPad + 4 * ty);
+                const float pv[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int b = 0; b < DC; ++b) {
+                    const float4 v = *reinterpret_cast<const float4*>(sv + k * 64 * DC + b * 64 + 4 * tx);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        o[b][i][0] = fmaf(pv[i], v.x, o[b][i][0]);
+                        o[b][i][1] = fmaf(pv[i], v.y, o[b][i][1]);
+                        o[b][i][2] = fmaf(pv[i], v.z, o[b][i][2]);
+                        o[b][i][3] = fmaf(pv[i], v.w, o[b][i][3]);
+                    }
+                }
+            }
+        }
+        float* part = a.part + p.slot(cta) * attn_part_floats(a);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 4 * ty + i;
+            if (r >= n) continue;
+            const int64_t row = r0 + r;
+            const size_t at = (w.first + row / a.G) * a.Hq + p.head * a.G + row % a.G;
+            const float inv = sum[i] > 0.f ? 1.f / sum[i] : sum[i] == 0.f ? 0.f : sum[i];
+#pragma unroll
+            for (int b = 0; b < DC; ++b)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int d = b * 64 + 4 * tx + j;
+                    if (d >= a.D) continue;
+                    if (p.whole()) store_act(a.out, at * a.D + d, o[b][i][j] * inv, a.dtype);
+                    else part[(size_t)r * a.D + d] = o[b][i][j];
+                }
+            if (tx == 0) {
+                if (!p.whole()) {
+                    part[(size_t)a.block * a.D + r] = top[i];
+                    part[(size_t)a.block * (a.D + 1) + r] = sum[i];
+                } else if (a.lse) {
+                    a.lse[at] = sum[i] == 0.f ? -INFINITY : (top[i] + log2f(sum[i])) * 0.6931471805599453f;
+                }
+            }
+        }
+    }
+}
+
+template <typename E, int DC> cudaError_t simt_launch(const AttnArgs& a, cudaStream_t st) {
+    const size_t D4 = (a.D + 3) / 4 * 4, bytes = 4 * (2 * D4 * kSimtPad + (size_t)kSimtKeys * 64 * DC + kSimtKeys * kSimtPad);
+    static bool set[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+    if (dev < 0 || dev >= 64 || !set[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<E, DC>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) set[dev] = true;
+    }
+    attn_simt_kernel<E, DC><<<a.ctas, kSimtThreads, bytes, st>>>(a);
+    return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ host
+
+size_t up(size_t n) { return (n + 255) / 256 * 256; }
+
+kda_status attn_check(const kda_attention_dims* d, bool varlen, bool append, AttnArgs* a) {
+    if (!d || d->rows < 1 || d->tokens < 1 || d->Hkv < 1 || d->D < 1) return KDA_ERR_INVALID_ARG;
+    if (d->dtype != KDA_BF16 && d->dtype != KDA_FP32) return KDA_ERR_INVALID_ARG;
+    if (d->num_pages < 1 || d->page_tokens < 1 || d->table_rows < 1 || d->max_pages < 1 || d->window < 0) return KDA_ERR_INVALID_ARG;
+    if (!append && (d->Hq < 1 || d->Hq % d->Hkv)) return KDA_ERR_INVALID_ARG;
+    if (!varlen && d->tokens % d->rows) return KDA_ERR_INVALID_ARG;
+    if (d->D > 256) return KDA_ERR_UNSUPPORTED;
+    const int64_t kv = (int64_t)d->Hkv * d->D, q = (int64_t)d->Hq * d->D;
+    if (append ? (d->k_stride != 0 && d->k_stride < kv) || (d->v_stride != 0 && d->v_stride < kv) : d->q_stride != 0 && d->q_stride < q)
+        return KDA_ERR_INVALID_ARG;
+    const int64_t most = 1LL << 30;
+    if (d->tokens > most || d->rows > (1 << 24) || kv > (1 << 24) || q > (1 << 24) || (int64_t)d->num_pages > most ||
+        (int64_t)d->max_pages * d->page_tokens > most || (int64_t)d->table_rows * d->max_pages > (1LL << 40))
+        return KDA_ERR_UNSUPPORTED;
+    if (2 * kv * d->page_tokens > (1LL << 40) / d->num_pages) return KDA_ERR_UNSUPPORTED;
+    if (!append && (int64_t)d->tokens * d->Hq > (1LL << 31) - 1) return KDA_ERR_UNSUPPORTED;
+    for (int64_t s : {d->q_stride, d->k_stride, d->v_stride})
+        if (s > (1LL << 40) / d->tokens) return KDA_ERR_UNSUPPORTED;
+    memset(a, 0, sizeof(*a));
+    a->rows = d->rows; a->tokens = d->tokens; a->per_row = varlen ? 0 : d->tokens / d->rows;
+    a->Hq = d->Hq; a->Hkv = d->Hkv; a->G = append ? 1 : d->Hq / d->Hkv; a->D = d->D; a->dtype = d->dtype;
+    a->pages = d->num_pages; a->pt = d->page_tokens; a->table_rows = d->table_rows; a->max_pages = d->max_pages;
+    a->window = d->window;
+    a->qs = d->q_stride ? d->q_stride : q;
+    return KDA_OK;
+}
+
+// The cut for a kernel of `block` packed rows, `tile` keys and at most `ctas` CTAs.
+void attn_cut(AttnArgs* a, int block, int tile, int ctas) {
+    a->block = block;
+    a->tile = tile;
+    a->ctas = ctas;
+    const int64_t most = ((int64_t)a->tokens * a->G + block - 1) / block + a->rows;      // a row's last block may be short
+    a->units_most = (int)(most < (1LL << 30) ? most : (1LL << 30));
+}
+size_t attn_layout(char* ws, AttnArgs* a) {
+    size_t o = 0;
+    auto take = [&](size_t n) {
+        char* p = ws ? ws + o : nullptr;
+        o += up(n);
+        return p;
+    };
+    a->units = reinterpret_cast<int*>(take(4));
+    a->start = reinterpret_cast<int64_t*>(take(8 * ((size_t)a->units_most + 1)));
+    a->unit_row = reinterpret_cast<int*>(take(8 * (size_t)a->units_most));
+    a->part = reinterpret_cast<float*>(take((size_t)2 * a->ctas * a->block * (a->D + 2) * 4));
+    return o;
+}
+
+// Which kernel a call takes, and its cut.
+void attn_choose(AttnArgs* a) { attn_cut(a, kSimtRows, kSimtKeys, a->D > 128 ? 152 : 304); }
+
+}  // namespace
+
+cudaError_t launch_attn_simt(const AttnArgs& a, cudaStream_t st) {
+#define KDA_ATTN_SIMT(DC) return a.dtype == KDA_BF16 ? simt_launch<__nv_bfloat16, DC>(a, st) : simt_launch<float, DC>(a, st)
+    if (a.D <= 64) KDA_ATTN_SIMT(1);
+    if (a.D <= 128) KDA_ATTN_SIMT(2);
+    KDA_ATTN_SIMT(4);
+#undef KDA_ATTN_SIMT
+}
+
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" {
+
+kda_status kda_pages_append(const kda_attention_dims* dims, void* pool, const int32_t* table, const int32_t* lengths,
+                            const int32_t* seqs, const int32_t* cu_seqlens, const int32_t* cu_seqlens_host, const void* k,
+                            const void* v, cudaStream_t stream) {
+    AppendArgs p;
+    memset(&p, 0, sizeof(p));
+    kda_status st = attn_check(dims, cu_seqlens != nullptr, true, &p.a);
+    if (st != KDA_OK) return st;
+    if (!pool || !table || !lengths || !k || !v) return KDA_ERR_INVALID_ARG;
+    if (!seqs && p.a.rows > p.a.table_rows) return KDA_ERR_INVALID_ARG;
+    st = check_offsets_host(p.a.rows, p.a.tokens, cu_seqlens, cu_seqlens_host);
+    if (st != KDA_OK) return st;
+    const int64_t kv = (int64_t)p.a.Hkv * p.a.D, es = p.a.dtype == KDA_BF16 ? 2 : 4;
+    p.k = k; p.v = v; p.pool = pool;
+    p.ks = dims->k_stride ? dims->k_stride : kv;
+    p.vs = dims->v_stride ? dims->v_stride : kv;
+    const size_t np = (size_t)p.a.pages * 2 * kv * p.a.pt * es;
+    if (ranges_meet(pool, np, k, ((size_t)(p.a.tokens - 1) * p.ks + kv) * es) || ranges_meet(pool, np, v, ((size_t)(p.a.tokens - 1) * p.vs + kv) * es))
+        return KDA_ERR_INVALID_ARG;
+    p.a.table = table; p.a.lengths = lengths; p.a.seqs = seqs; p.a.cu = cu_seqlens;
+    st = status_ptr(&p.a.status);
+    if (st != KDA_OK) return st;
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(pool) | reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
+                           (uintptr_t)(p.ks * es) | (uintptr_t)(p.vs * es) | (uintptr_t)(p.a.D * es);
+    const int grid = (p.a.tokens + kAppendWarps - 1) / kAppendWarps;
+    timing_pre(stream, K_PAGES_APPEND);
+    if (bits % 16 == 0) append_kernel<uint4><<<grid, kAppendWarps * 32, 0, stream>>>(p);
+    else if (es == 4) append_kernel<uint32_t><<<grid, kAppendWarps * 32, 0, stream>>>(p);
+    else append_kernel<uint16_t><<<grid, kAppendWarps * 32, 0, stream>>>(p);
+    timing_post(stream);
+    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+size_t kda_pages_attention_workspace_size(const kda_attention_dims* dims) {
+    AttnArgs a;
+    if (!dims || attn_check(dims, true, false, &a) != KDA_OK) return 0;
+    attn_choose(&a);
+    return attn_layout(nullptr, &a);
+}
+
+kda_status kda_pages_attention(const kda_attention_dims* dims, const void* q, const void* pool, const int32_t* table,
+                               const int32_t* lengths, const int32_t* seqs, const int32_t* cu_seqlens,
+                               const int32_t* cu_seqlens_host, float scale, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, cudaStream_t stream) {
+    AttnArgs a;
+    kda_status st = attn_check(dims, cu_seqlens != nullptr, false, &a);
+    if (st != KDA_OK) return st;
+    if (!q || !pool || !table || !lengths || !out || !isfinite(scale)) return KDA_ERR_INVALID_ARG;
+    if (!seqs && a.rows > a.table_rows) return KDA_ERR_INVALID_ARG;
+    st = check_offsets_host(a.rows, a.tokens, cu_seqlens, cu_seqlens_host);
+    if (st != KDA_OK) return st;
+    const size_t es = a.dtype == KDA_BF16 ? 2 : 4, no = (size_t)a.tokens * a.Hq * a.D * es, nl = (size_t)a.tokens * a.Hq * 4;
+    const size_t nq = ((size_t)(a.tokens - 1) * a.qs + (size_t)a.Hq * a.D) * es, np = (size_t)a.pages * 2 * a.Hkv * a.pt * a.D * es;
+    if (ranges_meet(out, no, q, nq) || ranges_meet(out, no, pool, np) || ranges_meet(lse, nl, q, nq) || ranges_meet(lse, nl, pool, np) ||
+        ranges_meet(out, no, lse, nl))
+        return KDA_ERR_INVALID_ARG;
+    attn_choose(&a);
+    if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || workspace_bytes < attn_layout(nullptr, &a)) return KDA_ERR_WORKSPACE;
+    attn_layout(static_cast<char*>(workspace), &a);
+    a.q = q; a.pool = pool; a.table = table; a.lengths = lengths; a.seqs = seqs; a.cu = cu_seqlens; a.scale = scale; a.out = out; a.lse = lse;
+    if ((int64_t)a.units_most * a.Hkv > (1LL << 30)) return KDA_ERR_UNSUPPORTED;
+    st = status_ptr(&a.status);
+    if (st != KDA_OK) return st;
+    timing_pre(stream, K_ATTN_PLAN);
+    attn_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
+    timing_post(stream);
+    if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+    timing_pre(stream, K_ATTN);
+    const cudaError_t e = launch_attn_simt(a, stream);
+    timing_post(stream);
+    if (e != cudaSuccess) return KDA_ERR_CUDA;
+    timing_pre(stream, K_ATTN_JOIN);
+    attn_join_kernel<<<a.units_most * a.Hkv, kJoinThreads, 0, stream>>>(a);
+    timing_post(stream);
+    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // extern "C"

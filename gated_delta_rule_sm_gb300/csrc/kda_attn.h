@@ -1,0 +1,132 @@
+// kda_attn.h -- what the attention kernels over paged keys and values share: the problem, how it is cut into pieces,
+// and what a piece leaves behind.
+//
+// The query heads of one key head and the new tokens of a row are one axis of packed query rows, token by token
+// (packed row = token * G + head in the group), so that a tile of keys serves all of them.  A unit is a block of
+// `block` packed rows of one row of the call with every key tile that one of them sees, at least one; an item is a unit
+// for one key head.  All items' key tiles, laid end to end, are cut into equal spans, one to a CTA: a CTA finishes the
+// items that lie in its span, and leaves the sums of those that it shares with other CTAs for the join.
+#pragma once
+
+#include "kda_internal.h"
+
+namespace kda {
+
+struct AttnArgs {
+    int rows, tokens, per_row;           // per_row: tokens of a row without cu
+    int Hq, Hkv, G, D, dtype;
+    int pages, pt, table_rows, max_pages, window;
+    int64_t qs;                          // elements between tokens of q
+    float scale;
+    const void *q, *pool;
+    const int32_t *table, *lengths, *seqs, *cu;
+    void* out;
+    float* lse;
+    // the cut
+    int block, tile;                     // packed rows of a unit, keys of a tile
+    int ctas;                            // most spans; with fewer tiles than that a tile each
+    int units_most;
+    int* units;                          // [1] units of the call, -1: nothing to do (workspace)
+    int64_t* start;                      // [units + 1] tiles of one key head before each unit (workspace)
+    int* unit_row;                       // [units] row of the call, [units_most + units] block in it (workspace)
+    float* part;                         // [2 ctas] sums of shared items: block x D, then block maxima, then block sums
+    int* status;
+};
+
+struct AttnRow {
+    int seq, len, n, first;              // table row (-1: idle), its tokens, new ones, the first one's index
+};
+
+// Row r of the call; what is wrong with it is recorded by one thread where `report`.
+__device__ __forceinline__ AttnRow attn_row(const AttnArgs& a, int r, bool report) {
+    AttnRow w;
+    w.first = a.cu ? a.cu[r] : r * a.per_row;
+    w.n = a.cu ? a.cu[r + 1] - w.first : a.per_row;
+    w.seq = a.seqs ? a.seqs[r] : r;
+    w.len = 0;
+    bool bad = w.seq >= a.table_rows;
+    if (!bad && w.seq >= 0) {
+        w.len = max(a.lengths[w.seq], 0);
+        bad = w.len > (int64_t)a.max_pages * a.pt;
+    }
+    if (bad) {
+        if (report) record_error(a.status, KDA_ERR_INVALID_ARG);
+        w.seq = -1;
+        w.len = 0;
+    }
+    return w;
+}
+
+// Keys [begin, end) that the packed rows of a block see, and the tiles that hold them: at least one, which may hold none.
+struct AttnSpan {
+    int begin, end, tile0, tiles;
+};
+__device__ __forceinline__ AttnSpan attn_span(const AttnArgs& a, const AttnRow& w, int block) {
+    AttnSpan s;
+    const int64_t r0 = (int64_t)block * a.block, last = (int64_t)w.n * a.G - 1;
+    const int64_t r1 = r0 + a.block - 1 < last ? r0 + a.block - 1 : last;
+    const int p0 = w.len - w.n + (int)(r0 / a.G), p1 = w.len - w.n + (int)(r1 / a.G);
+    s.end = w.seq < 0 ? 0 : max(p1 + 1, 0);
+    s.begin = a.window ? max(p0 - a.window + 1, 0) : 0;
+    if (s.begin >= s.end) s.begin = s.end = 0;
+    s.tile0 = s.begin / a.tile;
+    s.tiles = max((s.end + a.tile - 1) / a.tile - s.tile0, 1);
+    return s;
+}
+__device__ __forceinline__ int attn_blocks(const AttnArgs& a, int n) { return (int)(((int64_t)n * a.G + a.block - 1) / a.block); }
+
+// The spans of the CTAs over `total` tiles.
+struct AttnCut {
+    int64_t total;
+    int ctas;
+    __device__ __forceinline__ AttnCut(const AttnArgs& a, int64_t t) : total(t), ctas((int)(t < a.ctas ? t : a.ctas)) {}
+    __device__ __forceinline__ int64_t begin(int c) const { return total * c / ctas; }
+    __device__ __forceinline__ int owner(int64_t x) const { return (int)(((x + 1) * ctas + total - 1) / total) - 1; }   // begin(owner) <= x
+};
+
+// The unit that holds tile x of all key heads' tiles.
+__device__ __forceinline__ int attn_unit(const AttnArgs& a, int units, int64_t x) {
+    int lo = 0, hi = units - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a.start[mid] * a.Hkv <= x) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+// One CTA's part of one item: tiles [t0, t1) of its `tiles`.
+struct AttnPiece {
+    int row, block, head, t0, t1, tiles;
+    __device__ __forceinline__ bool whole() const { return t1 - t0 == tiles; }
+    // where its sums go: a CTA shares at most the item it starts inside of and the one it does not finish
+    __device__ __forceinline__ int slot(int cta) const { return 2 * cta + (t0 == 0); }
+};
+__device__ __forceinline__ AttnPiece attn_piece(const AttnArgs& a, int units, int64_t x, int64_t end) {
+    AttnPiece p;
+    const int u = attn_unit(a, units, x);
+    const int64_t first = a.start[u], off = x - first * a.Hkv;
+    p.tiles = (int)(a.start[u + 1] - first);
+    p.row = a.unit_row[u];
+    p.block = a.unit_row[a.units_most + u];
+    p.head = (int)(off / p.tiles);
+    p.t0 = (int)(off - (int64_t)p.head * p.tiles);
+    p.t1 = (int)(end - x < p.tiles - p.t0 ? p.t0 + (end - x) : p.tiles);
+    return p;
+}
+
+__device__ __forceinline__ size_t attn_part_floats(const AttnArgs& a) { return (size_t)a.block * (a.D + 2); }
+
+// Address of a page's keys (values: + Hkv page_tokens D elements) for key head h; nullptr where the table names none.
+__device__ __forceinline__ const char* attn_page(const AttnArgs& a, int seq, int key, int head, int es) {
+    const int page = a.table[(size_t)seq * a.max_pages + key / a.pt];
+    if (page < 0 || page >= a.pages) {
+        record_error(a.status, KDA_ERR_INVALID_ARG);
+        return nullptr;
+    }
+    const size_t head_bytes = (size_t)a.pt * a.D * es;
+    return static_cast<const char*>(a.pool) + ((size_t)page * 2 * a.Hkv + head) * head_bytes + (size_t)(key % a.pt) * a.D * es;
+}
+
+cudaError_t launch_attn_simt(const AttnArgs& a, cudaStream_t st);
+
+}  // namespace kda

@@ -70,6 +70,8 @@ enum KernelId {
     K_CONV_FWD, K_CONV_BWD, K_CONV_REDUCE, K_DIAG_TC, K_SEG_COMBINE, K_NORM_FWD, K_NORM_BWD, K_NORM_REDUCE,
     K_DECODE_STEP, K_SSM_STEP, K_CONV_PROMPT, K_CONV_STEP, K_SSM_PLAN, K_SSM_STATE, K_SSM_JOIN, K_SSM_OUT,
     K_PAGES_COUNT, K_PAGES_ASSIGN, K_PAGES_APPLY, K_PAGES_COPY,
+    K_GATED_PLAN, K_GATED_SCAN, K_GATED_BWD, K_GATED_REDUCE, K_GATED_STEP,
+    K_PAGES_APPEND, K_ATTN_PLAN, K_ATTN, K_ATTN_JOIN,
     K_NUM_KERNELS
 };
 

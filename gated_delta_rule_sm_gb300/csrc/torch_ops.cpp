@@ -532,6 +532,203 @@ PyObject* pages_compact(PyObject* const* o) {
     return map.object();
 }
 
+// ------------------------------------------------------------------ gated linear recurrence
+
+struct GatedIn {
+    const Tensor *x, *g, *i;
+    int dev;
+    int64_t C;
+    kda_gated_dims dims;
+    const float* a_log;
+};
+// x, g_raw, i_raw, a_log
+GatedIn gated_in(PyObject* const* o, int lead) {
+    GatedIn s;
+    s.x = &leading("x", o[0], lead + 1);
+    s.g = &tensor("g_raw", o[1]);
+    s.i = &tensor("i_raw", o[2]);
+    s.dev = (int)s.x->get_device();
+    memset(&s.dims, 0, sizeof(s.dims));
+    s.dims.dtype = dtype_code(*s.x);
+    if (s.g->sizes() != s.x->sizes() || s.i->sizes() != s.x->sizes()) refuse("x, g_raw and i_raw must have one shape");
+    if (s.g->scalar_type() != s.x->scalar_type() || s.i->scalar_type() != s.x->scalar_type())
+        refuse("x, g_raw and i_raw must have one dtype");
+    on_device("g_raw", *s.g, s.dev);
+    on_device("i_raw", *s.i, s.dev);
+    s.C = s.x->size(lead);
+    s.dims.B = as_int("B", s.x->size(0));
+    s.dims.T = lead == 2 ? as_int("T", s.x->size(1)) : 1;
+    s.dims.C = as_int("C", s.C);
+    s.dims.x_stride = token_stride("x", *s.x, lead);
+    s.dims.g_stride = token_stride("g_raw", *s.g, lead);
+    s.dims.i_stride = token_stride("i_raw", *s.i, lead);
+    s.a_log = need_f("a_log", o[3], {s.C}, s.dev);
+    return s;
+}
+
+// A buffer of bytes, whatever its tensor's type.
+struct Bytes {
+    void* p = nullptr;
+    size_t size = 0;
+    Bytes(const char* name, PyObject* o, int dev) {
+        if (o == Py_None) return;
+        const Tensor& t = tensor(name, o);
+        on_device(name, t, dev);
+        if (!t.is_contiguous()) refuse(std::string(name) + " must be contiguous");
+        p = t.data_ptr();
+        size = t.nbytes();
+    }
+};
+
+// Rows of a call, its offsets' address in *cu (num_seqs in *n) where it has some.
+int64_t packed_rows(PyObject* o, int64_t B, int dev, const int32_t** cu, int* n) {
+    *cu = nullptr;
+    if (o == Py_None) return B;
+    const int64_t rows = documents(o);
+    *cu = need_i("cu_seqlens", o, {rows + 1}, dev);
+    *n = (int)rows;
+    return rows;
+}
+
+// (x, g_raw, i_raw, a_log, cu_seqlens, host offsets' address, initial_state, output_final_state, out, final_state, saved)
+PyObject* gated_scan(PyObject* const* o) {
+    GatedIn s = gated_in(o, 2);
+    const int32_t* cu;
+    const int64_t rows = packed_rows(o[4], s.dims.B, s.dev, &cu, &s.dims.num_seqs);
+    const int64_t state[2] = {rows, s.C};
+    const float* s0 = need_f("initial_state", o[6], state, s.dev);
+    const cudaStream_t st = current_stream(s.dev);
+    const Result out("out", o[8], *s.x, s.x->sizes(), s.x->scalar_type());
+    const int wants = PyObject_IsTrue(o[7]);
+    if (wants < 0) throw Raised();
+    PyObject* last = Py_None;
+    void* pf = nullptr;
+    Tensor own;
+    if (wants) {
+        const Result f("final_state", o[9], *s.x, state, at::kFloat);
+        own = f.own;
+        last = f.given;
+        pf = f.p;
+    }
+    const Bytes saved("saved", o[10], s.dev);
+    const Scratch ws(*s.x, "gated", st, kda_gated_scan_fwd_workspace_size(&s.dims));
+    check(kda_gated_scan_fwd(&s.dims, s.x->data_ptr(), s.g->data_ptr(), s.i->data_ptr(), s.a_log, cu, host_copy(o[5]), s0, out.p,
+                             static_cast<float*>(pf), saved.p, saved.size, ws.p, ws.size, st), "kda_gated_scan_fwd");
+    return pair(out.object(), last ? Py_NewRef(last) : THPVariable_Wrap(own));
+}
+
+// (x)
+PyObject* gated_scan_saved_size(PyObject* const* o) {
+    const Tensor& x = tensor("x", o[0]);
+    if (x.dim() != 3) refuse("x must have 3 axes, got " + shape_text(x.sizes()));
+    kda_gated_dims d;
+    memset(&d, 0, sizeof(d));
+    d.B = as_int("B", x.size(0)); d.T = as_int("T", x.size(1)); d.C = as_int("C", x.size(2)); d.dtype = dtype_code(x);
+    return PyLong_FromSize_t(kda_gated_scan_saved_size(&d));
+}
+
+// (x, g_raw, i_raw, a_log, dy, cu_seqlens, host offsets' address, initial_state, dfinal_state, want_dinitial_state, saved)
+PyObject* gated_scan_backward(PyObject* const* o) {
+    GatedIn s = gated_in(o, 2);
+    const void* dy = need("dy", o[4], s.x->scalar_type(), s.x->sizes(), s.dev);
+    const int32_t* cu;
+    const int64_t rows = packed_rows(o[5], s.dims.B, s.dev, &cu, &s.dims.num_seqs);
+    const int64_t state[2] = {rows, s.C};
+    const float *s0 = need_f("initial_state", o[7], state, s.dev), *ds = need_f("dfinal_state", o[8], state, s.dev);
+    const int wants = PyObject_IsTrue(o[9]);
+    if (wants < 0) throw Raised();
+    const Bytes saved("saved", o[10], s.dev);
+    const cudaStream_t st = current_stream(s.dev);
+    const Tensor dx = fresh(*s.x, s.x->sizes(), at::kFloat), dg = fresh(*s.x, s.x->sizes(), at::kFloat), di = fresh(*s.x, s.x->sizes(), at::kFloat),
+                 da = fresh(*s.x, {s.C}, at::kFloat), d0 = wants ? fresh(*s.x, state, at::kFloat) : Tensor();
+    const Scratch ws(*s.x, "gated_bwd", st, kda_gated_scan_bwd_workspace_size(&s.dims));
+    auto f = [](const Tensor& t) { return t.defined() ? static_cast<float*>(t.data_ptr()) : nullptr; };
+    check(kda_gated_scan_bwd(&s.dims, s.x->data_ptr(), s.g->data_ptr(), s.i->data_ptr(), s.a_log, cu, host_copy(o[6]), s0, dy, ds, f(dx), f(dg),
+                             f(di), f(da), f(d0), saved.p, saved.size, ws.p, ws.size, st), "kda_gated_scan_bwd");
+    PyObject* r = PyTuple_New(5);
+    if (!r) throw Raised();
+    int k = 0;
+    for (const Tensor* t : {&dx, &dg, &di, &da, &d0}) PyTuple_SET_ITEM(r, k++, t->defined() ? THPVariable_Wrap(*t) : Py_NewRef(Py_None));
+    return r;
+}
+
+// (x, g_raw, i_raw, a_log, state, slots, state_out, out)
+PyObject* gated_step(PyObject* const* o) {
+    const GatedIn s = gated_in(o, 1);
+    const Pool pool("state", o[4], o[5], o[6], s.dims.B, {s.C}, at::kFloat, s.dev);
+    const Result out("out", o[7], *s.x, s.x->sizes(), s.x->scalar_type());
+    check(kda_gated_step(&s.dims, s.x->data_ptr(), s.g->data_ptr(), s.i->data_ptr(), s.a_log, pool.slots, pool.n,
+                         static_cast<const float*>(pool.in), static_cast<float*>(pool.out), out.p, current_stream(s.dev)), "kda_gated_step");
+    return pair(out.object(), Py_NewRef(pool.written));
+}
+
+// ------------------------------------------------------------------ keys and values in pages
+
+struct KeysIn {
+    int dev;
+    kda_attention_dims d;
+    void* pool;
+    const int32_t *table, *lengths, *seqs, *cu;
+};
+// t: the call's tokens [B, n, heads, D] (k or q)
+KeysIn keys_in(const char* name, const Tensor& t, PyObject* pool, PyObject* table, PyObject* lengths, PyObject* seqs, PyObject* cu) {
+    KeysIn s;
+    s.dev = (int)t.get_device();
+    memset(&s.d, 0, sizeof(s.d));
+    s.d.dtype = dtype_code(t);
+    const Tensor &p = tensor("pool", pool), &tab = tensor("table", table);
+    if (p.dim() != 5 || p.size(1) != 2 || p.size(4) != t.size(3))
+        refuse("pool must be [pages, 2, key heads, page tokens, D] with " + std::string(name) + "'s D, got " + shape_text(p.sizes()));
+    if (tab.dim() != 2) refuse("table must be [sequences, pages of a row], got " + shape_text(tab.sizes()));
+    s.pool = need("pool", pool, t.scalar_type(), p.sizes(), s.dev);
+    s.table = need_i("table", table, tab.sizes(), s.dev);
+    s.lengths = need_i("lengths", lengths, {tab.size(0)}, s.dev);
+    if (!s.lengths) refuse("lengths must be a tensor");
+    int n = 0;
+    const int64_t rows = packed_rows(cu, t.size(0), s.dev, &s.cu, &n);
+    if (s.cu && t.size(0) != 1) refuse(std::string(name) + " must be [1, tokens, heads, D] with cu_seqlens");
+    s.seqs = need_i("seqs", seqs, {rows}, s.dev);
+    s.d.rows = as_int("rows", rows);
+    s.d.tokens = as_int("tokens", t.size(0) * t.size(1));
+    s.d.Hkv = as_int("heads", p.size(2));
+    s.d.D = as_int("D", p.size(4));
+    s.d.num_pages = as_int("pages", p.size(0));
+    s.d.page_tokens = as_int("page tokens", p.size(3));
+    s.d.table_rows = as_int("sequences", tab.size(0));
+    s.d.max_pages = as_int("pages of a row", tab.size(1));
+    return s;
+}
+
+// (pool, table, lengths, k, v, seqs, cu_seqlens, host offsets' address)
+PyObject* pages_append(PyObject* const* o) {
+    const Tensor &k = leading("k", o[3], 4), &v = tensor("v", o[4]);
+    KeysIn s = keys_in("k", k, o[0], o[1], o[2], o[5], o[6]);
+    if (v.sizes() != k.sizes() || v.scalar_type() != k.scalar_type()) refuse("k and v must have one shape and dtype");
+    on_device("v", v, s.dev);
+    if (k.size(2) != s.d.Hkv) refuse("k must have the pool's heads (" + std::to_string(s.d.Hkv) + "), got " + shape_text(k.sizes()));
+    s.d.k_stride = token_stride("k", k, 2);
+    s.d.v_stride = token_stride("v", v, 2);
+    check(kda_pages_append(&s.d, s.pool, s.table, s.lengths, s.seqs, s.cu, host_copy(o[7]), k.data_ptr(), v.data_ptr(), current_stream(s.dev)),
+          "kda_pages_append");
+    return Py_NewRef(o[0]);
+}
+
+// (q, pool, table, lengths, scale, seqs, cu_seqlens, host offsets' address, window, out, lse)
+PyObject* pages_attention(PyObject* const* o) {
+    const Tensor& q = leading("q", o[0], 4);
+    KeysIn s = keys_in("q", q, o[1], o[2], o[3], o[5], o[6]);
+    s.d.Hq = as_int("heads", q.size(2));
+    s.d.q_stride = token_stride("q", q, 2);
+    s.d.window = (int)integer("window", o[8]);
+    const cudaStream_t st = current_stream(s.dev);
+    const Result out("out", o[9], q, q.sizes(), q.scalar_type());
+    float* lse = need_f("lse", o[10], q.sizes().slice(0, 3), s.dev);
+    const Scratch ws(q, "attention", st, kda_pages_attention_workspace_size(&s.d));
+    check(kda_pages_attention(&s.d, q.data_ptr(), s.pool, s.table, s.lengths, s.seqs, s.cu, host_copy(o[7]), (float)number(o[4]), out.p, lse,
+                              ws.p, ws.size, st), "kda_pages_attention");
+    return out.object();
+}
+
 // (t, lead)
 PyObject* token_stride_of(PyObject* const* o) { return PyLong_FromLongLong(token_stride("x", tensor("x", o[0]), (int)integer("lead", o[1]))); }
 
@@ -594,6 +791,9 @@ PyMethodDef methods[] = {
     method<short_conv_prompt, 8>("short_conv_prompt"), method<short_conv_step, 7>("short_conv_step"),
     method<pages_copy, 4>("pages_copy"), method<pages_fork, 11>("pages_fork"), method<pages_extend, 10>("pages_extend"),
     method<pages_free, 7>("pages_free"), method<pages_compact, 6>("pages_compact"),
+    method<gated_scan, 11>("gated_scan"), method<gated_scan_saved_size, 1>("gated_scan_saved_size"),
+    method<gated_scan_backward, 11>("gated_scan_backward"), method<gated_step, 8>("gated_step"),
+    method<pages_append, 8>("pages_append"), method<pages_attention, 11>("pages_attention"),
     method<token_stride_of, 2>("token_stride"),
     {"device_of", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&device_of_args)), METH_FASTCALL, nullptr},
     {"setup", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&setup)), METH_FASTCALL, nullptr},

@@ -515,6 +515,52 @@ kda_status kda_short_conv_step(int B, int C, int W, kda_dtype dtype, const void*
                                const void* history_in, void* history_out, void* y, cudaStream_t stream);
 
 /*
+ * Gated linear recurrence, the elementwise mixer: per channel
+ *     log a_t = -exp(a_log) sigmoid(g_t),   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t,   y_t = h_t
+ * x, g_raw, i_raw, y, dy [B, T, C] in dtype, a_log [C] fp32, states [rows, C] fp32 (rows = B, or num_seqs with
+ * cu_seqlens).  x, g_raw and i_raw may be slices of one projection's output: *_stride as in kda_ssm_dims; y and dy are
+ * contiguous.  Any C >= 1 and any alignment of the elements; bf16 with an even C, even strides and pairs of channels that
+ * are aligned as such is read two channels at a time.  Arithmetic and states in fp32.
+ * cu_seqlens and cu_seqlens_host: as for kda_ssm_fwd.  An empty document passes its state through.
+ * Results do not depend on timing (the order of every sum is fixed).  Gates: e^-g and e^-i stop at 2^60.
+ *
+ * kda_gated_scan_fwd: initial_state (NULL: zero) and final_state (NULL: not wanted).  saved (NULL: not wanted):
+ *   kda_gated_scan_saved_size() bytes, 256-byte aligned, gets the states that enter every 64th token of the flattened
+ *   tokens for kda_gated_scan_bwd on the same inputs.
+ *   In place: y may be x where x is contiguous, final_state may be initial_state; any other overlap of a result with
+ *   another or with x, g_raw, i_raw or initial_state is KDA_ERR_INVALID_ARG.
+ * kda_gated_scan_bwd: from dy and dfinal_state (NULL: zero), dx, dg_raw, di_raw [B, T, C], da_log [C] and dinitial_state
+ *   [rows, C] (NULL: not wanted), all fp32.  saved may be NULL: the states are then computed again.  No result may
+ *   overlap an input or another result.
+ * Both need a workspace (256-byte aligned) of kda_gated_scan_fwd_workspace_size / _bwd_workspace_size bytes; the sizes are
+ * 0 on invalid input.  A device-only cu_seqlens that breaks the contract records KDA_ERR_INVALID_ARG in the device status
+ * word; y and the per-token gradients are then not written, final_state gets the entering state, dinitial_state the
+ * final state's gradient, da_log zeros.
+ * kda_gated_step: one token per row (dims->T == 1, x, g_raw, i_raw, y [B, C]; strides are row strides) on a slot pool
+ *   [num_slots, C] fp32.
+ */
+typedef struct {
+    int B, T, C;
+    kda_dtype dtype;
+    int num_seqs;
+    int64_t x_stride, g_stride, i_stride;
+} kda_gated_dims;
+size_t kda_gated_scan_fwd_workspace_size(const kda_gated_dims* dims);
+size_t kda_gated_scan_bwd_workspace_size(const kda_gated_dims* dims);
+size_t kda_gated_scan_saved_size(const kda_gated_dims* dims);
+kda_status kda_gated_scan_fwd(const kda_gated_dims* dims, const void* x, const void* g_raw, const void* i_raw, const float* a_log,
+                              const int32_t* cu_seqlens, const int32_t* cu_seqlens_host, const float* initial_state, void* y,
+                              float* final_state, void* saved, size_t saved_bytes, void* workspace, size_t workspace_bytes,
+                              cudaStream_t stream);
+kda_status kda_gated_scan_bwd(const kda_gated_dims* dims, const void* x, const void* g_raw, const void* i_raw, const float* a_log,
+                              const int32_t* cu_seqlens, const int32_t* cu_seqlens_host, const float* initial_state, const void* dy,
+                              const float* dfinal_state, float* dx, float* dg_raw, float* di_raw, float* da_log,
+                              float* dinitial_state, const void* saved, size_t saved_bytes, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
+kda_status kda_gated_step(const kda_gated_dims* dims, const void* x, const void* g_raw, const void* i_raw, const float* a_log,
+                          const int32_t* slots, int num_slots, const float* state_in, float* state_out, void* y, cudaStream_t stream);
+
+/*
  * Pages of a cache.  A pool holds `layers` arrays of `num_pages` pages of page_bytes bytes, layer l at
  * pool + l * layer_stride (bytes; >= num_pages * page_bytes).  Every sequence has a row of
  * table [num_seqs, max_pages] (int32 page ids, -1 past its end) and a length in tokens; it holds
@@ -569,6 +615,51 @@ kda_status kda_pages_free(const kda_pages_dims* dims, const int32_t* table, cons
 kda_status kda_pages_compact(const kda_pages_dims* dims, void* pool, const int32_t* table, const int32_t* refs,
                              int32_t* table_out, int32_t* refs_out, int32_t* page_map, void* workspace,
                              size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Keys and values in the pages of a cache, and attention over them.  Page p of one layer's pool holds
+ * [2, Hkv, page_tokens, D] in dtype: the keys of page_tokens tokens, head by head, then their values; the page operators
+ * above move it as a whole.  Row r of a call works on table row seqs[r] (seqs NULL: row r); a negative seqs[r] marks
+ * an idle row.  lengths[s] counts the tokens of table row s, this call's new ones among them (kda_pages_extend comes
+ * first): the n_r new tokens of row r are at positions lengths[s] - n_r .. lengths[s] - 1.  n_r is tokens / rows without
+ * cu_seqlens, and cu_seqlens[r + 1] - cu_seqlens[r] with it (rows + 1 offsets from 0 to tokens, which never decrease).
+ *
+ * kda_pages_append: k and v [tokens, Hkv, D] into their places.  Tokens of idle rows and at negative positions are
+ *   not written.  seqs must not repeat, and no page may be held by two rows at the positions written.
+ * kda_pages_attention: for every new token and query head of q [tokens, Hq, D], with p its position,
+ *     out = sum_j softmax_j(scale q . k_j) v_j    over the keys j of p - window < j <= p (window 0: of 0 <= j <= p)
+ *   where query head h reads key head h / (Hq / Hkv).  out [tokens, Hq, D] in dtype; lse [tokens, Hq] fp32 (NULL: not
+ *   wanted) is the natural logarithm of the sum of exponentials.  A token without keys (an idle row, a negative position)
+ *   gets zeros, and lse -inf.  Keys past the window and the position are not read as numbers: whatever their pages
+ *   hold there, a masked key's score counts as nothing.  Only a value that is not finite, at a position that another
+ *   query of the same row may see, reaches queries that may not see it if both are in one tile of keys (0 times it).
+ *   Sums and statistics are fp32; bf16 calls round the weights to bf16 once before they meet the values.
+ *
+ * q, k and v may be slices of one projection's output: *_stride is the distance in elements between neighbouring tokens,
+ * 0 meaning contiguous.  out and lse are contiguous and overlap no input.
+ * Requirements: D <= 256, Hq a multiple of Hkv.  A seqs[r] past the table, a length past max_pages * page_tokens (the
+ * row then counts as idle), a page id outside [0, num_pages) at a position that is read or written (its keys and values
+ * read as zeros, nothing is written), or a device-only cu_seqlens that breaks its contract (nothing is written) records
+ * KDA_ERR_INVALID_ARG in the device status word.
+ * kda_pages_attention needs a workspace (256-byte aligned) of kda_pages_attention_workspace_size() bytes (0 on invalid
+ * input).  Long rows are cut into pieces that are joined by a second launch; the cut depends on the lengths only, so
+ * results do not depend on timing.
+ */
+typedef struct {
+    int rows, tokens, Hq, Hkv, D;
+    kda_dtype dtype;
+    int num_pages, page_tokens, table_rows, max_pages;
+    int window;
+    int64_t q_stride, k_stride, v_stride;
+} kda_attention_dims;
+kda_status kda_pages_append(const kda_attention_dims* dims, void* pool, const int32_t* table, const int32_t* lengths,
+                            const int32_t* seqs, const int32_t* cu_seqlens, const int32_t* cu_seqlens_host, const void* k,
+                            const void* v, cudaStream_t stream);
+size_t kda_pages_attention_workspace_size(const kda_attention_dims* dims);
+kda_status kda_pages_attention(const kda_attention_dims* dims, const void* q, const void* pool, const int32_t* table,
+                               const int32_t* lengths, const int32_t* seqs, const int32_t* cu_seqlens,
+                               const int32_t* cu_seqlens_host, float scale, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
