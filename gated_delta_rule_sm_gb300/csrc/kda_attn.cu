@@ -482,8 +482,17 @@ size_t attn_layout(char* ws, AttnArgs* a) {
     return o;
 }
 
-// Which kernel a call takes, and its cut.
-void attn_choose(AttnArgs* a) { attn_cut(a, kSimtRows, kSimtKeys, a->D > 128 ? 152 : 304); }
+// Which kernel a call takes, and its cut.  aligned: the pool's base allows 16-byte copies.
+void attn_choose(AttnArgs* a, bool aligned) {
+    const int64_t packed = (int64_t)a->tokens * a->G;
+    if (a->dtype == KDA_BF16 && a->D % 8 == 0 && aligned) {
+        a->kernel = kAttnMma;
+        attn_cut(a, a->D > 128 || packed <= 16 * (int64_t)a->rows ? 16 : 32, kAttnMmaKeys, a->D > 128 ? 152 : 304);
+    } else {
+        a->kernel = kAttnSimt;
+        attn_cut(a, kSimtRows, kSimtKeys, a->D > 128 ? 152 : 304);
+    }
+}
 
 }  // namespace
 
@@ -536,8 +545,13 @@ kda_status kda_pages_append(const kda_attention_dims* dims, void* pool, const in
 size_t kda_pages_attention_workspace_size(const kda_attention_dims* dims) {
     AttnArgs a;
     if (!dims || attn_check(dims, true, false, &a) != KDA_OK) return 0;
-    attn_choose(&a);
-    return attn_layout(nullptr, &a);
+    size_t most = 0;
+    for (bool aligned : {false, true}) {
+        attn_choose(&a, aligned);
+        const size_t n = attn_layout(nullptr, &a);
+        if (n > most) most = n;
+    }
+    return most;
 }
 
 kda_status kda_pages_attention(const kda_attention_dims* dims, const void* q, const void* pool, const int32_t* table,
@@ -556,7 +570,7 @@ kda_status kda_pages_attention(const kda_attention_dims* dims, const void* q, co
     if (ranges_meet(out, no, q, nq) || ranges_meet(out, no, pool, np) || ranges_meet(lse, nl, q, nq) || ranges_meet(lse, nl, pool, np) ||
         ranges_meet(out, no, lse, nl))
         return KDA_ERR_INVALID_ARG;
-    attn_choose(&a);
+    attn_choose(&a, reinterpret_cast<uintptr_t>(pool) % 16 == 0);
     if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || workspace_bytes < attn_layout(nullptr, &a)) return KDA_ERR_WORKSPACE;
     attn_layout(static_cast<char*>(workspace), &a);
     a.q = q; a.pool = pool; a.table = table; a.lengths = lengths; a.seqs = seqs; a.cu = cu_seqlens; a.scale = scale; a.out = out; a.lse = lse;
@@ -568,7 +582,7 @@ kda_status kda_pages_attention(const kda_attention_dims* dims, const void* q, co
     timing_post(stream);
     if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
     timing_pre(stream, K_ATTN);
-    const cudaError_t e = launch_attn_simt(a, stream);
+    const cudaError_t e = a.kernel == kAttnMma ? launch_attn_mma(a, stream) : launch_attn_simt(a, stream);
     timing_post(stream);
     if (e != cudaSuccess) return KDA_ERR_CUDA;
     timing_pre(stream, K_ATTN_JOIN);

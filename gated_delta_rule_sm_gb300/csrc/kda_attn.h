@@ -12,12 +12,15 @@
 
 namespace kda {
 
+enum AttnKernel { kAttnSimt, kAttnMma };
+
 struct AttnArgs {
     int rows, tokens, per_row;           // per_row: tokens of a row without cu
     int Hq, Hkv, G, D, dtype;
     int pages, pt, table_rows, max_pages, window;
     int64_t qs;                          // elements between tokens of q
     float scale;
+    int kernel;                          // AttnKernel
     const void *q, *pool;
     const int32_t *table, *lengths, *seqs, *cu;
     void* out;
@@ -127,6 +130,9 @@ __device__ __forceinline__ const char* attn_page(const AttnArgs& a, int seq, int
     return static_cast<const char*>(a.pool) + ((size_t)page * 2 * a.Hkv + head) * head_bytes + (size_t)(key % a.pt) * a.D * es;
 }
 
+// The kernels.  mma: bf16, D a multiple of 8, 16-byte aligned pool; blocks of 16 or 32 packed rows (16 with D above 128).
+constexpr int kAttnMmaKeys = 64;
+cudaError_t launch_attn_mma(const AttnArgs& a, cudaStream_t st);
 cudaError_t launch_attn_simt(const AttnArgs& a, cudaStream_t st);
 
 }  // namespace kda

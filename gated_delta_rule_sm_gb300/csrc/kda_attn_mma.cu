@@ -1,0 +1,351 @@
+// kda_attn_mma.cu -- attention of a few query rows over paged keys and values: the steps of a decoder.  bf16, D a multiple
+// of 8.
+//
+// One query row per head and token against every key of its sequence: 4 D operations for 4 D bytes of a key and its
+// value, times the query heads that share them (and the tokens of a short chunk).  Bound by memory; the warps' matrix
+// instructions (m16n8k16) do 16 packed rows at the price of one, which is what there is to hide behind the loads.
+//
+// A warp is on its own: it takes 16 of a tile's 64 keys, copies them and their values to its own ring in shared memory
+// (cp.async, two stages ahead, so that an SM has 128 KB on the way), and keeps its own maxima, sums and output; the
+// four warps of a CTA meet when a piece ends.  A lane looks up the page of one key, a stage before its address is needed.
+// Precision: scores and sums fp32; a weight is rounded to bf16 for its product with the values, 2^-8 of it at most,
+// and its sum is taken before that.  The maximum that scores are taken from is raised only when it is passed by more
+// than 8 (in log2): weights up to 2^8 lose nothing in bf16 or fp32, and the output is rescaled a few times, not each tile.
+#include <math.h>
+
+#include "kda.h"
+#include "kda_attn.h"
+#include "kda_common.cuh"
+#include "kda_sm100.cuh"
+
+namespace kda {
+
+using namespace sm100;
+
+namespace {
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kGroup = 16;      // kGroup: keys of a warp's step
+static_assert(kWarps * kGroup == kAttnMmaKeys, "a tile is a step of the four warps");
+constexpr float kRaise = 8.f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4t(uint32_t addr, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// d (16 x 8, fp32) += A (16 x 16) B (16 x 8), bf16
+__device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Byte of 16-byte piece c of row r in a tile of DP columns: the pieces of eight rows lie in different banks.
+template <int DP> __device__ __forceinline__ uint32_t piece(int r, int c) { return (uint32_t)(r * DP * 2 + ((c ^ (r & 7)) << 4)); }
+
+template <int DP, int MT> struct Lay {
+    static constexpr int STAGES = DP == 64 ? 4 : 3;
+    static constexpr uint32_t KV = kGroup * DP * 2;                       // keys (or values) of a stage
+    static constexpr uint32_t RING = kWarps * STAGES * 2 * KV;            // the warps' rings, then, at a piece's end, their outputs
+    static constexpr uint32_t Q = RING;                                   // MT tiles of 16 rows
+    static constexpr uint32_t STAT = Q + MT * 16 * DP * 2;                // [2][kWarps][16 MT] maxima, sums
+    static constexpr uint32_t TOTAL = STAT + 2 * kWarps * 16 * MT * 4;
+    static_assert(RING >= kWarps * 16 * MT * DP * 4, "the outputs fit into the rings");
+};
+
+template <int DP, int MT>
+__global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attn_mma_kernel(const __grid_constant__ AttnArgs a) {
+    using L = Lay<DP, MT>;
+    constexpr int KS = DP / 16, NT = DP / 8, ROWS = 16 * MT;
+    constexpr bool QREG = DP * MT <= 128;             // Q's fragments stay in registers
+    extern __shared__ __align__(128) uint8_t smem[];
+    const uint32_t sbase = smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+    const int units = *a.units;
+    if (units <= 0) return;
+    const AttnCut cut(a, a.start[units] * a.Hkv);
+    if (cta >= cut.ctas) return;
+    const bool vq = a.qs % 8 == 0 && reinterpret_cast<uintptr_t>(a.q) % 16 == 0;
+    const bool vo = reinterpret_cast<uintptr_t>(a.out) % 4 == 0;
+    const size_t values = (size_t)a.Hkv * a.pt * a.D * 2;
+    const float c = a.scale * 1.4426950408889634f;
+    float* stat = reinterpret_cast<float*>(smem + L::STAT);
+    const uint32_t ring = sbase + warp * L::STAGES * 2 * L::KV;
+    // what a lane reads of a tile: row and piece of its address in the four 8 x 8 blocks
+    const int krow = (lane & 7) + ((lane >> 4) << 3), kpiece = (lane >> 3) & 1;       // keys (and, transposed, nothing)
+    const int vrow = lane & 15, vpiece = lane >> 4;                                    // values, and Q
+    const int64_t end = cut.begin(cta + 1);
+    for (int64_t x = cut.begin(cta); x < end;) {
+        const AttnPiece p = attn_piece(a, units, x, end);
+        x += p.t1 - p.t0;
+        const AttnRow w = attn_row(a, p.row, false);
+        const AttnSpan s = attn_span(a, w, p.block);
+        const int64_t r0 = (int64_t)p.block * a.block, left = (int64_t)w.n * a.G - r0;
+        const int n = (int)(left < ROWS ? left : ROWS);
+        const int steps = p.t1 - p.t0, first = (s.tile0 + p.t0) * kAttnMmaKeys + warp * kGroup;
+        const int32_t* pages = a.table + (size_t)max(w.seq, 0) * a.max_pages;
+        const char* pool = static_cast<const char*>(a.pool);
+
+        // the page of this lane's key of step t (lanes 16 apart: the same); -1: none to read
+        auto look = [&](int t) {
+            const int key = first + t * kAttnMmaKeys + (lane & 15);
+            if (t >= steps || key < s.begin || key >= s.end) return -1;
+            const int page = pages[key / a.pt];
+            if (page < 0 || page >= a.pages) {
+                record_error(a.status, KDA_ERR_INVALID_ARG);
+                return -1;
+            }
+            return page;
+        };
+        auto fetch = [&](int t, int page) {
+            if (t < steps) {
+                const int key = first + t * kAttnMmaKeys + (lane & 15);
+                const int64_t at = page < 0 ? 0 : (((int64_t)page * 2 * a.Hkv + p.head) * a.pt + key % a.pt) * (a.D * 2);
+                const uint32_t to = ring + (t % L::STAGES) * 2 * L::KV;
+                constexpr int PER = DP / 8, ROUNDS = kGroup * PER / 32;        // pieces of a row; rows of 32 lanes' pieces
+#pragma unroll
+                for (int j = 0; j < ROUNDS; ++j) {
+                    const int r = (j * 32 + lane) / PER, b = (j * 32 + lane) % PER;
+                    const int64_t from = __shfl_sync(0xffffffffu, at, r);
+                    const bool ok = __shfl_sync(0xffffffffu, page, r) >= 0 && b * 8 < a.D;
+                    const char* src = pool + from + (ok ? b * 16 : 0);
+                    cp_async16(to + piece<DP>(r, b), src, ok ? 16 : 0);
+                    cp_async16(to + L::KV + piece<DP>(r, b), ok ? src + values : src, ok ? 16 : 0);
+                }
+            }
+            cp_commit();
+        };
+        __syncthreads();          // the last piece's outputs have been read
+        int page = look(0);
+#pragma unroll
+        for (int t = 0; t < L::STAGES - 1; ++t) {
+            const int next = look(t + 1);
+            fetch(t, page);
+            page = next;
+        }
+        // Q, zeros past its rows and columns
+        for (int i = tid; i < ROWS * (DP / 8); i += kThreads) {
+            const int r = i / (DP / 8), b = i % (DP / 8);
+            uint4 f = make_uint4(0, 0, 0, 0);
+            if (r < n && b * 8 < a.D) {
+                const int64_t row = r0 + r, token = w.first + row / a.G;
+                const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + token * a.qs + (int64_t)(p.head * a.G + row % a.G) * a.D + b * 8;
+                if (vq) f = *reinterpret_cast<const uint4*>(q);
+                else {
+                    const unsigned short* e = reinterpret_cast<const unsigned short*>(q);
+                    f = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16, e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
+                }
+            }
+            *reinterpret_cast<uint4*>(smem + L::Q + (r >> 4) * (16 * DP * 2) + piece<DP>(r & 15, b)) = f;
+        }
+        __syncthreads();
+        uint32_t qf[QREG ? MT * KS : 1][4];
+        if constexpr (QREG)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int k = 0; k < KS; ++k) ldmatrix4(sbase + L::Q + m * (16 * DP * 2) + piece<DP>(vrow, 2 * k + vpiece), qf[m * KS + k]);
+
+        float o[MT][NT][4], base[MT][2], sum[MT][2];
+        int pos[MT][2];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = m * 16 + h * 8 + (lane >> 2);
+                base[m][h] = -INFINITY;
+                sum[m][h] = 0.f;
+                pos[m][h] = r < n ? w.len - w.n + (int)((r0 + r) / a.G) : -1;
+            }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int k = 0; k < NT; ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[m][k][j] = 0.f;
+
+        for (int t = 0; t < steps; ++t) {
+            const int next = look(t + L::STAGES);
+            fetch(t + L::STAGES - 1, page);       // into the stage that was read a step ago (by this warp alone)
+            page = next;
+            cp_wait<L::STAGES - 1>();
+            __syncwarp();
+            const int k0 = first + t * kAttnMmaKeys;
+            if (k0 < s.end) {
+                const uint32_t keys = ring + (t % L::STAGES) * 2 * L::KV, vals = keys + L::KV;
+                float z[MT][2][4];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) z[m][j >> 2][j & 3] = 0.f;
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    uint32_t b[4];
+                    ldmatrix4(keys + piece<DP>(krow, 2 * k + kpiece), b);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        uint32_t q[4];
+                        if constexpr (!QREG) ldmatrix4(sbase + L::Q + m * (16 * DP * 2) + piece<DP>(vrow, 2 * k + vpiece), q);
+                        const uint32_t* f = QREG ? qf[m * KS + k] : q;
+                        mma16816(z[m][0], f, b[0], b[1]);
+                        mma16816(z[m][1], f, b[2], b[3]);
+                    }
+                }
+                uint32_t wgt[MT][4];
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    bool raise = false;
+                    float top[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        top[h] = -INFINITY;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int key = k0 + (j >> 1) * 8 + 2 * (lane & 3) + (j & 1);
+                            float& v = z[m][j >> 1][2 * h + (j & 1)];
+                            v = key > pos[m][h] || (a.window && key <= pos[m][h] - a.window) ? -INFINITY : v * c;
+                            top[h] = fmaxf(top[h], v);
+                        }
+                        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+                        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+                        raise |= top[h] > base[m][h] + kRaise;
+                    }
+                    if (__any_sync(0xffffffffu, raise))
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float now = top[h] > base[m][h] + kRaise ? top[h] : base[m][h];
+                            const float f = now == -INFINITY ? 1.f : ex2(base[m][h] - now);
+                            base[m][h] = now;
+                            sum[m][h] *= f;
+#pragma unroll
+                            for (int k = 0; k < NT; ++k) {
+                                o[m][k][2 * h] *= f;
+                                o[m][k][2 * h + 1] *= f;
+                            }
+                        }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float from = base[m][h] == -INFINITY ? 0.f : base[m][h];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            float *v = z[m][j] + 2 * h;
+                            v[0] = ex2(v[0] - from);
+                            v[1] = ex2(v[1] - from);
+                            sum[m][h] += v[0] + v[1];
+                            wgt[m][2 * j + h] = pack_bf16(v[0], v[1]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < NT; k += 2) {
+                    uint32_t b[4];
+                    ldmatrix4t(vals + piece<DP>(vrow, k + vpiece), b);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        mma16816(o[m][k], wgt[m], b[0], b[1]);
+                        mma16816(o[m][k + 1], wgt[m], b[2], b[3]);
+                    }
+                }
+            }
+            __syncwarp();          // all lanes have read the stage that the next step fills
+        }
+        cp_wait<0>();
+        // the warps' outputs, taken from the largest of their maxima
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                sum[m][h] += __shfl_xor_sync(0xffffffffu, sum[m][h], 1);
+                sum[m][h] += __shfl_xor_sync(0xffffffffu, sum[m][h], 2);
+                if ((lane & 3) == 0) {
+                    const int r = m * 16 + h * 8 + (lane >> 2);
+                    stat[warp * ROWS + r] = base[m][h];
+                    stat[(kWarps + warp) * ROWS + r] = sum[m][h];
+                }
+            }
+        __syncthreads();
+        float* outs = reinterpret_cast<float*>(smem);       // [kWarps][ROWS][DP]
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = m * 16 + h * 8 + (lane >> 2);
+                if (r >= n) continue;
+                float top = -INFINITY;
+#pragma unroll
+                for (int v = 0; v < kWarps; ++v) top = fmaxf(top, stat[v * ROWS + r]);
+                const float f = base[m][h] == -INFINITY ? 0.f : ex2(base[m][h] - top);
+#pragma unroll
+                for (int k = 0; k < NT; ++k)
+                    *reinterpret_cast<float2*>(outs + (warp * ROWS + r) * DP + k * 8 + 2 * (lane & 3)) =
+                        make_float2(o[m][k][2 * h] * f, o[m][k][2 * h + 1] * f);
+            }
+        __syncthreads();
+        float* part = a.part + p.slot(cta) * attn_part_floats(a);
+        for (int i = tid; i < n * (DP / 2); i += kThreads) {
+            const int r = i / (DP / 2), d = i % (DP / 2) * 2;
+            if (d >= a.D) continue;
+            float top = -INFINITY, sum_r = 0.f;
+#pragma unroll
+            for (int v = 0; v < kWarps; ++v) top = fmaxf(top, stat[v * ROWS + r]);
+            float2 y = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int v = 0; v < kWarps; ++v) {
+                const float b = stat[v * ROWS + r], f = b == -INFINITY ? 0.f : ex2(b - top);
+                sum_r = fmaf(stat[(kWarps + v) * ROWS + r], f, sum_r);
+                const float2 add = *reinterpret_cast<const float2*>(outs + (v * ROWS + r) * DP + d);
+                y.x += add.x;
+                y.y += add.y;
+            }
+            if (!p.whole()) {
+                *reinterpret_cast<float2*>(part + (size_t)r * a.D + d) = y;
+                if (d == 0) {
+                    part[(size_t)a.block * a.D + r] = top;
+                    part[(size_t)a.block * (a.D + 1) + r] = sum_r;
+                }
+                continue;
+            }
+            const float inv = sum_r > 0.f ? 1.f / sum_r : sum_r == 0.f ? 0.f : sum_r;
+            const int64_t row = r0 + r;
+            const size_t at = (w.first + row / a.G) * a.Hq + p.head * a.G + row % a.G;
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + at * a.D + d;
+            if (vo) *reinterpret_cast<uint32_t*>(out) = pack_bf16(y.x * inv, y.y * inv);
+            else {
+                out[0] = __float2bfloat16_rn(y.x * inv);
+                out[1] = __float2bfloat16_rn(y.y * inv);
+            }
+            if (a.lse && d == 0) a.lse[at] = sum_r == 0.f ? -INFINITY : (top + log2f(sum_r)) * 0.6931471805599453f;
+        }
+    }
+}
+
+template <int DP, int MT> cudaError_t go(const AttnArgs& a, cudaStream_t st) {
+    const cudaError_t e = cudaFuncSetAttribute(attn_mma_kernel<DP, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<DP, MT>::TOTAL);
+    if (e != cudaSuccess) return e;
+    attn_mma_kernel<DP, MT><<<a.ctas, kThreads, Lay<DP, MT>::TOTAL, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_mma(const AttnArgs& a, cudaStream_t st) {
+    if (a.D > 128) return go<256, 1>(a, st);
+    if (a.D > 64) return a.block == 16 ? go<128, 1>(a, st) : go<128, 2>(a, st);
+    return a.block == 16 ? go<64, 1>(a, st) : go<64, 2>(a, st);
+}
+
+}  // namespace kda
