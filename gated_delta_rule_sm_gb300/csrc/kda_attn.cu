@@ -176,46 +176,93 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
 
 // ------------------------------------------------------------------ join
 
-// A CTA takes one item (a unit for one key head); most items have one part and are done already.
-constexpr int kJoinThreads = 256;
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnArgs a) {
+// A CTA takes kJoinRows rows of one item (a unit for one key head); most items have one part and are done already.  With few
+// parts a warp takes a row; with many (a few rows over a long cache) the warps split the parts of a row, four of each
+// warp's on the way at once, since then it is their latency that counts.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinFew = 4;
+struct JoinSum {
+    float o[8], sum;
+};
+// Parts c0 + at, c0 + at + step, ... of row i, weighted from `base`.
+__device__ __forceinline__ JoinSum join_parts(const AttnArgs& a, int c0, int c1, int at, int step, int i, float base) {
+    const int lane = threadIdx.x & 31;
+    const size_t size = attn_part_floats(a), top = (size_t)a.block * a.D + i;
+    JoinSum s;
+    s.sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s.o[k] = 0.f;
+    constexpr int AHEAD = 4;
+    for (int c = c0 + at; c <= c1; c += AHEAD * step) {
+        float f[AHEAD], add[AHEAD], v[AHEAD][8];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            const int now = c + j * step;
+            const float* p = a.part + (size_t)(2 * now + (now == c0)) * size;
+            f[j] = now <= c1 ? p[top] : -INFINITY;
+            add[j] = now <= c1 ? p[top + a.block] : 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[j][k] = now <= c1 && k * 32 + lane < a.D ? p[(size_t)i * a.D + k * 32 + lane] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            const float w = f[j] == -INFINITY ? 0.f : exp2f(f[j] - base);
+            s.sum = fmaf(w, add[j], s.sum);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s.o[k] = fmaf(w, v[j][k], s.o[k]);
+        }
+    }
+    return s;
+}
+__device__ __forceinline__ void join_write(const AttnArgs& a, size_t at, const JoinSum& s, float base) {
+    const int lane = threadIdx.x & 31;
+    const float inv = s.sum > 0.f ? 1.f / s.sum : s.sum == 0.f ? 0.f : s.sum;      // (NaN stays)
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (k * 32 + lane < a.D) store_act(a.out, at * a.D + k * 32 + lane, s.o[k] * inv, a.dtype);
+    if (a.lse && lane == 0) a.lse[at] = s.sum == 0.f ? -INFINITY : (base + log2f(s.sum)) * 0.6931471805599453f;
+}
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnArgs a, int rows_each) {
+    __shared__ float so[kJoinWarps][256], ss[kJoinWarps];
     const int units = *a.units, u = blockIdx.x / a.Hkv, head = blockIdx.x - u * a.Hkv;
     if (u >= units) return;
-    const int64_t first = a.start[u];
+    const int64_t first = a.start[u], total = a.start[units] * a.Hkv;
     const int tiles = (int)(a.start[u + 1] - first);
-    const AttnCut cut(a, a.start[units] * a.Hkv);
+    const AttnCut cut(a, total);
     const int64_t x = first * a.Hkv + (int64_t)head * tiles;
     const int c0 = cut.owner(x), c1 = cut.owner(x + tiles - 1);
     if (c0 == c1) return;
     const AttnRow w = attn_row(a, a.unit_row[u], false);
     const int64_t r0 = (int64_t)a.unit_row[a.units_most + u] * a.block, left = (int64_t)w.n * a.G - r0;
     const int n = (int)(left < a.block ? left : a.block), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const size_t size = attn_part_floats(a);
-    auto part = [&](int c) { return a.part + (size_t)(2 * c + (c == c0)) * size; };
-    for (int i = warp; i < n; i += kJoinThreads / 32) {
+    const int i0 = blockIdx.y * rows_each, i1 = min(n, i0 + rows_each);
+    const bool few = c1 - c0 < kJoinFew;
+    for (int i = few ? i0 + warp : i0; i < i1; i += few ? kJoinWarps : 1) {
         float top = -INFINITY;
-        for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, part(c)[(size_t)a.block * a.D + i]);
+        for (int c = c0 + lane; c <= c1; c += 32)
+            top = fmaxf(top, a.part[(size_t)(2 * c + (c == c0)) * attn_part_floats(a) + (size_t)a.block * a.D + i]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         const float base = top == -INFINITY ? 0.f : top;
-        float sum = 0.f, o[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] = 0.f;
-        for (int c = c0; c <= c1; ++c) {
-            const float* p = part(c);
-            const float f = exp2f(p[(size_t)a.block * a.D + i] - base);
-            sum = fmaf(f, p[(size_t)a.block * (a.D + 1) + i], sum);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (k * 32 + lane < a.D) o[k] = fmaf(f, p[(size_t)i * a.D + k * 32 + lane], o[k]);
-        }
-        const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;      // (NaN stays)
         const int64_t row = r0 + i;
-        const size_t token = w.first + row / a.G, at = token * a.Hq + head * a.G + row % a.G;
+        const size_t at = (w.first + row / a.G) * a.Hq + head * a.G + row % a.G;
+        JoinSum s = join_parts(a, c0, c1, few ? 0 : warp, few ? 1 : kJoinWarps, i, base);
+        if (few) {
+            join_write(a, at, s, base);
+            continue;
+        }
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (k * 32 + lane < a.D) store_act(a.out, at * a.D + k * 32 + lane, o[k] * inv, a.dtype);
-        if (a.lse && lane == 0) a.lse[at] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * 0.6931471805599453f;
+        for (int k = 0; k < 8; ++k) so[warp][k * 32 + lane] = s.o[k];
+        if (lane == 0) ss[warp] = s.sum;
+        __syncthreads();
+        if (warp == 0) {
+            for (int v = 1; v < kJoinWarps; ++v) {
+                s.sum += ss[v];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) s.o[k] += so[v][k * 32 + lane];
+            }
+            join_write(a, at, s, base);
+        }
+        __syncthreads();
     }
 }
 
@@ -586,7 +633,10 @@ kda_status kda_pages_attention(const kda_attention_dims* dims, const void* q, co
     timing_post(stream);
     if (e != cudaSuccess) return KDA_ERR_CUDA;
     timing_pre(stream, K_ATTN_JOIN);
-    attn_join_kernel<<<a.units_most * a.Hkv, kJoinThreads, 0, stream>>>(a);
+    // rows of an item that may exist; a CTA for each where they are few
+    const int64_t longest = cu_seqlens ? (int64_t)a.tokens * a.G : (int64_t)a.per_row * a.G, rows = longest < a.block ? longest : a.block;
+    const int each = a.block <= 32 ? 1 : 2 * kJoinWarps;
+    attn_join_kernel<<<dim3(a.units_most * a.Hkv, (int)((rows + each - 1) / each)), kJoinThreads, 0, stream>>>(a, each);
     timing_post(stream);
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
