@@ -302,23 +302,21 @@ __global__ void __launch_bounds__(kSimtThreads, DC > 2 ? 1 : 2) attn_simt_kernel
     float* sv = sk + (size_t)D4 * kSimtPad;          // [kSimtKeys][64 DC] values
     float* sp = sv + kSimtKeys * 64 * DC;            // [kSimtKeys][kSimtPad] weights by key
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, warp = tid >> 5;
-    const int units = *a.units;
-    if (units <= 0) return;
-    const AttnCut cut(a, a.start[units] * a.Hkv);
+    __shared__ int64_t own[kAttnDirectRows + 1];
+    const AttnUnits units = attn_units(a, own);
+    if (units.units <= 0) return;
+    const AttnCut cut(a, units.tiles(a));
     const int cta = blockIdx.x;
     if (cta >= cut.ctas) return;
     const bool vq = a.D % 4 == 0 && a.qs % 4 == 0 && reinterpret_cast<uintptr_t>(a.q) % (4 * sizeof(E)) == 0;
     const bool vk = a.D % 4 == 0 && reinterpret_cast<uintptr_t>(a.pool) % (4 * sizeof(E)) == 0;
     const size_t values = (size_t)a.Hkv * a.pt * a.D * sizeof(E);      // from a page's keys to its values
     const float c = a.scale * 1.4426950408889634f;
-    const int64_t end = cut.begin(cta + 1);
-    for (int64_t x = cut.begin(cta); x < end;) {
-        const AttnPiece p = attn_piece(a, units, x, end);
-        x += p.t1 - p.t0;
-        const AttnRow w = attn_row(a, p.row, false);
-        const AttnSpan s = attn_span(a, w, p.block);
-        const int64_t r0 = (int64_t)p.block * a.block, left = (int64_t)w.n * a.G - r0;
-        const int n = (int)(left < a.block ? left : a.block);
+    for (AttnWalk p(a, units, cut, cta); p.more(); p.next(a, units)) {
+        const AttnRow w = p.w;
+        const AttnSpan s = p.s;
+        const int64_t r0 = p.first_row(a);
+        const int n = p.rows(a);
         __syncthreads();
         for (int i = tid; i < kSimtRows * (D4 / 4); i += kSimtThreads) {
             const int r = i % kSimtRows, d = i / kSimtRows * 4;
@@ -468,7 +466,7 @@ template <typename E, int DC> cudaError_t simt_launch(const AttnArgs& a, cudaStr
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
     if (dev < 0 || dev >= 64 || !set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<E, DC>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        const cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<E, DC>, cudaFuncAttributeMaxDynamicSharedMemorySize, 222 * 1024);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) set[dev] = true;
     }
@@ -532,13 +530,17 @@ size_t attn_layout(char* ws, AttnArgs* a) {
 // Which kernel a call takes, and its cut.  aligned: the pool's base allows 16-byte copies.
 void attn_choose(AttnArgs* a, bool aligned) {
     const int64_t packed = (int64_t)a->tokens * a->G;
-    if (a->dtype == KDA_BF16 && a->D % 8 == 0 && aligned) {
+    if (a->dtype == KDA_BF16 && a->D % 8 == 0 && aligned && a->D <= 128 && packed > 32 * (int64_t)a->rows) {
+        a->kernel = kAttnTc;
+        attn_cut(a, kAttnTcRows, kAttnTcKeys, 152);
+    } else if (a->dtype == KDA_BF16 && a->D % 8 == 0 && aligned) {
         a->kernel = kAttnMma;
         attn_cut(a, a->D > 128 || packed <= 16 * (int64_t)a->rows ? 16 : 32, kAttnMmaKeys, a->D > 128 ? 152 : 304);
     } else {
         a->kernel = kAttnSimt;
         attn_cut(a, kSimtRows, kSimtKeys, a->D > 128 ? 152 : 304);
     }
+    a->direct = a->per_row && (int64_t)a->per_row * a->G <= a->block && a->rows <= kAttnDirectRows;
 }
 
 }  // namespace
@@ -624,12 +626,14 @@ kda_status kda_pages_attention(const kda_attention_dims* dims, const void* q, co
     if ((int64_t)a.units_most * a.Hkv > (1LL << 30)) return KDA_ERR_UNSUPPORTED;
     st = status_ptr(&a.status);
     if (st != KDA_OK) return st;
-    timing_pre(stream, K_ATTN_PLAN);
-    attn_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
-    timing_post(stream);
-    if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+    if (!a.direct) {
+        timing_pre(stream, K_ATTN_PLAN);
+        attn_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
+        timing_post(stream);
+        if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+    }
     timing_pre(stream, K_ATTN);
-    const cudaError_t e = a.kernel == kAttnMma ? launch_attn_mma(a, stream) : launch_attn_simt(a, stream);
+    const cudaError_t e = a.kernel == kAttnTc ? launch_attn_tc(a, stream) : a.kernel == kAttnMma ? launch_attn_mma(a, stream) : launch_attn_simt(a, stream);
     timing_post(stream);
     if (e != cudaSuccess) return KDA_ERR_CUDA;
     timing_pre(stream, K_ATTN_JOIN);

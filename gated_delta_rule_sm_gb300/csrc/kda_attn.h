@@ -12,7 +12,7 @@
 
 namespace kda {
 
-enum AttnKernel { kAttnSimt, kAttnMma };
+enum AttnKernel { kAttnSimt, kAttnMma, kAttnTc };
 
 struct AttnArgs {
     int rows, tokens, per_row;           // per_row: tokens of a row without cu
@@ -20,7 +20,7 @@ struct AttnArgs {
     int pages, pt, table_rows, max_pages, window;
     int64_t qs;                          // elements between tokens of q
     float scale;
-    int kernel;                          // AttnKernel
+    int kernel, direct;                  // AttnKernel; every row one unit
     const void *q, *pool;
     const int32_t *table, *lengths, *seqs, *cu;
     void* out;
@@ -87,35 +87,106 @@ struct AttnCut {
     __device__ __forceinline__ int owner(int64_t x) const { return (int)(((x + 1) * ctas + total - 1) / total) - 1; }   // begin(owner) <= x
 };
 
-// The unit that holds tile x of all key heads' tiles.
-__device__ __forceinline__ int attn_unit(const AttnArgs& a, int units, int64_t x) {
-    int lo = 0, hi = units - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.start[mid] * a.Hkv <= x) lo = mid; else hi = mid - 1;
+// The units of a call: read from the plan's arrays, or, where every row is one unit and the rows are few (direct), counted by
+// every CTA for itself, which saves the plan's launch.
+constexpr int kAttnDirectRows = 512;
+struct AttnUnits {
+    int units;
+    const int64_t* start;
+    __device__ __forceinline__ int64_t tiles(const AttnArgs& a) const { return start[units] * a.Hkv; }
+};
+// All threads of a CTA; own: [kAttnDirectRows + 1] in shared memory.  The first CTA leaves what it counted to the join.
+__device__ __forceinline__ AttnUnits attn_units(const AttnArgs& a, int64_t* own) {
+    AttnUnits s;
+    if (!a.direct) {
+        s.units = *a.units;
+        s.start = a.start;
+        return s;
     }
-    return lo;
+    for (int r = threadIdx.x; r < a.rows; r += blockDim.x) own[r + 1] = attn_span(a, attn_row(a, r, blockIdx.x == 0), 0).tiles;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int64_t before = 0;
+        for (int r0 = 0; r0 < a.rows; r0 += 32) {
+            int64_t x = r0 + lane < a.rows ? own[r0 + lane + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t up = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += up;
+            }
+            x += before;
+            if (r0 + lane < a.rows) own[r0 + lane + 1] = x;
+            before = __shfl_sync(0xffffffffu, x, 31);
+        }
+        if (lane == 0) own[0] = 0;
+    }
+    __syncthreads();
+    if (blockIdx.x == 0) {
+        for (int r = threadIdx.x; r <= a.rows; r += blockDim.x) {
+            a.start[r] = own[r];
+            if (r < a.rows) {
+                a.unit_row[r] = r;
+                a.unit_row[a.units_most + r] = 0;
+            }
+        }
+        if (threadIdx.x == 0) *a.units = a.rows;
+    }
+    s.units = a.rows;
+    s.start = own;
+    return s;
 }
 
-// One CTA's part of one item: tiles [t0, t1) of its `tiles`.
-struct AttnPiece {
-    int row, block, head, t0, t1, tiles;
+// The pieces of a CTA's span, one after the other: tiles [t0, t1) of an item's `tiles`.
+struct AttnWalk {
+    int u, head, t0, t1, tiles, row, block;
+    int64_t x, end;
+    AttnRow w;
+    AttnSpan s;
+    __device__ __forceinline__ AttnWalk(const AttnArgs& a, const AttnUnits& n, const AttnCut& cut, int cta) {
+        x = cut.begin(cta);
+        end = cut.begin(cta + 1);
+        int lo = 0, hi = n.units - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (n.start[mid] * a.Hkv <= x) lo = mid; else hi = mid - 1;
+        }
+        u = lo;
+        unit(a, n);
+        const int64_t off = x - n.start[u] * a.Hkv;
+        head = (int)(off / tiles);
+        t0 = (int)(off - (int64_t)head * tiles);
+        cut_off();
+    }
+    __device__ __forceinline__ void unit(const AttnArgs& a, const AttnUnits& n) {
+        row = a.direct ? u : a.unit_row[u];
+        block = a.direct ? 0 : a.unit_row[a.units_most + u];
+        w = attn_row(a, row, false);
+        s = attn_span(a, w, block);
+        tiles = (int)(n.start[u + 1] - n.start[u]);
+    }
+    __device__ __forceinline__ void cut_off() { t1 = (int)(end - x < tiles - t0 ? t0 + (end - x) : tiles); }
+    __device__ __forceinline__ bool more() const { return x < end; }
+    __device__ __forceinline__ void next(const AttnArgs& a, const AttnUnits& n) {
+        x += t1 - t0;
+        if (x >= end) return;
+        t0 = 0;
+        if (++head == a.Hkv) {
+            head = 0;
+            ++u;
+            unit(a, n);
+        }
+        cut_off();
+    }
     __device__ __forceinline__ bool whole() const { return t1 - t0 == tiles; }
     // where its sums go: a CTA shares at most the item it starts inside of and the one it does not finish
     __device__ __forceinline__ int slot(int cta) const { return 2 * cta + (t0 == 0); }
+    __device__ __forceinline__ int64_t first_row(const AttnArgs& a) const { return (int64_t)block * a.block; }
+    __device__ __forceinline__ int rows(const AttnArgs& a) const {
+        const int64_t left = (int64_t)w.n * a.G - first_row(a);
+        return (int)(left < a.block ? left : a.block);
+    }
 };
-__device__ __forceinline__ AttnPiece attn_piece(const AttnArgs& a, int units, int64_t x, int64_t end) {
-    AttnPiece p;
-    const int u = attn_unit(a, units, x);
-    const int64_t first = a.start[u], off = x - first * a.Hkv;
-    p.tiles = (int)(a.start[u + 1] - first);
-    p.row = a.unit_row[u];
-    p.block = a.unit_row[a.units_most + u];
-    p.head = (int)(off / p.tiles);
-    p.t0 = (int)(off - (int64_t)p.head * p.tiles);
-    p.t1 = (int)(end - x < p.tiles - p.t0 ? p.t0 + (end - x) : p.tiles);
-    return p;
-}
 
 __device__ __forceinline__ size_t attn_part_floats(const AttnArgs& a) { return (size_t)a.block * (a.D + 2); }
 
@@ -133,6 +204,9 @@ __device__ __forceinline__ const char* attn_page(const AttnArgs& a, int seq, int
 // The kernels.  mma: bf16, D a multiple of 8, 16-byte aligned pool; blocks of 16 or 32 packed rows (16 with D above 128).
 constexpr int kAttnMmaKeys = 64;
 cudaError_t launch_attn_mma(const AttnArgs& a, cudaStream_t st);
+// tc: bf16, D a multiple of 8 up to 128, 16-byte aligned pool; two tiles of 128 packed rows against tiles of 128 keys.
+constexpr int kAttnTcRows = 256, kAttnTcKeys = 128;
+cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t st);
 cudaError_t launch_attn_simt(const AttnArgs& a, cudaStream_t st);
 
 }  // namespace kda

@@ -75,9 +75,10 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attn_mma_kernel(c
     extern __shared__ __align__(128) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
-    const int units = *a.units;
-    if (units <= 0) return;
-    const AttnCut cut(a, a.start[units] * a.Hkv);
+    __shared__ int64_t own[kAttnDirectRows + 1];
+    const AttnUnits units = attn_units(a, own);
+    if (units.units <= 0) return;
+    const AttnCut cut(a, units.tiles(a));
     if (cta >= cut.ctas) return;
     const bool vq = a.qs % 8 == 0 && reinterpret_cast<uintptr_t>(a.q) % 16 == 0;
     const bool vo = reinterpret_cast<uintptr_t>(a.out) % 4 == 0;
@@ -88,14 +89,11 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attn_mma_kernel(c
     // what a lane reads of a tile: row and piece of its address in the four 8 x 8 blocks
     const int krow = (lane & 7) + ((lane >> 4) << 3), kpiece = (lane >> 3) & 1;       // keys (and, transposed, nothing)
     const int vrow = lane & 15, vpiece = lane >> 4;                                    // values, and Q
-    const int64_t end = cut.begin(cta + 1);
-    for (int64_t x = cut.begin(cta); x < end;) {
-        const AttnPiece p = attn_piece(a, units, x, end);
-        x += p.t1 - p.t0;
-        const AttnRow w = attn_row(a, p.row, false);
-        const AttnSpan s = attn_span(a, w, p.block);
-        const int64_t r0 = (int64_t)p.block * a.block, left = (int64_t)w.n * a.G - r0;
-        const int n = (int)(left < ROWS ? left : ROWS);
+    for (AttnWalk p(a, units, cut, cta); p.more(); p.next(a, units)) {
+        const AttnRow w = p.w;
+        const AttnSpan s = p.s;
+        const int64_t r0 = p.first_row(a);
+        const int n = p.rows(a);
         const int steps = p.t1 - p.t0, first = (s.tile0 + p.t0) * kAttnMmaKeys + warp * kGroup;
         const int32_t* pages = a.table + (size_t)max(w.seq, 0) * a.max_pages;
         const char* pool = static_cast<const char*>(a.pool);

@@ -1,0 +1,460 @@
+// kda_attn_tc.cu -- attention of chunks of new tokens over paged keys and values on the tensor cores (tcgen05, TMEM): bf16,
+// D <= 128.
+//
+// A CTA takes 256 packed query rows as two tiles of 128 and walks the key tiles of its piece, 128 keys each:
+//     S = Q K^T  (fp32, TMEM),   P = 2^(c S - c m) in bf16 over S's columns,   O += P V  (fp32, TMEM)
+// One thread owns one query row: its 128 scores come out of TMEM at once, so that maximum and sum need no exchange.
+// The maximum m that scores are taken from is raised only when it is passed by more than 8 in log2; then, a few times in
+// a row's life, the row's output is rescaled in TMEM, between the products that add to it.
+//
+// Operands: K and V lie in one ring of four 32 KB slots (K, V, K, V, ...), rows of 128 bytes in the 128-byte swizzle, where two
+// warps' cp.async puts them: a page may be of any size, end inside a tile or be missing, and what is past the sequence's end is
+// filled with zeros (its values meet zero weights).  K is read K-major, V MN-major (keys as K), P from TMEM.
+//
+// Roles (12 warps): 0-3 and 4-7 the softmax of the two tiles, 8 and 9 issue the products of one tile each, 10 and 11
+// copy.  The tiles go their own ways: S -> softmax -> P V -> next S each, so that one's products run while the other's
+// exponentials do.  P of a tile lies where its next S goes, hence the next S is issued when P V is complete.
+// Registers: a softmax thread holds 128 scores, the others little: 208 and 88 (256 x 208 + 128 x 88 = 384 x 168).
+// TMEM columns: S (and P) 2 x 128, O 2 x 128.
+// Bound: per pair of tiles and 128 keys 16.8 MFLOP, 2050 cycles of the tensor core at its dense rate, beside 32768 exponentials,
+// 1024 cycles of the special function units, and 128 KB of operands and 64 KB of copies through shared memory.
+#include <math.h>
+
+#include <type_traits>
+
+#include "kda.h"
+#include "kda_attn.h"
+#include "kda_common.cuh"
+#include "kda_sm100.cuh"
+
+namespace kda {
+
+using namespace sm100;
+
+namespace {
+
+constexpr int kThreads = 384, KT = kAttnTcKeys;
+constexpr float kRaise = 8.f;
+constexpr uint32_t HALF = 16384;       // 128 rows of 128 bytes (64 bf16 columns)
+
+// Shared memory: NB halves of 64 columns of D.
+template <int NB> struct Lay {
+    static constexpr uint32_t TILE = NB * HALF;
+    static constexpr int SLOTS = 4;
+    static constexpr uint32_t Q = 0;                          // two tiles
+    static constexpr uint32_t KV = 2 * TILE;                  // the ring
+    static constexpr uint32_t BAR = KV + SLOTS * TILE;
+    static constexpr uint32_t TOTAL = BAR + 256;
+};
+
+enum Bars {
+    kFull = 0,       // [4] a slot's copies landed (2 warps)
+    kEmpty = 4,      // [4] its products complete, of both tiles
+    kQFull = 8,      // Q landed (2 warps)
+    kQEmpty = 9,     // the piece's products with Q complete, of both tiles
+    kS = 10,         // [2] S complete
+    kP = 12,         // [2] P written, O rescaled (4 warps)
+    kO = 14,         // [2] P V complete
+    kOFree = 16,     // [2] the piece's O read (4 warps)
+    kBars = 18
+};
+
+constexpr uint32_t TS = 0, TO = 256, TCOLS = 512;       // + 128 tile
+
+// (as in the state space scan: low descriptor words with the offsets added beside their use, 128-byte swizzle)
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | (lbo >> 4 << 16); }
+constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
+template <int OA, int OB>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 da, db;\n\tadd.u32 x, %1, %5;\n\tadd.u32 y, %2, %6;\n\t"
+        "mov.b64 da, {x, %7};\n\tmov.b64 db, {y, %7};\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(OA >> 4), "n"(OB >> 4), "r"(kDescHi));
+}
+template <int OB>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b32 y;\n\t.reg .b64 db;\n\tadd.u32 y, %2, %5;\n\tmov.b64 db, {y, %6};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(OB >> 4), "r"(kDescHi));
+}
+template <int N, typename F, int I = 0>
+__device__ __forceinline__ void steps(F&& f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>());
+        steps<N, F, I + 1>(static_cast<F&&>(f));
+    }
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return fma2(a, dup(1.f), b); }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Byte of 16-byte piece c (of NB x 8) of row r in a tile.
+__device__ __forceinline__ uint32_t piece(int r, int c) { return (c >> 3) * HALF + (uint32_t)(r * 128 + (((c & 7) ^ (r & 7)) << 4)); }
+
+// Values that a load from TMEM has left are used after its wait: the wait alone names no register.
+template <int N> __device__ __forceinline__ void landed(float* v) {
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < N; ++j) asm volatile("" : "+f"(v[j]));
+}
+
+template <int NB>
+__global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnArgs a) {
+    using L = Lay<NB>;
+    constexpr int DP = 64 * NB;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ int64_t own[kAttnDirectRows + 1];
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::BAR);
+    volatile int* fail = reinterpret_cast<volatile int*>(smem + L::BAR + 8 * kBars);
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::BAR + 8 * kBars + 4);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+    const AttnUnits units = attn_units(a, own);
+    if (units.units <= 0) return;
+    const AttnCut cut(a, units.tiles(a));
+    if (cta >= cut.ctas) return;
+    if (tid == 0) {
+        for (int i = 0; i < kBars; ++i) mbar_init(&bar[i], i >= kP && i < kO || i >= kOFree ? 4 : i >= kS ? 1 : 2);
+        *fail = 0;
+        mbar_fence_init();
+    }
+    if (warp == 0) tmem_alloc(tslot, TCOLS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+
+    // Bounded waits: false, and the CTA marked as failed, after about a second; the role then leaves its loops, and those that
+    // wait for it give up in turn.
+    constexpr uint32_t kTries = 1u << 17;
+    auto wait1 = [&](int b, uint32_t parity) {
+        if (mbar_test_wait(&bar[b], parity)) return true;
+#pragma unroll 1
+        for (uint32_t i = 0; i < kTries; ++i)
+            if (mbar_try_wait_ns(&bar[b], parity, 10000)) return true;
+        *fail = 1;
+        return false;
+    };
+    auto wait = [&](int b, uint32_t parity) {      // one answer for the whole warp
+        if (__all_sync(0xffffffffu, mbar_test_wait(&bar[b], parity))) return true;
+#pragma unroll 1
+        for (uint32_t i = 0; i < kTries; ++i)
+            if (__all_sync(0xffffffffu, mbar_try_wait_ns(&bar[b], parity, 10000))) return true;
+        *fail = 1;
+        return false;
+    };
+    auto arrive_warp = [&](int b) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[b]);
+    };
+
+    // Phases: every wait names the use of its barrier that it waits for (the n-th completes parity n & 1), and nobody is two uses
+    // behind or ahead: a slot's next use waits for both tiles' products with it, S and P of a tile alternate, O's last phase of
+    // a piece is followed by another only after its readers gave O free.
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        // ---------------------------------------------------------------- softmax
+        const int tile = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, ts = tmem + TS + 128 * tile + lanes, to = tmem + TO + 128 * tile + lanes;
+        // the scale in log2 units, its sign apart; a scale of 0 leaves every score that is not masked at 0
+        const bool negative = a.scale < 0.f;
+        const float c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
+        uint32_t n = 0;                              // key tiles so far
+        for (AttnWalk p(a, units, cut, cta); p.more(); p.next(a, units)) {
+            const int rows = p.rows(a) - 128 * tile;
+            if (rows <= 0) continue;                 // (the other roles leave this tile out as well)
+            const int64_t packed = p.first_row(a) + 128 * tile + row;
+            const int pos = row < rows ? p.w.len - p.w.n + (int)(packed / a.G) : -1;
+            // positions of the warp's rows, for tiles that need no mask
+            const int low = __reduce_min_sync(0xffffffffu, pos), high = __reduce_max_sync(0xffffffffu, pos);
+            float base = -INFINITY;                  // what scores are taken from (a score, not yet times c)
+            float2 sum = make_float2(0.f, 0.f);
+            bool ok = true;
+            for (int t = p.t0; t < p.t1; ++t, ++n) {
+                const int k0 = (p.s.tile0 + t) * KT;
+                if (!wait(kS + tile, n & 1)) { ok = false; break; }
+                tc_fence_after();
+                float v[KT];
+#pragma unroll
+                for (int j = 0; j < KT; j += 16) tmem_ld16(ts + j, v + j);
+                landed<KT>(v);
+                if (negative)
+#pragma unroll
+                    for (int j = 0; j < KT; ++j) v[j] = -v[j];
+                if (k0 + KT - 1 > low || (a.window && k0 <= high - a.window)) {
+                    const int last = pos - k0, first = a.window ? last - a.window : -1;      // keys first < j <= last
+#pragma unroll
+                    for (int j = 0; j < KT; ++j)
+                        if (j > last || j <= first) v[j] = -INFINITY;
+                }
+                float m[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) m[j] = fmaxf(v[j], v[j + 4]);
+#pragma unroll
+                for (int j = 8; j < KT; j += 4)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) m[i] = fmaxf(m[i], v[j + i]);
+                const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+                const bool raise = top * c > base * c + kRaise;
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float now = raise ? top : base, f = now == -INFINITY ? 1.f : ex2((base - now) * c);
+                    base = now;
+                    sum = mul2(sum, dup(f));
+                    if (t > p.t0) {
+                        // (S of this tile came after P V of the last one: O is at rest)
+#pragma unroll 1
+                        for (int j = 0; j < DP; j += 16) {
+                            float o[16];
+                            tmem_ld16(to + j, o);
+                            landed<16>(o);
+                            uint32_t w[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * f);
+                            tmem_st16(to + j, w);
+                        }
+                    }
+                }
+                const float from = base == -INFINITY ? 0.f : -base * c;
+#pragma unroll
+                for (int j = 0; j < KT; j += 32) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float2 z = fma2(make_float2(v[j + 2 * i], v[j + 2 * i + 1]), dup(c), dup(from));
+                        z.x = ex2(z.x);
+                        z.y = ex2(z.y);
+                        sum = add2(sum, z);
+                        w[i] = pack_bf16(z.x, z.y);
+                    }
+                    tmem_st16(ts + j / 2, w);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                arrive_warp(kP + tile);
+            }
+            if (!ok || !wait(kO + tile, (n - 1) & 1)) break;
+            tc_fence_after();
+            const float l = sum.x + sum.y;
+            const bool whole = p.whole(), live = row < rows;
+            const int64_t token = p.w.first + packed / a.G;
+            const size_t at = (size_t)token * a.Hq + p.head * a.G + packed % a.G;
+            const float inv = whole ? l > 0.f ? 1.f / l : l == 0.f ? 0.f : l : 1.f;
+            float* part = a.part + p.slot(cta) * attn_part_floats(a);
+            const int prow = 128 * tile + row;
+            const bool vec = reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
+#pragma unroll 1
+            for (int j = 0; j < DP; j += 16) {
+                float o[16];
+                tmem_ld16(to + j, o);
+                landed<16>(o);
+                if (!live) continue;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] *= inv;
+#pragma unroll
+                for (int i = 0; i < 16; i += 8) {
+                    if (j + i >= a.D) continue;
+                    if (whole) {
+                        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.out) + at * a.D + j + i;
+                        if (vec) *reinterpret_cast<uint4*>(y) = pack8_bf16(o + i);
+                        else
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) y[e] = __float2bfloat16_rn(o[i + e]);
+                    } else {
+                        float4* y = reinterpret_cast<float4*>(part + (size_t)prow * a.D + j + i);
+                        y[0] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        y[1] = make_float4(o[i + 4], o[i + 5], o[i + 6], o[i + 7]);
+                    }
+                }
+            }
+            tc_fence_before();
+            arrive_warp(kOFree + tile);
+            if (live) {
+                const float at_log2 = base == -INFINITY ? -INFINITY : base * c;
+                if (!whole) {
+                    part[(size_t)a.block * a.D + prow] = at_log2;
+                    part[(size_t)a.block * (a.D + 1) + prow] = l;
+                } else if (a.lse) {
+                    a.lse[at] = l == 0.f ? -INFINITY : (at_log2 + log2f(l)) * 0.6931471805599453f;
+                }
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp < 10) {
+            // ------------------------------------------------------------ products of a tile
+            const int tile = warp - 8;
+            if (lane == 0) {
+                constexpr uint32_t idS = idesc_bf16(128, KT, 0, 0), idO = idesc_bf16(128, DP, 0, 1);
+                const uint32_t sq = desc_lo(smem_u32(smem + L::Q + tile * L::TILE), 16), ts = tmem + TS + 128 * tile, to = tmem + TO + 128 * tile;
+                uint32_t n = 0, g = 0, pieces = 0, mine = 0;     // this tile's and all key tiles, pieces, and those with this tile
+                bool ok = true;
+                for (AttnWalk p(a, units, cut, cta); ok && p.more(); p.next(a, units), ++pieces) {
+                    const bool live = p.rows(a) > 128 * tile;
+                    ok = wait1(kQFull, pieces & 1);
+                    for (int t = p.t0; ok && t < p.t1; ++t, ++g) {
+                        const int ks = (2 * g) % L::SLOTS, vs = ks + 1;
+                        const uint32_t use = (2 * g) / L::SLOTS & 1;
+                        if (!live) {                            // slots wait for both tiles
+                            ok = wait1(kFull + ks, use);
+                            if (!ok) break;
+                            mbar_arrive(&bar[kEmpty + ks]);
+                            ok = wait1(kFull + vs, use);
+                            if (!ok) break;
+                            mbar_arrive(&bar[kEmpty + vs]);
+                            continue;
+                        }
+                        ok = wait1(kFull + ks, use) && (t == p.t0 || wait1(kO + tile, (n - 1) & 1));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t sk = desc_lo(smem_u32(smem + L::KV + ks * L::TILE), 16);
+                        steps<4 * NB>([&](auto k) {
+                            constexpr int o = (k >> 2) * HALF + (k & 3) * 32;
+                            mma_ss<o, o>(ts, sq, sk, idS, k > 0);
+                        });
+                        mma_commit(&bar[kS + tile]);
+                        mma_commit(&bar[kEmpty + ks]);
+                        ok = wait1(kFull + vs, use) && wait1(kP + tile, n & 1) && (t > p.t0 || mine == 0 || wait1(kOFree + tile, (mine - 1) & 1));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t sv = desc_lo(smem_u32(smem + L::KV + vs * L::TILE), HALF);
+                        steps<KT / 16>([&](auto k) { mma_ts<k * 2048>(to, ts + 8 * k, sv, idO, t > p.t0 || k > 0); });
+                        mma_commit(&bar[kEmpty + vs]);
+                        mma_commit(&bar[kO + tile]);
+                        ++n;
+                    }
+                    if (!ok) break;
+                    if (live) {
+                        ++mine;
+                        mma_commit(&bar[kQEmpty]);
+                    } else {
+                        mbar_arrive(&bar[kQEmpty]);
+                    }
+                }
+            }
+            __syncwarp();
+        } else {
+            // ------------------------------------------------------------ copies: half of a tile's keys a warp
+            const int half = warp - 10;
+            constexpr int PER = DP / 8, EACH = 32 / PER, ROUNDS = 64 / EACH;      // pieces of a row, rows of one round of the lanes, rounds
+            const int c = lane % PER, sub = lane / PER;
+            const bool column = c * 8 < a.D, vq = a.qs % 8 == 0 && reinterpret_cast<uintptr_t>(a.q) % 16 == 0;
+            const size_t values = (size_t)a.Hkv * a.pt * a.D * 2;
+            const char* pool = static_cast<const char*>(a.pool);
+            uint32_t g = 0, pieces = 0, told = 0;        // slots filled; of them announced
+            bool ok = true;
+            auto tell = [&]() {
+                fence_async_smem();
+                arrive_warp(kFull + told % L::SLOTS);
+                ++told;
+            };
+            for (AttnWalk p(a, units, cut, cta); ok && p.more(); p.next(a, units), ++pieces) {
+                if (pieces && !wait(kQEmpty, (pieces - 1) & 1)) break;
+                const int64_t r0 = p.first_row(a);
+                const int rows = p.rows(a);
+#pragma unroll 1
+                for (int i = 0; i < 256 / EACH; i += 2) {
+                    const int r = (i + half) * EACH + sub;
+                    const uint32_t to = smem_u32(smem + L::Q + (r >> 7) * L::TILE) + piece(r & 127, c);
+                    const bool in = r < rows && column;
+                    const int64_t row = in ? r0 + r : 0;
+                    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
+                    if (in) q += (p.w.first + row / a.G) * a.qs + (int64_t)(p.head * a.G + row % a.G) * a.D + c * 8;
+                    if (vq) {
+                        cp_async16(to, q, in ? 16 : 0);
+                    } else {
+                        uint4 f = make_uint4(0, 0, 0, 0);
+                        if (in) {
+                            const unsigned short* e = reinterpret_cast<const unsigned short*>(q);
+                            f = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16, e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
+                        }
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(f.x), "r"(f.y), "r"(f.z), "r"(f.w) : "memory");
+                    }
+                }
+                cp_commit();
+                cp_wait<0>();
+                fence_async_smem();
+                arrive_warp(kQFull);
+                // where this lane's two keys of tile t lie, -1: nowhere
+                const int32_t* pages = a.table + (size_t)max(p.w.seq, 0) * a.max_pages;
+                auto look = [&](int t, int64_t* at) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int key = (p.s.tile0 + t) * KT + half * 64 + e * 32 + lane;
+                        at[e] = -1;
+                        if (t >= p.t1 || key < p.s.begin || key >= p.s.end) continue;
+                        const int page = pages[key / a.pt];
+                        if (page < 0 || page >= a.pages) record_error(a.status, KDA_ERR_INVALID_ARG);
+                        else at[e] = (((int64_t)page * 2 * a.Hkv + p.head) * a.pt + key % a.pt) * (a.D * 2);
+                    }
+                };
+                int64_t at[2], next[2];
+                look(p.t0, at);
+                for (int t = p.t0; ok && t < p.t1; ++t) {
+                    look(t + 1, next);
+#pragma unroll 1
+                    for (int kv = 0; kv < 2; ++kv, ++g) {
+                        const int slot = g % L::SLOTS;
+                        if (g >= L::SLOTS && !wait(kEmpty + slot, (g / L::SLOTS - 1) & 1)) { ok = false; break; }
+                        const uint32_t to = smem_u32(smem + L::KV + slot * L::TILE);
+                        const char* from = pool + (kv ? values : 0) + c * 16;
+#pragma unroll 4
+                        for (int i = 0; i < ROUNDS; ++i) {
+                            const int r = i * EACH + sub;            // of this warp's 64 rows
+                            const int64_t lo = __shfl_sync(0xffffffffu, at[0], r & 31), hi = __shfl_sync(0xffffffffu, at[1], r & 31);
+                            const int64_t x = r < 32 ? lo : hi;
+                            const bool in = x >= 0 && column;
+                            cp_async16(to + piece(half * 64 + r, c), in ? from + x : pool, in ? 16 : 0);
+                        }
+                        cp_commit();
+                        if (g >= told + 2) {
+                            cp_wait<2>();
+                            tell();
+                        }
+                    }
+                    at[0] = next[0];
+                    at[1] = next[1];
+                }
+                // (all of the piece is announced before Q's place is waited for)
+                cp_wait<0>();
+                while (ok && told < g) tell();
+            }
+            cp_wait<0>();
+        }
+    }
+    __syncthreads();
+    if (*fail && tid == 0) {
+        // give products in flight a bounded chance to land before the memory is released
+        record_error(a.status, KDA_ERR_TIMEOUT);
+#pragma unroll 1
+        for (int b = 0; b < kBars; ++b) {
+            mbar_wait(&bar[b], 0, 1u << 12);
+            mbar_wait(&bar[b], 1, 1u << 12);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tmem, TCOLS);
+}
+
+template <int NB> cudaError_t go(const AttnArgs& a, cudaStream_t st) {
+    const cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<NB>::TOTAL);
+    if (e != cudaSuccess) return e;
+    attn_tc_kernel<NB><<<a.ctas, kThreads, Lay<NB>::TOTAL, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t st) { return a.D > 64 ? go<2>(a, st) : go<1>(a, st); }
+
+}  // namespace kda
