@@ -530,7 +530,8 @@ size_t attn_layout(char* ws, AttnArgs* a) {
 // Which kernel a call takes, and its cut.  aligned: the pool's base allows 16-byte copies.
 void attn_choose(AttnArgs* a, bool aligned) {
     const int64_t packed = (int64_t)a->tokens * a->G;
-    if (a->dtype == KDA_BF16 && a->D % 8 == 0 && aligned && a->D <= 128 && packed > 32 * (int64_t)a->rows) {
+    if (a->dtype == KDA_BF16 && a->D % 8 == 0 && aligned && a->D <= 128 && packed > 32 * (int64_t)a->rows &&
+        (int64_t)a->pages * 2 * a->Hkv < (1 << 30)) {      // (a tensor map's coordinate)
         a->kernel = kAttnTc;
         attn_cut(a, kAttnTcRows, kAttnTcKeys, 152);
     } else if (a->dtype == KDA_BF16 && a->D % 8 == 0 && aligned) {

@@ -7,12 +7,15 @@
 // The maximum m that scores are taken from is raised only when it is passed by more than 8 in log2; then, a few times in
 // a row's life, the row's output is rescaled in TMEM, between the products that add to it.
 //
-// Operands: K and V lie in one ring of four 32 KB slots (K, V, K, V, ...), rows of 128 bytes in the 128-byte swizzle, where two
-// warps' cp.async puts them: a page may be of any size, end inside a tile or be missing, and what is past the sequence's end is
-// filled with zeros (its values meet zero weights).  K is read K-major, V MN-major (keys as K), P from TMEM.
+// Operands: K and V lie in one ring of four 32 KB slots (K, V, K, V, ...), rows of 128 bytes in the 128-byte swizzle, put there
+// by TMA in boxes of R keys, the largest power of two that divides the page's tokens, so that a box lies in one page; a lane
+// of the copying warp looks up the page of one box and issues its copy.  Boxes without a key to read, and missing pages, lie out of
+// the map's range, which gives zeros.  A box that a row's end (or its window's begin) cuts would bring values that are nobody's, and
+// zero times those need not be zero: its values are copied row by row with cp.async, zeros for the others.  K is read
+// K-major, V MN-major (keys as K), P from TMEM.
 //
-// Roles (12 warps): 0-3 and 4-7 the softmax of the two tiles, 8 and 9 issue the products of one tile each, 10 and 11
-// copy.  The tiles go their own ways: S -> softmax -> P V -> next S each, so that one's products run while the other's
+// Roles (12 warps): 0-3 and 4-7 the softmax of the two tiles, 8 and 9 issue the products of one tile each, 10 copies keys and
+// values, 11 Q.  The tiles go their own ways: S -> softmax -> P V -> next S each, so that one's products run while the other's
 // exponentials do.  P of a tile lies where its next S goes, hence the next S is issued when P V is complete.
 // Registers: a softmax thread holds 128 scores, the others little: 208 and 88 (256 x 208 + 128 x 88 = 384 x 168).
 // TMEM columns: S (and P) 2 x 128, O 2 x 128.
@@ -26,6 +29,7 @@
 #include "kda_attn.h"
 #include "kda_common.cuh"
 #include "kda_sm100.cuh"
+#include "kda_tma.h"
 
 namespace kda {
 
@@ -48,9 +52,9 @@ template <int NB> struct Lay {
 };
 
 enum Bars {
-    kFull = 0,       // [4] a slot's copies landed (2 warps)
+    kFull = 0,       // [4] a slot's copies landed
     kEmpty = 4,      // [4] its products complete, of both tiles
-    kQFull = 8,      // Q landed (2 warps)
+    kQFull = 8,      // Q landed
     kQEmpty = 9,     // the piece's products with Q complete, of both tiles
     kS = 10,         // [2] S complete
     kP = 12,         // [2] P written, O rescaled (4 warps)
@@ -99,6 +103,13 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+__device__ __forceinline__ void tma_load_3d_to(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(mbar))
+        : "memory");
+}
+
 // Byte of 16-byte piece c (of NB x 8) of row r in a tile.
 __device__ __forceinline__ uint32_t piece(int r, int c) { return (c >> 3) * HALF + (uint32_t)(r * 128 + (((c & 7) ^ (r & 7)) << 4)); }
 
@@ -110,7 +121,7 @@ template <int N> __device__ __forceinline__ void landed(float* v) {
 }
 
 template <int NB>
-__global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map, int box_log2) {
     using L = Lay<NB>;
     constexpr int DP = 64 * NB;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -124,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     const AttnCut cut(a, units.tiles(a));
     if (cta >= cut.ctas) return;
     if (tid == 0) {
-        for (int i = 0; i < kBars; ++i) mbar_init(&bar[i], i >= kP && i < kO || i >= kOFree ? 4 : i >= kS ? 1 : 2);
+        for (int i = 0; i < kBars; ++i) mbar_init(&bar[i], i >= kP && i < kO || i >= kOFree ? 4 : i >= kEmpty && i < kQFull || i == kQEmpty ? 2 : 1);
         *fail = 0;
         mbar_fence_init();
     }
@@ -342,28 +353,85 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 }
             }
             __syncwarp();
+        } else if (warp == 10) {
+            // ------------------------------------------------------------ keys and values
+            const int R = 1 << box_log2, boxes = (KT >> box_log2) * NB, nowhere = a.pages * 2 * a.Hkv;
+            uint32_t g = 0;
+            bool ok = true;
+            for (AttnWalk p(a, units, cut, cta); ok && p.more(); p.next(a, units)) {
+                const int32_t* pages = a.table + (size_t)max(p.w.seq, 0) * a.max_pages;
+                // the map's third coordinate of the keys (values: + Hkv) of the box that begins at `key`
+                auto look = [&](int key) {
+                    if (key + R <= p.s.begin || key >= p.s.end) return nowhere;
+                    const int page = pages[key / a.pt];
+                    if (page >= 0 && page < a.pages) return page * 2 * a.Hkv + p.head;
+                    record_error(a.status, KDA_ERR_INVALID_ARG);
+                    return nowhere;
+                };
+                auto cut_box = [&](int key) { return (key < p.s.begin && key + R > p.s.begin) || (key < p.s.end && key + R > p.s.end); };
+                const int mine = (lane / NB) << box_log2;       // this lane's first box: its keys in a tile
+                int next = look((p.s.tile0 + p.t0) * KT + mine);
+                for (int t = p.t0; ok && t < p.t1; ++t) {
+                    const int k0 = (p.s.tile0 + t) * KT, first = next;
+                    if (t + 1 < p.t1) next = look(k0 + KT + mine);
+#pragma unroll 1
+                    for (int kv = 0; kv < 2; ++kv, ++g) {
+                        const int slot = g % L::SLOTS;
+                        if (g >= L::SLOTS && !wait(kEmpty + slot, (g / L::SLOTS - 1) & 1)) { ok = false; break; }
+                        const uint32_t to = smem_u32(smem + L::KV + slot * L::TILE);
+                        int by_row = 0;
+                        if (kv && R > 1) {
+                            // (the box of the window's begin and that of the end; one box may be both)
+                            int done = -1;
+#pragma unroll 1
+                            for (int edge : {p.s.begin, p.s.end}) {
+                                const int key = edge & ~(R - 1);
+                                if (key == edge || key < k0 || key >= k0 + KT || key == done) continue;
+                                done = key;
+                                ++by_row;
+                                const int z = look(key);
+                                const char* from = static_cast<const char*>(a.pool) + ((int64_t)(z + a.Hkv) * a.pt + key % a.pt) * (a.D * 2);
+#pragma unroll 1
+                                for (int i = lane; i < R * 8 * NB; i += 32) {
+                                    const int r = i / (8 * NB), c = i % (8 * NB);
+                                    const bool in = z != nowhere && key + r >= p.s.begin && key + r < p.s.end && c * 8 < a.D;
+                                    cp_async16(to + piece(key - k0 + r, c), in ? from + (int64_t)r * a.D * 2 + c * 16 : a.pool, in ? 16 : 0);
+                                }
+                            }
+                            if (by_row) {
+                                cp_commit();
+                                cp_wait<0>();
+                                fence_async_smem();
+                                __syncwarp();
+                            }
+                        }
+                        if (lane == 0) mbar_expect_tx(&bar[kFull + slot], (boxes - by_row * NB) * R * 128);
+                        __syncwarp();
+#pragma unroll 1
+                        for (int i = lane; i < boxes; i += 32) {
+                            const int at = (i / NB) << box_log2, key = k0 + at;
+                            const int z = (i < 32 ? first : look(key));
+                            if (kv && R > 1 && cut_box(key)) continue;
+                            tma_load_3d_to(to + (i % NB) * HALF + at * 128, &map, (i % NB) * 64, key % a.pt, z == nowhere ? nowhere : z + kv * a.Hkv,
+                                           &bar[kFull + slot]);
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
         } else {
-            // ------------------------------------------------------------ copies: half of a tile's keys a warp
-            const int half = warp - 10;
-            constexpr int PER = DP / 8, EACH = 32 / PER, ROUNDS = 64 / EACH;      // pieces of a row, rows of one round of the lanes, rounds
+            // ------------------------------------------------------------ Q
+            constexpr int PER = DP / 8, EACH = 32 / PER;      // pieces of a row, rows of one round of the lanes
             const int c = lane % PER, sub = lane / PER;
             const bool column = c * 8 < a.D, vq = a.qs % 8 == 0 && reinterpret_cast<uintptr_t>(a.q) % 16 == 0;
-            const size_t values = (size_t)a.Hkv * a.pt * a.D * 2;
-            const char* pool = static_cast<const char*>(a.pool);
-            uint32_t g = 0, pieces = 0, told = 0;        // slots filled; of them announced
-            bool ok = true;
-            auto tell = [&]() {
-                fence_async_smem();
-                arrive_warp(kFull + told % L::SLOTS);
-                ++told;
-            };
-            for (AttnWalk p(a, units, cut, cta); ok && p.more(); p.next(a, units), ++pieces) {
+            uint32_t pieces = 0;
+            for (AttnWalk p(a, units, cut, cta); p.more(); p.next(a, units), ++pieces) {
                 if (pieces && !wait(kQEmpty, (pieces - 1) & 1)) break;
                 const int64_t r0 = p.first_row(a);
                 const int rows = p.rows(a);
-#pragma unroll 1
-                for (int i = 0; i < 256 / EACH; i += 2) {
-                    const int r = (i + half) * EACH + sub;
+#pragma unroll 4
+                for (int i = 0; i < 256 / EACH; ++i) {
+                    const int r = i * EACH + sub;
                     const uint32_t to = smem_u32(smem + L::Q + (r >> 7) * L::TILE) + piece(r & 127, c);
                     const bool in = r < rows && column;
                     const int64_t row = in ? r0 + r : 0;
@@ -384,51 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 cp_wait<0>();
                 fence_async_smem();
                 arrive_warp(kQFull);
-                // where this lane's two keys of tile t lie, -1: nowhere
-                const int32_t* pages = a.table + (size_t)max(p.w.seq, 0) * a.max_pages;
-                auto look = [&](int t, int64_t* at) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int key = (p.s.tile0 + t) * KT + half * 64 + e * 32 + lane;
-                        at[e] = -1;
-                        if (t >= p.t1 || key < p.s.begin || key >= p.s.end) continue;
-                        const int page = pages[key / a.pt];
-                        if (page < 0 || page >= a.pages) record_error(a.status, KDA_ERR_INVALID_ARG);
-                        else at[e] = (((int64_t)page * 2 * a.Hkv + p.head) * a.pt + key % a.pt) * (a.D * 2);
-                    }
-                };
-                int64_t at[2], next[2];
-                look(p.t0, at);
-                for (int t = p.t0; ok && t < p.t1; ++t) {
-                    look(t + 1, next);
-#pragma unroll 1
-                    for (int kv = 0; kv < 2; ++kv, ++g) {
-                        const int slot = g % L::SLOTS;
-                        if (g >= L::SLOTS && !wait(kEmpty + slot, (g / L::SLOTS - 1) & 1)) { ok = false; break; }
-                        const uint32_t to = smem_u32(smem + L::KV + slot * L::TILE);
-                        const char* from = pool + (kv ? values : 0) + c * 16;
-#pragma unroll 4
-                        for (int i = 0; i < ROUNDS; ++i) {
-                            const int r = i * EACH + sub;            // of this warp's 64 rows
-                            const int64_t lo = __shfl_sync(0xffffffffu, at[0], r & 31), hi = __shfl_sync(0xffffffffu, at[1], r & 31);
-                            const int64_t x = r < 32 ? lo : hi;
-                            const bool in = x >= 0 && column;
-                            cp_async16(to + piece(half * 64 + r, c), in ? from + x : pool, in ? 16 : 0);
-                        }
-                        cp_commit();
-                        if (g >= told + 2) {
-                            cp_wait<2>();
-                            tell();
-                        }
-                    }
-                    at[0] = next[0];
-                    at[1] = next[1];
-                }
-                // (all of the piece is announced before Q's place is waited for)
-                cp_wait<0>();
-                while (ok && told < g) tell();
             }
-            cp_wait<0>();
         }
     }
     __syncthreads();
@@ -447,9 +471,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 }
 
 template <int NB> cudaError_t go(const AttnArgs& a, cudaStream_t st) {
-    const cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<NB>::TOTAL);
+    cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<NB>::TOTAL);
     if (e != cudaSuccess) return e;
-    attn_tc_kernel<NB><<<a.ctas, kThreads, Lay<NB>::TOTAL, st>>>(a);
+    int box_log2 = 0;
+    while (box_log2 < 7 && a.pt % (2 << box_log2) == 0) ++box_log2;
+    // a pool as [pages x (keys, values) x heads][page tokens][D]
+    auto enc = map_encoder();
+    if (!enc) return cudaErrorNotSupported;
+    CUtensorMap map;
+    const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.pt, (cuuint64_t)a.pages * 2 * a.Hkv};
+    const cuuint64_t strides[2] = {(cuuint64_t)a.D * 2, (cuuint64_t)a.pt * a.D * 2};
+    const cuuint32_t box[3] = {64, 1u << box_log2, 1}, es[3] = {1, 1, 1};
+    if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.pool), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    attn_tc_kernel<NB><<<a.ctas, kThreads, Lay<NB>::TOTAL, st>>>(a, map, box_log2);
     return cudaGetLastError();
 }
 

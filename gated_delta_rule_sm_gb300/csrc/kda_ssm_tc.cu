@@ -36,7 +36,6 @@
 // of a chunk's 7300 cycles.  The source asks for about 1650 of those accesses (M's factors 160, Y 512, the copies of S
 // 512, U's loads 256); the other 1500 are conflicts or replays whose cause has not been found.  And the roles' loops together fill the instruction cache, which is why
 // they are kept short (M unrolled over its 32 columns and two copies of copy_state: 222 us).
-#include <cudaTypedefs.h>
 #include <string.h>
 
 #include <type_traits>
@@ -44,6 +43,7 @@
 #include "kda.h"
 #include "kda_sm100.cuh"
 #include "kda_ssm.h"
+#include "kda_tma.h"
 
 namespace kda {
 
@@ -867,18 +867,6 @@ ssm_tc_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ CUtenso
 }
 
 // ------------------------------------------------------------------ launch
-
-PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            f = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    }();
-    return fn;
-}
 
 // [TT tokens, `stride` elements apart][heads][cols] bf16 -> boxes of 128 tokens x 1 head x 64 columns in 128-byte
 // swizzled rows; columns past `cols`, heads past `heads` and tokens past TT read as zeros.
