@@ -14,9 +14,11 @@
 // zero times those need not be zero: its values are copied row by row with cp.async, zeros for the others.  K is read
 // K-major, V MN-major (keys as K), P from TMEM.
 //
-// Roles (12 warps): 0-3 and 4-7 the softmax of the two tiles, 8 and 9 issue the products of one tile each, 10 copies keys and
-// values, 11 Q.  The tiles go their own ways: S -> softmax -> P V -> next S each, so that one's products run while the other's
-// exponentials do.  P of a tile lies where its next S goes, hence the next S is issued when P V is complete.
+// Roles (12 warps): 0-3 and 4-7 the softmax of the two tiles, 8 issues the products, 10 copies keys and values, 11 Q (9 has
+// nothing to do).  The products come in the order P V and next S of one tile, P V and next S of the other, so that one's run
+// while the other's exponentials do.  (A thread for each tile's products, in no order between them, let both tiles fall into
+// step: products, then exponentials, 4430 cycles a step.)  P of a tile lies where its next S goes, hence the next S is issued when P
+// V is complete.  P is handed over in halves of 64 keys.
 // Registers: a softmax thread holds 128 scores, the others little: 208 and 88 (256 x 208 + 128 x 88 = 384 x 168).
 // TMEM columns: S (and P) 2 x 128, O 2 x 128.
 // Bound: per pair of tiles and 128 keys 16.8 MFLOP, 2050 cycles of the tensor core at its dense rate, beside 32768 exponentials,
@@ -53,14 +55,14 @@ template <int NB> struct Lay {
 
 enum Bars {
     kFull = 0,       // [4] a slot's copies landed
-    kEmpty = 4,      // [4] its products complete, of both tiles
+    kEmpty = 4,      // [4] its products complete
     kQFull = 8,      // Q landed
-    kQEmpty = 9,     // the piece's products with Q complete, of both tiles
+    kQEmpty = 9,     // the piece's products complete
     kS = 10,         // [2] S complete
-    kP = 12,         // [2] P written, O rescaled (4 warps)
-    kO = 14,         // [2] P V complete
-    kOFree = 16,     // [2] the piece's O read (4 warps)
-    kBars = 18
+    kO = 12,         // [2] P V complete
+    kP = 14,         // [2][2] half the keys of P written, and O rescaled before (4 warps)
+    kOFree = 18,     // [2] the piece's O read (4 warps)
+    kBars = 20
 };
 
 constexpr uint32_t TS = 0, TO = 256, TCOLS = 512;       // + 128 tile
@@ -95,6 +97,11 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+__device__ __forceinline__ float max3(float x, float y, float z) {      // (a NaN counts as nothing, as in fmaxf)
+    float m;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
+    return m;
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) { return fma2(a, dup(1.f), b); }
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
@@ -135,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     const AttnCut cut(a, units.tiles(a));
     if (cta >= cut.ctas) return;
     if (tid == 0) {
-        for (int i = 0; i < kBars; ++i) mbar_init(&bar[i], i >= kP && i < kO || i >= kOFree ? 4 : i >= kEmpty && i < kQFull || i == kQEmpty ? 2 : 1);
+        for (int i = 0; i < kBars; ++i) mbar_init(&bar[i], i >= kP ? 4 : 1);
         *fail = 0;
         mbar_fence_init();
     }
@@ -189,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             // positions of the warp's rows, for tiles that need no mask
             const int low = __reduce_min_sync(0xffffffffu, pos), high = __reduce_max_sync(0xffffffffu, pos);
             float base = -INFINITY;                  // what scores are taken from (a score, not yet times c)
-            float2 sum = make_float2(0.f, 0.f);
+            float2 sum = make_float2(0.f, 0.f), also = make_float2(0.f, 0.f);
             bool ok = true;
             for (int t = p.t0; t < p.t1; ++t, ++n) {
                 const int k0 = (p.s.tile0 + t) * KT;
@@ -208,19 +215,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     for (int j = 0; j < KT; ++j)
                         if (j > last || j <= first) v[j] = -INFINITY;
                 }
-                float m[4];
+                float m[8];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) m[j] = fmaxf(v[j], v[j + 4]);
+                for (int i = 0; i < 8; ++i) m[i] = v[i];
 #pragma unroll
-                for (int j = 8; j < KT; j += 4)
+                for (int j = 8; j + 16 <= KT; j += 16)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) m[i] = fmaxf(m[i], v[j + i]);
-                const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+                    for (int i = 0; i < 8; ++i) m[i] = max3(m[i], v[j + i], v[j + 8 + i]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m[i] = fmaxf(m[i], v[KT - 8 + i]);
+                const float top = fmaxf(max3(max3(m[0], m[1], m[2]), m[3], m[4]), max3(m[5], m[6], m[7]));
                 const bool raise = top * c > base * c + kRaise;
                 if (__any_sync(0xffffffffu, raise)) {
                     const float now = raise ? top : base, f = now == -INFINITY ? 1.f : ex2((base - now) * c);
                     base = now;
                     sum = mul2(sum, dup(f));
+                    also = mul2(also, dup(f));
                     if (t > p.t0) {
                         // (S of this tile came after P V of the last one: O is at rest)
 #pragma unroll 1
@@ -244,18 +254,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                         float2 z = fma2(make_float2(v[j + 2 * i], v[j + 2 * i + 1]), dup(c), dup(from));
                         z.x = ex2(z.x);
                         z.y = ex2(z.y);
-                        sum = add2(sum, z);
+                        if (i & 1) also = add2(also, z);
+                        else sum = add2(sum, z);
                         w[i] = pack_bf16(z.x, z.y);
                     }
                     tmem_st16(ts + j / 2, w);
+                    if (j % 64 == 32) {
+                        tmem_st_wait();
+                        tc_fence_before();
+                        arrive_warp(kP + 2 * tile + j / 64);
+                    }
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                arrive_warp(kP + tile);
             }
             if (!ok || !wait(kO + tile, (n - 1) & 1)) break;
             tc_fence_after();
-            const float l = sum.x + sum.y;
+            const float l = (sum.x + sum.y) + (also.x + also.y);
             const bool whole = p.whole(), live = row < rows;
             const int64_t token = p.w.first + packed / a.G;
             const size_t at = (size_t)token * a.Hq + p.head * a.G + packed % a.G;
@@ -301,55 +314,59 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-        if (warp < 10) {
-            // ------------------------------------------------------------ products of a tile
-            const int tile = warp - 8;
+        if (warp == 8) {
+            // ------------------------------------------------------------ products
             if (lane == 0) {
                 constexpr uint32_t idS = idesc_bf16(128, KT, 0, 0), idO = idesc_bf16(128, DP, 0, 1);
-                const uint32_t sq = desc_lo(smem_u32(smem + L::Q + tile * L::TILE), 16), ts = tmem + TS + 128 * tile, to = tmem + TO + 128 * tile;
-                uint32_t n = 0, g = 0, pieces = 0, mine = 0;     // this tile's and all key tiles, pieces, and those with this tile
+                uint32_t n[2] = {0, 0}, mine[2] = {0, 0}, g = 0, pieces = 0;     // key tiles and pieces of each query tile, and of both
+                auto keys = [&](uint32_t at, int v) { return wait1(kFull + (2 * at + v) % L::SLOTS, (2 * at + v) / L::SLOTS & 1); };
+                auto scores = [&](int tile, uint32_t at) {
+                    const uint32_t sq = desc_lo(smem_u32(smem + L::Q + tile * L::TILE), 16), ts = tmem + TS + 128 * tile;
+                    const uint32_t sk = desc_lo(smem_u32(smem + L::KV + 2 * at % L::SLOTS * L::TILE), 16);
+                    tc_fence_after();
+                    steps<4 * NB>([&](auto k) {
+                        constexpr int o = (k >> 2) * HALF + (k & 3) * 32;
+                        mma_ss<o, o>(ts, sq, sk, idS, k > 0);
+                    });
+                    mma_commit(&bar[kS + tile]);
+                };
                 bool ok = true;
                 for (AttnWalk p(a, units, cut, cta); ok && p.more(); p.next(a, units), ++pieces) {
-                    const bool live = p.rows(a) > 128 * tile;
-                    ok = wait1(kQFull, pieces & 1);
+                    const int tiles = p.rows(a) > 128 ? 2 : 1, last = tiles - 1;
+                    // (the last piece's products are complete: Q's place was given up after them)
+                    ok = wait1(kQFull, pieces & 1) && keys(g, 0);
+                    if (!ok) break;
+                    for (int tile = 0; tile < tiles; ++tile) scores(tile, g);
+                    mma_commit(&bar[kEmpty + 2 * g % L::SLOTS]);
                     for (int t = p.t0; ok && t < p.t1; ++t, ++g) {
-                        const int ks = (2 * g) % L::SLOTS, vs = ks + 1;
-                        const uint32_t use = (2 * g) / L::SLOTS & 1;
-                        if (!live) {                            // slots wait for both tiles
-                            ok = wait1(kFull + ks, use);
+                        const bool next = t + 1 < p.t1;
+                        const uint32_t vs = (2 * g + 1) % L::SLOTS, sv = desc_lo(smem_u32(smem + L::KV + vs * L::TILE), HALF);
+                        ok = keys(g, 1);
+#pragma unroll 1
+                        for (int tile = 0; ok && tile < tiles; ++tile) {
+                            const uint32_t ts = tmem + TS + 128 * tile, to = tmem + TO + 128 * tile;
+                            ok = wait1(kP + 2 * tile, n[tile] & 1) && (t > p.t0 || mine[tile] == 0 || wait1(kOFree + tile, (mine[tile] - 1) & 1));
                             if (!ok) break;
-                            mbar_arrive(&bar[kEmpty + ks]);
-                            ok = wait1(kFull + vs, use);
+                            tc_fence_after();
+                            steps<KT / 32>([&](auto k) { mma_ts<k * 2048>(to, ts + 8 * k, sv, idO, t > p.t0 || k > 0); });
+                            ok = wait1(kP + 2 * tile + 1, n[tile] & 1);
                             if (!ok) break;
-                            mbar_arrive(&bar[kEmpty + vs]);
-                            continue;
+                            tc_fence_after();
+                            steps<KT / 32>([&](auto k) { mma_ts<(k + KT / 32) * 2048>(to, ts + 8 * (k + KT / 32), sv, idO, 1); });
+                            mma_commit(&bar[kO + tile]);
+                            if (tile == last) mma_commit(&bar[kEmpty + vs]);
+                            if (next) {
+                                ok = (tile || keys(g + 1, 0)) && wait1(kO + tile, n[tile] & 1);
+                                if (!ok) break;
+                                scores(tile, g + 1);
+                                if (tile == last) mma_commit(&bar[kEmpty + (2 * g + 2) % L::SLOTS]);
+                            }
+                            ++n[tile];
                         }
-                        ok = wait1(kFull + ks, use) && (t == p.t0 || wait1(kO + tile, (n - 1) & 1));
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t sk = desc_lo(smem_u32(smem + L::KV + ks * L::TILE), 16);
-                        steps<4 * NB>([&](auto k) {
-                            constexpr int o = (k >> 2) * HALF + (k & 3) * 32;
-                            mma_ss<o, o>(ts, sq, sk, idS, k > 0);
-                        });
-                        mma_commit(&bar[kS + tile]);
-                        mma_commit(&bar[kEmpty + ks]);
-                        ok = wait1(kFull + vs, use) && wait1(kP + tile, n & 1) && (t > p.t0 || mine == 0 || wait1(kOFree + tile, (mine - 1) & 1));
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t sv = desc_lo(smem_u32(smem + L::KV + vs * L::TILE), HALF);
-                        steps<KT / 16>([&](auto k) { mma_ts<k * 2048>(to, ts + 8 * k, sv, idO, t > p.t0 || k > 0); });
-                        mma_commit(&bar[kEmpty + vs]);
-                        mma_commit(&bar[kO + tile]);
-                        ++n;
                     }
                     if (!ok) break;
-                    if (live) {
-                        ++mine;
-                        mma_commit(&bar[kQEmpty]);
-                    } else {
-                        mbar_arrive(&bar[kQEmpty]);
-                    }
+                    for (int tile = 0; tile < tiles; ++tile) ++mine[tile];
+                    mma_commit(&bar[kQEmpty]);
                 }
             }
             __syncwarp();
@@ -419,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     }
                 }
             }
-        } else {
+        } else if (warp == 11) {
             // ------------------------------------------------------------ Q
             constexpr int PER = DP / 8, EACH = 32 / PER;      // pieces of a row, rows of one round of the lanes
             const int c = lane % PER, sub = lane / PER;
