@@ -232,8 +232,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     const int c0 = cut.owner(x), c1 = cut.owner(x + tiles - 1);
     if (c0 == c1) return;
     const AttnRow w = attn_row(a, a.unit_row[u], false);
-    const int64_t r0 = (int64_t)a.unit_row[a.units_most + u] * a.block, left = (int64_t)w.n * a.G - r0;
-    const int n = (int)(left < a.block ? left : a.block), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t r0 = (uint32_t)a.unit_row[a.units_most + u] * a.block;
+    const int n = (int)min((uint32_t)w.n * a.G - r0, (uint32_t)a.block), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int i0 = blockIdx.y * rows_each, i1 = min(n, i0 + rows_each);
     const bool few = c1 - c0 < kJoinFew;
     for (int i = few ? i0 + warp : i0; i < i1; i += few ? kJoinWarps : 1) {
@@ -243,8 +243,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         const float base = top == -INFINITY ? 0.f : top;
-        const int64_t row = r0 + i;
-        const size_t at = (w.first + row / a.G) * a.Hq + head * a.G + row % a.G;
+        const uint32_t row = r0 + i, token = row / (uint32_t)a.G;
+        const size_t at = (size_t)(w.first + token) * a.Hq + head * a.G + (row - token * a.G);
         JoinSum s = join_parts(a, c0, c1, few ? 0 : warp, few ? 1 : kJoinWarps, i, base);
         if (few) {
             join_write(a, at, s, base);
@@ -315,15 +315,14 @@ __global__ void __launch_bounds__(kSimtThreads, DC > 2 ? 1 : 2) attn_simt_kernel
     for (AttnWalk p(a, units, cut, cta); p.more(); p.next(a, units)) {
         const AttnRow w = p.w;
         const AttnSpan s = p.s;
-        const int64_t r0 = p.first_row(a);
         const int n = p.rows(a);
         __syncthreads();
         for (int i = tid; i < kSimtRows * (D4 / 4); i += kSimtThreads) {
             const int r = i % kSimtRows, d = i / kSimtRows * 4;
             float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < n) {
-                const int64_t row = r0 + r, token = w.first + row / a.G;
-                const char* q = static_cast<const char*>(a.q) + (token * a.qs + (int64_t)(p.head * a.G + row % a.G) * a.D) * (int64_t)sizeof(E);
+                const AttnWalk::Place from = p.place(a, r);
+                const char* q = static_cast<const char*>(a.q) + (from.token * a.qs + from.head * a.D) * (int64_t)sizeof(E);
                 f = load4<E>(q, d, a.D, vq);
             }
             sq[d * kSimtPad + r] = f.x;
@@ -337,8 +336,7 @@ __global__ void __launch_bounds__(kSimtThreads, DC > 2 ? 1 : 2) attn_simt_kernel
         for (int i = 0; i < 4; ++i) {
             top[i] = -INFINITY;
             sum[i] = 0.f;
-            const int64_t row = r0 + 4 * ty + i;
-            pos[i] = 4 * ty + i < n ? w.len - w.n + (int)(row / a.G) : -1;
+            pos[i] = 4 * ty + i < n ? p.position(a, 4 * ty + i) : -1;
 #pragma unroll
             for (int k = 0; k < DC; ++k)
 #pragma unroll
@@ -436,8 +434,8 @@ __global__ void __launch_bounds__(kSimtThreads, DC > 2 ? 1 : 2) attn_simt_kernel
         for (int i = 0; i < 4; ++i) {
             const int r = 4 * ty + i;
             if (r >= n) continue;
-            const int64_t row = r0 + r;
-            const size_t at = (w.first + row / a.G) * a.Hq + p.head * a.G + row % a.G;
+            const AttnWalk::Place to_row = p.place(a, r);
+            const size_t at = (size_t)to_row.token * a.Hq + to_row.head;
             const float inv = sum[i] > 0.f ? 1.f / sum[i] : sum[i] == 0.f ? 0.f : sum[i];
 #pragma unroll
             for (int b = 0; b < DC; ++b)

@@ -66,9 +66,9 @@ struct AttnSpan {
 };
 __device__ __forceinline__ AttnSpan attn_span(const AttnArgs& a, const AttnRow& w, int block) {
     AttnSpan s;
-    const int64_t r0 = (int64_t)block * a.block, last = (int64_t)w.n * a.G - 1;
-    const int64_t r1 = r0 + a.block - 1 < last ? r0 + a.block - 1 : last;
-    const int p0 = w.len - w.n + (int)(r0 / a.G), p1 = w.len - w.n + (int)(r1 / a.G);
+    // (packed rows fit 32 bits: tokens x query heads does)
+    const uint32_t r0 = (uint32_t)block * a.block, r1 = min(r0 + a.block, (uint32_t)w.n * a.G) - 1;
+    const int p0 = w.len - w.n + (int)(r0 / (uint32_t)a.G), p1 = w.len - w.n + (int)(r1 / (uint32_t)a.G);
     s.end = w.seq < 0 ? 0 : max(p1 + 1, 0);
     s.begin = a.window ? max(p0 - a.window + 1, 0) : 0;
     if (s.begin >= s.end) s.begin = s.end = 0;
@@ -181,11 +181,17 @@ struct AttnWalk {
     __device__ __forceinline__ bool whole() const { return t1 - t0 == tiles; }
     // where its sums go: a CTA shares at most the item it starts inside of and the one it does not finish
     __device__ __forceinline__ int slot(int cta) const { return 2 * cta + (t0 == 0); }
-    __device__ __forceinline__ int64_t first_row(const AttnArgs& a) const { return (int64_t)block * a.block; }
-    __device__ __forceinline__ int rows(const AttnArgs& a) const {
-        const int64_t left = (int64_t)w.n * a.G - first_row(a);
-        return (int)(left < a.block ? left : a.block);
+    __device__ __forceinline__ uint32_t first_row(const AttnArgs& a) const { return (uint32_t)block * a.block; }
+    __device__ __forceinline__ int rows(const AttnArgs& a) const { return (int)min((uint32_t)w.n * a.G - first_row(a), (uint32_t)a.block); }
+    // The token and the query head of packed row i of the block.
+    struct Place {
+        int token, head;
+    };
+    __device__ __forceinline__ Place place(const AttnArgs& a, int i) const {
+        const uint32_t r = first_row(a) + i, t = r / (uint32_t)a.G;
+        return {w.first + (int)t, head * a.G + (int)(r - t * a.G)};
     }
+    __device__ __forceinline__ int position(const AttnArgs& a, int i) const { return w.len - w.n + (int)((first_row(a) + i) / (uint32_t)a.G); }
 };
 
 __device__ __forceinline__ size_t attn_part_floats(const AttnArgs& a) { return (size_t)a.block * (a.D + 2); }

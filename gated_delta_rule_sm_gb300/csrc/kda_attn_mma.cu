@@ -92,7 +92,6 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attn_mma_kernel(c
     for (AttnWalk p(a, units, cut, cta); p.more(); p.next(a, units)) {
         const AttnRow w = p.w;
         const AttnSpan s = p.s;
-        const int64_t r0 = p.first_row(a);
         const int n = p.rows(a);
         const int steps = p.t1 - p.t0, first = (s.tile0 + p.t0) * kAttnMmaKeys + warp * kGroup;
         const int32_t* pages = a.table + (size_t)max(w.seq, 0) * a.max_pages;
@@ -140,8 +139,8 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attn_mma_kernel(c
             const int r = i / (DP / 8), b = i % (DP / 8);
             uint4 f = make_uint4(0, 0, 0, 0);
             if (r < n && b * 8 < a.D) {
-                const int64_t row = r0 + r, token = w.first + row / a.G;
-                const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + token * a.qs + (int64_t)(p.head * a.G + row % a.G) * a.D + b * 8;
+                const AttnWalk::Place from = p.place(a, r);
+                const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + from.token * a.qs + from.head * a.D + b * 8;
                 if (vq) f = *reinterpret_cast<const uint4*>(q);
                 else {
                     const unsigned short* e = reinterpret_cast<const unsigned short*>(q);
@@ -167,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attn_mma_kernel(c
                 const int r = m * 16 + h * 8 + (lane >> 2);
                 base[m][h] = -INFINITY;
                 sum[m][h] = 0.f;
-                pos[m][h] = r < n ? w.len - w.n + (int)((r0 + r) / a.G) : -1;
+                pos[m][h] = r < n ? p.position(a, r) : -1;
             }
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -318,8 +317,8 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attn_mma_kernel(c
                 continue;
             }
             const float inv = sum_r > 0.f ? 1.f / sum_r : sum_r == 0.f ? 0.f : sum_r;
-            const int64_t row = r0 + r;
-            const size_t at = (w.first + row / a.G) * a.Hq + p.head * a.G + row % a.G;
+            const AttnWalk::Place to_row = p.place(a, r);
+            const size_t at = (size_t)to_row.token * a.Hq + to_row.head;
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + at * a.D + d;
             if (vo) *reinterpret_cast<uint32_t*>(out) = pack_bf16(y.x * inv, y.y * inv);
             else {

@@ -14,8 +14,8 @@
 // zero times those need not be zero: its values are copied row by row with cp.async, zeros for the others.  K is read
 // K-major, V MN-major (keys as K), P from TMEM.
 //
-// Roles (12 warps): 0-3 and 4-7 the softmax of the two tiles, 8 issues the products, 10 copies keys and values, 11 Q (9 has
-// nothing to do).  The products come in the order P V and next S of one tile, P V and next S of the other, so that one's run
+// Roles (12 warps): 0-3 and 4-7 the softmax of the two tiles, 8 issues the products, 10 copies keys and values, 9 and 11
+// Q.  The products come in the order P V and next S of one tile, P V and next S of the other, so that one's run
 // while the other's exponentials do.  (A thread for each tile's products, in no order between them, let both tiles fall into
 // step: products, then exponentials, 4430 cycles a step.)  P of a tile lies where its next S goes, hence the next S is issued when P
 // V is complete.  P is handed over in halves of 64 keys.
@@ -56,8 +56,8 @@ template <int NB> struct Lay {
 enum Bars {
     kFull = 0,       // [4] a slot's copies landed
     kEmpty = 4,      // [4] its products complete
-    kQFull = 8,      // Q landed
-    kQEmpty = 9,     // the piece's products complete
+    kQFull = 8,      // Q landed (2 warps)
+    kQEmpty = 9,     // the piece's products with Q complete
     kS = 10,         // [2] S complete
     kO = 12,         // [2] P V complete
     kP = 14,         // [2][2] half the keys of P written, and O rescaled before (4 warps)
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     const AttnCut cut(a, units.tiles(a));
     if (cta >= cut.ctas) return;
     if (tid == 0) {
-        for (int i = 0; i < kBars; ++i) mbar_init(&bar[i], i >= kP ? 4 : 1);
+        for (int i = 0; i < kBars; ++i) mbar_init(&bar[i], i >= kP ? 4 : i == kQFull ? 2 : 1);
         *fail = 0;
         mbar_fence_init();
     }
@@ -191,8 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         for (AttnWalk p(a, units, cut, cta); p.more(); p.next(a, units)) {
             const int rows = p.rows(a) - 128 * tile;
             if (rows <= 0) continue;                 // (the other roles leave this tile out as well)
-            const int64_t packed = p.first_row(a) + 128 * tile + row;
-            const int pos = row < rows ? p.w.len - p.w.n + (int)(packed / a.G) : -1;
+            const int pos = row < rows ? p.position(a, 128 * tile + row) : -1;
             // positions of the warp's rows, for tiles that need no mask
             const int low = __reduce_min_sync(0xffffffffu, pos), high = __reduce_max_sync(0xffffffffu, pos);
             float base = -INFINITY;                  // what scores are taken from (a score, not yet times c)
@@ -270,8 +269,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             tc_fence_after();
             const float l = (sum.x + sum.y) + (also.x + also.y);
             const bool whole = p.whole(), live = row < rows;
-            const int64_t token = p.w.first + packed / a.G;
-            const size_t at = (size_t)token * a.Hq + p.head * a.G + packed % a.G;
+            const AttnWalk::Place to_row = p.place(a, live ? 128 * tile + row : 0);
+            const size_t at = (size_t)to_row.token * a.Hq + to_row.head;
             const float inv = whole ? l > 0.f ? 1.f / l : l == 0.f ? 0.f : l : 1.f;
             float* part = a.part + p.slot(cta) * attn_part_floats(a);
             const int prow = 128 * tile + row;
@@ -333,11 +332,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 bool ok = true;
                 for (AttnWalk p(a, units, cut, cta); ok && p.more(); p.next(a, units), ++pieces) {
                     const int tiles = p.rows(a) > 128 ? 2 : 1, last = tiles - 1;
-                    // (the last piece's products are complete: Q's place was given up after them)
                     ok = wait1(kQFull, pieces & 1) && keys(g, 0);
+                    for (int tile = 0; ok && tile < tiles; ++tile) {
+                        ok = n[tile] == 0 || wait1(kO + tile, (n[tile] - 1) & 1);      // P of the last piece has been read
+                        if (ok) scores(tile, g);
+                    }
                     if (!ok) break;
-                    for (int tile = 0; tile < tiles; ++tile) scores(tile, g);
                     mma_commit(&bar[kEmpty + 2 * g % L::SLOTS]);
+                    if (p.t1 - p.t0 == 1) mma_commit(&bar[kQEmpty]);
                     for (int t = p.t0; ok && t < p.t1; ++t, ++g) {
                         const bool next = t + 1 < p.t1;
                         const uint32_t vs = (2 * g + 1) % L::SLOTS, sv = desc_lo(smem_u32(smem + L::KV + vs * L::TILE), HALF);
@@ -359,14 +361,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                                 ok = (tile || keys(g + 1, 0)) && wait1(kO + tile, n[tile] & 1);
                                 if (!ok) break;
                                 scores(tile, g + 1);
-                                if (tile == last) mma_commit(&bar[kEmpty + (2 * g + 2) % L::SLOTS]);
+                                if (tile == last) {
+                                    mma_commit(&bar[kEmpty + (2 * g + 2) % L::SLOTS]);
+                                    if (t + 2 == p.t1) mma_commit(&bar[kQEmpty]);
+                                }
                             }
                             ++n[tile];
                         }
                     }
                     if (!ok) break;
                     for (int tile = 0; tile < tiles; ++tile) ++mine[tile];
-                    mma_commit(&bar[kQEmpty]);
                 }
             }
             __syncwarp();
@@ -436,24 +440,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     }
                 }
             }
-        } else if (warp == 11) {
-            // ------------------------------------------------------------ Q
+        } else {
+            // ------------------------------------------------------------ Q, half each of warps 9 and 11
             constexpr int PER = DP / 8, EACH = 32 / PER;      // pieces of a row, rows of one round of the lanes
             const int c = lane % PER, sub = lane / PER;
             const bool column = c * 8 < a.D, vq = a.qs % 8 == 0 && reinterpret_cast<uintptr_t>(a.q) % 16 == 0;
             uint32_t pieces = 0;
             for (AttnWalk p(a, units, cut, cta); p.more(); p.next(a, units), ++pieces) {
                 if (pieces && !wait(kQEmpty, (pieces - 1) & 1)) break;
-                const int64_t r0 = p.first_row(a);
                 const int rows = p.rows(a);
 #pragma unroll 4
-                for (int i = 0; i < 256 / EACH; ++i) {
+                for (int i = warp == 9; i < 256 / EACH; i += 2) {
                     const int r = i * EACH + sub;
                     const uint32_t to = smem_u32(smem + L::Q + (r >> 7) * L::TILE) + piece(r & 127, c);
                     const bool in = r < rows && column;
-                    const int64_t row = in ? r0 + r : 0;
                     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
-                    if (in) q += (p.w.first + row / a.G) * a.qs + (int64_t)(p.head * a.G + row % a.G) * a.D + c * 8;
+                    if (in) {
+                        const AttnWalk::Place from = p.place(a, r);
+                        q += from.token * a.qs + from.head * a.D + c * 8;
+                    }
                     if (vq) {
                         cp_async16(to, q, in ? 16 : 0);
                     } else {
