@@ -9,7 +9,8 @@
 //
 // Operands: K and V lie in one ring of four 32 KB slots (K, V, K, V, ...), rows of 128 bytes in the 128-byte swizzle, put there
 // by TMA in boxes of R keys, the largest power of two that divides the page's tokens, so that a box lies in one page; a lane
-// of the copying warp looks up the page of one box and issues its copy.  Boxes without a key to read, and missing pages, lie out of
+// of the copying warp looks up the page of one box and issues its copy.  With D = 128 and R >= 8 a box holds both halves of its
+// keys' columns, 8 keys at a time (WIDE): half as many copies.  Boxes without a key to read, and missing pages, lie out of
 // the map's range, which gives zeros.  A box that a row's end (or its window's begin) cuts would bring values that are nobody's, and
 // zero times those need not be zero: its values are copied row by row with cp.async, zeros for the others.  K is read
 // K-major, V MN-major (keys as K), P from TMEM.
@@ -67,23 +68,24 @@ enum Bars {
 
 constexpr uint32_t TS = 0, TO = 256, TCOLS = 512;       // + 128 tile
 
-// (as in the state space scan: low descriptor words with the offsets added beside their use, 128-byte swizzle)
+// (as in the state space scan: low descriptor words with the offsets added beside their use, 128-byte swizzle; sbo: bytes
+// between groups of eight rows)
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | (lbo >> 4 << 16); }
-constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo) { return (sbo >> 4) | (1u << 14) | (2u << 29); }
 template <int OA, int OB>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 da, db;\n\tadd.u32 x, %1, %5;\n\tadd.u32 y, %2, %6;\n\t"
-        "mov.b64 da, {x, %7};\n\tmov.b64 db, {y, %7};\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 da, {x, %7};\n\tmov.b64 db, {y, %8};\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}\n" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(OA >> 4), "n"(OB >> 4), "r"(kDescHi));
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(OA >> 4), "n"(OB >> 4), "r"(desc_hi(1024)), "r"(hi));
 }
 template <int OB>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b32 y;\n\t.reg .b64 db;\n\tadd.u32 y, %2, %5;\n\tmov.b64 db, {y, %6};\n\t"
         "setp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}\n" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(OB >> 4), "r"(kDescHi));
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(OB >> 4), "r"(hi));
 }
 template <int N, typename F, int I = 0>
 __device__ __forceinline__ void steps(F&& f) {
@@ -117,7 +119,15 @@ __device__ __forceinline__ void tma_load_3d_to(uint32_t dst, const CUtensorMap* 
         : "memory");
 }
 
-// Byte of 16-byte piece c (of NB x 8) of row r in a tile.
+__device__ __forceinline__ void tma_load_5d_to(uint32_t dst, const CUtensorMap* map, int c3, int c4, uint64_t* mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(c3), "r"(c4), "r"(smem_u32(mbar))
+        : "memory");
+}
+
+// Byte of 16-byte piece c (of NB x 8) of row r in a tile of Q, or of keys: halves of 128 rows, or (WIDE) groups of eight rows
+// with both halves each.
 __device__ __forceinline__ uint32_t piece(int r, int c) { return (c >> 3) * HALF + (uint32_t)(r * 128 + (((c & 7) ^ (r & 7)) << 4)); }
 
 // Values that a load from TMEM has left are used after its wait: the wait alone names no register.
@@ -127,7 +137,11 @@ template <int N> __device__ __forceinline__ void landed(float* v) {
     for (int j = 0; j < N; ++j) asm volatile("" : "+f"(v[j]));
 }
 
-template <int NB>
+template <bool WIDE> __device__ __forceinline__ uint32_t key_piece(int r, int c) {
+    return WIDE ? (uint32_t)((r >> 3) * 2048 + (c >> 3) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4)) : piece(r, c);
+}
+
+template <int NB, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map, int box_log2) {
     using L = Lay<NB>;
     constexpr int DP = 64 * NB;
@@ -316,7 +330,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         if (warp == 8) {
             // ------------------------------------------------------------ products
             if (lane == 0) {
-                constexpr uint32_t idS = idesc_bf16(128, KT, 0, 0), idO = idesc_bf16(128, DP, 0, 1);
+                constexpr uint32_t idS = idesc_bf16(128, KT, 0, 0), idO = idesc_bf16(128, DP, 0, 1), hi = desc_hi(WIDE ? 2048 : 1024);
+                constexpr int STEP = WIDE ? 4096 : 2048;       // bytes of 16 keys' values in a half
                 uint32_t n[2] = {0, 0}, mine[2] = {0, 0}, g = 0, pieces = 0;     // key tiles and pieces of each query tile, and of both
                 auto keys = [&](uint32_t at, int v) { return wait1(kFull + (2 * at + v) % L::SLOTS, (2 * at + v) / L::SLOTS & 1); };
                 auto scores = [&](int tile, uint32_t at) {
@@ -325,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     tc_fence_after();
                     steps<4 * NB>([&](auto k) {
                         constexpr int o = (k >> 2) * HALF + (k & 3) * 32;
-                        mma_ss<o, o>(ts, sq, sk, idS, k > 0);
+                        mma_ss<o, WIDE ? (k >> 2) * 1024 + (k & 3) * 32 : o>(ts, sq, sk, hi, idS, k > 0);
                     });
                     mma_commit(&bar[kS + tile]);
                 };
@@ -342,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     if (p.t1 - p.t0 == 1) mma_commit(&bar[kQEmpty]);
                     for (int t = p.t0; ok && t < p.t1; ++t, ++g) {
                         const bool next = t + 1 < p.t1;
-                        const uint32_t vs = (2 * g + 1) % L::SLOTS, sv = desc_lo(smem_u32(smem + L::KV + vs * L::TILE), HALF);
+                        const uint32_t vs = (2 * g + 1) % L::SLOTS, sv = desc_lo(smem_u32(smem + L::KV + vs * L::TILE), WIDE ? 1024 : HALF);
                         ok = keys(g, 1);
 #pragma unroll 1
                         for (int tile = 0; ok && tile < tiles; ++tile) {
@@ -350,11 +365,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                             ok = wait1(kP + 2 * tile, n[tile] & 1) && (t > p.t0 || mine[tile] == 0 || wait1(kOFree + tile, (mine[tile] - 1) & 1));
                             if (!ok) break;
                             tc_fence_after();
-                            steps<KT / 32>([&](auto k) { mma_ts<k * 2048>(to, ts + 8 * k, sv, idO, t > p.t0 || k > 0); });
+                            steps<KT / 32>([&](auto k) { mma_ts<k * STEP>(to, ts + 8 * k, sv, hi, idO, t > p.t0 || k > 0); });
                             ok = wait1(kP + 2 * tile + 1, n[tile] & 1);
                             if (!ok) break;
                             tc_fence_after();
-                            steps<KT / 32>([&](auto k) { mma_ts<(k + KT / 32) * 2048>(to, ts + 8 * (k + KT / 32), sv, idO, 1); });
+                            steps<KT / 32>([&](auto k) { mma_ts<(k + KT / 32) * STEP>(to, ts + 8 * (k + KT / 32), sv, hi, idO, 1); });
                             mma_commit(&bar[kO + tile]);
                             if (tile == last) mma_commit(&bar[kEmpty + vs]);
                             if (next) {
@@ -376,7 +391,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             __syncwarp();
         } else if (warp == 10) {
             // ------------------------------------------------------------ keys and values
-            const int R = 1 << box_log2, boxes = (KT >> box_log2) * NB, nowhere = a.pages * 2 * a.Hkv;
+            constexpr int PARTS = WIDE ? 1 : NB;              // copies of a box's keys
+            const int R = 1 << box_log2, boxes = (KT >> box_log2) * PARTS, nowhere = a.pages * 2 * a.Hkv;
             uint32_t g = 0;
             bool ok = true;
             for (AttnWalk p(a, units, cut, cta); ok && p.more(); p.next(a, units)) {
@@ -390,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     return nowhere;
                 };
                 auto cut_box = [&](int key) { return (key < p.s.begin && key + R > p.s.begin) || (key < p.s.end && key + R > p.s.end); };
-                const int mine = (lane / NB) << box_log2;       // this lane's first box: its keys in a tile
+                const int mine = (lane / PARTS) << box_log2;       // this lane's first box: its keys in a tile
                 int next = look((p.s.tile0 + p.t0) * KT + mine);
                 for (int t = p.t0; ok && t < p.t1; ++t) {
                     const int k0 = (p.s.tile0 + t) * KT, first = next;
@@ -416,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                                 for (int i = lane; i < R * 8 * NB; i += 32) {
                                     const int r = i / (8 * NB), c = i % (8 * NB);
                                     const bool in = z != nowhere && key + r >= p.s.begin && key + r < p.s.end && c * 8 < a.D;
-                                    cp_async16(to + piece(key - k0 + r, c), in ? from + (int64_t)r * a.D * 2 + c * 16 : a.pool, in ? 16 : 0);
+                                    cp_async16(to + key_piece<WIDE>(key - k0 + r, c), in ? from + (int64_t)r * a.D * 2 + c * 16 : a.pool, in ? 16 : 0);
                                 }
                             }
                             if (by_row) {
@@ -426,48 +442,58 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                                 __syncwarp();
                             }
                         }
-                        if (lane == 0) mbar_expect_tx(&bar[kFull + slot], (boxes - by_row * NB) * R * 128);
+                        if (lane == 0) mbar_expect_tx(&bar[kFull + slot], ((KT >> box_log2) - by_row) * NB * R * 128);
                         __syncwarp();
 #pragma unroll 1
                         for (int i = lane; i < boxes; i += 32) {
-                            const int at = (i / NB) << box_log2, key = k0 + at;
+                            const int at = (i / PARTS) << box_log2, key = k0 + at;
                             const int z = (i < 32 ? first : look(key));
                             if (kv && R > 1 && cut_box(key)) continue;
-                            tma_load_3d_to(to + (i % NB) * HALF + at * 128, &map, (i % NB) * 64, key % a.pt, z == nowhere ? nowhere : z + kv * a.Hkv,
-                                           &bar[kFull + slot]);
+                            const int page = z == nowhere ? nowhere : z + kv * a.Hkv, in_page = key % a.pt;
+                            if constexpr (WIDE) tma_load_5d_to(to + at * 256, &map, in_page >> 3, page, &bar[kFull + slot]);
+                            else tma_load_3d_to(to + (i % NB) * HALF + at * 128, &map, (i % NB) * 64, in_page, page, &bar[kFull + slot]);
                         }
                         __syncwarp();
                     }
                 }
             }
         } else {
-            // ------------------------------------------------------------ Q, half each of warps 9 and 11
+            // ------------------------------------------------------------ Q, a tile each of warps 9 and 11
             constexpr int PER = DP / 8, EACH = 32 / PER;      // pieces of a row, rows of one round of the lanes
             const int c = lane % PER, sub = lane / PER;
             const bool column = c * 8 < a.D, vq = a.qs % 8 == 0 && reinterpret_cast<uintptr_t>(a.q) % 16 == 0;
+            const int tile = warp == 11, each_token = EACH / a.G, each_head = EACH % a.G;
+            const uint32_t sq = smem_u32(smem + L::Q + tile * L::TILE);
             uint32_t pieces = 0;
             for (AttnWalk p(a, units, cut, cta); p.more(); p.next(a, units), ++pieces) {
                 if (pieces && !wait(kQEmpty, (pieces - 1) & 1)) break;
-                const int rows = p.rows(a);
+                const int rows = p.rows(a) - 128 * tile;
+                if (rows > 0) {
+                    // (rows one after the other: no division but the first)
+                    AttnWalk::Place at = p.place(a, 128 * tile + sub);
+                    at.head -= p.head * a.G;
 #pragma unroll 4
-                for (int i = warp == 9; i < 256 / EACH; i += 2) {
-                    const int r = i * EACH + sub;
-                    const uint32_t to = smem_u32(smem + L::Q + (r >> 7) * L::TILE) + piece(r & 127, c);
-                    const bool in = r < rows && column;
-                    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
-                    if (in) {
-                        const AttnWalk::Place from = p.place(a, r);
-                        q += from.token * a.qs + from.head * a.D + c * 8;
-                    }
-                    if (vq) {
-                        cp_async16(to, q, in ? 16 : 0);
-                    } else {
-                        uint4 f = make_uint4(0, 0, 0, 0);
-                        if (in) {
-                            const unsigned short* e = reinterpret_cast<const unsigned short*>(q);
-                            f = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16, e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
+                    for (int r = sub; r < 128; r += EACH) {
+                        const bool in = r < rows && column;
+                        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
+                        if (in) q += at.token * a.qs + (p.head * a.G + at.head) * a.D + c * 8;
+                        const uint32_t to = sq + piece(r, c);
+                        if (vq) {
+                            cp_async16(to, q, in ? 16 : 0);
+                        } else {
+                            uint4 f = make_uint4(0, 0, 0, 0);
+                            if (in) {
+                                const unsigned short* e = reinterpret_cast<const unsigned short*>(q);
+                                f = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16, e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
+                            }
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(f.x), "r"(f.y), "r"(f.z), "r"(f.w) : "memory");
                         }
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(f.x), "r"(f.y), "r"(f.z), "r"(f.w) : "memory");
+                        at.token += each_token;
+                        at.head += each_head;
+                        if (at.head >= a.G) {
+                            at.head -= a.G;
+                            ++at.token;
+                        }
                     }
                 }
                 cp_commit();
@@ -492,27 +518,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     if (warp == 0) tmem_dealloc(tmem, TCOLS);
 }
 
-template <int NB> cudaError_t go(const AttnArgs& a, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<NB>::TOTAL);
+template <int NB, bool WIDE> cudaError_t go(const AttnArgs& a, int box_log2, cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<NB, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<NB>::TOTAL);
     if (e != cudaSuccess) return e;
-    int box_log2 = 0;
-    while (box_log2 < 7 && a.pt % (2 << box_log2) == 0) ++box_log2;
-    // a pool as [pages x (keys, values) x heads][page tokens][D]
     auto enc = map_encoder();
     if (!enc) return cudaErrorNotSupported;
+    // a pool as [pages x (keys, values) x heads][page tokens][D]; WIDE: [..][page tokens / 8][halves of D][8][64]
     CUtensorMap map;
-    const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.pt, (cuuint64_t)a.pages * 2 * a.Hkv};
-    const cuuint64_t strides[2] = {(cuuint64_t)a.D * 2, (cuuint64_t)a.pt * a.D * 2};
-    const cuuint32_t box[3] = {64, 1u << box_log2, 1}, es[3] = {1, 1, 1};
-    if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.pool), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    const cuuint64_t D = a.D, pt = a.pt, all = (cuuint64_t)a.pages * 2 * a.Hkv;
+    const cuuint32_t R = 1u << box_log2, es[5] = {1, 1, 1, 1, 1};
+    const cuuint64_t dims3[3] = {D, pt, all}, strides3[2] = {D * 2, pt * D * 2};
+    const cuuint32_t box3[3] = {64, R, 1};
+    const cuuint64_t dims5[5] = {64, 8, 2, pt / 8, all}, strides5[4] = {256, 128, 2048, pt * 256};
+    const cuuint32_t box5[5] = {64, 8, 2, R / 8, 1};
+    if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, WIDE ? 5 : 3, const_cast<void*>(a.pool), WIDE ? dims5 : dims3, WIDE ? strides5 : strides3,
+            WIDE ? box5 : box3, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    attn_tc_kernel<NB><<<a.ctas, kThreads, Lay<NB>::TOTAL, st>>>(a, map, box_log2);
+    attn_tc_kernel<NB, WIDE><<<a.ctas, kThreads, Lay<NB>::TOTAL, st>>>(a, map, box_log2);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t st) { return a.D > 64 ? go<2>(a, st) : go<1>(a, st); }
+cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t st) {
+    int box_log2 = 0;
+    while (box_log2 < 7 && a.pt % (2 << box_log2) == 0) ++box_log2;
+    if (a.D == 128 && box_log2 >= 3) return go<2, true>(a, box_log2, st);
+    return a.D > 64 ? go<2, false>(a, box_log2, st) : go<1, false>(a, box_log2, st);
+}
 
 }  // namespace kda
