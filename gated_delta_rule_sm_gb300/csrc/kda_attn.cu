@@ -131,6 +131,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* tmp, int64_t* 
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_constant__ AttnArgs a) {
     __shared__ int64_t tmp[32];
     const int tid = threadIdx.x;
+    cudaTriggerProgrammaticLaunchCompletion();       // the attention may be launched; it waits for this kernel's end
     bool bad = false;
     if (a.cu) {
         for (int n = tid; n < a.rows; n += kPlanThreads) bad |= a.cu[n + 1] < a.cu[n];
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
 
 // ------------------------------------------------------------------ join
 
-// A CTA takes kJoinRows rows of one item (a unit for one key head); most items have one part and are done already.  With few
+// A CTA takes some rows of one item (a unit for one key head) that several CTAs share; the others are done already.  With few
 // parts a warp takes a row; with many (a few rows over a long cache) the warps split the parts of a row, four of each
 // warp's on the way at once, since then it is their latency that counts.
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinFew = 4;
@@ -221,16 +222,35 @@ __device__ __forceinline__ void join_write(const AttnArgs& a, size_t at, const J
         if (k * 32 + lane < a.D) store_act(a.out, at * a.D + k * 32 + lane, s.o[k] * inv, a.dtype);
     if (a.lse && lane == 0) a.lse[at] = s.sum == 0.f ? -INFINITY : (base + log2f(s.sum)) * 0.6931471805599453f;
 }
+// The last unit that begins at or before tile x, by 32 units at a time (one warp).
+__device__ __forceinline__ int unit_of(const AttnArgs& a, int units, int64_t x) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = units;
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const unsigned hit = __ballot_sync(0xffffffffu, lane * step < n && a.start[lo + lane * step] * a.Hkv <= x);
+        const int k = 31 - __clz(hit | 1u);
+        n = min(step, n - k * step);
+        lo += k * step;
+    }
+    return lo;
+}
+
+// blockIdx.x + 1: a CTA of the attention whose span may begin inside an item; the first such one of an item stands for it.
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnArgs a, int rows_each) {
     __shared__ float so[kJoinWarps][256], ss[kJoinWarps];
-    const int units = *a.units, u = blockIdx.x / a.Hkv, head = blockIdx.x - u * a.Hkv;
-    if (u >= units) return;
-    const int64_t first = a.start[u], total = a.start[units] * a.Hkv;
-    const int tiles = (int)(a.start[u + 1] - first);
-    const AttnCut cut(a, total);
+    cudaGridDependencySynchronize();
+    const int units = *a.units, c1st = blockIdx.x + 1;
+    if (units <= 0) return;
+    const AttnCut cut(a, a.start[units] * a.Hkv);
+    if (c1st >= cut.ctas) return;
+    const int64_t begin = cut.begin(c1st);
+    const int u = unit_of(a, units, begin);
+    const int64_t first = a.start[u];
+    const int tiles = (int)(a.start[u + 1] - first), head = (int)((begin - first * a.Hkv) / tiles);
     const int64_t x = first * a.Hkv + (int64_t)head * tiles;
-    const int c0 = cut.owner(x), c1 = cut.owner(x + tiles - 1);
-    if (c0 == c1) return;
+    const int c0 = c1st - 1, c1 = cut.owner(x + tiles - 1);
+    if (x == begin || cut.begin(c0) > x) return;          // the item begins here; an earlier one stands for it
     const AttnRow w = attn_row(a, a.unit_row[u], false);
     const uint32_t r0 = (uint32_t)a.unit_row[a.units_most + u] * a.block;
     const int n = (int)min((uint32_t)w.n * a.G - r0, (uint32_t)a.block), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -468,8 +488,7 @@ template <typename E, int DC> cudaError_t simt_launch(const AttnArgs& a, cudaStr
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) set[dev] = true;
     }
-    attn_simt_kernel<E, DC><<<a.ctas, kSimtThreads, bytes, st>>>(a);
-    return cudaGetLastError();
+    return attn_launch(attn_simt_kernel<E, DC>, a.ctas, kSimtThreads, bytes, !a.direct, st, a);
 }
 
 // ------------------------------------------------------------------ host
@@ -635,13 +654,16 @@ kda_status kda_pages_attention(const kda_attention_dims* dims, const void* q, co
     const cudaError_t e = a.kernel == kAttnTc ? launch_attn_tc(a, stream) : a.kernel == kAttnMma ? launch_attn_mma(a, stream) : launch_attn_simt(a, stream);
     timing_post(stream);
     if (e != cudaSuccess) return KDA_ERR_CUDA;
+    // rows of a block that may exist; a CTA for each where they are few
+    const int64_t longest = (cu_seqlens ? a.tokens : a.per_row) * (int64_t)a.G;
+    const int rows = (int)(longest < a.block ? longest : a.block), each = a.block <= 32 ? 1 : 4 * kJoinWarps;
     timing_pre(stream, K_ATTN_JOIN);
-    // rows of an item that may exist; a CTA for each where they are few
-    const int64_t longest = cu_seqlens ? (int64_t)a.tokens * a.G : (int64_t)a.per_row * a.G, rows = longest < a.block ? longest : a.block;
-    const int each = a.block <= 32 ? 1 : 2 * kJoinWarps;
-    attn_join_kernel<<<dim3(a.units_most * a.Hkv, (int)((rows + each - 1) / each)), kJoinThreads, 0, stream>>>(a, each);
+    // (launched while the attention still runs; it waits for its end itself)
+    if (a.ctas > 1)
+        st = attn_launch(attn_join_kernel, dim3(a.ctas - 1, (rows + each - 1) / each), kJoinThreads, 0, true, stream, a, each) == cudaSuccess
+                 ? KDA_OK : KDA_ERR_CUDA;
     timing_post(stream);
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return st;
 }
 
 }  // extern "C"

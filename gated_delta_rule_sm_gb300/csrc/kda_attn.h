@@ -98,7 +98,9 @@ struct AttnUnits {
 // All threads of a CTA; own: [kAttnDirectRows + 1] in shared memory.  The first CTA leaves what it counted to the join.
 __device__ __forceinline__ AttnUnits attn_units(const AttnArgs& a, int64_t* own) {
     AttnUnits s;
+    cudaTriggerProgrammaticLaunchCompletion();       // the join may be launched
     if (!a.direct) {
+        cudaGridDependencySynchronize();             // (the plan)
         s.units = *a.units;
         s.start = a.start;
         return s;
@@ -209,6 +211,22 @@ __device__ __forceinline__ const char* attn_page(const AttnArgs& a, int seq, int
 
 // The kernels.  mma: bf16, D a multiple of 8, 16-byte aligned pool; blocks of 16 or 32 packed rows (16 with D above 128).
 constexpr int kAttnMmaKeys = 64;
+// Launches a kernel; early: while the one before it in the stream still runs (it begins with a wait for that one's end).
+template <typename... P, typename... A>
+cudaError_t attn_launch(void (*kernel)(P...), dim3 grid, int threads, size_t shared, bool early, cudaStream_t st, const A&... args) {
+    cudaLaunchConfig_t c = {};
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = shared;
+    c.stream = st;
+    c.attrs = &at;
+    c.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
+}
+
 cudaError_t launch_attn_mma(const AttnArgs& a, cudaStream_t st);
 // tc: bf16, D a multiple of 8 up to 128, 16-byte aligned pool; two tiles of 128 packed rows against tiles of 128 keys.
 constexpr int kAttnTcRows = 256, kAttnTcKeys = 128;

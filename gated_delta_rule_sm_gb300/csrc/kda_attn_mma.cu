@@ -333,8 +333,7 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attn_mma_kernel(c
 template <int DP, int MT> cudaError_t go(const AttnArgs& a, cudaStream_t st) {
     const cudaError_t e = cudaFuncSetAttribute(attn_mma_kernel<DP, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<DP, MT>::TOTAL);
     if (e != cudaSuccess) return e;
-    attn_mma_kernel<DP, MT><<<a.ctas, kThreads, Lay<DP, MT>::TOTAL, st>>>(a);
-    return cudaGetLastError();
+    return attn_launch(attn_mma_kernel<DP, MT>, a.ctas, kThreads, Lay<DP, MT>::TOTAL, !a.direct, st, a);
 }
 
 }  // namespace

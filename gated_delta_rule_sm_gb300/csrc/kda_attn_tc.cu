@@ -535,8 +535,7 @@ template <int NB, bool WIDE> cudaError_t go(const AttnArgs& a, int box_log2, cud
             WIDE ? box5 : box3, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    attn_tc_kernel<NB, WIDE><<<a.ctas, kThreads, Lay<NB>::TOTAL, st>>>(a, map, box_log2);
-    return cudaGetLastError();
+    return attn_launch(attn_tc_kernel<NB, WIDE>, a.ctas, kThreads, Lay<NB>::TOTAL, !a.direct, st, a, map, box_log2);
 }
 
 }  // namespace
