@@ -33,18 +33,17 @@ using namespace sm100;
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kFwdTok = 16, kFwdTile = kWarps * kFwdTok;     // tokens of a thread and of a CTA, forward
-constexpr int kBwdTok = 8, kBwdTile = kWarps * kBwdTok;      // backward; the forward's record has a state every kBwdTile tokens
+constexpr int kTok = 8, kTile = kWarps * kTok;      // tokens of a thread and of a CTA
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct GatedArgs {
-    int T, TT, C, rows, tiles, cols, planned;
+    int T, TT, C, rows, tiles, cols, planned, aligned;   // aligned: 16-byte copies of the token arrays
     int64_t xs, gs, is;                  // elements between neighbouring tokens
     const void *x, *g, *i, *dy;
     const float *a_log, *s0, *dsT;
     const int32_t* cu;
     void* y;
-    float *sT, *rec;                     // rec [ceil(TT / kBwdTile), C]: the state that enters each kBwdTile tokens
+    float *sT, *rec;                     // rec [tiles, C]: the state that enters each tile
     float *dx, *dg, *di, *da_log, *ds0;
     // workspace (planned)
     int *ticket, *ok, *flags, *first;    // flags [tiles, cols]; first [tiles]: the first row that begins at or after the tile's first token
@@ -157,26 +156,25 @@ __device__ __forceinline__ float wide_log(float g, float log2_rate) {
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(l) : "f"(1.f + ex2(t)));
     return -min_nan(ex2(log2_rate - (t > 30.f ? t : l)), 1e30f);
 }
-__device__ __forceinline__ float log_decay(float g, float sig, const Rate<float>& r) {
-    return r.wide && !(r.n >= -0.25f) ? wide_log(g, r.log2) : sig * r.n;
+template <bool WIDE> __device__ __forceinline__ float log_decay(float g, float sig, const Rate<float>& r) {
+    return WIDE && r.wide && !(r.n >= -0.25f) ? wide_log(g, r.log2) : sig * r.n;
 }
-__device__ __forceinline__ float2 log_decay(float2 g, float2 sig, const Rate<float2>& r) {
+template <bool WIDE> __device__ __forceinline__ float2 log_decay(float2 g, float2 sig, const Rate<float2>& r) {
     float2 l = mul2(sig, r.n);
-    if (r.wide) {
+    if (WIDE && r.wide) {
         if (!(r.n.x >= -0.25f)) l.x = wide_log(g.x, r.log2.x);
         if (!(r.n.y >= -0.25f)) l.y = wide_log(g.y, r.log2.y);
     }
     return l;
 }
 
-// 1 - e^l for l <= 0: the series to l^7 / 5040 down to -1/4 (its rest is below 2^-28 of the value), the exponential below
-// that, which only a wide rate can reach.
+// 1 - e^l for l <= 0.  Down to -1/4, -l times a polynomial of degree 4 for (1 - e^l) / -l (interpolated at the Chebyshev points of
+// [-1/4, 0] in 64 bits; off by 5e-9 of the value with its coefficients in fp32); below, which only a wide rate can reach,
+// the exponential.
 template <typename V> __device__ __forceinline__ V one_minus_exp(V l, bool wide) {
-    V p = vfma(l, vdup<V>(1.f / 5040.f), vdup<V>(1.f / 720.f));
-    p = vfma(p, l, vdup<V>(1.f / 120.f));
-    p = vfma(p, l, vdup<V>(1.f / 24.f));
-    p = vfma(p, l, vdup<V>(1.f / 6.f));
-    p = vfma(p, l, vdup<V>(0.5f));
+    V p = vfma(l, vdup<V>(0.007513606455177069f), vdup<V>(0.04149065539240837f));
+    p = vfma(p, l, vdup<V>(0.16665108501911163f));
+    p = vfma(p, l, vdup<V>(0.4999995231628418f));
     p = vfma(p, l, vdup<V>(1.f));
     V e = vmul(vmul(l, vdup<V>(-1.f)), p);
     if (wide) {
@@ -187,19 +185,28 @@ template <typename V> __device__ __forceinline__ V one_minus_exp(V l, bool wide)
     return e;
 }
 
-// e = 1 - a, 1 / sqrt(1 - a^2) (0 where a is 1: there the input's factor is 0 and so is the limit of the gradients'
-// a^2 log a / sqrt(1 - a^2)), and w = 1 - a^2
-template <typename V> struct Decay {
-    V e, rb, w;
-};
-template <typename V> __device__ __forceinline__ Decay<V> decay_of(V g, V sig, const Rate<V>& r) {
-    Decay<V> d;
-    d.e = one_minus_exp(log_decay(g, sig, r), r.wide);
-    d.w = vmul(d.e, vfma(d.e, vdup<V>(-1.f), vdup<V>(2.f)));
-    d.rb = vmap([](float t) { return t > 1e-36f ? rsq(t) : 0.f; }, d.w);
-    return d;
+// 1 / sqrt(1 - a^2) from w = 1 - a^2 = e (2 - e).  Where a is 1 to fp32 it stops at 1e18: the input's factor w / sqrt(w) is then 0, and
+// log a, which the gradients multiply by it, is below 1e-36.
+template <typename V> __device__ __forceinline__ V square_of(V e) { return vmul(e, vfma(e, vdup<V>(-1.f), vdup<V>(2.f))); }
+template <typename V> __device__ __forceinline__ V root_of(V w) {
+    return vmap([](float t) { return rsq(fmaxf(t, 1e-36f)); }, w);
 }
 template <typename V> __device__ __forceinline__ V keep_of(V e) { return vfma(e, vdup<V>(-1.f), vdup<V>(1.f)); }
+
+// Both gates of a token: their sigmoids, and 1 less them (e^-z times them, exact where they are close to 1).
+template <typename V> struct Gates {
+    V eg, ei, sg, si;
+};
+template <typename V> __device__ __forceinline__ Gates<V> gates_of(V g, V i) {
+    Gates<V> k;
+    k.eg = exp_neg(g);
+    k.ei = exp_neg(i);
+    const V one = vdup<V>(1.f), da = vfma(k.eg, one, one), db = vfma(k.ei, one, one);
+    const V r = vmap([](float t) { return rcp(t); }, vmul(da, db));
+    k.sg = vmul(r, db);
+    k.si = vmul(r, da);
+    return k;
+}
 
 // ------------------------------------------------------------------ rows inside a tile
 
@@ -240,10 +247,8 @@ __device__ __forceinline__ void store_release(int* p, int v) {
 
 enum Flag { kNothing = 0, kPair = 1, kState = 2 };
 
-// Called by one warp.  (The lanes' stores come before lane 0's release: __syncwarp orders them, the fence carries them to
-// the other CTAs.)
+// Called by one warp.  (__syncwarp puts the lanes' stores before lane 0's release, which covers what it has observed.)
 __device__ __forceinline__ void publish(const GatedArgs& a, int o, int col, Flag f) {
-    __threadfence();
     __syncwarp();
     if ((threadIdx.x & 31) == 0) store_release(a.flags + (size_t)o * a.cols + col, f);
 }
@@ -264,7 +269,7 @@ template <typename V> __device__ __forceinline__ V look_back(const GatedArgs& a,
                 if (lane == 0) record_error(a.status, KDA_ERR_TIMEOUT);
                 return vdup<V>(0.f);
             }
-            __nanosleep(64);
+            __nanosleep(32);
         } else if (state) {
             from = max(back - (__ffs(state) - 1), 0);
         } else {
@@ -286,7 +291,7 @@ template <typename V> __device__ __forceinline__ V look_back(const GatedArgs& a,
             }
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k)
-            if (j + k < o) s = join(P[k], s, h[k]);
+            if (j + k < o) s = vfma(P[k], s, h[k]);
     }
     return s;
 }
@@ -309,7 +314,7 @@ __device__ __forceinline__ V join_chain(const GatedArgs& a, int o, int col, int 
     }
     publish(a, o, col, kPair);
     const V s = look_back<V>(a, o, col, c, in);
-    if (in) vstore(leaving, join(P, s, h));
+    if (in) vstore(leaving, vfma(P, s, h));
     publish(a, o, col, kState);
     return s;
 }
@@ -324,7 +329,8 @@ __device__ __forceinline__ int take_ticket(const GatedArgs& a, int* slot) {
 
 // Clears the counter and the flags, checks the offsets, finds each tile's first row, and passes the states of rows without
 // tokens through (of all rows where the offsets break the contract).
-__global__ void __launch_bounds__(kThreads) gated_plan_kernel(GatedArgs a, int tile_tokens, const float* from, float* to) {
+__global__ void __launch_bounds__(kThreads) gated_plan_kernel(GatedArgs a, const float* from, float* to) {
+    cudaTriggerProgrammaticLaunchCompletion();       // the pass may be launched; it waits for this kernel's end
     bool bad = false;
     if (a.cu) {
         for (int n = threadIdx.x; n < a.rows; n += kThreads) bad |= a.cu[n + 1] < a.cu[n];
@@ -343,7 +349,7 @@ __global__ void __launch_bounds__(kThreads) gated_plan_kernel(GatedArgs a, int t
         int lo = 0, hi = a.rows;          // (cu[rows] = TT is past every tile's first token)
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
-            if (a.cu[mid] >= k * tile_tokens) hi = mid; else lo = mid + 1;
+            if (a.cu[mid] >= k * kTile) hi = mid; else lo = mid + 1;
         }
         a.first[k] = lo;
     }
@@ -354,237 +360,313 @@ __global__ void __launch_bounds__(kThreads) gated_plan_kernel(GatedArgs a, int t
                     to[(size_t)n * a.C + c] = from ? from[(size_t)n * a.C + c] : 0.f;
 }
 
+// What a thread has of a tile: its channels, and where its tokens lie.
+struct Spot {
+    int tile, col, warp, lane, c, t0, tb, n;      // c: first channel; tb, n: first token and how many there are
+    bool in;
+};
+template <int VEC> __device__ __forceinline__ Spot spot_of(const GatedArgs& a, int tile, int col) {
+    Spot s;
+    s.tile = tile;
+    s.col = col;
+    s.warp = threadIdx.x >> 5;
+    s.lane = threadIdx.x & 31;
+    s.c = (col * 32 + s.lane) * VEC;
+    s.in = s.c < a.C;
+    s.t0 = tile * kTile;
+    s.tb = s.t0 + s.warp * kTok;
+    s.n = s.in ? max(0, min(kTok, a.TT - s.tb)) : 0;
+    return s;
+}
+// A [tokens, C] array's elements of the tile, a token's 32 lanes side by side as the threads will read them.
+template <typename E, int VEC> using Plane = Raw<E, VEC>[kTok][kThreads];
+template <int BYTES> __device__ __forceinline__ void copy_async(void* dst, const void* src) {
+    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copies_landed() {
+    asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+}
+// Whole tiles of arrays that allow it move 16 bytes at a time; otherwise a thread brings its own elements.  (The tile's base is one for
+// the CTA; an offset from it fits 32 bits.)
+template <typename E, int VEC>
+__device__ __forceinline__ void load_plane(const void* p, int64_t stride, const Spot& s, bool whole, bool aligned, Plane<E, VEC>& to) {
+    const E* base = static_cast<const E*>(p) + s.t0 * stride;
+    const uint32_t step = (uint32_t)stride;
+    if (sizeof(Raw<E, VEC>) == 4 && whole && aligned) {
+        constexpr int PER = 128 / 16;        // pieces of a token's 32 lanes
+#pragma unroll
+        for (int i = 0; i < kTile * PER / kThreads; ++i) {
+            const int id = i * kThreads + threadIdx.x, token = id / PER, piece = id % PER;
+            copy_async<16>(&to[token % kTok][token / kTok * 32 + piece * 4], base + (token * step + s.col * 32 * VEC + piece * (int)(16 / sizeof(E))));
+        }
+        return;
+    }
+    const uint32_t at = s.warp * kTok * step + s.c;
+#pragma unroll
+    for (int k = 0; k < kTok; ++k) {
+        Raw<E, VEC>& r = to[k][threadIdx.x];
+        if (k >= s.n) r.zero();
+        else if constexpr (sizeof(Raw<E, VEC>) == 4) copy_async<4>(&r, base + (at + k * step));
+        else r.load(base, at + k * step);
+    }
+}
+
+// Whether every thread of the CTA has all its tokens and channels.
+template <int VEC> __device__ __forceinline__ bool whole_tile(const GatedArgs& a, const Spot& s) {
+    return s.t0 + kTile <= a.TT && (s.col + 1) * 32 * VEC <= a.C;
+}
+
 // ------------------------------------------------------------------ forward
 
-template <typename E, int VEC>
-__global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(const __grid_constant__ GatedArgs a) {
+template <typename E, int VEC> struct FwdShared {
     using V = Val<VEC>;
-    using R = Raw<E, VEC>;
-    __shared__ Edges<kFwdTile> edges;
-    __shared__ V sp[kWarps][32], sh[kWarps][32], senter[32];
-    __shared__ int slot;
-    const int idx = take_ticket(a, &slot), tile = idx / a.cols, col = idx - tile * a.cols;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = (col * 32 + lane) * VEC;
-    const bool in = c < a.C;
-    const int t0 = tile * kFwdTile, tb = t0 + warp * kFwdTok;
-    const int n = in ? max(0, min(kFwdTok, a.TT - tb)) : 0;
-    R rx[kFwdTok], rg[kFwdTok], ri[kFwdTok];
-#pragma unroll
-    for (int k = 0; k < kFwdTok; ++k)
-        if (k < n) {
-            rx[k].load(a.x, (size_t)(tb + k) * a.xs + c);
-            rg[k].load(a.g, (size_t)(tb + k) * a.gs + c);
-            ri[k].load(a.i, (size_t)(tb + k) * a.is + c);
-        } else {
-            rx[k].zero();
-            rg[k].zero();
-            ri[k].zero();
-        }
-    if (a.planned && !*a.ok) return;
-    const bool split = find_edges(a, t0, tile, edges);
-    const Rate<V> rate = rate_of<V>(a.a_log, c, in);
-    auto begins_at = [&](int k) { return split ? edges.first[warp * kFwdTok + k] : -1; };
+    Plane<E, VEC> x, g, i;
+    Edges<kTile> edges;
+    V sp[kWarps][32], sh[kWarps][32], senter[32];
+    int slot;
+};
+
+// EDGE: the tile has rows that begin or end in it, tokens or channels past the last, or a rate above 1/4.
+template <typename E, int VEC, bool EDGE>
+__device__ __forceinline__ void forward_tile(const GatedArgs& a, const Spot& s, FwdShared<E, VEC>& m_, bool split, const Rate<Val<VEC>>& rate) {
+    using V = Val<VEC>;
+    const Edges<kTile>& edges = m_.edges;
+    auto &sp = m_.sp, &sh = m_.sh;
+    auto& senter = m_.senter;
+    const int tid = threadIdx.x;
+    auto begins_at = [&](int k) { return EDGE && split ? edges.first[s.warp * kTok + k] : -1; };
     // a token as h -> ka h + kb; where a row begins the state is the row's own, and ka is 0
-    V ka[kFwdTok], kb[kFwdTok], P = vdup<V>(1.f), h = vdup<V>(0.f);
+    V ka[kTok], kb[kTok], P, h;
 #pragma unroll
-    for (int k = 0; k < kFwdTok; ++k) {
-        const V da = vfma(exp_neg(rg[k].get()), vdup<V>(1.f), vdup<V>(1.f)), db = vfma(exp_neg(ri[k].get()), vdup<V>(1.f), vdup<V>(1.f));
-        const V r = vmap([](float t) { return rcp(t); }, vmul(da, db));
-        const Decay<V> d = decay_of(rg[k].get(), vmul(r, db), rate);
-        ka[k] = keep_of(d.e);
-        kb[k] = vmul(vmul(vmul(d.w, d.rb), vmul(r, da)), rx[k].get());
-        if (k >= n) {
+    for (int k = 0; k < kTok; ++k) {
+        const V g = m_.g[k][tid].get();
+        const Gates<V> z = gates_of(g, m_.i[k][tid].get());
+        const V e = one_minus_exp(log_decay<EDGE>(g, z.sg, rate), EDGE && rate.wide), w = square_of(e);
+        ka[k] = keep_of(e);
+        kb[k] = vmul(vmul(w, root_of(w)), vmul(z.si, m_.x[k][tid].get()));
+        if (EDGE && k >= s.n) {
             ka[k] = vdup<V>(1.f);
             kb[k] = vdup<V>(0.f);
-        } else if (begins_at(k) >= 0) {
-            if (a.s0) kb[k] = vfma(ka[k], vload<V>(a.s0 + (size_t)begins_at(k) * a.C + c), kb[k]);
-            P = h = ka[k] = vdup<V>(0.f);
         }
-        P = vmul(P, ka[k]);
-        h = vfma(ka[k], h, kb[k]);
+        const bool begins = begins_at(k) >= 0;
+        if (EDGE && begins) {
+            if (a.s0) kb[k] = vfma(ka[k], vload<V>(a.s0 + (size_t)begins_at(k) * a.C + s.c), kb[k]);
+            ka[k] = vdup<V>(0.f);
+        }
+        if (k == 0 || (EDGE && begins)) {
+            P = ka[k];
+            h = kb[k];
+        } else {
+            P = vmul(P, ka[k]);
+            h = vfma(ka[k], h, kb[k]);
+        }
     }
-    sp[warp][lane] = P;
-    sh[warp][lane] = h;
+    sp[s.warp][s.lane] = P;
+    sh[s.warp][s.lane] = h;
     bool begins = false;
-    if (split)
-        for (int k = lane; k < kFwdTile; k += 32) begins |= edges.first[k] >= 0;
-    begins = __any_sync(0xffffffffu, begins);
+    if (EDGE && split)
+        for (int k = s.lane; k < kTile; k += 32) begins |= edges.first[k] >= 0;
+    if (EDGE) begins = __any_sync(0xffffffffu, begins);
     __syncthreads();
-    if (warp == 0) {
-        P = vdup<V>(1.f);
-        h = vdup<V>(0.f);
+    auto over = [](V P, V s, V h) { return EDGE ? join(P, s, h) : vfma(P, s, h); };
+    if (s.warp == 0) {
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            P = join(sp[w][lane], P, vdup<V>(0.f));
-            h = join(sp[w][lane], h, sh[w][lane]);
+        for (int w = 1; w < kWarps; ++w) {
+            P = over(sp[w][s.lane], P, vdup<V>(0.f));
+            h = over(sp[w][s.lane], h, sh[w][s.lane]);
         }
-        senter[lane] = join_chain<V>(a, tile, col, c, in, P, h, begins, edges.first[0] < 0);
+        h = join_chain<V>(a, s.tile, s.col, s.c, s.in, P, h, EDGE && begins, !EDGE || edges.first[0] < 0);
+        senter[s.lane] = h;
+        if (a.rec && s.in) vstore(a.rec + (size_t)s.tile * a.C + s.c, h);
     }
     __syncthreads();
-    h = senter[lane];
-    for (int w = 0; w < warp; ++w) h = join(sp[w][lane], h, sh[w][lane]);
-    if (a.rec && n > 0 && warp * kFwdTok % kBwdTile == 0) vstore(a.rec + (size_t)(tb / kBwdTile) * a.C + c, h);
+    h = senter[s.lane];
+    for (int w = 0; w < s.warp; ++w) h = over(sp[w][s.lane], h, sh[w][s.lane]);
+    E* y = static_cast<E*>(a.y) + (size_t)s.t0 * a.C;
+    const uint32_t at = s.warp * kTok * (uint32_t)a.C + s.c;
 #pragma unroll
-    for (int k = 0; k < kFwdTok; ++k)
-        if (k < n) {
-            h = begins_at(k) >= 0 ? kb[k] : vfma(ka[k], h, kb[k]);
-            if (a.y) R::store(a.y, (size_t)(tb + k) * a.C + c, h);
-            if (split && a.sT && edges.last[warp * kFwdTok + k] >= 0)
-                vstore(a.sT + (size_t)edges.last[warp * kFwdTok + k] * a.C + c, h);
+    for (int k = 0; k < kTok; ++k)
+        if (!EDGE || k < s.n) {
+            h = EDGE && begins_at(k) >= 0 ? kb[k] : vfma(ka[k], h, kb[k]);
+            if (a.y) Raw<E, VEC>::store(y, at + k * (uint32_t)a.C, h);
+            if (EDGE && split && a.sT && edges.last[s.warp * kTok + k] >= 0)
+                vstore(a.sT + (size_t)edges.last[s.warp * kTok + k] * a.C + s.c, h);
         }
+}
+
+// With four CTAs on an SM their phases (loads, gates, the wait for the state, stores) overlap.
+template <typename E, int VEC>
+__global__ void __launch_bounds__(kThreads, 4) gated_fwd_kernel(const __grid_constant__ GatedArgs a) {
+    __shared__ __align__(16) FwdShared<E, VEC> m;
+    cudaGridDependencySynchronize();
+    const int idx = take_ticket(a, &m.slot), tile = idx / a.cols;
+    const Spot s = spot_of<VEC>(a, tile, idx - tile * a.cols);
+    const bool whole = whole_tile<VEC>(a, s);
+    load_plane<E, VEC>(a.x, a.xs, s, whole, a.aligned, m.x);
+    load_plane<E, VEC>(a.g, a.gs, s, whole, a.aligned, m.g);
+    load_plane<E, VEC>(a.i, a.is, s, whole, a.aligned, m.i);
+    const Rate<Val<VEC>> rate = rate_of<Val<VEC>>(a.a_log, s.c, s.in);
+    const bool go = !a.planned || *a.ok, split = go && find_edges(a, s.t0, tile, m.edges);
+    copies_landed();
+    if (!go) return;
+    if (whole && !split && !rate.wide) forward_tile<E, VEC, false>(a, s, m, split, rate);
+    else forward_tile<E, VEC, true>(a, s, m, split, rate);
 }
 
 // ------------------------------------------------------------------ backward
 
-template <typename E, int VEC>
-__global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(const __grid_constant__ GatedArgs a) {
+// The gates are formed twice, before and after the chain: keeping them in between would halve the number of CTAs.
+template <typename E, int VEC> struct BwdShared {
     using V = Val<VEC>;
-    using R = Raw<E, VEC>;
-    constexpr int N = kBwdTok;
-    __shared__ Edges<kBwdTile> edges;
-    __shared__ V sp[kWarps][32], sh[kWarps][32], sq[kWarps][32], sm[kWarps][32], senter[32];
-    __shared__ int slot;
-    const int idx = take_ticket(a, &slot), o = idx / a.cols, col = idx - o * a.cols, tile = a.tiles - 1 - o;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = (col * 32 + lane) * VEC;
-    const bool in = c < a.C;
-    const int t0 = tile * kBwdTile, tb = t0 + warp * N;
-    const int n = in ? max(0, min(N, a.TT - tb)) : 0;
-    R rx[N], rg[N], ri[N], rd[N];
-#pragma unroll
-    for (int k = 0; k < N; ++k)
-        if (k < n) {
-            rx[k].load(a.x, (size_t)(tb + k) * a.xs + c);
-            rg[k].load(a.g, (size_t)(tb + k) * a.gs + c);
-            ri[k].load(a.i, (size_t)(tb + k) * a.is + c);
-            rd[k].load(a.dy, (size_t)(tb + k) * a.C + c);
-        } else {
-            rx[k].zero();
-            rg[k].zero();
-            ri[k].zero();
-            rd[k].zero();
-        }
-    if (a.planned && !*a.ok) return;
-    const bool split = find_edges(a, t0, tile, edges);
-    auto begins_at = [&](int k) { return split ? edges.first[warp * N + k] : -1; };
-    auto ends_at = [&](int k) { return split ? edges.last[warp * N + k] : -1; };
-    const Rate<V> rate = rate_of<V>(a.a_log, c, in);
-    // the forward's runs, from the first token on
-    V eg[N], ei[N], e[N], rb[N], P = vdup<V>(1.f), h = vdup<V>(0.f);
+    Plane<E, VEC> x, g, i, dy;
+    Edges<kTile> edges;
+    V sp[kWarps][32], sh[kWarps][32], sq[kWarps][32], sm[kWarps][32], senter[32];
+    V e[kTok][kThreads], b[kTok][kThreads];       // e = 1 - a; the inputs, then the states before the tokens
+    int slot;
+};
+
+template <typename E, int VEC, bool EDGE>
+__device__ __forceinline__ void backward_tile(const GatedArgs& a, const Spot& s, int o, BwdShared<E, VEC>& m_, bool split, const Rate<Val<VEC>>& rate) {
+    using V = Val<VEC>;
+    const int tid = threadIdx.x, warp = s.warp, lane = s.lane, c = s.c;
+    auto begins_at = [&](int k) { return EDGE && split ? m_.edges.first[warp * kTok + k] : -1; };
+    auto ends_at = [&](int k) { return EDGE && split ? m_.edges.last[warp * kTok + k] : -1; };
+    auto row_of = [&](const float* p, int row) { return p ? vload<V>(p + (size_t)row * a.C + c) : vdup<V>(0.f); };
+    auto over = [](V P, V s, V h) { return EDGE ? join(P, s, h) : vfma(P, s, h); };
     const V one = vdup<V>(1.f);
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-        eg[k] = exp_neg(rg[k].get());
-        ei[k] = exp_neg(ri[k].get());
-        const V da = vfma(eg[k], one, one), db = vfma(ei[k], one, one), r = vmap([](float t) { return rcp(t); }, vmul(da, db));
-        const Decay<V> d = decay_of(rg[k].get(), vmul(r, db), rate);
-        e[k] = d.e;
-        rb[k] = d.rb;
-        if (k >= n) {
-            e[k] = vdup<V>(0.f);
-            rb[k] = vdup<V>(0.f);
-        } else if (begins_at(k) >= 0) {
+    // the forward's runs, from the first token on
+    V P = one, h = vdup<V>(0.f);
+#pragma unroll 4
+    for (int k = 0; k < kTok; ++k) {
+        const V g = m_.g[k][tid].get();
+        const Gates<V> z = gates_of(g, m_.i[k][tid].get());
+        V e = one_minus_exp(log_decay<EDGE>(g, z.sg, rate), EDGE && rate.wide);
+        if (EDGE && k >= s.n) e = vdup<V>(0.f);
+        const V w = square_of(e), b = vmul(vmul(w, root_of(w)), vmul(z.si, m_.x[k][tid].get())), ka = keep_of(e);
+        if (EDGE && begins_at(k) >= 0) {
             P = vdup<V>(0.f);
-            h = a.s0 ? vload<V>(a.s0 + (size_t)begins_at(k) * a.C + c) : vdup<V>(0.f);
+            h = row_of(a.s0, begins_at(k));
         }
-        const V ka = keep_of(e[k]);
         P = vmul(P, ka);
-        h = vfma(ka, h, vmul(vmul(vmul(d.w, rb[k]), vmul(r, da)), rx[k].get()));
+        h = vfma(ka, h, b);
+        m_.e[k][tid] = e;
+        m_.b[k][tid] = b;
     }
-    sp[warp][lane] = P;
-    sh[warp][lane] = h;
+    m_.sp[warp][lane] = P;
+    m_.sh[warp][lane] = h;
     // the gradient's, from the last
     P = one;
     V m = vdup<V>(0.f);
-#pragma unroll
-    for (int k = N - 1; k >= 0; --k) {
-        if (k < n && ends_at(k) >= 0) {
+#pragma unroll 4
+    for (int k = kTok - 1; k >= 0; --k) {
+        if (EDGE && k < s.n && ends_at(k) >= 0) {
             P = vdup<V>(0.f);
-            m = a.dsT ? vload<V>(a.dsT + (size_t)ends_at(k) * a.C + c) : vdup<V>(0.f);
+            m = row_of(a.dsT, ends_at(k));
         }
-        const V ka = keep_of(e[k]);
+        const V ka = keep_of(m_.e[k][tid]);
         P = vmul(P, ka);
-        m = vmul(ka, vfma(rd[k].get(), one, m));
+        m = vmul(ka, vfma(m_.dy[k][tid].get(), one, m));
     }
-    sq[warp][lane] = P;
-    sm[warp][lane] = m;
+    m_.sq[warp][lane] = P;
+    m_.sm[warp][lane] = m;
     bool ends = false;
-    if (split)
-        for (int k = lane; k < kBwdTile; k += 32) ends |= edges.last[k] >= 0;
-    ends = __any_sync(0xffffffffu, ends);
+    if (EDGE && split)
+        for (int k = lane; k < kTile; k += 32) ends |= m_.edges.last[k] >= 0;
+    if (EDGE) ends = __any_sync(0xffffffffu, ends);
     __syncthreads();
     if (warp == 0) {
-        P = one;
-        m = vdup<V>(0.f);
+        P = m_.sq[kWarps - 1][lane];
+        m = m_.sm[kWarps - 1][lane];
 #pragma unroll
-        for (int w = kWarps - 1; w >= 0; --w) {
-            P = join(sq[w][lane], P, vdup<V>(0.f));
-            m = join(sq[w][lane], m, sm[w][lane]);
+        for (int w = kWarps - 2; w >= 0; --w) {
+            P = over(m_.sq[w][lane], P, vdup<V>(0.f));
+            m = over(m_.sq[w][lane], m, m_.sm[w][lane]);
         }
-        senter[lane] = join_chain<V>(a, o, col, c, in, P, m, ends, edges.last[min(kBwdTile, a.TT - t0) - 1] < 0);
+        m_.senter[lane] = join_chain<V>(a, o, s.col, c, s.in, P, m, EDGE && ends, !EDGE || m_.edges.last[min(kTile, a.TT - s.t0) - 1] < 0);
     }
     // meanwhile the states before the tokens
-    auto input = [&](int k) {      // sqrt(1 - a^2) sigmoid(i) x
-        const V da = vfma(eg[k], one, one), db = vfma(ei[k], one, one), r = vmap([](float t) { return rcp(t); }, vmul(da, db));
-        const V w = vmul(e[k], vfma(e[k], vdup<V>(-1.f), vdup<V>(2.f)));
-        return vmul(vmul(vmul(w, rb[k]), vmul(r, da)), rx[k].get());
-    };
-    h = in ? vload<V>(a.rec + (size_t)tile * a.C + c) : vdup<V>(0.f);
-    for (int w = 0; w < warp; ++w) h = join(sp[w][lane], h, sh[w][lane]);
-    V before[N];
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-        if (k < n && begins_at(k) >= 0) h = a.s0 ? vload<V>(a.s0 + (size_t)begins_at(k) * a.C + c) : vdup<V>(0.f);
-        before[k] = h;
-        h = vfma(keep_of(e[k]), h, input(k));
+    h = s.in ? vload<V>(a.rec + (size_t)s.tile * a.C + c) : vdup<V>(0.f);
+    for (int w = 0; w < warp; ++w) h = over(m_.sp[w][lane], h, m_.sh[w][lane]);
+#pragma unroll 4
+    for (int k = 0; k < kTok; ++k) {
+        if (EDGE && k < s.n && begins_at(k) >= 0) h = row_of(a.s0, begins_at(k));
+        const V b = m_.b[k][tid];
+        m_.b[k][tid] = h;
+        h = vfma(keep_of(m_.e[k][tid]), h, b);
     }
     __syncthreads();
-    m = senter[lane];
-    for (int w = kWarps - 1; w > warp; --w) m = join(sq[w][lane], m, sm[w][lane]);
+    m = m_.senter[lane];
+    for (int w = kWarps - 1; w > warp; --w) m = over(m_.sq[w][lane], m, m_.sm[w][lane]);
     V dlog = vdup<V>(0.f);
-#pragma unroll
-    for (int k = N - 1; k >= 0; --k)
-        if (k < n) {
-            if (ends_at(k) >= 0) m = a.dsT ? vload<V>(a.dsT + (size_t)ends_at(k) * a.C + c) : vdup<V>(0.f);
-            const V da = vfma(eg[k], one, one), db = vfma(ei[k], one, one), r = vmap([](float t) { return rcp(t); }, vmul(da, db));
-            const V sg = vmul(r, db), si = vmul(r, da), ka = keep_of(e[k]);
-            const V w = vmul(e[k], vfma(e[k], vdup<V>(-1.f), vdup<V>(2.f)));
-            const V dh = vfma(rd[k].get(), one, m);                  // the gradient of h_t
+    const size_t base = (size_t)s.t0 * a.C;
+    float *dx = a.dx + base, *dg = a.dg + base, *di = a.di + base;
+    const uint32_t at = warp * kTok * (uint32_t)a.C + c;
+#pragma unroll 4
+    for (int k = kTok - 1; k >= 0; --k)
+        if (!EDGE || k < s.n) {
+            if (EDGE && ends_at(k) >= 0) m = row_of(a.dsT, ends_at(k));
+            const V g = m_.g[k][tid].get();
+            const Gates<V> z = gates_of(g, m_.i[k][tid].get());
+            const V e = m_.e[k][tid], w = square_of(e), root = root_of(w), ka = keep_of(e);
+            const V dh = vfma(m_.dy[k][tid].get(), one, m);                  // the gradient of h_t
             m = vmul(ka, dh);
-            if (begins_at(k) >= 0 && a.ds0) vstore(a.ds0 + (size_t)begins_at(k) * a.C + c, m);
-            const V u = vmul(si, rx[k].get()), du = vmul(dh, vmul(w, rb[k]));
+            if (EDGE && begins_at(k) >= 0 && a.ds0) vstore(a.ds0 + (size_t)begins_at(k) * a.C + c, m);
+            const V u = vmul(z.si, m_.x[k][tid].get()), du = vmul(dh, vmul(w, root));
             // of log a: a (h_{t-1} - u a / sqrt(1 - a^2)) times that of h_t; then times log a for a_log, and 1 - sigmoid(g) for g
-            const V dl = vmul(vmul(m, vfma(vmul(u, vdup<V>(-1.f)), vmul(ka, rb[k]), before[k])), log_decay(rg[k].get(), sg, rate));
+            const V dl = vmul(vmul(m, vfma(vmul(u, vdup<V>(-1.f)), vmul(ka, root), m_.b[k][tid])), log_decay<EDGE>(g, z.sg, rate));
             dlog = vfma(dl, one, dlog);
-            const size_t at = (size_t)(tb + k) * a.C + c;
-            vstore_stream(a.dx + at, vmul(du, si));
-            vstore_stream(a.dg + at, vmul(dl, vmul(eg[k], sg)));
-            vstore_stream(a.di + at, vmul(vmul(du, u), vmul(ei[k], si)));
+            const uint32_t to = at + k * (uint32_t)a.C;
+            vstore_stream(dx + to, vmul(du, z.si));
+            vstore_stream(dg + to, vmul(dl, vmul(z.eg, z.sg)));
+            vstore_stream(di + to, vmul(vmul(du, u), vmul(z.ei, z.si)));
         }
     __syncthreads();
-    sp[warp][lane] = dlog;
+    m_.sp[warp][lane] = dlog;
     __syncthreads();
-    if (warp == 0 && in) {
-        dlog = sp[0][lane];
+    if (warp == 0 && s.in) {
+        dlog = m_.sp[0][lane];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) dlog = vfma(sp[w][lane], one, dlog);
-        vstore(a.part + (size_t)tile * a.C + c, dlog);
+        for (int w = 1; w < kWarps; ++w) dlog = vfma(m_.sp[w][lane], one, dlog);
+        vstore(a.part + (size_t)s.tile * a.C + c, dlog);
     }
 }
 
+template <typename E, int VEC>
+__global__ void __launch_bounds__(kThreads, 3) gated_bwd_kernel(const __grid_constant__ GatedArgs a) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    BwdShared<E, VEC>& m = *reinterpret_cast<BwdShared<E, VEC>*>(smem);
+    cudaGridDependencySynchronize();
+    const int idx = take_ticket(a, &m.slot), o = idx / a.cols, tile = a.tiles - 1 - o;
+    const Spot s = spot_of<VEC>(a, tile, idx - o * a.cols);
+    const bool whole = whole_tile<VEC>(a, s);
+    load_plane<E, VEC>(a.x, a.xs, s, whole, a.aligned, m.x);
+    load_plane<E, VEC>(a.g, a.gs, s, whole, a.aligned, m.g);
+    load_plane<E, VEC>(a.i, a.is, s, whole, a.aligned, m.i);
+    load_plane<E, VEC>(a.dy, a.C, s, whole, a.aligned, m.dy);
+    const Rate<Val<VEC>> rate = rate_of<Val<VEC>>(a.a_log, s.c, s.in);
+    const bool go = !a.planned || *a.ok, split = go && find_edges(a, s.t0, tile, m.edges);
+    copies_landed();
+    if (!go) return;
+    if (whole && !split && !rate.wide) backward_tile<E, VEC, false>(a, s, o, m, split, rate);
+    else backward_tile<E, VEC, true>(a, s, o, m, split, rate);
+}
+
 // da_log: the tiles' parts in a fixed order, 32 channels to a CTA.
-__global__ void __launch_bounds__(kThreads) gated_reduce_kernel(const __grid_constant__ GatedArgs a) {
-    __shared__ float s[kWarps][32];
+constexpr int kReduceWarps = 32;
+__global__ void __launch_bounds__(kReduceWarps * 32) gated_reduce_kernel(const __grid_constant__ GatedArgs a) {
+    __shared__ float s[kReduceWarps][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
+    cudaGridDependencySynchronize();
     float t = 0.f;
     if (c < a.C && (!a.planned || *a.ok))
-        for (int k = warp; k < a.tiles; k += kWarps) t += a.part[(size_t)k * a.C + c];
+        for (int k = warp; k < a.tiles; k += kReduceWarps) t += a.part[(size_t)k * a.C + c];
     s[warp][lane] = t;
     __syncthreads();
     if (warp || c >= a.C) return;
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) t += s[w][lane];
+    for (int w = 1; w < kReduceWarps; ++w) t += s[w][lane];
     a.da_log[c] = t;
 }
 
@@ -624,10 +706,9 @@ __global__ void __launch_bounds__(kStepThreads) gated_step_kernel(const __grid_c
     ri.load(a.i, (size_t)b * a.is + c);
     const V old = vload<V>(a.s_in + (size_t)slot * a.C + c);
     const Rate<V> rate = rate_of<V>(a.a_log, c, true);
-    const V one = vdup<V>(1.f), da = vfma(exp_neg(rg.get()), one, one), db = vfma(exp_neg(ri.get()), one, one);
-    const V r = vmap([](float t) { return rcp(t); }, vmul(da, db));
-    const Decay<V> d = decay_of(rg.get(), vmul(r, db), rate);
-    const V h = vfma(keep_of(d.e), old, vmul(vmul(vmul(d.w, d.rb), vmul(r, da)), rx.get()));
+    const Gates<V> z = gates_of(rg.get(), ri.get());
+    const V e = one_minus_exp(log_decay<true>(rg.get(), z.sg, rate), rate.wide), w = square_of(e);
+    const V h = vfma(keep_of(e), old, vmul(vmul(w, root_of(w)), vmul(z.si, rx.get())));
     vstore(a.s_out + (size_t)slot * a.C + c, h);
     R::store(a.y, (size_t)b * a.C + c, h);
 }
@@ -654,16 +735,16 @@ kda_status gated_check(const kda_gated_dims* d, bool varlen, Shape* s) {
     for (int64_t st : {s->xs, s->gs, s->is})
         if (s->TT > 1 && st > (1LL << 40) / s->TT) return KDA_ERR_UNSUPPORTED;
     // (tiles x columns and the workspace's indices)
-    if ((int64_t)((s->TT + kBwdTile - 1) / kBwdTile) * ((s->C + 31) / 32) > (1LL << 30)) return KDA_ERR_UNSUPPORTED;
+    if ((int64_t)((s->TT + kTile - 1) / kTile) * ((s->C + 31) / 32) > (1LL << 30)) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
-size_t gated_record_bytes(const Shape& s) { return (size_t)((s.TT + kBwdTile - 1) / kBwdTile) * s.C * 4; }
+size_t gated_record_bytes(const Shape& s) { return (size_t)((s.TT + kTile - 1) / kTile) * s.C * 4; }
 
-// Workspace of one pass over tiles of `tile` tokens; fills the views where ws is given.
-size_t gated_layout(const Shape& s, int tile, bool reduce, char* ws, GatedArgs* a) {
-    const size_t tiles = (s.TT + tile - 1) / tile, most = (s.C + 31) / 32;
+// Workspace of one pass; fills the views where ws is given.
+size_t gated_layout(const Shape& s, bool reduce, char* ws, GatedArgs* a) {
+    const size_t tiles = (s.TT + kTile - 1) / kTile, most = (s.C + 31) / 32;
     size_t o = 0;
     auto take = [&](size_t n) {
         char* p = ws ? ws + o : nullptr;
@@ -697,6 +778,14 @@ bool pairs_ok(const Shape& s, std::initializer_list<const void*> acts, std::init
     return true;
 }
 
+bool rows16(const Shape& s, std::initializer_list<const void*> acts) {
+    for (const void* p : acts)
+        if (reinterpret_cast<uintptr_t>(p) % 16) return false;
+    for (int64_t st : {s.xs, s.gs, s.is, (int64_t)s.C})
+        if (st * s.es % 16) return false;
+    return true;
+}
+
 GatedArgs gated_args(const Shape& s, const void* x, const void* g, const void* i, const float* a_log, const int32_t* cu, const float* s0) {
     GatedArgs a;
     memset(&a, 0, sizeof(a));
@@ -705,29 +794,46 @@ GatedArgs gated_args(const Shape& s, const void* x, const void* g, const void* i
     return a;
 }
 
+// early: while the launch before it in the stream still runs (the kernels begin with a wait for that one's end).
+cudaError_t gated_launch(void (*kernel)(GatedArgs), int ctas, int threads, size_t shared, bool early, const GatedArgs& a, cudaStream_t st) {
+    if (shared) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t c = {};
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    c.gridDim = dim3(ctas);
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = shared;
+    c.stream = st;
+    c.attrs = &at;
+    c.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&c, kernel, a);
+}
+
 // The plan where the call has more than one tile or packed documents; from, to: the states that pass through.
-cudaError_t gated_begin(GatedArgs& a, int tile, int vec, const float* from, float* to, cudaStream_t st) {
-    a.tiles = (a.TT + tile - 1) / tile;
+cudaError_t gated_begin(GatedArgs& a, int vec, const float* from, float* to, cudaStream_t st) {
+    a.tiles = (a.TT + kTile - 1) / kTile;
     a.cols = (a.C + 32 * vec - 1) / (32 * vec);
     a.planned = a.tiles > 1 || a.cu;
     if (!a.planned) return cudaSuccess;
     const int64_t work = (int64_t)a.tiles * a.cols / kThreads + 1, most = a.cu ? (work > a.rows ? work : a.rows) : work;
     timing_pre(st, K_GATED_PLAN);
-    gated_plan_kernel<<<(int)(most < 152 ? most : 152), kThreads, 0, st>>>(a, tile, from, to);
+    gated_plan_kernel<<<(int)(most < 152 ? most : 152), kThreads, 0, st>>>(a, from, to);
     timing_post(st);
     return cudaGetLastError();
 }
 
 cudaError_t gated_forward(GatedArgs a, int dtype, bool pairs, cudaStream_t st) {
-    cudaError_t e = gated_begin(a, kFwdTile, pairs ? 2 : 1, a.s0, a.sT, st);
+    cudaError_t e = gated_begin(a, pairs ? 2 : 1, a.s0, a.sT, st);
     if (e != cudaSuccess) return e;
-    const int ctas = a.tiles * a.cols;
     timing_pre(st, K_GATED_SCAN);
-    if (pairs) gated_fwd_kernel<__nv_bfloat16, 2><<<ctas, kThreads, 0, st>>>(a);
-    else if (dtype == KDA_BF16) gated_fwd_kernel<__nv_bfloat16, 1><<<ctas, kThreads, 0, st>>>(a);
-    else gated_fwd_kernel<float, 1><<<ctas, kThreads, 0, st>>>(a);
+    e = gated_launch(pairs ? gated_fwd_kernel<__nv_bfloat16, 2> : dtype == KDA_BF16 ? gated_fwd_kernel<__nv_bfloat16, 1> : gated_fwd_kernel<float, 1>,
+                     a.tiles * a.cols, kThreads, 0, a.planned, a, st);
     timing_post(st);
-    return cudaGetLastError();
+    return e;
 }
 
 size_t span_bytes(const Shape& s, int64_t stride) { return ((size_t)(s.TT - 1) * stride + s.C) * s.es; }
@@ -743,13 +849,13 @@ extern "C" {
 size_t kda_gated_scan_fwd_workspace_size(const kda_gated_dims* dims) {
     Shape s;
     if (!dims || gated_check(dims, false, &s) != KDA_OK) return 0;
-    return gated_layout(s, kFwdTile, false, nullptr, nullptr);
+    return gated_layout(s, false, nullptr, nullptr);
 }
 
 size_t kda_gated_scan_bwd_workspace_size(const kda_gated_dims* dims) {
     Shape s;
     if (!dims || gated_check(dims, false, &s) != KDA_OK) return 0;
-    const size_t f = gated_layout(s, kFwdTile, false, nullptr, nullptr), b = gated_layout(s, kBwdTile, true, nullptr, nullptr);
+    const size_t f = gated_layout(s, false, nullptr, nullptr), b = gated_layout(s, true, nullptr, nullptr);
     return up(gated_record_bytes(s)) + (f > b ? f : b);
 }
 
@@ -771,7 +877,7 @@ kda_status kda_gated_scan_fwd(const kda_gated_dims* dims, const void* x, const v
     if (st != KDA_OK) return st;
     const size_t rec = saved ? gated_record_bytes(s) : 0;
     if (saved && (saved_bytes < rec || reinterpret_cast<uintptr_t>(saved) % 256)) return KDA_ERR_WORKSPACE;
-    if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || workspace_bytes < gated_layout(s, kFwdTile, false, nullptr, nullptr))
+    if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || workspace_bytes < gated_layout(s, false, nullptr, nullptr))
         return KDA_ERR_WORKSPACE;
     // a thread has read an element of x before it writes y's there, and a row's first tile its state before its last tile
     // writes one; the tiles otherwise run in no order
@@ -789,8 +895,9 @@ kda_status kda_gated_scan_fwd(const kda_gated_dims* dims, const void* x, const v
     }
     if (ranges_meet(final_state, ns, saved, rec)) return KDA_ERR_INVALID_ARG;
     GatedArgs a = gated_args(s, x, g_raw, i_raw, a_log, cu_seqlens, initial_state);
+    a.aligned = rows16(s, {x, g_raw, i_raw});
     a.y = y; a.sT = final_state; a.rec = static_cast<float*>(saved);
-    gated_layout(s, kFwdTile, false, static_cast<char*>(workspace), &a);
+    gated_layout(s, false, static_cast<char*>(workspace), &a);
     st = status_ptr(&a.status);
     if (st != KDA_OK) return st;
     const bool pairs = pairs_ok(s, {x, g_raw, i_raw, y}, {a_log, initial_state, final_state});
@@ -829,28 +936,28 @@ kda_status kda_gated_scan_bwd(const kda_gated_dims* dims, const void* x, const v
     GatedArgs a = gated_args(s, x, g_raw, i_raw, a_log, cu_seqlens, initial_state);
     st = status_ptr(&a.status);
     if (st != KDA_OK) return st;
+    a.aligned = rows16(s, {x, g_raw, i_raw, dy});
     char* ws = static_cast<char*>(workspace);
     const bool pairs = pairs_ok(s, {x, g_raw, i_raw, dy}, {a_log, initial_state, dfinal_state, dx, dg_raw, di_raw, dinitial_state});
     a.rec = static_cast<float*>(const_cast<void*>(saved));
     if (!saved) {      // the states again: a forward that writes only its record
         a.rec = reinterpret_cast<float*>(ws);
-        gated_layout(s, kFwdTile, false, ws + up(rec), &a);
+        gated_layout(s, false, ws + up(rec), &a);
         if (gated_forward(a, s.dtype, pairs, stream) != cudaSuccess) return KDA_ERR_CUDA;
     }
-    gated_layout(s, kBwdTile, true, ws + up(rec), &a);
+    gated_layout(s, true, ws + up(rec), &a);
     a.dy = dy; a.dsT = dfinal_state; a.dx = dx; a.dg = dg_raw; a.di = di_raw; a.da_log = da_log; a.ds0 = dinitial_state;
-    if (gated_begin(a, kBwdTile, pairs ? 2 : 1, dfinal_state, dinitial_state, stream) != cudaSuccess) return KDA_ERR_CUDA;
-    const int ctas = a.tiles * a.cols;
+    if (gated_begin(a, pairs ? 2 : 1, dfinal_state, dinitial_state, stream) != cudaSuccess) return KDA_ERR_CUDA;
     timing_pre(stream, K_GATED_BWD);
-    if (pairs) gated_bwd_kernel<__nv_bfloat16, 2><<<ctas, kThreads, 0, stream>>>(a);
-    else if (s.dtype == KDA_BF16) gated_bwd_kernel<__nv_bfloat16, 1><<<ctas, kThreads, 0, stream>>>(a);
-    else gated_bwd_kernel<float, 1><<<ctas, kThreads, 0, stream>>>(a);
+    cudaError_t e = gated_launch(pairs ? gated_bwd_kernel<__nv_bfloat16, 2> : s.dtype == KDA_BF16 ? gated_bwd_kernel<__nv_bfloat16, 1> : gated_bwd_kernel<float, 1>,
+                                 a.tiles * a.cols, kThreads, pairs ? sizeof(BwdShared<__nv_bfloat16, 2>) : s.dtype == KDA_BF16 ? sizeof(BwdShared<__nv_bfloat16, 1>) : sizeof(BwdShared<float, 1>),
+                                 a.planned, a, stream);
     timing_post(stream);
-    if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+    if (e != cudaSuccess) return KDA_ERR_CUDA;
     timing_pre(stream, K_GATED_REDUCE);
-    gated_reduce_kernel<<<(s.C + 31) / 32, kThreads, 0, stream>>>(a);
+    e = gated_launch(gated_reduce_kernel, (s.C + 31) / 32, kReduceWarps * 32, 0, true, a, stream);
     timing_post(stream);
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 kda_status kda_gated_step(const kda_gated_dims* dims, const void* x, const void* g_raw, const void* i_raw, const float* a_log,
