@@ -32,8 +32,10 @@ using namespace sm100;
 
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+// Eight warps do a tile's arithmetic, a ninth joins it to the chain of tiles.
+constexpr int kThreads = 256, kWarps = kThreads / 32, kAll = kThreads + 32;
 constexpr int kTok = 8, kTile = kWarps * kTok;      // tokens of a thread and of a CTA
+constexpr int kFwdCtas = 4, kBwdCtas = 2;           // CTAs of an SM
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct GatedArgs {
@@ -46,8 +48,9 @@ struct GatedArgs {
     float *sT, *rec;                     // rec [tiles, C]: the state that enters each tile
     float *dx, *dg, *di, *da_log, *ds0;
     // workspace (planned)
-    int *ticket, *ok, *flags, *first;    // flags [tiles, cols]; first [tiles]: the first row that begins at or after the tile's first token
-    float *agg, *inc;                    // agg [tiles, C] pairs, inc [tiles, C] leaving states; by order in the chain
+    int *ticket, *ok, *first;            // first [tiles]: the first row that begins at or after the tile's first token
+    float *agg, *inc;                    // agg [tiles, C] pairs, inc [tiles, C] leaving states; by order in the chain; kUnset before they are known
+    int64_t unset;                       // 16-byte pieces of agg and inc together
     float* part;                         // [tiles, C] da_log's parts
     int* status;
 };
@@ -137,9 +140,8 @@ template <typename V> struct Rate {
     V n, log2;
     bool wide;
 };
-template <typename V> __device__ __forceinline__ Rate<V> rate_of(const float* a_log, int c, bool in) {
+template <typename V> __device__ __forceinline__ Rate<V> rate_of(V a) {
     Rate<V> r;
-    const V a = in ? vload<V>(a_log + c) : vdup<V>(-1e30f);
     r.n = vmap([](float t) { return -expf(t); }, a);
     r.log2 = vmul(a, vdup<V>(kLog2e));
     bool over = false;
@@ -210,124 +212,156 @@ template <typename V> __device__ __forceinline__ Gates<V> gates_of(V g, V i) {
 
 // ------------------------------------------------------------------ rows inside a tile
 
-// Which rows begin at and end with a token of the tile, -1: none.  All threads; the answer: whether any does.
-template <int TILE> struct Edges {
-    int first[TILE], last[TILE];
+// Which rows begin at and end with a token of the tile, -1: none.
+struct Edges {
+    int first[kTile], last[kTile];
 };
-template <int TILE> __device__ __forceinline__ bool find_edges(const GatedArgs& a, int t0, int tile, Edges<TILE>& s) {
-    if (threadIdx.x < TILE) s.first[threadIdx.x] = s.last[threadIdx.x] = -1;
-    __syncthreads();
-    bool any = false;
-    const int t1 = min(t0 + TILE, a.TT);
-    for (int m = (a.cu ? a.first[tile] : (t0 + a.T - 1) / a.T) + threadIdx.x; m <= a.rows; m += kThreads) {
+__device__ __forceinline__ void tile_sync();
+
+// The first row that begins at or after token t0 of a tile, and where.
+struct RowHint {
+    int row, begin;
+};
+__device__ __forceinline__ RowHint row_hint(const GatedArgs& a, int tile) {
+    RowHint h;
+    h.row = a.cu ? a.first[tile] : (int)(((int64_t)tile * kTile + a.T - 1) / a.T);
+    h.begin = row_begin(a, h.row);
+    return h;
+}
+__device__ __forceinline__ bool has_edges(const GatedArgs& a, int t0, const RowHint& h) { return h.begin <= t0 + kTile; }
+__device__ __forceinline__ void find_edges(const GatedArgs& a, int t0, const RowHint& hint, Edges& s) {
+    if (threadIdx.x < kTile) s.first[threadIdx.x] = s.last[threadIdx.x] = -1;
+    tile_sync();
+    const int t1 = min(t0 + kTile, a.TT);
+    for (int m = hint.row + threadIdx.x; m <= a.rows; m += kThreads) {
         const int at = row_begin(a, m);
         if (at > t1) break;
-        if (m < a.rows && at < t1 && row_begin(a, m + 1) > at) {
-            s.first[at - t0] = m;
-            any = true;
-        }
-        if (m > 0 && at > t0 && row_begin(a, m - 1) < at) {
-            s.last[at - 1 - t0] = m - 1;
-            any = true;
-        }
+        if (m < a.rows && at < t1 && row_begin(a, m + 1) > at) s.first[at - t0] = m;
+        if (m > 0 && at > t0 && row_begin(a, m - 1) < at) s.last[at - 1 - t0] = m - 1;
     }
-    return __syncthreads_or(any);
+    tile_sync();
 }
 
 // ------------------------------------------------------------------ the chain of tiles
 
-__device__ __forceinline__ int load_acquire(const int* p) {
-    int v;
-    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
+// What a tile tells its successors are single words, each of which says itself whether it is there: kUnset is a NaN that no operation
+// gives.  So nothing has to be ordered, and what is read is the value itself: a flag beside it would cost the writer a wait for its
+// stores and the reader a second trip to the L2.
+constexpr uint32_t kUnset = 0xffffffffu;
+__device__ __forceinline__ float told(float v) { return __float_as_uint(v) == kUnset ? __uint_as_float(0x7fffffffu) : v; }
+__device__ __forceinline__ bool known(float v) { return __float_as_uint(v) != kUnset; }
+__device__ __forceinline__ bool known(float2 v) { return known(v.x) && known(v.y); }
+__device__ __forceinline__ void tell(float* p, float v) { asm volatile("st.relaxed.gpu.global.f32 [%0], %1;" ::"l"(p), "f"(told(v)) : "memory"); }
+__device__ __forceinline__ void tell(float* p, float2 v) {
+    asm volatile("st.relaxed.gpu.global.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(told(v.x)), "f"(told(v.y)) : "memory");
 }
-__device__ __forceinline__ void store_release(int* p, int v) {
-    asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+__device__ __forceinline__ void tell(float* p, float a, float b) { tell(p, make_float2(a, b)); }
+__device__ __forceinline__ void tell(float* p, float2 a, float2 b) {
+    asm volatile("st.relaxed.gpu.global.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(told(a.x)), "f"(told(a.y)), "f"(told(b.x)), "f"(told(b.y)) : "memory");
+}
+__device__ __forceinline__ void ask(const float* p, float& v) { asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory"); }
+__device__ __forceinline__ void ask(const float* p, float2& v) {
+    asm volatile("ld.relaxed.gpu.global.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
+}
+__device__ __forceinline__ void ask(const float* p, float& a, float& b) {
+    float2 v;
+    ask(p, v);
+    a = v.x;
+    b = v.y;
+}
+__device__ __forceinline__ void ask(const float* p, float2& a, float2& b) {
+    asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(a.x), "=f"(a.y), "=f"(b.x), "=f"(b.y) : "l"(p) : "memory");
 }
 
-enum Flag { kNothing = 0, kPair = 1, kState = 2 };
-
-// Called by one warp.  (__syncwarp puts the lanes' stores before lane 0's release, which covers what it has observed.)
-__device__ __forceinline__ void publish(const GatedArgs& a, int o, int col, Flag f) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) store_release(a.flags + (size_t)o * a.cols + col, f);
-}
-
-// The state that enters the o-th tile of the chain: from the nearest tile before it that has published its leaving state
-// on, the pairs of those between.  The first tile of a chain, and every tile in which a row begins, publishes a
-// state, so there is one.  One warp; at most about a second, then the error is recorded and the state is 0.
-template <typename V> __device__ __forceinline__ V look_back(const GatedArgs& a, int o, int col, int c, bool in) {
-    const int lane = threadIdx.x & 31;
-    int from = -1;
-    for (int back = o - 1, tries = 0; from < 0;) {
-        const int j = back - lane;
-        const int f = j >= 0 ? load_acquire(a.flags + (size_t)j * a.cols + col) : (int)kState;
-        const unsigned none = __ballot_sync(0xffffffffu, f == kNothing), state = __ballot_sync(0xffffffffu, f == kState);
-        const unsigned before = state ? (state & (0u - state)) - 1u : 0xffffffffu;
-        if (none & before) {
-            if (++tries > (1 << 20)) {
-                if (lane == 0) record_error(a.status, KDA_ERR_TIMEOUT);
-                return vdup<V>(0.f);
+// The state that enters the o-th tile of the chain, of this lane's channels: from the nearest tile before it that has told its
+// leaving state on, the pairs of those between, in order.  The first tile of a chain, and every tile in which a row begins,
+// tells a state, so there is one.  At most about a second, then the error is recorded and the state is 0.
+template <typename V> __device__ __forceinline__ V look_back(const GatedArgs& a, int o, int c) {
+    constexpr int W = 4;                 // tiles looked at together
+    const float *inc = a.inc + c, *agg = a.agg + 2 * (size_t)c;
+    int near = o - 1;                    // the pairs of the tiles above it are there
+    V s = vdup<V>(0.f);
+    for (int tries = 0;;) {
+        V state[W], P[W], h[W];
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            const size_t j = max(near - k, 0);
+            ask(inc + j * a.C, state[k]);
+            ask(agg + 2 * j * a.C, P[k], h[k]);
+        }
+        // the nearest state, if every pair before it is there
+        int at = -1;
+        bool open = true;
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+            if (open) {
+                if (known(state[k])) {
+                    at = k;
+                    open = false;
+                } else {
+                    open = known(P[k]) && known(h[k]);
+                }
             }
-            __nanosleep(32);
-        } else if (state) {
-            from = max(back - (__ffs(state) - 1), 0);
-        } else {
-            back -= 32;
+        if (at >= 0) {
+#pragma unroll
+            for (int k = W - 1; k >= 0; --k)
+                if (k == at) s = state[k];
+                else if (k < at) s = vfma(P[k], s, h[k]);
+            break;
+        }
+        if (open && near - W >= 0) {
+            near -= W;
+        } else if (++tries > (1 << 20)) {
+            record_error(a.status, KDA_ERR_TIMEOUT);
+            return vdup<V>(0.f);
         }
     }
-    __syncwarp();
-    if (!in) return vdup<V>(0.f);
-    V s = vload_l2<V>(a.inc + (size_t)from * a.C + c);
-    constexpr int AHEAD = 8;
-    for (int j = from + 1; j < o; j += AHEAD) {
-        V P[AHEAD], h[AHEAD];
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k)
-            if (j + k < o) {
-                const float* p = a.agg + 2 * ((size_t)(j + k) * a.C + c);
-                P[k] = vload_l2<V>(p);
-                h[k] = vload_l2<V>(p + sizeof(V) / 4);
-            }
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k)
-            if (j + k < o) s = vfma(P[k], s, h[k]);
+    // the pairs that were passed on the way
+    for (int j = near + 1; j < o; ++j) {
+        V P, h;
+        ask(agg + 2 * (size_t)j * a.C, P, h);
+        s = vfma(P, s, h);
     }
     return s;
 }
 
-// The tile's pair or leaving state for its successors, and the state that enters it.  closed: a row begins in the tile, so
-// that what leaves it does not depend on what enters.  needs: some token depends on what enters.
-template <typename V>
-__device__ __forceinline__ V join_chain(const GatedArgs& a, int o, int col, int c, bool in, V P, V h, bool closed, bool needs) {
-    if (!a.planned) return vdup<V>(0.f);
+// The chain's warp.  closed: a row begins in the tile, so that what leaves it does not depend on what enters; needs: some token
+// depends on what enters; give(the state that enters).
+template <typename V, typename F>
+__device__ __forceinline__ void join_chain(const GatedArgs& a, int o, int c, bool in, V P, V h, bool closed, bool needs, F&& give) {
+    if (!a.planned || !in) return give(vdup<V>(0.f));
     float* leaving = a.inc + (size_t)o * a.C + c;
     if (closed) {
-        if (in) vstore(leaving, h);
-        publish(a, o, col, kState);
-        return needs ? look_back<V>(a, o, col, c, in) : vdup<V>(0.f);
+        tell(leaving, h);
+        return give(needs ? look_back<V>(a, o, c) : vdup<V>(0.f));
     }
-    if (in) {
-        float* p = a.agg + 2 * ((size_t)o * a.C + c);
-        vstore(p, P);
-        vstore(p + sizeof(V) / 4, h);
-    }
-    publish(a, o, col, kPair);
-    const V s = look_back<V>(a, o, col, c, in);
-    if (in) vstore(leaving, vfma(P, s, h));
-    publish(a, o, col, kState);
-    return s;
+    tell(a.agg + 2 * ((size_t)o * a.C + c), P, h);
+    const V s = look_back<V>(a, o, c);
+    tell(leaving, vfma(P, s, h));
+    give(s);
 }
 
-// The tile and the columns of this CTA, in the order in which tiles are begun.
-__device__ __forceinline__ int take_ticket(const GatedArgs& a, int* slot) {
-    if (!a.planned) return blockIdx.x;
-    if (threadIdx.x == 0) *slot = atomicAdd(a.ticket, 1);
-    __syncthreads();
-    return *slot;
+// Barriers of a tile: its runs are in shared memory (the chain's warp waits), the entering state is (the others wait), and one
+// of the eight warps alone.
+__device__ __forceinline__ void runs_ready() {
+    __syncwarp();
+    asm volatile("bar.arrive 1, %0;" ::"n"(kAll) : "memory");
+}
+__device__ __forceinline__ void runs_wait() { asm volatile("bar.sync 1, %0;" ::"n"(kAll) : "memory"); }
+__device__ __forceinline__ void state_ready() {
+    __syncwarp();
+    asm volatile("bar.arrive 2, %0;" ::"n"(kAll) : "memory");
+}
+__device__ __forceinline__ void state_wait() { asm volatile("bar.sync 2, %0;" ::"n"(kAll) : "memory"); }
+__device__ __forceinline__ void tile_sync() { asm volatile("bar.sync 3, %0;" ::"n"(kThreads) : "memory"); }
+
+// Tiles in the order in which they are begun: a CTA takes its next one while it works on one, so that the next one's loads run
+// meanwhile.  (Every CTA finishes its tiles in the order it took them, so the first unfinished tile is always being worked on.)
+__device__ __forceinline__ int take_ticket(const GatedArgs& a, int before) {
+    return a.planned ? atomicAdd(a.ticket, 1) : before < 0 ? (int)blockIdx.x : before + (int)gridDim.x;
 }
 
-// Clears the counter and the flags, checks the offsets, finds each tile's first row, and passes the states of rows without
+// Clears the counter and what the tiles will tell, checks the offsets, finds each tile's first row, and passes the states of rows without
 // tokens through (of all rows where the offsets break the contract).
 __global__ void __launch_bounds__(kThreads) gated_plan_kernel(GatedArgs a, const float* from, float* to) {
     cudaTriggerProgrammaticLaunchCompletion();       // the pass may be launched; it waits for this kernel's end
@@ -343,7 +377,7 @@ __global__ void __launch_bounds__(kThreads) gated_plan_kernel(GatedArgs a, const
         *a.ok = !bad;
         if (bad) record_error(a.status, KDA_ERR_INVALID_ARG);
     }
-    for (int64_t k = id; k < (int64_t)a.tiles * a.cols; k += all) a.flags[k] = kNothing;
+    for (int64_t k = id; k < a.unset; k += all) reinterpret_cast<uint4*>(a.agg)[k] = make_uint4(kUnset, kUnset, kUnset, kUnset);
     if (!a.cu) return;
     for (int k = id; !bad && k < a.tiles; k += all) {
         int lo = 0, hi = a.rows;          // (cu[rows] = TT is past every tile's first token)
@@ -384,9 +418,11 @@ template <int BYTES> __device__ __forceinline__ void copy_async(void* dst, const
     if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
     else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
 }
+__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All groups but the last.
 __device__ __forceinline__ void copies_landed() {
-    asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
-    __syncthreads();
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    tile_sync();
 }
 // Whole tiles of arrays that allow it move 16 bytes at a time; otherwise a thread brings its own elements.  (The tile's base is one for
 // the CTA; an offset from it fits 32 bits.)
@@ -420,32 +456,35 @@ template <int VEC> __device__ __forceinline__ bool whole_tile(const GatedArgs& a
 
 // ------------------------------------------------------------------ forward
 
+struct TileWords {
+    int ticket[3], closed, needs;
+};
 template <typename E, int VEC> struct FwdShared {
     using V = Val<VEC>;
-    Plane<E, VEC> x, g, i;
-    Edges<kTile> edges;
+    Plane<E, VEC> x[2], g[2], i[2];
+    Edges edges;
     V sp[kWarps][32], sh[kWarps][32], senter[32];
-    int slot;
+    TileWords w;
 };
 
 // EDGE: the tile has rows that begin or end in it, tokens or channels past the last, or a rate above 1/4.
 template <typename E, int VEC, bool EDGE>
-__device__ __forceinline__ void forward_tile(const GatedArgs& a, const Spot& s, FwdShared<E, VEC>& m_, bool split, const Rate<Val<VEC>>& rate) {
+__device__ __forceinline__ void forward_tile(const GatedArgs& a, const Spot& s, FwdShared<E, VEC>& m_, int buf, bool split, const Rate<Val<VEC>>& rate) {
     using V = Val<VEC>;
-    const Edges<kTile>& edges = m_.edges;
+    const Edges& edges = m_.edges;
     auto &sp = m_.sp, &sh = m_.sh;
-    auto& senter = m_.senter;
+    auto &mx = m_.x[buf], &mg = m_.g[buf], &mi = m_.i[buf];
     const int tid = threadIdx.x;
     auto begins_at = [&](int k) { return EDGE && split ? edges.first[s.warp * kTok + k] : -1; };
     // a token as h -> ka h + kb; where a row begins the state is the row's own, and ka is 0
     V ka[kTok], kb[kTok], P, h;
 #pragma unroll
     for (int k = 0; k < kTok; ++k) {
-        const V g = m_.g[k][tid].get();
-        const Gates<V> z = gates_of(g, m_.i[k][tid].get());
+        const V g = mg[k][tid].get();
+        const Gates<V> z = gates_of(g, mi[k][tid].get());
         const V e = one_minus_exp(log_decay<EDGE>(g, z.sg, rate), EDGE && rate.wide), w = square_of(e);
         ka[k] = keep_of(e);
-        kb[k] = vmul(vmul(w, root_of(w)), vmul(z.si, m_.x[k][tid].get()));
+        kb[k] = vmul(vmul(w, root_of(w)), vmul(z.si, mx[k][tid].get()));
         if (EDGE && k >= s.n) {
             ka[k] = vdup<V>(1.f);
             kb[k] = vdup<V>(0.f);
@@ -465,24 +504,18 @@ __device__ __forceinline__ void forward_tile(const GatedArgs& a, const Spot& s, 
     }
     sp[s.warp][s.lane] = P;
     sh[s.warp][s.lane] = h;
-    bool begins = false;
-    if (EDGE && split)
-        for (int k = s.lane; k < kTile; k += 32) begins |= edges.first[k] >= 0;
-    if (EDGE) begins = __any_sync(0xffffffffu, begins);
-    __syncthreads();
-    auto over = [](V P, V s, V h) { return EDGE ? join(P, s, h) : vfma(P, s, h); };
     if (s.warp == 0) {
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) {
-            P = over(sp[w][s.lane], P, vdup<V>(0.f));
-            h = over(sp[w][s.lane], h, sh[w][s.lane]);
-        }
-        h = join_chain<V>(a, s.tile, s.col, s.c, s.in, P, h, EDGE && begins, !EDGE || edges.first[0] < 0);
-        senter[s.lane] = h;
-        if (a.rec && s.in) vstore(a.rec + (size_t)s.tile * a.C + s.c, h);
+        bool begins = false;
+        if (EDGE && split)
+            for (int k = s.lane; k < kTile; k += 32) begins |= edges.first[k] >= 0;
+        if (EDGE) begins = __any_sync(0xffffffffu, begins);
+        m_.w.closed = begins;
+        m_.w.needs = !EDGE || !split || edges.first[0] < 0;
     }
-    __syncthreads();
-    h = senter[s.lane];
+    runs_ready();
+    state_wait();
+    h = m_.senter[s.lane];
+    auto over = [](V P, V s, V h) { return EDGE ? join(P, s, h) : vfma(P, s, h); };
     for (int w = 0; w < s.warp; ++w) h = over(sp[w][s.lane], h, sh[w][s.lane]);
     E* y = static_cast<E*>(a.y) + (size_t)s.t0 * a.C;
     const uint32_t at = s.warp * kTok * (uint32_t)a.C + s.c;
@@ -496,23 +529,91 @@ __device__ __forceinline__ void forward_tile(const GatedArgs& a, const Spot& s, 
         }
 }
 
-// With four CTAs on an SM their phases (loads, gates, the wait for the state, stores) overlap.
+// (not inlined: its registers are not the others')
 template <typename E, int VEC>
-__global__ void __launch_bounds__(kThreads, 4) gated_fwd_kernel(const __grid_constant__ GatedArgs a) {
-    __shared__ __align__(16) FwdShared<E, VEC> m;
+__device__ __noinline__ void forward_edge(const GatedArgs& a, const Spot& s, FwdShared<E, VEC>& m, int buf, bool split, const Rate<Val<VEC>>& rate) {
+    forward_tile<E, VEC, true>(a, s, m, buf, split, rate);
+}
+
+// The loop of both passes: a CTA's tiles, each one's copies issued while the one before is worked on.  load(spot, buffer) issues a tile's
+// copies, work(spot, buffer, hint, rate) does it.  The ninth warp takes the tickets and joins the chain: the runs of the warps from the
+// first (or, backwards, from the last) on.
+template <bool BACK, int VEC, typename L, typename W>
+__device__ __forceinline__ void walk_tiles(const GatedArgs& a, TileWords& w, Val<VEC> (&sp)[kWarps][32], Val<VEC> (&sh)[kWarps][32],
+                                           Val<VEC> (&senter)[32], L&& load, W&& work) {
+    using V = Val<VEC>;
+    const int total = a.tiles * a.cols, lane = threadIdx.x & 31;
+    const bool chain = threadIdx.x >= kThreads;
+    if (threadIdx.x == kThreads) {
+        w.ticket[0] = take_ticket(a, -1);
+        w.ticket[1] = w.ticket[0] < total ? take_ticket(a, w.ticket[0]) : total;
+    }
+    const bool go = !a.planned || *a.ok;
+    __syncthreads();
+    int idx = w.ticket[0];
+    if (!go || idx >= total) return;
+    auto spot = [&](int idx) {
+        const int o = idx / a.cols;
+        return spot_of<VEC>(a, BACK ? a.tiles - 1 - o : o, idx - o * a.cols);
+    };
+    if (chain) {
+        for (int it = 0; idx < total; ++it) {
+            const int next = w.ticket[(it + 1) % 3], o = idx / a.cols, c = ((idx - o * a.cols) * 32 + lane) * VEC;
+            int taken = total;
+            if (lane == 0 && next < total) taken = take_ticket(a, next);
+            runs_wait();
+            V P = sp[BACK ? kWarps - 1 : 0][lane], h = sh[BACK ? kWarps - 1 : 0][lane];
+#pragma unroll
+            for (int k = 1; k < kWarps; ++k) {
+                const V p = sp[BACK ? kWarps - 1 - k : k][lane], q = sh[BACK ? kWarps - 1 - k : k][lane];
+                P = join(p, P, vdup<V>(0.f));
+                h = join(p, h, q);
+            }
+            V enters;
+            join_chain<V>(a, o, c, c < a.C, P, h, w.closed, w.needs, [&](V v) { enters = v; });
+            senter[lane] = enters;
+            if (lane == 0) w.ticket[(it + 2) % 3] = taken;
+            state_ready();
+            if (!BACK && a.rec && c < a.C) vstore(a.rec + (size_t)o * a.C + c, enters);
+            idx = next;
+        }
+        return;
+    }
+    load(spot(idx), 0);
+    copies_issued();
+    for (int it = 0;; ++it) {
+        const int next = w.ticket[(it + 1) % 3];
+        if (next < total) load(spot(next), (it + 1) & 1);
+        copies_issued();
+        const Spot s = spot(idx);
+        const RowHint hint = row_hint(a, s.tile);
+        const Rate<V> rate = rate_of(s.in ? vload<V>(a.a_log + s.c) : vdup<V>(-1e30f));
+        copies_landed();
+        work(s, it & 1, hint, rate);
+        if (next >= total) return;
+        idx = next;
+    }
+}
+
+template <typename E, int VEC>
+__global__ void __launch_bounds__(kAll, kFwdCtas) gated_fwd_kernel(const __grid_constant__ GatedArgs a) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    FwdShared<E, VEC>& m = *reinterpret_cast<FwdShared<E, VEC>*>(smem);
     cudaGridDependencySynchronize();
-    const int idx = take_ticket(a, &m.slot), tile = idx / a.cols;
-    const Spot s = spot_of<VEC>(a, tile, idx - tile * a.cols);
-    const bool whole = whole_tile<VEC>(a, s);
-    load_plane<E, VEC>(a.x, a.xs, s, whole, a.aligned, m.x);
-    load_plane<E, VEC>(a.g, a.gs, s, whole, a.aligned, m.g);
-    load_plane<E, VEC>(a.i, a.is, s, whole, a.aligned, m.i);
-    const Rate<Val<VEC>> rate = rate_of<Val<VEC>>(a.a_log, s.c, s.in);
-    const bool go = !a.planned || *a.ok, split = go && find_edges(a, s.t0, tile, m.edges);
-    copies_landed();
-    if (!go) return;
-    if (whole && !split && !rate.wide) forward_tile<E, VEC, false>(a, s, m, split, rate);
-    else forward_tile<E, VEC, true>(a, s, m, split, rate);
+    walk_tiles<false, VEC>(
+        a, m.w, m.sp, m.sh, m.senter,
+        [&](const Spot& s, int buf) {
+            const bool whole = whole_tile<VEC>(a, s);
+            load_plane<E, VEC>(a.x, a.xs, s, whole, a.aligned, m.x[buf]);
+            load_plane<E, VEC>(a.g, a.gs, s, whole, a.aligned, m.g[buf]);
+            load_plane<E, VEC>(a.i, a.is, s, whole, a.aligned, m.i[buf]);
+        },
+        [&](const Spot& s, int buf, const RowHint& hint, const Rate<Val<VEC>>& rate) {
+            const bool split = has_edges(a, s.t0, hint);
+            if (split) find_edges(a, s.t0, hint, m.edges);
+            if (whole_tile<VEC>(a, s) && !split && !rate.wide) forward_tile<E, VEC, false>(a, s, m, buf, split, rate);
+            else forward_edge<E, VEC>(a, s, m, buf, split, rate);
+        });
 }
 
 // ------------------------------------------------------------------ backward
@@ -520,31 +621,32 @@ __global__ void __launch_bounds__(kThreads, 4) gated_fwd_kernel(const __grid_con
 // The gates are formed twice, before and after the chain: keeping them in between would halve the number of CTAs.
 template <typename E, int VEC> struct BwdShared {
     using V = Val<VEC>;
-    Plane<E, VEC> x, g, i, dy;
-    Edges<kTile> edges;
+    Plane<E, VEC> x[2], g[2], i[2], dy[2];
+    Edges edges;
     V sp[kWarps][32], sh[kWarps][32], sq[kWarps][32], sm[kWarps][32], senter[32];
     V e[kTok][kThreads], b[kTok][kThreads];       // e = 1 - a; the inputs, then the states before the tokens
-    int slot;
+    TileWords w;
 };
 
 template <typename E, int VEC, bool EDGE>
-__device__ __forceinline__ void backward_tile(const GatedArgs& a, const Spot& s, int o, BwdShared<E, VEC>& m_, bool split, const Rate<Val<VEC>>& rate) {
+__device__ __forceinline__ void backward_tile(const GatedArgs& a, const Spot& s, BwdShared<E, VEC>& m_, int buf, bool split, const Rate<Val<VEC>>& rate) {
     using V = Val<VEC>;
     const int tid = threadIdx.x, warp = s.warp, lane = s.lane, c = s.c;
+    auto &mx = m_.x[buf], &mg = m_.g[buf], &mi = m_.i[buf], &md = m_.dy[buf];
     auto begins_at = [&](int k) { return EDGE && split ? m_.edges.first[warp * kTok + k] : -1; };
     auto ends_at = [&](int k) { return EDGE && split ? m_.edges.last[warp * kTok + k] : -1; };
     auto row_of = [&](const float* p, int row) { return p ? vload<V>(p + (size_t)row * a.C + c) : vdup<V>(0.f); };
     auto over = [](V P, V s, V h) { return EDGE ? join(P, s, h) : vfma(P, s, h); };
-    const V one = vdup<V>(1.f);
+    const V one = vdup<V>(1.f), entering = s.in ? vload<V>(a.rec + (size_t)s.tile * a.C + c) : vdup<V>(0.f);
     // the forward's runs, from the first token on
     V P = one, h = vdup<V>(0.f);
 #pragma unroll 4
     for (int k = 0; k < kTok; ++k) {
-        const V g = m_.g[k][tid].get();
-        const Gates<V> z = gates_of(g, m_.i[k][tid].get());
+        const V g = mg[k][tid].get();
+        const Gates<V> z = gates_of(g, mi[k][tid].get());
         V e = one_minus_exp(log_decay<EDGE>(g, z.sg, rate), EDGE && rate.wide);
         if (EDGE && k >= s.n) e = vdup<V>(0.f);
-        const V w = square_of(e), b = vmul(vmul(w, root_of(w)), vmul(z.si, m_.x[k][tid].get())), ka = keep_of(e);
+        const V w = square_of(e), b = vmul(vmul(w, root_of(w)), vmul(z.si, mx[k][tid].get())), ka = keep_of(e);
         if (EDGE && begins_at(k) >= 0) {
             P = vdup<V>(0.f);
             h = row_of(a.s0, begins_at(k));
@@ -567,27 +669,22 @@ __device__ __forceinline__ void backward_tile(const GatedArgs& a, const Spot& s,
         }
         const V ka = keep_of(m_.e[k][tid]);
         P = vmul(P, ka);
-        m = vmul(ka, vfma(m_.dy[k][tid].get(), one, m));
+        m = vmul(ka, vfma(md[k][tid].get(), one, m));
     }
     m_.sq[warp][lane] = P;
     m_.sm[warp][lane] = m;
-    bool ends = false;
-    if (EDGE && split)
-        for (int k = lane; k < kTile; k += 32) ends |= m_.edges.last[k] >= 0;
-    if (EDGE) ends = __any_sync(0xffffffffu, ends);
-    __syncthreads();
     if (warp == 0) {
-        P = m_.sq[kWarps - 1][lane];
-        m = m_.sm[kWarps - 1][lane];
-#pragma unroll
-        for (int w = kWarps - 2; w >= 0; --w) {
-            P = over(m_.sq[w][lane], P, vdup<V>(0.f));
-            m = over(m_.sq[w][lane], m, m_.sm[w][lane]);
-        }
-        m_.senter[lane] = join_chain<V>(a, o, s.col, c, s.in, P, m, EDGE && ends, !EDGE || m_.edges.last[min(kTile, a.TT - s.t0) - 1] < 0);
+        bool ends = false;
+        if (EDGE && split)
+            for (int k = lane; k < kTile; k += 32) ends |= m_.edges.last[k] >= 0;
+        if (EDGE) ends = __any_sync(0xffffffffu, ends);
+        m_.w.closed = ends;
+        m_.w.needs = !EDGE || !split || m_.edges.last[min(kTile, a.TT - s.t0) - 1] < 0;
     }
+    runs_ready();
+    tile_sync();
     // meanwhile the states before the tokens
-    h = s.in ? vload<V>(a.rec + (size_t)s.tile * a.C + c) : vdup<V>(0.f);
+    h = entering;
     for (int w = 0; w < warp; ++w) h = over(m_.sp[w][lane], h, m_.sh[w][lane]);
 #pragma unroll 4
     for (int k = 0; k < kTok; ++k) {
@@ -596,7 +693,7 @@ __device__ __forceinline__ void backward_tile(const GatedArgs& a, const Spot& s,
         m_.b[k][tid] = h;
         h = vfma(keep_of(m_.e[k][tid]), h, b);
     }
-    __syncthreads();
+    state_wait();
     m = m_.senter[lane];
     for (int w = kWarps - 1; w > warp; --w) m = over(m_.sq[w][lane], m, m_.sm[w][lane]);
     V dlog = vdup<V>(0.f);
@@ -607,13 +704,13 @@ __device__ __forceinline__ void backward_tile(const GatedArgs& a, const Spot& s,
     for (int k = kTok - 1; k >= 0; --k)
         if (!EDGE || k < s.n) {
             if (EDGE && ends_at(k) >= 0) m = row_of(a.dsT, ends_at(k));
-            const V g = m_.g[k][tid].get();
-            const Gates<V> z = gates_of(g, m_.i[k][tid].get());
+            const V g = mg[k][tid].get();
+            const Gates<V> z = gates_of(g, mi[k][tid].get());
             const V e = m_.e[k][tid], w = square_of(e), root = root_of(w), ka = keep_of(e);
-            const V dh = vfma(m_.dy[k][tid].get(), one, m);                  // the gradient of h_t
+            const V dh = vfma(md[k][tid].get(), one, m);                  // the gradient of h_t
             m = vmul(ka, dh);
             if (EDGE && begins_at(k) >= 0 && a.ds0) vstore(a.ds0 + (size_t)begins_at(k) * a.C + c, m);
-            const V u = vmul(z.si, m_.x[k][tid].get()), du = vmul(dh, vmul(w, root));
+            const V u = vmul(z.si, mx[k][tid].get()), du = vmul(dh, vmul(w, root));
             // of log a: a (h_{t-1} - u a / sqrt(1 - a^2)) times that of h_t; then times log a for a_log, and 1 - sigmoid(g) for g
             const V dl = vmul(vmul(m, vfma(vmul(u, vdup<V>(-1.f)), vmul(ka, root), m_.b[k][tid])), log_decay<EDGE>(g, z.sg, rate));
             dlog = vfma(dl, one, dlog);
@@ -622,9 +719,9 @@ __device__ __forceinline__ void backward_tile(const GatedArgs& a, const Spot& s,
             vstore_stream(dg + to, vmul(dl, vmul(z.eg, z.sg)));
             vstore_stream(di + to, vmul(vmul(du, u), vmul(z.ei, z.si)));
         }
-    __syncthreads();
+    tile_sync();
     m_.sp[warp][lane] = dlog;
-    __syncthreads();
+    tile_sync();
     if (warp == 0 && s.in) {
         dlog = m_.sp[0][lane];
 #pragma unroll
@@ -634,23 +731,30 @@ __device__ __forceinline__ void backward_tile(const GatedArgs& a, const Spot& s,
 }
 
 template <typename E, int VEC>
-__global__ void __launch_bounds__(kThreads, 3) gated_bwd_kernel(const __grid_constant__ GatedArgs a) {
+__device__ __noinline__ void backward_edge(const GatedArgs& a, const Spot& s, BwdShared<E, VEC>& m, int buf, bool split, const Rate<Val<VEC>>& rate) {
+    backward_tile<E, VEC, true>(a, s, m, buf, split, rate);
+}
+
+template <typename E, int VEC>
+__global__ void __launch_bounds__(kAll, kBwdCtas) gated_bwd_kernel(const __grid_constant__ GatedArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];
     BwdShared<E, VEC>& m = *reinterpret_cast<BwdShared<E, VEC>*>(smem);
     cudaGridDependencySynchronize();
-    const int idx = take_ticket(a, &m.slot), o = idx / a.cols, tile = a.tiles - 1 - o;
-    const Spot s = spot_of<VEC>(a, tile, idx - o * a.cols);
-    const bool whole = whole_tile<VEC>(a, s);
-    load_plane<E, VEC>(a.x, a.xs, s, whole, a.aligned, m.x);
-    load_plane<E, VEC>(a.g, a.gs, s, whole, a.aligned, m.g);
-    load_plane<E, VEC>(a.i, a.is, s, whole, a.aligned, m.i);
-    load_plane<E, VEC>(a.dy, a.C, s, whole, a.aligned, m.dy);
-    const Rate<Val<VEC>> rate = rate_of<Val<VEC>>(a.a_log, s.c, s.in);
-    const bool go = !a.planned || *a.ok, split = go && find_edges(a, s.t0, tile, m.edges);
-    copies_landed();
-    if (!go) return;
-    if (whole && !split && !rate.wide) backward_tile<E, VEC, false>(a, s, o, m, split, rate);
-    else backward_tile<E, VEC, true>(a, s, o, m, split, rate);
+    walk_tiles<true, VEC>(
+        a, m.w, m.sq, m.sm, m.senter,
+        [&](const Spot& s, int buf) {
+            const bool whole = whole_tile<VEC>(a, s);
+            load_plane<E, VEC>(a.x, a.xs, s, whole, a.aligned, m.x[buf]);
+            load_plane<E, VEC>(a.g, a.gs, s, whole, a.aligned, m.g[buf]);
+            load_plane<E, VEC>(a.i, a.is, s, whole, a.aligned, m.i[buf]);
+            load_plane<E, VEC>(a.dy, a.C, s, whole, a.aligned, m.dy[buf]);
+        },
+        [&](const Spot& s, int buf, const RowHint& hint, const Rate<Val<VEC>>& rate) {
+            const bool split = has_edges(a, s.t0, hint);
+            if (split) find_edges(a, s.t0, hint, m.edges);
+            if (whole_tile<VEC>(a, s) && !split && !rate.wide) backward_tile<E, VEC, false>(a, s, m, buf, split, rate);
+            else backward_edge<E, VEC>(a, s, m, buf, split, rate);
+        });
 }
 
 // da_log: the tiles' parts in a fixed order, 32 channels to a CTA.
@@ -705,7 +809,7 @@ __global__ void __launch_bounds__(kStepThreads) gated_step_kernel(const __grid_c
     rg.load(a.g, (size_t)b * a.gs + c);
     ri.load(a.i, (size_t)b * a.is + c);
     const V old = vload<V>(a.s_in + (size_t)slot * a.C + c);
-    const Rate<V> rate = rate_of<V>(a.a_log, c, true);
+    const Rate<V> rate = rate_of(vload<V>(a.a_log + c));
     const Gates<V> z = gates_of(rg.get(), ri.get());
     const V e = one_minus_exp(log_decay<true>(rg.get(), z.sg, rate), rate.wide), w = square_of(e);
     const V h = vfma(keep_of(e), old, vmul(vmul(w, root_of(w)), vmul(z.si, rx.get())));
@@ -744,7 +848,7 @@ size_t gated_record_bytes(const Shape& s) { return (size_t)((s.TT + kTile - 1) /
 
 // Workspace of one pass; fills the views where ws is given.
 size_t gated_layout(const Shape& s, bool reduce, char* ws, GatedArgs* a) {
-    const size_t tiles = (s.TT + kTile - 1) / kTile, most = (s.C + 31) / 32;
+    const size_t tiles = (s.TT + kTile - 1) / kTile;
     size_t o = 0;
     auto take = [&](size_t n) {
         char* p = ws ? ws + o : nullptr;
@@ -752,7 +856,6 @@ size_t gated_layout(const Shape& s, bool reduce, char* ws, GatedArgs* a) {
         return p;
     };
     char* head = take(8);
-    char* flags = take(tiles * most * 4);
     char* first = take(tiles * 4);
     char* agg = take(tiles * s.C * 8);
     char* inc = take(tiles * s.C * 4);
@@ -760,10 +863,10 @@ size_t gated_layout(const Shape& s, bool reduce, char* ws, GatedArgs* a) {
     if (a) {
         a->ticket = reinterpret_cast<int*>(head);
         a->ok = a->ticket + 1;
-        a->flags = reinterpret_cast<int*>(flags);
         a->first = reinterpret_cast<int*>(first);
         a->agg = reinterpret_cast<float*>(agg);
         a->inc = reinterpret_cast<float*>(inc);
+        a->unset = (int64_t)((up(tiles * s.C * 8) + up(tiles * s.C * 4)) / 16);      // (inc follows agg)
         a->part = reinterpret_cast<float*>(part);
     }
     return o;
@@ -819,9 +922,9 @@ cudaError_t gated_begin(GatedArgs& a, int vec, const float* from, float* to, cud
     a.cols = (a.C + 32 * vec - 1) / (32 * vec);
     a.planned = a.tiles > 1 || a.cu;
     if (!a.planned) return cudaSuccess;
-    const int64_t work = (int64_t)a.tiles * a.cols / kThreads + 1, most = a.cu ? (work > a.rows ? work : a.rows) : work;
+    const int64_t work = a.unset / (4 * kThreads) + 1, most = a.cu ? (work > a.rows ? work : a.rows) : work;
     timing_pre(st, K_GATED_PLAN);
-    gated_plan_kernel<<<(int)(most < 152 ? most : 152), kThreads, 0, st>>>(a, from, to);
+    gated_plan_kernel<<<(int)(most < 608 ? most : 608), kThreads, 0, st>>>(a, from, to);
     timing_post(st);
     return cudaGetLastError();
 }
@@ -830,8 +933,10 @@ cudaError_t gated_forward(GatedArgs a, int dtype, bool pairs, cudaStream_t st) {
     cudaError_t e = gated_begin(a, pairs ? 2 : 1, a.s0, a.sT, st);
     if (e != cudaSuccess) return e;
     timing_pre(st, K_GATED_SCAN);
+    const int ctas = a.tiles * a.cols, most = 152 * kFwdCtas;
     e = gated_launch(pairs ? gated_fwd_kernel<__nv_bfloat16, 2> : dtype == KDA_BF16 ? gated_fwd_kernel<__nv_bfloat16, 1> : gated_fwd_kernel<float, 1>,
-                     a.tiles * a.cols, kThreads, 0, a.planned, a, st);
+                     ctas < most ? ctas : most, kAll, pairs ? sizeof(FwdShared<__nv_bfloat16, 2>) : dtype == KDA_BF16 ? sizeof(FwdShared<__nv_bfloat16, 1>) : sizeof(FwdShared<float, 1>),
+                     a.planned, a, st);
     timing_post(st);
     return e;
 }
@@ -949,8 +1054,9 @@ kda_status kda_gated_scan_bwd(const kda_gated_dims* dims, const void* x, const v
     a.dy = dy; a.dsT = dfinal_state; a.dx = dx; a.dg = dg_raw; a.di = di_raw; a.da_log = da_log; a.ds0 = dinitial_state;
     if (gated_begin(a, pairs ? 2 : 1, dfinal_state, dinitial_state, stream) != cudaSuccess) return KDA_ERR_CUDA;
     timing_pre(stream, K_GATED_BWD);
+    const int ctas = a.tiles * a.cols, most = 152 * kBwdCtas;
     cudaError_t e = gated_launch(pairs ? gated_bwd_kernel<__nv_bfloat16, 2> : s.dtype == KDA_BF16 ? gated_bwd_kernel<__nv_bfloat16, 1> : gated_bwd_kernel<float, 1>,
-                                 a.tiles * a.cols, kThreads, pairs ? sizeof(BwdShared<__nv_bfloat16, 2>) : s.dtype == KDA_BF16 ? sizeof(BwdShared<__nv_bfloat16, 1>) : sizeof(BwdShared<float, 1>),
+                                 ctas < most ? ctas : most, kAll, pairs ? sizeof(BwdShared<__nv_bfloat16, 2>) : s.dtype == KDA_BF16 ? sizeof(BwdShared<__nv_bfloat16, 1>) : sizeof(BwdShared<float, 1>),
                                  a.planned, a, stream);
     timing_post(stream);
     if (e != cudaSuccess) return KDA_ERR_CUDA;
