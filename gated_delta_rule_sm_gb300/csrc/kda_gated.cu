@@ -222,12 +222,6 @@ __device__ __forceinline__ void tile_sync();
 struct RowHint {
     int row, begin;
 };
-__device__ __forceinline__ RowHint row_hint(const GatedArgs& a, int tile) {
-    RowHint h;
-    h.row = a.cu ? a.first[tile] : (int)(((int64_t)tile * kTile + a.T - 1) / a.T);
-    h.begin = row_begin(a, h.row);
-    return h;
-}
 __device__ __forceinline__ bool has_edges(const GatedArgs& a, int t0, const RowHint& h) { return h.begin <= t0 + kTile; }
 __device__ __forceinline__ void find_edges(const GatedArgs& a, int t0, const RowHint& hint, Edges& s) {
     if (threadIdx.x < kTile) s.first[threadIdx.x] = s.last[threadIdx.x] = -1;
@@ -456,8 +450,14 @@ template <int VEC> __device__ __forceinline__ bool whole_tile(const GatedArgs& a
 
 // ------------------------------------------------------------------ forward
 
+// A tile as the ninth warp announces it: its place in the chain (past the last: none), itself, its columns, and the first row that
+// begins in or after it.
+struct TileWord {
+    int o, tile, col, row, begin;
+};
 struct TileWords {
-    int ticket[3], closed, needs;
+    TileWord at[3];
+    int closed, needs;
 };
 template <typename E, int VEC> struct FwdShared {
     using V = Val<VEC>;
@@ -542,25 +542,37 @@ template <bool BACK, int VEC, typename L, typename W>
 __device__ __forceinline__ void walk_tiles(const GatedArgs& a, TileWords& w, Val<VEC> (&sp)[kWarps][32], Val<VEC> (&sh)[kWarps][32],
                                            Val<VEC> (&senter)[32], L&& load, W&& work) {
     using V = Val<VEC>;
-    const int total = a.tiles * a.cols, lane = threadIdx.x & 31;
+    const uint32_t total = (uint32_t)a.tiles * a.cols;
+    const int lane = threadIdx.x & 31;
     const bool chain = threadIdx.x >= kThreads;
-    if (threadIdx.x == kThreads) {
-        w.ticket[0] = take_ticket(a, -1);
-        w.ticket[1] = w.ticket[0] < total ? take_ticket(a, w.ticket[0]) : total;
-    }
-    const bool go = !a.planned || *a.ok;
-    __syncthreads();
-    int idx = w.ticket[0];
-    if (!go || idx >= total) return;
-    auto spot = [&](int idx) {
-        const int o = idx / a.cols;
-        return spot_of<VEC>(a, BACK ? a.tiles - 1 - o : o, idx - o * a.cols);
+    auto announce = [&](uint32_t ticket, TileWord& to) {
+        TileWord n;
+        n.o = a.tiles;
+        if (ticket < total) {
+            n.o = (int)(ticket / (uint32_t)a.cols);
+            n.col = (int)(ticket - (uint32_t)n.o * a.cols);
+            n.tile = BACK ? a.tiles - 1 - n.o : n.o;
+            n.row = a.cu ? a.first[n.tile] : (int)(((uint32_t)n.tile * kTile + a.T - 1) / (uint32_t)a.T);
+            n.begin = row_begin(a, n.row);
+        }
+        to = n;
     };
+    // (offsets that break the contract: the plan has found no tile's first row, and nothing is read by them)
+    const bool go = !a.planned || *a.ok;
+    if (!go) return;
+    uint32_t ticket = total;       // the last one taken (by one lane)
+    if (threadIdx.x == kThreads) {
+        ticket = take_ticket(a, -1);
+        announce(ticket, w.at[0]);
+        if (ticket < total) ticket = take_ticket(a, (int)ticket);
+        announce(ticket, w.at[1]);
+    }
+    __syncthreads();
     if (chain) {
-        for (int it = 0; idx < total; ++it) {
-            const int next = w.ticket[(it + 1) % 3], o = idx / a.cols, c = ((idx - o * a.cols) * 32 + lane) * VEC;
-            int taken = total;
-            if (lane == 0 && next < total) taken = take_ticket(a, next);
+        for (int it = 0;; ++it) {
+            const int o = w.at[it % 3].o, c = (w.at[it % 3].col * 32 + lane) * VEC;
+            if (o >= a.tiles) return;
+            if (lane == 0 && ticket < total) ticket = take_ticket(a, (int)ticket);
             runs_wait();
             V P = sp[BACK ? kWarps - 1 : 0][lane], h = sh[BACK ? kWarps - 1 : 0][lane];
 #pragma unroll
@@ -572,26 +584,24 @@ __device__ __forceinline__ void walk_tiles(const GatedArgs& a, TileWords& w, Val
             V enters;
             join_chain<V>(a, o, c, c < a.C, P, h, w.closed, w.needs, [&](V v) { enters = v; });
             senter[lane] = enters;
-            if (lane == 0) w.ticket[(it + 2) % 3] = taken;
+            if (lane == 0) announce(ticket, w.at[(it + 2) % 3]);
             state_ready();
             if (!BACK && a.rec && c < a.C) vstore(a.rec + (size_t)o * a.C + c, enters);
-            idx = next;
         }
-        return;
     }
-    load(spot(idx), 0);
+    auto spot = [&](const TileWord& n) { return spot_of<VEC>(a, n.tile, n.col); };
+    if (w.at[0].o < a.tiles) load(spot(w.at[0]), 0);
     copies_issued();
     for (int it = 0;; ++it) {
-        const int next = w.ticket[(it + 1) % 3];
-        if (next < total) load(spot(next), (it + 1) & 1);
+        const TileWord &now = w.at[it % 3], &next = w.at[(it + 1) % 3];
+        if (now.o >= a.tiles) return;
+        if (next.o < a.tiles) load(spot(next), (it + 1) & 1);
         copies_issued();
-        const Spot s = spot(idx);
-        const RowHint hint = row_hint(a, s.tile);
+        const Spot s = spot(now);
+        const RowHint hint = {now.row, now.begin};
         const Rate<V> rate = rate_of(s.in ? vload<V>(a.a_log + s.c) : vdup<V>(-1e30f));
         copies_landed();
         work(s, it & 1, hint, rate);
-        if (next >= total) return;
-        idx = next;
     }
 }
 
