@@ -35,7 +35,7 @@ namespace {
 // Eight warps do a tile's arithmetic, a ninth joins it to the chain of tiles.
 constexpr int kThreads = 256, kWarps = kThreads / 32, kAll = kThreads + 32;
 constexpr int kTok = 8, kTile = kWarps * kTok;      // tokens of a thread and of a CTA
-constexpr int kFwdCtas = 4, kBwdCtas = 2;           // CTAs of an SM
+constexpr int kFwdCtas = 4, kBwdCtas = 3;           // CTAs of an SM
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct GatedArgs {
@@ -325,17 +325,14 @@ template <typename V, typename F>
 __device__ __forceinline__ void join_chain(const GatedArgs& a, int o, int c, bool in, V P, V h, bool closed, bool needs, F&& give) {
     if (!a.planned || !in) return give(vdup<V>(0.f));
     float* leaving = a.inc + (size_t)o * a.C + c;
-    if (closed) {
-        tell(leaving, h);
-        return give(needs ? look_back<V>(a, o, c) : vdup<V>(0.f));
-    }
-    tell(a.agg + 2 * ((size_t)o * a.C + c), P, h);
-    const V s = look_back<V>(a, o, c);
-    tell(leaving, vfma(P, s, h));
+    if (closed) tell(leaving, h);
+    else tell(a.agg + 2 * ((size_t)o * a.C + c), P, h);
+    const V s = needs || !closed ? look_back<V>(a, o, c) : vdup<V>(0.f);
+    if (!closed) tell(leaving, vfma(P, s, h));
     give(s);
 }
 
-// Barriers of a tile: its runs are in shared memory (the chain's warp waits), the entering state is (the others wait), and one
+// Barriers of a tile: which one it is is known, its runs are in shared memory (the chain's warp waits), the entering state is (the others wait), and one
 // of the eight warps alone.
 __device__ __forceinline__ void runs_ready() {
     __syncwarp();
@@ -347,10 +344,16 @@ __device__ __forceinline__ void state_ready() {
     asm volatile("bar.arrive 2, %0;" ::"n"(kAll) : "memory");
 }
 __device__ __forceinline__ void state_wait() { asm volatile("bar.sync 2, %0;" ::"n"(kAll) : "memory"); }
+template <bool TELLS> __device__ __forceinline__ void tile_known() {
+    __syncwarp();
+    if constexpr (TELLS) asm volatile("bar.arrive 4, %0;" ::"n"(kAll) : "memory");
+    else asm volatile("bar.sync 4, %0;" ::"n"(kAll) : "memory");
+}
 __device__ __forceinline__ void tile_sync() { asm volatile("bar.sync 3, %0;" ::"n"(kThreads) : "memory"); }
 
-// Tiles in the order in which they are begun: a CTA takes its next one while it works on one, so that the next one's loads run
-// meanwhile.  (Every CTA finishes its tiles in the order it took them, so the first unfinished tile is always being worked on.)
+// Tiles in the order in which they are begun.  A CTA takes the next one when it knows the state that enters the one it has, not
+// earlier: a tile that was taken and not begun holds up all that wait for it.  (With its copies a tile ahead the scan took 188 us for 167 with
+// tiles dealt out in advance, but then one late CTA is late in every round.)
 __device__ __forceinline__ int take_ticket(const GatedArgs& a, int before) {
     return a.planned ? atomicAdd(a.ticket, 1) : before < 0 ? (int)blockIdx.x : before + (int)gridDim.x;
 }
@@ -412,10 +415,8 @@ template <int BYTES> __device__ __forceinline__ void copy_async(void* dst, const
     if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
     else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
 }
-__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// All groups but the last.
 __device__ __forceinline__ void copies_landed() {
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
     tile_sync();
 }
 // Whole tiles of arrays that allow it move 16 bytes at a time; otherwise a thread brings its own elements.  (The tile's base is one for
@@ -450,18 +451,17 @@ template <int VEC> __device__ __forceinline__ bool whole_tile(const GatedArgs& a
 
 // ------------------------------------------------------------------ forward
 
-// A tile as the ninth warp announces it: its place in the chain (past the last: none), itself, its columns, and the first row that
-// begins in or after it.
+// A tile as the ninth warp announces it: its place in the chain (past the last: none), itself, its columns.
 struct TileWord {
-    int o, tile, col, row, begin;
+    int o, tile, col;
 };
 struct TileWords {
-    TileWord at[3];
+    TileWord at[2];
     int closed, needs;
 };
 template <typename E, int VEC> struct FwdShared {
     using V = Val<VEC>;
-    Plane<E, VEC> x[2], g[2], i[2];
+    Plane<E, VEC> x, g, i;
     Edges edges;
     V sp[kWarps][32], sh[kWarps][32], senter[32];
     TileWords w;
@@ -469,11 +469,11 @@ template <typename E, int VEC> struct FwdShared {
 
 // EDGE: the tile has rows that begin or end in it, tokens or channels past the last, or a rate above 1/4.
 template <typename E, int VEC, bool EDGE>
-__device__ __forceinline__ void forward_tile(const GatedArgs& a, const Spot& s, FwdShared<E, VEC>& m_, int buf, bool split, const Rate<Val<VEC>>& rate) {
+__device__ __forceinline__ void forward_tile(const GatedArgs& a, const Spot& s, FwdShared<E, VEC>& m_, bool split, const Rate<Val<VEC>>& rate) {
     using V = Val<VEC>;
     const Edges& edges = m_.edges;
     auto &sp = m_.sp, &sh = m_.sh;
-    auto &mx = m_.x[buf], &mg = m_.g[buf], &mi = m_.i[buf];
+    auto &mx = m_.x, &mg = m_.g, &mi = m_.i;
     const int tid = threadIdx.x;
     auto begins_at = [&](int k) { return EDGE && split ? edges.first[s.warp * kTok + k] : -1; };
     // a token as h -> ka h + kb; where a row begins the state is the row's own, and ka is 0
@@ -531,48 +531,37 @@ __device__ __forceinline__ void forward_tile(const GatedArgs& a, const Spot& s, 
 
 // (not inlined: its registers are not the others')
 template <typename E, int VEC>
-__device__ __noinline__ void forward_edge(const GatedArgs& a, const Spot& s, FwdShared<E, VEC>& m, int buf, bool split, const Rate<Val<VEC>>& rate) {
-    forward_tile<E, VEC, true>(a, s, m, buf, split, rate);
+__device__ __noinline__ void forward_edge(const GatedArgs& a, const Spot& s, FwdShared<E, VEC>& m, bool split, const Rate<Val<VEC>>& rate) {
+    forward_tile<E, VEC, true>(a, s, m, split, rate);
 }
 
-// The loop of both passes: a CTA's tiles, each one's copies issued while the one before is worked on.  load(spot, buffer) issues a tile's
-// copies, work(spot, buffer, hint, rate) does it.  The ninth warp takes the tickets and joins the chain: the runs of the warps from the
-// first (or, backwards, from the last) on.
+// The loop of both passes.  load(spot) issues a tile's copies, work(spot, hint, rate) does it.  The ninth warp takes the tickets and joins
+// the chain: the runs of the warps from the first (or, backwards, from the last) on.
 template <bool BACK, int VEC, typename L, typename W>
 __device__ __forceinline__ void walk_tiles(const GatedArgs& a, TileWords& w, Val<VEC> (&sp)[kWarps][32], Val<VEC> (&sh)[kWarps][32],
                                            Val<VEC> (&senter)[32], L&& load, W&& work) {
     using V = Val<VEC>;
     const uint32_t total = (uint32_t)a.tiles * a.cols;
-    const int lane = threadIdx.x & 31;
-    const bool chain = threadIdx.x >= kThreads;
-    auto announce = [&](uint32_t ticket, TileWord& to) {
-        TileWord n;
-        n.o = a.tiles;
-        if (ticket < total) {
-            n.o = (int)(ticket / (uint32_t)a.cols);
-            n.col = (int)(ticket - (uint32_t)n.o * a.cols);
-            n.tile = BACK ? a.tiles - 1 - n.o : n.o;
-            n.row = a.cu ? a.first[n.tile] : (int)(((uint32_t)n.tile * kTile + a.T - 1) / (uint32_t)a.T);
-            n.begin = row_begin(a, n.row);
-        }
-        to = n;
-    };
     // (offsets that break the contract: the plan has found no tile's first row, and nothing is read by them)
     const bool go = !a.planned || *a.ok;
     if (!go) return;
-    uint32_t ticket = total;       // the last one taken (by one lane)
-    if (threadIdx.x == kThreads) {
-        ticket = take_ticket(a, -1);
-        announce(ticket, w.at[0]);
-        if (ticket < total) ticket = take_ticket(a, (int)ticket);
-        announce(ticket, w.at[1]);
-    }
-    __syncthreads();
-    if (chain) {
+    if (threadIdx.x >= kThreads) {
+        const int lane = threadIdx.x & 31;
+        int before = -1;
         for (int it = 0;; ++it) {
-            const int o = w.at[it % 3].o, c = (w.at[it % 3].col * 32 + lane) * VEC;
+            uint32_t ticket = 0;
+            if (lane == 0) {
+                ticket = take_ticket(a, before);
+                before = (int)ticket;
+                TileWord n;
+                n.o = ticket < total ? (int)(ticket / (uint32_t)a.cols) : a.tiles;
+                n.col = (int)(ticket - (uint32_t)n.o * a.cols);
+                n.tile = BACK ? a.tiles - 1 - n.o : n.o;
+                w.at[it & 1] = n;
+            }
+            tile_known<true>();
+            const int o = w.at[it & 1].o, c = (w.at[it & 1].col * 32 + lane) * VEC;
             if (o >= a.tiles) return;
-            if (lane == 0 && ticket < total) ticket = take_ticket(a, (int)ticket);
             runs_wait();
             V P = sp[BACK ? kWarps - 1 : 0][lane], h = sh[BACK ? kWarps - 1 : 0][lane];
 #pragma unroll
@@ -584,24 +573,22 @@ __device__ __forceinline__ void walk_tiles(const GatedArgs& a, TileWords& w, Val
             V enters;
             join_chain<V>(a, o, c, c < a.C, P, h, w.closed, w.needs, [&](V v) { enters = v; });
             senter[lane] = enters;
-            if (lane == 0) announce(ticket, w.at[(it + 2) % 3]);
             state_ready();
             if (!BACK && a.rec && c < a.C) vstore(a.rec + (size_t)o * a.C + c, enters);
         }
     }
-    auto spot = [&](const TileWord& n) { return spot_of<VEC>(a, n.tile, n.col); };
-    if (w.at[0].o < a.tiles) load(spot(w.at[0]), 0);
-    copies_issued();
     for (int it = 0;; ++it) {
-        const TileWord &now = w.at[it % 3], &next = w.at[(it + 1) % 3];
+        tile_known<false>();
+        const TileWord now = w.at[it & 1];
         if (now.o >= a.tiles) return;
-        if (next.o < a.tiles) load(spot(next), (it + 1) & 1);
-        copies_issued();
-        const Spot s = spot(now);
-        const RowHint hint = {now.row, now.begin};
+        const Spot s = spot_of<VEC>(a, now.tile, now.col);
+        load(s);
+        RowHint hint;
+        hint.row = a.cu ? a.first[s.tile] : (int)(((uint32_t)s.t0 + a.T - 1) / (uint32_t)a.T);
+        hint.begin = row_begin(a, hint.row);
         const Rate<V> rate = rate_of(s.in ? vload<V>(a.a_log + s.c) : vdup<V>(-1e30f));
         copies_landed();
-        work(s, it & 1, hint, rate);
+        work(s, hint, rate);
     }
 }
 
@@ -612,17 +599,17 @@ __global__ void __launch_bounds__(kAll, kFwdCtas) gated_fwd_kernel(const __grid_
     cudaGridDependencySynchronize();
     walk_tiles<false, VEC>(
         a, m.w, m.sp, m.sh, m.senter,
-        [&](const Spot& s, int buf) {
+        [&](const Spot& s) {
             const bool whole = whole_tile<VEC>(a, s);
-            load_plane<E, VEC>(a.x, a.xs, s, whole, a.aligned, m.x[buf]);
-            load_plane<E, VEC>(a.g, a.gs, s, whole, a.aligned, m.g[buf]);
-            load_plane<E, VEC>(a.i, a.is, s, whole, a.aligned, m.i[buf]);
+            load_plane<E, VEC>(a.x, a.xs, s, whole, a.aligned, m.x);
+            load_plane<E, VEC>(a.g, a.gs, s, whole, a.aligned, m.g);
+            load_plane<E, VEC>(a.i, a.is, s, whole, a.aligned, m.i);
         },
-        [&](const Spot& s, int buf, const RowHint& hint, const Rate<Val<VEC>>& rate) {
+        [&](const Spot& s, const RowHint& hint, const Rate<Val<VEC>>& rate) {
             const bool split = has_edges(a, s.t0, hint);
             if (split) find_edges(a, s.t0, hint, m.edges);
-            if (whole_tile<VEC>(a, s) && !split && !rate.wide) forward_tile<E, VEC, false>(a, s, m, buf, split, rate);
-            else forward_edge<E, VEC>(a, s, m, buf, split, rate);
+            if (whole_tile<VEC>(a, s) && !split && !rate.wide) forward_tile<E, VEC, false>(a, s, m, split, rate);
+            else forward_edge<E, VEC>(a, s, m, split, rate);
         });
 }
 
@@ -631,7 +618,7 @@ __global__ void __launch_bounds__(kAll, kFwdCtas) gated_fwd_kernel(const __grid_
 // The gates are formed twice, before and after the chain: keeping them in between would halve the number of CTAs.
 template <typename E, int VEC> struct BwdShared {
     using V = Val<VEC>;
-    Plane<E, VEC> x[2], g[2], i[2], dy[2];
+    Plane<E, VEC> x, g, i, dy;
     Edges edges;
     V sp[kWarps][32], sh[kWarps][32], sq[kWarps][32], sm[kWarps][32], senter[32];
     V e[kTok][kThreads], b[kTok][kThreads];       // e = 1 - a; the inputs, then the states before the tokens
@@ -639,10 +626,10 @@ template <typename E, int VEC> struct BwdShared {
 };
 
 template <typename E, int VEC, bool EDGE>
-__device__ __forceinline__ void backward_tile(const GatedArgs& a, const Spot& s, BwdShared<E, VEC>& m_, int buf, bool split, const Rate<Val<VEC>>& rate) {
+__device__ __forceinline__ void backward_tile(const GatedArgs& a, const Spot& s, BwdShared<E, VEC>& m_, bool split, const Rate<Val<VEC>>& rate) {
     using V = Val<VEC>;
     const int tid = threadIdx.x, warp = s.warp, lane = s.lane, c = s.c;
-    auto &mx = m_.x[buf], &mg = m_.g[buf], &mi = m_.i[buf], &md = m_.dy[buf];
+    auto &mx = m_.x, &mg = m_.g, &mi = m_.i, &md = m_.dy;
     auto begins_at = [&](int k) { return EDGE && split ? m_.edges.first[warp * kTok + k] : -1; };
     auto ends_at = [&](int k) { return EDGE && split ? m_.edges.last[warp * kTok + k] : -1; };
     auto row_of = [&](const float* p, int row) { return p ? vload<V>(p + (size_t)row * a.C + c) : vdup<V>(0.f); };
@@ -741,8 +728,8 @@ __device__ __forceinline__ void backward_tile(const GatedArgs& a, const Spot& s,
 }
 
 template <typename E, int VEC>
-__device__ __noinline__ void backward_edge(const GatedArgs& a, const Spot& s, BwdShared<E, VEC>& m, int buf, bool split, const Rate<Val<VEC>>& rate) {
-    backward_tile<E, VEC, true>(a, s, m, buf, split, rate);
+__device__ __noinline__ void backward_edge(const GatedArgs& a, const Spot& s, BwdShared<E, VEC>& m, bool split, const Rate<Val<VEC>>& rate) {
+    backward_tile<E, VEC, true>(a, s, m, split, rate);
 }
 
 template <typename E, int VEC>
@@ -752,18 +739,18 @@ __global__ void __launch_bounds__(kAll, kBwdCtas) gated_bwd_kernel(const __grid_
     cudaGridDependencySynchronize();
     walk_tiles<true, VEC>(
         a, m.w, m.sq, m.sm, m.senter,
-        [&](const Spot& s, int buf) {
+        [&](const Spot& s) {
             const bool whole = whole_tile<VEC>(a, s);
-            load_plane<E, VEC>(a.x, a.xs, s, whole, a.aligned, m.x[buf]);
-            load_plane<E, VEC>(a.g, a.gs, s, whole, a.aligned, m.g[buf]);
-            load_plane<E, VEC>(a.i, a.is, s, whole, a.aligned, m.i[buf]);
-            load_plane<E, VEC>(a.dy, a.C, s, whole, a.aligned, m.dy[buf]);
+            load_plane<E, VEC>(a.x, a.xs, s, whole, a.aligned, m.x);
+            load_plane<E, VEC>(a.g, a.gs, s, whole, a.aligned, m.g);
+            load_plane<E, VEC>(a.i, a.is, s, whole, a.aligned, m.i);
+            load_plane<E, VEC>(a.dy, a.C, s, whole, a.aligned, m.dy);
         },
-        [&](const Spot& s, int buf, const RowHint& hint, const Rate<Val<VEC>>& rate) {
+        [&](const Spot& s, const RowHint& hint, const Rate<Val<VEC>>& rate) {
             const bool split = has_edges(a, s.t0, hint);
             if (split) find_edges(a, s.t0, hint, m.edges);
-            if (whole_tile<VEC>(a, s) && !split && !rate.wide) backward_tile<E, VEC, false>(a, s, m, buf, split, rate);
-            else backward_edge<E, VEC>(a, s, m, buf, split, rate);
+            if (whole_tile<VEC>(a, s) && !split && !rate.wide) backward_tile<E, VEC, false>(a, s, m, split, rate);
+            else backward_edge<E, VEC>(a, s, m, split, rate);
         });
 }
 
