@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_
 
 // ------------------------------------------------------------------ plan
 
-// Units of every row, then tiles of every unit, each as a running sum.
+// Units of every row, then the cost of every unit, each as a running sum.
 constexpr int kPlanThreads = 1024;
 __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* tmp, int64_t* total) {     // what comes before this thread
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
         int64_t n = 0;
         if (u < units) {
             const int b = a.unit_row[a.units_most + u];
-            n = attn_span(a, attn_row(a, a.unit_row[u], b == 0), b).tiles;
+            n = attn_span(a, attn_row(a, a.unit_row[u], b == 0), b).tiles + a.extra;
         }
         const int64_t at = tiles + block_scan(n, tmp, &total);
         if (u < units) a.start[u] = at;
@@ -247,10 +247,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     const int64_t begin = cut.begin(c1st);
     const int u = unit_of(a, units, begin);
     const int64_t first = a.start[u];
-    const int tiles = (int)(a.start[u + 1] - first), head = (int)((begin - first * a.Hkv) / tiles);
-    const int64_t x = first * a.Hkv + (int64_t)head * tiles;
-    const int c0 = c1st - 1, c1 = cut.owner(x + tiles - 1);
-    if (x == begin || cut.begin(c0) > x) return;          // the item begins here; an earlier one stands for it
+    const int cost = (int)(a.start[u + 1] - first), head = (int)((begin - first * a.Hkv) / cost);
+    const int64_t x = first * a.Hkv + (int64_t)head * cost + a.extra;      // the item's first tile
+    const int c0 = c1st - 1, c1 = cut.owner(x + (cost - a.extra) - 1);
+    if (begin <= x || cut.begin(c0) > x) return;          // no tile of the item lies before; an earlier CTA stands for it
     const AttnRow w = attn_row(a, a.unit_row[u], false);
     const uint32_t r0 = (uint32_t)a.unit_row[a.units_most + u] * a.block;
     const int n = (int)min((uint32_t)w.n * a.G - r0, (uint32_t)a.block), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kSimtThreads, DC > 2 ? 1 : 2) attn_simt_kernel
     __shared__ int64_t own[kAttnDirectRows + 1];
     const AttnUnits units = attn_units(a, own);
     if (units.units <= 0) return;
-    const AttnCut cut(a, units.tiles(a));
+    const AttnCut cut(a, units.cost(a));
     const int cta = blockIdx.x;
     if (cta >= cut.ctas) return;
     const bool vq = a.D % 4 == 0 && a.qs % 4 == 0 && reinterpret_cast<uintptr_t>(a.q) % (4 * sizeof(E)) == 0;
@@ -523,9 +523,10 @@ kda_status attn_check(const kda_attention_dims* d, bool varlen, bool append, Att
 }
 
 // The cut for a kernel of `block` packed rows, `tile` keys and at most `ctas` CTAs.
-void attn_cut(AttnArgs* a, int block, int tile, int ctas) {
+void attn_cut(AttnArgs* a, int block, int tile, int extra, int ctas) {
     a->block = block;
     a->tile = tile;
+    a->extra = extra;
     a->ctas = ctas;
     const int64_t most = ((int64_t)a->tokens * a->G + block - 1) / block + a->rows;      // a row's last block may be short
     a->units_most = (int)(most < (1LL << 30) ? most : (1LL << 30));
@@ -550,13 +551,13 @@ void attn_choose(AttnArgs* a, bool aligned) {
     if (a->dtype == KDA_BF16 && a->D % 8 == 0 && aligned && a->D <= 128 && packed > 32 * (int64_t)a->rows &&
         (int64_t)a->pages * 2 * a->Hkv < (1 << 30)) {      // (a tensor map's coordinate)
         a->kernel = kAttnTc;
-        attn_cut(a, kAttnTcRows, kAttnTcKeys, 152);
+        attn_cut(a, kAttnTcRows, kAttnTcKeys, 3, 152);
     } else if (a->dtype == KDA_BF16 && a->D % 8 == 0 && aligned) {
         a->kernel = kAttnMma;
-        attn_cut(a, a->D > 128 || packed <= 16 * (int64_t)a->rows ? 16 : 32, kAttnMmaKeys, a->D > 128 ? 152 : 304);
+        attn_cut(a, a->D > 128 || packed <= 16 * (int64_t)a->rows ? 16 : 32, kAttnMmaKeys, 2, a->D > 128 ? 152 : 304);
     } else {
         a->kernel = kAttnSimt;
-        attn_cut(a, kSimtRows, kSimtKeys, a->D > 128 ? 152 : 304);
+        attn_cut(a, kSimtRows, kSimtKeys, 1, a->D > 128 ? 152 : 304);
     }
     a->direct = a->per_row && (int64_t)a->per_row * a->G <= a->block && a->rows <= kAttnDirectRows;
 }

@@ -4,8 +4,9 @@
 // The query heads of one key head and the new tokens of a row are one axis of packed query rows, token by token
 // (packed row = token * G + head in the group), so that a tile of keys serves all of them.  A unit is a block of
 // `block` packed rows of one row of the call with every key tile that one of them sees, at least one; an item is a unit
-// for one key head.  All items' key tiles, laid end to end, are cut into equal spans, one to a CTA: a CTA finishes the
-// items that lie in its span, and leaves the sums of those that it shares with other CTAs for the join.
+// for one key head.  An item costs its key tiles and, before them, `extra` tiles for its beginning and end.  All items' costs,
+// laid end to end, are cut into equal spans, one to a CTA: a CTA finishes the items whose tiles lie in its span, and
+// leaves the sums of those that it shares with other CTAs for the join.
 #pragma once
 
 #include "kda_internal.h"
@@ -26,11 +27,11 @@ struct AttnArgs {
     void* out;
     float* lse;
     // the cut
-    int block, tile;                     // packed rows of a unit, keys of a tile
+    int block, tile, extra;              // packed rows of a unit, keys of a tile, an item's cost beside its tiles
     int ctas;                            // most spans; with fewer tiles than that a tile each
     int units_most;
     int* units;                          // [1] units of the call, -1: nothing to do (workspace)
-    int64_t* start;                      // [units + 1] tiles of one key head before each unit (workspace)
+    int64_t* start;                      // [units + 1] cost of one key head before each unit (workspace)
     int* unit_row;                       // [units] row of the call, [units_most + units] block in it (workspace)
     float* part;                         // [2 ctas] sums of shared items: block x D, then block maxima, then block sums
     int* status;
@@ -78,7 +79,7 @@ __device__ __forceinline__ AttnSpan attn_span(const AttnArgs& a, const AttnRow& 
 }
 __device__ __forceinline__ int attn_blocks(const AttnArgs& a, int n) { return (int)(((int64_t)n * a.G + a.block - 1) / a.block); }
 
-// The spans of the CTAs over `total` tiles.
+// The spans of the CTAs over a total cost.
 struct AttnCut {
     int64_t total;
     int ctas;
@@ -93,7 +94,7 @@ constexpr int kAttnDirectRows = 512;
 struct AttnUnits {
     int units;
     const int64_t* start;
-    __device__ __forceinline__ int64_t tiles(const AttnArgs& a) const { return start[units] * a.Hkv; }
+    __device__ __forceinline__ int64_t cost(const AttnArgs& a) const { return start[units] * a.Hkv; }
 };
 // All threads of a CTA; own: [kAttnDirectRows + 1] in shared memory.  The first CTA leaves what it counted to the join.
 __device__ __forceinline__ AttnUnits attn_units(const AttnArgs& a, int64_t* own) {
@@ -105,7 +106,7 @@ __device__ __forceinline__ AttnUnits attn_units(const AttnArgs& a, int64_t* own)
         s.start = a.start;
         return s;
     }
-    for (int r = threadIdx.x; r < a.rows; r += blockDim.x) own[r + 1] = attn_span(a, attn_row(a, r, blockIdx.x == 0), 0).tiles;
+    for (int r = threadIdx.x; r < a.rows; r += blockDim.x) own[r + 1] = attn_span(a, attn_row(a, r, blockIdx.x == 0), 0).tiles + a.extra;
     __syncthreads();
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
@@ -142,11 +143,11 @@ __device__ __forceinline__ AttnUnits attn_units(const AttnArgs& a, int64_t* own)
 // The pieces of a CTA's span, one after the other: tiles [t0, t1) of an item's `tiles`.
 struct AttnWalk {
     int u, head, t0, t1, tiles, row, block;
-    int64_t x, end;
+    int64_t item, end;                   // where the item's cost begins, and where the span ends
     AttnRow w;
     AttnSpan s;
     __device__ __forceinline__ AttnWalk(const AttnArgs& a, const AttnUnits& n, const AttnCut& cut, int cta) {
-        x = cut.begin(cta);
+        const int64_t x = cut.begin(cta);
         end = cut.begin(cta + 1);
         int lo = 0, hi = n.units - 1;
         while (lo < hi) {
@@ -155,30 +156,37 @@ struct AttnWalk {
         }
         u = lo;
         unit(a, n);
-        const int64_t off = x - n.start[u] * a.Hkv;
-        head = (int)(off / tiles);
-        t0 = (int)(off - (int64_t)head * tiles);
-        cut_off();
+        const int cost = tiles + a.extra;
+        item = n.start[u] * a.Hkv;
+        head = (int)((x - item) / cost);
+        item += (int64_t)head * cost;
+        t0 = max((int)(x - item) - a.extra, 0);
+        if (!cut_off(a)) next(a, n);
     }
     __device__ __forceinline__ void unit(const AttnArgs& a, const AttnUnits& n) {
         row = a.direct ? u : a.unit_row[u];
         block = a.direct ? 0 : a.unit_row[a.units_most + u];
         w = attn_row(a, row, false);
         s = attn_span(a, w, block);
-        tiles = (int)(n.start[u + 1] - n.start[u]);
+        tiles = (int)(n.start[u + 1] - n.start[u]) - a.extra;
     }
-    __device__ __forceinline__ void cut_off() { t1 = (int)(end - x < tiles - t0 ? t0 + (end - x) : tiles); }
-    __device__ __forceinline__ bool more() const { return x < end; }
+    // Whether the span reaches a tile of the item.
+    __device__ __forceinline__ bool cut_off(const AttnArgs& a) {
+        const int64_t left = end - item - a.extra;
+        t1 = (int)(left < tiles ? left : tiles);
+        return t1 > t0;
+    }
+    __device__ __forceinline__ bool more() const { return item < end; }
     __device__ __forceinline__ void next(const AttnArgs& a, const AttnUnits& n) {
-        x += t1 - t0;
-        if (x >= end) return;
+        item += tiles + a.extra;
+        if (item >= end) return;
         t0 = 0;
         if (++head == a.Hkv) {
             head = 0;
             ++u;
             unit(a, n);
         }
-        cut_off();
+        if (!cut_off(a)) item = end;         // (what is left pays for the next CTA's beginning)
     }
     __device__ __forceinline__ bool whole() const { return t1 - t0 == tiles; }
     // where its sums go: a CTA shares at most the item it starts inside of and the one it does not finish

@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attn_mma_kernel(c
     __shared__ int64_t own[kAttnDirectRows + 1];
     const AttnUnits units = attn_units(a, own);
     if (units.units <= 0) return;
-    const AttnCut cut(a, units.tiles(a));
+    const AttnCut cut(a, units.cost(a));
     if (cta >= cut.ctas) return;
     const bool vq = a.qs % 8 == 0 && reinterpret_cast<uintptr_t>(a.q) % 16 == 0;
     const bool vo = reinterpret_cast<uintptr_t>(a.out) % 4 == 0;

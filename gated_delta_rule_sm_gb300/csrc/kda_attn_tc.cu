@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
     const AttnUnits units = attn_units(a, own);
     if (units.units <= 0) return;
-    const AttnCut cut(a, units.tiles(a));
+    const AttnCut cut(a, units.cost(a));
     if (cta >= cut.ctas) return;
     if (tid == 0) {
         for (int i = 0; i < kBars; ++i) mbar_init(&bar[i], i >= kP ? 4 : i == kQFull ? 2 : 1);
