@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
 
 // ------------------------------------------------------------------ join
 
-// A CTA takes some rows of one item (a unit for one key head) that several CTAs share; the others are done already.  With few
+// A CTA takes some rows of one item (a unit for one key head) that several CTAs share.  With few
 // parts a warp takes a row; with many (a few rows over a long cache) the warps split the parts of a row, four of each
 // warp's on the way at once, since then it is their latency that counts.
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinFew = 4;
@@ -222,40 +222,15 @@ __device__ __forceinline__ void join_write(const AttnArgs& a, size_t at, const J
         if (k * 32 + lane < a.D) store_act(a.out, at * a.D + k * 32 + lane, s.o[k] * inv, a.dtype);
     if (a.lse && lane == 0) a.lse[at] = s.sum == 0.f ? -INFINITY : (base + log2f(s.sum)) * 0.6931471805599453f;
 }
-// The last unit that begins at or before tile x, by 32 units at a time (one warp).
-__device__ __forceinline__ int unit_of(const AttnArgs& a, int units, int64_t x) {
-    const int lane = threadIdx.x & 31;
-    int lo = 0, n = units;
-    while (n > 1) {
-        const int step = (n + 31) / 32;
-        const unsigned hit = __ballot_sync(0xffffffffu, lane * step < n && a.start[lo + lane * step] * a.Hkv <= x);
-        const int k = 31 - __clz(hit | 1u);
-        n = min(step, n - k * step);
-        lo += k * step;
-    }
-    return lo;
-}
-
-// blockIdx.x + 1: a CTA of the attention whose span may begin inside an item; the first such one of an item stands for it.
+// blockIdx.x: the CTA of the attention that began the item.
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnArgs a, int rows_each) {
     __shared__ float so[kJoinWarps][256], ss[kJoinWarps];
     cudaGridDependencySynchronize();
-    const int units = *a.units, c1st = blockIdx.x + 1;
-    if (units <= 0) return;
-    const AttnCut cut(a, a.start[units] * a.Hkv);
-    if (c1st >= cut.ctas) return;
-    const int64_t begin = cut.begin(c1st);
-    const int u = unit_of(a, units, begin);
-    const int64_t first = a.start[u];
-    const int cost = (int)(a.start[u + 1] - first), head = (int)((begin - first * a.Hkv) / cost);
-    const int64_t x = first * a.Hkv + (int64_t)head * cost + a.extra;      // the item's first tile
-    const int c0 = c1st - 1, c1 = cut.owner(x + (cost - a.extra) - 1);
-    if (begin <= x || cut.begin(c0) > x) return;          // no tile of the item lies before; an earlier CTA stands for it
-    const AttnRow w = attn_row(a, a.unit_row[u], false);
-    const uint32_t r0 = (uint32_t)a.unit_row[a.units_most + u] * a.block;
-    const int n = (int)min((uint32_t)w.n * a.G - r0, (uint32_t)a.block), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int i0 = blockIdx.y * rows_each, i1 = min(n, i0 + rows_each);
-    const bool few = c1 - c0 < kJoinFew;
+    const AttnShared it = a.shared[blockIdx.x];
+    const int i0 = blockIdx.y * rows_each, i1 = min(it.rows, i0 + rows_each), c0 = blockIdx.x, c1 = it.last;
+    if (i0 >= i1) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool few = rows_each > 1 || c1 - c0 < kJoinFew;      // a warp to a row
     for (int i = few ? i0 + warp : i0; i < i1; i += few ? kJoinWarps : 1) {
         float top = -INFINITY;
         for (int c = c0 + lane; c <= c1; c += 32)
@@ -263,8 +238,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         const float base = top == -INFINITY ? 0.f : top;
-        const uint32_t row = r0 + i, token = row / (uint32_t)a.G;
-        const size_t at = (size_t)(w.first + token) * a.Hq + head * a.G + (row - token * a.G);
+        const uint32_t row = (uint32_t)it.first_row + i, token = row / (uint32_t)a.G;
+        const size_t at = (size_t)(it.token + (int)token) * a.Hq + it.head + (row - token * a.G);
         JoinSum s = join_parts(a, c0, c1, few ? 0 : warp, few ? 1 : kJoinWarps, i, base);
         if (few) {
             join_write(a, at, s, base);
@@ -449,6 +424,7 @@ __global__ void __launch_bounds__(kSimtThreads, DC > 2 ? 1 : 2) attn_simt_kernel
                 }
             }
         }
+        if (tid == 0) p.tell_join(a, cut, cta);
         float* part = a.part + p.slot(cta) * attn_part_floats(a);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -541,6 +517,7 @@ size_t attn_layout(char* ws, AttnArgs* a) {
     a->units = reinterpret_cast<int*>(take(4));
     a->start = reinterpret_cast<int64_t*>(take(8 * ((size_t)a->units_most + 1)));
     a->unit_row = reinterpret_cast<int*>(take(8 * (size_t)a->units_most));
+    a->shared = reinterpret_cast<AttnShared*>(take(sizeof(AttnShared) * (size_t)a->ctas));
     a->part = reinterpret_cast<float*>(take((size_t)2 * a->ctas * a->block * (a->D + 2) * 4));
     return o;
 }
@@ -657,7 +634,7 @@ kda_status kda_pages_attention(const kda_attention_dims* dims, const void* q, co
     if (e != cudaSuccess) return KDA_ERR_CUDA;
     // rows of a block that may exist; a CTA for each where they are few
     const int64_t longest = (cu_seqlens ? a.tokens : a.per_row) * (int64_t)a.G;
-    const int rows = (int)(longest < a.block ? longest : a.block), each = a.block <= 32 ? 1 : 4 * kJoinWarps;
+    const int rows = (int)(longest < a.block ? longest : a.block), each = a.block <= 32 ? 1 : 2 * kJoinWarps;
     timing_pre(stream, K_ATTN_JOIN);
     // (launched while the attention still runs; it waits for its end itself)
     if (a.ctas > 1)

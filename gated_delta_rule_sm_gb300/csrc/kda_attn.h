@@ -15,6 +15,12 @@ namespace kda {
 
 enum AttnKernel { kAttnSimt, kAttnMma, kAttnTc };
 
+// What a CTA tells the join of the item that it begins and does not finish (rows 0: there is none): the first token's index and query head,
+// the first of its packed rows, how many there are, and the last CTA with a part of it.
+struct AttnShared {
+    int token, head, first_row, rows, last;
+};
+
 struct AttnArgs {
     int rows, tokens, per_row;           // per_row: tokens of a row without cu
     int Hq, Hkv, G, D, dtype;
@@ -33,6 +39,7 @@ struct AttnArgs {
     int* units;                          // [1] units of the call, -1: nothing to do (workspace)
     int64_t* start;                      // [units + 1] cost of one key head before each unit (workspace)
     int* unit_row;                       // [units] row of the call, [units_most + units] block in it (workspace)
+    AttnShared* shared;                  // [ctas] (workspace)
     float* part;                         // [2 ctas] sums of shared items: block x D, then block maxima, then block sums
     int* status;
 };
@@ -96,10 +103,11 @@ struct AttnUnits {
     const int64_t* start;
     __device__ __forceinline__ int64_t cost(const AttnArgs& a) const { return start[units] * a.Hkv; }
 };
-// All threads of a CTA; own: [kAttnDirectRows + 1] in shared memory.  The first CTA leaves what it counted to the join.
+// All threads of a CTA; own: [kAttnDirectRows + 1] in shared memory.
 __device__ __forceinline__ AttnUnits attn_units(const AttnArgs& a, int64_t* own) {
     AttnUnits s;
     cudaTriggerProgrammaticLaunchCompletion();       // the join may be launched
+    if (threadIdx.x == 0) a.shared[blockIdx.x].rows = 0;
     if (!a.direct) {
         cudaGridDependencySynchronize();             // (the plan)
         s.units = *a.units;
@@ -125,16 +133,6 @@ __device__ __forceinline__ AttnUnits attn_units(const AttnArgs& a, int64_t* own)
         if (lane == 0) own[0] = 0;
     }
     __syncthreads();
-    if (blockIdx.x == 0) {
-        for (int r = threadIdx.x; r <= a.rows; r += blockDim.x) {
-            a.start[r] = own[r];
-            if (r < a.rows) {
-                a.unit_row[r] = r;
-                a.unit_row[a.units_most + r] = 0;
-            }
-        }
-        if (threadIdx.x == 0) *a.units = a.rows;
-    }
     s.units = a.rows;
     s.start = own;
     return s;
@@ -189,6 +187,11 @@ struct AttnWalk {
         if (!cut_off(a)) item = end;         // (what is left pays for the next CTA's beginning)
     }
     __device__ __forceinline__ bool whole() const { return t1 - t0 == tiles; }
+    // Tells the join of an item that this CTA begins and does not finish (by thread 0).
+    __device__ __forceinline__ void tell_join(const AttnArgs& a, const AttnCut& cut, int cta) const {
+        if (t0 == 0 && t1 < tiles)
+            a.shared[cta] = {w.first, head * a.G, (int)first_row(a), rows(a), cut.owner(item + a.extra + tiles - 1)};
+    }
     // where its sums go: a CTA shares at most the item it starts inside of and the one it does not finish
     __device__ __forceinline__ int slot(int cta) const { return 2 * cta + (t0 == 0); }
     __device__ __forceinline__ uint32_t first_row(const AttnArgs& a) const { return (uint32_t)block * a.block; }

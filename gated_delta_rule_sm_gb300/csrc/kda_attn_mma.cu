@@ -292,6 +292,7 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attn_mma_kernel(c
                         make_float2(o[m][k][2 * h] * f, o[m][k][2 * h + 1] * f);
             }
         __syncthreads();
+        if (tid == 0) p.tell_join(a, cut, cta);
         float* part = a.part + p.slot(cta) * attn_part_floats(a);
         for (int i = tid; i < n * (DP / 2); i += kThreads) {
             const int r = i / (DP / 2), d = i % (DP / 2) * 2;

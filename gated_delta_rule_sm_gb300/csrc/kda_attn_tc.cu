@@ -286,6 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             const AttnWalk::Place to_row = p.place(a, live ? 128 * tile + row : 0);
             const size_t at = (size_t)to_row.token * a.Hq + to_row.head;
             const float inv = whole ? l > 0.f ? 1.f / l : l == 0.f ? 0.f : l : 1.f;
+            if (tid == 0) p.tell_join(a, cut, cta);
             float* part = a.part + p.slot(cta) * attn_part_floats(a);
             const int prow = 128 * tile + row;
             const bool vec = reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
