@@ -349,10 +349,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 for (AttnWalk p(a, units, cut, cta); ok && p.more(); p.next(a, units), ++pieces) {
                     const int tiles = p.rows(a) > 128 ? 2 : 1, last = tiles - 1;
                     ok = wait1(kQFull, pieces & 1) && keys(g, 0);
-                    for (int tile = 0; ok && tile < tiles; ++tile) {
+                    steps<2>([&](auto tile) {
+                        if (!ok || tile >= tiles) return;
                         ok = n[tile] == 0 || wait1(kO + tile, (n[tile] - 1) & 1);      // P of the last piece has been read
                         if (ok) scores(tile, g);
-                    }
+                    });
                     if (!ok) break;
                     mma_commit(&bar[kEmpty + 2 * g % L::SLOTS]);
                     if (p.t1 - p.t0 == 1) mma_commit(&bar[kQEmpty]);
@@ -360,22 +361,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                         const bool next = t + 1 < p.t1;
                         const uint32_t vs = (2 * g + 1) % L::SLOTS, sv = desc_lo(smem_u32(smem + L::KV + vs * L::TILE), WIDE ? 1024 : HALF);
                         ok = keys(g, 1);
-#pragma unroll 1
-                        for (int tile = 0; ok && tile < tiles; ++tile) {
+                        // (a copy of the code for each tile: its counters stay in registers)
+                        steps<2>([&](auto tile) {
+                            if (!ok || tile >= tiles) return;
                             const uint32_t ts = tmem + TS + 128 * tile, to = tmem + TO + 128 * tile;
                             ok = wait1(kP + 2 * tile, n[tile] & 1) && (t > p.t0 || mine[tile] == 0 || wait1(kOFree + tile, (mine[tile] - 1) & 1));
-                            if (!ok) break;
+                            if (!ok) return;
                             tc_fence_after();
                             steps<KT / 32>([&](auto k) { mma_ts<k * STEP>(to, ts + 8 * k, sv, hi, idO, t > p.t0 || k > 0); });
                             ok = wait1(kP + 2 * tile + 1, n[tile] & 1);
-                            if (!ok) break;
+                            if (!ok) return;
                             tc_fence_after();
                             steps<KT / 32>([&](auto k) { mma_ts<(k + KT / 32) * STEP>(to, ts + 8 * (k + KT / 32), sv, hi, idO, 1); });
                             mma_commit(&bar[kO + tile]);
                             if (tile == last) mma_commit(&bar[kEmpty + vs]);
                             if (next) {
                                 ok = (tile || keys(g + 1, 0)) && wait1(kO + tile, n[tile] & 1);
-                                if (!ok) break;
+                                if (!ok) return;
                                 scores(tile, g + 1);
                                 if (tile == last) {
                                     mma_commit(&bar[kEmpty + (2 * g + 2) % L::SLOTS]);
@@ -383,10 +385,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                                 }
                             }
                             ++n[tile];
-                        }
+                        });
                     }
                     if (!ok) break;
-                    for (int tile = 0; tile < tiles; ++tile) ++mine[tile];
+                    steps<2>([&](auto tile) { mine[tile] += tile < tiles; });
                 }
             }
             __syncwarp();

@@ -539,12 +539,6 @@ __device__ __forceinline__ void forward_tile(const GatedArgs& a, const Spot& s, 
         }
 }
 
-// (not inlined: its registers are not the others')
-template <typename E, int VEC>
-__device__ __noinline__ void forward_edge(const GatedArgs& a, const Spot& s, FwdShared<E, VEC>& m, bool split, const Rate<Val<VEC>>& rate) {
-    forward_tile<E, VEC, true>(a, s, m, split, rate);
-}
-
 // The loop of both passes.  load(spot) issues a tile's copies, work(spot, hint, rate) does it, soon(tile, columns)
 // asks the L2 for a later one (backwards alone: 301 -> 287 us there, 154 -> 159 us forward).  The ninth warp takes the tickets and joins
 // the chain: the runs of the warps from the first (or, backwards, from the last) on.
@@ -628,7 +622,7 @@ __global__ void __launch_bounds__(kAll, kFwdCtas) gated_fwd_kernel(const __grid_
             const bool split = has_edges(a, s.t0, hint);
             if (split) find_edges(a, s.t0, hint, m.edges);
             if (whole_tile<VEC>(a, s) && !split && !rate.wide) forward_tile<E, VEC, false>(a, s, m, split, rate);
-            else forward_edge<E, VEC>(a, s, m, split, rate);
+            else forward_tile<E, VEC, true>(a, s, m, split, rate);
         });
 }
 
@@ -747,11 +741,6 @@ __device__ __forceinline__ void backward_tile(const GatedArgs& a, const Spot& s,
 }
 
 template <typename E, int VEC>
-__device__ __noinline__ void backward_edge(const GatedArgs& a, const Spot& s, BwdShared<E, VEC>& m, bool split, const Rate<Val<VEC>>& rate) {
-    backward_tile<E, VEC, true>(a, s, m, split, rate);
-}
-
-template <typename E, int VEC>
 __global__ void __launch_bounds__(kAll, kBwdCtas) gated_bwd_kernel(const __grid_constant__ GatedArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];
     BwdShared<E, VEC>& m = *reinterpret_cast<BwdShared<E, VEC>*>(smem);
@@ -776,7 +765,7 @@ __global__ void __launch_bounds__(kAll, kBwdCtas) gated_bwd_kernel(const __grid_
             const bool split = has_edges(a, s.t0, hint);
             if (split) find_edges(a, s.t0, hint, m.edges);
             if (whole_tile<VEC>(a, s) && !split && !rate.wide) backward_tile<E, VEC, false>(a, s, m, split, rate);
-            else backward_edge<E, VEC>(a, s, m, split, rate);
+            else backward_tile<E, VEC, true>(a, s, m, split, rate);
         });
 }
 
