@@ -15,8 +15,8 @@
 // zero times those need not be zero: its values are copied row by row with cp.async, zeros for the others.  K is read
 // K-major, V MN-major (keys as K), P from TMEM.
 //
-// Roles (12 warps): 0-3 and 4-7 the softmax of the two tiles, 8 issues the products, 10 copies keys and values, 9 and 11
-// Q.  The products come in the order P V and next S of one tile, P V and next S of the other, so that one's run
+// Roles (12 warps): 0-3 and 4-7 the softmax of the two tiles, 8 issues the products, 10 copies keys, 9 values, and
+// 9 and 11 Q.  The products come in the order P V and next S of one tile, P V and next S of the other, so that one's run
 // while the other's exponentials do.  (A thread for each tile's products, in no order between them, let both tiles fall into
 // step: products, then exponentials, 4430 cycles a step.)  P of a tile lies where its next S goes, hence the next S is issued when P
 // V is complete.  P is handed over in halves of 64 keys.
@@ -73,19 +73,28 @@ constexpr uint32_t TS = 0, TO = 256, TCOLS = 512;       // + 128 tile
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | (lbo >> 4 << 16); }
 __host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo) { return (sbo >> 4) | (1u << 14) | (2u << 29); }
 template <int OA, int OB>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 da, db;\n\tadd.u32 x, %1, %5;\n\tadd.u32 y, %2, %6;\n\t"
-        "mov.b64 da, {x, %7};\n\tmov.b64 db, {y, %8};\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}\n" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(OA >> 4), "n"(OB >> 4), "r"(desc_hi(1024)), "r"(hi));
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 x, y;\n\t.reg .b64 da, db;\n\tadd.u32 x, %1, %5;\n\tadd.u32 y, %2, %6;\n\t"
+        "mov.b64 da, {x, %7};\n\tmov.b64 db, {y, %8};\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %9, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(OA >> 4), "n"(OB >> 4), "r"(desc_hi(1024)), "r"(hi), "r"(leader));
 }
 template <int OB>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b32 y;\n\t.reg .b64 db;\n\tadd.u32 y, %2, %5;\n\tmov.b64 db, {y, %6};\n\t"
-        "setp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}\n" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(OB >> 4), "r"(hi));
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 y;\n\t.reg .b64 db;\n\tadd.u32 y, %2, %5;\n\tmov.b64 db, {y, %6};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(OB >> 4), "r"(hi), "r"(leader));
+}
+__device__ __forceinline__ void commit(uint32_t leader, uint64_t* mbar) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_u32(mbar)), "r"(leader) : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(r));
+    return r;
 }
 template <int N, typename F, int I = 0>
 __device__ __forceinline__ void steps(F&& f) {
@@ -330,20 +339,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 8) {
             // ------------------------------------------------------------ products
-            if (lane == 0) {
+            {
+                // (the whole warp runs the loop and one lane issues: what the products take stays in uniform registers)
+                const uint32_t leader = elect_one();
+                const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), sm = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
                 constexpr uint32_t idS = idesc_bf16(128, KT, 0, 0), idO = idesc_bf16(128, DP, 0, 1), hi = desc_hi(WIDE ? 2048 : 1024);
                 constexpr int STEP = WIDE ? 4096 : 2048;       // bytes of 16 keys' values in a half
                 uint32_t n[2] = {0, 0}, mine[2] = {0, 0}, g = 0, pieces = 0;     // key tiles and pieces of each query tile, and of both
                 auto keys = [&](uint32_t at, int v) { return wait1(kFull + (2 * at + v) % L::SLOTS, (2 * at + v) / L::SLOTS & 1); };
                 auto scores = [&](int tile, uint32_t at) {
-                    const uint32_t sq = desc_lo(smem_u32(smem + L::Q + tile * L::TILE), 16), ts = tmem + TS + 128 * tile;
-                    const uint32_t sk = desc_lo(smem_u32(smem + L::KV + 2 * at % L::SLOTS * L::TILE), 16);
+                    const uint32_t sq = desc_lo((sm + L::Q + tile * L::TILE), 16), ts = tm + TS + 128 * tile;
+                    const uint32_t sk = desc_lo((sm + L::KV + 2 * at % L::SLOTS * L::TILE), 16);
                     tc_fence_after();
                     steps<4 * NB>([&](auto k) {
                         constexpr int o = (k >> 2) * HALF + (k & 3) * 32;
-                        mma_ss<o, WIDE ? (k >> 2) * 1024 + (k & 3) * 32 : o>(ts, sq, sk, hi, idS, k > 0);
+                        mma_ss<o, WIDE ? (k >> 2) * 1024 + (k & 3) * 32 : o>(leader, ts, sq, sk, hi, idS, k > 0);
                     });
-                    mma_commit(&bar[kS + tile]);
+                    commit(leader, &bar[kS + tile]);
                 };
                 bool ok = true;
                 for (AttnWalk p(a, units, cut, cta); ok && p.more(); p.next(a, units), ++pieces) {
@@ -355,33 +367,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                         if (ok) scores(tile, g);
                     });
                     if (!ok) break;
-                    mma_commit(&bar[kEmpty + 2 * g % L::SLOTS]);
-                    if (p.t1 - p.t0 == 1) mma_commit(&bar[kQEmpty]);
+                    commit(leader, &bar[kEmpty + 2 * g % L::SLOTS]);
+                    if (p.t1 - p.t0 == 1) commit(leader, &bar[kQEmpty]);
                     for (int t = p.t0; ok && t < p.t1; ++t, ++g) {
                         const bool next = t + 1 < p.t1;
-                        const uint32_t vs = (2 * g + 1) % L::SLOTS, sv = desc_lo(smem_u32(smem + L::KV + vs * L::TILE), WIDE ? 1024 : HALF);
+                        const uint32_t vs = (2 * g + 1) % L::SLOTS, sv = desc_lo((sm + L::KV + vs * L::TILE), WIDE ? 1024 : HALF);
                         ok = keys(g, 1);
                         // (a copy of the code for each tile: its counters stay in registers)
                         steps<2>([&](auto tile) {
                             if (!ok || tile >= tiles) return;
-                            const uint32_t ts = tmem + TS + 128 * tile, to = tmem + TO + 128 * tile;
+                            const uint32_t ts = tm + TS + 128 * tile, to = tm + TO + 128 * tile;
                             ok = wait1(kP + 2 * tile, n[tile] & 1) && (t > p.t0 || mine[tile] == 0 || wait1(kOFree + tile, (mine[tile] - 1) & 1));
                             if (!ok) return;
                             tc_fence_after();
-                            steps<KT / 32>([&](auto k) { mma_ts<k * STEP>(to, ts + 8 * k, sv, hi, idO, t > p.t0 || k > 0); });
+                            steps<KT / 32>([&](auto k) { mma_ts<k * STEP>(leader, to, ts + 8 * k, sv, hi, idO, t > p.t0 || k > 0); });
                             ok = wait1(kP + 2 * tile + 1, n[tile] & 1);
                             if (!ok) return;
                             tc_fence_after();
-                            steps<KT / 32>([&](auto k) { mma_ts<(k + KT / 32) * STEP>(to, ts + 8 * (k + KT / 32), sv, hi, idO, 1); });
-                            mma_commit(&bar[kO + tile]);
-                            if (tile == last) mma_commit(&bar[kEmpty + vs]);
+                            steps<KT / 32>([&](auto k) { mma_ts<(k + KT / 32) * STEP>(leader, to, ts + 8 * (k + KT / 32), sv, hi, idO, 1); });
+                            commit(leader, &bar[kO + tile]);
+                            if (tile == last) commit(leader, &bar[kEmpty + vs]);
                             if (next) {
                                 ok = (tile || keys(g + 1, 0)) && wait1(kO + tile, n[tile] & 1);
                                 if (!ok) return;
                                 scores(tile, g + 1);
                                 if (tile == last) {
-                                    mma_commit(&bar[kEmpty + (2 * g + 2) % L::SLOTS]);
-                                    if (t + 2 == p.t1) mma_commit(&bar[kQEmpty]);
+                                    commit(leader, &bar[kEmpty + (2 * g + 2) % L::SLOTS]);
+                                    if (t + 2 == p.t1) commit(leader, &bar[kQEmpty]);
                                 }
                             }
                             ++n[tile];
@@ -392,86 +404,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 }
             }
             __syncwarp();
-        } else if (warp == 10) {
-            // ------------------------------------------------------------ keys and values
-            constexpr int PARTS = WIDE ? 1 : NB;              // copies of a box's keys
-            const int R = 1 << box_log2, boxes = (KT >> box_log2) * PARTS, nowhere = a.pages * 2 * a.Hkv;
-            uint32_t g = 0;
-            bool ok = true;
-            for (AttnWalk p(a, units, cut, cta); ok && p.more(); p.next(a, units)) {
-                const int32_t* pages = a.table + (size_t)max(p.w.seq, 0) * a.max_pages;
-                // the map's third coordinate of the keys (values: + Hkv) of the box that begins at `key`
-                auto look = [&](int key) {
-                    if (key + R <= p.s.begin || key >= p.s.end) return nowhere;
-                    const int page = pages[key / a.pt];
-                    if (page >= 0 && page < a.pages) return page * 2 * a.Hkv + p.head;
-                    record_error(a.status, KDA_ERR_INVALID_ARG);
-                    return nowhere;
-                };
-                auto cut_box = [&](int key) { return (key < p.s.begin && key + R > p.s.begin) || (key < p.s.end && key + R > p.s.end); };
-                const int mine = (lane / PARTS) << box_log2;       // this lane's first box: its keys in a tile
-                int next = look((p.s.tile0 + p.t0) * KT + mine);
-                for (int t = p.t0; ok && t < p.t1; ++t) {
-                    const int k0 = (p.s.tile0 + t) * KT, first = next;
-                    if (t + 1 < p.t1) next = look(k0 + KT + mine);
-#pragma unroll 1
-                    for (int kv = 0; kv < 2; ++kv, ++g) {
-                        const int slot = g % L::SLOTS;
-                        if (g >= L::SLOTS && !wait(kEmpty + slot, (g / L::SLOTS - 1) & 1)) { ok = false; break; }
-                        const uint32_t to = smem_u32(smem + L::KV + slot * L::TILE);
-                        int by_row = 0;
-                        if (kv && R > 1) {
-                            // (the box of the window's begin and that of the end; one box may be both)
-                            int done = -1;
-#pragma unroll 1
-                            for (int edge : {p.s.begin, p.s.end}) {
-                                const int key = edge & ~(R - 1);
-                                if (key == edge || key < k0 || key >= k0 + KT || key == done) continue;
-                                done = key;
-                                ++by_row;
-                                const int z = look(key);
-                                const char* from = static_cast<const char*>(a.pool) + ((int64_t)(z + a.Hkv) * a.pt + key % a.pt) * (a.D * 2);
-#pragma unroll 1
-                                for (int i = lane; i < R * 8 * NB; i += 32) {
-                                    const int r = i / (8 * NB), c = i % (8 * NB);
-                                    const bool in = z != nowhere && key + r >= p.s.begin && key + r < p.s.end && c * 8 < a.D;
-                                    cp_async16(to + key_piece<WIDE>(key - k0 + r, c), in ? from + (int64_t)r * a.D * 2 + c * 16 : a.pool, in ? 16 : 0);
-                                }
-                            }
-                            if (by_row) {
-                                cp_commit();
-                                cp_wait<0>();
-                                fence_async_smem();
-                                __syncwarp();
-                            }
-                        }
-                        if (lane == 0) mbar_expect_tx(&bar[kFull + slot], ((KT >> box_log2) - by_row) * NB * R * 128);
-                        __syncwarp();
-#pragma unroll 1
-                        for (int i = lane; i < boxes; i += 32) {
-                            const int at = (i / PARTS) << box_log2, key = k0 + at;
-                            const int z = (i < 32 ? first : look(key));
-                            if (kv && R > 1 && cut_box(key)) continue;
-                            const int page = z == nowhere ? nowhere : z + kv * a.Hkv, in_page = key % a.pt;
-                            if constexpr (WIDE) tma_load_5d_to(to + at * 256, &map, in_page >> 3, page, &bar[kFull + slot]);
-                            else tma_load_3d_to(to + (i % NB) * HALF + at * 128, &map, (i % NB) * 64, in_page, page, &bar[kFull + slot]);
-                        }
-                        __syncwarp();
-                    }
-                }
-            }
         } else {
-            // ------------------------------------------------------------ Q, a tile each of warps 9 and 11
+            // ------------------------------------------------------------ Q: a tile each of warps 9 and 11
             constexpr int PER = DP / 8, EACH = 32 / PER;      // pieces of a row, rows of one round of the lanes
             const int c = lane % PER, sub = lane / PER;
             const bool column = c * 8 < a.D, vq = a.qs % 8 == 0 && reinterpret_cast<uintptr_t>(a.q) % 16 == 0;
-            const int tile = warp == 11, each_token = EACH / a.G, each_head = EACH % a.G;
-            const uint32_t sq = smem_u32(smem + L::Q + tile * L::TILE);
+            const int each_token = EACH / a.G, each_head = EACH % a.G;
             uint32_t pieces = 0;
-            for (AttnWalk p(a, units, cut, cta); p.more(); p.next(a, units), ++pieces) {
-                if (pieces && !wait(kQEmpty, (pieces - 1) & 1)) break;
+            auto queries = [&](const AttnWalk& p, int tile) {
+                if (pieces && !wait(kQEmpty, (pieces - 1) & 1)) return false;
+                ++pieces;
                 const int rows = p.rows(a) - 128 * tile;
                 if (rows > 0) {
+                    const uint32_t sq = smem_u32(smem + L::Q + tile * L::TILE);
                     // (rows one after the other: no division but the first)
                     AttnWalk::Place at = p.place(a, 128 * tile + sub);
                     at.head -= p.head * a.G;
@@ -503,7 +448,75 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 cp_wait<0>();
                 fence_async_smem();
                 arrive_warp(kQFull);
+                return true;
+            };
+            // ------------------------------------------------------------ keys (warp 10) and values (warp 9)
+            constexpr int PARTS = WIDE ? 1 : NB;              // copies of a box's keys
+            const int kv = warp == 9, R = 1 << box_log2, boxes = (KT >> box_log2) * PARTS, nowhere = a.pages * 2 * a.Hkv;
+            uint32_t g = 0;                                   // key tiles
+            bool ok = true;
+            for (AttnWalk p(a, units, cut, cta); ok && p.more(); p.next(a, units)) {
+                if (warp != 10) ok = queries(p, warp == 9);
+                if (warp == 11) continue;
+                const int32_t* pages = a.table + (size_t)max(p.w.seq, 0) * a.max_pages;
+                // the map's third coordinate of the keys (values: + Hkv) of the box that begins at `key`
+                auto look = [&](int key) {
+                    if (key + R <= p.s.begin || key >= p.s.end) return nowhere;
+                    const int page = pages[key / a.pt];
+                    if (page >= 0 && page < a.pages) return page * 2 * a.Hkv + p.head;
+                    record_error(a.status, KDA_ERR_INVALID_ARG);
+                    return nowhere;
+                };
+                auto cut_box = [&](int key) { return (key < p.s.begin && key + R > p.s.begin) || (key < p.s.end && key + R > p.s.end); };
+                const int mine = (lane / PARTS) << box_log2;       // this lane's first box: its keys in a tile
+                int next = look((p.s.tile0 + p.t0) * KT + mine);
+                for (int t = p.t0; ok && t < p.t1; ++t, ++g) {
+                    const int k0 = (p.s.tile0 + t) * KT, first = next;
+                    if (t + 1 < p.t1) next = look(k0 + KT + mine);
+                    const uint32_t n = 2 * g + kv, slot = n % L::SLOTS;
+                    if (n >= L::SLOTS && !wait(kEmpty + slot, (n / L::SLOTS - 1) & 1)) { ok = false; break; }
+                    const uint32_t to = smem_u32(smem + L::KV + slot * L::TILE);
+                    int by_row = 0;
+                    if (kv && R > 1) {
+                        // (the box of the window's begin and that of the end; one box may be both)
+                        int done = -1;
+#pragma unroll 1
+                        for (int edge : {p.s.begin, p.s.end}) {
+                            const int key = edge & ~(R - 1);
+                            if (key == edge || key < k0 || key >= k0 + KT || key == done) continue;
+                            done = key;
+                            ++by_row;
+                            const int z = look(key);
+                            const char* from = static_cast<const char*>(a.pool) + ((int64_t)(z + a.Hkv) * a.pt + key % a.pt) * (a.D * 2);
+#pragma unroll 1
+                            for (int i = lane; i < R * 8 * NB; i += 32) {
+                                const int r = i / (8 * NB), b = i % (8 * NB);
+                                const bool in = z != nowhere && key + r >= p.s.begin && key + r < p.s.end && b * 8 < a.D;
+                                cp_async16(to + key_piece<WIDE>(key - k0 + r, b), in ? from + (int64_t)r * a.D * 2 + b * 16 : a.pool, in ? 16 : 0);
+                            }
+                        }
+                        if (by_row) {
+                            cp_commit();
+                            cp_wait<0>();
+                            fence_async_smem();
+                            __syncwarp();
+                        }
+                    }
+                    if (lane == 0) mbar_expect_tx(&bar[kFull + slot], ((KT >> box_log2) - by_row) * NB * R * 128);
+                    __syncwarp();
+#pragma unroll 1
+                    for (int i = lane; i < boxes; i += 32) {
+                        const int at = (i / PARTS) << box_log2, key = k0 + at;
+                        const int z = (i < 32 ? first : look(key));
+                        if (kv && R > 1 && cut_box(key)) continue;
+                        const int page = z == nowhere ? nowhere : z + kv * a.Hkv, in_page = key % a.pt;
+                        if constexpr (WIDE) tma_load_5d_to(to + at * 256, &map, in_page >> 3, page, &bar[kFull + slot]);
+                        else tma_load_3d_to(to + (i % NB) * HALF + at * 128, &map, (i % NB) * 64, in_page, page, &bar[kFull + slot]);
+                    }
+                    __syncwarp();
+                }
             }
+            cp_wait<0>();
         }
     }
     __syncthreads();
