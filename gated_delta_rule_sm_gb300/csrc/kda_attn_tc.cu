@@ -8,8 +8,8 @@
 // a row's life, the row's output is rescaled in TMEM, between the products that add to it.
 //
 // Operands: K and V lie in one ring of four 32 KB slots (K, V, K, V, ...), rows of 128 bytes in the 128-byte swizzle, put there
-// by TMA in boxes of R keys, the largest power of two that divides the page's tokens, so that a box lies in one page; a lane
-// of the copying warp looks up the page of one box and issues its copy.  With D = 128 and R >= 8 a box holds both halves of its
+// by TMA in boxes of R keys, the largest power of two up to 32 that divides the page's tokens, so that a box lies in one page; a
+// lane of the copying warp looks up the page of one box and issues its copy.  With D = 128 and R >= 8 a box holds both halves of its
 // keys' columns, 8 keys at a time (WIDE): half as many copies.  Boxes without a key to read, and missing pages, lie out of
 // the map's range, which gives zeros.  A box that a row's end (or its window's begin) cuts would bring values that are nobody's, and
 // zero times those need not be zero: its values are copied row by row with cp.async, zeros for the others.  K is read
@@ -558,7 +558,7 @@ template <int NB, bool WIDE> cudaError_t go(const AttnArgs& a, int box_log2, cud
 
 cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t st) {
     int box_log2 = 0;
-    while (box_log2 < 7 && a.pt % (2 << box_log2) == 0) ++box_log2;
+    while (box_log2 < 5 && a.pt % (2 << box_log2) == 0) ++box_log2;
     if (a.D == 128 && box_log2 >= 3) return go<2, true>(a, box_log2, st);
     return a.D > 64 ? go<2, false>(a, box_log2, st) : go<1, false>(a, box_log2, st);
 }
