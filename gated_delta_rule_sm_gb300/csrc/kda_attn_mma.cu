@@ -8,8 +8,8 @@
 // A warp is on its own: it takes 16 of a tile's 64 keys, copies them and their values to its own ring in shared memory
 // (cp.async, two stages ahead, so that an SM has 128 KB on the way), and keeps its own maxima, sums and output; the
 // four warps of a CTA meet when a piece ends.  A lane looks up the page of one key, a stage before its address is needed.
-// Precision: scores and sums fp32; a weight is rounded to bf16 for its product with the values, 2^-8 of it at most,
-// and its sum is taken before that.  The maximum that scores are taken from is raised only when it is passed by more
+// Precision: scores and sums fp32; a weight meets the values as the sum of two bf16 values, off by 2^-16 of it at most (the
+// second products are hidden behind the loads too).  The maximum that scores are taken from is raised only when it is passed by more
 // than 8 (in log2): weights up to 2^8 lose nothing in bf16 or fp32, and the output is rescaled a few times, not each tile.
 #include <math.h>
 
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attn_mma_kernel(c
                         mma16816(z[m][1], f, b[2], b[3]);
                     }
                 }
-                uint32_t wgt[MT][4];
+                uint32_t wgt[MT][4], low[MT][4];
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
                     bool raise = false;
@@ -243,7 +243,9 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attn_mma_kernel(c
                             v[0] = ex2(v[0] - from);
                             v[1] = ex2(v[1] - from);
                             sum[m][h] += v[0] + v[1];
-                            wgt[m][2 * j + h] = pack_bf16(v[0], v[1]);
+                            const uint32_t w = pack_bf16(v[0], v[1]);
+                            wgt[m][2 * j + h] = w;
+                            low[m][2 * j + h] = pack_bf16(v[0] - __uint_as_float(w << 16), v[1] - __uint_as_float(w & 0xffff0000u));
                         }
                     }
                 }
@@ -255,6 +257,8 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attn_mma_kernel(c
                     for (int m = 0; m < MT; ++m) {
                         mma16816(o[m][k], wgt[m], b[0], b[1]);
                         mma16816(o[m][k + 1], wgt[m], b[2], b[3]);
+                        mma16816(o[m][k], low[m], b[0], b[1]);
+                        mma16816(o[m][k + 1], low[m], b[2], b[3]);
                     }
                 }
             }
