@@ -493,7 +493,7 @@ kda_status attn_check(const kda_attention_dims* d, bool varlen, bool append, Att
     a->rows = d->rows; a->tokens = d->tokens; a->per_row = varlen ? 0 : d->tokens / d->rows;
     a->Hq = d->Hq; a->Hkv = d->Hkv; a->G = append ? 1 : d->Hq / d->Hkv; a->D = d->D; a->dtype = d->dtype;
     a->pages = d->num_pages; a->pt = d->page_tokens; a->table_rows = d->table_rows; a->max_pages = d->max_pages;
-    a->window = d->window;
+    a->window = d->window < most ? d->window : 0;      // (no position reaches it, and differences of positions stay in 32 bits)
     a->qs = d->q_stride ? d->q_stride : q;
     return KDA_OK;
 }
@@ -539,6 +539,16 @@ void attn_choose(AttnArgs* a, bool aligned) {
     a->direct = a->per_row && (int64_t)a->per_row * a->G <= a->block && a->rows <= kAttnDirectRows;
 }
 
+struct Span {
+    const void* p;
+    size_t n;
+};
+// Whether a result lies over what names the rows and their pages.
+bool over_tables(const Span& r, const AttnArgs& a, const int32_t* table, const int32_t* lengths, const int32_t* seqs, const int32_t* cu) {
+    return ranges_meet(r.p, r.n, table, (size_t)a.table_rows * a.max_pages * 4) || ranges_meet(r.p, r.n, lengths, (size_t)a.table_rows * 4) ||
+           ranges_meet(r.p, r.n, seqs, (size_t)a.rows * 4) || ranges_meet(r.p, r.n, cu, ((size_t)a.rows + 1) * 4);
+}
+
 }  // namespace
 
 cudaError_t launch_attn_simt(const AttnArgs& a, cudaStream_t st) {
@@ -573,6 +583,7 @@ kda_status kda_pages_append(const kda_attention_dims* dims, void* pool, const in
     const size_t np = (size_t)p.a.pages * 2 * kv * p.a.pt * es;
     if (ranges_meet(pool, np, k, ((size_t)(p.a.tokens - 1) * p.ks + kv) * es) || ranges_meet(pool, np, v, ((size_t)(p.a.tokens - 1) * p.vs + kv) * es))
         return KDA_ERR_INVALID_ARG;
+    if (over_tables({pool, np}, p.a, table, lengths, seqs, cu_seqlens)) return KDA_ERR_INVALID_ARG;
     p.a.table = table; p.a.lengths = lengths; p.a.seqs = seqs; p.a.cu = cu_seqlens;
     st = status_ptr(&p.a.status);
     if (st != KDA_OK) return st;
@@ -615,6 +626,8 @@ kda_status kda_pages_attention(const kda_attention_dims* dims, const void* q, co
     if (ranges_meet(out, no, q, nq) || ranges_meet(out, no, pool, np) || ranges_meet(lse, nl, q, nq) || ranges_meet(lse, nl, pool, np) ||
         ranges_meet(out, no, lse, nl))
         return KDA_ERR_INVALID_ARG;
+    for (const Span& r : {Span{out, no}, Span{lse, nl}})
+        if (over_tables(r, a, table, lengths, seqs, cu_seqlens)) return KDA_ERR_INVALID_ARG;
     attn_choose(&a, reinterpret_cast<uintptr_t>(pool) % 16 == 0);
     if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || workspace_bytes < attn_layout(nullptr, &a)) return KDA_ERR_WORKSPACE;
     attn_layout(static_cast<char*>(workspace), &a);

@@ -75,7 +75,6 @@ __device__ __forceinline__ float2 join(float2 P, float2 s, float2 h) { return ma
 template <typename F> __device__ __forceinline__ float vmap(F&& f, float a) { return f(a); }
 template <typename F> __device__ __forceinline__ float2 vmap(F&& f, float2 a) { return make_float2(f(a.x), f(a.y)); }
 template <typename V> __device__ __forceinline__ V vload(const float* p) { return *reinterpret_cast<const V*>(p); }
-template <typename V> __device__ __forceinline__ V vload_l2(const float* p) { return __ldcg(reinterpret_cast<const V*>(p)); }
 template <typename V> __device__ __forceinline__ void vstore(float* p, V v) { *reinterpret_cast<V*>(p) = v; }
 template <typename V> __device__ __forceinline__ void vstore_stream(float* p, V v) { __stcs(reinterpret_cast<V*>(p), v); }
 
@@ -836,20 +835,22 @@ struct Shape {
     int64_t xs, gs, is;
 };
 
+constexpr int64_t kMostStride = 1 << 25;      // an offset inside a tile fits 32 bits
+
 kda_status gated_check(const kda_gated_dims* d, bool varlen, Shape* s) {
     if (!d || d->B < 1 || d->T < 1 || d->C < 1) return KDA_ERR_INVALID_ARG;
     if (d->dtype != KDA_BF16 && d->dtype != KDA_FP32) return KDA_ERR_INVALID_ARG;
     if (varlen && (d->B != 1 || d->num_seqs < 1)) return KDA_ERR_INVALID_ARG;
     for (int64_t st : {d->x_stride, d->g_stride, d->i_stride})
         if (st != 0 && st < d->C) return KDA_ERR_INVALID_ARG;
-    if ((int64_t)d->B * d->T > (1LL << 30) || (varlen && d->num_seqs > (1 << 24))) return KDA_ERR_UNSUPPORTED;
+    if ((int64_t)d->B * d->T > (1LL << 30) || d->C > kMostStride || (varlen && d->num_seqs > (1 << 24))) return KDA_ERR_UNSUPPORTED;
     s->B = d->B; s->T = d->T; s->TT = d->B * d->T; s->C = d->C; s->rows = varlen ? d->num_seqs : d->B;
     s->dtype = d->dtype; s->es = d->dtype == KDA_BF16 ? 2 : 4;
     s->xs = d->x_stride ? d->x_stride : d->C;
     s->gs = d->g_stride ? d->g_stride : d->C;
     s->is = d->i_stride ? d->i_stride : d->C;
     for (int64_t st : {s->xs, s->gs, s->is})
-        if (s->TT > 1 && st > (1LL << 40) / s->TT) return KDA_ERR_UNSUPPORTED;
+        if (s->TT > 1 && (st > (1LL << 40) / s->TT || st > kMostStride)) return KDA_ERR_UNSUPPORTED;
     // (tiles x columns and the workspace's indices)
     if ((int64_t)((s->TT + kTile - 1) / kTile) * ((s->C + 31) / 32) > (1LL << 30)) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
@@ -953,6 +954,14 @@ cudaError_t gated_forward(GatedArgs a, int dtype, bool pairs, cudaStream_t st) {
     return e;
 }
 
+struct Span {
+    const void* p;
+    size_t n;
+};
+// Whether a result lies over the rates or the offsets.
+bool over_tables(const void* out, size_t n, const Shape& s, const float* a_log, const int32_t* cu) {
+    return ranges_meet(out, n, a_log, (size_t)s.C * 4) || ranges_meet(out, n, cu, ((size_t)s.rows + 1) * 4);
+}
 size_t span_bytes(const Shape& s, int64_t stride) { return ((size_t)(s.TT - 1) * stride + s.C) * s.es; }
 
 }  // namespace
@@ -1002,12 +1011,14 @@ kda_status kda_gated_scan_fwd(const kda_gated_dims* dims, const void* x, const v
     const size_t ns = (size_t)s.rows * s.C * 4;
     const bool y_on_x = y == x && s.xs == s.C;
     if ((!y_on_x && ranges_meet(y, ny, x, nx)) || ranges_meet(y, ny, g_raw, ng) || ranges_meet(y, ny, i_raw, ni) ||
-        ranges_meet(y, ny, initial_state, ns) || ranges_meet(y, ny, final_state, ns) || ranges_meet(y, ny, saved, rec))
+        ranges_meet(y, ny, initial_state, ns) || ranges_meet(y, ny, final_state, ns) || ranges_meet(y, ny, saved, rec) ||
+        over_tables(y, ny, s, a_log, cu_seqlens))
         return KDA_ERR_INVALID_ARG;
     for (void* out : {static_cast<void*>(final_state), saved}) {
         const size_t n = out == saved ? rec : ns;
         if (ranges_meet(out, n, x, nx) || ranges_meet(out, n, g_raw, ng) || ranges_meet(out, n, i_raw, ni) ||
-            (out != initial_state && ranges_meet(out, n, initial_state, ns)) || (out == saved && out == initial_state && out))
+            (out != initial_state && ranges_meet(out, n, initial_state, ns)) || (out == saved && out == initial_state && out) ||
+            over_tables(out, n, s, a_log, cu_seqlens))
             return KDA_ERR_INVALID_ARG;
     }
     if (ranges_meet(final_state, ns, saved, rec)) return KDA_ERR_INVALID_ARG;
@@ -1037,16 +1048,14 @@ kda_status kda_gated_scan_bwd(const kda_gated_dims* dims, const void* x, const v
     if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || workspace_bytes < kda_gated_scan_bwd_workspace_size(dims))
         return KDA_ERR_WORKSPACE;
     const size_t nf = (size_t)s.TT * s.C * 4, ns = (size_t)s.rows * s.C * 4;
-    struct Span {
-        const void* p;
-        size_t n;
-    };
     const Span in[] = {{x, span_bytes(s, s.xs)}, {g_raw, span_bytes(s, s.gs)}, {i_raw, span_bytes(s, s.is)}, {dy, (size_t)s.TT * s.C * s.es},
                        {a_log, (size_t)s.C * 4}, {initial_state, ns}, {dfinal_state, ns}, {saved, rec}};
+    const Span offsets = {cu_seqlens, ((size_t)s.rows + 1) * 4};
     const Span out[] = {{dx, nf}, {dg_raw, nf}, {di_raw, nf}, {da_log, (size_t)s.C * 4}, {dinitial_state, ns}};
     for (int k = 0; k < 5; ++k) {
         for (const Span& q : in)
             if (ranges_meet(out[k].p, out[k].n, q.p, q.n)) return KDA_ERR_INVALID_ARG;
+        if (ranges_meet(out[k].p, out[k].n, offsets.p, offsets.n)) return KDA_ERR_INVALID_ARG;
         for (int j = 0; j < k; ++j)
             if (ranges_meet(out[k].p, out[k].n, out[j].p, out[j].n)) return KDA_ERR_INVALID_ARG;
     }
@@ -1086,6 +1095,15 @@ kda_status kda_gated_step(const kda_gated_dims* dims, const void* x, const void*
     if (st != KDA_OK) return st;
     if (!x || !g_raw || !i_raw || !a_log || !y || !state_in || !state_out) return KDA_ERR_INVALID_ARG;
     if (num_slots < 1 || (!slots && num_slots < s.B)) return KDA_ERR_INVALID_ARG;
+    // a thread has read its elements before it writes them
+    const size_t ny = (size_t)s.B * s.C * s.es, np = (size_t)num_slots * s.C * 4;
+    const Span in[] = {{x, span_bytes(s, s.xs)}, {g_raw, span_bytes(s, s.gs)}, {i_raw, span_bytes(s, s.is)}, {a_log, (size_t)s.C * 4},
+                       {slots, (size_t)s.B * 4}, {state_in, np}};
+    for (const Span& q : in)
+        if ((ranges_meet(y, ny, q.p, q.n) && !(q.p == x && y == x && s.xs == s.C)) ||
+            (ranges_meet(state_out, np, q.p, q.n) && !(q.p == state_in && state_out == state_in)))
+            return KDA_ERR_INVALID_ARG;
+    if (ranges_meet(y, ny, state_out, np)) return KDA_ERR_INVALID_ARG;
     StepArgs a;
     memset(&a, 0, sizeof(a));
     a.B = s.B; a.C = s.C; a.num_slots = num_slots; a.xs = s.xs; a.gs = s.gs; a.is = s.is;

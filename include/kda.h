@@ -528,7 +528,7 @@ kda_status kda_short_conv_step(int B, int C, int W, kda_dtype dtype, const void*
  *   kda_gated_scan_saved_size() bytes, 256-byte aligned, gets the states that enter every 64th token of the flattened
  *   tokens for kda_gated_scan_bwd on the same inputs.
  *   In place: y may be x where x is contiguous, final_state may be initial_state; any other overlap of a result with
- *   another or with x, g_raw, i_raw or initial_state is KDA_ERR_INVALID_ARG.
+ *   another or with an input is KDA_ERR_INVALID_ARG.
  * kda_gated_scan_bwd: from dy and dfinal_state (NULL: zero), dx, dg_raw, di_raw [B, T, C], da_log [C] and dinitial_state
  *   [rows, C] (NULL: not wanted), all fp32.  saved may be NULL: the states are then computed again.  No result may
  *   overlap an input or another result.
@@ -537,7 +537,9 @@ kda_status kda_short_conv_step(int B, int C, int W, kda_dtype dtype, const void*
  * word; y and the per-token gradients are then not written, final_state gets the entering state, dinitial_state the
  * final state's gradient, da_log zeros.
  * kda_gated_step: one token per row (dims->T == 1, x, g_raw, i_raw, y [B, C]; strides are row strides) on a slot pool
- *   [num_slots, C] fp32.
+ *   [num_slots, C] fp32.  slots must name distinct slots; an idle row (a negative one) gets zeros.  In place: y may be x
+ *   where x is contiguous, state_out may be state_in; any other overlap of a result is KDA_ERR_INVALID_ARG.
+ * C above 2^25, or a stride above it (with more than one token), is KDA_ERR_UNSUPPORTED.
  */
 typedef struct {
     int B, T, C;
@@ -625,7 +627,8 @@ kda_status kda_pages_compact(const kda_pages_dims* dims, void* pool, const int32
  * cu_seqlens, and cu_seqlens[r + 1] - cu_seqlens[r] with it (rows + 1 offsets from 0 to tokens, which never decrease).
  *
  * kda_pages_append: k and v [tokens, Hkv, D] into their places.  Tokens of idle rows and at negative positions are
- *   not written.  seqs must not repeat, and no page may be held by two rows at the positions written.
+ *   not written.  seqs must not repeat, and no page may be held by two rows at the positions written.  The pool may
+ *   overlap no other array of the call.
  * kda_pages_attention: for every new token and query head of q [tokens, Hq, D], with p its position,
  *     out = sum_j softmax_j(scale q . k_j) v_j    over the keys j of p - window < j <= p (window 0: of 0 <= j <= p)
  *   where query head h reads key head h / (Hq / Hkv).  out [tokens, Hq, D] in dtype; lse [tokens, Hq] fp32 (NULL: not
@@ -633,7 +636,8 @@ kda_status kda_pages_compact(const kda_pages_dims* dims, void* pool, const int32
  *   gets zeros, and lse -inf.  Keys past the window and the position are not read as numbers: whatever their pages
  *   hold there, a masked key's score counts as nothing.  Only a value that is not finite, at a position that another
  *   query of the same row may see, reaches queries that may not see it if both are in one tile of keys (0 times it).
- *   Sums and statistics are fp32; bf16 calls round the weights to bf16 once before they meet the values.
+ *   Sums and statistics are fp32.  In bf16 calls the weights meet the values rounded to bf16, or, with few new tokens, as
+ *   two bf16 terms.
  *
  * q, k and v may be slices of one projection's output: *_stride is the distance in elements between neighbouring tokens,
  * 0 meaning contiguous.  out and lse are contiguous and overlap no input.

@@ -109,6 +109,33 @@ def test_gated_gradients_over_anything(lib, out, at):
         assert bwd(lib, **{out: G[at]}) == BAD
 
 
+@pytest.mark.parametrize("kw", [dict(x_stride=(1 << 25) + 8), dict(g_stride=(1 << 25) + 8), dict(i_stride=1 << 31), dict(C=(1 << 25) + 2)])
+def test_gated_offsets_that_pass_32_bits(lib, kw):
+    big = dict(nws=1 << 40, nsaved=1 << 40)
+    assert fwd(lib, gated_dims(**kw), **big) == UNSUP and bwd(lib, gated_dims(**kw), **big) == UNSUP
+    assert step(lib, gated_dims(B=4, T=1, **kw)) == UNSUP
+
+
+@pytest.mark.parametrize("at", ["a", "cu"])
+def test_gated_results_over_the_rates_or_the_offsets(lib, at):
+    dims, cu = gated_dims(num_seqs=3), 20 * MB
+    to = cu + 12 if at == "cu" else G["a"] + 252
+    for out in ("y", "sT", "saved"):
+        over = to if out != "saved" else (cu if at == "cu" else G["a"])
+        assert fwd(lib, dims, cu=cu, **{out: over}) == BAD
+    for out in ("dx", "dg", "di", "da", "ds0"):
+        assert bwd(lib, dims, cu=cu, **{out: to}) == BAD
+
+
+@pytest.mark.parametrize("kw", [
+    dict(y=2 * MB), dict(y=3 * MB + 500), dict(y=1 * MB + 2), dict(y=4 * MB), dict(y=5 * MB), dict(y=20 * MB + 12), dict(s_out=1 * MB),
+    dict(s_out=2 * MB), dict(s_out=3 * MB), dict(s_out=4 * MB), dict(s_out=5 * MB + 256), dict(s_out=6 * MB), dict(s_out=20 * MB + 12),
+])
+def test_gated_step_results_over_inputs(lib, kw):
+    assert step(lib, slots=20 * MB, **kw) == BAD
+    assert step(lib, gated_dims(B=4, T=1, x_stride=128), y=G["x"]) == BAD
+
+
 # ------------------------------------------------------------------------------------------- pages
 
 
@@ -184,6 +211,14 @@ Q, POOL = 20 * 4 * 64 * 2, 8 * 2 * 2 * 16 * 64 * 2
 ])
 def test_attention_results_over_inputs(lib, kw):
     assert attend(lib, **kw) == BAD
+
+
+@pytest.mark.parametrize("at", ["table", "lengths", "seqs", "cu"])
+def test_results_over_what_names_the_pages(lib, at):
+    cu = dict(cu=18 * MB)
+    for out in ("out", "lse"):
+        assert attend(lib, **cu, **{out: {**A, **cu}[at]}) == BAD
+    assert append(lib, **{**cu, at: A["pool"] + POOL - 4}) == BAD
 
 
 @pytest.mark.parametrize("kw", [dict(k=2 * MB), dict(v=2 * MB + POOL - 16), dict(v=2 * MB - 16)])

@@ -129,6 +129,20 @@ def test_long_rows_are_cut_and_joined(dtype, D, new):
     c.check(*c.run(window=5000), window=5000)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,pt,dtype,new", [
+    (8, 2, 128, 16, "bf16", 3), (8, 2, 128, 16, "bf16", 8), (8, 2, 128, 16, "bf16", 9), (4, 1, 64, 8, "bf16", 64), (4, 1, 64, 8, "bf16", 65),
+    (2, 1, 256, 16, "bf16", 8), (2, 1, 256, 16, "bf16", 9), (4, 2, 64, 16, "fp32", 32), (4, 2, 64, 16, "fp32", 33),
+])
+def test_as_many_new_tokens_in_every_row(Hq, Hkv, D, pt, dtype, new):
+    """Without offsets, around the sizes at which a row stops being one block; a window that no position reaches is none."""
+    c = Case([new + p for p in (0, 1, 77, 300, 3, 900)], [new] * 6, Hq, Hkv, D, pt, dtype, seed=new, seqs=lambda o: [-1 if r == 4 else s for r, s in enumerate(o)])
+    q = c.q.to(DEV).reshape(6, new, Hq, D)
+    out, lse = c.run(q=q, packed=False)
+    c.check(out.reshape(1, -1, Hq, D), lse.reshape(1, -1, Hq))
+    out2, lse2 = c.run(2 ** 31 - 1, q=q, packed=False)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
 def test_a_chunk_longer_than_its_sequence():
     """Tokens at negative positions have no keys: zeros, and they are not written."""
     for dtype in ("bf16", "fp32"):
