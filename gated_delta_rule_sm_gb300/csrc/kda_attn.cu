@@ -528,7 +528,7 @@ void attn_choose(AttnArgs* a, bool aligned) {
     if (a->dtype == KDA_BF16 && a->D % 8 == 0 && aligned && a->D <= 128 && packed > 32 * (int64_t)a->rows &&
         (int64_t)a->pages * 2 * a->Hkv < (1 << 30)) {      // (a tensor map's coordinate)
         a->kernel = kAttnTc;
-        attn_cut(a, kAttnTcRows, kAttnTcKeys, 4, 152);
+        attn_cut(a, kAttnTcRows, kAttnTcKeys, 5, 152);
     } else if (a->dtype == KDA_BF16 && a->D % 8 == 0 && aligned) {
         a->kernel = kAttnMma;
         attn_cut(a, a->D > 128 || packed <= 16 * (int64_t)a->rows ? 16 : 32, kAttnMmaKeys, 2, a->D > 128 ? 152 : 304);

@@ -214,7 +214,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         for (AttnWalk p(a, units, cut, cta); p.more(); p.next(a, units)) {
             const int rows = p.rows(a) - 128 * tile;
             if (rows <= 0) continue;                 // (the other roles leave this tile out as well)
-            const int pos = row < rows ? p.position(a, 128 * tile + row) : -1;
+            // (a row past the last sees what that one does, so that it asks for no masks of its own; nothing of it is kept)
+            const int pos = p.position(a, 128 * tile + min(row, rows - 1));
             // positions of the warp's rows, for tiles that need no mask
             const int low = __reduce_min_sync(0xffffffffu, pos), high = __reduce_max_sync(0xffffffffu, pos);
             float base = -INFINITY;                  // what scores are taken from (a score, not yet times c)
