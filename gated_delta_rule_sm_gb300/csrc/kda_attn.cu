@@ -184,15 +184,17 @@ constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinFew = 4;
 struct JoinSum {
     float o[8], sum;
 };
-// Parts c0 + at, c0 + at + step, ... of row i, weighted from `base`.
-__device__ __forceinline__ JoinSum join_parts(const AttnArgs& a, int c0, int c1, int at, int step, int i, float base) {
+// Parts c0 + at, c0 + at + step, ... of row i, weighted from `base`; ALL: these are all there are, four at most, and base is their
+// largest maximum, found here.
+template <bool ALL>
+__device__ __forceinline__ JoinSum join_parts(const AttnArgs& a, int c0, int c1, int at, int step, int i, float& base) {
     const int lane = threadIdx.x & 31;
     const size_t size = attn_part_floats(a), top = (size_t)a.block * a.D + i;
     JoinSum s;
     s.sum = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) s.o[k] = 0.f;
-    constexpr int AHEAD = 4;
+    constexpr int AHEAD = kJoinFew;
     for (int c = c0 + at; c <= c1; c += AHEAD * step) {
         float f[AHEAD], add[AHEAD], v[AHEAD][8];
 #pragma unroll
@@ -203,6 +205,12 @@ __device__ __forceinline__ JoinSum join_parts(const AttnArgs& a, int c0, int c1,
             add[j] = now <= c1 ? p[top + a.block] : 0.f;
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[j][k] = now <= c1 && k * 32 + lane < a.D ? p[(size_t)i * a.D + k * 32 + lane] : 0.f;
+        }
+        if constexpr (ALL) {
+            base = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) base = fmaxf(base, f[j]);
+            if (base == -INFINITY) base = 0.f;
         }
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
@@ -231,16 +239,23 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     if (i0 >= i1) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool few = rows_each > 1 || c1 - c0 < kJoinFew;      // a warp to a row
+    const bool all = c1 - c0 < kJoinFew;
     for (int i = few ? i0 + warp : i0; i < i1; i += few ? kJoinWarps : 1) {
+        const uint32_t row = (uint32_t)it.first_row + i, token = row / (uint32_t)a.G;
+        const size_t at = (size_t)(it.token + (int)token) * a.Hq + it.head + (row - token * a.G);
+        if (all) {
+            float base;
+            const JoinSum s = join_parts<true>(a, c0, c1, 0, 1, i, base);
+            join_write(a, at, s, base);
+            continue;
+        }
         float top = -INFINITY;
         for (int c = c0 + lane; c <= c1; c += 32)
             top = fmaxf(top, a.part[(size_t)(2 * c + (c == c0)) * attn_part_floats(a) + (size_t)a.block * a.D + i]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float base = top == -INFINITY ? 0.f : top;
-        const uint32_t row = (uint32_t)it.first_row + i, token = row / (uint32_t)a.G;
-        const size_t at = (size_t)(it.token + (int)token) * a.Hq + it.head + (row - token * a.G);
-        JoinSum s = join_parts(a, c0, c1, few ? 0 : warp, few ? 1 : kJoinWarps, i, base);
+        float base = top == -INFINITY ? 0.f : top;
+        JoinSum s = join_parts<false>(a, c0, c1, few ? 0 : warp, few ? 1 : kJoinWarps, i, base);
         if (few) {
             join_write(a, at, s, base);
             continue;
