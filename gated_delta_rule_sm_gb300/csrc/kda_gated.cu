@@ -2,18 +2,25 @@
 // single-token step.  Per channel
 //     log a_t = -exp(a_log) sigmoid(g_t),   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t,   y_t = h_t.
 //
-// One pass over the data: 8 bytes an element forward and 20 backward in bf16 (the gradients are fp32).  The tokens
-// are cut into tiles, a CTA takes one tile of 64 channels (32 where two channels cannot be read at once) and keeps
-// it in registers: a warp takes consecutive tokens, a lane neighbouring channels.  The recurrence is affine, so that
-// a run of tokens is a pair (P, h): state -> P state + h, and runs are joined in three steps: a thread's tokens, the
-// warps of a CTA, the tiles.  The last is a chain along the tokens inside the one launch: a tile publishes its pair
-// as soon as it has it, then looks back over its predecessors to the nearest one whose leaving state is known, and
-// applies the pairs between in order.  Tiles are taken from a counter, so that whatever a tile waits for was begun
+// One pass over the data: 8 bytes an element forward and 20 backward in bf16 (the gradients are fp32).  The tokens are cut
+// into tiles of 64 tokens and 64 channels (32 where two channels cannot be read at once).  A CTA copies a tile's rows to
+// shared memory (cp.async, 16 bytes at a time where they are aligned); each of eight warps takes eight consecutive tokens, a
+// lane a pair of neighbouring channels.  The recurrence is affine, so that a run of tokens is a pair (P, h): state -> P state
+// + h, and runs are joined in three steps: a thread's tokens, the warps of a CTA, the tiles.  The last is a chain along the
+// tokens inside the one launch, which a ninth warp follows: it tells the tile's pair, looks back over the tiles before it
+// to the nearest one whose leaving state is told, and applies the pairs between in order.  Pairs and states are words that
+// say themselves whether they are there.  Tiles are taken from a counter, so that whatever a tile waits for was begun
 // before it; the waits are bounded.  A state is the same chain of the same operations wherever the look-back began, so
 // results do not depend on timing.
 // The backward pass runs the same chain from the last token to the first, on m_t = a_t (dy_t + m_{t+1}), the
 // gradient of h_{t-1}; the states it needs enter every 64th token from the forward's record and are carried on inside
 // a tile.
+// Measured, 16384 tokens x 4096 channels in bf16: forward 149 us with 12 documents and 142 us with 4 rows (537 MB: 3.7
+// TB/s), backward 262 us (1.34 GB: 5.1 TB/s; a copy reaches 6.7).  Bound by both sides of a tile's life: the instructions
+// (100 for two channels of a token forward, 190 backward, 60% of the issue slots) and the waits between its phases.
+// Without the chain's waits the forward took 123 us, without the gates' arithmetic as well 108.  The tile's size is at its best: eight
+// warps and 4 CTAs of an SM forward, 3 backward; with 16 warps and tiles of 128 tokens 164 and 323 us, with 4 warps and tiles of
+// 32 tokens 163 and 276.  A fifth CTA (the inputs kept in shared memory, 40 registers) changed nothing.
 // Precision: everything in fp32.  1 - a comes from a series in log a, so that decays next to 1, the long memories,
 // are right to a rounding, and sqrt(1 - a^2) = sqrt(e (2 - e)) with e = 1 - a loses nothing there either.
 #include <math.h>
@@ -36,7 +43,7 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32, kAll = kThreads + 32;
 constexpr int kTok = 8, kTile = kWarps * kTok;      // tokens of a thread and of a CTA
 static_assert(kThreads == 4 * kTile, "a thread asks for a row of one of four arrays");
-constexpr int kFwdCtas = 4, kBwdCtas = 3;           // CTAs of an SM
+constexpr int kFwdCtas = 4, kBwdCtas = 3;           // CTAs of an SM: as many as registers and shared memory allow
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct GatedArgs {
@@ -123,14 +130,20 @@ __device__ __forceinline__ float rsq(float x) {
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float sqr(float x) {
+    float y;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ float min_nan(float x, float y) {     // NaN if either is
     float z;
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
     return z;
 }
 
-// e^-z, which stops at 2^60: the product of two sums 1 + e^-z stays finite, and one reciprocal serves both gates.  From
-// there, z = -41.6, a sigmoid stays at 2^-60, 9e-19, which no sum it enters can tell from zero.
+// e^-z for the gradients, which need 1 less the sigmoid as well; it stops at 2^60: the product of two sums 1 + e^-z stays
+// finite, and one reciprocal serves both gates.  From there, z = -41.6, a sigmoid stays at 2^-60, 9e-19, which no sum it
+// enters can tell from zero.
 template <typename V> __device__ __forceinline__ V exp_neg(V z) {
     return vmap([](float t) { return min_nan(ex2(t), 0x1p60f); }, vmul(z, vdup<V>(-kLog2e)));
 }
@@ -210,6 +223,18 @@ template <typename V> __device__ __forceinline__ Gates<V> gates_of(V g, V i) {
     return k;
 }
 
+// What the state needs of them: a reciprocal each, which takes an infinite e^-z as it is.
+template <typename V> __device__ __forceinline__ V sigmoid(V z) {
+    const V one = vdup<V>(1.f), e = vmap([](float t) { return ex2(t); }, vmul(z, vdup<V>(-kLog2e)));
+    return vmap([](float t) { return rcp(t); }, vfma(e, one, one));
+}
+// 1 - a of a token and its input sqrt(1 - a^2) sigmoid(i) x.
+template <bool WIDE, typename V> __device__ __forceinline__ V decay_of(V g, V i, V x, const Rate<V>& rate, V& b) {
+    const V e = one_minus_exp(log_decay<WIDE>(g, sigmoid(g), rate), WIDE && rate.wide);
+    b = vmul(vmap([](float t) { return sqr(t); }, square_of(e)), vmul(sigmoid(i), x));
+    return e;
+}
+
 // ------------------------------------------------------------------ rows inside a tile
 
 // Which rows begin at and end with a token of the tile, -1: none.
@@ -271,7 +296,7 @@ __device__ __forceinline__ void ask(const float* p, float2& a, float2& b) {
 // leaving state on, the pairs of those between, in order.  The first tile of a chain, and every tile in which a row begins,
 // tells a state, so there is one.  At most about a second, then the error is recorded and the state is 0.
 template <typename V> __device__ __forceinline__ V look_back(const GatedArgs& a, int o, int c) {
-    constexpr int W = 4;                 // tiles looked at together
+    constexpr int W = 4;                 // tiles looked at together (1, 2: the same time; 8: 166 us for 146, the L2 is asked too often)
     const float *inc = a.inc + c, *agg = a.agg + 2 * (size_t)c;
     int near = o - 1;                    // the pairs of the tiles above it are there
     V s = vdup<V>(0.f);
@@ -332,8 +357,8 @@ __device__ __forceinline__ void join_chain(const GatedArgs& a, int o, int c, boo
     give(s);
 }
 
-// Barriers of a tile: which one it is is known, its runs are in shared memory (the chain's warp waits), the entering state is (the others wait), and one
-// of the eight warps alone.
+// Barriers of a tile: 4, which tile it is, is known (the eight warps wait); 1, its runs are in shared memory (the chain's warp
+// waits); 2, the entering state is (the others wait); 3, the eight warps among themselves.
 __device__ __forceinline__ void runs_ready() {
     __syncwarp();
     asm volatile("bar.arrive 1, %0;" ::"n"(kAll) : "memory");
@@ -352,8 +377,7 @@ template <bool TELLS> __device__ __forceinline__ void tile_known() {
 __device__ __forceinline__ void tile_sync() { asm volatile("bar.sync 3, %0;" ::"n"(kThreads) : "memory"); }
 
 // Tiles in the order in which they are begun.  A CTA takes the next one when it knows the state that enters the one it has, not
-// earlier: a tile that was taken and not begun holds up all that wait for it.  (With its copies a tile ahead the scan took 188 us for 167 with
-// tiles dealt out in advance, but then one late CTA is late in every round.)
+// earlier: a tile that was taken and not begun holds up all that wait for it (188 us for 154 with tickets and copies a tile ahead).
 __device__ __forceinline__ int take_ticket(const GatedArgs& a, int before) {
     return a.planned ? atomicAdd(a.ticket, 1) : before < 0 ? (int)blockIdx.x : before + (int)gridDim.x;
 }
@@ -489,11 +513,7 @@ __device__ __forceinline__ void forward_tile(const GatedArgs& a, const Spot& s, 
     V ka[kTok], kb[kTok], P, h;
 #pragma unroll
     for (int k = 0; k < kTok; ++k) {
-        const V g = mg[k][tid].get();
-        const Gates<V> z = gates_of(g, mi[k][tid].get());
-        const V e = one_minus_exp(log_decay<EDGE>(g, z.sg, rate), EDGE && rate.wide), w = square_of(e);
-        ka[k] = keep_of(e);
-        kb[k] = vmul(vmul(w, root_of(w)), vmul(z.si, mx[k][tid].get()));
+        ka[k] = keep_of(decay_of<EDGE>(mg[k][tid].get(), mi[k][tid].get(), mx[k][tid].get(), rate, kb[k]));
         if (EDGE && k >= s.n) {
             ka[k] = vdup<V>(1.f);
             kb[k] = vdup<V>(0.f);
@@ -539,11 +559,11 @@ __device__ __forceinline__ void forward_tile(const GatedArgs& a, const Spot& s, 
 }
 
 // The loop of both passes.  load(spot) issues a tile's copies, work(spot, hint, rate) does it, soon(tile, columns)
-// asks the L2 for a later one (backwards alone: 301 -> 287 us there, 154 -> 159 us forward).  The ninth warp takes the tickets and joins
+// asks the L2 for a later one (backwards alone: it brought 301 to 287 us there, but 154 to 159 forward).  The ninth warp takes the tickets and joins
 // the chain: the runs of the warps from the first (or, backwards, from the last) on.
-template <bool BACK, int VEC, typename L, typename P, typename W>
+template <bool BACK, int VEC, typename L, typename N, typename W>
 __device__ __forceinline__ void walk_tiles(const GatedArgs& a, TileWords& w, Val<VEC> (&sp)[kWarps][32], Val<VEC> (&sh)[kWarps][32],
-                                           Val<VEC> (&senter)[32], L&& load, P&& soon, W&& work) {
+                                           Val<VEC> (&senter)[32], L&& load, N&& soon, W&& work) {
     using V = Val<VEC>;
     const uint32_t total = (uint32_t)a.tiles * a.cols;
     // (offsets that break the contract: the plan has found no tile's first row, and nothing is read by them)
@@ -651,11 +671,9 @@ __device__ __forceinline__ void backward_tile(const GatedArgs& a, const Spot& s,
     V P = one, h = vdup<V>(0.f);
 #pragma unroll 4
     for (int k = 0; k < kTok; ++k) {
-        const V g = mg[k][tid].get();
-        const Gates<V> z = gates_of(g, mi[k][tid].get());
-        V e = one_minus_exp(log_decay<EDGE>(g, z.sg, rate), EDGE && rate.wide);
-        if (EDGE && k >= s.n) e = vdup<V>(0.f);
-        const V w = square_of(e), b = vmul(vmul(w, root_of(w)), vmul(z.si, mx[k][tid].get())), ka = keep_of(e);
+        V b, e = decay_of<EDGE>(mg[k][tid].get(), mi[k][tid].get(), mx[k][tid].get(), rate, b);
+        if (EDGE && k >= s.n) e = b = vdup<V>(0.f);
+        const V ka = keep_of(e);
         if (EDGE && begins_at(k) >= 0) {
             P = vdup<V>(0.f);
             h = row_of(a.s0, begins_at(k));
@@ -821,9 +839,8 @@ __global__ void __launch_bounds__(kStepThreads) gated_step_kernel(const __grid_c
     ri.load(a.i, (size_t)b * a.is + c);
     const V old = vload<V>(a.s_in + (size_t)slot * a.C + c);
     const Rate<V> rate = rate_of(vload<V>(a.a_log + c));
-    const Gates<V> z = gates_of(rg.get(), ri.get());
-    const V e = one_minus_exp(log_decay<true>(rg.get(), z.sg, rate), rate.wide), w = square_of(e);
-    const V h = vfma(keep_of(e), old, vmul(vmul(w, root_of(w)), vmul(z.si, rx.get())));
+    V add;
+    const V e = decay_of<true>(rg.get(), ri.get(), rx.get(), rate, add), h = vfma(keep_of(e), old, add);
     vstore(a.s_out + (size_t)slot * a.C + c, h);
     R::store(a.y, (size_t)b * a.C + c, h);
 }
