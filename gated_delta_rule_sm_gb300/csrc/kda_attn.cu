@@ -20,7 +20,9 @@ namespace {
 // ------------------------------------------------------------------ append
 
 // A warp takes a token, its lanes the 16-byte pieces (elements where those are not aligned) of its keys and values.  Bound by
-// memory; the tokens' addresses come from three small loads, which the loads of the data do not wait for.
+// memory; the tokens' addresses come from three small loads, one after the other, which the loads of the data do not wait for.
+// Measured: 8192 tokens, 8 heads of 128 in bf16 (67 MB): 17.7 us with its launch, 128 single tokens 4.1 us.  Fewer pieces
+// at once, or CTAs that take several tokens, were slower.
 constexpr int kAppendWarps = 8;
 struct AppendArgs {
     AttnArgs a;
@@ -101,7 +103,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_
 
 // ------------------------------------------------------------------ plan
 
-// Units of every row, then the cost of every unit, each as a running sum.
+// Units of every row, then the cost of every unit, each as a running sum, by one CTA: 4 us, and the attention is launched meanwhile.
 constexpr int kPlanThreads = 1024;
 __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* tmp, int64_t* total) {     // what comes before this thread
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -177,9 +179,11 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
 
 // ------------------------------------------------------------------ join
 
-// A CTA takes some rows of one item (a unit for one key head) that several CTAs share.  With few
-// parts a warp takes a row; with many (a few rows over a long cache) the warps split the parts of a row, four of each
-// warp's on the way at once, since then it is their latency that counts.
+// A CTA takes some rows of one item (a unit for one key head) that several CTAs share.  With few parts a warp takes a
+// row and reads them and their maxima at once; with many (a few rows over a long cache) the warps split the parts of a row,
+// four of each warp's on the way at once, since it is their latency that counts (43 -> 37 us for one row over 32768 tokens).
+// The attention's CTAs say which items they share, and the join is launched while they run: 3 us after a step, 14 us after
+// a chunk of 8192 tokens.
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinFew = 4;
 struct JoinSum {
     float o[8], sum;
@@ -280,7 +284,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
 
 // 64 packed rows against 64 keys at a time, 256 threads of 4 x 4 scores each; Q, K and the weights lie transposed in
 // shared memory, so that a step of a product is two 16-byte reads for 16 multiplications.  A thread keeps 4 rows of D / 16
-// columns of the output.  Bound by fp32 arithmetic with full blocks; a block of few rows leaves most warps idle.
+// columns of the output.  Bound by fp32 arithmetic with full blocks; a block of few rows leaves most warps idle.  Measured:
+// 301 tokens of three requests over 700, 6 heads of 40, 30.4 us with the plan and the join, mostly latency: the cut gives a CTA a few tiles.
 constexpr int kSimtRows = 64, kSimtKeys = 64, kSimtThreads = 256, kSimtPad = 68;
 
 template <typename E> __device__ __forceinline__ float4 load4(const char* p, int d, int D, bool vec) {
@@ -538,15 +543,22 @@ size_t attn_layout(char* ws, AttnArgs* a) {
 }
 
 // Which kernel a call takes, and its cut.  aligned: the pool's base allows 16-byte copies.
+// mma reads a row's keys once for 16 packed rows, tc for 256: mma where a row has 16 on average at most (4 query heads to a key
+// head, D = 128, attention and join: 16 packed rows of 8 requests over 8192 keys 71 us by mma, 68 by tc; of 64 over 2048 115
+// and 115; with D = 64 single tokens of the 8 requests 45 and 50, of the 64 76 and 92), tc above it (32 packed rows: 93 us by mma, 70 by
+// tc; 198 and 118).
+// Their two or one CTAs of an SM share its registers and shared memory; extra: an item's beginning and end in key tiles, fitted to the
+// CTAs' own times (tc: 8.2 us for an item, 1.53 us for a tile; cuts with 1 in place of 4 left some CTAs at twice the mean of
+// short causal items, 774 for 1103 TFLOP/s).
 void attn_choose(AttnArgs* a, bool aligned) {
     const int64_t packed = (int64_t)a->tokens * a->G;
-    if (a->dtype == KDA_BF16 && a->D % 8 == 0 && aligned && a->D <= 128 && packed > 32 * (int64_t)a->rows &&
+    if (a->dtype == KDA_BF16 && a->D % 8 == 0 && aligned && a->D <= 128 && packed > kAttnMmaRows * (int64_t)a->rows &&
         (int64_t)a->pages * 2 * a->Hkv < (1 << 30)) {      // (a tensor map's coordinate)
         a->kernel = kAttnTc;
         attn_cut(a, kAttnTcRows, kAttnTcKeys, 5, 152);
     } else if (a->dtype == KDA_BF16 && a->D % 8 == 0 && aligned) {
         a->kernel = kAttnMma;
-        attn_cut(a, a->D > 128 || packed <= 16 * (int64_t)a->rows ? 16 : 32, kAttnMmaKeys, 2, a->D > 128 ? 152 : 304);
+        attn_cut(a, kAttnMmaRows, kAttnMmaKeys, 2, a->D > 128 ? 152 : 304);
     } else {
         a->kernel = kAttnSimt;
         attn_cut(a, kSimtRows, kSimtKeys, 1, a->D > 128 ? 152 : 304);

@@ -220,8 +220,8 @@ __device__ __forceinline__ const char* attn_page(const AttnArgs& a, int seq, int
     return static_cast<const char*>(a.pool) + ((size_t)page * 2 * a.Hkv + head) * head_bytes + (size_t)(key % a.pt) * a.D * es;
 }
 
-// The kernels.  mma: bf16, D a multiple of 8, 16-byte aligned pool; blocks of 16 or 32 packed rows (16 with D above 128).
-constexpr int kAttnMmaKeys = 64;
+// The kernels.  mma: bf16, D a multiple of 8, 16-byte aligned pool; blocks of 16 packed rows.
+constexpr int kAttnMmaRows = 16, kAttnMmaKeys = 64;
 // Launches a kernel; early: while the one before it in the stream still runs (it begins with a wait for that one's end).
 template <typename... P, typename... A>
 cudaError_t attn_launch(void (*kernel)(P...), dim3 grid, int threads, size_t shared, bool early, cudaStream_t st, const A&... args) {

@@ -8,9 +8,12 @@
 // A warp is on its own: it takes 16 of a tile's 64 keys, copies them and their values to its own ring in shared memory
 // (cp.async, two stages ahead, so that an SM has 128 KB on the way), and keeps its own maxima, sums and output; the
 // four warps of a CTA meet when a piece ends.  A lane looks up the page of one key, a stage before its address is needed.
+// Measured: one token over 32768 keys, 32 query heads on 8 key heads, D = 128 (134 MB): 30.8 us of the kernel, of which the copies
+// run 22 (6.2 TB/s); 4 go by before the first are issued (lengths and the page table are read one after the other, by all
+// CTAs at once) and 3 for the first to arrive.  A batch of 64 such rows of up to 8192 tokens: 148 to 170 us for 0.91 GB, 5.4 to 6.2 TB/s.
 // Precision: scores and sums fp32; a weight meets the values as the sum of two bf16 values, off by 2^-16 of it at most (the
-// second products are hidden behind the loads too).  The maximum that scores are taken from is raised only when it is passed by more
-// than 8 (in log2): weights up to 2^8 lose nothing in bf16 or fp32, and the output is rescaled a few times, not each tile.
+// second products cost no time; the output's error is then its own rounding, 0.0017 for 0.0021).  The maximum that scores
+// are taken from is raised only when it is passed by more than 8 (in log2): weights up to 2^8 lose nothing in bf16 or fp32, and the output is rescaled a few times, not each tile.
 #include <math.h>
 
 #include "kda.h"
@@ -26,6 +29,7 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps, kGroup = 16;      // kGroup: keys of a warp's step
 static_assert(kWarps * kGroup == kAttnMmaKeys, "a tile is a step of the four warps");
+constexpr int kRows = kAttnMmaRows;
 constexpr float kRaise = 8.f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -57,21 +61,21 @@ template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.as
 // Byte of 16-byte piece c of row r in a tile of DP columns: the pieces of eight rows lie in different banks.
 template <int DP> __device__ __forceinline__ uint32_t piece(int r, int c) { return (uint32_t)(r * DP * 2 + ((c ^ (r & 7)) << 4)); }
 
-template <int DP, int MT> struct Lay {
+template <int DP> struct Lay {
     static constexpr int STAGES = DP == 64 ? 4 : 3;
     static constexpr uint32_t KV = kGroup * DP * 2;                       // keys (or values) of a stage
     static constexpr uint32_t RING = kWarps * STAGES * 2 * KV;            // the warps' rings, then, at a piece's end, their outputs
-    static constexpr uint32_t Q = RING;                                   // MT tiles of 16 rows
-    static constexpr uint32_t STAT = Q + MT * 16 * DP * 2;                // [2][kWarps][16 MT] maxima, sums
-    static constexpr uint32_t TOTAL = STAT + 2 * kWarps * 16 * MT * 4;
-    static_assert(RING >= kWarps * 16 * MT * DP * 4, "the outputs fit into the rings");
+    static constexpr uint32_t Q = RING;                                   // 16 rows
+    static constexpr uint32_t STAT = Q + kRows * DP * 2;                  // [2][kWarps][kRows] maxima, sums
+    static constexpr uint32_t TOTAL = STAT + 2 * kWarps * kRows * 4;
+    static_assert(RING >= kWarps * kRows * DP * 4, "the outputs fit into the rings");
 };
 
-template <int DP, int MT>
+template <int DP>
 __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attn_mma_kernel(const __grid_constant__ AttnArgs a) {
-    using L = Lay<DP, MT>;
-    constexpr int KS = DP / 16, NT = DP / 8, ROWS = 16 * MT;
-    constexpr bool QREG = DP * MT <= 128;             // Q's fragments stay in registers
+    using L = Lay<DP>;
+    constexpr int KS = DP / 16, NT = DP / 8;
+    constexpr bool QREG = DP <= 128;             // Q's fragments stay in registers
     extern __shared__ __align__(128) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
@@ -135,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attn_mma_kernel(c
             page = next;
         }
         // Q, zeros past its rows and columns
-        for (int i = tid; i < ROWS * (DP / 8); i += kThreads) {
+        for (int i = tid; i < kRows * (DP / 8); i += kThreads) {
             const int r = i / (DP / 8), b = i % (DP / 8);
             uint4 f = make_uint4(0, 0, 0, 0);
             if (r < n && b * 8 < a.D) {
@@ -147,33 +151,27 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attn_mma_kernel(c
                     f = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16, e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
                 }
             }
-            *reinterpret_cast<uint4*>(smem + L::Q + (r >> 4) * (16 * DP * 2) + piece<DP>(r & 15, b)) = f;
+            *reinterpret_cast<uint4*>(smem + L::Q + piece<DP>(r, b)) = f;
         }
         __syncthreads();
-        uint32_t qf[QREG ? MT * KS : 1][4];
+        uint32_t qf[QREG ? KS : 1][4];
         if constexpr (QREG)
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int k = 0; k < KS; ++k) ldmatrix4(sbase + L::Q + m * (16 * DP * 2) + piece<DP>(vrow, 2 * k + vpiece), qf[m * KS + k]);
+            for (int k = 0; k < KS; ++k) ldmatrix4(sbase + L::Q + piece<DP>(vrow, 2 * k + vpiece), qf[k]);
 
-        float o[MT][NT][4], base[MT][2], sum[MT][2];
-        int pos[MT][2];
+        float o[NT][4], base[2], sum[2];
+        int pos[2];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int h = 0; h < 2; ++h) {
+            const int r = h * 8 + (lane >> 2);
+            base[h] = -INFINITY;
+            sum[h] = 0.f;
+            pos[h] = r < n ? p.position(a, r) : -1;
+        }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = m * 16 + h * 8 + (lane >> 2);
-                base[m][h] = -INFINITY;
-                sum[m][h] = 0.f;
-                pos[m][h] = r < n ? p.position(a, r) : -1;
-            }
+        for (int k = 0; k < NT; ++k)
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int k = 0; k < NT; ++k)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) o[m][k][j] = 0.f;
+            for (int j = 0; j < 4; ++j) o[k][j] = 0.f;
 
         for (int t = 0; t < steps; ++t) {
             const int next = look(t + L::STAGES);
@@ -184,82 +182,71 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attn_mma_kernel(c
             const int k0 = first + t * kAttnMmaKeys;
             if (k0 < s.end) {
                 const uint32_t keys = ring + (t % L::STAGES) * 2 * L::KV, vals = keys + L::KV;
-                float z[MT][2][4];
+                float z[2][4];
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) z[m][j >> 2][j & 3] = 0.f;
+                for (int j = 0; j < 8; ++j) z[j >> 2][j & 3] = 0.f;
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
                     uint32_t b[4];
                     ldmatrix4(keys + piece<DP>(krow, 2 * k + kpiece), b);
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        uint32_t q[4];
-                        if constexpr (!QREG) ldmatrix4(sbase + L::Q + m * (16 * DP * 2) + piece<DP>(vrow, 2 * k + vpiece), q);
-                        const uint32_t* f = QREG ? qf[m * KS + k] : q;
-                        mma16816(z[m][0], f, b[0], b[1]);
-                        mma16816(z[m][1], f, b[2], b[3]);
-                    }
+                    uint32_t q[4];
+                    if constexpr (!QREG) ldmatrix4(sbase + L::Q + piece<DP>(vrow, 2 * k + vpiece), q);
+                    const uint32_t* f = QREG ? qf[k] : q;
+                    mma16816(z[0], f, b[0], b[1]);
+                    mma16816(z[1], f, b[2], b[3]);
                 }
-                uint32_t wgt[MT][4], low[MT][4];
+                uint32_t wgt[4], low[4];
+                bool raise = false;
+                float top[2];
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    bool raise = false;
-                    float top[2];
+                for (int h = 0; h < 2; ++h) {
+                    top[h] = -INFINITY;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        top[h] = -INFINITY;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int key = k0 + (j >> 1) * 8 + 2 * (lane & 3) + (j & 1);
-                            float& v = z[m][j >> 1][2 * h + (j & 1)];
-                            v = key > pos[m][h] || (a.window && key <= pos[m][h] - a.window) ? -INFINITY : v * c;
-                            top[h] = fmaxf(top[h], v);
-                        }
-                        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
-                        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
-                        raise |= top[h] > base[m][h] + kRaise;
+                    for (int j = 0; j < 4; ++j) {
+                        const int key = k0 + (j >> 1) * 8 + 2 * (lane & 3) + (j & 1);
+                        float& v = z[j >> 1][2 * h + (j & 1)];
+                        v = key > pos[h] || (a.window && key <= pos[h] - a.window) ? -INFINITY : v * c;
+                        top[h] = fmaxf(top[h], v);
                     }
-                    if (__any_sync(0xffffffffu, raise))
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const float now = top[h] > base[m][h] + kRaise ? top[h] : base[m][h];
-                            const float f = now == -INFINITY ? 1.f : ex2(base[m][h] - now);
-                            base[m][h] = now;
-                            sum[m][h] *= f;
-#pragma unroll
-                            for (int k = 0; k < NT; ++k) {
-                                o[m][k][2 * h] *= f;
-                                o[m][k][2 * h + 1] *= f;
-                            }
-                        }
+                    top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+                    top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+                    raise |= top[h] > base[h] + kRaise;
+                }
+                if (__any_sync(0xffffffffu, raise))
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float from = base[m][h] == -INFINITY ? 0.f : base[m][h];
+                        const float now = top[h] > base[h] + kRaise ? top[h] : base[h];
+                        const float f = now == -INFINITY ? 1.f : ex2(base[h] - now);
+                        base[h] = now;
+                        sum[h] *= f;
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            float *v = z[m][j] + 2 * h;
-                            v[0] = ex2(v[0] - from);
-                            v[1] = ex2(v[1] - from);
-                            sum[m][h] += v[0] + v[1];
-                            const uint32_t w = pack_bf16(v[0], v[1]);
-                            wgt[m][2 * j + h] = w;
-                            low[m][2 * j + h] = pack_bf16(v[0] - __uint_as_float(w << 16), v[1] - __uint_as_float(w & 0xffff0000u));
+                        for (int k = 0; k < NT; ++k) {
+                            o[k][2 * h] *= f;
+                            o[k][2 * h + 1] *= f;
                         }
+                    }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float from = base[h] == -INFINITY ? 0.f : base[h];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float *v = z[j] + 2 * h;
+                        v[0] = ex2(v[0] - from);
+                        v[1] = ex2(v[1] - from);
+                        sum[h] += v[0] + v[1];
+                        const uint32_t w = pack_bf16(v[0], v[1]);
+                        wgt[2 * j + h] = w;
+                        low[2 * j + h] = pack_bf16(v[0] - __uint_as_float(w << 16), v[1] - __uint_as_float(w & 0xffff0000u));
                     }
                 }
 #pragma unroll
                 for (int k = 0; k < NT; k += 2) {
                     uint32_t b[4];
                     ldmatrix4t(vals + piece<DP>(vrow, k + vpiece), b);
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        mma16816(o[m][k], wgt[m], b[0], b[1]);
-                        mma16816(o[m][k + 1], wgt[m], b[2], b[3]);
-                        mma16816(o[m][k], low[m], b[0], b[1]);
-                        mma16816(o[m][k + 1], low[m], b[2], b[3]);
-                    }
+                    mma16816(o[k], wgt, b[0], b[1]);
+                    mma16816(o[k + 1], wgt, b[2], b[3]);
+                    mma16816(o[k], low, b[0], b[1]);
+                    mma16816(o[k + 1], low, b[2], b[3]);
                 }
             }
             __syncwarp();          // all lanes have read the stage that the next step fills
@@ -267,34 +254,30 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attn_mma_kernel(c
         cp_wait<0>();
         // the warps' outputs, taken from the largest of their maxima
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                sum[m][h] += __shfl_xor_sync(0xffffffffu, sum[m][h], 1);
-                sum[m][h] += __shfl_xor_sync(0xffffffffu, sum[m][h], 2);
-                if ((lane & 3) == 0) {
-                    const int r = m * 16 + h * 8 + (lane >> 2);
-                    stat[warp * ROWS + r] = base[m][h];
-                    stat[(kWarps + warp) * ROWS + r] = sum[m][h];
-                }
+        for (int h = 0; h < 2; ++h) {
+            sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
+            sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
+            if ((lane & 3) == 0) {
+                const int r = h * 8 + (lane >> 2);
+                stat[warp * kRows + r] = base[h];
+                stat[(kWarps + warp) * kRows + r] = sum[h];
             }
+        }
         __syncthreads();
-        float* outs = reinterpret_cast<float*>(smem);       // [kWarps][ROWS][DP]
+        float* outs = reinterpret_cast<float*>(smem);       // [kWarps][kRows][DP]
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int h = 0; h < 2; ++h) {
+            const int r = h * 8 + (lane >> 2);
+            if (r >= n) continue;
+            float top = -INFINITY;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = m * 16 + h * 8 + (lane >> 2);
-                if (r >= n) continue;
-                float top = -INFINITY;
+            for (int v = 0; v < kWarps; ++v) top = fmaxf(top, stat[v * kRows + r]);
+            const float f = base[h] == -INFINITY ? 0.f : ex2(base[h] - top);
 #pragma unroll
-                for (int v = 0; v < kWarps; ++v) top = fmaxf(top, stat[v * ROWS + r]);
-                const float f = base[m][h] == -INFINITY ? 0.f : ex2(base[m][h] - top);
-#pragma unroll
-                for (int k = 0; k < NT; ++k)
-                    *reinterpret_cast<float2*>(outs + (warp * ROWS + r) * DP + k * 8 + 2 * (lane & 3)) =
-                        make_float2(o[m][k][2 * h] * f, o[m][k][2 * h + 1] * f);
-            }
+            for (int k = 0; k < NT; ++k)
+                *reinterpret_cast<float2*>(outs + (warp * kRows + r) * DP + k * 8 + 2 * (lane & 3)) =
+                    make_float2(o[k][2 * h] * f, o[k][2 * h + 1] * f);
+        }
         __syncthreads();
         if (tid == 0) p.tell_join(a, cut, cta);
         float* part = a.part + p.slot(cta) * attn_part_floats(a);
@@ -303,13 +286,13 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attn_mma_kernel(c
             if (d >= a.D) continue;
             float top = -INFINITY, sum_r = 0.f;
 #pragma unroll
-            for (int v = 0; v < kWarps; ++v) top = fmaxf(top, stat[v * ROWS + r]);
+            for (int v = 0; v < kWarps; ++v) top = fmaxf(top, stat[v * kRows + r]);
             float2 y = make_float2(0.f, 0.f);
 #pragma unroll
             for (int v = 0; v < kWarps; ++v) {
-                const float b = stat[v * ROWS + r], f = b == -INFINITY ? 0.f : ex2(b - top);
-                sum_r = fmaf(stat[(kWarps + v) * ROWS + r], f, sum_r);
-                const float2 add = *reinterpret_cast<const float2*>(outs + (v * ROWS + r) * DP + d);
+                const float b = stat[v * kRows + r], f = b == -INFINITY ? 0.f : ex2(b - top);
+                sum_r = fmaf(stat[(kWarps + v) * kRows + r], f, sum_r);
+                const float2 add = *reinterpret_cast<const float2*>(outs + (v * kRows + r) * DP + d);
                 y.x += add.x;
                 y.y += add.y;
             }
@@ -335,18 +318,16 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) attn_mma_kernel(c
     }
 }
 
-template <int DP, int MT> cudaError_t go(const AttnArgs& a, cudaStream_t st) {
-    const cudaError_t e = cudaFuncSetAttribute(attn_mma_kernel<DP, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<DP, MT>::TOTAL);
+template <int DP> cudaError_t go(const AttnArgs& a, cudaStream_t st) {
+    const cudaError_t e = cudaFuncSetAttribute(attn_mma_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<DP>::TOTAL);
     if (e != cudaSuccess) return e;
-    return attn_launch(attn_mma_kernel<DP, MT>, a.ctas, kThreads, Lay<DP, MT>::TOTAL, !a.direct, st, a);
+    return attn_launch(attn_mma_kernel<DP>, a.ctas, kThreads, Lay<DP>::TOTAL, !a.direct, st, a);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_mma(const AttnArgs& a, cudaStream_t st) {
-    if (a.D > 128) return go<256, 1>(a, st);
-    if (a.D > 64) return a.block == 16 ? go<128, 1>(a, st) : go<128, 2>(a, st);
-    return a.block == 16 ? go<64, 1>(a, st) : go<64, 2>(a, st);
+    return a.D > 128 ? go<256>(a, st) : a.D > 64 ? go<128>(a, st) : go<64>(a, st);
 }
 
 }  // namespace kda

@@ -22,8 +22,15 @@
 // V is complete.  P is handed over in halves of 64 keys.
 // Registers: a softmax thread holds 128 scores, the others little: 208 and 88 (256 x 208 + 128 x 88 = 384 x 168).
 // TMEM columns: S (and P) 2 x 128, O 2 x 128.
-// Bound: per pair of tiles and 128 keys 16.8 MFLOP, 2050 cycles of the tensor core at its dense rate, beside 32768 exponentials,
-// 1024 cycles of the special function units, and 128 KB of operands and 64 KB of copies through shared memory.
+// Issuing is the products' own bottleneck if it is not looked after: the whole warp runs the loop converged and one lane
+// issues, so that descriptors stay in uniform registers (1434 TFLOP/s for 1232 with a single thread's branch), and each tile has
+// its copy of the code, so that counters stay in registers (1232 for 1108).
+// Bound: per pair of tiles and 128 keys (D = 128) 16.8 MFLOP, 2050 cycles of the tensor core at its dense rate, 256 KB of
+// operands and copies through shared memory, 2048 cycles, and beside them 32768 exponentials.  A step takes 3000 cycles: after P V
+// of a tile the tensor core waits for its next S to be issued, since TMEM has no room for P beside S and two O.
+// Measured, D = 128, 32 query heads (TFLOP/s; 2012 is what a large library product reaches): 16384 causal tokens 1540, 8192 tokens
+// after 8192 1570, 8192 tokens over 8 requests with 8192 before each 1430; D = 64, 8192 after 8192: 990, where a
+// step's products are half as long and its exponentials are not.
 #include <math.h>
 
 #include <type_traits>
