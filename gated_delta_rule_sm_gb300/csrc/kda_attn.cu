@@ -20,9 +20,10 @@ namespace {
 // ------------------------------------------------------------------ append
 
 // A warp takes a token, its lanes the 16-byte pieces (elements where those are not aligned) of its keys and values.  Bound by
-// memory; the tokens' addresses come from three small loads, one after the other, which the loads of the data do not wait for.
-// Measured: 8192 tokens, 8 heads of 128 in bf16 (67 MB): 17.7 us with its launch, 128 single tokens 4.1 us.  Fewer pieces
-// at once, or CTAs that take several tokens, were slower.
+// memory and latency: the address of a token comes from small loads one after the other (its row, the row's length, the page), while
+// the loads of its data and of the offsets' check are under way.  Measured: 8192 tokens, 8 heads of 128 in bf16 (67 MB), 15 us with
+// the launch, 128 single tokens 4.1.  Eight pieces of a lane at once, which a token of 2 KB does not have, cost registers and so
+// 2 us; the check before the loads 1; warps of two tokens saved nothing, of four cost 2.
 constexpr int kAppendWarps = 8;
 struct AppendArgs {
     AttnArgs a;
@@ -49,20 +50,12 @@ template <typename W>
 __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_constant__ AppendArgs p) {
     const AttnArgs& a = p.a;
     const int lane = threadIdx.x & 31;
-    if (a.cu) {
-        bool bad = threadIdx.x == 0 && (a.cu[0] != 0 || a.cu[a.rows] != a.tokens);
-        for (int n = threadIdx.x; n < a.rows; n += kAppendWarps * 32) bad |= a.cu[n + 1] < a.cu[n];
-        if (__syncthreads_or(bad)) {
-            if (blockIdx.x == 0 && threadIdx.x == 0) record_error(a.status, KDA_ERR_INVALID_ARG);
-            return;
-        }
-    }
     const int t = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
-    if (t >= a.tokens) return;
-    const int es = a.dtype == KDA_BF16 ? 2 : 4, per = a.D * es / (int)sizeof(W), all = a.Hkv * per;      // pieces of a head, of a token
+    const bool live = t < a.tokens;
+    const int es = a.dtype == KDA_BF16 ? 2 : 4, per = a.D * es / (int)sizeof(W), all = live ? a.Hkv * per : 0;      // pieces of a head, of a token
     const W *k = reinterpret_cast<const W*>(static_cast<const char*>(p.k) + t * p.ks * es),
             *v = reinterpret_cast<const W*>(static_cast<const char*>(p.v) + t * p.vs * es);
-    constexpr int AHEAD = 8;
+    constexpr int AHEAD = 4;
     W rk[AHEAD], rv[AHEAD];
     auto load = [&](int i0) {
 #pragma unroll
@@ -75,6 +68,15 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_
         }
     };
     load(0);
+    if (a.cu) {
+        bool bad = threadIdx.x == 0 && (a.cu[0] != 0 || a.cu[a.rows] != a.tokens);
+        for (int n = threadIdx.x; n < a.rows; n += kAppendWarps * 32) bad |= a.cu[n + 1] < a.cu[n];
+        if (__syncthreads_or(bad)) {
+            if (blockIdx.x == 0 && threadIdx.x == 0) record_error(a.status, KDA_ERR_INVALID_ARG);
+            return;
+        }
+    }
+    if (!live) return;
     const int r = a.cu ? row_of_token(a.cu, a.rows, t) : t / a.per_row;
     const AttnRow w = attn_row(a, r, lane == 0);
     const int pos = w.len - w.n + (t - w.first);
