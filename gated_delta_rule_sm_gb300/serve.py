@@ -209,11 +209,14 @@ def prompt(model: Decoder, cache: StateCache, tokens, cu_seqlens, rows, more: bo
 
 
 def step(model: Decoder, cache: StateCache, tokens, rows):
-    """The next token [B] of each row.  Returns the logits [B, vocab]."""
+    """The next token [B] of each row.  Returns the logits [B, vocab]; a row whose keys and values find no free page stays as
+    it is and gets NaN."""
     H, P, N, G = model.heads, model.head_dim, model.state_dim, model.groups
     h = model.embed[tokens]
     slots = cache.slots(rows)
-    cache.grow(rows, 1)
+    if cache.kv is not None:
+        refused = cache.grow(rows, 1) == 0
+        rows, slots = (t.masked_fill(refused, -1) for t in (rows, slots))
     for layer, pool in zip(model.layers, cache.pools):
         conv, gate, rest = _split(model, layer, _rms(h) @ layer["w_in"])
         if layer["kind"] == "a":
@@ -234,7 +237,8 @@ def step(model: Decoder, cache: StateCache, tokens, rows):
             y, _ = gated_step(conv, g_raw, i_raw, layer["a_log"], state=pool["state"][0], slots=slots)
             y = y.unflatten(-1, (H, P))
         h = _mix_out(model, layer, h, y, gate)
-    return (_rms(h) @ model.head).float()
+    logits = (_rms(h) @ model.head).float()
+    return logits if cache.kv is None else logits.masked_fill(refused[:, None], math.nan)
 
 
 def offsets(lengths, device="cuda"):

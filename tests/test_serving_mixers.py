@@ -84,6 +84,28 @@ def test_refused_admissions_and_forks_leave_no_pages():
     assert kda.device_status() == 0
 
 
+def test_a_step_without_a_free_page_changes_nothing():
+    """Its row is left as it was, gets NaN, and goes on when there is a page again; the other rows do not notice."""
+    model = serve.Decoder(pattern="dsga")
+    g = torch.Generator().manual_seed(5)
+    prompts, nxt = torch.randint(0, 512, (1, 62), generator=g).cuda(), torch.randint(0, 512, (2, 3), generator=g).cuda()
+    rows, off = ids(0, 1), serve.offsets([30, 32])
+    caches = [serve.StateCache(model, slots=4, sequences=3, kv_pages=n, kv_row=4) for n in (12, 5)]
+    for cache in caches:
+        assert cache.admit(ids(0, 1, 2), ids(30, 32, 9)).tolist() == [1] * 3      # 2, 2 and 1 pages
+        serve.prompt(model, cache, prompts, off, rows)
+    plenty, few = caches
+    want = [serve.step(model, plenty, nxt[:, k], rows) for k in range(3)]
+    for k in range(2):
+        got = serve.step(model, few, nxt[:, k], rows)                             # row 1 would need a third page
+        assert close(got[0], want[k][0]) and bool(torch.isnan(got[1]).all())
+    assert few.kv_lengths.tolist() == [32, 32, 9]
+    few.release(ids(2))
+    for k in range(3):
+        assert close(serve.step(model, few, nxt[1:, k], rows[1:])[0], want[k][1])
+    assert kda.device_status() == 0
+
+
 def test_command_runs(monkeypatch, capsys):
     monkeypatch.setattr("sys.argv", ["serve", "--prompts", "9", "70", "--samples", "2", "--steps", "3", "--layers", "4", "--pattern", "dgas"])
     serve.main()
