@@ -15,12 +15,12 @@
 // The backward pass runs the same chain from the last token to the first, on m_t = a_t (dy_t + m_{t+1}), the
 // gradient of h_{t-1}; the states it needs enter every 64th token from the forward's record and are carried on inside
 // a tile.
-// Measured, 16384 tokens x 4096 channels in bf16: forward 149 us with 12 documents and 142 us with 4 rows (537 MB: 3.7
+// Measured, 16384 tokens x 4096 channels in bf16: forward 135 us with 12 documents and 131 us with 4 rows (537 MB: 4.1
 // TB/s), backward 262 us (1.34 GB: 5.1 TB/s; a copy reaches 6.7).  Bound by both sides of a tile's life: the instructions
-// (100 for two channels of a token forward, 190 backward, 60% of the issue slots) and the waits between its phases.
-// Without the chain's waits the forward took 123 us, without the gates' arithmetic as well 108.  The tile's size is at its best: eight
-// warps and 4 CTAs of an SM forward, 3 backward; with 16 warps and tiles of 128 tokens 164 and 323 us, with 4 warps and tiles of
-// 32 tokens 163 and 276.  A fifth CTA (the inputs kept in shared memory, 40 registers) changed nothing.
+// (some 90 for two channels of a token forward, 180 backward, 60% of the issue slots) and the waits between its phases.
+// Without the chain's waits the forward took 117 us.  The tile's size is at its best: eight warps and 4 CTAs of an SM forward,
+// 3 backward; before the copies went ahead (149 and 262 us), 16 warps and tiles of 128 tokens took 164 and 323, 4 warps and tiles of
+// 32 tokens 163 and 276, and a fifth CTA (the inputs kept in shared memory, 40 registers) as long as four.
 // Precision: everything in fp32.  1 - a comes from a series in log a, so that decays next to 1, the long memories,
 // are right to a rounding, and sqrt(1 - a^2) = sqrt(e (2 - e)) with e = 1 - a loses nothing there either.
 #include <math.h>
@@ -296,7 +296,7 @@ __device__ __forceinline__ void ask(const float* p, float2& a, float2& b) {
 // leaving state on, the pairs of those between, in order.  The first tile of a chain, and every tile in which a row begins,
 // tells a state, so there is one.  At most about a second, then the error is recorded and the state is 0.
 template <typename V> __device__ __forceinline__ V look_back(const GatedArgs& a, int o, int c) {
-    constexpr int W = 4;                 // tiles looked at together (1, 2: the same time; 8: 166 us for 146, the L2 is asked too often)
+    constexpr int W = 4;                 // tiles looked at together (1, 2: the same time; 8: 158 us for 137, the L2 is asked too often)
     const float *inc = a.inc + c, *agg = a.agg + 2 * (size_t)c;
     int near = o - 1;                    // the pairs of the tiles above it are there
     V s = vdup<V>(0.f);
@@ -357,7 +357,7 @@ __device__ __forceinline__ void join_chain(const GatedArgs& a, int o, int c, boo
     give(s);
 }
 
-// Barriers of a tile: 4, which tile it is, is known (the eight warps wait); 1, its runs are in shared memory (the chain's warp
+// Barriers of a tile: 4, backward, which tile it is, is known (the eight warps wait); 1, its runs are in shared memory (the chain's warp
 // waits); 2, the entering state is (the others wait); 3, the eight warps among themselves.
 __device__ __forceinline__ void runs_ready() {
     __syncwarp();
@@ -376,8 +376,10 @@ template <bool TELLS> __device__ __forceinline__ void tile_known() {
 }
 __device__ __forceinline__ void tile_sync() { asm volatile("bar.sync 3, %0;" ::"n"(kThreads) : "memory"); }
 
-// Tiles in the order in which they are begun.  A CTA takes the next one when it knows the state that enters the one it has, not
-// earlier: a tile that was taken and not begun holds up all that wait for it (188 us for 154 with tickets and copies a tile ahead).
+// Tiles in the order in which they are begun.  A tile that was taken and not begun holds up all that wait for it.  Forward a CTA
+// takes its next one when it has told the runs of the one it has, and copies it while it waits for the entering state
+// (taken with that state known, 149 us for 141; a whole tile ahead, 188).  Backward the copies have to stay until the gradients are
+// formed, and the next tile is taken when the entering state is known.
 __device__ __forceinline__ int take_ticket(const GatedArgs& a, int before) {
     return a.planned ? atomicAdd(a.ticket, 1) : before < 0 ? (int)blockIdx.x : before + (int)gridDim.x;
 }
@@ -483,7 +485,7 @@ template <int VEC> __device__ __forceinline__ bool whole_tile(const GatedArgs& a
 
 // ------------------------------------------------------------------ forward
 
-// A tile as the ninth warp announces it: its place in the chain (past the last: none), itself, its columns; and, backwards, one that
+// A tile as the one who takes it announces it (the first thread, backward the ninth warp): its place in the chain (past the last: none), itself, its columns; and, backwards, one that
 // comes as many tickets later as there are CTAs.
 struct TileWord {
     int o, tile, col, soon_o, soon_col;
@@ -501,8 +503,8 @@ template <typename E, int VEC> struct FwdShared {
 };
 
 // EDGE: the tile has rows that begin or end in it, tokens or channels past the last, or a rate above 1/4.
-template <typename E, int VEC, bool EDGE>
-__device__ __forceinline__ void forward_tile(const GatedArgs& a, const Spot& s, FwdShared<E, VEC>& m_, bool split, const Rate<Val<VEC>>& rate) {
+template <typename E, int VEC, bool EDGE, typename N>
+__device__ __forceinline__ void forward_tile(const GatedArgs& a, const Spot& s, FwdShared<E, VEC>& m_, bool split, const Rate<Val<VEC>>& rate, N&& next) {
     using V = Val<VEC>;
     const Edges& edges = m_.edges;
     auto &sp = m_.sp, &sh = m_.sh;
@@ -542,10 +544,18 @@ __device__ __forceinline__ void forward_tile(const GatedArgs& a, const Spot& s, 
         m_.w.needs = !EDGE || !split || edges.first[0] < 0;
     }
     runs_ready();
-    state_wait();
-    h = m_.senter[s.lane];
+    next();
+    // meanwhile the runs of the warps before this one
     auto over = [](V P, V s, V h) { return EDGE ? join(P, s, h) : vfma(P, s, h); };
-    for (int w = 0; w < s.warp; ++w) h = over(sp[w][s.lane], h, sh[w][s.lane]);
+    P = vdup<V>(1.f);
+    h = vdup<V>(0.f);
+    for (int w = 0; w < s.warp; ++w) {
+        const V p = sp[w][s.lane];
+        P = over(p, P, vdup<V>(0.f));
+        h = over(p, h, sh[w][s.lane]);
+    }
+    state_wait();
+    h = over(P, m_.senter[s.lane], h);
     E* y = static_cast<E*>(a.y) + (size_t)s.t0 * a.C;
     const uint32_t at = s.warp * kTok * (uint32_t)a.C + s.c;
 #pragma unroll
@@ -558,8 +568,9 @@ __device__ __forceinline__ void forward_tile(const GatedArgs& a, const Spot& s, 
         }
 }
 
-// The loop of both passes.  load(spot) issues a tile's copies, work(spot, hint, rate) does it, soon(tile, columns)
-// asks the L2 for a later one (backwards alone: it brought 301 to 287 us there, but 154 to 159 forward).  The ninth warp takes the tickets and joins
+// The loop of both passes.  load(spot) issues a tile's copies, work(spot, hint, rate, next) does it and, forward, calls next() when its
+// copies have been read, soon(tile, columns)
+// asks the L2 for a later one (backwards alone: it brought 301 to 287 us there, but 154 to 159 forward).  The ninth warp joins
 // the chain: the runs of the warps from the first (or, backwards, from the last) on.
 template <bool BACK, int VEC, typename L, typename N, typename W>
 __device__ __forceinline__ void walk_tiles(const GatedArgs& a, TileWords& w, Val<VEC> (&sp)[kWarps][32], Val<VEC> (&sh)[kWarps][32],
@@ -569,29 +580,32 @@ __device__ __forceinline__ void walk_tiles(const GatedArgs& a, TileWords& w, Val
     // (offsets that break the contract: the plan has found no tile's first row, and nothing is read by them)
     const bool go = !a.planned || *a.ok;
     if (!go) return;
+    const int lane = threadIdx.x & 31;
+    int before = -1;
+    auto take = [&](int it) {            // (by one thread)
+        const uint32_t ticket = take_ticket(a, before);
+        before = (int)ticket;
+        TileWord n;
+        n.o = ticket < total ? (int)(ticket / (uint32_t)a.cols) : a.tiles;
+        n.col = (int)(ticket - (uint32_t)n.o * a.cols);
+        n.tile = BACK ? a.tiles - 1 - n.o : n.o;
+        if constexpr (BACK) {
+            const uint32_t later = ticket + gridDim.x;
+            n.soon_o = later < total ? (int)(later / (uint32_t)a.cols) : a.tiles;
+            n.soon_col = (int)(later - (uint32_t)n.soon_o * a.cols);
+        }
+        w.at[it & 1] = n;
+    };
     if (threadIdx.x >= kThreads) {
-        const int lane = threadIdx.x & 31;
-        int before = -1;
         for (int it = 0;; ++it) {
-            uint32_t ticket = 0;
-            if (lane == 0) {
-                ticket = take_ticket(a, before);
-                before = (int)ticket;
-                TileWord n;
-                n.o = ticket < total ? (int)(ticket / (uint32_t)a.cols) : a.tiles;
-                n.col = (int)(ticket - (uint32_t)n.o * a.cols);
-                n.tile = BACK ? a.tiles - 1 - n.o : n.o;
-                if constexpr (BACK) {
-                    const uint32_t later = ticket + gridDim.x;
-                    n.soon_o = later < total ? (int)(later / (uint32_t)a.cols) : a.tiles;
-                    n.soon_col = (int)(later - (uint32_t)n.soon_o * a.cols);
-                }
-                w.at[it & 1] = n;
+            if constexpr (BACK) {
+                if (lane == 0) take(it);
+                tile_known<true>();
+                if (w.at[it & 1].o >= a.tiles) return;
             }
-            tile_known<true>();
-            const int o = w.at[it & 1].o, c = (w.at[it & 1].col * 32 + lane) * VEC;
-            if (o >= a.tiles) return;
             runs_wait();
+            const int o = w.at[it & 1].o, c = (w.at[it & 1].col * 32 + lane) * VEC;
+            if (!BACK && o >= a.tiles) return;
             V P = sp[BACK ? kWarps - 1 : 0][lane], h = sh[BACK ? kWarps - 1 : 0][lane];
 #pragma unroll
             for (int k = 1; k < kWarps; ++k) {
@@ -606,20 +620,35 @@ __device__ __forceinline__ void walk_tiles(const GatedArgs& a, TileWords& w, Val
             if (!BACK && a.rec && c < a.C) vstore(a.rec + (size_t)o * a.C + c, enters);
         }
     }
+    if constexpr (!BACK) {
+        if (threadIdx.x == 0) take(0);
+        tile_sync();
+        if (w.at[0].o < a.tiles) load(spot_of<VEC>(a, w.at[0].tile, w.at[0].col));
+    }
     for (int it = 0;; ++it) {
-        tile_known<false>();
+        if constexpr (BACK) tile_known<false>();
         const TileWord now = w.at[it & 1];
-        if (now.o >= a.tiles) return;
+        if (now.o >= a.tiles) {
+            if (!BACK) runs_ready();
+            return;
+        }
         const Spot s = spot_of<VEC>(a, now.tile, now.col);
-        load(s);
-        if constexpr (BACK)
+        if constexpr (BACK) {
+            load(s);
             if (now.soon_o < a.tiles) soon(a.tiles - 1 - now.soon_o, now.soon_col);
+        }
         RowHint hint;
         hint.row = a.cu ? a.first[s.tile] : (int)(((uint32_t)s.t0 + a.T - 1) / (uint32_t)a.T);
         hint.begin = row_begin(a, hint.row);
         const Rate<V> rate = rate_of(s.in ? vload<V>(a.a_log + s.c) : vdup<V>(-1e30f));
         copies_landed();
-        work(s, hint, rate);
+        work(s, hint, rate, [&]() {
+            // the next tile, whose copies go where this one's were
+            if (threadIdx.x == 0) take(it + 1);
+            tile_sync();
+            const TileWord next = w.at[(it + 1) & 1];
+            if (next.o < a.tiles) load(spot_of<VEC>(a, next.tile, next.col));
+        });
     }
 }
 
@@ -637,11 +666,11 @@ __global__ void __launch_bounds__(kAll, kFwdCtas) gated_fwd_kernel(const __grid_
             load_plane<E, VEC>(a.i, a.is, s, whole, a.aligned, m.i);
         },
         [](int, int) {},
-        [&](const Spot& s, const RowHint& hint, const Rate<Val<VEC>>& rate) {
+        [&](const Spot& s, const RowHint& hint, const Rate<Val<VEC>>& rate, auto&& next) {
             const bool split = has_edges(a, s.t0, hint);
             if (split) find_edges(a, s.t0, hint, m.edges);
-            if (whole_tile<VEC>(a, s) && !split && !rate.wide) forward_tile<E, VEC, false>(a, s, m, split, rate);
-            else forward_tile<E, VEC, true>(a, s, m, split, rate);
+            if (whole_tile<VEC>(a, s) && !split && !rate.wide) forward_tile<E, VEC, false>(a, s, m, split, rate, next);
+            else forward_tile<E, VEC, true>(a, s, m, split, rate, next);
         });
 }
 
@@ -778,7 +807,7 @@ __global__ void __launch_bounds__(kAll, kBwdCtas) gated_bwd_kernel(const __grid_
             else if (threadIdx.x < 3 * kTile) prefetch_row<E, VEC>(a, a.i, a.is, tile, col, row);
             else prefetch_row<E, VEC>(a, a.dy, a.C, tile, col, row);
         },
-        [&](const Spot& s, const RowHint& hint, const Rate<Val<VEC>>& rate) {
+        [&](const Spot& s, const RowHint& hint, const Rate<Val<VEC>>& rate, auto&&) {
             const bool split = has_edges(a, s.t0, hint);
             if (split) find_edges(a, s.t0, hint, m.edges);
             if (whole_tile<VEC>(a, s) && !split && !rate.wide) backward_tile<E, VEC, false>(a, s, m, split, rate);

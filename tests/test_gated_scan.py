@@ -141,6 +141,31 @@ def test_document_untouched_by_its_neighbours():
     assert torch.equal(y[:, 70:220], y2[:, 70:220]) and torch.equal(last[1], last2[1])
 
 
+@pytest.mark.parametrize("first", [5, 8, 30, 61, 64, 100])
+def test_documents_beside_broken_ones_in_a_tile(first):
+    """NaN in every input of the documents around it, at any place of a tile of tokens, forward and backward."""
+    off = [0, first, first + 23, first + 60]
+    cu = torch.tensor(off, dtype=torch.int32, device=DEV)
+    i, g = inputs(11, (1, off[-1]), 66, "bf16")
+    s0, ds = torch.randn(3, 66, generator=g).to(DEV), torch.randn(3, 66, generator=g).to(DEV)
+    dy = torch.randn(1, off[-1], 66, generator=g).to(DT["bf16"]).to(DEV)
+    y, last = run(i, initial_state=s0, output_final_state=True, cu_seqlens=cu)
+    grads = kda.gated_scan_backward(i["x"], i["g_raw"], i["i_raw"], i["a_log"], dy, cu_seqlens=cu, initial_state=s0, dfinal_state=ds)
+    mine = slice(off[1], off[2])
+    j = {k: v.clone() for k, v in i.items()}
+    others = [j["x"], j["g_raw"], j["i_raw"], dy]
+    for t in others:
+        t[:, :off[1]], t[:, off[2]:] = float("nan"), float("nan")
+    for t in (s0, ds):
+        t[0], t[2] = float("nan"), float("nan")
+    y2, last2 = run(j, initial_state=s0, output_final_state=True, cu_seqlens=cu)
+    assert torch.equal(y[:, mine], y2[:, mine]) and torch.equal(last[1], last2[1])
+    grads2 = kda.gated_scan_backward(j["x"], j["g_raw"], j["i_raw"], j["a_log"], dy, cu_seqlens=cu, initial_state=s0, dfinal_state=ds)
+    for n in ("dx", "dg_raw", "di_raw"):
+        assert torch.equal(grads[n][:, mine], grads2[n][:, mine]), n
+    assert torch.equal(grads["dinitial_state"][1], grads2["dinitial_state"][1])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_gates_and_rates_at_their_ends(dtype):
     """Closed and open gates, rates from 0 to past fp32: no NaN, and the reference's values."""
