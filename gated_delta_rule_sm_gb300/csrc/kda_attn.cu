@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
 
 // A CTA takes some rows of one item (a unit for one key head) that several CTAs share.  With few parts a warp takes a
 // row and reads them and their maxima at once; with many (a few rows over a long cache) the warps split the parts of a row,
-// four of each warp's on the way at once, since it is their latency that counts (43 -> 37 us for one row over 32768 tokens).
+// four of each warp's on the way at once, since it is their latency that counts (61 -> 43 us for one row over 32768 tokens).
 // The attention's CTAs say which items they share, and the join is launched while they run: 3 us after a step, 14 us after
 // a chunk of 8192 tokens.
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinFew = 4;
@@ -547,7 +547,7 @@ size_t attn_layout(char* ws, AttnArgs* a) {
 // Which kernel a call takes, and its cut.  aligned: the pool's base allows 16-byte copies.
 // mma reads a row's keys once for 16 packed rows, tc for 256: mma where a row has 16 on average at most (4 query heads to a key
 // head, D = 128, attention and join: 16 packed rows of 8 requests over 8192 keys 71 us by mma, 68 by tc; of 64 over 2048 115
-// and 115; with D = 64 single tokens of the 8 requests 45 and 50, of the 64 76 and 92), tc above it (32 packed rows: 93 us by mma, 70 by
+// and 115; with D = 64 single tokens of the 8 requests 48 and 53, of the 64 77 and 95), tc above it (32 packed rows: 93 us by mma, 70 by
 // tc; 198 and 118).
 // Their two or one CTAs of an SM share its registers and shared memory; extra: an item's beginning and end in key tiles, fitted to the
 // CTAs' own times (tc: 8.2 us for an item, 1.53 us for a tile; cuts with 1 in place of 4 left some CTAs at twice the mean of
@@ -674,9 +674,9 @@ kda_status kda_pages_attention(const kda_attention_dims* dims, const void* q, co
     const cudaError_t e = a.kernel == kAttnTc ? launch_attn_tc(a, stream) : a.kernel == kAttnMma ? launch_attn_mma(a, stream) : launch_attn_simt(a, stream);
     timing_post(stream);
     if (e != cudaSuccess) return KDA_ERR_CUDA;
-    // rows of a block that may exist; a CTA for each where they are few
+    // rows of a block that may exist; a CTA for each where they are few, else a warp (two rows of a warp: 2 us more for small chunks)
     const int64_t longest = (cu_seqlens ? a.tokens : a.per_row) * (int64_t)a.G;
-    const int rows = (int)(longest < a.block ? longest : a.block), each = a.block <= 32 ? 1 : 2 * kJoinWarps;
+    const int rows = (int)(longest < a.block ? longest : a.block), each = a.block <= 32 ? 1 : kJoinWarps;
     timing_pre(stream, K_ATTN_JOIN);
     // (launched while the attention still runs; it waits for its end itself)
     if (a.ctas > 1)

@@ -8,7 +8,7 @@
 // A warp is on its own: it takes 16 of a tile's 64 keys, copies them and their values to its own ring in shared memory
 // (cp.async, two stages ahead, so that an SM has 128 KB on the way), and keeps its own maxima, sums and output; the
 // four warps of a CTA meet when a piece ends.  A lane looks up the page of one key, a stage before its address is needed.
-// Measured: one token over 32768 keys, 32 query heads on 8 key heads, D = 128 (134 MB): 30.8 us of the kernel, of which the copies
+// Measured: one token over 32768 keys, 32 query heads on 8 key heads, D = 128 (134 MB): 30 us of the kernel, of which the copies
 // run 22 (6.2 TB/s); 4 go by before the first are issued (lengths and the page table are read one after the other, by all
 // CTAs at once) and 3 for the first to arrive.  A batch of 64 such rows of up to 8192 tokens: 148 to 170 us for 0.91 GB, 5.4 to 6.2 TB/s.
 // Precision: scores and sums fp32; a weight meets the values as the sum of two bf16 values, off by 2^-16 of it at most (the
