@@ -143,6 +143,17 @@ def test_as_many_new_tokens_in_every_row(Hq, Hkv, D, pt, dtype, new):
     assert torch.equal(out, out2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("G,n,dtype", [(4, 1, "bf16"), (16, 2, "bf16"), (4, 1, "fp32")])
+def test_more_rows_than_a_cta_counts_for_itself(G, n, dtype):
+    """The plan's launch, for rows of one block each: lengths around a page, every ninth row idle, others without a token yet."""
+    rows = 601
+    held = [0 if r % 7 == 3 else n + r % 40 for r in range(rows)]
+    c = Case(held, [n] * rows, G, 1, 64, 16, dtype, seed=n, seqs=lambda o: [-1 if r % 9 == 5 else s for r, s in enumerate(o)])
+    q = c.q.to(DEV).reshape(rows, n, G, 64)
+    out, lse = c.run(q=q, packed=False)
+    c.check(out.reshape(1, -1, G, 64), lse.reshape(1, -1, G))
+
+
 def test_a_chunk_longer_than_its_sequence():
     """Tokens at negative positions have no keys: zeros, and they are not written."""
     for dtype in ("bf16", "fp32"):
