@@ -15,8 +15,8 @@
 // The backward pass runs the same chain from the last token to the first, on m_t = a_t (dy_t + m_{t+1}), the
 // gradient of h_{t-1}; the states it needs enter every 64th token from the forward's record and are carried on inside
 // a tile.
-// Measured, 16384 tokens x 4096 channels in bf16: forward 135 us with 12 documents and 131 us with 4 rows (537 MB: 4.1
-// TB/s), backward 262 us (1.34 GB: 5.1 TB/s; a copy reaches 6.7).  Bound by both sides of a tile's life: the instructions
+// Measured, 16384 tokens x 4096 channels in bf16: forward 134 us with 12 documents and 131 us with 4 rows (537 MB: 4.1
+// TB/s), backward 260 us (1.34 GB: 5.1 TB/s; a copy reaches 6.7).  Bound by both sides of a tile's life: the instructions
 // (some 90 for two channels of a token forward, 180 backward, 60% of the issue slots) and the waits between its phases.
 // Without the chain's waits the forward took 117 us.  The tile's size is at its best: eight warps and 4 CTAs of an SM forward,
 // 3 backward; before the copies went ahead (149 and 262 us), 16 warps and tiles of 128 tokens took 164 and 323, 4 warps and tiles of
@@ -183,15 +183,15 @@ template <bool WIDE> __device__ __forceinline__ float2 log_decay(float2 g, float
     return l;
 }
 
-// 1 - e^l for l <= 0.  Down to -1/4, -l times a polynomial of degree 4 for (1 - e^l) / -l (interpolated at the Chebyshev points of
+// 1 - e^l for l <= 0.  Down to -1/4, l times a polynomial of degree 4 for (1 - e^l) / l (interpolated at the Chebyshev points of
 // [-1/4, 0] in 64 bits; off by 5e-9 of the value with its coefficients in fp32); below, which only a wide rate can reach,
 // the exponential.
 template <typename V> __device__ __forceinline__ V one_minus_exp(V l, bool wide) {
-    V p = vfma(l, vdup<V>(0.007513606455177069f), vdup<V>(0.04149065539240837f));
-    p = vfma(p, l, vdup<V>(0.16665108501911163f));
-    p = vfma(p, l, vdup<V>(0.4999995231628418f));
-    p = vfma(p, l, vdup<V>(1.f));
-    V e = vmul(vmul(l, vdup<V>(-1.f)), p);
+    V p = vfma(l, vdup<V>(-0.007513606455177069f), vdup<V>(-0.04149065539240837f));
+    p = vfma(p, l, vdup<V>(-0.16665108501911163f));
+    p = vfma(p, l, vdup<V>(-0.4999995231628418f));
+    p = vfma(p, l, vdup<V>(-1.f));
+    V e = vmul(l, p);
     if (wide) {
         auto far = [](float t, float near) { return t < -0.25f ? 1.f - ex2(t * kLog2e) : near; };
         if constexpr (std::is_same_v<V, float2>) e = make_float2(far(l.x, e.x), far(l.y, e.y));
@@ -698,7 +698,7 @@ __device__ __forceinline__ void backward_tile(const GatedArgs& a, const Spot& s,
     const V one = vdup<V>(1.f), entering = s.in ? vload<V>(a.rec + (size_t)s.tile * a.C + c) : vdup<V>(0.f);
     // the forward's runs, from the first token on
     V P = one, h = vdup<V>(0.f);
-#pragma unroll 4
+#pragma unroll 8
     for (int k = 0; k < kTok; ++k) {
         V b, e = decay_of<EDGE>(mg[k][tid].get(), mi[k][tid].get(), mx[k][tid].get(), rate, b);
         if (EDGE && k >= s.n) e = b = vdup<V>(0.f);
@@ -717,7 +717,7 @@ __device__ __forceinline__ void backward_tile(const GatedArgs& a, const Spot& s,
     // the gradient's, from the last
     P = one;
     V m = vdup<V>(0.f);
-#pragma unroll 4
+#pragma unroll 8
     for (int k = kTok - 1; k >= 0; --k) {
         if (EDGE && k < s.n && ends_at(k) >= 0) {
             P = vdup<V>(0.f);
@@ -742,7 +742,7 @@ __device__ __forceinline__ void backward_tile(const GatedArgs& a, const Spot& s,
     // meanwhile the states before the tokens
     h = entering;
     for (int w = 0; w < warp; ++w) h = over(m_.sp[w][lane], h, m_.sh[w][lane]);
-#pragma unroll 4
+#pragma unroll 8
     for (int k = 0; k < kTok; ++k) {
         if (EDGE && k < s.n && begins_at(k) >= 0) h = row_of(a.s0, begins_at(k));
         const V b = m_.b[k][tid];
@@ -756,7 +756,7 @@ __device__ __forceinline__ void backward_tile(const GatedArgs& a, const Spot& s,
     const size_t base = (size_t)s.t0 * a.C;
     float *dx = a.dx + base, *dg = a.dg + base, *di = a.di + base;
     const uint32_t at = warp * kTok * (uint32_t)a.C + c;
-#pragma unroll 4
+#pragma unroll 8
     for (int k = kTok - 1; k >= 0; --k)
         if (!EDGE || k < s.n) {
             if (EDGE && ends_at(k) >= 0) m = row_of(a.dsT, ends_at(k));
