@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
 // 64 packed rows against 64 keys at a time, 256 threads of 4 x 4 scores each; Q, K and the weights lie transposed in
 // shared memory, so that a step of a product is two 16-byte reads for 16 multiplications.  A thread keeps 4 rows of D / 16
 // columns of the output.  Bound by fp32 arithmetic with full blocks; a block of few rows leaves most warps idle.  Measured:
-// 301 tokens of three requests over 700, 6 heads of 40, 30.4 us with the plan and the join, mostly latency: the cut gives a CTA a few tiles.
+// 301 tokens of three requests over 700, 6 heads of 40, 28.6 us with the plan and the join, mostly latency: the cut gives a CTA a few tiles.
 constexpr int kSimtRows = 64, kSimtKeys = 64, kSimtThreads = 256, kSimtPad = 68;
 
 template <typename E> __device__ __forceinline__ float4 load4(const char* p, int d, int D, bool vec) {
