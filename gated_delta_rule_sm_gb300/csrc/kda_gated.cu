@@ -30,6 +30,7 @@
 
 #include "kda.h"
 #include "kda_common.cuh"
+#include "kda_gated.h"
 #include "kda_internal.h"
 #include "kda_sm100.cuh"
 
@@ -39,9 +40,10 @@ using namespace sm100;
 
 namespace {
 
-// Eight warps do a tile's arithmetic, a ninth joins it to the chain of tiles.
-constexpr int kThreads = 256, kWarps = kThreads / 32, kAll = kThreads + 32;
-constexpr int kTok = 8, kTile = kWarps * kTok;      // tokens of a thread and of a CTA
+constexpr int kThreads = kGatedThreads, kWarps = kGatedWarps, kAll = kThreads + 32;
+constexpr int kTok = kGatedTok, kTile = kGatedTile;
+using Spot = GatedSpot;
+using Edges = GatedEdges;
 static_assert(kThreads == 4 * kTile, "a thread asks for a row of one of four arrays");
 constexpr int kFwdCtas = 4, kBwdCtas = 3;           // CTAs of an SM: as many as registers and shared memory allow
 constexpr float kLog2e = 1.4426950408889634f;
@@ -237,10 +239,6 @@ template <bool WIDE, typename V> __device__ __forceinline__ V decay_of(V g, V i,
 
 // ------------------------------------------------------------------ rows inside a tile
 
-// Which rows begin at and end with a token of the tile, -1: none.
-struct Edges {
-    int first[kTile], last[kTile];
-};
 __device__ __forceinline__ void tile_sync();
 
 // The first row that begins at or after token t0 of a tile, and where.
@@ -417,23 +415,8 @@ __global__ void __launch_bounds__(kThreads) gated_plan_kernel(GatedArgs a, const
                     to[(size_t)n * a.C + c] = from ? from[(size_t)n * a.C + c] : 0.f;
 }
 
-// What a thread has of a tile: its channels, and where its tokens lie.
-struct Spot {
-    int tile, col, warp, lane, c, t0, tb, n;      // c: first channel; tb, n: first token and how many there are
-    bool in;
-};
 template <int VEC> __device__ __forceinline__ Spot spot_of(const GatedArgs& a, int tile, int col) {
-    Spot s;
-    s.tile = tile;
-    s.col = col;
-    s.warp = threadIdx.x >> 5;
-    s.lane = threadIdx.x & 31;
-    s.c = (col * 32 + s.lane) * VEC;
-    s.in = s.c < a.C;
-    s.t0 = tile * kTile;
-    s.tb = s.t0 + s.warp * kTok;
-    s.n = s.in ? max(0, min(kTok, a.TT - s.tb)) : 0;
-    return s;
+    return gated_spot<VEC>(a.TT, a.C, tile, col, threadIdx.x);
 }
 // A [tokens, C] array's elements of the tile, a token's 32 lanes side by side as the threads will read them.
 template <typename E, int VEC> using Plane = Raw<E, VEC>[kTok][kThreads];
@@ -511,7 +494,8 @@ __device__ __forceinline__ void forward_tile(const GatedArgs& a, const Spot& s, 
     auto &mx = m_.x, &mg = m_.g, &mi = m_.i;
     const int tid = threadIdx.x;
     auto begins_at = [&](int k) { return EDGE && split ? edges.first[s.warp * kTok + k] : -1; };
-    // a token as h -> ka h + kb; where a row begins the state is the row's own, and ka is 0
+    // a token as h -> ka h + kb; where a row begins the state is the row's own, and ka is 0 (also for lanes past the last channel, which
+    // ask for no state: a branch of the whole warp took 1 % less than one of its lanes)
     V ka[kTok], kb[kTok], P, h;
 #pragma unroll
     for (int k = 0; k < kTok; ++k) {
@@ -522,7 +506,7 @@ __device__ __forceinline__ void forward_tile(const GatedArgs& a, const Spot& s, 
         }
         const bool begins = begins_at(k) >= 0;
         if (EDGE && begins) {
-            if (a.s0) kb[k] = vfma(ka[k], vload<V>(a.s0 + (size_t)begins_at(k) * a.C + s.c), kb[k]);
+            if (a.s0 && edges.begins(s, k) >= 0) kb[k] = vfma(ka[k], vload<V>(a.s0 + (size_t)begins_at(k) * a.C + s.c), kb[k]);
             ka[k] = vdup<V>(0.f);
         }
         if (k == 0 || (EDGE && begins)) {
@@ -563,8 +547,7 @@ __device__ __forceinline__ void forward_tile(const GatedArgs& a, const Spot& s, 
         if (!EDGE || k < s.n) {
             h = EDGE && begins_at(k) >= 0 ? kb[k] : vfma(ka[k], h, kb[k]);
             if (a.y) Raw<E, VEC>::store(y, at + k * (uint32_t)a.C, h);
-            if (EDGE && split && a.sT && edges.last[s.warp * kTok + k] >= 0)
-                vstore(a.sT + (size_t)edges.last[s.warp * kTok + k] * a.C + s.c, h);
+            if (EDGE && split && a.sT && edges.ends(s, k) >= 0) vstore(a.sT + (size_t)edges.ends(s, k) * a.C + s.c, h);
         }
 }
 
@@ -691,8 +674,8 @@ __device__ __forceinline__ void backward_tile(const GatedArgs& a, const Spot& s,
     using V = Val<VEC>;
     const int tid = threadIdx.x, warp = s.warp, lane = s.lane, c = s.c;
     auto &mx = m_.x, &mg = m_.g, &mi = m_.i, &md = m_.dy;
-    auto begins_at = [&](int k) { return EDGE && split ? m_.edges.first[warp * kTok + k] : -1; };
-    auto ends_at = [&](int k) { return EDGE && split ? m_.edges.last[warp * kTok + k] : -1; };
+    auto begins_at = [&](int k) { return EDGE && split ? m_.edges.begins(s, k) : -1; };
+    auto ends_at = [&](int k) { return EDGE && split ? m_.edges.ends(s, k) : -1; };
     auto row_of = [&](const float* p, int row) { return p ? vload<V>(p + (size_t)row * a.C + c) : vdup<V>(0.f); };
     auto over = [](V P, V s, V h) { return EDGE ? join(P, s, h) : vfma(P, s, h); };
     const V one = vdup<V>(1.f), entering = s.in ? vload<V>(a.rec + (size_t)s.tile * a.C + c) : vdup<V>(0.f);
@@ -719,7 +702,7 @@ __device__ __forceinline__ void backward_tile(const GatedArgs& a, const Spot& s,
     V m = vdup<V>(0.f);
 #pragma unroll 8
     for (int k = kTok - 1; k >= 0; --k) {
-        if (EDGE && k < s.n && ends_at(k) >= 0) {
+        if (EDGE && ends_at(k) >= 0) {
             P = vdup<V>(0.f);
             m = row_of(a.dsT, ends_at(k));
         }
@@ -744,7 +727,7 @@ __device__ __forceinline__ void backward_tile(const GatedArgs& a, const Spot& s,
     for (int w = 0; w < warp; ++w) h = over(m_.sp[w][lane], h, m_.sh[w][lane]);
 #pragma unroll 8
     for (int k = 0; k < kTok; ++k) {
-        if (EDGE && k < s.n && begins_at(k) >= 0) h = row_of(a.s0, begins_at(k));
+        if (EDGE && begins_at(k) >= 0) h = row_of(a.s0, begins_at(k));
         const V b = m_.b[k][tid];
         m_.b[k][tid] = h;
         h = vfma(keep_of(m_.e[k][tid]), h, b);
