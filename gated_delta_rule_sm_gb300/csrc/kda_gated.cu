@@ -144,10 +144,11 @@ __device__ __forceinline__ float min_nan(float x, float y) {     // NaN if eithe
 }
 
 // e^-z for the gradients, which need 1 less the sigmoid as well; it stops at 2^60: the product of two sums 1 + e^-z stays
-// finite, and one reciprocal serves both gates.  From there, z = -41.6, a sigmoid stays at 2^-60, 9e-19, which no sum it
-// enters can tell from zero.
+// finite, and one reciprocal serves both gates.  From there, z = -41.6, the sigmoid stays at 2^-60, 9e-19.  Next to x and 1 - sigmoid,
+// which is 1, that is zero; log a is not formed from it (decay_log).
+constexpr float kGateStop = 0x1p60f;
 template <typename V> __device__ __forceinline__ V exp_neg(V z) {
-    return vmap([](float t) { return min_nan(ex2(t), 0x1p60f); }, vmul(z, vdup<V>(-kLog2e)));
+    return vmap([](float t) { return min_nan(ex2(t), kGateStop); }, vmul(z, vdup<V>(-kLog2e)));
 }
 
 // The rate of a channel, -exp(a_log); wide: some rate of the warp is above 1/4.
@@ -202,8 +203,8 @@ template <typename V> __device__ __forceinline__ V one_minus_exp(V l, bool wide)
     return e;
 }
 
-// 1 / sqrt(1 - a^2) from w = 1 - a^2 = e (2 - e).  Where a is 1 to fp32 it stops at 1e18: the input's factor w / sqrt(w) is then 0, and
-// log a, which the gradients multiply by it, is below 1e-36.
+// 1 / sqrt(1 - a^2) from w = 1 - a^2 = e (2 - e).  Where a is 1 to fp32 it stops at 1e18: w, and with it -log a, is then below 1e-36, so that
+// the input's factor w / sqrt(w) and the gradients' log a / sqrt(w) are below 1e-18, as their limit is.
 template <typename V> __device__ __forceinline__ V square_of(V e) { return vmul(e, vfma(e, vdup<V>(-1.f), vdup<V>(2.f))); }
 template <typename V> __device__ __forceinline__ V root_of(V w) {
     return vmap([](float t) { return rsq(fmaxf(t, 1e-36f)); }, w);
@@ -223,6 +224,19 @@ template <typename V> __device__ __forceinline__ Gates<V> gates_of(V g, V i) {
     k.sg = vmul(r, db);
     k.si = vmul(r, da);
     return k;
+}
+
+// log a of a token whose e = 1 - a is known, for the gradients, which divide it by sqrt(1 - a^2).  Where the gate's e^-g stopped the sigmoid is too
+// large by up to any factor, and the quotient would be of the order of 1 where its limit is 0; e is of the true sigmoid, and
+// log a is -e there to less than a rounding (e < 2^-61).
+template <bool WIDE> __device__ __forceinline__ float decay_log(float g, float e, const Gates<float>& z, const Rate<float>& r) {
+    return WIDE && r.wide && !(r.n >= -0.25f) ? wide_log(g, r.log2) : z.eg == kGateStop ? -e : z.sg * r.n;
+}
+template <bool WIDE> __device__ __forceinline__ float2 decay_log(float2 g, float2 e, const Gates<float2>& z, const Rate<float2>& r) {
+    float2 l = log_decay<WIDE>(g, z.sg, r);
+    if (z.eg.x == kGateStop && (!WIDE || r.n.x >= -0.25f)) l.x = -e.x;
+    if (z.eg.y == kGateStop && (!WIDE || r.n.y >= -0.25f)) l.y = -e.y;
+    return l;
 }
 
 // What the state needs of them: a reciprocal each, which takes an infinite e^-z as it is.
@@ -751,7 +765,7 @@ __device__ __forceinline__ void backward_tile(const GatedArgs& a, const Spot& s,
             if (EDGE && begins_at(k) >= 0 && a.ds0) vstore(a.ds0 + (size_t)begins_at(k) * a.C + c, m);
             const V u = vmul(z.si, mx[k][tid].get()), du = vmul(dh, vmul(w, root));
             // of log a: a (h_{t-1} - u a / sqrt(1 - a^2)) times that of h_t; then times log a for a_log, and 1 - sigmoid(g) for g
-            const V dl = vmul(vmul(m, vfma(vmul(u, vdup<V>(-1.f)), vmul(ka, root), m_.b[k][tid])), log_decay<EDGE>(g, z.sg, rate));
+            const V dl = vmul(vmul(m, vfma(vmul(u, vdup<V>(-1.f)), vmul(ka, root), m_.b[k][tid])), decay_log<EDGE>(g, e, z, rate));
             dlog = vfma(dl, one, dlog);
             const uint32_t to = at + k * (uint32_t)a.C;
             vstore_stream(dx + to, vmul(du, z.si));

@@ -522,7 +522,8 @@ kda_status kda_short_conv_step(int B, int C, int W, kda_dtype dtype, const void*
  * contiguous.  Any C >= 1 and any alignment of the elements; bf16 with an even C, even strides and pairs of channels that
  * are aligned as such is read two channels at a time.  Arithmetic and states in fp32.
  * cu_seqlens and cu_seqlens_host: as for kda_ssm_fwd.  An empty document passes its state through.
- * Results do not depend on timing (the order of every sum is fixed).  Gates: in the gradients e^-g and e^-i stop at 2^60.
+ * Results do not depend on timing (the order of every sum is fixed).  In the gradients e^-g and e^-i stop at 2^60 where they give
+ * 1 - sigmoid and sigmoid(i), which is then 2^-60 at least; log a follows g all the way to 0.
  *
  * kda_gated_scan_fwd: initial_state (NULL: zero) and final_state (NULL: not wanted).  saved (NULL: not wanted):
  *   kda_gated_scan_saved_size() bytes, 256-byte aligned, gets the states that enter every 64th token of the flattened

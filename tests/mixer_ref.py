@@ -46,6 +46,36 @@ def gated_grads(x, g_raw, i_raw, a_log, offsets, state, dy, dlast):
             rate.grad.abs().sum(0))
 
 
+def gated_back(x, g_raw, i_raw, a_log, offsets, state, dy, dlast):
+    """The gradients by the chain rule, token by token, also where a decay is 1 or 0 in 64 bits: log a a / sqrt(1 - a^2) is then
+    its limit, 0.  Returns them, and for each the sizes its errors go by: per channel M, H and U, the largest gradient of a
+    state, state and input u = sigmoid(i) x, and per token the terms of d log a with M for the gradient, H and U for the state and u."""
+    x, g, i, rate, dy = d(x), d(g_raw), d(i_raw), d(a_log), d(dy)
+    log_a = -torch.exp(rate) * torch.sigmoid(g)
+    a, root = torch.exp(log_a), torch.sqrt(-torch.expm1(2 * log_a))
+    keep = torch.sigmoid(i)
+    u = keep * x
+    put = torch.where(root > 0, a * log_a / root.clamp(min=1e-300), torch.zeros_like(root))
+    decay = torch.where(a > 0, a * log_a, torch.zeros_like(a))
+    put = torch.where(a > 0, put, torch.zeros_like(put))
+    old, dh, first = torch.zeros_like(x), torch.zeros_like(x), []
+    for n in range(len(offsets) - 1):
+        h = torch.zeros_like(rate) if state is None else d(state)[n]
+        for t in range(offsets[n], offsets[n + 1]):
+            old[t] = h
+            h = a[t] * h + root[t] * u[t]
+        m = torch.zeros_like(rate) if dlast is None else d(dlast)[n]
+        for t in reversed(range(offsets[n], offsets[n + 1])):
+            dh[t] = dy[t] + m
+            m = a[t] * dh[t]
+        first.append(m)
+    dl = dh * (old * decay - u * a * put)
+    grads = dict(dx=dh * root * keep, dg_raw=dl * torch.sigmoid(-g), di_raw=dh * root * u * torch.sigmoid(-i), da_log=dl.sum(0),
+                 dinitial_state=torch.stack(first))
+    M, H, U = dh.abs().amax(0), old.abs().amax(0), u.abs().amax(0)
+    return grads, dict(M=M, H=H, U=U, X=x.abs().amax(0), log_a=log_a, root=root, keep=keep, terms=M * (H * decay.abs() + U * (a * put).abs()))
+
+
 def rows_of(offsets, lengths, seqs):
     """(tokens of the call, table row, positions) of every row; table row None: idle."""
     for r, (a, b) in enumerate(zip(offsets, offsets[1:])):

@@ -251,6 +251,50 @@ def test_gradients_of_documents(lengths, C, dtype):
         assert torch.equal(again[n], grads[n]), n
 
 
+def check_grads_at_the_ends(i, s0, dy, dlast):
+    """Against the chain rule, every gradient by its own terms.  Derived before the first run, u = 2^-24: GRAD for the products, as above;
+    a rate above 1/4 forms log a in exponents of up to |a_log| + |g|, three roundings of u each there, which the state and its
+    gradient take over once more: 8 u (|a_log| + |g|); a decay is 1 - e, off by u whatever it is, twice, with a factor log a that matters
+    down to e^-20: 2^-21 min(|log a|, 20); 1 - sigmoid and the input's sigmoid stop at 2^-60: 2^-59."""
+    T, C = i["x"].shape[1:]
+    grads = backward(i, dy, initial_state=s0, dfinal_state=dlast)
+    want, z = ref.gated_back(*[i[n].reshape(-1, C) for n in ("x", "g_raw", "i_raw")], i["a_log"], [0, T], s0, dy.reshape(-1, C), dlast)
+    rel = GRAD + 8 * 2.0 ** -24 * (ref.d(i["a_log"]).abs() + ref.d(i["g_raw"][0]).clamp(-400, 400).abs())
+    stop = 2.0 ** -59 * z["M"] * (z["H"] + z["X"] + 1)
+    tol = rel * z["terms"] + 2.0 ** -21 * z["log_a"].abs().clamp(max=20) * z["M"] * (z["H"] + z["U"]) + stop
+    tols = dict(dx=rel * z["M"] * z["root"] * z["keep"] + stop, dg_raw=tol, di_raw=rel * z["M"] * z["root"] * z["U"] + stop, da_log=tol.sum(0),
+                dinitial_state=rel.amax(0) * z["M"] + stop)
+    for n, t in tols.items():
+        err = (ref.d(grads[n]).reshape(want[n].shape) - want[n]).abs() / t
+        assert float(err.max()) <= 1.0, (n, float(err.max()), int(err.amax(0).argmax()) if err.dim() > 1 else int(err.argmax()))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_gradients_of_closed_gates(dtype):
+    """Gates that a large negative logit closes, at rates that the ordinary tiles take: whole tiles and those of the row's ends."""
+    T, rates = 256, [0.01, 0.05, 0.1, 0.24]
+    gates = [-1.0, -20.0, -30.0, -40.0, -41.0, -42.0, -45.0, -50.0, -55.0, -60.0, -70.0, -80.0, -90.0, -300.0, -1e4, -np.inf]
+    C = len(rates) * len(gates)
+    i, g = inputs(13, (1, T), C, dtype)
+    i["a_log"] = torch.log(torch.tensor(rates)).to(DEV).repeat_interleave(len(gates)).contiguous()
+    i["g_raw"] = torch.tensor(gates, device=DEV).repeat(len(rates)).expand(1, T, C).to(DT[dtype]).contiguous()
+    s0, dlast = (torch.randn(1, C, generator=g).to(DEV) for _ in range(2))
+    check_grads_at_the_ends(i, s0, torch.randn(1, T, C, generator=g).to(DT[dtype]).to(DEV), dlast)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_gradients_of_gates_and_rates_at_their_ends(dtype):
+    T, rates = 90, [-300.0, -60.0, -20.0, -1.4, -1.3, 0.0, 3.0, 88.0, 400.0]
+    gates = [-300.0, -90.0, -60.0, -41.0, -1.0, 0.0, 1.0, 41.0, 90.0, 300.0]
+    C = len(rates) * len(gates)
+    i, g = inputs(3, (1, T), C, dtype)
+    i["a_log"] = torch.tensor(rates, device=DEV).repeat_interleave(len(gates)).contiguous()
+    i["g_raw"] = torch.tensor(gates, device=DEV).repeat(len(rates)).expand(1, T, C).to(DT[dtype]).contiguous()
+    i["i_raw"] = torch.tensor(gates, device=DEV).flip(0).repeat(len(rates)).expand(1, T, C).to(DT[dtype]).contiguous()
+    s0 = torch.randn(1, C, generator=g).to(DEV)
+    check_grads_at_the_ends(i, s0, torch.randn(1, T, C, generator=g).to(DT[dtype]).to(DEV), None)
+
+
 def test_gradients_against_differences():
     """Along a direction, the gradients' product is the slope of the 64-bit forward (central differences, whose own error
     is h^2 of the third derivative, about 1e-8 here)."""
