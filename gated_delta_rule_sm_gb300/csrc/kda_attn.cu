@@ -478,14 +478,9 @@ __global__ void __launch_bounds__(kSimtThreads, DC > 2 ? 1 : 2) attn_simt_kernel
 
 template <typename E, int DC> cudaError_t simt_launch(const AttnArgs& a, cudaStream_t st) {
     const size_t D4 = (a.D + 3) / 4 * 4, bytes = 4 * (2 * D4 * kSimtPad + (size_t)kSimtKeys * 64 * DC + kSimtKeys * kSimtPad);
-    static bool set[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
-    if (dev < 0 || dev >= 64 || !set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<E, DC>, cudaFuncAttributeMaxDynamicSharedMemorySize, 222 * 1024);
-        if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) set[dev] = true;
-    }
+    // (the same for every D of the instance: calls of several threads may come between this and the launch)
+    const cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<E, DC>, cudaFuncAttributeMaxDynamicSharedMemorySize, 222 * 1024);
+    if (e != cudaSuccess) return e;
     return attn_launch(attn_simt_kernel<E, DC>, a.ctas, kSimtThreads, bytes, !a.direct, st, a);
 }
 

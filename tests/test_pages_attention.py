@@ -346,6 +346,39 @@ def test_streams_and_captured_graphs():
     c.check(outs[0], None, scale=0.1)
 
 
+def test_calls_of_several_host_threads():
+    """The C entry from four threads at once, head sizes of one kernel among them, each on its own stream with its own workspace."""
+    import ctypes
+    import threading
+    lib = _lib.load()
+    cases = [Case([400, 90], [30, 1], 4, 2, D, 16, dtype, seed=D, dirty=False) for D, dtype in ((40, "fp32"), (64, "fp32"), (250, "fp32"), (33, "bf16"))]
+    args = []
+    for c in cases:
+        t = dict(q=c.q.to(DEV), pool=c.pool.to(DEV), table=c.table.to(DEV), lengths=c.lengths.to(DEV), seqs=c.seqs.to(DEV), cu=ints(c.off))
+        dims = _lib.AttentionDims(rows=2, tokens=31, Hq=4, Hkv=2, D=c.D, dtype=_lib.KDA_BF16 if c.dtype == "bf16" else _lib.KDA_FP32, num_pages=c.pool.shape[0],
+                                  page_tokens=16, table_rows=c.table.shape[0], max_pages=c.table.shape[1])
+        ws = torch.empty(lib.kda_pages_attention_workspace_size(ctypes.byref(dims)), dtype=torch.uint8, device=DEV)
+        args.append((dims, t, ws, torch.zeros(31, 4, c.D, dtype=DT[c.dtype], device=DEV), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    said, gate = [], threading.Barrier(len(args))
+
+    def work(dims, t, ws, out, stream):
+        gate.wait()
+        for _ in range(50):
+            said.append(lib.kda_pages_attention(ctypes.byref(dims), t["q"].data_ptr(), t["pool"].data_ptr(), t["table"].data_ptr(), t["lengths"].data_ptr(),
+                                                t["seqs"].data_ptr(), t["cu"].data_ptr(), None, dims.D ** -0.5, out.data_ptr(), None, ws.data_ptr(),
+                                                ws.numel(), stream.cuda_stream))
+    threads = [threading.Thread(target=work, args=a) for a in args]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert said == [0] * 200 and kda.device_status() == 0
+    for c, a in zip(cases, args):
+        c.check(a[3][None], None)
+
+
 def test_a_cache_grows_forks_and_moves():
     """Extend, append, attend, fork, extend both, compact: as a sequence of its own each."""
     g = torch.Generator().manual_seed(4)
