@@ -98,12 +98,16 @@ class StateCache:
                 yield from pool.values()
 
     def admit(self, rows, tokens):
-        """Pages for sequences of the given lengths.  Returns ok: 0 where there were not enough (the row then has none)."""
+        """Pages for sequences of the given lengths.  Returns ok: 0 where there were not enough (the row then stays as it was)."""
+        before = self.lengths[rows.long().clamp(0, self.lengths.numel() - 1)]      # (rows that are none are refused below)
         ok = pages_extend(self.table, self.lengths, self.refs, rows, tokens, page_tokens=WHOLE)
         if self.kv is not None:
             both = pages_extend(self.kv_table, self.kv_lengths, self.kv_refs, torch.where(ok > 0, rows, -1), tokens,
                                 page_tokens=self.page_tokens)
-            pages_free(self.table, self.lengths, self.refs, torch.where((ok > 0) & (both == 0), rows, -1))
+            back = (ok > 0) & (both == 0)
+            # (a page that the row had before this call holds its states)
+            pages_free(self.table, self.lengths, self.refs, torch.where(back & (before == 0), rows, -1))
+            self.lengths[rows[back].long()] = before[back]
             ok = both
         return ok
 

@@ -84,6 +84,31 @@ def test_refused_admissions_and_forks_leave_no_pages():
     assert kda.device_status() == 0
 
 
+def test_a_longer_admission_that_is_refused_changes_nothing():
+    """A row that holds its states and keys already keeps them where there is no room for more, and goes on."""
+    model = serve.Decoder(pattern="dsga")
+    g = torch.Generator().manual_seed(6)
+    prompts, nxt = torch.randint(0, 512, (1, 50), generator=g).cuda(), torch.randint(0, 512, (2, 3), generator=g).cuda()
+    rows, off = ids(0, 1), serve.offsets([20, 30])
+    caches = [serve.StateCache(model, slots=4, sequences=3, kv_pages=n, kv_row=6) for n in (18, 5)]
+    for cache in caches:
+        assert cache.admit(rows, ids(20, 30)).tolist() == [1] * 2                     # 2 pages each
+        serve.prompt(model, cache, prompts, off, rows)
+    plenty, few = caches
+    held = few.table.clone(), few.kv_table.clone()
+    assert few.admit(ids(1, 2, 0), ids(90, 40, 60)).tolist() == [0] * 3               # 6, 3 and 4 pages of keys: one is free
+    assert torch.equal(few.table, held[0]) and torch.equal(few.kv_table, held[1])
+    assert few.lengths.tolist() == [20, 30, 0] and few.kv_lengths.tolist() == [20, 30, 0]
+    assert int((few.refs > 0).sum()) == 2 and int((few.kv_refs > 0).sum()) == 4
+    for k in range(2):
+        want, got = (serve.step(model, cache, nxt[:, k], rows) for cache in caches)
+        assert all(close(got[r], want[r]) for r in range(2))
+    assert few.admit(ids(1), ids(40)).tolist() == [1] and few.lengths.tolist() == [20, 40, 0]
+    assert few.admit(ids(-1, 3, 99), ids(5, 5, 5)).tolist() == [0] * 3                # rows that are none
+    assert few.lengths.tolist() == [20, 40, 0] and few.kv_lengths.tolist() == [22, 40, 0]
+    assert kda.device_status() == 0
+
+
 def test_a_step_without_a_free_page_changes_nothing():
     """Its row is left as it was, gets NaN, and goes on when there is a page again; the other rows do not notice."""
     model = serve.Decoder(pattern="dsga")
