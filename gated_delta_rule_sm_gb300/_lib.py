@@ -708,6 +708,7 @@ def pages_attention(q, pool, table, lengths, *, scale: float, seqs=None, cu_seql
     q [B, n, Hq, D] or [1, T, Hq, D] with ``cu_seqlens``, rows as for :func:`pages_append`, whose keys and values come
     first; query head h reads key head h // (Hq // Hkv).  The token at position p attends to the positions 0 .. p, with
     ``window`` > 0 to the last ``window`` of them.  Returns out like q, contiguous; rows without keys (idle, empty) get
-    zeros.  ``lse`` [.., Hq] fp32, if given, gets the logarithms of the sums of exponentials."""
+    zeros.  ``lse`` [.., Hq] fp32, if given, gets the logarithms of the sums of exponentials.  bf16 calls of more than 16 tokens x
+    Hq / Hkv a row on average (D <= 128) round the softmax weights to bf16, others keep them to 2^-16 or better."""
     address, held = _host_address(cu_seqlens, cu_seqlens_host)
     return _run("pages_attention", stream, q, pool, table, lengths, scale, seqs, cu_seqlens, address, window, out, lse)

@@ -20,10 +20,10 @@ namespace {
 // ------------------------------------------------------------------ append
 
 // A warp takes a token, its lanes the 16-byte pieces (elements where those are not aligned) of its keys and values.  Bound by
-// memory and latency: the address of a token comes from small loads one after the other (its row, the row's length, the page), while
-// the loads of its data and of the offsets' check are under way.  Measured: 8192 tokens, 8 heads of 128 in bf16 (67 MB), 15 us with
-// the launch, 128 single tokens 4.1.  Eight pieces of a lane at once, which a token of 2 KB does not have, cost registers and so
-// 2 us; the check before the loads 1; warps of two tokens saved nothing, of four cost 2.
+// latency: the CTA meets at the offsets' check (the first of its stalls), and the address of a token comes from small loads one after the
+// other (its row, the row's length, the page), while the loads of its data are under way.  Measured: 8192 tokens, 8 heads of 128
+// in bf16 (67 MB), 16 us with the launch, 128 single tokens 4.1.  Eight pieces of a lane at once, which a token of 2 KB does not
+// have, cost registers and so 2 us; the check before the loads 1; warps of two tokens saved nothing, of four cost 2.
 constexpr int kAppendWarps = 8;
 struct AppendArgs {
     AttnArgs a;
@@ -539,11 +539,13 @@ size_t attn_layout(char* ws, AttnArgs* a) {
     return o;
 }
 
-// Which kernel a call takes, and its cut.  aligned: the pool's base allows 16-byte copies.
+// Which kernel a call takes, and its cut.  aligned: the pool's base allows 16-byte copies.  The choice is the call's, by its rows'
+// average, so that the same row may get the weights' one bf16 term (tc) in one call and two (mma) in another.
 // mma reads a row's keys once for 16 packed rows, tc for 256: mma where a row has 16 on average at most (4 query heads to a key
 // head, D = 128, attention and join: 16 packed rows of 8 requests over 8192 keys 71 us by mma, 68 by tc; of 64 over 2048 115
 // and 115; with D = 64 single tokens of the 8 requests 48 and 53, of the 64 77 and 95), tc above it (32 packed rows: 93 us by mma, 70 by
 // tc; 198 and 118).
+// Above D = 128 mma has chunks as well, 16 packed rows to a read of the keys: 8192 tokens after 8192, 32 heads on 8 of 256, 34 ms.
 // Their two or one CTAs of an SM share its registers and shared memory; extra: an item's beginning and end in key tiles, fitted to the
 // CTAs' own times (tc: 8.2 us for an item, 1.53 us for a tile; cuts with 1 in place of 4 left some CTAs at twice the mean of
 // short causal items, 774 for 1103 TFLOP/s).

@@ -28,9 +28,10 @@
 // Bound: per pair of tiles and 128 keys (D = 128) 16.8 MFLOP, 2050 cycles of the tensor core at its dense rate, 256 KB of
 // operands and copies through shared memory, 2048 cycles, and beside them 32768 exponentials.  A step takes 3000 cycles: after P V
 // of a tile the tensor core waits for its next S to be issued, since TMEM has no room for P beside S and two O.
-// Measured, D = 128, 32 query heads (TFLOP/s; 2012 is what a large library product reaches): 16384 causal tokens 1540, 8192 tokens
-// after 8192 1570, 8192 tokens over 8 requests with 8192 before each 1430; D = 64, 8192 after 8192: 990, where a
-// step's products are half as long and its exponentials are not.
+// Measured, D = 128, 32 query heads, calls with the plan and the join (TFLOP/s; 2012 is what a large library product reaches): 16384
+// causal tokens 1480, 8192 tokens after 8192 1535 (with a window of 2048: 948), 8192 tokens over 8 requests with 8192 before each
+// 1380; D = 64, 8192 after 8192: 946.  There O takes half its columns, and P still lies over S: the products are half as long, the wait
+// of a tile's next S for its P V is not.
 #include <math.h>
 
 #include <type_traits>

@@ -637,8 +637,9 @@ kda_status kda_pages_compact(const kda_pages_dims* dims, void* pool, const int32
  *   gets zeros, and lse -inf.  Keys past the window and the position are not read as numbers: whatever their pages
  *   hold there, a masked key's score counts as nothing.  Only a value that is not finite, at a position that another
  *   query of the same row may see, reaches queries that may not see it if both are in one tile of keys (0 times it).
- *   Sums and statistics are fp32.  In bf16 calls the weights meet the values rounded to bf16, or, with few new tokens, as
- *   two bf16 terms.
+ *   Sums and statistics are fp32.  In bf16 calls with D a multiple of 8 (and the pool 16-byte aligned) the weights meet the values
+ *   as two bf16 terms where D > 128 or the call's rows have 16 packed rows (new tokens times Hq / Hkv) on average at most, and
+ *   rounded to bf16 otherwise: which of them a row gets, and with it its bits, depends on the call that it is in.
  *
  * q, k and v may be slices of one projection's output: *_stride is the distance in elements between neighbouring tokens,
  * 0 meaning contiguous.  out and lse are contiguous and overlap no input.
