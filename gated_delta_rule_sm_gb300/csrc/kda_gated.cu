@@ -18,14 +18,15 @@
 // Measured, 16384 tokens x 4096 channels in bf16: forward 134 us with 12 documents and 131 us with 4 rows (537 MB: 4.1
 // TB/s), backward 264 us (1.34 GB: 5.1 TB/s; a copy reaches 6.7).  Bound by both sides of a tile's life: the instructions
 // (some 90 for two channels of a token forward, 180 backward, 60% of the issue slots) and the waits between its phases.
-// Calls of that size with the plan (10 us): 142 and 282 us; every tile with row edges (256 documents of 64 tokens) 190 and 352 us; rates
-// above 1/4 everywhere 202 and 397 us; fp32 200 and 368 us (1.07 GB and 1.9).
+// Calls of that size with the plan (10 us): 142 and 282 us; every tile with row edges (256 documents of 64 tokens) 190 and 371 us; rates
+// above 1/4 everywhere 201 and 417 us; fp32 200 and 368 us (1.07 GB and 1.9).
 // Without the chain's waits the forward took 117 us.  The tile's size is at its best: eight warps and 4 CTAs of an SM forward,
 // 3 backward; before the copies went ahead (149 and 262 us), 16 warps and tiles of 128 tokens took 164 and 323, 4 warps and tiles of
 // 32 tokens 163 and 276, and a fifth CTA (the inputs kept in shared memory, 40 registers) as long as four.
 // Precision: everything in fp32, the gates through the approximate exponential, reciprocal and square root (2^-22 or so each; the fp32
 // gradients are 2.9e-7 of the norm off where a form with library functions is 2.2e-7).  1 - a comes from a series in
-// log a, so that decays next to 1, the long memories, are right to a rounding, and sqrt(1 - a^2) = sqrt(e (2 - e)) with e = 1 - a loses nothing there either.
+// log a, so that decays next to 1, the long memories, are right to a rounding, and sqrt(1 - a^2) = sqrt(e (2 - e)) with e = 1 - a loses
+// nothing there either; decays next to 0, of fast rates, are right to a rounding of themselves.
 #include <math.h>
 #include <string.h>
 
@@ -189,21 +190,50 @@ template <bool WIDE> __device__ __forceinline__ float2 log_decay(float2 g, float
     return l;
 }
 
-// 1 - e^l for l <= 0.  Down to -1/4, l times a polynomial of degree 4 for (1 - e^l) / l (interpolated at the Chebyshev points of
-// [-1/4, 0] in 64 bits; off by 5e-9 of the value with its coefficients in fp32); below, which only a wide rate can reach,
-// the exponential.
-template <typename V> __device__ __forceinline__ V one_minus_exp(V l, bool wide) {
+// A decay a = e^l, l <= 0, and e = 1 - a, each right to a rounding of itself.  Down to -1/4 e is l times a polynomial of degree 4 for
+// (1 - e^l) / l (interpolated at the Chebyshev points of [-1/4, 0] in 64 bits; off by 5e-9 of the value with its coefficients in
+// fp32), and a is 1 - e; below, which only a wide rate can reach, a is the exponential, and e is 1 - a.
+template <typename V> struct Decay {
+    V a, e;
+};
+template <typename V> __device__ __forceinline__ Decay<V> exp_decay(V l, bool wide) {
     V p = vfma(l, vdup<V>(-0.007513606455177069f), vdup<V>(-0.04149065539240837f));
     p = vfma(p, l, vdup<V>(-0.16665108501911163f));
     p = vfma(p, l, vdup<V>(-0.4999995231628418f));
     p = vfma(p, l, vdup<V>(-1.f));
-    V e = vmul(l, p);
+    Decay<V> d;
+    d.e = vmul(l, p);
+    d.a = vfma(d.e, vdup<V>(-1.f), vdup<V>(1.f));
     if (wide) {
-        auto far = [](float t, float near) { return t < -0.25f ? 1.f - ex2(t * kLog2e) : near; };
-        if constexpr (std::is_same_v<V, float2>) e = make_float2(far(l.x, e.x), far(l.y, e.y));
-        else e = far(l, e);
+        auto far = [](float t, float& a, float& e) {
+            if (t < -0.25f) {
+                a = ex2(t * kLog2e);
+                e = 1.f - a;
+            }
+        };
+        if constexpr (std::is_same_v<V, float2>) {
+            far(l.x, d.a.x, d.e.x);
+            far(l.y, d.a.y, d.e.y);
+        } else {
+            far(l, d.a, d.e);
+        }
     }
-    return e;
+    return d;
+}
+// Both in one word, which the backward pass keeps: e, or, where a is below a half, a with its sign set (-0 where a is 0).  (Only where a
+// rate may be wide; the backward calls with row edges or wide rates everywhere took 352 and 397 us with e alone, 371 and 417 so.)
+template <bool WIDE> __device__ __forceinline__ float pack(const Decay<float>& d) { return WIDE && d.a < 0.5f ? -d.a : d.e; }
+template <bool WIDE> __device__ __forceinline__ float2 pack(const Decay<float2>& d) {
+    return make_float2(WIDE && d.a.x < 0.5f ? -d.a.x : d.e.x, WIDE && d.a.y < 0.5f ? -d.a.y : d.e.y);
+}
+template <bool WIDE> __device__ __forceinline__ bool holds_a(float w) { return WIDE && __float_as_int(w) < 0; }
+template <bool WIDE> __device__ __forceinline__ float keep_of(float w) { return holds_a<WIDE>(w) ? -w : 1.f - w; }
+template <bool WIDE> __device__ __forceinline__ float2 keep_of(float2 w) {
+    const float2 a = fma2(w, make_float2(-1.f, -1.f), make_float2(1.f, 1.f));
+    return make_float2(holds_a<WIDE>(w.x) ? -w.x : a.x, holds_a<WIDE>(w.y) ? -w.y : a.y);
+}
+template <bool WIDE, typename V> __device__ __forceinline__ V loss_of(V w) {
+    return vmap([](float t) { return holds_a<WIDE>(t) ? 1.f + t : t; }, w);
 }
 
 // 1 / sqrt(1 - a^2) from w = 1 - a^2 = e (2 - e).  Where a is 1 to fp32 it stops at 1e18: w, and with it -log a, is then below 1e-36, so that
@@ -212,7 +242,6 @@ template <typename V> __device__ __forceinline__ V square_of(V e) { return vmul(
 template <typename V> __device__ __forceinline__ V root_of(V w) {
     return vmap([](float t) { return rsq(fmaxf(t, 1e-36f)); }, w);
 }
-template <typename V> __device__ __forceinline__ V keep_of(V e) { return vfma(e, vdup<V>(-1.f), vdup<V>(1.f)); }
 
 // Both gates of a token: their sigmoids, and 1 less them (e^-z times them, exact where they are close to 1).
 template <typename V> struct Gates {
@@ -247,11 +276,11 @@ template <typename V> __device__ __forceinline__ V sigmoid(V z) {
     const V one = vdup<V>(1.f), e = vmap([](float t) { return ex2(t); }, vmul(z, vdup<V>(-kLog2e)));
     return vmap([](float t) { return rcp(t); }, vfma(e, one, one));
 }
-// 1 - a of a token and its input sqrt(1 - a^2) sigmoid(i) x.
-template <bool WIDE, typename V> __device__ __forceinline__ V decay_of(V g, V i, V x, const Rate<V>& rate, V& b) {
-    const V e = one_minus_exp(log_decay<WIDE>(g, sigmoid(g), rate), WIDE && rate.wide);
-    b = vmul(vmap([](float t) { return sqr(t); }, square_of(e)), vmul(sigmoid(i), x));
-    return e;
+// The decay of a token and its input sqrt(1 - a^2) sigmoid(i) x.
+template <bool WIDE, typename V> __device__ __forceinline__ Decay<V> decay_of(V g, V i, V x, const Rate<V>& rate, V& b) {
+    const Decay<V> d = exp_decay(log_decay<WIDE>(g, sigmoid(g), rate), WIDE && rate.wide);
+    b = vmul(vmap([](float t) { return sqr(t); }, square_of(d.e)), vmul(sigmoid(i), x));
+    return d;
 }
 
 // ------------------------------------------------------------------ rows inside a tile
@@ -516,7 +545,7 @@ __device__ __forceinline__ void forward_tile(const GatedArgs& a, const Spot& s, 
     V ka[kTok], kb[kTok], P, h;
 #pragma unroll
     for (int k = 0; k < kTok; ++k) {
-        ka[k] = keep_of(decay_of<EDGE>(mg[k][tid].get(), mi[k][tid].get(), mx[k][tid].get(), rate, kb[k]));
+        ka[k] = decay_of<EDGE>(mg[k][tid].get(), mi[k][tid].get(), mx[k][tid].get(), rate, kb[k]).a;
         if (EDGE && k >= s.n) {
             ka[k] = vdup<V>(1.f);
             kb[k] = vdup<V>(0.f);
@@ -682,7 +711,7 @@ template <typename E, int VEC> struct BwdShared {
     Plane<E, VEC> x, g, i, dy;
     Edges edges;
     V sp[kWarps][32], sh[kWarps][32], sq[kWarps][32], sm[kWarps][32], senter[32];
-    V e[kTok][kThreads], b[kTok][kThreads];       // e = 1 - a; the inputs, then the states before the tokens
+    V d[kTok][kThreads], b[kTok][kThreads];       // the decays; the inputs, then the states before the tokens
     TileWords w;
 };
 
@@ -700,16 +729,17 @@ __device__ __forceinline__ void backward_tile(const GatedArgs& a, const Spot& s,
     V P = one, h = vdup<V>(0.f);
 #pragma unroll 8
     for (int k = 0; k < kTok; ++k) {
-        V b, e = decay_of<EDGE>(mg[k][tid].get(), mi[k][tid].get(), mx[k][tid].get(), rate, b);
-        if (EDGE && k >= s.n) e = b = vdup<V>(0.f);
-        const V ka = keep_of(e);
+        V b;
+        Decay<V> d = decay_of<EDGE>(mg[k][tid].get(), mi[k][tid].get(), mx[k][tid].get(), rate, b);
+        if (EDGE && k >= s.n) d = {one, b = vdup<V>(0.f)};
+        const V ka = d.a;
         if (EDGE && begins_at(k) >= 0) {
             P = vdup<V>(0.f);
             h = row_of(a.s0, begins_at(k));
         }
         P = vmul(P, ka);
         h = vfma(ka, h, b);
-        m_.e[k][tid] = e;
+        m_.d[k][tid] = pack<EDGE>(d);
         m_.b[k][tid] = b;
     }
     m_.sp[warp][lane] = P;
@@ -723,7 +753,7 @@ __device__ __forceinline__ void backward_tile(const GatedArgs& a, const Spot& s,
             P = vdup<V>(0.f);
             m = row_of(a.dsT, ends_at(k));
         }
-        const V ka = keep_of(m_.e[k][tid]);
+        const V ka = keep_of<EDGE>(m_.d[k][tid]);
         P = vmul(P, ka);
         m = vmul(ka, vfma(md[k][tid].get(), one, m));
     }
@@ -747,7 +777,7 @@ __device__ __forceinline__ void backward_tile(const GatedArgs& a, const Spot& s,
         if (EDGE && begins_at(k) >= 0) h = row_of(a.s0, begins_at(k));
         const V b = m_.b[k][tid];
         m_.b[k][tid] = h;
-        h = vfma(keep_of(m_.e[k][tid]), h, b);
+        h = vfma(keep_of<EDGE>(m_.d[k][tid]), h, b);
     }
     state_wait();
     m = m_.senter[lane];
@@ -762,7 +792,7 @@ __device__ __forceinline__ void backward_tile(const GatedArgs& a, const Spot& s,
             if (EDGE && ends_at(k) >= 0) m = row_of(a.dsT, ends_at(k));
             const V g = mg[k][tid].get();
             const Gates<V> z = gates_of(g, mi[k][tid].get());
-            const V e = m_.e[k][tid], w = square_of(e), root = root_of(w), ka = keep_of(e);
+            const V d = m_.d[k][tid], e = loss_of<EDGE>(d), w = square_of(e), root = root_of(w), ka = keep_of<EDGE>(d);
             const V dh = vfma(md[k][tid].get(), one, m);                  // the gradient of h_t
             m = vmul(ka, dh);
             if (EDGE && begins_at(k) >= 0 && a.ds0) vstore(a.ds0 + (size_t)begins_at(k) * a.C + c, m);
@@ -869,7 +899,7 @@ __global__ void __launch_bounds__(kStepThreads) gated_step_kernel(const __grid_c
     const V old = vload<V>(a.s_in + (size_t)slot * a.C + c);
     const Rate<V> rate = rate_of(vload<V>(a.a_log + c));
     V add;
-    const V e = decay_of<true>(rg.get(), ri.get(), rx.get(), rate, add), h = vfma(keep_of(e), old, add);
+    const V h = vfma(decay_of<true>(rg.get(), ri.get(), rx.get(), rate, add).a, old, add);
     vstore(a.s_out + (size_t)slot * a.C + c, h);
     R::store(a.y, (size_t)b * a.C + c, h);
 }

@@ -295,6 +295,37 @@ def test_gradients_of_gates_and_rates_at_their_ends(dtype):
     check_grads_at_the_ends(i, s0, torch.randn(1, T, C, generator=g).to(DT[dtype]).to(DEV), None)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_fast_rates_keep_their_small_decays(dtype):
+    """Decays down to e^-50: states that only decay, and the gradients of their rates, by their own size.  With u = 2^-24: log a is off
+    by 8 u (|a_log| + |g|) and 16 u of itself (as above), a decay by |log a| times that and 2^-21 of itself (one exponential whose
+    argument has been rounded); a gradient's term takes it twice more, with GRAD for the other factors."""
+    B, T, rates = 40, 3, [0.3, 1.0, 4.0, 12.0, 30.0, 60.0, 100.0, 0.1]
+    C = 9 * len(rates)
+    i, g = inputs(17, (B, T), C, dtype)
+    i["a_log"] = torch.log(torch.tensor(rates)).to(DEV).repeat_interleave(9).contiguous()
+    s0, dlast = (torch.randn(B, C, generator=g).to(DEV) for _ in range(2))
+    al, gr = ref.d(i["a_log"]), ref.d(i["g_raw"])
+    log_a = -torch.exp(al) * torch.sigmoid(gr)
+    off = log_a.abs() * 2.0 ** -24 * (8 * (al.abs() + gr.abs()) + 16) + 2.0 ** -21          # of each decay, relative
+    # closed input gates: what is left of the state is the product of the decays
+    only = dict(i, x=torch.zeros_like(i["x"]))
+    y, last = run(only, initial_state=s0, output_final_state=True)
+    want, tol = torch.exp(log_a.cumsum(1)) * ref.d(s0)[:, None], off.cumsum(1) + (2.0 ** -8 if dtype == "bf16" else 0.0)
+    assert bool(((ref.d(y) - want).abs() <= tol * want.abs() + 1e-37).all())
+    assert bool(((ref.d(last) - want[:, -1]).abs() <= off.sum(1) * want[:, -1].abs() + 1e-37).all())
+    step = {n: t[:, 0].contiguous() if t.dim() == 3 else t for n, t in only.items()}
+    y, pool = kda.gated_step(step["x"], step["g_raw"], step["i_raw"], step["a_log"], state=s0.clone())
+    assert bool(((ref.d(pool) - want[:, 0]).abs() <= off[:, 0] * want[:, 0].abs() + 1e-37).all())
+    # the gradients of the rates, by the sizes of their terms
+    dy = torch.randn(B, T, C, generator=g).to(DT[dtype]).to(DEV)
+    grads = backward(i, dy, initial_state=s0, dfinal_state=dlast)
+    want, terms = ref.gated_grads(*[i[n].reshape(-1, C) for n in ("x", "g_raw", "i_raw")], i["a_log"], [n * T for n in range(B + 1)], s0,
+                                  dy.reshape(-1, C), dlast)
+    rel = GRAD + 3 * off.reshape(-1, C).amax(0)
+    assert bool(((ref.d(grads["da_log"]) - want["da_log"]).abs() <= rel * terms + 1e-36).all())
+
+
 def test_gradients_against_differences():
     """Along a direction, the gradients' product is the slope of the 64-bit forward (central differences, whose own error
     is h^2 of the third derivative, about 1e-8 here)."""
